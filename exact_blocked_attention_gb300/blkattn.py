@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -32,7 +33,11 @@ EXPORTED = ("blkattn_fwd", "blkattn_merge", "blkattn_status_string",
             "blkattn_check_device_error", "blkattn_debug_plan", "blkattn_debug_set_split_event",
             "blkattn_fwd_static_scratch", "blkattn_last_cuda_error", "blkattn_fwd_tree",
             "blkattn_spec_sample", "blkattn_fwd_window", "blkattn_bwd", "blkattn_bwd_window",
-            "blkattn_debug_stall_next_decode")
+            "blkattn_debug_stall_next_decode", "blkattn_rope_angles", "blkattn_rope_phases", "blkattn_rope",
+            "blkattn_rope_bwd", "blkattn_paged_append")
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3}
 
 
 class Tensor(ctypes.Structure):
@@ -53,6 +58,12 @@ class Plan(ctypes.Structure):
 
     def as_dict(self):
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class RopeSpec(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int32), ("scaling", ctypes.c_int32), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("trained", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double)]
 
 
 class BlkattnError(RuntimeError):
@@ -88,6 +99,15 @@ def load(path: str = LIB_PATH):
             lib.blkattn_spec_sample.argtypes = [P] * 8
             lib.blkattn_fwd_static_scratch.restype = ctypes.c_int
             lib.blkattn_fwd_static_scratch.argtypes = [P, P, P, P, P, P, ctypes.c_float, P, P, P]
+            lib.blkattn_rope_angles.restype = ctypes.c_int
+            lib.blkattn_rope_angles.argtypes = [P, P, P]
+            lib.blkattn_rope_phases.restype = ctypes.c_int
+            lib.blkattn_rope_phases.argtypes = [P, ctypes.c_int64, P]
+            for f in (lib.blkattn_rope, lib.blkattn_rope_bwd):
+                f.restype = ctypes.c_int
+                f.argtypes = [P, P, P, ctypes.c_int32, ctypes.c_float, P, P]
+            lib.blkattn_paged_append.restype = ctypes.c_int
+            lib.blkattn_paged_append.argtypes = [P] * 7 + [ctypes.c_int32, ctypes.c_float, P, P, P]
             lib.blkattn_merge.restype = ctypes.c_int
             lib.blkattn_merge.argtypes = [P, P, P, P]
             lib.blkattn_status_string.restype = ctypes.c_char_p
@@ -249,6 +269,97 @@ def spec_sample(p, q, draft, u_accept, u_sample, n_accepted=None, token=None, st
     descs = [describe(t) for t in (p, q, draft, u_accept, u_sample, n_accepted, token)]
     _check(lib.blkattn_spec_sample(*[_ref(d) for d in descs], _stream_handle(stream) if p.is_cuda else None))
     return n_accepted, token
+
+
+# One descriptor as bytes: the layout of Tensor, packed in one call.
+_PACK = struct.Struct("<Qii4q4qi4x")
+assert _PACK.size == ctypes.sizeof(Tensor)
+_PAD = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())
+
+
+def _pack(t):
+    """describe() as a bytes object that ctypes passes as a pointer: a decode
+    step's calls spend most of their host time on descriptors."""
+    if t is None:
+        return None
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"blkattn: unsupported dtype {t.dtype}")
+    shape, n = t.shape, t.dim()
+    if n > 4:
+        raise ValueError("blkattn: at most 4 dimensions")
+    pad = _PAD[n]
+    return _PACK.pack(t.data_ptr() if t.numel() else 0, dt, n, *shape, *pad, *t.stride(), *pad,
+                      t.device.index if t.is_cuda else -1)
+
+
+def _layout(layout) -> int:
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"blkattn: layout {layout!r} is none of {sorted(ROPE_LAYOUTS)}")
+    return ROPE_LAYOUTS[layout]
+
+
+def _stream_of(t, stream):
+    if not t.is_cuda:
+        return None
+    if stream is None:
+        return torch.cuda.current_stream(t.device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def rope_angles(rot: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0, trained: float = 0.0,
+                low: float = 1.0, high: float = 32.0):
+    """(angles, mscale) of blkattn_rope_angles: the angle of one position for
+    each of the rot / 2 pairs (list of floats) and the factor that goes with it."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"blkattn: scaling {scaling!r} is none of {sorted(ROPE_SCALINGS)}")
+    spec = RopeSpec(int(rot), ROPE_SCALINGS[scaling], base, factor, trained, low, high)
+    w = (ctypes.c_double * max(1, min(int(rot), 1024) // 2))()
+    m = ctypes.c_float()
+    _check(load().blkattn_rope_angles(ctypes.byref(spec), w, ctypes.byref(m)))
+    return list(w), m.value
+
+
+def rope_phases(angles, device="cuda"):
+    """The phase table of angles (blkattn_rope_phases) on the device, made once and kept by the caller."""
+    angles = [float(a) for a in angles]
+    w = (ctypes.c_double * max(1, len(angles)))(*angles)
+    f = (ctypes.c_int64 * max(1, len(angles)))()
+    _check(load().blkattn_rope_phases(w, len(angles), f))
+    return torch.tensor(list(f)[:len(angles)], dtype=torch.int64, device=device)
+
+
+def _rope(fn, x, pos, phases, out, layout, mscale, out_dtype, stream):
+    if out is None:
+        out = torch.empty_like(x, dtype=out_dtype or x.dtype, memory_format=torch.contiguous_format)
+    _check(fn(_pack(x), _pack(pos), _pack(phases), _layout(layout), mscale, _pack(out), _stream_of(x, stream)))
+    return out
+
+
+def rope(x, pos, phases, out=None, layout="half", mscale: float = 1.0, out_dtype=None, stream=None):
+    """blkattn_rope: rows x [B,H,T,d] turned by their positions pos int32
+    [B,T]; out (default: a new contiguous tensor) may be x itself."""
+    return _rope(load().blkattn_rope, x, pos, phases, out, layout, mscale, out_dtype, stream)
+
+
+def rope_backward(dy, pos, phases, out=None, layout="half", mscale: float = 1.0, out_dtype=None, stream=None):
+    """blkattn_rope_bwd: the gradient of rope's x from that of its result."""
+    return _rope(load().blkattn_rope_bwd, dy, pos, phases, out, layout, mscale, out_dtype, stream)
+
+
+def paged_append(k, v, pos, page_table, k_pages, v_pages, phases=None, layout="half", mscale: float = 1.0, q=None,
+                 q_out=None, stream=None):
+    """blkattn_paged_append: rows k, v [B,H_kv,T,d] into the pools [N,H_kv,P,d]
+    at the cache rows pos int32 [B,T] (negative: padding, not written) through
+    page_table int32 [B,entries]; with phases, k and q turn on the way.
+    Returns q_out (allocated as zeros when q is given without it: rows of
+    padding stay unwritten), or None."""
+    if q is not None and q_out is None:
+        q_out = torch.zeros_like(q, memory_format=torch.contiguous_format)
+    _check(load().blkattn_paged_append(_pack(k), _pack(v), _pack(pos), _pack(page_table), _pack(k_pages),
+                                       _pack(v_pages), _pack(phases), _layout(layout), mscale, _pack(q),
+                                       _pack(q_out), _stream_of(k, stream)))
+    return q_out
 
 
 def _states(m, l, u) -> States:

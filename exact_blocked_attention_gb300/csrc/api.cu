@@ -15,6 +15,7 @@
 
 #include "blkattn.h"
 #include "kernels.h"
+#include "paged.h"
 
 namespace {
 
@@ -593,6 +594,36 @@ int launch_fwd(const FwdParams& p, const Checked& c, const Plan& pl, const blkat
 }  // namespace
 
 namespace blkattn {
+
+bool tensor_dims_ok(const blkattn_tensor* t, int ndim) { return dims_ok(t, ndim); }
+bool tensors_on_one_device(const blkattn_tensor* first, std::initializer_list<const blkattn_tensor*> ts) {
+  return same_device(first, ts);
+}
+int require_current_device(int32_t device) { return check_current_device(device); }
+
+int check_pages(const blkattn_tensor* k_pages, const blkattn_tensor* v_pages, const blkattn_tensor* table,
+                int32_t dtype, int64_t B, int64_t H, int64_t d, PageTable* out) {
+  if (!dims_ok(k_pages, 4) || !dims_ok(v_pages, 4) || !dims_ok(table, 2)) return BLKATTN_ERR_INVALID_ARG;
+  if (k_pages->dtype != dtype || v_pages->dtype != dtype || table->dtype != BLKATTN_I32)
+    return BLKATTN_ERR_INVALID_ARG;
+  const int64_t N = k_pages->sizes[0], rows = k_pages->sizes[2], entries = table->sizes[1];
+  for (int i = 0; i < 4; ++i)
+    if (v_pages->sizes[i] != k_pages->sizes[i]) return BLKATTN_ERR_INVALID_ARG;
+  if (H < 1 || N < 1 || rows < 1 || entries < 1 || k_pages->sizes[1] != H || k_pages->sizes[3] != d ||
+      table->sizes[0] != B)
+    return BLKATTN_ERR_INVALID_ARG;
+  if ((rows & (rows - 1)) != 0 || rows < kMinPageRows || rows > kMaxPageRows) return BLKATTN_ERR_UNSUPPORTED;
+  if (N > 0x7fffffff || entries > 0x7fffffff / rows) return BLKATTN_ERR_UNSUPPORTED;
+  out->table = static_cast<const int32_t*>(table->data);
+  out->sb = table->strides[0];
+  out->sp = table->strides[1];
+  out->entries = (int)entries;
+  out->rows = (int)rows;
+  out->shift = 0;
+  while ((1 << out->shift) < rows) ++out->shift;
+  out->n_pages = (int)N;
+  return BLKATTN_OK;
+}
 
 int validate_fwd_args(const blkattn_tensor* q, const blkattn_tensor* k, const blkattn_tensor* v,
                       const blkattn_tensor* seqlens_k, const blkattn_tensor* q_logical_pos,

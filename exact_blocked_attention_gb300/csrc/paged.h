@@ -1,0 +1,43 @@
+// The paged KV cache: pools of pages [N, H_kv, rows, d] and a table of page
+// numbers per sequence.  Cache row t of sequence b is row t mod `rows` of page
+// table[b, t / rows]; an entry outside [0, N) holds no page.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <initializer_list>
+
+#include "blkattn.h"
+
+namespace blkattn {
+
+struct PageTable {
+  const int32_t* table;
+  int64_t sb, sp;  // strides of the sequence and the entry
+  int entries;     // per sequence
+  int shift;       // log2 of the rows of a page
+  int rows;
+  int n_pages;     // pages in the pool
+};
+
+// Page of cache row t of sequence b, or -1: t outside the table (or
+// negative), or no page there.
+__device__ __forceinline__ int page_of(const PageTable& pt, int b, int t) {
+  const int i = t >> pt.shift;  // (negative t: negative i)
+  if ((unsigned)i >= (unsigned)pt.entries) return -1;
+  const int page = __ldg(pt.table + b * pt.sb + i * pt.sp);
+  return (unsigned)page < (unsigned)pt.n_pages ? page : -1;
+}
+
+constexpr int64_t kMinPageRows = 8, kMaxPageRows = 65536;
+
+// Host checks shared by the operators of the paged cache (no CUDA call).
+bool tensor_dims_ok(const blkattn_tensor* t, int ndim);
+// Every tensor given (NULL skipped) names the device of `first`, a real one.
+bool tensors_on_one_device(const blkattn_tensor* first, std::initializer_list<const blkattn_tensor*> ts);
+int require_current_device(int32_t device);
+// k_pages, v_pages [N, H, rows, d] of one dtype, and table int32 [B, entries].
+int check_pages(const blkattn_tensor* k_pages, const blkattn_tensor* v_pages, const blkattn_tensor* table,
+                int32_t dtype, int64_t B, int64_t H, int64_t d, PageTable* out);
+
+}  // namespace blkattn

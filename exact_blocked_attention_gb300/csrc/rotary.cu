@@ -1,0 +1,367 @@
+// Rotary positions: rows rotated by their logical position, forward and
+// backward, and appended to a paged KV cache with the rotation on the way.
+//
+// Pair i of a row's rotated dims turns by t w_i at position t:
+//
+//     (y_a, y_b) = mscale (x_a cos - x_b sin, x_a sin + x_b cos)
+//
+// and the gradient turns back by the same angle (the map is mscale times a
+// rotation, so its transpose is mscale times the inverse rotation).  The
+// angles come as phases F_i = round(2^64 w_i / 2 pi): the product t F_i mod
+// 2^64 is t w_i in units of 2^-64 turns with whole turns dropped, exactly, so
+// a position near 2^31 loses no more than one near 0 (the table's rounding
+// grows to |t| 2^-63 turns).  Its top 32 bits as a float go to
+// sincospif: the angle is off by at most 2^-24 of itself (|angle| <= pi).
+// All arithmetic is fp32; the only rounding to fewer bits is the store.
+//
+// One kernel serves every operator: up to three row sets (append: k, v, q)
+// with their own source, destination, heads and whether they turn.
+#include <cuda_bf16.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "kernels.h"
+#include "paged.h"
+
+namespace blkattn {
+namespace {
+
+struct RowSet {
+  const void* src;
+  int64_t s_b, s_h, s_t, s_d;  // element strides
+  void* dst;
+  int64_t d_b, d_h, d_t, d_d;  // dense: batch, head, row, dim; paged: page, head, row in page, dim
+  int heads;
+  bool turn;   // false: rows are copied
+  bool paged;  // destination rows follow the page table
+};
+
+struct RotaryParams {
+  RowSet set[3];
+  int n_sets;
+  const int32_t* pos;
+  int64_t p_b, p_t;
+  const int64_t* phases;
+  int64_t ph_s;
+  bool back;           // turn by the negative angle
+  bool skip_negative;  // append: rows at a negative position are padding
+  float mscale;
+  int rot, d;
+  int B, T;
+  PageTable pages;
+};
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T x) { return static_cast<float>(x); }
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float x) { return static_cast<T>(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// sin and cos of position t at phase F.
+__device__ __forceinline__ void turn_of(int t, int64_t F, float& sn, float& cs) {
+  const uint64_t a = (uint64_t)(int64_t)t * (uint64_t)F;
+  // top 32 bits: a signed fraction of half a turn in [-1, 1)
+  sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &sn, &cs);
+}
+
+constexpr int kThreads = 256;
+
+// One thread per (token, item, head): an item is one pair, or two of the dims
+// past the rotated part.
+template <typename TI, typename TO, bool INTER>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
+  int h = blockIdx.y, si = 0;
+  while (h >= p.set[si].heads) h -= p.set[si++].heads;
+  const RowSet& s = p.set[si];
+  const int rot = s.turn ? p.rot : 0;
+  const int items = rot / 2 + (p.d - rot + 1) / 2;
+  const int64_t n = (int64_t)p.B * p.T * items;
+  for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < n; u += (int64_t)gridDim.x * kThreads) {
+    const int64_t tok = u / items;
+    const int it = (int)(u - tok * items);
+    const int b = (int)(tok / p.T);
+    const int t = (int)(tok - (int64_t)b * p.T);
+    const int pos = p.pos[b * p.p_b + t * p.p_t];
+    if (p.skip_negative && pos < 0) continue;
+    const TI* src = static_cast<const TI*>(s.src) + (b * s.s_b + h * s.s_h + t * s.s_t);
+    TO* dst = static_cast<TO*>(s.dst);
+    if (s.paged) {
+      const int page = page_of(p.pages, b, pos);
+      if (page < 0) continue;
+      dst += page * s.d_b + h * s.d_h + (pos & (p.pages.rows - 1)) * s.d_t;
+    } else {
+      dst += b * s.d_b + h * s.d_h + t * s.d_t;
+    }
+    if (it < rot / 2) {
+      const int i0 = INTER ? 2 * it : it;
+      const int i1 = INTER ? 2 * it + 1 : rot / 2 + it;
+      const float u0 = to_f32(src[i0 * s.s_d]), u1 = to_f32(src[i1 * s.s_d]);
+      float sn, cs;
+      turn_of(pos, p.phases[it * p.ph_s], sn, cs);
+      if (p.back) sn = -sn;
+      dst[i0 * s.d_d] = from_f32<TO>(p.mscale * (u0 * cs - u1 * sn));
+      dst[i1 * s.d_d] = from_f32<TO>(p.mscale * (u0 * sn + u1 * cs));
+    } else {
+      const int i0 = rot + 2 * (it - rot / 2);
+      const float u0 = to_f32(src[i0 * s.s_d]);
+      if (i0 + 1 < p.d) dst[(i0 + 1) * s.d_d] = from_f32<TO>(to_f32(src[(i0 + 1) * s.s_d]));
+      dst[i0 * s.d_d] = from_f32<TO>(u0);
+    }
+  }
+}
+
+template <typename TI, typename TO>
+cudaError_t launch_types(const RotaryParams& p, bool inter, cudaStream_t stream) {
+  int heads = 0;
+  for (int i = 0; i < p.n_sets; ++i) heads += p.set[i].heads;
+  const int64_t n = (int64_t)p.B * p.T * ((p.d + 1) / 2);
+  const int64_t blocks = (n + kThreads - 1) / kThreads;
+  const dim3 grid((unsigned)(blocks < 0x7fffffff ? blocks : 0x7fffffff), (unsigned)heads);
+  if (inter)
+    rotary_kernel<TI, TO, true><<<grid, kThreads, 0, stream>>>(p);
+  else
+    rotary_kernel<TI, TO, false><<<grid, kThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_rotary(const RotaryParams& p, int32_t in, int32_t out, bool inter, cudaStream_t stream) {
+  if (in == BLKATTN_BF16 && out == BLKATTN_BF16) return launch_types<__nv_bfloat16, __nv_bfloat16>(p, inter, stream);
+  if (in == BLKATTN_BF16) return launch_types<__nv_bfloat16, float>(p, inter, stream);
+  if (out == BLKATTN_BF16) return launch_types<float, __nv_bfloat16>(p, inter, stream);
+  return launch_types<float, float>(p, inter, stream);
+}
+
+// ------------------------------------------------------------- validation
+constexpr int64_t kMaxDim = 1024;
+
+bool floats(const blkattn_tensor* t) { return t->dtype == BLKATTN_BF16 || t->dtype == BLKATTN_F32; }
+
+// No two elements of a tensor that is written share an address through a
+// broadcast dim.
+bool writable(const blkattn_tensor* t) {
+  bool ok = true, empty = false;
+  for (int i = 0; i < t->ndim; ++i) {
+    empty = empty || t->sizes[i] == 0;
+    ok = ok && !(t->sizes[i] > 1 && t->strides[i] == 0);
+  }
+  return ok || empty;
+}
+
+// Rows of the same shape at one address: the call may work in place only on
+// the very same view.
+bool in_place_ok(const blkattn_tensor* a, const blkattn_tensor* b) {
+  if (a->data != b->data) return true;
+  if (a->dtype != b->dtype) return false;
+  for (int i = 0; i < a->ndim; ++i)
+    if (a->sizes[i] > 1 && a->strides[i] != b->strides[i]) return false;
+  return true;
+}
+
+bool finite(float x) { return x - x == 0.f; }
+
+void set_src(RowSet* s, const blkattn_tensor* t) {
+  s->src = t->data;
+  s->s_b = t->strides[0]; s->s_h = t->strides[1]; s->s_t = t->strides[2]; s->s_d = t->strides[3];
+  s->heads = (int)t->sizes[1];
+}
+void set_dst(RowSet* s, const blkattn_tensor* t) {
+  s->dst = t->data;
+  s->d_b = t->strides[0]; s->d_h = t->strides[1]; s->d_t = t->strides[2]; s->d_d = t->strides[3];
+}
+
+// Phases [rot / 2] int64, rot <= d; and the layout.
+int check_phases(const blkattn_tensor* ph, int32_t layout, int64_t d) {
+  if (layout != BLKATTN_ROPE_HALF && layout != BLKATTN_ROPE_INTERLEAVED) return BLKATTN_ERR_INVALID_ARG;
+  if (!tensor_dims_ok(ph, 1) || ph->dtype != BLKATTN_I64 || ph->sizes[0] < 1 || 2 * ph->sizes[0] > d)
+    return BLKATTN_ERR_INVALID_ARG;
+  return BLKATTN_OK;
+}
+
+int rope(const blkattn_tensor* x, const blkattn_tensor* pos, const blkattn_tensor* ph, int32_t layout, float mscale,
+         const blkattn_tensor* y, bool back, blkattn_stream_t stream) {
+  if (!tensor_dims_ok(x, 4) || !tensor_dims_ok(pos, 2) || !tensor_dims_ok(y, 4)) return BLKATTN_ERR_INVALID_ARG;
+  if (!floats(x) || !floats(y) || pos->dtype != BLKATTN_I32) return BLKATTN_ERR_INVALID_ARG;
+  for (int i = 0; i < 4; ++i)
+    if (x->sizes[i] != y->sizes[i]) return BLKATTN_ERR_INVALID_ARG;
+  const int64_t B = x->sizes[0], H = x->sizes[1], T = x->sizes[2], d = x->sizes[3];
+  if (pos->sizes[0] != B || pos->sizes[1] != T) return BLKATTN_ERR_INVALID_ARG;
+  if (int st = check_phases(ph, layout, d); st != BLKATTN_OK) return st;
+  if (!finite(mscale) || !writable(y) || !in_place_ok(x, y)) return BLKATTN_ERR_INVALID_ARG;
+  if (!tensors_on_one_device(x, {pos, ph, y})) return BLKATTN_ERR_INVALID_ARG;
+  if (d > kMaxDim || H > 0xffff || B > 0x7fffffff || T > 0x7fffffff || (B > 0 && T > 0x7fffffff / B))
+    return BLKATTN_ERR_UNSUPPORTED;
+  if (B == 0 || H == 0 || T == 0) return BLKATTN_OK;
+  for (const blkattn_tensor* t : {x, pos, ph, y})
+    if (t->data == nullptr) return BLKATTN_ERR_INVALID_ARG;
+  if (int st = require_current_device(x->device); st != BLKATTN_OK) return st;
+  RotaryParams p{};
+  set_src(&p.set[0], x);
+  set_dst(&p.set[0], y);
+  p.set[0].turn = true;
+  p.n_sets = 1;
+  p.pos = static_cast<const int32_t*>(pos->data);
+  p.p_b = pos->strides[0]; p.p_t = pos->strides[1];
+  p.phases = static_cast<const int64_t*>(ph->data);
+  p.ph_s = ph->strides[0];
+  p.rot = (int)(2 * ph->sizes[0]);
+  p.back = back;
+  p.mscale = mscale;
+  p.d = (int)d; p.B = (int)B; p.T = (int)T;
+  if (cudaError_t e = launch_rotary(p, x->dtype, y->dtype, layout == BLKATTN_ROPE_INTERLEAVED,
+                                    reinterpret_cast<cudaStream_t>(stream));
+      e != cudaSuccess)
+    return report_cuda_failure(e);
+  return BLKATTN_OK;
+}
+
+}  // namespace
+}  // namespace blkattn
+
+extern "C" {
+
+int blkattn_rope_angles(const blkattn_rope_spec* spec, double* angles, float* mscale) {
+  if (spec == nullptr || angles == nullptr) return BLKATTN_ERR_INVALID_ARG;
+  const int r = spec->rot;
+  if (r < 2 || r % 2 != 0 || r > blkattn::kMaxDim || !(spec->base > 1.0) || std::isinf(spec->base))
+    return BLKATTN_ERR_INVALID_ARG;
+  const bool scaled = spec->scaling != BLKATTN_ROPE_PLAIN;
+  if (scaled && (!(spec->factor >= 1.0) || std::isinf(spec->factor))) return BLKATTN_ERR_INVALID_ARG;
+  double base = spec->base;
+  switch (spec->scaling) {
+    case BLKATTN_ROPE_PLAIN:
+    case BLKATTN_ROPE_LINEAR: break;
+    case BLKATTN_ROPE_BASE:
+      if (r < 4) return BLKATTN_ERR_INVALID_ARG;
+      base *= std::pow(spec->factor, (double)r / (r - 2));
+      break;
+    case BLKATTN_ROPE_RAMP:
+      if (!(spec->trained > 0.0) || !(spec->low >= 0.0) || !(spec->high > spec->low) || std::isinf(spec->high) ||
+          std::isinf(spec->trained))
+        return BLKATTN_ERR_INVALID_ARG;
+      break;
+    default: return BLKATTN_ERR_INVALID_ARG;
+  }
+  const double two_pi = 6.283185307179586476925286766559;
+  for (int i = 0; i < r / 2; ++i) {
+    double w = std::pow(base, -2.0 * i / r);
+    if (spec->scaling == BLKATTN_ROPE_LINEAR) w /= spec->factor;
+    if (spec->scaling == BLKATTN_ROPE_RAMP) {
+      double keep = (spec->trained * w / two_pi - spec->low) / (spec->high - spec->low);
+      keep = keep < 0.0 ? 0.0 : (keep > 1.0 ? 1.0 : keep);
+      w = w * keep + w / spec->factor * (1.0 - keep);
+    }
+    angles[i] = w;
+  }
+  if (mscale) *mscale = spec->scaling == BLKATTN_ROPE_RAMP ? (float)(0.1 * std::log(spec->factor) + 1.0) : 1.f;
+  return BLKATTN_OK;
+}
+
+int blkattn_rope_phases(const double* angles, int64_t n, int64_t* phases) {
+  if (n < 0 || (n > 0 && (angles == nullptr || phases == nullptr))) return BLKATTN_ERR_INVALID_ARG;
+  for (int64_t i = 0; i < n; ++i)
+    if (!(std::fabs(angles[i]) <= 8.0)) return BLKATTN_ERR_INVALID_ARG;
+  // 2^66 / (2 pi) rounded down, as 64 + 64 bits below the point
+  constexpr uint64_t kTurnHi = 0xA2F9836E4E441529ull;
+  for (int64_t i = 0; i < n; ++i) {
+    int e = 0;
+    const double m = std::frexp(std::fabs(angles[i]), &e);  // angle = m 2^e, m in [1/2, 1)
+    const uint64_t M = (uint64_t)std::ldexp(m, 53);         // exact: 53 bits
+    // angle 2^64 / (2 pi) = M 2^(e - 53) * 2^64 * (kTurnHi 2^-66)
+    const unsigned __int128 prod = (unsigned __int128)M * kTurnHi;  // below 2^117
+    const int sh = 55 - e;  // phase = prod 2^-sh; at least 51 for the angles allowed
+    const uint64_t f = sh > 118 ? 0 : (uint64_t)((prod + ((unsigned __int128)1 << (sh - 1))) >> sh);
+    phases[i] = (int64_t)(angles[i] < 0.0 ? 0 - f : f);
+  }
+  return BLKATTN_OK;
+}
+
+int blkattn_rope(const blkattn_tensor* x, const blkattn_tensor* pos, const blkattn_tensor* phases, int32_t layout,
+                 float mscale, const blkattn_tensor* y, blkattn_stream_t stream) {
+  return blkattn::rope(x, pos, phases, layout, mscale, y, false, stream);
+}
+
+int blkattn_rope_bwd(const blkattn_tensor* dy, const blkattn_tensor* pos, const blkattn_tensor* phases,
+                     int32_t layout, float mscale, const blkattn_tensor* dx, blkattn_stream_t stream) {
+  return blkattn::rope(dy, pos, phases, layout, mscale, dx, true, stream);
+}
+
+int blkattn_paged_append(const blkattn_tensor* k, const blkattn_tensor* v, const blkattn_tensor* pos,
+                         const blkattn_tensor* page_table, const blkattn_tensor* k_pages,
+                         const blkattn_tensor* v_pages, const blkattn_tensor* phases_opt, int32_t layout,
+                         float mscale, const blkattn_tensor* q_opt, const blkattn_tensor* q_out_opt,
+                         blkattn_stream_t stream) {
+  using namespace blkattn;
+  if (!tensor_dims_ok(k, 4) || !tensor_dims_ok(v, 4) || !tensor_dims_ok(pos, 2)) return BLKATTN_ERR_INVALID_ARG;
+  if (!floats(k) || v->dtype != k->dtype || pos->dtype != BLKATTN_I32) return BLKATTN_ERR_INVALID_ARG;
+  const int64_t B = k->sizes[0], H = k->sizes[1], T = k->sizes[2], d = k->sizes[3];
+  for (int i = 0; i < 4; ++i)
+    if (v->sizes[i] != k->sizes[i]) return BLKATTN_ERR_INVALID_ARG;
+  if (pos->sizes[0] != B || pos->sizes[1] != T || d < 1) return BLKATTN_ERR_INVALID_ARG;
+  PageTable pt;
+  if (int st = check_pages(k_pages, v_pages, page_table, k->dtype, B, H, d, &pt); st != BLKATTN_OK) return st;
+  if (!writable(k_pages) || !writable(v_pages) || (k_pages->data == v_pages->data && k_pages->data != nullptr))
+    return BLKATTN_ERR_INVALID_ARG;
+  if (phases_opt) {
+    if (int st = check_phases(phases_opt, layout, d); st != BLKATTN_OK) return st;
+    if (!finite(mscale)) return BLKATTN_ERR_INVALID_ARG;
+  }
+  if ((q_opt == nullptr) != (q_out_opt == nullptr)) return BLKATTN_ERR_INVALID_ARG;
+  int64_t Hq = 0;
+  if (q_opt) {
+    if (!tensor_dims_ok(q_opt, 4) || !tensor_dims_ok(q_out_opt, 4)) return BLKATTN_ERR_INVALID_ARG;
+    if (q_opt->dtype != k->dtype || q_out_opt->dtype != k->dtype) return BLKATTN_ERR_INVALID_ARG;
+    Hq = q_opt->sizes[1];
+    if (q_opt->sizes[0] != B || q_opt->sizes[2] != T || q_opt->sizes[3] != d) return BLKATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < 4; ++i)
+      if (q_out_opt->sizes[i] != q_opt->sizes[i]) return BLKATTN_ERR_INVALID_ARG;
+    if (!writable(q_out_opt) || !in_place_ok(q_opt, q_out_opt)) return BLKATTN_ERR_INVALID_ARG;
+  }
+  if (!tensors_on_one_device(k, {v, pos, page_table, k_pages, v_pages, phases_opt, q_opt, q_out_opt}))
+    return BLKATTN_ERR_INVALID_ARG;
+  if (d > kMaxDim || H > 0x7fff || Hq > 0x7fff || B > 0x7fffffff || T > 0x7fffffff ||
+      (B > 0 && T > 0x7fffffff / B))
+    return BLKATTN_ERR_UNSUPPORTED;
+  if (B == 0 || T == 0) return BLKATTN_OK;
+  for (const blkattn_tensor* t : {k, v, pos, page_table, k_pages, v_pages})
+    if (t->data == nullptr) return BLKATTN_ERR_INVALID_ARG;
+  if (phases_opt && phases_opt->data == nullptr) return BLKATTN_ERR_INVALID_ARG;
+  if (q_opt && Hq > 0 && (q_opt->data == nullptr || q_out_opt->data == nullptr)) return BLKATTN_ERR_INVALID_ARG;
+  if (int st = require_current_device(k->device); st != BLKATTN_OK) return st;
+  RotaryParams p{};
+  set_src(&p.set[0], k);
+  set_dst(&p.set[0], k_pages);
+  p.set[0].turn = phases_opt != nullptr;
+  p.set[0].paged = true;
+  set_src(&p.set[1], v);
+  set_dst(&p.set[1], v_pages);
+  p.set[1].paged = true;
+  p.n_sets = 2;
+  if (q_opt && Hq > 0) {
+    set_src(&p.set[2], q_opt);
+    set_dst(&p.set[2], q_out_opt);
+    p.set[2].turn = phases_opt != nullptr;
+    p.n_sets = 3;
+  }
+  p.pos = static_cast<const int32_t*>(pos->data);
+  p.p_b = pos->strides[0]; p.p_t = pos->strides[1];
+  if (phases_opt) {
+    p.phases = static_cast<const int64_t*>(phases_opt->data);
+    p.ph_s = phases_opt->strides[0];
+    p.rot = (int)(2 * phases_opt->sizes[0]);
+  }
+  p.skip_negative = true;
+  p.mscale = mscale;
+  p.d = (int)d; p.B = (int)B; p.T = (int)T;
+  p.pages = pt;
+  if (cudaError_t e = launch_rotary(p, k->dtype, k->dtype, phases_opt && layout == BLKATTN_ROPE_INTERLEAVED,
+                                    reinterpret_cast<cudaStream_t>(stream));
+      e != cudaSuccess)
+    return report_cuda_failure(e);
+  return BLKATTN_OK;
+}
+
+}  // extern "C"

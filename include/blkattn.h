@@ -313,6 +313,106 @@ int blkattn_bwd_window(const blkattn_tensor* q, const blkattn_tensor* k,
                        blkattn_stream_t stream);
 
 /*
+ * Rotary positions.  Pair i of a row's first `rot` dims turns by the angle
+ * t w_i at logical position t; the dims from `rot` on stay as they are:
+ *     (y_a, y_b) = mscale (x_a cos - x_b sin, x_a sin + x_b cos)
+ * Layouts: HALF pairs dim i with dim i + rot / 2, INTERLEAVED dims 2i and
+ * 2i + 1.  The kernels take the angles as phases, int64 on the device:
+ * F_i = round(2^64 w_i / 2 pi) mod 2^64, the turn of one position as a 64-bit
+ * fraction; t F_i mod 2^64 drops whole turns exactly, so far positions lose
+ * no precision: the angle is off by at most 2^-63 |t| turns for the table and
+ * 2^-24 of a half turn for the float that the sine is taken of.
+ */
+enum {
+  BLKATTN_ROPE_HALF = 0,
+  BLKATTN_ROPE_INTERLEAVED = 1
+};
+
+enum {
+  BLKATTN_ROPE_PLAIN = 0,   /* w_i = base^(-2i / rot) */
+  BLKATTN_ROPE_LINEAR = 1,  /* w_i / factor (positions interpolated) */
+  BLKATTN_ROPE_BASE = 2,    /* base factor^(rot / (rot - 2)) in place of base: the slowest pair turns `factor` times
+                               slower, the fastest as before (rot >= 4) */
+  BLKATTN_ROPE_RAMP = 3     /* w_i keep_i + w_i / factor (1 - keep_i), keep_i = clamp((turns_i - low) / (high - low)),
+                               turns_i = trained w_i / 2 pi: fast pairs keep their angle, slow ones interpolate */
+};
+typedef struct {
+  int32_t rot;      /* rotated dims: even, 2..1024 */
+  int32_t scaling;  /* BLKATTN_ROPE_PLAIN | _LINEAR | _BASE | _RAMP */
+  double base;      /* > 1 */
+  double factor;    /* context extension, >= 1 (not read by PLAIN) */
+  double trained;   /* RAMP: positions of the unscaled table */
+  double low, high; /* RAMP: 0 <= low < high, in turns */
+} blkattn_rope_spec;
+
+/*
+ * Host only (no CUDA call).  blkattn_rope_angles writes the rot / 2 angles
+ * w_i of a spec and, when mscale is not NULL, the factor on the rotated dims
+ * that goes with it (0.1 ln factor + 1 for RAMP, else 1; a caller may pass
+ * another to the kernels).  blkattn_rope_phases turns any n angles (|w| <= 8)
+ * into phases, each within 2 units of the exact value; the caller copies them to the device once.
+ * Return BLKATTN_OK or BLKATTN_ERR_INVALID_ARG.
+ */
+int blkattn_rope_angles(const blkattn_rope_spec* spec, double* angles, float* mscale);
+int blkattn_rope_phases(const double* angles, int64_t n, int64_t* phases);
+
+/*
+ * blkattn_rope — rotate rows by their logical positions.
+ *
+ * x       [B, H, T, d] bf16 or f32, any strides (0 broadcasts), d <= 1024.
+ * pos     [B, T] int32, any strides: the rows' positions (as q_logical_pos).
+ *         A negative position turns backwards.
+ * phases  [rot / 2] int64, 2 <= rot <= d.
+ * layout  BLKATTN_ROPE_HALF or BLKATTN_ROPE_INTERLEAVED.
+ * mscale  finite; applies to the rotated dims only.
+ * y       [B, H, T, d] bf16 or f32, any strides but no broadcast dim:
+ *         written.  It may be x itself (same address, dtype and strides);
+ *         any other overlap is out of contract.
+ * Computed in fp32, rounded once to y's dtype.  One kernel, no workspace, any
+ * stream; calls on different streams are independent.  Sizes of 0 are a
+ * no-op.  Returns as blkattn_fwd; BLKATTN_ERR_UNSUPPORTED for d > 1024,
+ * H > 65535 or B T > 2^31 - 1.
+ *
+ * blkattn_rope_bwd — its gradient: dx = mscale (rotation)^T dy on the rotated
+ * dims, dy on the others.  Same arguments; dy is typically the f32 dq or dk
+ * of blkattn_bwd, dx bf16 or f32.
+ */
+int blkattn_rope(const blkattn_tensor* x, const blkattn_tensor* pos, const blkattn_tensor* phases, int32_t layout,
+                 float mscale, const blkattn_tensor* y, blkattn_stream_t stream);
+int blkattn_rope_bwd(const blkattn_tensor* dy, const blkattn_tensor* pos, const blkattn_tensor* phases,
+                     int32_t layout, float mscale, const blkattn_tensor* dx, blkattn_stream_t stream);
+
+/*
+ * The paged KV cache.  K and V live in pools of pages [N, H_kv, P, d] (any
+ * strides: [N, P, H_kv, d] memory is a view of it); row t of sequence b is
+ * row t mod P of page page_table[b, t / P].  An entry outside [0, N) holds no
+ * page.  P is a power of two, 8 <= P <= 65536, and entries x P < 2^31; other
+ * P give BLKATTN_ERR_UNSUPPORTED.  Sequences may share pages.
+ *
+ * blkattn_paged_append — write new rows into the cache, rotated on the way.
+ *
+ * k, v        [B, H_kv, T, d] bf16 or f32, any strides: the new rows.
+ * pos         [B, T] int32: logical position of each row, which is also its
+ *             cache row.  A negative position marks a row of padding: nothing
+ *             of it is written (not its q_out row either).
+ * page_table  [B, entries] int32, any strides.  A row past the table or on
+ *             an entry that holds no page is not written (its q_out row is).
+ * k_pages, v_pages  [N, H_kv, P, d] of k's dtype, any strides but no
+ *             broadcast dim: the rows named by pos are written, nothing else.
+ * phases      NULL (k and q are copied) or as for blkattn_rope: k and q turn,
+ *             v never does.
+ * q, q_out    both NULL, or [B, H_q, T, d] of k's dtype: q_out = q turned;
+ *             q_out may be q itself, as in blkattn_rope.
+ * Two rows of one call that name the same cache row leave it with either's
+ * elements, in any mixture.  The new rows must not overlap the pools.  One
+ * kernel, no workspace, any stream.  Returns as blkattn_rope.
+ */
+int blkattn_paged_append(const blkattn_tensor* k, const blkattn_tensor* v, const blkattn_tensor* pos,
+                         const blkattn_tensor* page_table, const blkattn_tensor* k_pages,
+                         const blkattn_tensor* v_pages, const blkattn_tensor* phases, int32_t layout, float mscale,
+                         const blkattn_tensor* q, const blkattn_tensor* q_out, blkattn_stream_t stream);
+
+/*
  * Attention states of rows, in the sufficient statistics of eq. 33.3:
  *   m [rows]           f32, the maximum score (natural-log units); -inf = empty
  *   l [rows]           f32, sum e^{z_j - m}; NULL means "normalised": l = 1 and

@@ -285,25 +285,25 @@ def _pack(t):
     dt = _DTYPES.get(t.dtype)
     if dt is None:
         raise ValueError(f"blkattn: unsupported dtype {t.dtype}")
-    shape, n = t.shape, t.dim()
+    n = t.dim()
     if n > 4:
         raise ValueError("blkattn: at most 4 dimensions")
     pad = _PAD[n]
-    return _PACK.pack(t.data_ptr() if t.numel() else 0, dt, n, *shape, *pad, *t.stride(), *pad,
-                      t.device.index if t.is_cuda else -1)
+    # (a tensor of no elements has the null address; get_device() is -1 for host memory)
+    return _PACK.pack(t.data_ptr(), dt, n, *t.shape, *pad, *t.stride(), *pad, t.get_device())
 
 
 def _layout(layout) -> int:
-    if layout not in ROPE_LAYOUTS:
+    code = ROPE_LAYOUTS.get(layout)
+    if code is None:
         raise ValueError(f"blkattn: layout {layout!r} is none of {sorted(ROPE_LAYOUTS)}")
-    return ROPE_LAYOUTS[layout]
+    return code
 
 
 def _stream_of(t, stream):
-    if not t.is_cuda:
-        return None
+    """The stream handle of a call on tensor t: the given one, or the current one of t's device."""
     if stream is None:
-        return torch.cuda.current_stream(t.device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else None
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -331,7 +331,7 @@ def rope_phases(angles, device="cuda"):
 
 def _rope(fn, x, pos, phases, out, layout, mscale, out_dtype, stream):
     if out is None:
-        out = torch.empty_like(x, dtype=out_dtype or x.dtype, memory_format=torch.contiguous_format)
+        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
     _check(fn(_pack(x), _pack(pos), _pack(phases), _layout(layout), mscale, _pack(out), _stream_of(x, stream)))
     return out
 
@@ -339,12 +339,12 @@ def _rope(fn, x, pos, phases, out, layout, mscale, out_dtype, stream):
 def rope(x, pos, phases, out=None, layout="half", mscale: float = 1.0, out_dtype=None, stream=None):
     """blkattn_rope: rows x [B,H,T,d] turned by their positions pos int32
     [B,T]; out (default: a new contiguous tensor) may be x itself."""
-    return _rope(load().blkattn_rope, x, pos, phases, out, layout, mscale, out_dtype, stream)
+    return _rope((_lib or load()).blkattn_rope, x, pos, phases, out, layout, mscale, out_dtype, stream)
 
 
 def rope_backward(dy, pos, phases, out=None, layout="half", mscale: float = 1.0, out_dtype=None, stream=None):
     """blkattn_rope_bwd: the gradient of rope's x from that of its result."""
-    return _rope(load().blkattn_rope_bwd, dy, pos, phases, out, layout, mscale, out_dtype, stream)
+    return _rope((_lib or load()).blkattn_rope_bwd, dy, pos, phases, out, layout, mscale, out_dtype, stream)
 
 
 def paged_append(k, v, pos, page_table, k_pages, v_pages, phases=None, layout="half", mscale: float = 1.0, q=None,
@@ -356,7 +356,7 @@ def paged_append(k, v, pos, page_table, k_pages, v_pages, phases=None, layout="h
     padding stay unwritten), or None."""
     if q is not None and q_out is None:
         q_out = torch.zeros_like(q, memory_format=torch.contiguous_format)
-    _check(load().blkattn_paged_append(_pack(k), _pack(v), _pack(pos), _pack(page_table), _pack(k_pages),
+    _check((_lib or load()).blkattn_paged_append(_pack(k), _pack(v), _pack(pos), _pack(page_table), _pack(k_pages),
                                        _pack(v_pages), _pack(phases), _layout(layout), mscale, _pack(q),
                                        _pack(q_out), _stream_of(k, stream)))
     return q_out

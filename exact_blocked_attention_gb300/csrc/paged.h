@@ -4,6 +4,7 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <initializer_list>
 
@@ -30,6 +31,22 @@ __device__ __forceinline__ int page_of(const PageTable& pt, int b, int t) {
 }
 
 constexpr int64_t kMinPageRows = 8, kMaxPageRows = 65536;
+
+// A kernel's shared-memory limit, raised once on each device that launches it
+// (the attribute belongs to the device's copy of the kernel).
+struct DeviceOnce {
+  std::atomic<uint64_t> done{0};  // bit d: device d
+  cudaError_t set_smem(const void* kernel, int bytes) {
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+};
 
 // Host checks shared by the operators of the paged cache (no CUDA call).
 bool tensor_dims_ok(const blkattn_tensor* t, int ndim);

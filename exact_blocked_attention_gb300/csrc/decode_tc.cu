@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const int len = len_raw < 0 ? 0 : (len_raw > p.Tmax ? p.Tmax : len_raw);
-      const int uend = maxpos < 0 ? 0 : min(maxpos + 1, len);
+      const int uend = maxpos < 0 ? 0 : min(maxpos, len - 1) + 1;  // (a position may be INT_MAX)
       // sliding window: the unit starts at the tile of its earliest visible key
       const int s0 = (p.window > 0 && minpos != 0x7fffffff) ? max(0, minpos - p.window + 1) / BK : 0;
       const int n = (uend + BK - 1) / BK - s0;
@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t tr = ~0ull;
         if (real[h2]) {
           const int h = hrow[h2], i = irow[h2];
-          e = pos[h2] < 0 ? 0 : min(pos[h2] + 1, len);
+          e = pos[h2] < 0 ? 0 : min(pos[h2], len - 1) + 1;
           if (p.tree != nullptr) tr = (uint64_t)p.tree[(int64_t)b * p.tr_sb + (int64_t)i * p.tr_si];
           if (p.window > 0) {  // the row's first visible key (no overflow: pos >= 0 first)
             tr = (uint64_t)(pos[h2] < 0 ? 0 : max(0, pos[h2] - p.window + 1));

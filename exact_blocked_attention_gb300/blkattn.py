@@ -34,7 +34,7 @@ EXPORTED = ("blkattn_fwd", "blkattn_merge", "blkattn_status_string",
             "blkattn_fwd_static_scratch", "blkattn_last_cuda_error", "blkattn_fwd_tree",
             "blkattn_spec_sample", "blkattn_fwd_window", "blkattn_bwd", "blkattn_bwd_window",
             "blkattn_debug_stall_next_decode", "blkattn_rope_angles", "blkattn_rope_phases", "blkattn_rope",
-            "blkattn_rope_bwd", "blkattn_paged_append")
+            "blkattn_rope_bwd", "blkattn_paged_append", "blkattn_fwd_paged")
 
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3}
@@ -108,6 +108,8 @@ def load(path: str = LIB_PATH):
                 f.argtypes = [P, P, P, ctypes.c_int32, ctypes.c_float, P, P]
             lib.blkattn_paged_append.restype = ctypes.c_int
             lib.blkattn_paged_append.argtypes = [P] * 7 + [ctypes.c_int32, ctypes.c_float, P, P, P]
+            lib.blkattn_fwd_paged.restype = ctypes.c_int
+            lib.blkattn_fwd_paged.argtypes = [P] * 7 + [ctypes.c_int64, ctypes.c_float, P, P, P]
             lib.blkattn_merge.restype = ctypes.c_int
             lib.blkattn_merge.argtypes = [P, P, P, P]
             lib.blkattn_status_string.restype = ctypes.c_char_p
@@ -360,6 +362,27 @@ def paged_append(k, v, pos, page_table, k_pages, v_pages, phases=None, layout="h
                                        _pack(v_pages), _pack(phases), _layout(layout), mscale, _pack(q),
                                        _pack(q_out), _stream_of(k, stream)))
     return q_out
+
+
+def fwd_paged(q, k_pages, v_pages, page_table, seqlens_k, q_logical_pos, scale: float, out, lse, stream=None,
+              tree=None, window: int = 0):
+    """blkattn_fwd_paged: attention over the pools k_pages, v_pages
+    [N,H_kv,P,d] through page_table int32 [B,entries]; out and lse are written
+    in place.  tree and window as for fwd."""
+    _check((_lib or load()).blkattn_fwd_paged(_pack(q), _pack(k_pages), _pack(v_pages), _pack(page_table),
+                                              _pack(seqlens_k), _pack(q_logical_pos), _pack(tree), window, scale,
+                                              _pack(out), _pack(lse), _stream_of(q, stream)))
+    return out, lse
+
+
+def attention_paged(q, k_pages, v_pages, page_table, seqlens_k, q_logical_pos, scale=None, out_dtype=torch.float32,
+                    stream=None, tree=None, window: int = 0):
+    """Allocate out/lse with torch and run blkattn_fwd_paged (scale defaults to 1/sqrt(d))."""
+    shape = q.shape
+    out = torch.empty(shape, dtype=out_dtype, device=q.device)
+    lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
+    return fwd_paged(q, k_pages, v_pages, page_table, seqlens_k, q_logical_pos,
+                     shape[3] ** -0.5 if scale is None else scale, out, lse, stream, tree=tree, window=window)
 
 
 def _states(m, l, u) -> States:

@@ -99,10 +99,12 @@ int resident_ctas_per_sm(size_t smem_bytes) {
 // d = 128, no bias, 16-byte aligned query rows) if it also has T_q >= 64.
 // q_vec_ok: the query rows are contiguous and 16-byte aligned (the tcgen05
 // decode kernel loads them with 16-byte vector loads).
+// paged: the cache lies in pages (blkattn_fwd_paged): the tcgen05 decode kernel
+// also takes d = 64, and what it does not take goes to the CUDA-core kernel.
 // windowed: a sliding-window call (the tcgen05 decode kernel then keeps its
 // per-unit start tiles in half of its unit table).
 Plan make_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t Tq, int64_t Tmax, int d, Elt elt,
-               int sms, bool prefill_ok, bool q_vec_ok, bool windowed = false) {
+               int sms, bool prefill_ok, bool q_vec_ok, bool windowed = false, bool paged = false) {
   Plan pl;
   const int64_t rows = (Hq / Hkv) * Tq;  // query rows that read one KV head
   const char* force = std::getenv("BLKATTN_KERNEL");  // comparison runs only
@@ -131,7 +133,7 @@ Plan make_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t Tq, int64_t Tmax, int
     // (the kernel's schedule uses 32-bit arithmetic: fewer than 2^24 key
     // tiles in all, at most 255 CTAs)
     const int64_t max_tiles = B * Hkv * rg * ((Tmax + 127) / 128 + 2);  // + the per-unit weight
-    if (q_vec_ok && elt == Elt::BF16 && d == 128 && !force_mma && !force_cudacore && rows >= 1 &&
+    if (q_vec_ok && elt == Elt::BF16 && (d == 128 || paged) && !force_mma && !force_cudacore && rows >= 1 &&
         B * rg <= (windowed ? blkattn::kDecodeTcMaxEntries / 2 : blkattn::kDecodeTcMaxEntries) &&
         Tmax <= 65535LL * 128 && max_tiles < (1LL << 24) &&
         (sms > 0 ? sms : 148) <= 255) {
@@ -154,7 +156,7 @@ Plan make_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t Tq, int64_t Tmax, int
     }
   }
   size_t smem;
-  bool tensor = (elt == Elt::BF16) && !force_cudacore;
+  bool tensor = (elt == Elt::BF16) && !force_cudacore && !paged;
   if (tensor) {
     // bf16: warp-level tensor cores, 16-row m-tiles (up to 3 per CTA)
     int64_t mt = (rows + 15) / 16;
@@ -533,6 +535,15 @@ FwdParams fill_params(const blkattn_tensor* q, const blkattn_tensor* k, const bl
   return p;
 }
 
+// bf16 output rows the prefill kernel can store 16 bytes at a time.
+bool out_vec16_ok(const blkattn_tensor* out) {
+  if (out->dtype != BLKATTN_BF16 || out->strides[3] != 1) return false;
+  if ((reinterpret_cast<uintptr_t>(out->data) % 16) != 0) return false;
+  for (int i = 0; i < 3; ++i)
+    if ((out->strides[i] * 2) % 16 != 0) return false;
+  return true;
+}
+
 // Enqueue the split-KV kernel and, with more than one split, the merge.
 int launch_fwd(const FwdParams& p, const Checked& c, const Plan& pl, const blkattn_tensor* q,
                const blkattn_tensor* k, const blkattn_tensor* v, const blkattn_tensor* out,
@@ -575,6 +586,7 @@ int launch_fwd(const FwdParams& p, const Checked& c, const Plan& pl, const blkat
         if (st != BLKATTN_OK) return st;
         pp.o_tma = 1;
       }
+      pp.o_vec16 = out_vec16_ok(out) ? 1 : 0;
       le = blkattn::launch_prefill_tc(pp, pl.cfg.row_groups, mq, mk, mv, mo, stream);
     } else {
       le = blkattn::launch_decode_mma(p, (int)c.d, pl.cfg, mk, mv, stream);
@@ -702,6 +714,121 @@ int fwd_impl(const blkattn_tensor* q, const blkattn_tensor* k, const blkattn_ten
   const FwdParams p = fill_params(q, k, v, seqlens_k, q_logical_pos, tree, mask_bias, scale, out, lse, c, pl,
                                   ds->ws, ds->err, ds->cnt);
   return launch_fwd(p, c, pl, q, k, v, out, stream);
+}
+
+// blkattn_fwd_paged: the pools take the places of k and v, their strides those
+// of the cache rows.  The tcgen05 decode kernel's unit table holds a limited
+// number of sequences: longer batches run slice by slice, one after another on
+// the stream, in the same workspace.
+int fwd_paged_impl(const blkattn_tensor* q, const blkattn_tensor* k_pages, const blkattn_tensor* v_pages,
+                   const blkattn_tensor* page_table, const blkattn_tensor* seqlens_k,
+                   const blkattn_tensor* q_logical_pos, const blkattn_tensor* tree, int64_t window, float scale,
+                   const blkattn_tensor* out, const blkattn_tensor* lse, blkattn_stream_t stream_) {
+  if (!dims_ok(q, 4) || !dims_ok(k_pages, 4) || !dims_ok(v_pages, 4)) return BLKATTN_ERR_INVALID_ARG;
+  PageTable pt;
+  int st = check_pages(k_pages, v_pages, page_table, q->dtype, q->sizes[0], k_pages->sizes[1], q->sizes[3], &pt);
+  if (st != BLKATTN_OK) return st;
+  if (window < 0 || window > 0x7fffffff || (window > 0 && tree != nullptr)) return BLKATTN_ERR_INVALID_ARG;
+  if (!(scale - scale == 0.f)) return BLKATTN_ERR_INVALID_ARG;
+  // the pools as a cache of entries x rows keys per sequence
+  blkattn_tensor kc = *k_pages, vc = *v_pages;
+  kc.sizes[0] = vc.sizes[0] = q->sizes[0];
+  kc.sizes[2] = vc.sizes[2] = (int64_t)pt.entries * pt.rows;
+  Checked c;
+  st = validate_fwd(q, &kc, &vc, seqlens_k, q_logical_pos, tree, nullptr, out, lse, &c);
+  if (st != BLKATTN_OK) return st;
+  if (!same_device(q, {page_table})) return BLKATTN_ERR_INVALID_ARG;
+  for (const blkattn_tensor* t : {out, lse})
+    for (int i = 0; i < t->ndim; ++i)
+      if (t->sizes[i] > 1 && t->strides[i] == 0 && c.B > 0 && c.Tq > 0) return BLKATTN_ERR_INVALID_ARG;
+  c.window = window;
+  if (c.B == 0 || c.Tq == 0) return BLKATTN_OK;
+  if (page_table->data == nullptr) return BLKATTN_ERR_INVALID_ARG;
+  if ((st = check_current_device(c.device)) != BLKATTN_OK) return st;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState* ds = nullptr;
+  if ((st = device_state(&ds)) != BLKATTN_OK) return st;
+  const bool prefill_ok = c.prefill_ok && scale > 0.f;
+  auto plan_of = [&](int64_t B) {
+    return make_plan(B, c.Hq, c.Hkv, c.Tq, c.Tmax, (int)c.d, c.elt, ds->sms, prefill_ok, c.q_vec_ok, window > 0, true);
+  };
+  // sequences per launch: all, or as many as keep the fast kernel
+  int64_t nb = c.B;
+  Plan pl = plan_of(nb);
+  if (pl.cfg.kernel == blkattn::Kernel::CudaCore && nb > 1) {
+    const int64_t rg = (c.Hq / c.Hkv * c.Tq + 47) / 48;
+    const int64_t fit = (window > 0 ? blkattn::kDecodeTcMaxEntries / 2 : blkattn::kDecodeTcMaxEntries) / rg;
+    const int64_t tiles = c.Hkv * rg * ((c.Tmax + 127) / 128 + 2);
+    int64_t m = ((1LL << 24) - 1) / tiles;  // (the kernel's tile count stays below 2^24)
+    if (fit < m) m = fit;
+    if (m > nb) m = nb;
+    if (m >= 1) {
+      const Plan alt = plan_of(m);
+      if (alt.cfg.kernel == blkattn::Kernel::DecodeTc) {
+        nb = m;
+        pl = alt;
+      }
+    }
+    if (pl.cfg.kernel == blkattn::Kernel::CudaCore && nb * pl.cfg.row_groups > 65535) {  // grid z
+      nb = 65535 / pl.cfg.row_groups;
+      if (nb < 1) return BLKATTN_ERR_UNSUPPORTED;
+      pl = plan_of(nb);
+    }
+  } else if (pl.cfg.kernel == blkattn::Kernel::CudaCore && pl.cfg.row_groups > 65535) {
+    return BLKATTN_ERR_UNSUPPORTED;
+  }
+  if (pl.ws_bytes > 0 && (st = ensure_workspace(ds, (size_t)pl.ws_bytes, stream)) != BLKATTN_OK) return st;
+  if (pl.units > 0 && (st = ensure_counters(ds, pl.units, stream)) != BLKATTN_OK) return st;
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return cuda_fail(e);
+  CUtensorMap mk, mv, mq, mo;
+  const bool prefill = pl.cfg.kernel == blkattn::Kernel::Prefill;
+  bool o_tma = false;
+  if (pl.cfg.kernel != blkattn::Kernel::CudaCore) {
+    const int box = pt.rows < 128 ? pt.rows : 128;
+    if ((st = kv_tensor_map(dev, k_pages, box, &mk)) != BLKATTN_OK) return st;
+    if ((st = kv_tensor_map(dev, v_pages, box, &mv)) != BLKATTN_OK) return st;
+    if (prefill) {
+      if ((st = kv_tensor_map(dev, q, 128, &mq)) != BLKATTN_OK) return st;
+      mo = mq;  // not read unless o_tma
+      o_tma = out_tma_ok(out);
+      if (o_tma && (st = tensor_map(dev, out, 32, 32, &mo)) != BLKATTN_OK) return st;
+    }
+  }
+  for (int64_t b0 = 0; b0 < c.B; b0 += nb) {
+    Checked cs = c;
+    cs.B = c.B - b0 < nb ? c.B - b0 : nb;
+    Plan ps = pl;
+    if (cs.B != nb && !prefill) {
+      ps = plan_of(cs.B);  // the last slice: its own split (never more scratch than the full ones' maximum below)
+      if (ps.ws_bytes > 0 && (st = ensure_workspace(ds, (size_t)ps.ws_bytes, stream)) != BLKATTN_OK) return st;
+    }
+    FwdParams p = fill_params(q, &kc, &vc, seqlens_k, q_logical_pos, tree, nullptr, scale, out, lse, cs, ps, ds->ws,
+                              ds->err, ds->cnt);
+    p.pages = pt;
+    p.pages.table += b0 * pt.sb;
+    p.q = static_cast<const char*>(p.q) + b0 * p.q_sb * elt_bytes(q->dtype);
+    p.seqlens += b0 * p.sl_s;
+    p.qpos += b0 * p.qp_sb;
+    if (p.tree) p.tree += b0 * p.tr_sb;
+    p.out = static_cast<char*>(p.out) + b0 * p.o_sb * elt_bytes(out->dtype);
+    p.lse += b0 * p.l_sb;
+    cudaError_t le;
+    if (prefill) {
+      p.o_tma = o_tma ? 1 : 0;
+      p.o_vec16 = out_vec16_ok(out) ? 1 : 0;
+      le = blkattn::launch_prefill_tc_paged(p, ps.cfg.row_groups, mq, mk, mv, mo, stream);
+    } else if (ps.cfg.kernel == blkattn::Kernel::DecodeTc) {
+      le = blkattn::launch_decode_tc_paged(p, (int)c.d, (int)ps.ctas, mk, mv, stream);
+    } else {
+      le = blkattn::launch_decode_split_paged(p, c.elt, (int)c.d, ps.cfg, stream);
+      if (le == cudaSuccess && ps.cfg.n_splits > 1) le = blkattn::launch_split_merge(p, (int)c.d, stream);
+    }
+    if (le != cudaSuccess) return cuda_fail(le);
+  }
+  return BLKATTN_OK;
 }
 
 // CUDA failures of entry points outside this file: recorded for
@@ -900,6 +1027,14 @@ int blkattn_fwd_window(const blkattn_tensor* q, const blkattn_tensor* k, const b
                        const blkattn_tensor* lse, blkattn_stream_t stream_) {
   if (window < 1) return BLKATTN_ERR_INVALID_ARG;
   return blkattn::fwd_impl(q, k, v, seqlens_k, q_logical_pos, nullptr, window, mask_bias, scale, out, lse, stream_);
+}
+
+int blkattn_fwd_paged(const blkattn_tensor* q, const blkattn_tensor* k_pages, const blkattn_tensor* v_pages,
+                      const blkattn_tensor* page_table, const blkattn_tensor* seqlens_k,
+                      const blkattn_tensor* q_logical_pos, const blkattn_tensor* tree_mask, int64_t window, float scale,
+                      const blkattn_tensor* out, const blkattn_tensor* lse, blkattn_stream_t stream_) {
+  return blkattn::fwd_paged_impl(q, k_pages, v_pages, page_table, seqlens_k, q_logical_pos, tree_mask, window, scale,
+                                 out, lse, stream_);
 }
 
 int blkattn_bwd(const blkattn_tensor* q, const blkattn_tensor* k, const blkattn_tensor* v,

@@ -104,7 +104,10 @@ struct DecodeLayout {
   static_assert(kRedBytes <= kKvBytes, "reduction area must fit in the ring");
 };
 
-template <typename T, int D, int R, int NW, int STAGES>
+// PAGED: the cache lies in pages (paged.h): rows are looked up one by one, a
+// key without a page is not visible, and the value product skips every key
+// that no row of the CTA sees (rows never written may hold anything).
+template <typename T, int D, int R, int NW, int STAGES, bool PAGED>
 __global__ void __launch_bounds__((NW + 1) * 32)
     decode_split_kernel(const FwdParams p) {
   using L = DecodeLayout<T, D, R, NW, STAGES>;
@@ -201,8 +204,8 @@ __global__ void __launch_bounds__((NW + 1) * 32)
   if (warp == NW) {
     // ---------------- producer warp: bulk copies of K and V rows ----------------
     const uint64_t pol = policy_evict_first();
-    const char* kbase = p.k + (int64_t)b * p.k_sb + (int64_t)hk * p.k_sh;
-    const char* vbase = p.v + (int64_t)b * p.v_sb + (int64_t)hk * p.v_sh;
+    const char* kbase = p.k + (PAGED ? 0 : (int64_t)b * p.k_sb) + (int64_t)hk * p.k_sh;
+    const char* vbase = p.v + (PAGED ? 0 : (int64_t)b * p.v_sb) + (int64_t)hk * p.v_sh;
     int t = 0;
     for (; t < n_tiles; ++t) {
       const int st = t % STAGES;
@@ -222,6 +225,14 @@ __global__ void __launch_bounds__((NW + 1) * 32)
       if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(2 * nrows * kRowBytes));
       __syncwarp();
       for (int r = lane; r < nrows; r += 32) {
+        if constexpr (PAGED) {
+          // (a key without a page copies page 0's row, which no row sees)
+          const int64_t page = max(0, page_of(p.pages, b, key0 + r));
+          const int64_t row = (key0 + r) & (p.pages.rows - 1);
+          bulk_g2s(kdst + r * kRowPad, kbase + page * p.k_sb + row * p.k_st, kRowBytes, &full[st], pol);
+          bulk_g2s(vdst + r * kRowPad, vbase + page * p.v_sb + row * p.v_st, kRowBytes, &full[st], pol);
+          continue;
+        }
         bulk_g2s(kdst + r * kRowPad, kbase + (int64_t)(key0 + r) * p.k_st, kRowBytes, &full[st], pol);
         bulk_g2s(vdst + r * kRowPad, vbase + (int64_t)(key0 + r) * p.v_st, kRowBytes, &full[st], pol);
       }
@@ -284,10 +295,12 @@ __global__ void __launch_bounds__((NW + 1) * 32)
         }
       }
       float s[R];
+      const bool has_page = !PAGED || (key < cta_end && page_of(p.pages, b, key) >= 0);
+      bool seen = false;  // by any row
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], 16);
-        bool vis = key < row_hi[r] && key >= row_lo[r];
+        bool vis = has_page && key < row_hi[r] && key >= row_lo[r];
         if (key >= tbase) {
           const int node = key - tbase;
           vis = vis && node < 64 && ((row_tree[r] >> (node & 63)) & 1ull);
@@ -299,7 +312,9 @@ __global__ void __launch_bounds__((NW + 1) * 32)
           vis = bias != kNegInf;
         }
         s[r] = vis ? fmaf(acc[r], p.scale_log2, bias * kLog2e) : kNegInf;
+        seen = seen || vis;
       }
+      const unsigned alive = PAGED ? __ballot_sync(0xffffffffu, seen) : 0xffffffffu;  // bit j: key j of the warp's 16
 
       // block statistics and the online merge (eqs. 33.3-33.5, valid flags)
       float pr[R];
@@ -331,6 +346,7 @@ __global__ void __launch_bounds__((NW + 1) * 32)
       const unsigned char* vrow = vst + (warp * 16) * kRowPad + lane * DPL * EltTraits<T>::kBytes;
 #pragma unroll 4
       for (int j = 0; j < nk; ++j) {
+        if (PAGED && !((alive >> j) & 1u)) continue;
         float vf[DPL];
         load_v<T, DPL>(vrow + j * kRowPad, vf);
         float pj[R];
@@ -448,28 +464,39 @@ __global__ void __launch_bounds__((NW + 1) * 32)
   }
 }
 
-template <typename T, int D, int R, int NW, int STAGES>
+template <typename T, int D, int R, int NW, int STAGES, bool PAGED>
 cudaError_t launch_one(const FwdParams& p, const DecodeConfig& cfg, cudaStream_t stream) {
   using L = DecodeLayout<T, D, R, NW, STAGES>;
-  auto kern = decode_split_kernel<T, D, R, NW, STAGES>;
-  static bool attr_set = false;  // per instantiation (one device per process is assumed per call)
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  auto kern = decode_split_kernel<T, D, R, NW, STAGES, PAGED>;
+  static DeviceOnce once;
+  if (cudaError_t e = once.set_smem(reinterpret_cast<const void*>(kern), L::kBytes, false); e != cudaSuccess) return e;
   dim3 grid(cfg.n_splits, p.Hkv, p.B * cfg.row_groups);
   kern<<<grid, (NW + 1) * 32, L::kBytes, stream>>>(p);
   return cudaGetLastError();
 }
 
-template <typename T, int D, int NW, int STAGES>
+template <typename T, int D, int NW, int STAGES, bool PAGED>
 cudaError_t dispatch_rows(const FwdParams& p, const DecodeConfig& cfg, cudaStream_t s) {
   switch (cfg.rows_per_cta) {
-    case 1: return launch_one<T, D, 1, NW, STAGES>(p, cfg, s);
-    case 2: return launch_one<T, D, 2, NW, STAGES>(p, cfg, s);
-    case 4: return launch_one<T, D, 4, NW, STAGES>(p, cfg, s);
-    case 8: return launch_one<T, D, 8, NW, STAGES>(p, cfg, s);
+    case 1: return launch_one<T, D, 1, NW, STAGES, PAGED>(p, cfg, s);
+    case 2: return launch_one<T, D, 2, NW, STAGES, PAGED>(p, cfg, s);
+    case 4: return launch_one<T, D, 4, NW, STAGES, PAGED>(p, cfg, s);
+    case 8: return launch_one<T, D, 8, NW, STAGES, PAGED>(p, cfg, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <bool PAGED>
+cudaError_t dispatch_types(const FwdParams& p, Elt elt, int d, const DecodeConfig& cfg, cudaStream_t stream) {
+  if (cfg.warps != 4) return cudaErrorInvalidValue;
+  if (elt == Elt::BF16) {
+    if (cfg.stages != 3) return cudaErrorInvalidValue;
+    if (d == 128) return dispatch_rows<__nv_bfloat16, 128, 4, 3, PAGED>(p, cfg, stream);
+    if (d == 64) return dispatch_rows<__nv_bfloat16, 64, 4, 3, PAGED>(p, cfg, stream);
+  } else {
+    if (cfg.stages != 2) return cudaErrorInvalidValue;
+    if (d == 128) return dispatch_rows<float, 128, 4, 2, PAGED>(p, cfg, stream);
+    if (d == 64) return dispatch_rows<float, 64, 4, 2, PAGED>(p, cfg, stream);
   }
   return cudaErrorInvalidValue;
 }
@@ -488,17 +515,12 @@ size_t decode_smem_bytes(Elt elt, int d, const DecodeConfig& cfg) {
 
 cudaError_t launch_decode_split(const FwdParams& p, Elt elt, int d, const DecodeConfig& cfg,
                                 cudaStream_t stream) {
-  if (cfg.warps != 4) return cudaErrorInvalidValue;
-  if (elt == Elt::BF16) {
-    if (cfg.stages != 3) return cudaErrorInvalidValue;
-    if (d == 128) return dispatch_rows<__nv_bfloat16, 128, 4, 3>(p, cfg, stream);
-    if (d == 64) return dispatch_rows<__nv_bfloat16, 64, 4, 3>(p, cfg, stream);
-  } else {
-    if (cfg.stages != 2) return cudaErrorInvalidValue;
-    if (d == 128) return dispatch_rows<float, 128, 4, 2>(p, cfg, stream);
-    if (d == 64) return dispatch_rows<float, 64, 4, 2>(p, cfg, stream);
-  }
-  return cudaErrorInvalidValue;
+  return dispatch_types<false>(p, elt, d, cfg, stream);
+}
+
+cudaError_t launch_decode_split_paged(const FwdParams& p, Elt elt, int d, const DecodeConfig& cfg,
+                                      cudaStream_t stream) {
+  return dispatch_types<true>(p, elt, d, cfg, stream);
 }
 
 }  // namespace blkattn

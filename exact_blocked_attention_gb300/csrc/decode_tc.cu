@@ -81,9 +81,7 @@ constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLazyRescale = 8.f;
 
 constexpr int BK = 128;               // keys per tile (TMEM lanes of S^T)
-constexpr int D = 128;                // head dim (TMEM lanes of U^T)
 constexpr int kBox = BK * 128;        // 128 rows x 64 dims, bf16: 16 KB
-constexpr int kSlotBytes = 2 * kBox;  // 128 rows x 128 dims
 constexpr int kKeyWarps = 8;   // two warps per TMEM lane quarter, each with half of the rows
 constexpr int kKeyThreads = 32 * kKeyWarps;
 constexpr int kTmaWarp = 8;
@@ -106,23 +104,27 @@ struct RowFacts {
                      // with a sliding window instead: the row's first visible key
   int end[NR];       // visible keys are [0, end): min(len, pos + 1), 0 for padding rows
   int unit_end;      // max over the rows
+  int unit_start;    // paged cache: the earliest key that a row sees (INT_MAX: none)
   int min_end;       // min over the real rows
   int tree_base;     // first key of the token tree (len - T_q); INT_MAX without a tree
   int win_max;       // sliding window: the largest first visible key of the rows (0 without)
 };
 
-template <int NR>
+template <int NR, int D>
 struct TcLayout {
+  static constexpr int kBoxes = D / 64;               // 64-dim boxes of a row
+  static constexpr int kSlotBytes = kBoxes * kBox;    // 128 rows x D dims
   // Up to 32 rows, P_hi and P_lo share one 64-column atom (P_lo from column
   // NR, the product's N = 2 NR), which leaves room for a fifth ring slot;
   // 48 rows take two atoms (P_lo from column 64, N = 64 + NR) and four slots.
   static constexpr bool kPacked = NR <= 32;
-  static constexpr int kSlots = kPacked ? 5 : 4;
+  // (the same bytes in flight for heads of 64: twice the slots of half the size)
+  static constexpr int kSlots = (kPacked ? 5 : 4) * (2 / kBoxes);
   static constexpr int kLo = kPacked ? NR : 64;          // column of P_lo / U_lo
   static constexpr int kPVN = kPacked ? 2 * NR : 64 + NR;  // N of the PV product
   static constexpr int kPBytes = kPacked ? kBox : 2 * kBox;  // one P^T buffer
   static constexpr int kQBox = NR * 128;  // NR rows x 64 dims
-  static constexpr int kQBytes = 2 * kQBox;
+  static constexpr int kQBytes = kBoxes * kQBox;
   static constexpr int kOffRing = 0;
   static constexpr int kOffQ = kSlots * kSlotBytes;              // two query buffers
   static constexpr int kOffP = kOffQ + 2 * kQBytes;              // two P^T buffers
@@ -256,11 +258,25 @@ __device__ __forceinline__ int scatter_base(int lane) {
   return ((lane >> 4) & 1) * (NH / 2) + ((lane >> 3) & 1) * (NH / 4) + ((lane >> 2) & 1) * (NH / 8);
 }
 
-template <int NR>
+// D: head dim, 128 or 64.  With 64 the value product still has M = 128: its
+// upper 64 TMEM lanes take whatever the next 16 KB of shared memory hold (the
+// next ring slot, past the last one the query and P buffers) and nothing reads
+// them.
+//
+// PAGED: the cache lies in pages (paged.h).  A tile of 128 keys is one box of
+// a page of at least 128 rows, or the boxes of 128 / P pages: the producer
+// warp's lanes each look one page up (a tile ahead) and issue its copies.  A
+// page number outside the pool goes to the copy as -1, which lies outside the
+// tensor map and reads as zeros, and the key threads mask its keys.  V rows
+// that no row of the unit sees (before a window, past the end, unlisted tree
+// nodes) are zero-filled in shared memory: rows of a page that were never
+// written may hold anything.
+template <int NR, int D, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_tc_kernel(const FwdParams p, const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv) {
-  using L = TcLayout<NR>;
+  using L = TcLayout<NR, D>;
+  constexpr int kSlotBytes = L::kSlotBytes;
   constexpr uint32_t kIdescQK = tc::idesc_bf16(128, NR, 0, 0);  // K, Q both K-major
   // V^T, P^T both MN-major; N spans the P_hi atom (NR used of 64) and the P_lo atom
   constexpr uint32_t kIdescPV = tc::idesc_bf16(128, L::kPVN, 1, 1);
@@ -464,7 +480,78 @@ __global__ void __launch_bounds__(kThreads, 1)
   // a range may start among a unit's weight-only tiles: begin at the next unit
   if (t0 < t1 && cur.j >= cur.n) cur.step_unit(ntab, RG, Hkv, B);
 
-  if (warp == kTmaWarp) {
+  if (PAGED && warp == kTmaWarp) {
+    // ---------------- producer: K and V tiles from pages (whole warp) ----------------
+    const uint64_t pol = policy_evict_first();
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmk)) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmv)) : "memory");
+    }
+    // lane: box `half` of piece `piece` of a tile; a piece is a page or the
+    // tile's part of one
+    const int box_shift = min(p.pages.shift, 7);
+    const int n_pieces = BK >> box_shift;
+    const int piece = lane & (n_pieces - 1);
+    const int half = lane >> (7 - box_shift);
+    const bool copies = half < L::kBoxes;
+    const uint32_t dst_off = (uint32_t)(half * kBox + (piece << box_shift) * 128);
+    int len_b = -1, len = 0;
+    // the lane's page for the tile at cursor c: -1 (zeros) past the length
+    auto look_up = [&](const Cursor& c) {
+      if (c.b != len_b) {
+        len_b = c.b;
+        len = min(p.seqlens[c.b * p.sl_s], p.Tmax);
+      }
+      const int key = c.key0() + (piece << box_shift);
+      return key < len ? page_of(p.pages, c.b, key) : -1;
+    };
+    int64_t issued = 0;
+    bool ok = true;
+    int page = cur.t < t1 ? look_up(cur) : -1;
+    for (int64_t g = 0; ok && cur.t < t1; ++g) {
+      const int row = (cur.key0() + (piece << box_shift)) & (p.pages.rows - 1);
+      const int kvh = cur.kvh;
+      cur.next(ntab, RG, Hkv, B);
+      const int page_next = cur.t < t1 ? look_up(cur) : -1;  // (the load is in flight meanwhile)
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const int64_t seq = 2 * g + kv;
+        const int s = (int)(seq % kSlots);
+        bool w = true;
+        if (lane == 0) {
+          if (seq >= kSlots) w = mbar_wait(&empty[s], (uint32_t)(((seq / kSlots) - 1) & 1));
+          if (w) mbar_arrive_expect_tx(&full[s], kSlotBytes);
+        }
+        if (!__shfl_sync(0xffffffffu, w, 0)) {  // (also orders the expected bytes before the copies)
+          ok = false;
+          break;
+        }
+        __syncwarp();
+        if (copies)
+          tma_load_4d(sm + L::kOffRing + s * kSlotBytes + dst_off,
+                      kv ? static_cast<const void*>(&tmv) : static_cast<const void*>(&tmk), 64 * half, row, kvh, page,
+                      &full[s], pol);
+        issued = seq + 1;
+      }
+      // (as below: the first unit's query rows before the stream goes on)
+      if (ok && g == 0) {
+        bool w = true;
+        if (lane == 0) w = mbar_wait(&q_full[0], 0);
+        ok = __shfl_sync(0xffffffffu, w, 0);
+      }
+      page = page_next;
+    }
+    __syncwarp();
+    if (lane == 0) {
+      // every issued copy must land before the CTA exits
+      for (int64_t seq = issued - kSlots < 0 ? 0 : issued - kSlots; seq < issued; ++seq)
+        if (!mbar_wait(&full[seq % kSlots], (uint32_t)((seq / kSlots) & 1))) ok = false;
+      if (!ok) {
+        record_error(p.err, kErrTimeout);
+        misc[1] = 1;
+      }
+    }
+  } else if (warp == kTmaWarp) {
     // ---------------- producer: K and V tiles ----------------
     const uint64_t pol = policy_evict_first();
     if (lane == 0) {
@@ -547,12 +634,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // asynchronous copies that bypass the registers: all of them are in
       // flight at once whatever the row count (rows past the unit's end are
       // zero-filled); they complete before the rows are announced below
+      constexpr int kRowChunks = D / 8, kRowsIt = 32 / kRowChunks;
 #pragma unroll
-      for (int it = 0; it < NR / 2; ++it) {
-        // chunk (lane & 15) of row 2 it + (lane >> 4), described by lane (row & 31)
-        const int r = 2 * it + (lane >> 4);
-        const int c = lane & 15;
-        const int set = (2 * it) >> 5;  // rows of this iteration are all < 32 or all >= 32
+      for (int it = 0; it < NR / kRowsIt; ++it) {
+        // one 16-byte chunk of one row a lane; the row is described by lane (row & 31)
+        const int r = kRowsIt * it + lane / kRowChunks;
+        const int c = lane % kRowChunks;
+        const int set = (kRowsIt * it) >> 5;  // rows of this iteration are all < 32 or all >= 32
         const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(
             __shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(qrow[set]), r & 31));
         const bool rr = __shfl_sync(0xffffffffu, real[set], r & 31);
@@ -562,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // integer facts of the rows
       const int len = len_raw < 0 ? 0 : (len_raw > p.Tmax ? p.Tmax : len_raw);
       RowFacts<NR>& rf = facts0[qb];
-      int umax = 0, umin = 0x7fffffff, wmax = 0;
+      int umax = 0, umin = 0x7fffffff, wmax = 0, ustart = 0x7fffffff;
 #pragma unroll
       for (int h2 = 0; h2 < 2; ++h2) {
         const int r = lane + 32 * h2;
@@ -577,6 +665,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (p.window > 0) {  // the row's first visible key (no overflow: pos >= 0 first)
             tr = (uint64_t)(pos[h2] < 0 ? 0 : max(0, pos[h2] - p.window + 1));
             wmax = max(wmax, (int)tr);
+          }
+          if (PAGED) {
+            const int lo = p.window > 0 ? (int)tr : 0;
+            if (lo < e) ustart = min(ustart, lo);
           }
           bo = (int64_t)b * p.bi_sb + (int64_t)h * p.bi_sh + (int64_t)i * p.bi_si;
           oo = (int64_t)b * p.o_sb + (int64_t)h * p.o_sh + (int64_t)i * p.o_si;
@@ -595,9 +687,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         umax = max(umax, __shfl_xor_sync(0xffffffffu, umax, off));
         umin = min(umin, __shfl_xor_sync(0xffffffffu, umin, off));
         wmax = max(wmax, __shfl_xor_sync(0xffffffffu, wmax, off));
+        if (PAGED) ustart = min(ustart, __shfl_xor_sync(0xffffffffu, ustart, off));
       }
       if (lane == 0) {
         rf.unit_end = umax;
+        rf.unit_start = ustart;
         rf.min_end = umin;
         rf.tree_base = p.tree != nullptr ? len - p.Tq : 0x7fffffff;
         rf.win_max = wmax;
@@ -718,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity));
     };
-    const bool has_bias = p.bias != nullptr;
+    const bool has_bias = !PAGED && p.bias != nullptr;
     float lp[NH];  // this thread's partial sums of P over its keys
 #pragma unroll
     for (int r = 0; r < NH; ++r) lp[r] = 0.f;
@@ -756,6 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row = c0 + r;
           if (row >= rr) break;
           const float o = (s_mfin[row] == kNegInf) ? 0.f : u[r] * s_inv[row];
+          if (D < 128 && k >= D) break;  // (lanes past the value dims)
           const int64_t oi = pf.ooff[row] + (int64_t)k * p.o_sd;
           if (p.out_bf16)
             static_cast<__nv_bfloat16*>(p.out)[oi] = __float2bfloat16_rn(o);
@@ -776,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int r = 0; r < NH; ++r) {
           const int row = c0 + r;
-          if (row >= rr) break;
+          if (row >= rr || (D < 128 && k >= D)) break;
           st_global_hint(p.ws_u + ((slot * R + row) * D) + k, u[r], keep);
         }
         if (half == 0 && k < rr) {
@@ -878,6 +973,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int key0 = cur.key0();
       const int key = key0 + k;
+      // (looked up before the wait: the load is in flight meanwhile)
+      bool no_page = false;
+      if (PAGED) no_page = key < rf.unit_end && page_of(p.pages, cur.b, key) < 0;
       float x[NH];
       if (has_bias) {
         // this tile's bias (rows of one sequence share lines: L1 hits); a
@@ -918,6 +1016,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int r = 0; r < NH; ++r)
             if (key >= rf.end[c0 + r]) x[r] = kNegInf;
+        }
+        if (PAGED && __any_sync(0xffffffffu, no_page)) {
+#pragma unroll
+          for (int r = 0; r < NH; ++r)
+            if (no_page) x[r] = kNegInf;
         }
         if (key0 < rf.win_max) {
           // sliding window: keys before a row's first visible key
@@ -1029,13 +1132,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4*>(ph + off_lo) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
-      if (cur.j == cur.n - 1 && key0 + BK > rf.unit_end) {
+      if ((cur.j == cur.n - 1 && key0 + BK > rf.unit_end) ||
+          (PAGED && (key0 < rf.unit_start || key0 + BK > rf.tree_base))) {
         // the unit's last tile: zero the V rows past every visible key (each
-        // half of the warps one 64-dim box)
+        // half of the warps one 64-dim box); in pages also those before a
+        // window and of tree nodes that no row lists
         const int64_t sv = 2 * g + 1;
         const bool vok = bar_and(kBarRows, kKeyThreads, wait_all(&full[sv % kSlots], (uint32_t)((sv / kSlots) & 1)));
         if (!vok) { ok = false; break; }
-        if (key >= rf.unit_end) {
+        bool unseen = key >= rf.unit_end;
+        if (PAGED) {
+          unseen = unseen || key < rf.unit_start;
+          const int node = key - rf.tree_base;
+          if (rf.tree_base != 0x7fffffff && node >= 0 && node < 64) {
+            bool seen = false;
+#pragma unroll 1
+            for (int r = 0; r < NR; ++r) seen = seen || (key < rf.end[r] && ((rf.tree[r] >> node) & 1ull));
+            unseen = unseen || !seen;
+          }
+        }
+        if (unseen && half < L::kBoxes) {
           unsigned char* vr = sm + L::kOffRing + (int)(sv % kSlots) * kSlotBytes + half * kBox + k * 128;
 #pragma unroll
           for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vr + ((c ^ (k & 7)) << 4)) = make_uint4(0, 0, 0, 0);
@@ -1099,38 +1215,47 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tc::dealloc(tb, kTmemCols);
 }
 
-template <int NR>
+template <int NR, int D, bool PAGED>
 cudaError_t launch_nr(const FwdParams& p, int ctas, const CUtensorMap& tmk, const CUtensorMap& tmv,
                       cudaStream_t stream) {
-  using L = TcLayout<NR>;
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(decode_tc_kernel<NR>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
-  decode_tc_kernel<NR><<<ctas, kThreads, L::kBytes, stream>>>(p, tmk, tmv);
+  using L = TcLayout<NR, D>;
+  static DeviceOnce once;
+  if (cudaError_t e = once.set_smem(reinterpret_cast<const void*>(&decode_tc_kernel<NR, D, PAGED>), L::kBytes);
+      e != cudaSuccess)
+    return e;
+  decode_tc_kernel<NR, D, PAGED><<<ctas, kThreads, L::kBytes, stream>>>(p, tmk, tmv);
   return cudaGetLastError();
+}
+
+template <int D, bool PAGED>
+cudaError_t launch_rows(const FwdParams& p, int ctas, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                        cudaStream_t stream) {
+  if (p.rows_cta < 1 || p.rows_cta > 48 || ctas < 1 ||
+      p.B * p.row_groups > (p.window > 0 ? kDecodeTcMaxEntries / 2 : kDecodeTcMaxEntries))
+    return cudaErrorInvalidValue;
+  if (p.rows_cta <= 16) return launch_nr<16, D, PAGED>(p, ctas, tmk, tmv, stream);
+  if (p.rows_cta <= 32) return launch_nr<32, D, PAGED>(p, ctas, tmk, tmv, stream);
+  return launch_nr<48, D, PAGED>(p, ctas, tmk, tmv, stream);
 }
 
 }  // namespace
 
 size_t decode_tc_smem_bytes(int nr) {
-  if (nr <= 16) return TcLayout<16>::kBytes;
-  if (nr <= 32) return TcLayout<32>::kBytes;
-  return TcLayout<48>::kBytes;
+  if (nr <= 16) return TcLayout<16, 128>::kBytes;
+  if (nr <= 32) return TcLayout<32, 128>::kBytes;
+  return TcLayout<48, 128>::kBytes;
 }
 
 cudaError_t launch_decode_tc(const FwdParams& p, int ctas, const CUtensorMap& tmk, const CUtensorMap& tmv,
                              cudaStream_t stream) {
-  if (p.rows_cta < 1 || p.rows_cta > 48 || ctas < 1 ||
-      p.B * p.row_groups > (p.window > 0 ? kDecodeTcMaxEntries / 2 : kDecodeTcMaxEntries))
-    return cudaErrorInvalidValue;
-  if (p.rows_cta <= 16) return launch_nr<16>(p, ctas, tmk, tmv, stream);
-  if (p.rows_cta <= 32) return launch_nr<32>(p, ctas, tmk, tmv, stream);
-  return launch_nr<48>(p, ctas, tmk, tmv, stream);
+  return launch_rows<128, false>(p, ctas, tmk, tmv, stream);
+}
+
+cudaError_t launch_decode_tc_paged(const FwdParams& p, int d, int ctas, const CUtensorMap& tmk,
+                                   const CUtensorMap& tmv, cudaStream_t stream) {
+  if (d == 128) return launch_rows<128, true>(p, ctas, tmk, tmv, stream);
+  if (d == 64) return launch_rows<64, true>(p, ctas, tmk, tmv, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace blkattn

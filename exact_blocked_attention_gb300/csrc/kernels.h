@@ -8,6 +8,7 @@
 #include <cstdint>
 
 #include "blkattn.h"
+#include "paged.h"
 
 namespace blkattn {
 
@@ -68,11 +69,17 @@ struct FwdParams {
   // prefill: 1 when the output tensor map (fp32, boxes {32, 32}, 128-byte
   // swizzle) is valid and the kernel stores whole output tiles with TMA
   int o_tma;
+  // prefill: 1 when the output is bf16 with unit dim stride and 16-byte
+  // aligned rows (16-byte stores)
+  int o_vec16;
   // test hook of the tcgen05 decode kernel (-1: none): the MMA-issuing thread
   // of this CTA waits on a barrier nothing completes, gives up after 1 ms
   // and issues no product, so the CTA's other roles run out their bounded
   // waits (blkattn_debug_stall_next_decode)
   int test_stall_cta;
+  // paged cache (blkattn_fwd_paged; the kernels' PAGED forms): k and v point
+  // at the pools and their strides are those of page, head and row in page
+  PageTable pages;
 };
 
 // Split-KV kernel configuration chosen by the planner.
@@ -89,6 +96,8 @@ struct DecodeConfig {
 
 cudaError_t launch_decode_split(const FwdParams& p, Elt elt, int d, const DecodeConfig& cfg,
                                 cudaStream_t stream);
+cudaError_t launch_decode_split_paged(const FwdParams& p, Elt elt, int d, const DecodeConfig& cfg,
+                                      cudaStream_t stream);
 cudaError_t launch_split_merge(const FwdParams& p, int d, cudaStream_t stream);
 
 struct MergeParams {
@@ -115,6 +124,9 @@ size_t decode_mma_smem_bytes(int d, int mt);
 // boxes {32, 32}, 128-byte swizzle.
 cudaError_t launch_prefill_tc(const FwdParams& p, int n_pairs, const CUtensorMap& tmq, const CUtensorMap& tmk,
                               const CUtensorMap& tmv, const CUtensorMap& tmo, cudaStream_t stream);
+// The same over a paged cache (maps of K and V as for launch_decode_tc_paged).
+cudaError_t launch_prefill_tc_paged(const FwdParams& p, int n_pairs, const CUtensorMap& tmq, const CUtensorMap& tmk,
+                                    const CUtensorMap& tmv, const CUtensorMap& tmo, cudaStream_t stream);
 int prefill_tc_smem_bytes();
 
 // Decode / verify on tcgen05 (bf16, d = 128, 16-byte aligned query rows, at
@@ -131,6 +143,10 @@ void clear_static_counters();
 cudaError_t launch_decode_tc(const FwdParams& p, int ctas, const CUtensorMap& tmk, const CUtensorMap& tmv,
                              cudaStream_t stream);
 size_t decode_tc_smem_bytes(int rows_cta);
+// The same over a paged cache, d = 64 or 128; maps over the pools with boxes
+// of 64 dims x min(rows of a page, 128) rows.
+cudaError_t launch_decode_tc_paged(const FwdParams& p, int d, int ctas, const CUtensorMap& tmk,
+                                   const CUtensorMap& tmv, cudaStream_t stream);
 
 // ---- backward pass (eqs. 33.6-33.8), tcgen05, bf16, d = 128 ----
 struct BwdParams {

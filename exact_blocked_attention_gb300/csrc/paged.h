@@ -36,13 +36,15 @@ constexpr int64_t kMinPageRows = 8, kMaxPageRows = 65536;
 // (the attribute belongs to the device's copy of the kernel).
 struct DeviceOnce {
   std::atomic<uint64_t> done{0};  // bit d: device d
-  cudaError_t set_smem(const void* kernel, int bytes) {
+  // carveout: also prefer all of the unified storage as shared memory
+  cudaError_t set_smem(const void* kernel, int bytes, bool carveout = true) {
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e == cudaSuccess && carveout)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
     return e;
   }

@@ -103,7 +103,11 @@ __device__ __forceinline__ int spec_first_tile(int q0, int window) {
   return s0 > 0 ? (int)(s0 / BN) : 0;
 }
 
-template <bool WIN>
+// PAGED: the cache lies in pages (paged.h).  A key tile is one box of a page of
+// at least 128 rows or the boxes of 128 / P pages: the producer warp's lanes
+// look their pages up a tile ahead and issue the copies; a page number outside
+// the pool goes to the copy as -1 (zeros) and the rows mask its keys.
+template <bool WIN, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const FwdParams p, const __grid_constant__ CUtensorMap tmq,
                       const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -182,6 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_load_4d(sm + kOffQ + t * kTileBytes, &tmq, 0, q0 + t * BM, h, b, q_full, pol_q);
       tma_load_4d(sm + kOffQ + t * kTileBytes + kBox, &tmq, 64, q0 + t * BM, h, b, q_full, pol_q);
     }
+    if (!PAGED) {
     // K/V tile 0 of the CTA's range right away; with a window the range
     // starts at the key tile of the CTA's earliest visible key, known only
     // from the positions, so the copy goes to the tile that rows at positions
@@ -194,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_arrive_expect_tx(&v_full[0], kTileBytes);
     tma_load_4d(sm + kOffV, &tmv, 0, key_first, hk, b, &v_full[0], pol_kv);
     tma_load_4d(sm + kOffV + kBox, &tmv, 64, key_first, hk, b, &v_full[0], pol_kv);
+    }
   }
 
   // ---- visibility of the rows (integers) ----
@@ -241,7 +247,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_max = j_hi - j_lo;  // key tiles the CTA loads
   // ring position of the CTA's key tile j: j + ro (ro = 1 when the copy made
   // before the positions were read holds another tile)
-  const int ro = (WIN && j_lo != spec_first_tile(2 * pair * BM, p.window)) ? 1 : 0;
+  const int ro = (WIN && !PAGED && j_lo != spec_first_tile(2 * pair * BM, p.window)) ? 1 : 0;
+  // paged cache: the CTA's earliest visible key (V rows before it are zeroed)
+  const int cta_start = WIN && PAGED ? min(n_t0 > 0 ? misc[6] : 0x7fffffff, n_t1 > 0 ? misc[8] : 0x7fffffff) : 0;
   const int cta_end = max(n_t0 > 0 ? misc[1] : 0, n_t1 > 0 ? misc[3] : 0);
   const int64_t out_row = (int64_t)b * p.o_sb + (int64_t)h * p.o_sh + (int64_t)row_i * p.o_si;
   const int64_t lse_idx = (int64_t)b * p.l_sb + (int64_t)h * p.l_sh + (int64_t)row_i * p.l_si;
@@ -266,9 +274,64 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (my_row) write_empty_row();
     if (warp == kTmaWarp && lane == 0) {
       bool landed = mbar_wait(q_full, 0);
-      landed = mbar_wait(&k_full[0], 0) && landed;
-      landed = mbar_wait(&v_full[0], 0) && landed;
+      if (!PAGED) {
+        landed = mbar_wait(&k_full[0], 0) && landed;
+        landed = mbar_wait(&v_full[0], 0) && landed;
+      }
       if (!landed) record_error(p.err, kErrTimeout);
+    }
+  } else if (PAGED && warp == kTmaWarp) {
+    // ---------------- TMA producer, pages (whole warp) ----------------
+    const int box_shift = min(p.pages.shift, 7);
+    const int n_pieces = BN >> box_shift;
+    const int piece = lane & (n_pieces - 1);  // of the tile's keys
+    const int half = lane >> (7 - box_shift);  // 64-dim box
+    const uint32_t dst_off = (uint32_t)(half * kBox + (piece << box_shift) * 128);
+    auto look_up = [&](int j) {  // this lane's page of key tile j: -1 (zeros) past the rows' ends
+      const int key = (j_lo + j) * BN + (piece << box_shift);
+      return j < n_max && key < cta_end ? page_of(p.pages, b, key) : -1;
+    };
+    int issued = 0;  // ring positions whose K and V copies were both issued
+    int k_issued = 0;
+    bool ok = true;
+    int page = look_up(0);
+    for (int j = 0; j < n_max && ok; ++j) {
+      const int s = j % STAGES;
+      const int row = ((j_lo + j) * BN + (piece << box_shift)) & (p.pages.rows - 1);
+      const int page_next = look_up(j + 1);  // (the load is in flight meanwhile)
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        uint64_t* full = kv ? &v_full[s] : &k_full[s];
+        bool w = true;
+        if (lane == 0) {
+          if (j >= STAGES) w = mbar_wait(kv ? &v_empty[s] : &k_empty[s], ((j / STAGES) - 1) & 1);
+          if (w) mbar_arrive_expect_tx(full, kTileBytes);
+        }
+        if (!__shfl_sync(0xffffffffu, w, 0)) {  // (also orders the expected bytes before the copies)
+          ok = false;
+          break;
+        }
+        __syncwarp();
+        if (half < 2)
+          tma_load_4d(sm + (kv ? kOffV : kOffK) + s * kTileBytes + dst_off,
+                      kv ? static_cast<const void*>(&tmv) : static_cast<const void*>(&tmk), 64 * half, row, hk, page,
+                      full, pol_kv);
+        if (kv == 0) k_issued = j + 1; else issued = j + 1;
+      }
+      page = page_next;
+    }
+    __syncwarp();
+    if (lane == 0) {
+      // every issued copy must land before the CTA can exit
+      if (!mbar_wait(q_full, 0)) ok = false;
+      for (int j = k_issued - STAGES < 0 ? 0 : k_issued - STAGES; j < k_issued; ++j)
+        if (!mbar_wait(&k_full[j % STAGES], (j / STAGES) & 1)) ok = false;
+      for (int j = issued - STAGES < 0 ? 0 : issued - STAGES; j < issued; ++j)
+        if (!mbar_wait(&v_full[j % STAGES], (j / STAGES) & 1)) ok = false;
+      if (!ok) {
+        record_error(p.err, kErrTimeout);
+        misc[5] = 1;
+      }
     }
   } else if (warp == kTmaWarp) {
     // ---------------- TMA producer ----------------
@@ -421,8 +484,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         return __all_sync(0xffffffffu, mbar_wait(bar, parity));
       };
       for (int j = 0; j < n_mine; ++j) {
+        // paged cache: bit i: piece i of this key tile has no page (looked up
+        // before the wait: the load is in flight meanwhile)
+        unsigned gone = 0;
+        if (PAGED) {
+          const int box_shift = min(p.pages.shift, 7);
+          const int key = (f_mine + j) * BN + (lane << box_shift);
+          const bool none = lane < (BN >> box_shift) && key < cta_end && page_of(p.pages, b, key) < 0;
+          gone = __ballot_sync(0xffffffffu, none);
+        }
         if (!wait_all(&s_full[x], j & 1)) { ok = false; break; }
         tc::fence_after();
+        if (PAGED && gone != 0) {
+          // their scores become -inf in tensor memory, 8 keys at a time (no
+          // register of the ordinary tiles is spent on it)
+          const int box_shift = min(p.pages.shift, 7);
+          uint32_t neg[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) neg[c] = __float_as_uint(kNegInf);
+#pragma unroll 1
+          for (int c8 = 0; c8 < BN / 8; ++c8)
+            if ((gone >> ((8 * c8) >> box_shift)) & 1u) tc::st8(tl + kColS + 8 * c8, neg);
+          tc::wait_st();
+        }
         float xs[128];
         {
           // all four 32-column loads in flight, one wait
@@ -541,16 +625,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 t2 = __fadd2_rn(a, c2);
           l += t2.x + t2.y;
         }
-        if (key0 + BN > cta_end) {
+        if (key0 + BN > cta_end || (WIN && PAGED && key0 < cta_start)) {
           // last tile of the CTA: zero the V rows past every visible key of
-          // both query tiles (both may do it; the values are the same)
+          // both query tiles (both may do it; the values are the same); in
+          // pages also those before every row's window
           const int u = f_mine - j_lo + j + ro;  // ring position of this key tile
           const int s = u % STAGES;
           if (!wait_all(&v_full[s], (u / STAGES) & 1)) { ok = false; break; }
           unsigned char* vt = sm + kOffV + s * kTileBytes;
-          const int z0 = cta_end - key0;
-          for (int idx = (int)(threadIdx.x & 127); idx < (BN - z0) * 16; idx += 128) {
-            const int r = z0 + (idx >> 4);
+          const int z0 = WIN && PAGED ? min(max(cta_end - key0, 0), BN) : cta_end - key0;
+          const int z1 = WIN && PAGED ? min(max(cta_start - key0, 0), BN) : 0;
+          const int nz = BN - z0 + z1;  // rows [z0, BN), then [0, z1)
+          for (int idx = (int)(threadIdx.x & 127); idx < nz * 16; idx += 128) {
+            int r = z0 + (idx >> 4);
+            if (WIN && PAGED && r >= BN) r -= BN;
             const int c = idx & 15;  // 16-byte chunk over the 128 dims (two boxes)
             *reinterpret_cast<uint4*>(vt + (c >> 3) * kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
                 make_uint4(0, 0, 0, 0);
@@ -639,6 +727,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int q4 = 0; q4 < 4; ++q4) tma_store_4d(&tmo, stage + q4 * 4096, 32 * q4, row_w, h, b);
             bulk_commit();
           }
+        } else if (p.o_vec16) {
+          // bf16 rows, staged like the fp32 ones: 64 dims at a time, rows
+          // padded to 144 bytes, stored back 8 lanes to a row (128 contiguous
+          // bytes per row per store instruction)
+          constexpr int kRow = 36;  // words
+          uint32_t* stg = reinterpret_cast<uint32_t*>(sm + (x == 0 ? kOffK : kOffV) + (warp & 3) * 32 * kRow * 4);
+          const int r0 = (2 * pair + x) * BM + 32 * (warp & 3);
+          const int rows = min(32, p.Tq - r0);
+          __nv_bfloat16* dst0 =
+              static_cast<__nv_bfloat16*>(p.out) + (int64_t)b * p.o_sb + (int64_t)h * p.o_sh + (int64_t)r0 * p.o_si;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll 1
+            for (int q2 = 0; q2 < 2; ++q2) {
+              uint32_t r[32];
+              tc::ld32(tl + kColO + 64 * half + 32 * q2, r);
+              tc::wait_ld();
+#pragma unroll
+              for (int c = 0; c < 32; c += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  w[e] = pack_bf16(__uint_as_float(r[c + 2 * e]) * inv, __uint_as_float(r[c + 2 * e + 1]) * inv);
+                *reinterpret_cast<uint4*>(stg + lane * kRow + 16 * q2 + c / 2) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int it = 0; it < 8; ++it) {
+              const int rr = 4 * it + (lane >> 3);
+              if (rr < rows)
+                *reinterpret_cast<uint4*>(dst0 + rr * p.o_si + 64 * half + 8 * (lane & 7)) =
+                    *reinterpret_cast<const uint4*>(stg + rr * kRow + 4 * (lane & 7));
+            }
+            __syncwarp();
+          }
         } else {
           // the tensor-memory loads are warp-collective: every lane takes
           // part, rows past Tq store nothing
@@ -678,28 +802,41 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 int prefill_tc_smem_bytes() { return kSmemBytes; }
 
-cudaError_t launch_prefill_tc(const FwdParams& p, int n_pairs, const CUtensorMap& tmq, const CUtensorMap& tmk,
-                              const CUtensorMap& tmv, const CUtensorMap& tmo, cudaStream_t stream) {
-  static bool attr_set = false;
-  if (!attr_set) {
-    for (const void* f : {(const void*)prefill_tc_kernel<false>, (const void*)prefill_tc_kernel<true>}) {
-      cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-      if (e != cudaSuccess) return e;
-      e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-      if (e != cudaSuccess) return e;
-    }
-    attr_set = true;
-  }
+namespace {
+
+template <bool WIN, bool PAGED>
+cudaError_t launch_kernel(const FwdParams& p, unsigned blocks, const CUtensorMap& tmq, const CUtensorMap& tmk,
+                          const CUtensorMap& tmv, const CUtensorMap& tmo, cudaStream_t stream) {
+  static DeviceOnce once;
+  if (cudaError_t e = once.set_smem(reinterpret_cast<const void*>(&prefill_tc_kernel<WIN, PAGED>), kSmemBytes);
+      e != cudaSuccess)
+    return e;
+  prefill_tc_kernel<WIN, PAGED><<<blocks, kThreads, kSmemBytes, stream>>>(p, tmq, tmk, tmv, tmo);
+  return cudaGetLastError();
+}
+
+template <bool PAGED>
+cudaError_t launch_form(const FwdParams& p, int n_pairs, const CUtensorMap& tmq, const CUtensorMap& tmk,
+                        const CUtensorMap& tmv, const CUtensorMap& tmo, cudaStream_t stream) {
   const int64_t heads = (int64_t)p.Hq * p.B;
   if (p.head_group < 1) return cudaErrorInvalidValue;
   const int64_t groups = (heads + p.head_group - 1) / p.head_group;
   const int64_t blocks = groups * p.head_group * n_pairs;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  if (p.window > 0)
-    prefill_tc_kernel<true><<<(unsigned)blocks, kThreads, kSmemBytes, stream>>>(p, tmq, tmk, tmv, tmo);
-  else
-    prefill_tc_kernel<false><<<(unsigned)blocks, kThreads, kSmemBytes, stream>>>(p, tmq, tmk, tmv, tmo);
-  return cudaGetLastError();
+  if (p.window > 0) return launch_kernel<true, PAGED>(p, (unsigned)blocks, tmq, tmk, tmv, tmo, stream);
+  return launch_kernel<false, PAGED>(p, (unsigned)blocks, tmq, tmk, tmv, tmo, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_tc(const FwdParams& p, int n_pairs, const CUtensorMap& tmq, const CUtensorMap& tmk,
+                              const CUtensorMap& tmv, const CUtensorMap& tmo, cudaStream_t stream) {
+  return launch_form<false>(p, n_pairs, tmq, tmk, tmv, tmo, stream);
+}
+
+cudaError_t launch_prefill_tc_paged(const FwdParams& p, int n_pairs, const CUtensorMap& tmq, const CUtensorMap& tmk,
+                                    const CUtensorMap& tmv, const CUtensorMap& tmo, cudaStream_t stream) {
+  return launch_form<true>(p, n_pairs, tmq, tmk, tmv, tmo, stream);
 }
 
 }  // namespace blkattn

@@ -413,6 +413,35 @@ int blkattn_paged_append(const blkattn_tensor* k, const blkattn_tensor* v, const
                          const blkattn_tensor* q, const blkattn_tensor* q_out, blkattn_stream_t stream);
 
 /*
+ * blkattn_fwd_paged — blkattn_fwd over the paged cache.
+ *
+ * q, seqlens_k, q_logical_pos, scale, out, lse, stream: as for blkattn_fwd
+ * (scale finite; out and lse without broadcast dims).
+ * k_pages, v_pages  [N, H_kv, P, d] of q's dtype, P as above: last stride 1,
+ *             the other strides and the base addresses multiples of 16 bytes.
+ * page_table  int32 [B, entries], any strides.  T_max = entries x P.
+ * tree_mask   NULL, or as for blkattn_fwd_tree.
+ * window      0 (none), or as for blkattn_fwd_window; not with a tree.
+ * Visibility is blkattn_fwd's, without a bias, and a key on an entry that
+ * holds no page is not visible (pages that a window left behind may be given
+ * back and their entries set to -1).  Entries past a sequence's length are
+ * not followed.  The K and V rows between the earliest and the latest key
+ * that query rows of one sequence see must be finite, except tree nodes that
+ * no row lists; every other row of the pools may hold anything.
+ * Kernels: bf16 prompts (T_q >= 64, d = 128, no tree, scale > 0) and bf16
+ * decode and verify rows (d = 64 or 128) run on tcgen05 when the query rows
+ * are contiguous and 16-byte aligned; the rest (f32, other query layouts, more
+ * than 49152 query rows to a KV head) on the CUDA cores.  Results do not
+ * depend on P or on the order of the pages.  Workspace, growth and overlap of
+ * calls as for blkattn_fwd.  Returns as blkattn_fwd; BLKATTN_ERR_UNSUPPORTED
+ * also for P outside the rule above.
+ */
+int blkattn_fwd_paged(const blkattn_tensor* q, const blkattn_tensor* k_pages, const blkattn_tensor* v_pages,
+                      const blkattn_tensor* page_table, const blkattn_tensor* seqlens_k,
+                      const blkattn_tensor* q_logical_pos, const blkattn_tensor* tree_mask, int64_t window,
+                      float scale, const blkattn_tensor* out, const blkattn_tensor* lse, blkattn_stream_t stream);
+
+/*
  * Attention states of rows, in the sufficient statistics of eq. 33.3:
  *   m [rows]           f32, the maximum score (natural-log units); -inf = empty
  *   l [rows]           f32, sum e^{z_j - m}; NULL means "normalised": l = 1 and

@@ -306,6 +306,65 @@ int tensor_map(int dev, const blkattn_tensor* t, int box_cols, int box_rows, CUt
   return BLKATTN_OK;
 }
 
+// Whether pages of 128-dim bf16 rows allow the wide boxes of the paged decode
+// kernel, and how the head enters: packed heads of a row ([N, P, H, d] memory:
+// the halves of head h are 2 h and 2 h + 1 of the row), or packed rows of a
+// page's heads ([N, H, P, d]: the 8-row groups of head h start at h P / 8).
+bool wide_pages(const blkattn_tensor* t, int* h2, int* h3) {
+  if (t->dtype != BLKATTN_BF16 || t->sizes[3] != 128) return false;
+  const int64_t H = t->sizes[1], P = t->sizes[2];
+  *h2 = *h3 = 0;
+  if (H == 1) return true;
+  if (t->strides[1] == 128) {
+    *h2 = 2;
+    return true;
+  }
+  if (t->strides[1] == P * t->strides[2]) {
+    *h3 = (int)(P / 8);
+    return true;
+  }
+  return false;
+}
+
+// 5-D map over a pool [N, H, P, 128] for wide boxes: {64 dims, 8 rows, halves,
+// 8-row groups, pages}, box {64, 8, 2, box_rows / 8, 1}, 128-byte swizzle.
+int wide_pages_map(int dev, const blkattn_tensor* t, int box_rows, int h2, int h3, CUtensorMap* out) {
+  MapKey key;
+  std::memset(&key, 0, sizeof key);
+  key.dev = dev;
+  key.dtype = t->dtype;
+  key.box_cols = -5;  // (no 4-D map's)
+  key.box_rows = box_rows;
+  key.ptr = t->data;
+  for (int i = 0; i < 4; ++i) key.sizes[i] = t->sizes[i];
+  for (int i = 0; i < 3; ++i) key.strides[i] = t->strides[i];
+  for (int i = 0; i < kMapCache; ++i)
+    if (g_maps[i].used && g_maps[i].key == key) {
+      *out = g_maps[i].map;
+      return BLKATTN_OK;
+    }
+  int st = get_encoder();
+  if (st != BLKATTN_OK) return st;
+  MapEntry& e = g_maps[g_map_next];
+  g_map_next = (g_map_next + 1) % kMapCache;
+  const cuuint64_t H = (cuuint64_t)t->sizes[1], P = (cuuint64_t)t->sizes[2], row = (cuuint64_t)t->strides[2] * 2;
+  const cuuint64_t dims[5] = {64, 8, h2 ? 2 * H : 2, h3 ? H * (P / 8) : P / 8, (cuuint64_t)t->sizes[0]};
+  const cuuint64_t strides[4] = {row, 128, 8 * row, (cuuint64_t)t->strides[0] * 2};
+  const cuuint32_t box[5] = {64, 8, 2, (cuuint32_t)box_rows / 8, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const CUresult r = g_encode(&e.map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, t->data, dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    e.used = false;
+    return cuda_fail(cudaErrorInvalidValue);  // the tensor map was refused
+  }
+  e.key = key;
+  e.used = true;
+  *out = e.map;
+  return BLKATTN_OK;
+}
+
 // bf16 K/V cache or Q: boxes of 64 dims (128 bytes) x box_rows rows.
 int kv_tensor_map(int dev, const blkattn_tensor* t, int box_rows, CUtensorMap* out) {
   return tensor_map(dev, t, 64, box_rows, out);
@@ -634,6 +693,7 @@ int check_pages(const blkattn_tensor* k_pages, const blkattn_tensor* v_pages, co
   out->shift = 0;
   while ((1 << out->shift) < rows) ++out->shift;
   out->n_pages = (int)N;
+  out->wide = out->wide_h2 = out->wide_h3 = 0;
   return BLKATTN_OK;
 }
 
@@ -788,8 +848,16 @@ int fwd_paged_impl(const blkattn_tensor* q, const blkattn_tensor* k_pages, const
   bool o_tma = false;
   if (pl.cfg.kernel != blkattn::Kernel::CudaCore) {
     const int box = pt.rows < 128 ? pt.rows : 128;
-    if ((st = kv_tensor_map(dev, k_pages, box, &mk)) != BLKATTN_OK) return st;
-    if ((st = kv_tensor_map(dev, v_pages, box, &mv)) != BLKATTN_OK) return st;
+    int v2 = 0, v3 = 0;
+    if (!prefill && wide_pages(k_pages, &pt.wide_h2, &pt.wide_h3) && wide_pages(v_pages, &v2, &v3) &&
+        v2 == pt.wide_h2 && v3 == pt.wide_h3) {
+      pt.wide = 1;
+      if ((st = wide_pages_map(dev, k_pages, box, v2, v3, &mk)) != BLKATTN_OK) return st;
+      if ((st = wide_pages_map(dev, v_pages, box, v2, v3, &mv)) != BLKATTN_OK) return st;
+    } else {
+      if ((st = kv_tensor_map(dev, k_pages, box, &mk)) != BLKATTN_OK) return st;
+      if ((st = kv_tensor_map(dev, v_pages, box, &mv)) != BLKATTN_OK) return st;
+    }
     if (prefill) {
       if ((st = kv_tensor_map(dev, q, 128, &mq)) != BLKATTN_OK) return st;
       mo = mq;  // not read unless o_tma

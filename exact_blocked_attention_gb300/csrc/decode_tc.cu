@@ -87,7 +87,9 @@ constexpr int kKeyThreads = 32 * kKeyWarps;
 constexpr int kTmaWarp = 8;
 constexpr int kMmaWarp = 9;
 constexpr int kLoadWarp = 10;
-constexpr int kThreads = 32 * 11;
+constexpr int kPageVWarp = 11;  // PAGED: V tiles (kTmaWarp: K tiles)
+template <bool PAGED>
+constexpr int kThreads = 32 * (PAGED ? 12 : 11);
 constexpr int kBarRows = 1;  // named barrier of the key threads
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;    // S^T of tiles with even / odd index: +0 / +64
@@ -105,6 +107,8 @@ struct RowFacts {
   int end[NR];       // visible keys are [0, end): min(len, pos + 1), 0 for padding rows
   int unit_end;      // max over the rows
   int unit_start;    // paged cache: the earliest key that a row sees (INT_MAX: none)
+  uint64_t tree_seen;  // paged cache: bit k = some row sees tree node k
+  int any_gone;      // paged cache: some key below unit_end in this CTA's tiles has no page
   int min_end;       // min over the real rows
   int tree_base;     // first key of the token tree (len - T_q); INT_MAX without a tree
   int win_max;       // sliding window: the largest first visible key of the rows (0 without)
@@ -272,7 +276,7 @@ __device__ __forceinline__ int scatter_base(int lane) {
 // nodes) are zero-filled in shared memory: rows of a page that were never
 // written may hold anything.
 template <int NR, int D, bool PAGED>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<PAGED>, 1)
     decode_tc_kernel(const FwdParams p, const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv) {
   using L = TcLayout<NR, D>;
@@ -328,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   {
     int* nb = reinterpret_cast<int*>(sm + L::kOffP);  // per-sequence totals (P^T area, start-up only)
     const int E = B * RG;
-    for (int e = threadIdx.x; e < E; e += kThreads) {
+    for (int e = threadIdx.x; e < E; e += kThreads<PAGED>) {
       const int b = e / RG;
       const int rg = e - b * RG;
       // the row end min(len, pos + 1) (0 for pos < 0) grows with pos, so the
@@ -393,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::relinquish();
     }
     __syncthreads();
-    for (int b = threadIdx.x; b < B; b += kThreads) {
+    for (int b = threadIdx.x; b < B; b += kThreads<PAGED>) {
       int s = 0;
       for (int rg = 0; rg < RG; ++rg) s += ntab[b * RG + rg] + kUnitExtra;
       nb[b] = s;
@@ -480,21 +484,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   // a range may start among a unit's weight-only tiles: begin at the next unit
   if (t0 < t1 && cur.j >= cur.n) cur.step_unit(ntab, RG, Hkv, B);
 
-  if (PAGED && warp == kTmaWarp) {
-    // ---------------- producer: K and V tiles from pages (whole warp) ----------------
+  if (PAGED && (warp == kTmaWarp || warp == kPageVWarp)) {
+    // ---------------- producers: K tiles, V tiles from pages (whole warps) ----------------
+    // Each takes every second ring entry: two warps, because one alone cannot
+    // issue the boxes of small pages fast enough.  With an odd number of slots
+    // a slot's entries alternate between the two.  Entry e waits for entry
+    // e - kSlots of its slot; that wait is by parity, so entry e - 2 kSlots has
+    // to be known consumed: this warp's entry e - 2 waited for e - 2 - kSlots,
+    // and the products S_0, S_1, U_0, S_2, U_1, ... (completed in order) consume
+    // e - 2 kSlots before it for either parity of e.
+    const int kv = warp == kPageVWarp ? 1 : 0;
+    const void* map = kv ? static_cast<const void*>(&tmv) : static_cast<const void*>(&tmk);
     const uint64_t pol = policy_evict_first();
-    if (lane == 0) {
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmk)) : "memory");
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmv)) : "memory");
-    }
+    if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
     // lane: box `half` of piece `piece` of a tile; a piece is a page or the
     // tile's part of one
     const int box_shift = min(p.pages.shift, 7);
     const int n_pieces = BK >> box_shift;
     const int piece = lane & (n_pieces - 1);
     const int half = lane >> (7 - box_shift);
-    const bool copies = half < L::kBoxes;
-    const uint32_t dst_off = (uint32_t)(half * kBox + (piece << box_shift) * 128);
+    const bool wide = p.pages.wide;
+    const bool copies = half < (wide ? 1 : L::kBoxes);
+    const uint32_t dst_off =
+        wide ? (uint32_t)((piece << box_shift) * 256) : (uint32_t)(half * kBox + (piece << box_shift) * 128);
     int len_b = -1, len = 0;
     // the lane's page for the tile at cursor c: -1 (zeros) past the length
     auto look_up = [&](const Cursor& c) {
@@ -505,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int key = c.key0() + (piece << box_shift);
       return key < len ? page_of(p.pages, c.b, key) : -1;
     };
-    int64_t issued = 0;
+    int64_t issued = 0;  // entries
     bool ok = true;
     int page = cur.t < t1 ? look_up(cur) : -1;
     for (int64_t g = 0; ok && cur.t < t1; ++g) {
@@ -513,29 +525,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kvh = cur.kvh;
       cur.next(ntab, RG, Hkv, B);
       const int page_next = cur.t < t1 ? look_up(cur) : -1;  // (the load is in flight meanwhile)
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const int64_t seq = 2 * g + kv;
-        const int s = (int)(seq % kSlots);
-        bool w = true;
-        if (lane == 0) {
-          if (seq >= kSlots) w = mbar_wait(&empty[s], (uint32_t)(((seq / kSlots) - 1) & 1));
-          if (w) mbar_arrive_expect_tx(&full[s], kSlotBytes);
-        }
-        if (!__shfl_sync(0xffffffffu, w, 0)) {  // (also orders the expected bytes before the copies)
-          ok = false;
-          break;
-        }
-        __syncwarp();
-        if (copies)
-          tma_load_4d(sm + L::kOffRing + s * kSlotBytes + dst_off,
-                      kv ? static_cast<const void*>(&tmv) : static_cast<const void*>(&tmk), 64 * half, row, kvh, page,
-                      &full[s], pol);
-        issued = seq + 1;
+      const int64_t seq = 2 * g + kv;
+      const int s = (int)(seq % kSlots);
+      bool w = true;
+      if (lane == 0) {
+        if (seq >= kSlots) w = mbar_wait(&empty[s], (uint32_t)(((seq / kSlots) - 1) & 1));
+        if (w) mbar_arrive_expect_tx(&full[s], kSlotBytes);
       }
+      ok = __shfl_sync(0xffffffffu, w, 0);  // (also orders the expected bytes before the copies)
+      if (!ok) break;
+      __syncwarp();
+      if (copies) {
+        unsigned char* dst = sm + L::kOffRing + s * kSlotBytes + dst_off;
+        if (wide)
+          tma_load_5d(dst, map, 0, 0, kvh * p.pages.wide_h2, (row >> 3) + kvh * p.pages.wide_h3, page, &full[s], pol);
+        else
+          tma_load_4d(dst, map, 64 * half, row, kvh, page, &full[s], pol);
+      }
+      issued = seq + 1;
       // (as below: the first unit's query rows before the stream goes on)
-      if (ok && g == 0) {
-        bool w = true;
+      if (g == 0) {
         if (lane == 0) w = mbar_wait(&q_full[0], 0);
         ok = __shfl_sync(0xffffffffu, w, 0);
       }
@@ -543,8 +552,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     if (lane == 0) {
-      // every issued copy must land before the CTA exits
-      for (int64_t seq = issued - kSlots < 0 ? 0 : issued - kSlots; seq < issued; ++seq)
+      // every issued copy must land before the CTA exits (an entry that has a
+      // successor in its slot has: the successor waited for its consumption)
+      const bool clean = ok;
+      const int64_t all = (issued + 1) / 2 * 2;  // entries of both producers
+      for (int64_t seq = issued - 1; seq >= 0 && seq >= all - kSlots - (clean ? 0 : kSlots); seq -= 2)
         if (!mbar_wait(&full[seq % kSlots], (uint32_t)((seq / kSlots) & 1))) ok = false;
       if (!ok) {
         record_error(p.err, kErrTimeout);
@@ -647,10 +659,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         cp_async_16(smem_u32(qs + (c >> 3) * L::kQBox + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
                     rr ? static_cast<const void*>(reinterpret_cast<const uint4*>(src) + c) : p.q, rr ? 16u : 0u);
       }
+      // paged cache: the first key of a page that is not there, among the
+      // entries of the unit's tiles of this CTA that this lane looks at (the
+      // first entry apart: a window may start behind it)
+      int gone_key = 0x7fffffff, gone_first = 0x7fffffff;
+      if (PAGED) {
+        const int last = (int)min((int64_t)cur.n, cur.j + (t1 - cur.t));  // tiles [cur.j, last)
+        const int i0 = cur.key0() >> p.pages.shift;
+        const int i1 = (int)min((int64_t)p.pages.entries, (((int64_t)(cur.s0 + last) * BK - 1) >> p.pages.shift) + 1);
+        for (int ib = i0 + lane; ib < i1; ib += 16 * 32) {
+          int e[16];  // (all in flight: one round trip)
+#pragma unroll
+          for (int x2 = 0; x2 < 16; ++x2)
+            e[x2] = ib + 32 * x2 < i1 ? __ldg(p.pages.table + b * p.pages.sb + (ib + 32 * x2) * p.pages.sp) : 0;
+#pragma unroll
+          for (int x2 = 0; x2 < 16; ++x2) {
+            const int i = ib + 32 * x2;
+            if ((unsigned)e[x2] >= (unsigned)p.pages.n_pages) {
+              if (i == i0 + lane)
+                gone_first = i << p.pages.shift;
+              else
+                gone_key = min(gone_key, i << p.pages.shift);
+            }
+          }
+        }
+      }
       // integer facts of the rows
       const int len = len_raw < 0 ? 0 : (len_raw > p.Tmax ? p.Tmax : len_raw);
       RowFacts<NR>& rf = facts0[qb];
       int umax = 0, umin = 0x7fffffff, wmax = 0, ustart = 0x7fffffff;
+      uint64_t nodes = 0;
 #pragma unroll
       for (int h2 = 0; h2 < 2; ++h2) {
         const int r = lane + 32 * h2;
@@ -669,6 +707,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (PAGED) {
             const int lo = p.window > 0 ? (int)tr : 0;
             if (lo < e) ustart = min(ustart, lo);
+            const int within = e - (len - p.Tq);  // nodes before the row's end
+            if (p.tree != nullptr && within > 0) nodes |= within < 64 ? tr & ((1ull << within) - 1) : tr;
           }
           bo = (int64_t)b * p.bi_sb + (int64_t)h * p.bi_sh + (int64_t)i * p.bi_si;
           oo = (int64_t)b * p.o_sb + (int64_t)h * p.o_sh + (int64_t)i * p.o_si;
@@ -688,13 +728,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         umin = min(umin, __shfl_xor_sync(0xffffffffu, umin, off));
         wmax = max(wmax, __shfl_xor_sync(0xffffffffu, wmax, off));
         if (PAGED) ustart = min(ustart, __shfl_xor_sync(0xffffffffu, ustart, off));
+        if (PAGED) nodes |= __shfl_xor_sync(0xffffffffu, nodes, off);
       }
       if (lane == 0) {
         rf.unit_end = umax;
         rf.unit_start = ustart;
+        rf.tree_seen = nodes;
         rf.min_end = umin;
         rf.tree_base = p.tree != nullptr ? len - p.Tq : 0x7fffffff;
         rf.win_max = wmax;
+      }
+      if (PAGED) {
+        const bool any = __any_sync(0xffffffffu, gone_key < umax || (gone_first < umax && gone_first + p.pages.rows > ustart));
+        if (lane == 0) rf.any_gone = any;
       }
       cp_async_wait_all();  // this lane's query-row copies have landed
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // Q rows -> tensor core
@@ -727,6 +773,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       RingPos kpos{0u, 0u}, vpos{1u, 0u};
       constexpr uint32_t kHi = tc::desc_hi(1024);
+      // K and V tiles: two 64-dim boxes 16 KB apart, rows 128 bytes apart; a
+      // page's wide box instead has the two halves of 8 rows side by side
+      // (8-row groups 2 KB apart, the second half 1 KB behind the first)
+      const bool wide = PAGED && p.pages.wide;
+      const uint32_t kHiKV = wide ? tc::desc_hi(2048) : kHi;
+      const uint32_t half_step = (wide ? 1024u : (uint32_t)kBox) >> 4;
+      const uint32_t key16_step = (wide ? 4096u : 2048u) >> 4;
       // shared-memory descriptors: only the address word moves per MMA
       const uint32_t qlo0 = tc::desc_lo(sQ, 16);
       auto issue_qk = [&](int64_t gq) -> bool {
@@ -743,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t qlo = qlo0 + (uint32_t)(qb * L::kQBytes >> 4);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          const uint64_t adesc = tc::desc_join(klo + (uint32_t)(((ks >> 2) * kBox + (ks & 3) * 32) >> 4), kHi);
+          const uint64_t adesc = tc::desc_join(klo + (uint32_t)(ks >> 2) * half_step + (uint32_t)((ks & 3) * 32 >> 4), kHiKV);
           const uint64_t bdesc = tc::desc_join(qlo + (uint32_t)(((ks >> 2) * L::kQBox + (ks & 3) * 32) >> 4), kHi);
           tc::mma_ss(tb + kColS + 64u * (uint32_t)(gq & 1), adesc, bdesc, kIdescQK, ks > 0 ? 1u : 0u);
         }
@@ -770,13 +823,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait(&full[vs_slot], vpos.phase)) { ok = false; break; }
         vpos.adv2();
         tc::fence_after();
-        const uint32_t vlo = tc::desc_lo(sRing + vs_slot * kSlotBytes, kBox);
+        const uint32_t vlo = tc::desc_lo(sRing + vs_slot * kSlotBytes, 0) | (half_step << 16);
         const uint32_t plo = tc::desc_lo(sP + (uint32_t)(g & 1) * kPBytes, kBox);
         const uint32_t ucol = tb + kColU + 128u * (uint32_t)(up & 1);
 #pragma unroll
         for (int ks = 0; ks < BK / 16; ++ks) {
           // A = V^T: 128 dims (two 64-dim boxes 16 KB apart) x keys [16 ks, 16 ks + 16)
-          const uint64_t adesc = tc::desc_join(vlo + (uint32_t)(ks * 2048 >> 4), kHi);
+          const uint64_t adesc = tc::desc_join(vlo + (uint32_t)ks * key16_step, kHiKV);
           // B = P^T: keys [16 ks, +16) x [P_hi | P_lo] (one atom, or two 16 KB apart)
           const uint64_t bdesc = tc::desc_join(plo + (uint32_t)(ks * 2048 >> 4), kHi);
           tc::mma_ss(ucol, adesc, bdesc, kIdescPV, (!first || ks > 0) ? 1u : 0u);
@@ -973,9 +1026,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int key0 = cur.key0();
       const int key = key0 + k;
-      // (looked up before the wait: the load is in flight meanwhile)
-      bool no_page = false;
-      if (PAGED) no_page = key < rf.unit_end && page_of(p.pages, cur.b, key) < 0;
       float x[NH];
       if (has_bias) {
         // this tile's bias (rows of one sequence share lines: L1 hits); a
@@ -1017,7 +1067,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int r = 0; r < NH; ++r)
             if (key >= rf.end[c0 + r]) x[r] = kNegInf;
         }
-        if (PAGED && __any_sync(0xffffffffu, no_page)) {
+        if (PAGED && rf.any_gone) {
+          // some visible key of the unit has no page: look this one's up
+          const bool no_page = page_of(p.pages, cur.b, key) < 0;
 #pragma unroll
           for (int r = 0; r < NH; ++r)
             if (no_page) x[r] = kNegInf;
@@ -1142,17 +1194,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!vok) { ok = false; break; }
         bool unseen = key >= rf.unit_end;
         if (PAGED) {
-          unseen = unseen || key < rf.unit_start;
           const int node = key - rf.tree_base;
-          if (rf.tree_base != 0x7fffffff && node >= 0 && node < 64) {
-            bool seen = false;
-#pragma unroll 1
-            for (int r = 0; r < NR; ++r) seen = seen || (key < rf.end[r] && ((rf.tree[r] >> node) & 1ull));
-            unseen = unseen || !seen;
-          }
+          unseen = unseen || key < rf.unit_start ||
+                   (rf.tree_base != 0x7fffffff && node >= 0 && node < 64 && !((rf.tree_seen >> node) & 1ull));
         }
         if (unseen && half < L::kBoxes) {
-          unsigned char* vr = sm + L::kOffRing + (int)(sv % kSlots) * kSlotBytes + half * kBox + k * 128;
+          unsigned char* vr = sm + L::kOffRing + (int)(sv % kSlots) * kSlotBytes +
+                              (PAGED && p.pages.wide ? (k >> 3) * 2048 + half * 1024 + (k & 7) * 128
+                                                     : half * kBox + k * 128);
 #pragma unroll
           for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vr + ((c ^ (k & 7)) << 4)) = make_uint4(0, 0, 0, 0);
         }
@@ -1223,7 +1272,7 @@ cudaError_t launch_nr(const FwdParams& p, int ctas, const CUtensorMap& tmk, cons
   if (cudaError_t e = once.set_smem(reinterpret_cast<const void*>(&decode_tc_kernel<NR, D, PAGED>), L::kBytes);
       e != cudaSuccess)
     return e;
-  decode_tc_kernel<NR, D, PAGED><<<ctas, kThreads, L::kBytes, stream>>>(p, tmk, tmv);
+  decode_tc_kernel<NR, D, PAGED><<<ctas, kThreads<PAGED>, L::kBytes, stream>>>(p, tmk, tmv);
   return cudaGetLastError();
 }
 

@@ -19,14 +19,23 @@ struct PageTable {
   int shift;       // log2 of the rows of a page
   int rows;
   int n_pages;     // pages in the pool
+  // rows of 128 bf16 dims whose heads or rows lie packed: one copy brings both
+  // 64-dim halves of a piece (5-D map: 64 dims, 8 rows, halves, 8-row groups,
+  // pages; the head moves the halves' or the groups' coordinate)
+  int wide;
+  int wide_h2, wide_h3;
 };
 
-// Page of cache row t of sequence b, or -1: t outside the table (or
-// negative), or no page there.
-__device__ __forceinline__ int page_of(const PageTable& pt, int b, int t) {
+// Table entry of cache row t of sequence b, -1 for a t outside the table (or
+// negative); any value may stand there.
+__device__ __forceinline__ int entry_of(const PageTable& pt, int b, int t) {
   const int i = t >> pt.shift;  // (negative t: negative i)
-  if ((unsigned)i >= (unsigned)pt.entries) return -1;
-  const int page = __ldg(pt.table + b * pt.sb + i * pt.sp);
+  return (unsigned)i < (unsigned)pt.entries ? __ldg(pt.table + b * pt.sb + i * pt.sp) : -1;
+}
+
+// Page of cache row t of sequence b, or -1: no page there.
+__device__ __forceinline__ int page_of(const PageTable& pt, int b, int t) {
+  const int page = entry_of(pt, b, t);
   return (unsigned)page < (unsigned)pt.n_pages ? page : -1;
 }
 

@@ -50,7 +50,10 @@
 //    once every earlier MMA of the thread has completed, so S_j ready
 //    implies the product with P_{j-2} is done and P^T buffer (j mod 2) is
 //    free; a rescale of U^T at tile j first waits for the product with
-//    P_{j-1} (one more barrier, rarely needed).
+//    P_{j-1}.  Both waits are on the `empty` barrier of the ring slot that
+//    the product read (K_j, V_{j-1}): its next completion needs P_j or a
+//    later one, so a key thread cannot miss it, and the thread issues two
+//    commits a tile instead of four.
 //
 // Statistics: every key thread keeps its own partial sums l over its keys
 // for its rows; the reference maxima m (base-2 units) live in shared memory.
@@ -140,9 +143,8 @@ struct TcLayout {
   // of the finished unit whose U readout is pending
   static constexpr int kOffStat = kOffRed + 4 * NR * 4;
   static constexpr int kOffBar = kOffStat + 7 * NR * 4;
-  // full[kSlots], empty[kSlots], q_full[2], q_empty[2], s_full[2], p_full[2], u_full[2],
-  // pv_done, drain
-  static constexpr int kNumBars = 2 * kSlots + 2 + 2 + 2 + 2 + 2 + 1 + 1;
+  // full[kSlots], empty[kSlots], q_full[2], q_empty[2], p_full[2], u_full[2], drain
+  static constexpr int kNumBars = 2 * kSlots + 2 + 2 + 2 + 2 + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kBytes = kOffMisc + 128 + 1024;  // + slack to align to 1024
   static_assert(kOffQ % 1024 == 0 && kQBox % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
@@ -310,11 +312,9 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
   uint64_t* empty = full + kSlots;
   uint64_t* q_full = empty + kSlots;  // [2]
   uint64_t* q_empty = q_full + 2;     // [2]
-  uint64_t* s_full = q_empty + 2;     // [2] by tile parity
-  uint64_t* p_full = s_full + 2;      // [2] by tile parity
+  uint64_t* p_full = q_empty + 2;     // [2] by tile parity
   uint64_t* u_full = p_full + 2;      // [2] by unit parity
-  uint64_t* pv_done = u_full + 2;     // once per U += P V product
-  uint64_t* drain = pv_done + 1;
+  uint64_t* drain = u_full + 2;
   // misc: [0] tmem base, [1] error seen by the producer / MMA thread,
   // [2] abort of the key threads, [3] "this CTA folds the unit" (both
   // written before a barrier of the key threads, read after it)
@@ -380,10 +380,8 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
         mbar_init(&u_full[x], 1);
       }
       for (int x = 0; x < 2; ++x) {
-        mbar_init(&s_full[x], 1);
         mbar_init(&p_full[x], kKeyWarps);  // one arrival per key warp
       }
-      mbar_init(pv_done, 1);
       mbar_init(drain, 1);
       fence_barrier_init();
     }
@@ -507,24 +505,25 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
     const bool copies = half < (wide ? 1 : L::kBoxes);
     const uint32_t dst_off =
         wide ? (uint32_t)((piece << box_shift) * 256) : (uint32_t)(half * kBox + (piece << box_shift) * 128);
-    int len_b = -1, len = 0;
-    // the lane's page for the tile at cursor c: -1 (zeros) past the length
+    // What the lane looks up for a tile, one tile ahead: its piece's table
+    // entry and the sequence's length.  Neither load waits for the other, and
+    // nothing looks at them before the tile's turn.
+    int nx_key = 0, nx_entry = -1, nx_len = 0;
     auto look_up = [&](const Cursor& c) {
-      if (c.b != len_b) {
-        len_b = c.b;
-        len = min(p.seqlens[c.b * p.sl_s], p.Tmax);
-      }
-      const int key = c.key0() + (piece << box_shift);
-      return key < len ? page_of(p.pages, c.b, key) : -1;
+      nx_key = c.key0() + (piece << box_shift);
+      nx_entry = entry_of(p.pages, c.b, nx_key);
+      nx_len = p.seqlens[c.b * p.sl_s];
     };
     int64_t issued = 0;  // entries
     bool ok = true;
-    int page = cur.t < t1 ? look_up(cur) : -1;
+    if (cur.t < t1) look_up(cur);
     for (int64_t g = 0; ok && cur.t < t1; ++g) {
-      const int row = (cur.key0() + (piece << box_shift)) & (p.pages.rows - 1);
+      const int row = nx_key & (p.pages.rows - 1);
       const int kvh = cur.kvh;
+      // past the length, or no page: -1 (zeros)
+      const int page = nx_key < nx_len && (unsigned)nx_entry < (unsigned)p.pages.n_pages ? nx_entry : -1;
       cur.next(ntab, RG, Hkv, B);
-      const int page_next = cur.t < t1 ? look_up(cur) : -1;  // (the load is in flight meanwhile)
+      if (cur.t < t1) look_up(cur);
       const int64_t seq = 2 * g + kv;
       const int s = (int)(seq % kSlots);
       bool w = true;
@@ -548,7 +547,6 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
         if (lane == 0) w = mbar_wait(&q_full[0], 0);
         ok = __shfl_sync(0xffffffffu, w, 0);
       }
-      page = page_next;
     }
     __syncwarp();
     if (lane == 0) {
@@ -659,29 +657,28 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
         cp_async_16(smem_u32(qs + (c >> 3) * L::kQBox + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
                     rr ? static_cast<const void*>(reinterpret_cast<const uint4*>(src) + c) : p.q, rr ? 16u : 0u);
       }
-      // paged cache: the first key of a page that is not there, among the
-      // entries of the unit's tiles of this CTA that this lane looks at (the
-      // first entry apart: a window may start behind it)
-      int gone_key = 0x7fffffff, gone_first = 0x7fffffff;
+      // paged cache: the table entries of the unit's tiles of this CTA, one a
+      // lane here (looked at further down), the others in batches
+      int gone_key = 0x7fffffff;  // first key (of this lane's entries past the first) without a page
+      int e0 = 0, e0_key = 0x7fffffff;
       if (PAGED) {
         const int last = (int)min((int64_t)cur.n, cur.j + (t1 - cur.t));  // tiles [cur.j, last)
         const int i0 = cur.key0() >> p.pages.shift;
         const int i1 = (int)min((int64_t)p.pages.entries, (((int64_t)(cur.s0 + last) * BK - 1) >> p.pages.shift) + 1);
-        for (int ib = i0 + lane; ib < i1; ib += 16 * 32) {
+        const int32_t* row = p.pages.table + b * p.pages.sb;
+        if (i0 + lane < i1) {
+          e0_key = (i0 + lane) << p.pages.shift;
+          e0 = __ldg(row + (i0 + lane) * p.pages.sp);
+        }
+        for (int ib = i0 + 32 + lane; ib < i1; ib += 16 * 32) {
           int e[16];  // (all in flight: one round trip)
 #pragma unroll
           for (int x2 = 0; x2 < 16; ++x2)
-            e[x2] = ib + 32 * x2 < i1 ? __ldg(p.pages.table + b * p.pages.sb + (ib + 32 * x2) * p.pages.sp) : 0;
+            e[x2] = ib + 32 * x2 < i1 ? __ldg(row + (ib + 32 * x2) * p.pages.sp) : 0;
 #pragma unroll
-          for (int x2 = 0; x2 < 16; ++x2) {
-            const int i = ib + 32 * x2;
-            if ((unsigned)e[x2] >= (unsigned)p.pages.n_pages) {
-              if (i == i0 + lane)
-                gone_first = i << p.pages.shift;
-              else
-                gone_key = min(gone_key, i << p.pages.shift);
-            }
-          }
+          for (int x2 = 0; x2 < 16; ++x2)
+            if ((unsigned)e[x2] >= (unsigned)p.pages.n_pages)
+              gone_key = min(gone_key, (ib + 32 * x2) << p.pages.shift);
         }
       }
       // integer facts of the rows
@@ -722,13 +719,14 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
         rf.ooff[r] = oo;
         rf.loff[r] = lo;
       }
-#pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) {
-        umax = max(umax, __shfl_xor_sync(0xffffffffu, umax, off));
-        umin = min(umin, __shfl_xor_sync(0xffffffffu, umin, off));
-        wmax = max(wmax, __shfl_xor_sync(0xffffffffu, wmax, off));
-        if (PAGED) ustart = min(ustart, __shfl_xor_sync(0xffffffffu, ustart, off));
-        if (PAGED) nodes |= __shfl_xor_sync(0xffffffffu, nodes, off);
+      umax = __reduce_max_sync(0xffffffffu, umax);
+      umin = __reduce_min_sync(0xffffffffu, umin);
+      if (p.window > 0) wmax = __reduce_max_sync(0xffffffffu, wmax);
+      if (PAGED) {
+        ustart = __reduce_min_sync(0xffffffffu, ustart);
+        if (p.tree != nullptr)
+          nodes = (uint64_t)__reduce_or_sync(0xffffffffu, (unsigned)nodes) |
+                  (uint64_t)__reduce_or_sync(0xffffffffu, (unsigned)(nodes >> 32)) << 32;
       }
       if (lane == 0) {
         rf.unit_end = umax;
@@ -739,7 +737,9 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
         rf.win_max = wmax;
       }
       if (PAGED) {
-        const bool any = __any_sync(0xffffffffu, gone_key < umax || (gone_first < umax && gone_first + p.pages.rows > ustart));
+        // (a window may start behind a first page that was given back)
+        const bool none = (unsigned)e0 >= (unsigned)p.pages.n_pages && e0_key < umax && e0_key + p.pages.rows > ustart;
+        const bool any = __any_sync(0xffffffffu, none || gone_key < umax);
         if (lane == 0) rf.any_gone = any;
       }
       cp_async_wait_all();  // this lane's query-row copies have landed
@@ -756,7 +756,13 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
     // Order S_0, S_1, U += P_0 V_0, S_2, U += P_1 V_1, ...: the products of
     // the next tile's scores run while the key threads work on this tile.
     if (lane == 0) {
-      Cursor cq = cur;  // tile of the next S product
+      // The S side runs one tile ahead of the U side.  Per tile only `left`
+      // (the unit's tiles of this CTA still to come) counts down; the cursors
+      // move from unit to unit.
+      auto tiles_here = [&](const Cursor& c) { return c.t < t1 ? (int)min((int64_t)(c.n - c.j), t1 - c.t) : 0; };
+      Cursor cq = cur;  // unit of the next S product
+      int left_q = tiles_here(cq), left = left_q;
+      bool first_q = true, first = true;
       int uq = 0, up = 0;  // unit counters of the S and the U sides
       // Ring positions of the next K (even entries) and V (odd entries)
       // tiles: slot and phase advance by two entries per tile, without
@@ -782,11 +788,9 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
       const uint32_t key16_step = (wide ? 4096u : 2048u) >> 4;
       // shared-memory descriptors: only the address word moves per MMA
       const uint32_t qlo0 = tc::desc_lo(sQ, 16);
-      auto issue_qk = [&](int64_t gq) -> bool {
-        const bool first = cq.t == t0 || cq.j == 0;
-        const bool last = cq.t == t1 - 1 || cq.j == cq.n - 1;
+      auto issue_qk = [&](uint32_t buf) -> bool {
         const int qb = uq & 1;
-        if (first && !mbar_wait(&q_full[qb], (uint32_t)((uq >> 1) & 1))) return false;
+        if (first_q && !mbar_wait(&q_full[qb], (uint32_t)((uq >> 1) & 1))) return false;
         const uint32_t ks_slot = kpos.slot;
         if (!mbar_wait(&full[ks_slot], kpos.phase)) return false;
         kpos.adv2();
@@ -798,33 +802,34 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint64_t adesc = tc::desc_join(klo + (uint32_t)(ks >> 2) * half_step + (uint32_t)((ks & 3) * 32 >> 4), kHiKV);
           const uint64_t bdesc = tc::desc_join(qlo + (uint32_t)(((ks >> 2) * L::kQBox + (ks & 3) * 32) >> 4), kHi);
-          tc::mma_ss(tb + kColS + 64u * (uint32_t)(gq & 1), adesc, bdesc, kIdescQK, ks > 0 ? 1u : 0u);
+          tc::mma_ss(tb + kColS + 64u * buf, adesc, bdesc, kIdescQK, ks > 0 ? 1u : 0u);
         }
-        tc::commit(&s_full[gq & 1]);
-        tc::commit(&empty[ks_slot]);
-        if (last) {
+        tc::commit(&empty[ks_slot]);  // K_j is free and S_j is ready
+        first_q = false;
+        if (--left_q == 0) {
           tc::commit(&q_empty[qb]);
           ++uq;
+          cq.step_unit(ntab, RG, Hkv, B);
+          left_q = tiles_here(cq);
+          first_q = true;
         }
-        cq.next(ntab, RG, Hkv, B);
         return true;
       };
       // (test hook: `drain` has no arrival before the thread's own commit
       // below, so this wait runs out)
       bool ok = blockIdx.x != (unsigned)p.test_stall_cta || mbar_wait_ns(drain, 0, 1000000ull);
-      ok = ok && (!(cq.t < t1) || issue_qk(0));
-      for (int64_t g = 0; ok && cur.t < t1; cur.next(ntab, RG, Hkv, B), ++g) {
-        const bool first = cur.t == t0 || cur.j == 0;
-        const bool last = cur.t == t1 - 1 || cur.j == cur.n - 1;
-        if (cq.t < t1 && !issue_qk(g + 1)) { ok = false; break; }
+      ok = ok && (left_q == 0 || issue_qk(0));
+      uint32_t buf = 0, p_phase = 0;  // tile parity, phase of its P^T buffer
+      while (ok && left > 0) {
+        if (left_q > 0 && !issue_qk(buf ^ 1u)) { ok = false; break; }
         // U^T += V_j^T [P_hi | P_lo]^T once the key threads wrote P^T
         const uint32_t vs_slot = vpos.slot;
-        if (!mbar_wait(&p_full[g & 1], (uint32_t)((g >> 1) & 1))) { ok = false; break; }
+        if (!mbar_wait(&p_full[buf], p_phase)) { ok = false; break; }
         if (!mbar_wait(&full[vs_slot], vpos.phase)) { ok = false; break; }
         vpos.adv2();
         tc::fence_after();
         const uint32_t vlo = tc::desc_lo(sRing + vs_slot * kSlotBytes, 0) | (half_step << 16);
-        const uint32_t plo = tc::desc_lo(sP + (uint32_t)(g & 1) * kPBytes, kBox);
+        const uint32_t plo = tc::desc_lo(sP + buf * kPBytes, kBox);
         const uint32_t ucol = tb + kColU + 128u * (uint32_t)(up & 1);
 #pragma unroll
         for (int ks = 0; ks < BK / 16; ++ks) {
@@ -835,10 +840,15 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
           tc::mma_ss(ucol, adesc, bdesc, kIdescPV, (!first || ks > 0) ? 1u : 0u);
         }
         tc::commit(&empty[vs_slot]);
-        tc::commit(pv_done);
-        if (last) {
+        first = false;
+        p_phase ^= buf;
+        buf ^= 1u;
+        if (--left == 0) {
           tc::commit(&u_full[up & 1]);
           ++up;
+          cur.step_unit(ntab, RG, Hkv, B);
+          left = tiles_here(cur);
+          first = true;
         }
       }
       if (!ok) {
@@ -931,13 +941,17 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
           st_global_hint(p.ws_m + slot * R + k, s_mfin[k], keep);
           st_global_hint(p.ws_l + slot * R + k, s_lfin[k], keep);
         }
-        __threadfence();  // the partial state is visible before the count says so
         bar_sync(kBarRows, kKeyThreads);
-        if (threadIdx.x == 0)
+        if (threadIdx.x == 0) {
+          // one thread's fences order all: the barriers before and after it
+          // carry the other threads' stores and loads (a fence by each of
+          // them costs every warp its round trip)
+          __threadfence();  // the partial state is visible before the count says so
           misc[3] = (atomicAdd(&p.unit_cnt[unit], 1u) == (unsigned)(nparts - 1)) ? 1 : 0;
+          __threadfence();  // the other parts are read after the count
+        }
         bar_sync(kBarRows, kKeyThreads);
         if (misc[3] != 0) {
-          __threadfence();
           if (threadIdx.x == 0) p.unit_cnt[unit] = 0u;  // ready for the next launch
           const int64_t fs = cf + unit;  // the unit's first slot; its parts are consecutive
           // items (row, 4 value dims) over the key threads, two items at a
@@ -1014,6 +1028,7 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
       if (threadIdx.x == 0) mbar_arrive(&q_empty[pb]);
       return true;
     };
+    uint32_t kslot = 0, kphase = 0;  // ring slot of the current K tile and its phase
     for (int64_t g = 0; cur.t < t1; cur.next(ntab, RG, Hkv, B), ++g) {
       const bool first = cur.t == t0 || cur.j == 0;
       const bool last = cur.t == t1 - 1 || cur.j == cur.n - 1;
@@ -1036,7 +1051,7 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
         for (int r = 0; r < NH; ++r)
           x[r] = kin ? __ldg(p.bias + rf.boff[c0 + r] + (int64_t)key * p.bi_sj) : 0.f;
       }
-      const bool sok = wait_all(&s_full[g & 1], (uint32_t)((g >> 1) & 1));
+      const bool sok = wait_all(&empty[kslot], kphase);
       bool trig = !sok;
       if (sok) {
         tc::fence_after();
@@ -1138,7 +1153,8 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
           // U^T lane k = value dim k, this half's columns of both parts; the
           // product with P_{j-1} must have completed (U += P_j V_j waits for
           // this tile's P)
-          const bool pv = bar_and(kBarRows, kKeyThreads, wait_all(pv_done, (uint32_t)((g - 1) & 1)));
+          const int64_t pv_seq = 2 * g - 1;  // V_{j-1}
+          const bool pv = bar_and(kBarRows, kKeyThreads, wait_all(&empty[pv_seq % kSlots], (uint32_t)((pv_seq / kSlots) & 1)));
           if (!pv) { ok = false; break; }
           tc::fence_after();
           const uint32_t ua = tl + kColU + 128u * (uint32_t)ub + c0;
@@ -1211,6 +1227,11 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
       tc::fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[g & 1]);
+      kslot += 2;
+      if (kslot >= (uint32_t)kSlots) {
+        kslot -= (uint32_t)kSlots;
+        kphase ^= 1u;
+      }
 
       // the U readout of the previous unit (its last product has long
       // completed by now)

@@ -380,26 +380,21 @@ bool out_tma_ok(const blkattn_tensor* out) {
   return true;
 }
 
-// Grow-only per-device scratch, grown stream-ordered on the call's stream:
-// the old buffer is released after the work already queued there
-// (cudaFreeAsync) and the new one is allocated from the device's memory pool
-// in stream order (cudaMallocAsync), so no call synchronises the device.
-// Work on other streams that used the old buffer must be ordered before this
-// call by the caller (calls on different streams must not overlap).  Growing
-// while the stream is being captured is refused (a capture may not allocate).
+// Grow-only per-device scratch, allocated from the device's memory pool in
+// stream order (cudaMallocAsync), so no call synchronises the device.  A
+// buffer that was outgrown is kept, not freed: graphs captured while it was
+// the current one hold its address and may be replayed at any time.  Growth
+// at least doubles, so what is kept never exceeds the current buffer.
+// Growing while the stream is being captured is refused (a capture may not
+// allocate).
 int grow_stream_ordered(void** buf, size_t* have, size_t bytes, cudaStream_t stream) {
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
   if (cudaError_t e = cudaStreamIsCapturing(stream, &cs); e != cudaSuccess) return cuda_fail(e);
   if (cs != cudaStreamCaptureStatusNone) return BLKATTN_ERR_NO_WORKSPACE;
-  if (*buf) {
-    if (cudaError_t e = cudaFreeAsync(*buf, stream); e != cudaSuccess) return cuda_fail(e);
-    *buf = nullptr;
-    *have = 0;
-  }
-  if (cudaError_t e = cudaMallocAsync(buf, bytes, stream); e != cudaSuccess) {
-    *buf = nullptr;
-    return cuda_fail(e);
-  }
+  if (bytes < 2 * *have) bytes = 2 * *have;
+  void* grown = nullptr;
+  if (cudaError_t e = cudaMallocAsync(&grown, bytes, stream); e != cudaSuccess) return cuda_fail(e);
+  *buf = grown;
   *have = bytes;
   return BLKATTN_OK;
 }
@@ -415,17 +410,14 @@ int ensure_counters(DeviceState* s, int64_t n, cudaStream_t stream) {
   if ((size_t)n <= s->cnt_n) return BLKATTN_OK;
   void* buf = s->cnt;
   size_t bytes = s->cnt_n * sizeof(unsigned);
-  const int st = grow_stream_ordered(&buf, &bytes, (size_t)n * sizeof(unsigned), stream);
-  s->cnt = static_cast<unsigned*>(buf);
-  s->cnt_n = bytes / sizeof(unsigned);
-  if (st != BLKATTN_OK) return st;
-  if (cudaError_t e = cudaMemsetAsync(s->cnt, 0, (size_t)n * sizeof(unsigned), stream); e != cudaSuccess) {
-    // the counters cannot be trusted: drop them so the next call reallocates
-    cudaFreeAsync(s->cnt, stream);
-    s->cnt = nullptr;
-    s->cnt_n = 0;
+  if (const int st = grow_stream_ordered(&buf, &bytes, (size_t)n * sizeof(unsigned), stream); st != BLKATTN_OK)
+    return st;
+  if (cudaError_t e = cudaMemsetAsync(buf, 0, bytes, stream); e != cudaSuccess) {
+    cudaFreeAsync(buf, stream);  // the counters cannot be trusted: the next call reallocates
     return cuda_fail(e);
   }
+  s->cnt = static_cast<unsigned*>(buf);
+  s->cnt_n = bytes / sizeof(unsigned);
   return BLKATTN_OK;
 }
 

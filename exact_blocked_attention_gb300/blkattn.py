@@ -1,7 +1,9 @@
 """Thin Python binding of libblkattn's C ABI (include/blkattn.h).
 
 Argument marshalling only: torch tensors are turned into strided descriptors
-(data pointer, sizes, strides) and the current torch stream is passed through.
+(data pointer, sizes, strides) and the current torch stream is passed through,
+here with ctypes, for the operators of a serving step (rope, paged_append,
+attention_paged) in the small extension csrc/torch_bind.cpp.
 Every step of the attention runs in the library's CUDA kernels; there is no
 CPU or eager fallback, and a missing library is an error.
 """
@@ -9,7 +11,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 import threading
 
 import torch
@@ -126,6 +127,26 @@ def load(path: str = LIB_PATH):
             lib.blkattn_last_cuda_error.argtypes = []
             _lib = lib
     return _lib
+
+
+_bind = None
+
+
+def _load_bind():
+    """The torch marshalling module (csrc/torch_bind.cpp), bound to the loaded library."""
+    global _bind
+    lib = load()
+    with _lock:
+        if _bind is None:
+            try:
+                from . import _torch_bind as bind
+            except ImportError as e:
+                raise RuntimeError(f"_torch_bind is not built or not loadable ({e}); run the package build first") from e
+            bind.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (lib.blkattn_rope, lib.blkattn_rope_bwd,
+                                                                        lib.blkattn_paged_append,
+                                                                        lib.blkattn_fwd_paged)))
+            _bind = bind
+    return _bind
 
 
 def status_string(status: int) -> str:
@@ -273,28 +294,6 @@ def spec_sample(p, q, draft, u_accept, u_sample, n_accepted=None, token=None, st
     return n_accepted, token
 
 
-# One descriptor as bytes: the layout of Tensor, packed in one call.
-_PACK = struct.Struct("<Qii4q4qi4x")
-assert _PACK.size == ctypes.sizeof(Tensor)
-_PAD = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())
-
-
-def _pack(t):
-    """describe() as a bytes object that ctypes passes as a pointer: a decode
-    step's calls spend most of their host time on descriptors."""
-    if t is None:
-        return None
-    dt = _DTYPES.get(t.dtype)
-    if dt is None:
-        raise ValueError(f"blkattn: unsupported dtype {t.dtype}")
-    n = t.dim()
-    if n > 4:
-        raise ValueError("blkattn: at most 4 dimensions")
-    pad = _PAD[n]
-    # (a tensor of no elements has the null address; get_device() is -1 for host memory)
-    return _PACK.pack(t.data_ptr(), dt, n, *t.shape, *pad, *t.stride(), *pad, t.get_device())
-
-
 def _layout(layout) -> int:
     code = ROPE_LAYOUTS.get(layout)
     if code is None:
@@ -302,10 +301,10 @@ def _layout(layout) -> int:
     return code
 
 
-def _stream_of(t, stream):
-    """The stream handle of a call on tensor t: the given one, or the current one of t's device."""
+def _handle(stream):
+    """A stream argument as a handle; None (the current stream of the tensors' device) stays None."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else None
+        return None
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -331,22 +330,21 @@ def rope_phases(angles, device="cuda"):
     return torch.tensor(list(f)[:len(angles)], dtype=torch.int64, device=device)
 
 
-def _rope(fn, x, pos, phases, out, layout, mscale, out_dtype, stream):
-    if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-    _check(fn(_pack(x), _pack(pos), _pack(phases), _layout(layout), mscale, _pack(out), _stream_of(x, stream)))
-    return out
-
-
 def rope(x, pos, phases, out=None, layout="half", mscale: float = 1.0, out_dtype=None, stream=None):
     """blkattn_rope: rows x [B,H,T,d] turned by their positions pos int32
     [B,T]; out (default: a new contiguous tensor) may be x itself."""
-    return _rope((_lib or load()).blkattn_rope, x, pos, phases, out, layout, mscale, out_dtype, stream)
+    st, out = (_bind or _load_bind()).rope(x, pos, phases, out, _layout(layout), mscale, out_dtype, _handle(stream),
+                                           False)
+    _check(st)
+    return out
 
 
 def rope_backward(dy, pos, phases, out=None, layout="half", mscale: float = 1.0, out_dtype=None, stream=None):
     """blkattn_rope_bwd: the gradient of rope's x from that of its result."""
-    return _rope((_lib or load()).blkattn_rope_bwd, dy, pos, phases, out, layout, mscale, out_dtype, stream)
+    st, out = (_bind or _load_bind()).rope(dy, pos, phases, out, _layout(layout), mscale, out_dtype, _handle(stream),
+                                           True)
+    _check(st)
+    return out
 
 
 def paged_append(k, v, pos, page_table, k_pages, v_pages, phases=None, layout="half", mscale: float = 1.0, q=None,
@@ -358,9 +356,8 @@ def paged_append(k, v, pos, page_table, k_pages, v_pages, phases=None, layout="h
     padding stay unwritten), or None."""
     if q is not None and q_out is None:
         q_out = torch.zeros_like(q, memory_format=torch.contiguous_format)
-    _check((_lib or load()).blkattn_paged_append(_pack(k), _pack(v), _pack(pos), _pack(page_table), _pack(k_pages),
-                                       _pack(v_pages), _pack(phases), _layout(layout), mscale, _pack(q),
-                                       _pack(q_out), _stream_of(k, stream)))
+    _check((_bind or _load_bind()).append(k, v, pos, page_table, k_pages, v_pages, phases, _layout(layout), mscale, q,
+                                          q_out, _handle(stream))[0])
     return q_out
 
 
@@ -369,20 +366,19 @@ def fwd_paged(q, k_pages, v_pages, page_table, seqlens_k, q_logical_pos, scale: 
     """blkattn_fwd_paged: attention over the pools k_pages, v_pages
     [N,H_kv,P,d] through page_table int32 [B,entries]; out and lse are written
     in place.  tree and window as for fwd."""
-    _check((_lib or load()).blkattn_fwd_paged(_pack(q), _pack(k_pages), _pack(v_pages), _pack(page_table),
-                                              _pack(seqlens_k), _pack(q_logical_pos), _pack(tree), window, scale,
-                                              _pack(out), _pack(lse), _stream_of(q, stream)))
+    st, out, lse = (_bind or _load_bind()).fwd(q, k_pages, v_pages, page_table, seqlens_k, q_logical_pos, tree, window,
+                                               scale, out, lse, None, _handle(stream))
+    _check(st)
     return out, lse
 
 
 def attention_paged(q, k_pages, v_pages, page_table, seqlens_k, q_logical_pos, scale=None, out_dtype=torch.float32,
                     stream=None, tree=None, window: int = 0):
     """Allocate out/lse with torch and run blkattn_fwd_paged (scale defaults to 1/sqrt(d))."""
-    shape = q.shape
-    out = torch.empty(shape, dtype=out_dtype, device=q.device)
-    lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
-    return fwd_paged(q, k_pages, v_pages, page_table, seqlens_k, q_logical_pos,
-                     shape[3] ** -0.5 if scale is None else scale, out, lse, stream, tree=tree, window=window)
+    st, out, lse = (_bind or _load_bind()).fwd(q, k_pages, v_pages, page_table, seqlens_k, q_logical_pos, tree, window,
+                                               scale, None, None, out_dtype, _handle(stream))
+    _check(st)
+    return out, lse
 
 
 def _states(m, l, u) -> States:

@@ -1,6 +1,8 @@
 """Build libblkattn.so in-tree with nvcc for sm_103a (GB300).
 
-Each translation unit in csrc/ is compiled in parallel to an object file
+Also _torch_bind.so, the marshalling extension of the serving-step operators
+(csrc/torch_bind.cpp, host C++ against the installed torch), beside the nvcc
+jobs.  Each translation unit in csrc/ is compiled in parallel to an object file
 under _build/, then linked into exact_blocked_attention_gb300/libblkattn.so.
 Rebuilds only what changed (source or any header newer than its object).
 """
@@ -18,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libblkattn.so")
+BIND = os.path.join(PKG, "_torch_bind.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -39,6 +42,27 @@ def _stale(target: str, deps) -> bool:
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _build_bind() -> None:
+    src = os.path.join(CSRC, "torch_bind.cpp")
+    if not _stale(BIND, [src] + _headers()):
+        return
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"), INCLUDE]
+    lib = os.path.join(root, "lib")
+    tmp = BIND + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *[f"-I{i}" for i in inc], src, "-o", tmp, f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu",
+           "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
 
 
 def build(verbose: bool = False, jobs: int | None = None, extra_flags=()) -> str:
@@ -63,11 +87,13 @@ def build(verbose: bool = False, jobs: int | None = None, extra_flags=()) -> str
         os.replace(obj + ".tmp", obj)
         return r.stderr
 
-    if todo:
-        with ThreadPoolExecutor(jobs or min(8, len(todo))) as ex:
+    with ThreadPoolExecutor(jobs or min(8, len(todo) + 1)) as ex:
+        bind = ex.submit(_build_bind)
+        if todo:
             for (src, _), err in zip(todo, ex.map(compile_one, todo)):
                 if verbose and err.strip():
                     print(f"[{os.path.basename(src)}]\n{err}", file=sys.stderr)
+        bind.result()
     if todo or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc, *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", tmp]

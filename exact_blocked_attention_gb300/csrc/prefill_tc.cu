@@ -604,7 +604,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           // every row sees every key of the tile: P rounded to bf16 (to
           // nearest) is the product's operand, and l sums the rounded values,
-          // so u / l stays a convex combination of the values
+          // so u / l stays a convex combination of the values (over pages l
+          // sums the values before rounding: u / l is as near, and lse keeps
+          // fp32 accuracy)
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) {  // 32 keys -> 16 columns of P
             uint32_t pb[16];
@@ -612,9 +614,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 16; ++c) {
               const int k2 = 32 * q4 + 2 * c;
               const float2 e = __ffma2_rn(make_float2(xs[k2], xs[k2 + 1]), sc2, nm2);
-              pb[c] = pack_bf16(fast_exp2(e.x), fast_exp2(e.y));
-              ls[c & 3] = __fadd2_rn(ls[c & 3], make_float2(__uint_as_float(pb[c] << 16),
-                                                            __uint_as_float(pb[c] & 0xffff0000u)));
+              const float2 pp = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+              pb[c] = pack_bf16(pp.x, pp.y);
+              ls[c & 3] = __fadd2_rn(ls[c & 3], PAGED ? pp : make_float2(__uint_as_float(pb[c] << 16),
+                                                                         __uint_as_float(pb[c] & 0xffff0000u)));
             }
             tc::st16(tl + kColS + 16 * q4, pb);
           }

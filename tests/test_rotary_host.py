@@ -207,10 +207,17 @@ def test_binding_refuses_by_name():
         blkattn.rope(x.double(), torch.zeros(1, 1, dtype=I32), torch.zeros(4, dtype=I64))
 
 
-def test_packed_descriptors_match():
-    for t in (torch.zeros(2, 3, 4, 5).transpose(1, 2), torch.zeros(3, dtype=I64), torch.zeros(0, 4, dtype=I32),
-              torch.zeros(2, 3, dtype=BF16).expand(4, 2, 3)):
-        a, b = blkattn.describe(t), blkattn.Tensor.from_buffer_copy(blkattn._pack(t))
-        n = t.dim()
-        assert (a.data, a.dtype, a.ndim, a.device) == (b.data, b.dtype, b.ndim, b.device)
-        assert list(a.sizes)[:n] == list(b.sizes)[:n] and list(a.strides)[:n] == list(b.strides)[:n]
+def test_binding_refuses_what_is_no_tensor():
+    x, pos, ph = torch.zeros(1, 1, 1, 8), torch.zeros(1, 1, dtype=I32), torch.zeros(4, dtype=I64)
+    with pytest.raises(TypeError):
+        blkattn.rope(3.0, pos, ph)
+    with pytest.raises(TypeError):
+        blkattn.rope(x, "pos", ph)
+    with pytest.raises(TypeError):
+        blkattn.rope(x, pos, ph, out_dtype="float")
+    with pytest.raises(ValueError):
+        blkattn.rope(torch.zeros(1, 1, 1, 1, 8), pos, ph)  # five dimensions
+    with pytest.raises(ValueError):
+        blkattn.rope(x.to_sparse(), pos, ph)
+    with pytest.raises(ValueError):
+        blkattn.rope(x, pos, None)  # a missing argument is the library's refusal

@@ -768,6 +768,25 @@ int fwd_impl(const blkattn_tensor* q, const blkattn_tensor* k, const blkattn_ten
   return launch_fwd(p, c, pl, q, k, v, out, stream);
 }
 
+// Whether T_q >= 64 query rows over pages go to the prompt kernel (a CTA for
+// 256 rows of a head, all its keys in turn) or to the decode kernel (48 rows a
+// unit, the key tiles of all units shared by every SM).  Fitted to both
+// kernels over T_q 64..1024, 512..8192 keys and 1..64 heads: the prompt kernel
+// takes 10 us and 1.4 us (one row tile) or 1.6 us (two) a key tile and wave,
+// the decode kernel 22 us and 1.15 us a unit's tile.  Examples: 64 rows x 32
+// heads at 8192 keys 99 and 43 us, 512 rows 114 and 184 us, 512 rows x 4 heads
+// 109 and 45 us.  The keys are the table's, as everywhere in a plan.
+bool prompt_kernel_pays(const Checked& c, int sms) {
+  const int64_t keys = c.window > 0 && c.window + c.Tq < c.Tmax ? c.window + c.Tq : c.Tmax;
+  const double tiles = (double)((keys + 127) / 128);
+  const int64_t P = sms > 0 ? sms : 148;
+  const int64_t ctas = (c.Tq + 255) / 256 * c.Hq * c.B;
+  const int64_t rows = c.Hq / c.Hkv * c.Tq;
+  const double prompt = 10.0 + (c.Tq > 128 ? 1.6 : 1.4) * tiles * (double)((ctas + P - 1) / P);
+  const double decode = 22.0 + 1.15 * tiles * (double)(c.B * c.Hkv * ((rows + 47) / 48)) / (double)P;
+  return prompt <= decode;
+}
+
 // blkattn_fwd_paged: the pools take the places of k and v, their strides those
 // of the cache rows.  The tcgen05 decode kernel's unit table holds a limited
 // number of sequences: longer batches run slice by slice, one after another on
@@ -802,7 +821,7 @@ int fwd_paged_impl(const blkattn_tensor* q, const blkattn_tensor* k_pages, const
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState* ds = nullptr;
   if ((st = device_state(&ds)) != BLKATTN_OK) return st;
-  const bool prefill_ok = c.prefill_ok && scale > 0.f;
+  const bool prefill_ok = c.prefill_ok && scale > 0.f && prompt_kernel_pays(c, ds->sms);
   auto plan_of = [&](int64_t B) {
     return make_plan(B, c.Hq, c.Hkv, c.Tq, c.Tmax, (int)c.d, c.elt, ds->sms, prefill_ok, c.q_vec_ok, window > 0, true);
   };

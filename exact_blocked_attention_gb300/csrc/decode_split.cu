@@ -104,11 +104,16 @@ struct DecodeLayout {
   static_assert(kRedBytes <= kKvBytes, "reduction area must fit in the ring");
 };
 
-// PAGED: the cache lies in pages (paged.h): rows are looked up one by one, a
-// key without a page is not visible, and the value product skips every key
+// PAGED: the cache lies in pages (paged.h).  There is no producer warp: each
+// consumer warp copies its own 16 keys of a tile (16-byte asynchronous copies
+// by all its lanes, two or three tiles ahead) and needs nobody's barrier.  A
+// bulk copy a row, as below, costs some 50 ns to issue, 128 of them a tile
+// (16 x 8 KV heads of 1000 f32 keys: 96 us with them, MEASURED us without).
+// Lane i looks up key i's page one tile before its copies.  A key without a
+// page reads zeros and is not visible, and the value product skips every key
 // that no row of the CTA sees (rows never written may hold anything).
 template <typename T, int D, int R, int NW, int STAGES, bool PAGED>
-__global__ void __launch_bounds__((NW + 1) * 32)
+__global__ void __launch_bounds__((NW + (PAGED ? 0 : 1)) * 32)
     decode_split_kernel(const FwdParams p) {
   using L = DecodeLayout<T, D, R, NW, STAGES>;
   constexpr int kRowBytes = L::kRowBytes;
@@ -141,6 +146,7 @@ __global__ void __launch_bounds__((NW + 1) * 32)
   int row_end[R];  // keys [0, row_end) pass the length and position tests
   int row_h[R], row_i[R];
   int cta_end = 0;
+  int cta_start = 0x7fffffff;  // PAGED: the earliest key that a row sees
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int pk = rg * R + r;
@@ -156,13 +162,20 @@ __global__ void __launch_bounds__((NW + 1) * 32)
       const int e = pos < 0 ? 0 : (pos >= len ? len : pos + 1);
       row_end[r] = e;
       cta_end = e > cta_end ? e : cta_end;
+      if (PAGED) {
+        const int lo = p.window > 0 && pos >= 0 ? max(0, pos - p.window + 1) : 0;
+        if (lo < e) cta_start = min(cta_start, lo);
+      }
     }
   }
   const int k0 = split * p.chunk;
   // Split 0 always runs: it writes the rows that no split sees.
   if (split > 0 && k0 >= cta_end) return;
   const int k1 = min(k0 + p.chunk, cta_end);
-  const int n_tiles = k1 > k0 ? (k1 - k0 + kTile - 1) / kTile : 0;
+  // first key that is copied: the split's, or (PAGED) the tile of the rows'
+  // earliest visible key
+  const int f0 = PAGED && cta_start > k0 ? min(k0 + (cta_start - k0) / kTile * kTile, k1) : k0;
+  const int n_tiles = k1 > f0 ? (k1 - f0 + kTile - 1) / kTile : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -201,11 +214,11 @@ __global__ void __launch_bounds__((NW + 1) * 32)
     for (int e = 0; e < DPL; ++e) u[r][e] = 0.f;
   }
 
-  if (warp == NW) {
+  if (!PAGED && warp == NW) {
     // ---------------- producer warp: bulk copies of K and V rows ----------------
     const uint64_t pol = policy_evict_first();
-    const char* kbase = p.k + (PAGED ? 0 : (int64_t)b * p.k_sb) + (int64_t)hk * p.k_sh;
-    const char* vbase = p.v + (PAGED ? 0 : (int64_t)b * p.v_sb) + (int64_t)hk * p.v_sh;
+    const char* kbase = p.k + (int64_t)b * p.k_sb + (int64_t)hk * p.k_sh;
+    const char* vbase = p.v + (int64_t)b * p.v_sb + (int64_t)hk * p.v_sh;
     int t = 0;
     for (; t < n_tiles; ++t) {
       const int st = t % STAGES;
@@ -225,14 +238,6 @@ __global__ void __launch_bounds__((NW + 1) * 32)
       if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(2 * nrows * kRowBytes));
       __syncwarp();
       for (int r = lane; r < nrows; r += 32) {
-        if constexpr (PAGED) {
-          // (a key without a page copies page 0's row, which no row sees)
-          const int64_t page = max(0, page_of(p.pages, b, key0 + r));
-          const int64_t row = (key0 + r) & (p.pages.rows - 1);
-          bulk_g2s(kdst + r * kRowPad, kbase + page * p.k_sb + row * p.k_st, kRowBytes, &full[st], pol);
-          bulk_g2s(vdst + r * kRowPad, vbase + page * p.v_sb + row * p.v_st, kRowBytes, &full[st], pol);
-          continue;
-        }
         bulk_g2s(kdst + r * kRowPad, kbase + (int64_t)(key0 + r) * p.k_st, kRowBytes, &full[st], pol);
         bulk_g2s(vdst + r * kRowPad, vbase + (int64_t)(key0 + r) * p.v_st, kRowBytes, &full[st], pol);
       }
@@ -259,14 +264,60 @@ __global__ void __launch_bounds__((NW + 1) * 32)
       }
     }
 
+    // PAGED: copies of this warp's 16 keys of tile t; page: of key lane & 15,
+    // looked up a tile before
+    const uint32_t my_ring = smem_u32(ring) + warp * 16 * kRowPad;
+    auto look_up = [&](int t) {
+      const int key = f0 + t * kTile + warp * 16 + kk;
+      return t < n_tiles && key < k1 ? page_of(p.pages, b, key) : -1;
+    };
+    unsigned have = 0;  // bit i: the key of the tile copied i calls ago has a page
+    auto copy = [&](int t, int page) {
+      have = have << 1 | (page >= 0 ? 1u : 0u);
+      if (t < n_tiles) {
+        const int row = (f0 + t * kTile + warp * 16 + kk) & (p.pages.rows - 1);
+        const char* kr = page < 0 ? nullptr : p.k + (page * p.k_sb + hk * p.k_sh + row * p.k_st);
+        const char* vr = page < 0 ? nullptr : p.v + (page * p.v_sb + hk * p.v_sh + row * p.v_st);
+        const uint32_t dst = my_ring + (t % STAGES) * L::kStageBytes;
+#pragma unroll 8
+        for (int i = 0; i < CH / 2; ++i) {
+          const int r = (i * 32 + lane) / CH, c = (i * 32 + lane) % CH;  // key and 16-byte chunk
+          const char* ks = reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(kr), r));
+          const char* vs = reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(vr), r));
+          const uint32_t n = ks != nullptr ? 16u : 0u;  // 0: zeros (the address is not read)
+          cp_async_16(dst + r * kRowPad + c * 16, n ? ks + c * 16 : p.k, n);
+          cp_async_16(dst + kTile * kRowPad + r * kRowPad + c * 16, n ? vs + c * 16 : p.k, n);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int page_next = -1;
+    if (PAGED) {
+      page_next = look_up(0);
+#pragma unroll
+      for (int t = 0; t < STAGES - 1; ++t) {
+        const int page = page_next;
+        page_next = look_up(t + 1);
+        copy(t, page);
+      }
+    }
+
     for (int t = 0; t < n_tiles; ++t) {
       const int st = t % STAGES;
-      const bool ok = mbar_wait(&full[st], (t / STAGES) & 1);
-      if (!ok) {
-        if (lane == 0) { record_error(p.err, kErrTimeout); *timeout_s = 1; }
-        break;
+      if constexpr (PAGED) {
+        const int page = page_next;
+        page_next = look_up(t + STAGES);
+        copy(t + STAGES - 1, page);  // (its slot was last read before the barrier that ended tile t - 1)
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+        __syncwarp();  // every lane's copies of tile t are in
+      } else {
+        const bool ok = mbar_wait(&full[st], (t / STAGES) & 1);
+        if (!ok) {
+          if (lane == 0) { record_error(p.err, kErrTimeout); *timeout_s = 1; }
+          break;
+        }
       }
-      const int tile_k0 = k0 + t * kTile;
+      const int tile_k0 = f0 + t * kTile;
       const int key = tile_k0 + warp * 16 + kk;
       const unsigned char* kst = ring + st * L::kStageBytes;
       const unsigned char* vst = kst + kTile * kRowPad;
@@ -295,7 +346,7 @@ __global__ void __launch_bounds__((NW + 1) * 32)
         }
       }
       float s[R];
-      const bool has_page = !PAGED || (key < cta_end && page_of(p.pages, b, key) >= 0);
+      const bool has_page = !PAGED || ((have >> (STAGES - 1)) & 1u) != 0;
       bool seen = false;  // by any row
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -366,8 +417,9 @@ __global__ void __launch_bounds__((NW + 1) * 32)
           for (int e = 0; e < DPL; ++e) u[r][e] = fmaf(pj[r], vf[e], u[r][e]);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
+      if (!PAGED && lane == 0) mbar_arrive(&empty[st]);
     }
+    if (PAGED) cp_async_wait_all();
     // this warp's l: sum of the 16 key slots
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -384,7 +436,7 @@ __global__ void __launch_bounds__((NW + 1) * 32)
 
   // ---- drain: every issued copy must have landed before the ring is reused ----
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (!PAGED && threadIdx.x == 0) {
     const int issued = *issued_s;
     for (int t = issued - STAGES < 0 ? 0 : issued - STAGES; t < issued; ++t)
       if (!mbar_wait(&full[t % STAGES], (t / STAGES) & 1)) {
@@ -471,7 +523,7 @@ cudaError_t launch_one(const FwdParams& p, const DecodeConfig& cfg, cudaStream_t
   static DeviceOnce once;
   if (cudaError_t e = once.set_smem(reinterpret_cast<const void*>(kern), L::kBytes, false); e != cudaSuccess) return e;
   dim3 grid(cfg.n_splits, p.Hkv, p.B * cfg.row_groups);
-  kern<<<grid, (NW + 1) * 32, L::kBytes, stream>>>(p);
+  kern<<<grid, (NW + (PAGED ? 0 : 1)) * 32, L::kBytes, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -417,7 +417,19 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
       const long long W = __shfl_sync(0xffffffffu, incl, 31);
       // with fewer tiles than CTAs the last CTAs stay idle, so that every
       // working CTA has a tile and the CTAs holding one unit are consecutive
-      const long long P = W < (long long)gridDim.x ? W : (long long)gridDim.x;
+      long long P = W < (long long)gridDim.x ? W : (long long)gridDim.x;
+      if (PAGED && P > 0) {
+        // Few long units spread over every CTA make many parts, and one CTA
+        // folds a unit's, 512 items (4 dims of a row) at a time, four parts a
+        // round trip: t tiles a CTA cost about 1.5 t us, and units of n tiles
+        // 0.17 n / t us a fold pass.  At least the t of the minimum (with
+        // twice the fold's cost, which fits best).  One KV head, 16384 keys:
+        // 48 rows 111 us without, 34 us with it, one row 33 and 20 us; 4 x 8
+        // units of 1000 keys 17.6 and 13.2 us.
+        const float n = (float)W / (float)(B * Hkv * RG);
+        const int t_min = (int)ceilf(sqrtf(0.233f * n * (float)((R * D + 2047) / 2048)) - 0.01f);
+        if (t_min > 1) P = min(P, max(1ll, W / t_min));
+      }
       const bool works = (long long)blockIdx.x < P;
       // c W / P in 32 bits: W = q P + r, c W / P = c q + c r / P (c r < 2^16)
       const uint32_t q = (uint32_t)W / (uint32_t)(P > 0 ? P : 1), r = (uint32_t)W - q * (uint32_t)P;

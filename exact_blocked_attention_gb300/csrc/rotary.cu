@@ -75,11 +75,22 @@ constexpr int kThreads = 256;
 constexpr int kRegHeads = 4;  // V < 8: heads whose loads a thread has in flight
 constexpr int kFillBlocks = 152 * 4;  // four blocks an SM at the kernels' registers
 
-// V elements of a row in registers, moved as one access (two for 8 floats).
+// V elements of a row in registers, moved as one access.
 template <typename T, int V>
 struct alignas(sizeof(T) * V > 16 ? 16 : sizeof(T) * V) Vec {
   T x[V];
 };
+template <typename T, int V>
+__device__ __forceinline__ void store(T* p, const Vec<T, V>& y) {
+  if constexpr (sizeof(T) * V == 32) {
+    // 8 floats in one 32-byte store (whole sectors)
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(y.x[0]), "f"(y.x[1]),
+                 "f"(y.x[2]), "f"(y.x[3]), "f"(y.x[4]), "f"(y.x[5]), "f"(y.x[6]), "f"(y.x[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<Vec<T, V>*>(p) = y;
+  }
+}
 
 // Waits until at most n (0..7, a constant after unrolling) of the thread's
 // groups of asynchronous copies are pending.
@@ -105,7 +116,7 @@ constexpr int kMostHeads = 8;  // heads of one thread: 64 KB of slots a block
 template <typename TI, typename TO, int V, bool INTER>
 __device__ __forceinline__ void turn_run(const Vec<TI, V>& x0, const Vec<TI, V>& x1, bool turn, const float (&sn)[V],
                                          const float (&cs)[V], Vec<TO, V>& y0, Vec<TO, V>& y1) {
-  // elements of both runs in order: pair j is (j, V + j) or (2j, 2j + 1)
+  // elements of both runs in order: pair j is (j, V + j) or the neighbours (2j, 2j + 1)
   float u[2 * V], w[2 * V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
@@ -135,9 +146,13 @@ __device__ __forceinline__ void turn_run(const Vec<TI, V>& x0, const Vec<TI, V>&
   }
 }
 
-// One thread turns one item of a token's rows, in `hg` heads: 2 V elements of
-// V pairs (HALF: V of each half; INTERLEAVED: 2 V neighbours), or copies 2 V
-// dims past the rotated part.  Angles depend on the token and the pair alone,
+// One thread turns one item of a token's rows, in `hg` heads: two runs of V
+// dims, one from each half of the rotated part (HALF: V pairs across them;
+// INTERLEAVED: V / 2 pairs within each), or copies two runs of the dims past
+// it.  Runs from the two halves, not 2 V neighbours: with these a warp's
+// 16-byte accesses would touch every second half of a sector (measured on
+// bf16 rows of 128, INTERLEAVED: 36.5 us with neighbours against 32.4).
+// Angles depend on the token and the pair alone,
 // so a thread takes its V sines and cosines once and walks its heads with
 // them in registers.  Consecutive threads hold consecutive items, then the
 // next token: a warp moves whole 128-byte lines.
@@ -174,10 +189,12 @@ __global__ void __launch_bounds__(kThreads, kSlots<TI, V> ? 4 : 1) rotary_kernel
   const int b = tok / p.T;
   const int t = tok - b * p.T;
   const bool turn = it < rot / (2 * V);
-  // the item's two runs of V dims
-  const int i0 = 2 * V * it;
-  const int a0 = turn && !INTER ? V * it : i0;
-  const int a1 = turn && !INTER ? rot / 2 + V * it : i0 + V;
+  // the item's two runs of V dims (single dims of an INTERLEAVED pair are
+  // neighbours)
+  const int part0 = turn ? 0 : rot, part = turn ? rot : p.d - rot;  // of the row
+  const int i = it - part0 / (2 * V);                               // item within the part
+  const int a0 = part0 + (V > 1 || (turn && !INTER) ? V * i : 2 * i);
+  const int a1 = V > 1 || (turn && !INTER) ? a0 + part / 2 : a0 + 1;
   const bool second = V > 1 || a1 < p.d;
   const TI* src = static_cast<const TI*>(s.src) + (b * s.s_b + t * s.s_t + h0 * s.s_h);
   TO* dst = static_cast<TO*>(s.dst) + h0 * s.d_h;
@@ -196,7 +213,9 @@ __global__ void __launch_bounds__(kThreads, kSlots<TI, V> ? 4 : 1) rotary_kernel
     if (!turn) return;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      turn_of(pos, p.phases[(V * it + j) * p.ph_s], sn[j], cs[j]);
+      // pair j of the item
+      const int pair = !INTER || V == 1 ? V * it + j : (j < V / 2 ? a0 / 2 + j : a1 / 2 + j - V / 2);
+      turn_of(pos, p.phases[pair * p.ph_s], sn[j], cs[j]);
       sn[j] *= p.back ? -p.mscale : p.mscale;
       cs[j] *= p.mscale;
     }
@@ -225,8 +244,8 @@ __global__ void __launch_bounds__(kThreads, kSlots<TI, V> ? 4 : 1) rotary_kernel
         Vec<TO, V> y0, y1;
         turn_run<TI, TO, V, INTER>(x0, x1, turn, sn, cs, y0, y1);
         TO* r = dst + k * s.d_h;
-        *reinterpret_cast<Vec<TO, V>*>(r + a0) = y0;
-        *reinterpret_cast<Vec<TO, V>*>(r + a1) = y1;
+        store(r + a0, y0);
+        store(r + a1, y1);
       }
     }
   } else {
@@ -250,8 +269,8 @@ __global__ void __launch_bounds__(kThreads, kSlots<TI, V> ? 4 : 1) rotary_kernel
           Vec<TO, V> y0, y1;
           turn_run<TI, TO, V, INTER>(x0[k], x1[k], turn, sn, cs, y0, y1);
           TO* r = dst + (h + k) * s.d_h;
-          *reinterpret_cast<Vec<TO, V>*>(r + a0 * s.d_d) = y0;
-          if (second) *reinterpret_cast<Vec<TO, V>*>(r + a1 * s.d_d) = y1;
+          store(r + a0 * s.d_d, y0);
+          if (second) store(r + a1 * s.d_d, y1);
         }
     }
   }
@@ -290,7 +309,7 @@ template <typename TI, typename TO>
 bool runs_of(const RotaryParams& p, int V) {
   if (p.rot % (2 * V) != 0 || p.d % (2 * V) != 0) return false;
   auto fits = [V](const void* base, int bytes, int64_t sb, int64_t sh, int64_t st, int64_t sd) {
-    const int access = V * bytes > 16 ? 16 : V * bytes;
+    const int access = V * bytes;
     return sd == 1 && reinterpret_cast<uintptr_t>(base) % access == 0 && sb * bytes % access == 0 &&
            sh * bytes % access == 0 && st * bytes % access == 0;
   };

@@ -166,6 +166,16 @@ def test_prompt_chunks(B, Hq, Hkv, Tq, P, lens, out_dtype, rows_major):
     check(a, *call(a, out_dtype))
 
 
+@pytest.mark.parametrize("Hq,Hkv,Tq,d,K,window", [(4, 1, 64, 128, 9000, 0), (1, 1, 130, 128, 8200, 0),
+                                                  (4, 4, 200, 128, 8192, 0), (8, 1, 100, 64, 6000, 0),
+                                                  (1, 1, 300, 128, 8000, 3000), (2, 1, 2, 64, 40000, 0)])
+def test_few_rows_over_long_contexts(Hq, Hkv, Tq, d, K, window):
+    # prompt rows that the decode kernel serves; units split over many CTAs
+    a = make(1, Hq, Hkv, Tq, d, 32, [K], seed=Tq + K)
+    a["window"] = window
+    check(a, *call(a, BF16))
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("Tq,d,window", [(1, 128, 1), (1, 64, 100), (5, 128, 128), (3, 64, 1000), (65, 128, 1),
                                          (300, 128, 200), (129, 128, 5000), (100, 64, 37)])
@@ -235,9 +245,9 @@ def test_positions_at_the_edges():
 
 @pytest.mark.parametrize("d,P,Tq", [(128, 8, 1), (128, 64, 5), (128, 256, 40)])
 def test_same_bits_as_the_contiguous_cache(d, P, Tq):
-    # one arithmetic, whatever the page size and order (prompts sum the
-    # weights before rounding them, the contiguous ones after)
-    lens = [900, 333]
+    # one arithmetic on units that no CTA boundary splits (longer ones may be
+    # cut elsewhere, and prompts sum the weights before rounding them)
+    lens = [128, 77]
     a = make(2, 8, 2, Tq, d, P, lens, seed=13, poison=False)
     K = a["table"].shape[1] * P
     k, v = (torch.zeros(2, 2, K, d, dtype=BF16, device=dev()) for _ in range(2))

@@ -174,13 +174,16 @@ Plan make_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t Tq, int64_t Tmax, int
     pl.cfg.rows_per_cta = R;
     pl.cfg.warps = 4;
     pl.cfg.stages = (elt == Elt::BF16) ? 3 : 2;
-    pl.tile = 16 * pl.cfg.warps;
+    if (paged && elt == Elt::F32 && d == 128) pl.cfg.keys_per_warp = 8;
+    pl.tile = pl.cfg.keys_per_warp * pl.cfg.warps;
     smem = blkattn::decode_smem_bytes(elt, d, pl.cfg);
   }
   pl.cfg.row_groups = (int)((rows + pl.cfg.rows_per_cta - 1) / pl.cfg.rows_per_cta);
   const int64_t units = B * Hkv * pl.cfg.row_groups;
   const int resident = resident_ctas_per_sm(smem);
-  const int64_t target = (int64_t)(sms > 0 ? sms : 148) * resident * 4;  // ~4 waves
+  // ~4 waves; over pages one wave (16384 f32 keys of one KV head 47 and 31 us,
+  // 4 x 5 rows at 1542 keys 38 and 33 us: fewer partial states)
+  const int64_t target = (int64_t)(sms > 0 ? sms : 148) * resident * (paged ? 1 : 4);
   int64_t chunk;
   if (units >= target) {
     chunk = Tmax;

@@ -86,17 +86,19 @@ __device__ __forceinline__ float load_elt(const void* base, int64_t idx) {
     return static_cast<const float*>(base)[idx];
 }
 
-template <typename T, int D, int R, int NW, int STAGES>
+// KPW: keys of a warp in a tile (16, or 8 to halve the ring).
+template <typename T, int D, int R, int NW, int STAGES, int KPW>
 struct DecodeLayout {
   static constexpr int kRowBytes = D * EltTraits<T>::kBytes;
   static constexpr int kRowPad = kRowBytes + 16;  // 16 B skew: conflict-free key-per-lane reads
-  static constexpr int kTile = 16 * NW;           // keys per stage
+  static constexpr int kTile = KPW * NW;          // keys per stage
   static constexpr int kStageBytes = 2 * kTile * kRowPad;
-  static constexpr int kQRow = D + 4;             // floats; 16 B gap between the two halves
+  static constexpr int kParts = 32 / KPW;         // lanes that share a key's dot product
+  static constexpr int kQRow = D + 4 * (kParts - 1);  // floats; 16 B gaps between the parts
   static constexpr int kKvBytes = STAGES * kStageBytes;
   static constexpr int kQOff = kKvBytes;
   static constexpr int kPOff = kQOff + R * kQRow * 4;
-  static constexpr int kBarOff = (kPOff + NW * 16 * R * 4 + 15) / 16 * 16;
+  static constexpr int kBarOff = (kPOff + NW * KPW * R * 4 + 15) / 16 * 16;
   static constexpr int kMiscOff = kBarOff + 2 * STAGES * 8;
   static constexpr int kBytes = kMiscOff + 16;
   // cross-warp reduction area (reuses the K/V ring once every copy has landed)
@@ -108,20 +110,21 @@ struct DecodeLayout {
 // consumer warp copies its own 16 keys of a tile (16-byte asynchronous copies
 // by all its lanes, two or three tiles ahead) and needs nobody's barrier.  A
 // bulk copy a row, as below, costs some 50 ns to issue, 128 of them a tile
-// (16 x 8 KV heads of 1000 f32 keys: 96 us with them, MEASURED us without).
-// Lane i looks up key i's page one tile before its copies.  A key without a
+// (16 x 8 KV heads of 1000 f32 keys: 96 us with them, 67 us without, 49 us with
+// 8 keys a warp, which lets three blocks share an SM; one row over 1000 keys
+// 10.8 and 6.5 us).  Lane i looks up key i's page a tile before its copies.  A key without a
 // page reads zeros and is not visible, and the value product skips every key
 // that no row of the CTA sees (rows never written may hold anything).
-template <typename T, int D, int R, int NW, int STAGES, bool PAGED>
-__global__ void __launch_bounds__((NW + (PAGED ? 0 : 1)) * 32)
+template <typename T, int D, int R, int NW, int STAGES, bool PAGED, int KPW>
+__global__ void __launch_bounds__((NW + (PAGED ? 0 : 1)) * 32, PAGED ? 3 : 1)
     decode_split_kernel(const FwdParams p) {
-  using L = DecodeLayout<T, D, R, NW, STAGES>;
+  using L = DecodeLayout<T, D, R, NW, STAGES, KPW>;
   constexpr int kRowBytes = L::kRowBytes;
   constexpr int kRowPad = L::kRowPad;
   constexpr int kTile = L::kTile;
   constexpr int CH = kRowBytes / 16;        // 16-byte chunks per row
   constexpr int EPC = 16 / EltTraits<T>::kBytes;
-  constexpr int HALF = D / 2;
+  constexpr int PART = D / L::kParts;       // dims of a key that a lane sums
   constexpr int DPL = D / 32;               // value dims per lane in the PV product
 
   extern __shared__ __align__(128) unsigned char smem[];
@@ -198,7 +201,7 @@ __global__ void __launch_bounds__((NW + (PAGED ? 0 : 1)) * 32)
       val = load_elt<T>(p.q, (int64_t)b * p.q_sb + (int64_t)(hk * p.G + g) * p.q_sh +
                                  (int64_t)i * p.q_si + (int64_t)d * p.q_sd);
     }
-    q_s[r * L::kQRow + (d < HALF ? d : d + 4)] = val;
+    q_s[r * L::kQRow + d + 4 * (d / PART)] = val;
   }
   __syncthreads();
 
@@ -245,8 +248,8 @@ __global__ void __launch_bounds__((NW + (PAGED ? 0 : 1)) * 32)
     if (lane == 0) *issued_s = t;
   } else {
     // ---------------- consumer warps ----------------
-    const int kk = lane & 15;    // key slot within the warp's 16 keys
-    const int half = lane >> 4;  // which half of the head dimension this lane sums
+    const int kk = lane & (KPW - 1);  // key slot within the warp's keys
+    const int half = lane / KPW;      // which part (half, quarter) of the head dimension this lane sums
     int row_hi[R];               // split-local end of the visible range per row
 #pragma unroll
     for (int r = 0; r < R; ++r) row_hi[r] = min(row_end[r], k0 + p.chunk);
@@ -264,23 +267,23 @@ __global__ void __launch_bounds__((NW + (PAGED ? 0 : 1)) * 32)
       }
     }
 
-    // PAGED: copies of this warp's 16 keys of tile t; page: of key lane & 15,
+    // PAGED: copies of this warp's keys of tile t; page: of the lane's key kk,
     // looked up a tile before
-    const uint32_t my_ring = smem_u32(ring) + warp * 16 * kRowPad;
+    const uint32_t my_ring = smem_u32(ring) + warp * KPW * kRowPad;
     auto look_up = [&](int t) {
-      const int key = f0 + t * kTile + warp * 16 + kk;
+      const int key = f0 + t * kTile + warp * KPW + kk;
       return t < n_tiles && key < k1 ? page_of(p.pages, b, key) : -1;
     };
     unsigned have = 0;  // bit i: the key of the tile copied i calls ago has a page
     auto copy = [&](int t, int page) {
       have = have << 1 | (page >= 0 ? 1u : 0u);
       if (t < n_tiles) {
-        const int row = (f0 + t * kTile + warp * 16 + kk) & (p.pages.rows - 1);
+        const int row = (f0 + t * kTile + warp * KPW + kk) & (p.pages.rows - 1);
         const char* kr = page < 0 ? nullptr : p.k + (page * p.k_sb + hk * p.k_sh + row * p.k_st);
         const char* vr = page < 0 ? nullptr : p.v + (page * p.v_sb + hk * p.v_sh + row * p.v_st);
         const uint32_t dst = my_ring + (t % STAGES) * L::kStageBytes;
-#pragma unroll 8
-        for (int i = 0; i < CH / 2; ++i) {
+#pragma unroll 4
+        for (int i = 0; i < KPW * CH / 32; ++i) {
           const int r = (i * 32 + lane) / CH, c = (i * 32 + lane) % CH;  // key and 16-byte chunk
           const char* ks = reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(kr), r));
           const char* vs = reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(vr), r));
@@ -318,7 +321,7 @@ __global__ void __launch_bounds__((NW + (PAGED ? 0 : 1)) * 32)
         }
       }
       const int tile_k0 = f0 + t * kTile;
-      const int key = tile_k0 + warp * 16 + kk;
+      const int key = tile_k0 + warp * KPW + kk;
       const unsigned char* kst = ring + st * L::kStageBytes;
       const unsigned char* vst = kst + kTile * kRowPad;
 
@@ -326,10 +329,10 @@ __global__ void __launch_bounds__((NW + (PAGED ? 0 : 1)) * 32)
       float acc[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) acc[r] = 0.f;
-      const unsigned char* krow = kst + (warp * 16 + kk) * kRowPad + half * (kRowBytes / 2);
-      const float* qh = q_s + half * (HALF + 4);
+      const unsigned char* krow = kst + (warp * KPW + kk) * kRowPad + half * (kRowBytes / L::kParts);
+      const float* qh = q_s + half * (PART + 4);
 #pragma unroll
-      for (int c = 0; c < CH / 2; ++c) {
+      for (int c = 0; c < CH / L::kParts; ++c) {
         float kf[EPC];
         unpack16<T>(*reinterpret_cast<const uint4*>(krow + c * 16), kf);
 #pragma unroll
@@ -350,7 +353,8 @@ __global__ void __launch_bounds__((NW + (PAGED ? 0 : 1)) * 32)
       bool seen = false;  // by any row
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], 16);
+#pragma unroll
+        for (int off = 16; off >= KPW; off >>= 1) acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], off);
         bool vis = has_page && key < row_hi[r] && key >= row_lo[r];
         if (key >= tbase) {
           const int node = key - tbase;
@@ -373,7 +377,7 @@ __global__ void __launch_bounds__((NW + (PAGED ? 0 : 1)) * 32)
       for (int r = 0; r < R; ++r) {
         float mt = s[r];
 #pragma unroll
-        for (int off = 8; off >= 1; off >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
+        for (int off = KPW / 2; off >= 1; off >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
         pr[r] = 0.f;
         if (mt != kNegInf) {  // this block has a valid key for row r
           const float m_new = fmaxf(m_run[r], mt);
@@ -385,16 +389,16 @@ __global__ void __launch_bounds__((NW + (PAGED ? 0 : 1)) * 32)
           for (int e = 0; e < DPL; ++e) u[r][e] *= alpha;
         }
       }
-      float* pw = p_s + warp * 16 * R;
-      if (lane < 16) {
+      float* pw = p_s + warp * KPW * R;
+      if (lane < KPW) {
 #pragma unroll
         for (int r = 0; r < R; ++r) pw[kk * R + r] = pr[r];
       }
       __syncwarp();
       // PV over this warp's keys that were loaded (never the rows past k1)
-      int nk = k1 - (tile_k0 + warp * 16);
-      nk = nk < 0 ? 0 : (nk > 16 ? 16 : nk);
-      const unsigned char* vrow = vst + (warp * 16) * kRowPad + lane * DPL * EltTraits<T>::kBytes;
+      int nk = k1 - (tile_k0 + warp * KPW);
+      nk = nk < 0 ? 0 : (nk > KPW ? KPW : nk);
+      const unsigned char* vrow = vst + (warp * KPW) * kRowPad + lane * DPL * EltTraits<T>::kBytes;
 #pragma unroll 4
       for (int j = 0; j < nk; ++j) {
         if (PAGED && !((alive >> j) & 1u)) continue;
@@ -420,10 +424,10 @@ __global__ void __launch_bounds__((NW + (PAGED ? 0 : 1)) * 32)
       if (!PAGED && lane == 0) mbar_arrive(&empty[st]);
     }
     if (PAGED) cp_async_wait_all();
-    // this warp's l: sum of the 16 key slots
+    // this warp's l: sum of the key slots
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float l = (lane < 16) ? l_lane[r] : 0.f;
+      float l = (lane < KPW) ? l_lane[r] : 0.f;
 #pragma unroll
       for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
       l_lane[r] = l;
@@ -518,8 +522,11 @@ __global__ void __launch_bounds__((NW + (PAGED ? 0 : 1)) * 32)
 
 template <typename T, int D, int R, int NW, int STAGES, bool PAGED>
 cudaError_t launch_one(const FwdParams& p, const DecodeConfig& cfg, cudaStream_t stream) {
-  using L = DecodeLayout<T, D, R, NW, STAGES>;
-  auto kern = decode_split_kernel<T, D, R, NW, STAGES, PAGED>;
+  // f32 rows of 128 over pages: 8 keys a warp, three blocks an SM
+  constexpr int KPW = PAGED && D * EltTraits<T>::kBytes == 512 ? 8 : 16;
+  using L = DecodeLayout<T, D, R, NW, STAGES, KPW>;
+  if (cfg.keys_per_warp != KPW) return cudaErrorInvalidValue;
+  auto kern = decode_split_kernel<T, D, R, NW, STAGES, PAGED, KPW>;
   static DeviceOnce once;
   if (cudaError_t e = once.set_smem(reinterpret_cast<const void*>(kern), L::kBytes, false); e != cudaSuccess) return e;
   dim3 grid(cfg.n_splits, p.Hkv, p.B * cfg.row_groups);
@@ -559,9 +566,9 @@ cudaError_t dispatch_types(const FwdParams& p, Elt elt, int d, const DecodeConfi
 // 16-bit rows of 128 (two CTAs fit an SM), 2 stages for 512-byte f32 rows.
 size_t decode_smem_bytes(Elt elt, int d, const DecodeConfig& cfg) {
   const int rb = d * (elt == Elt::BF16 ? 2 : 4);
-  const int tile = 16 * cfg.warps;
+  const int tile = cfg.keys_per_warp * cfg.warps;
   size_t bytes = (size_t)cfg.stages * 2 * tile * (rb + 16);
-  bytes += (size_t)cfg.rows_per_cta * (d + 4) * 4 + (size_t)cfg.warps * 16 * cfg.rows_per_cta * 4;
+  bytes += (size_t)cfg.rows_per_cta * (d + 4 * (32 / cfg.keys_per_warp - 1)) * 4 + (size_t)tile * cfg.rows_per_cta * 4;
   return bytes + 2 * cfg.stages * 8 + 32;
 }
 

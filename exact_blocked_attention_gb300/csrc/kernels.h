@@ -92,6 +92,7 @@ struct DecodeConfig {
   int chunk;
   int n_splits;
   int row_groups;
+  int keys_per_warp = 16;  // CUDA-core kernel: keys of a warp in a tile
 };
 
 cudaError_t launch_decode_split(const FwdParams& p, Elt elt, int d, const DecodeConfig& cfg,

@@ -679,7 +679,7 @@ int check_pages(const blkattn_tensor* k_pages, const blkattn_tensor* v_pages, co
       table->sizes[0] != B)
     return BLKATTN_ERR_INVALID_ARG;
   if ((rows & (rows - 1)) != 0 || rows < kMinPageRows || rows > kMaxPageRows) return BLKATTN_ERR_UNSUPPORTED;
-  if (N > 0x7fffffff || entries > 0x7fffffff / rows) return BLKATTN_ERR_UNSUPPORTED;
+  if (N > 0x7fffffff || entries > kMaxCacheRows / rows) return BLKATTN_ERR_UNSUPPORTED;
   out->table = static_cast<const int32_t*>(table->data);
   out->sb = table->strides[0];
   out->sp = table->strides[1];
@@ -794,11 +794,23 @@ bool prompt_kernel_pays(const Checked& c, int sms) {
 // of the cache rows.  The tcgen05 decode kernel's unit table holds a limited
 // number of sequences: longer batches run slice by slice, one after another on
 // the stream, in the same workspace.
-int fwd_paged_impl(const blkattn_tensor* q, const blkattn_tensor* k_pages, const blkattn_tensor* v_pages,
+int fwd_paged_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages_, const blkattn_tensor* v_pages_,
                    const blkattn_tensor* page_table, const blkattn_tensor* seqlens_k,
                    const blkattn_tensor* q_logical_pos, const blkattn_tensor* tree, int64_t window, float scale,
-                   const blkattn_tensor* out, const blkattn_tensor* lse, blkattn_stream_t stream_) {
-  if (!dims_ok(q, 4) || !dims_ok(k_pages, 4) || !dims_ok(v_pages, 4)) return BLKATTN_ERR_INVALID_ARG;
+                   const blkattn_tensor* out_, const blkattn_tensor* lse, blkattn_stream_t stream_) {
+  if (!dims_ok(q_, 4) || !dims_ok(k_pages_, 4) || !dims_ok(v_pages_, 4) || !dims_ok(out_, 4))
+    return BLKATTN_ERR_INVALID_ARG;
+  // The stride of a dim of size 1 is never used, but tensor maps and alignment
+  // checks look at it: the row's length stands in for it.
+  blkattn_tensor qn = *q_, kn = *k_pages_, vn = *v_pages_, on = *out_;
+  for (blkattn_tensor* t : {&qn, &kn, &vn, &on})
+    for (int i = 0; i < 3; ++i)
+      if (t->sizes[i] == 1) t->strides[i] = t->sizes[3];
+  const blkattn_tensor *q = &qn, *k_pages = &kn, *v_pages = &vn, *out = &on;
+  // (the pools' rows are told apart by their strides: none may broadcast)
+  for (const blkattn_tensor* t : {k_pages, v_pages})
+    for (int i = 0; i < 3; ++i)
+      if (t->sizes[i] > 1 && t->strides[i] == 0) return BLKATTN_ERR_INVALID_ARG;
   PageTable pt;
   int st = check_pages(k_pages, v_pages, page_table, q->dtype, q->sizes[0], k_pages->sizes[1], q->sizes[3], &pt);
   if (st != BLKATTN_OK) return st;
@@ -853,8 +865,13 @@ int fwd_paged_impl(const blkattn_tensor* q, const blkattn_tensor* k_pages, const
   } else if (pl.cfg.kernel == blkattn::Kernel::CudaCore && pl.cfg.row_groups > 65535) {
     return BLKATTN_ERR_UNSUPPORTED;
   }
-  if (pl.ws_bytes > 0 && (st = ensure_workspace(ds, (size_t)pl.ws_bytes, stream)) != BLKATTN_OK) return st;
-  if (pl.units > 0 && (st = ensure_counters(ds, pl.units, stream)) != BLKATTN_OK) return st;
+  // (the last slice has a plan of its own; scratch for both, before any launch)
+  const int64_t rest = c.B % nb;
+  const Plan tail = rest != 0 ? plan_of(rest) : pl;
+  const int64_t ws_bytes = pl.ws_bytes > tail.ws_bytes ? pl.ws_bytes : tail.ws_bytes;
+  const int64_t units = pl.units > tail.units ? pl.units : tail.units;
+  if (ws_bytes > 0 && (st = ensure_workspace(ds, (size_t)ws_bytes, stream)) != BLKATTN_OK) return st;
+  if (units > 0 && (st = ensure_counters(ds, units, stream)) != BLKATTN_OK) return st;
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return cuda_fail(e);
   CUtensorMap mk, mv, mq, mo;
@@ -882,11 +899,7 @@ int fwd_paged_impl(const blkattn_tensor* q, const blkattn_tensor* k_pages, const
   for (int64_t b0 = 0; b0 < c.B; b0 += nb) {
     Checked cs = c;
     cs.B = c.B - b0 < nb ? c.B - b0 : nb;
-    Plan ps = pl;
-    if (cs.B != nb && !prefill) {
-      ps = plan_of(cs.B);  // the last slice: its own split (never more scratch than the full ones' maximum below)
-      if (ps.ws_bytes > 0 && (st = ensure_workspace(ds, (size_t)ps.ws_bytes, stream)) != BLKATTN_OK) return st;
-    }
+    const Plan& ps = cs.B == nb ? pl : tail;
     FwdParams p = fill_params(q, &kc, &vc, seqlens_k, q_logical_pos, tree, nullptr, scale, out, lse, cs, ps, ds->ws,
                               ds->err, ds->cnt);
     p.pages = pt;

@@ -40,6 +40,7 @@ __device__ __forceinline__ int page_of(const PageTable& pt, int b, int t) {
 }
 
 constexpr int64_t kMinPageRows = 8, kMaxPageRows = 65536;
+constexpr int64_t kMaxCacheRows = (1 << 30) - 1;  // of a sequence: 32-bit sums of a key and a chunk do not overflow
 
 // A kernel's shared-memory limit, raised once on each device that launches it
 // (the attribute belongs to the device's copy of the kernel).

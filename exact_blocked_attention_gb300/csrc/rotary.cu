@@ -283,13 +283,21 @@ cudaError_t launch_v(RotaryParams p, cudaStream_t stream) {
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;  // (more elements than the card holds)
   // Heads of a thread: enough that the sines cost little, few enough that
   // every SM has its threads
-  int most = 0, groups = 0;
+  int most = 0;
   for (int i = 0; i < p.n_sets; ++i) most = p.set[i].heads > most ? p.set[i].heads : most;
   const int64_t want = (kFillBlocks + blocks - 1) / blocks;  // groups that fill the machine
   int64_t hg = (most + want - 1) / want;
   p.hg = (int)(hg < 1 ? 1 : (hg > kMostHeads ? kMostHeads : hg));
-  for (int i = 0; i < p.n_sets; ++i) groups += p.groups[i] = (p.set[i].heads + p.hg - 1) / p.hg;
-  if (groups > 65535) return cudaErrorInvalidValue;
+  auto count_groups = [&]() {
+    int n = 0;
+    for (int i = 0; i < p.n_sets; ++i) n += p.groups[i] = (p.set[i].heads + p.hg - 1) / p.hg;
+    return n;
+  };
+  int groups = count_groups();
+  if (groups > 65535) {  // (grid y; at most 98301 heads)
+    p.hg = kMostHeads;
+    groups = count_groups();
+  }
   const int smem = kSlots<TI, V> ? p.hg * 32 * kThreads : 0;
   if (smem > 48 * 1024) {
     static DeviceOnce once;

@@ -388,7 +388,7 @@ int blkattn_rope_bwd(const blkattn_tensor* dy, const blkattn_tensor* pos, const 
  * The paged KV cache.  K and V live in pools of pages [N, H_kv, P, d] (any
  * strides: [N, P, H_kv, d] memory is a view of it); row t of sequence b is
  * row t mod P of page page_table[b, t / P].  An entry outside [0, N) holds no
- * page.  P is a power of two, 8 <= P <= 65536, and entries x P < 2^31; other
+ * page.  P is a power of two, 8 <= P <= 65536, and entries x P < 2^30; other
  * P give BLKATTN_ERR_UNSUPPORTED.  Sequences may share pages.
  *
  * blkattn_paged_append — write new rows into the cache, rotated on the way.
@@ -420,7 +420,9 @@ int blkattn_paged_append(const blkattn_tensor* k, const blkattn_tensor* v, const
  * q, seqlens_k, q_logical_pos, scale, out, lse, stream: as for blkattn_fwd
  * (scale finite; out and lse without broadcast dims).
  * k_pages, v_pages  [N, H_kv, P, d] of q's dtype, P as above: last stride 1,
- *             the other strides and the base addresses multiples of 16 bytes.
+ *             the other strides (none 0) and the base addresses multiples of
+ *             16 bytes.  A dim of size 1 may have any stride, here and in q
+ *             and out.
  * page_table  int32 [B, entries], any strides.  T_max = entries x P.
  * tree_mask   NULL, or as for blkattn_fwd_tree.
  * window      0 (none), or as for blkattn_fwd_window; not with a tree.

@@ -305,6 +305,24 @@ def test_strided_views_and_shared_pages():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("Tq,d,dtype", [(1, 128, BF16), (70, 128, BF16), (2, 64, BF16), (1, 64, F32)])
+def test_strides_of_single_dims_do_not_matter(Tq, d, dtype):
+    # one sequence, one KV head, one page of 512 rows: every such dim with a stride of 0 or of no alignment
+    a = make(1, 4, 1, Tq, d, 512, [300], dtype, seed=20, spare=0, entries=1)
+    want = call(a, dtype)
+    check(a, *want)
+
+    def odd(t, s):
+        return t.as_strided(t.shape, [x if n > 1 else s for n, x in zip(t.shape, t.stride())])
+
+    for s in (0, 1, 7):
+        b = dict(a, q=odd(a["q"], s), kp=odd(a["kp"], s), vp=odd(a["vp"], s), table=odd(a["table"], s),
+                 pos=odd(a["pos"], s), lens=odd(a["lens"], s))
+        out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+        blkattn.fwd_paged(b["q"], b["kp"], b["vp"], b["table"], b["lens"], b["pos"], b["scale"], odd(out, s), odd(lse, s))
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
 @pytest.mark.parametrize("out_dtype", [F32, BF16])
 def test_prompt_output_layouts(out_dtype):
     a = make(1, 4, 2, 150, 128, 32, [400], seed=19)

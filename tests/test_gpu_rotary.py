@@ -345,6 +345,21 @@ def test_append_offsets_past_32_bits():
     assert int(torch.count_nonzero(vp[1:N - 1])) == 0
 
 
+def test_append_of_very_many_heads():
+    # more heads than grid rows: 3 x 22000
+    H, d = 22000, 16
+    k, v, q = (rows((1, H, 1, d), BF16, 70 + i, True) for i in range(3))
+    kp, vp = pools(2, H, 8, d, BF16, False, 73)
+    table = torch.tensor([[1]], dtype=torch.int32, device=dev())
+    pos = torch.tensor([[5]], dtype=torch.int32, device=dev())
+    w = angles(d)
+    ph = blkattn.rope_phases(w)
+    qo = blkattn.paged_append(k, v, pos, table, kp, vp, phases=ph, q=q)
+    check(qo, *turned(q, pos, w, "half"))
+    check(kp[1, :, 5], *(z[0, :, 0] for z in turned(k, pos, w, "half")))
+    assert torch.equal(vp[1, :, 5], v[0, :, 0])
+
+
 def test_append_q_in_place_and_graph():
     w = angles(128)
     ph = blkattn.rope_phases(w)

@@ -53,7 +53,9 @@ def call(lib, a):
     (dict(out=FakeTensor((2, 8, 3, 128), F32, strides=(1024, 0, 128, 1), addr=0x300000)), -1),
     (dict(lse=FakeTensor((2, 8, 3), F32, strides=(0, 3, 1), addr=0x400000)), -1),
     (dict(qp=FakeTensor((2, 4), I32)), -1), (dict(sl=FakeTensor((2,), I64)), -1),
-    (dict(table=FakeTensor((2, 1 << 27), I32)), -2),
+    (dict(table=FakeTensor((2, 1 << 27), I32)), -2), (dict(table=FakeTensor((2, 1 << 26), I32)), -2),
+    (dict(kp=FakeTensor((9, 2, 16, 128), BF16, strides=(4096, 0, 128, 1), addr=0x100000)), -1),
+    (dict(vp=FakeTensor((9, 2, 16, 128), BF16, strides=(0, 2048, 128, 1), addr=0x200000)), -1),
 ])
 def test_refuses(lib, change, want):
     a = args()

@@ -31,7 +31,7 @@
 // every CTA streams the same number of tiles whatever the length mix, and no
 // SM idles at the end.
 //
-// Roles (352 threads):
+// Roles (352 threads; over pages 384, see the kernel):
 //  * warps 0-7: key threads.  Thread k of lane quarter k / 32 owns key k of
 //    the current tile (TMEM lane k); the two warps of a quarter split the NR
 //    rows in halves.  A thread reads the scores of its key for its rows,
@@ -275,19 +275,32 @@ __device__ __forceinline__ int scatter_base(int lane) {
   return ((lane >> 4) & 1) * (NH / 2) + ((lane >> 3) & 1) * (NH / 4) + ((lane >> 2) & 1) * (NH / 8);
 }
 
-// D: head dim, 128 or 64.  With 64 the value product still has M = 128: its
-// upper 64 TMEM lanes take whatever the next 16 KB of shared memory hold (the
-// next ring slot, past the last one the query and P buffers) and nothing reads
-// them.
+// D: head dim, 128 or 64.  With 64 the value product has M = 64, whose rows lie
+// in the first 16 TMEM lanes of each warp's quarter (M = 128 with the upper
+// half unused takes the same time).
 //
 // PAGED: the cache lies in pages (paged.h).  A tile of 128 keys is one box of
-// a page of at least 128 rows, or the boxes of 128 / P pages: the producer
-// warp's lanes each look one page up (a tile ahead) and issue its copies.  A
-// page number outside the pool goes to the copy as -1, which lies outside the
-// tensor map and reads as zeros, and the key threads mask its keys.  V rows
-// that no row of the unit sees (before a window, past the end, unlisted tree
-// nodes) are zero-filled in shared memory: rows of a page that were never
-// written may hold anything.
+// a page of at least 128 rows, or the boxes of 128 / P pages, issued by lanes
+// of two producer warps, one for K and one for V: a copy takes its warp some
+// 50 ns to issue, and pages of 16 need 16 of them a tile.  Rows of 128 dims
+// that lie packed (PageTable::wide) come with both 64-dim halves in one box.
+// Measured on batch-32 GQA decode (571 MB), pages of 16: one warp and a box a
+// half 115 us, two warps 107, one box for both halves 100, both 96; pages of 8
+// 99, of 128 96; the contiguous cache 91 (the rest is per unit: the lookups
+// and the wider row facts).  One lane issuing every box in a loop: 110.
+// A page number outside the pool goes to the copy as -1, which lies outside
+// the tensor map and reads as zeros; the loader warp scans the unit's entries,
+// and only a unit that misses a page has its key threads look their keys up
+// and mask them (a lookup in every key thread cost the 48-row units 10 us of
+// 115).  V rows that no row of the unit sees (before a window, past the end,
+// unlisted tree nodes) are zero-filled in shared memory: rows of a page that
+// were never written may hold anything.
+//
+// What bounds it: memory at d = 128 (one 131072-key context 89-91 us, 88-90 %
+// of the copy bandwidth).  At d = 64 a tile is half the bytes for the same
+// chain of scores, P and value product, about 0.9 us: 16 x 8 windows of 4096
+// keys 39.7 us, half of the bandwidth, 15 us of it start and finish.  Two
+// issuing threads (scores, value products) did not shorten it.
 template <int NR, int D, bool PAGED>
 __global__ void __launch_bounds__(kThreads<PAGED>, 1)
     decode_tc_kernel(const FwdParams p, const __grid_constant__ CUtensorMap tmk,
@@ -296,7 +309,7 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
   constexpr int kSlotBytes = L::kSlotBytes;
   constexpr uint32_t kIdescQK = tc::idesc_bf16(128, NR, 0, 0);  // K, Q both K-major
   // V^T, P^T both MN-major; N spans the P_hi atom (NR used of 64) and the P_lo atom
-  constexpr uint32_t kIdescPV = tc::idesc_bf16(128, L::kPVN, 1, 1);
+  constexpr uint32_t kIdescPV = tc::idesc_bf16(D, L::kPVN, 1, 1);
   constexpr int kSlots = L::kSlots;
   // weight-only tiles per unit in the partition (its set-up and readout)
   constexpr int kUnitExtra = NR >= 48 ? 2 : 0;  // measured best: 48-row units pay a real set-up cost
@@ -893,6 +906,9 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
     const int quarter = warp & 3;
     const int half = warp >> 2;
     const int k = 32 * quarter + lane;
+    // value dim of this thread's TMEM lane in U^T
+    const int vd = D == 128 ? k : 16 * quarter + lane;
+    const bool has_vd = D == 128 || lane < 16;
     const int c0 = half * NH;
     const uint32_t tl = tb + ((uint32_t)(32 * quarter) << 16);
     auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -936,8 +952,8 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
           const int row = c0 + r;
           if (row >= rr) break;
           const float o = (s_mfin[row] == kNegInf) ? 0.f : u[r] * s_inv[row];
-          if (D < 128 && k >= D) break;  // (lanes past the value dims)
-          const int64_t oi = pf.ooff[row] + (int64_t)k * p.o_sd;
+          if (!has_vd) break;
+          const int64_t oi = pf.ooff[row] + (int64_t)vd * p.o_sd;
           if (p.out_bf16)
             static_cast<__nv_bfloat16*>(p.out)[oi] = __float2bfloat16_rn(o);
           else
@@ -957,8 +973,8 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
 #pragma unroll
         for (int r = 0; r < NH; ++r) {
           const int row = c0 + r;
-          if (row >= rr || (D < 128 && k >= D)) break;
-          st_global_hint(p.ws_u + ((slot * R + row) * D) + k, u[r], keep);
+          if (row >= rr || !has_vd) break;
+          st_global_hint(p.ws_u + ((slot * R + row) * D) + vd, u[r], keep);
         }
         if (half == 0 && k < rr) {
           st_global_hint(p.ws_m + slot * R + k, s_mfin[k], keep);

@@ -106,7 +106,10 @@ __device__ __forceinline__ int spec_first_tile(int q0, int window) {
 // PAGED: the cache lies in pages (paged.h).  A key tile is one box of a page of
 // at least 128 rows or the boxes of 128 / P pages: the producer warp's lanes
 // look their pages up a tile ahead and issue the copies; a page number outside
-// the pool goes to the copy as -1 (zeros) and the rows mask its keys.
+// the pool goes to the copy as -1 (zeros) and the rows mask its keys, in
+// tensor memory (a mask in registers spilled 576 bytes).  The chain of a key
+// tile bounds it as over a contiguous cache: 2 x 2048 rows of 32 heads at 8192
+// keys 376 us (1280 TFLOP/s, 65 % of the bf16 burst rate), contiguous 384.
 template <bool WIN, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const FwdParams p, const __grid_constant__ CUtensorMap tmq,

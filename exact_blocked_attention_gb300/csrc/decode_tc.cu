@@ -283,7 +283,7 @@ __device__ __forceinline__ int scatter_base(int lane) {
 // a page of at least 128 rows, or the boxes of 128 / P pages, issued by lanes
 // of two producer warps, one for K and one for V: a copy takes its warp some
 // 50 ns to issue, and pages of 16 need 16 of them a tile.  Rows of 128 dims
-// that lie packed (PageTable::wide) come with both 64-dim halves in one box.
+// that lie packed (WIDE) come with both 64-dim halves in one box.
 // Measured on batch-32 GQA decode (571 MB), pages of 16: one warp and a box a
 // half 115 us, two warps 107, one box for both halves 100, both 96; pages of 8
 // 99, of 128 96; the contiguous cache 91 (the rest is per unit: the lookups
@@ -301,7 +301,9 @@ __device__ __forceinline__ int scatter_base(int lane) {
 // chain of scores, P and value product, about 0.9 us: 16 x 8 windows of 4096
 // keys 39.7 us, half of the bandwidth, 15 us of it start and finish.  Two
 // issuing threads (scores, value products) did not shorten it.
-template <int NR, int D, bool PAGED>
+// (WIDE is a template argument for the issuing thread's sake: descriptor steps
+// that are constants take 1 us off 96, 1.4 off 39.7 at d = 64.)
+template <int NR, int D, bool PAGED, bool WIDE>
 __global__ void __launch_bounds__(kThreads<PAGED>, 1)
     decode_tc_kernel(const FwdParams p, const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv) {
@@ -537,10 +539,9 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
     const int n_pieces = BK >> box_shift;
     const int piece = lane & (n_pieces - 1);
     const int half = lane >> (7 - box_shift);
-    const bool wide = p.pages.wide;
-    const bool copies = half < (wide ? 1 : L::kBoxes);
+    const bool copies = half < (WIDE ? 1 : L::kBoxes);
     const uint32_t dst_off =
-        wide ? (uint32_t)((piece << box_shift) * 256) : (uint32_t)(half * kBox + (piece << box_shift) * 128);
+        WIDE ? (uint32_t)((piece << box_shift) * 256) : (uint32_t)(half * kBox + (piece << box_shift) * 128);
     // What the lane looks up for a tile, one tile ahead: its piece's table
     // entry and the sequence's length.  Neither load waits for the other, and
     // nothing looks at them before the tile's turn.
@@ -572,7 +573,7 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
       __syncwarp();
       if (copies) {
         unsigned char* dst = sm + L::kOffRing + s * kSlotBytes + dst_off;
-        if (wide)
+        if (WIDE)
           tma_load_5d(dst, map, 0, 0, kvh * p.pages.wide_h2, (row >> 3) + kvh * p.pages.wide_h3, page, &full[s], pol);
         else
           tma_load_4d(dst, map, 64 * half, row, kvh, page, &full[s], pol);
@@ -818,10 +819,9 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
       // K and V tiles: two 64-dim boxes 16 KB apart, rows 128 bytes apart; a
       // page's wide box instead has the two halves of 8 rows side by side
       // (8-row groups 2 KB apart, the second half 1 KB behind the first)
-      const bool wide = PAGED && p.pages.wide;
-      const uint32_t kHiKV = wide ? tc::desc_hi(2048) : kHi;
-      const uint32_t half_step = (wide ? 1024u : (uint32_t)kBox) >> 4;
-      const uint32_t key16_step = (wide ? 4096u : 2048u) >> 4;
+      constexpr uint32_t kHiKV = WIDE ? tc::desc_hi(2048) : kHi;
+      constexpr uint32_t half_step = (WIDE ? 1024u : (uint32_t)kBox) >> 4;
+      constexpr uint32_t key16_step = (WIDE ? 4096u : 2048u) >> 4;
       // shared-memory descriptors: only the address word moves per MMA
       const uint32_t qlo0 = tc::desc_lo(sQ, 16);
       auto issue_qk = [&](uint32_t buf) -> bool {
@@ -1255,7 +1255,7 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
         }
         if (unseen && half < L::kBoxes) {
           unsigned char* vr = sm + L::kOffRing + (int)(sv % kSlots) * kSlotBytes +
-                              (PAGED && p.pages.wide ? (k >> 3) * 2048 + half * 1024 + (k & 7) * 128
+                              (WIDE ? (k >> 3) * 2048 + half * 1024 + (k & 7) * 128
                                                      : half * kBox + k * 128);
 #pragma unroll
           for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vr + ((c ^ (k & 7)) << 4)) = make_uint4(0, 0, 0, 0);
@@ -1324,27 +1324,27 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
   if (warp == kMmaWarp) tc::dealloc(tb, kTmemCols);
 }
 
-template <int NR, int D, bool PAGED>
+template <int NR, int D, bool PAGED, bool WIDE>
 cudaError_t launch_nr(const FwdParams& p, int ctas, const CUtensorMap& tmk, const CUtensorMap& tmv,
                       cudaStream_t stream) {
   using L = TcLayout<NR, D>;
   static DeviceOnce once;
-  if (cudaError_t e = once.set_smem(reinterpret_cast<const void*>(&decode_tc_kernel<NR, D, PAGED>), L::kBytes);
+  if (cudaError_t e = once.set_smem(reinterpret_cast<const void*>(&decode_tc_kernel<NR, D, PAGED, WIDE>), L::kBytes);
       e != cudaSuccess)
     return e;
-  decode_tc_kernel<NR, D, PAGED><<<ctas, kThreads<PAGED>, L::kBytes, stream>>>(p, tmk, tmv);
+  decode_tc_kernel<NR, D, PAGED, WIDE><<<ctas, kThreads<PAGED>, L::kBytes, stream>>>(p, tmk, tmv);
   return cudaGetLastError();
 }
 
-template <int D, bool PAGED>
+template <int D, bool PAGED, bool WIDE>
 cudaError_t launch_rows(const FwdParams& p, int ctas, const CUtensorMap& tmk, const CUtensorMap& tmv,
                         cudaStream_t stream) {
   if (p.rows_cta < 1 || p.rows_cta > 48 || ctas < 1 ||
       p.B * p.row_groups > (p.window > 0 ? kDecodeTcMaxEntries / 2 : kDecodeTcMaxEntries))
     return cudaErrorInvalidValue;
-  if (p.rows_cta <= 16) return launch_nr<16, D, PAGED>(p, ctas, tmk, tmv, stream);
-  if (p.rows_cta <= 32) return launch_nr<32, D, PAGED>(p, ctas, tmk, tmv, stream);
-  return launch_nr<48, D, PAGED>(p, ctas, tmk, tmv, stream);
+  if (p.rows_cta <= 16) return launch_nr<16, D, PAGED, WIDE>(p, ctas, tmk, tmv, stream);
+  if (p.rows_cta <= 32) return launch_nr<32, D, PAGED, WIDE>(p, ctas, tmk, tmv, stream);
+  return launch_nr<48, D, PAGED, WIDE>(p, ctas, tmk, tmv, stream);
 }
 
 }  // namespace
@@ -1357,13 +1357,14 @@ size_t decode_tc_smem_bytes(int nr) {
 
 cudaError_t launch_decode_tc(const FwdParams& p, int ctas, const CUtensorMap& tmk, const CUtensorMap& tmv,
                              cudaStream_t stream) {
-  return launch_rows<128, false>(p, ctas, tmk, tmv, stream);
+  return launch_rows<128, false, false>(p, ctas, tmk, tmv, stream);
 }
 
 cudaError_t launch_decode_tc_paged(const FwdParams& p, int d, int ctas, const CUtensorMap& tmk,
                                    const CUtensorMap& tmv, cudaStream_t stream) {
-  if (d == 128) return launch_rows<128, true>(p, ctas, tmk, tmv, stream);
-  if (d == 64) return launch_rows<64, true>(p, ctas, tmk, tmv, stream);
+  if (d == 128 && p.pages.wide) return launch_rows<128, true, true>(p, ctas, tmk, tmv, stream);
+  if (d == 128) return launch_rows<128, true, false>(p, ctas, tmk, tmv, stream);
+  if (d == 64) return launch_rows<64, true, false>(p, ctas, tmk, tmv, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -278,6 +278,31 @@ def test_same_bits_whatever_the_pages(Tq, d, dtype):
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
+@pytest.mark.parametrize("Tq,d,dtype", [(1, 128, BF16), (6, 128, BF16), (90, 128, BF16), (2, 64, BF16), (2, 128, F32)])
+def test_same_bits_whatever_the_pool_layout(Tq, d, dtype):
+    # packed heads, packed rows, gaps behind every row, page part or head, K and V laid out differently
+    a = make(2, 8, 2, Tq, d, 16, [500, 333], dtype, seed=15)
+    want = call(a)
+    N = a["kp"].shape[0]
+
+    def padded(t, rows=0, dims=0, heads=0):
+        buf = torch.full((N, 2 + heads, 16 + rows, d + dims), math.nan, dtype=dtype, device=dev())
+        buf[:, :2, :16, :d] = t
+        return buf[:, :2, :16, :d]
+
+    def by_rows(t, heads=0):
+        buf = torch.full((N, 16, 2 + heads, d), math.nan, dtype=dtype, device=dev())
+        buf[:, :, :2] = t.transpose(1, 2)
+        return buf[:, :, :2].transpose(1, 2)
+
+    k, v = a["kp"], a["vp"]
+    for kp, vp in ((padded(k, rows=8), padded(v, rows=8)), (padded(k, dims=8), padded(v, dims=8)),
+                   (padded(k, heads=1), padded(v, heads=1)), (by_rows(k), by_rows(v)),
+                   (by_rows(k, 3), by_rows(v, 3)), (by_rows(k), padded(v)), (padded(k, dims=64, rows=3), by_rows(v))):
+        out, lse = call(dict(a, kp=kp, vp=vp))
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
 def test_strided_views_and_shared_pages():
     a = make(2, 8, 2, 3, 64, 16, [200, 200], seed=17)
     a["table"][1] = a["table"][0]  # the same pages under both sequences

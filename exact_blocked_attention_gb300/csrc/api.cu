@@ -110,7 +110,7 @@ Plan make_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t Tq, int64_t Tmax, int
   const char* force = std::getenv("BLKATTN_KERNEL");  // comparison runs only
   const bool force_mma = force && std::strcmp(force, "mma") == 0;
   const bool force_cudacore = force && std::strcmp(force, "cudacore") == 0;
-  if (prefill_ok && elt == Elt::BF16 && d == 128 && Tq >= 64 && (Tq + 255) / 256 <= 65535) {
+  if (prefill_ok && elt == Elt::BF16 && (d == 128 || paged) && Tq >= 64 && (Tq + 255) / 256 <= 65535) {
     // many query rows per head: two 128-row query tiles per CTA on tcgen05,
     // no splits
     pl.cfg.kernel = blkattn::Kernel::Prefill;
@@ -914,7 +914,7 @@ int fwd_paged_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages_, con
     if (prefill) {
       p.o_tma = o_tma ? 1 : 0;
       p.o_vec16 = out_vec16_ok(out) ? 1 : 0;
-      le = blkattn::launch_prefill_tc_paged(p, ps.cfg.row_groups, mq, mk, mv, mo, stream);
+      le = blkattn::launch_prefill_tc_paged(p, (int)c.d, ps.cfg.row_groups, mq, mk, mv, mo, stream);
     } else if (ps.cfg.kernel == blkattn::Kernel::DecodeTc) {
       le = blkattn::launch_decode_tc_paged(p, (int)c.d, (int)ps.ctas, mk, mv, stream);
     } else {

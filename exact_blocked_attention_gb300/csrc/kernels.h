@@ -125,9 +125,11 @@ size_t decode_mma_smem_bytes(int d, int mt);
 // boxes {32, 32}, 128-byte swizzle.
 cudaError_t launch_prefill_tc(const FwdParams& p, int n_pairs, const CUtensorMap& tmq, const CUtensorMap& tmk,
                               const CUtensorMap& tmv, const CUtensorMap& tmo, cudaStream_t stream);
-// The same over a paged cache (maps of K and V as for launch_decode_tc_paged).
-cudaError_t launch_prefill_tc_paged(const FwdParams& p, int n_pairs, const CUtensorMap& tmq, const CUtensorMap& tmk,
-                                    const CUtensorMap& tmv, const CUtensorMap& tmo, cudaStream_t stream);
+// The same over a paged cache, d = 64 or 128 (maps of K and V: boxes of 64
+// dims x min(rows of a page, 128) rows).
+cudaError_t launch_prefill_tc_paged(const FwdParams& p, int d, int n_pairs, const CUtensorMap& tmq,
+                                    const CUtensorMap& tmk, const CUtensorMap& tmv, const CUtensorMap& tmo,
+                                    cudaStream_t stream);
 int prefill_tc_smem_bytes();
 
 // Decode / verify on tcgen05 (bf16, d = 128, 16-byte aligned query rows, at

@@ -67,18 +67,23 @@ constexpr float kLazyRescale = 8.f;  // base-2 units: rescale only when max grow
 constexpr int BM = 128;  // query rows per query tile (TMEM lanes)
 constexpr int QT = 2;    // query tiles per CTA
 constexpr int BN = 128;  // keys per tile
-constexpr int D = 128;   // head dim
-constexpr int STAGES = 2;
 constexpr int kBox = 128 * 128;       // one 64-dim (128-byte) box of 128 rows: 16 KB
-constexpr int kTileBytes = 2 * kBox;  // one Q, K or V tile of 128 rows x 128 dims
-constexpr int kOffQ = 0;
-constexpr int kOffK = kOffQ + QT * kTileBytes;
-constexpr int kOffV = kOffK + STAGES * kTileBytes;
-constexpr int kOffBar = kOffV + STAGES * kTileBytes;
-// q_full, k_full[S], v_full[S], k_empty[S], v_empty[S], s_full[QT], p_full[QT], drain
-constexpr int kNumBars = 1 + 4 * STAGES + QT + QT + 1;
-constexpr int kOffMisc = kOffBar + kNumBars * 8;
-constexpr int kSmemBytes = kOffMisc + 64 + 1024;  // + slack to align to 1024
+// Head dims 128 and (over pages) 64: with 64 the tiles are half the size and
+// the ring has twice the stages.
+template <int D>
+struct Layout {
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kTileBytes = kBoxes * kBox;  // one Q, K or V tile of 128 rows
+  static constexpr int kStages = 2 * (2 / kBoxes);
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + QT * kTileBytes;
+  static constexpr int kOffV = kOffK + kStages * kTileBytes;
+  static constexpr int kOffBar = kOffV + kStages * kTileBytes;
+  // q_full, k_full[S], v_full[S], k_empty[S], v_empty[S], s_full[QT], p_full[QT], drain
+  static constexpr int kNumBars = 1 + 4 * kStages + QT + QT + 1;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kSmemBytes = kOffMisc + 64 + 1024;  // + slack to align to 1024
+};
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTileCols = 256;  // per query tile: S / P at [0, 128), U at [128, 256)
 constexpr uint32_t kColS = 0;
@@ -88,6 +93,7 @@ constexpr int kThreads = 320;
 constexpr int kTmaWarp = 8;
 constexpr int kMmaWarp = 9;
 constexpr uint32_t kIdescQK = tc::idesc_bf16(BM, BN, 0, 0);  // Q, K both K-major
+template <int D>
 constexpr uint32_t kIdescPV = tc::idesc_bf16(BM, D, 0, 1);   // P (TMEM), V MN-major
 
 __device__ __forceinline__ uint64_t policy_evict_last() {
@@ -110,11 +116,17 @@ __device__ __forceinline__ int spec_first_tile(int q0, int window) {
 // tensor memory (a mask in registers spilled 576 bytes).  The chain of a key
 // tile bounds it as over a contiguous cache: 2 x 2048 rows of 32 heads at 8192
 // keys 376 us (1280 TFLOP/s, 65 % of the bf16 burst rate), contiguous 384.
-template <bool WIN, bool PAGED>
+// At d = 64 the chain's products are half as long: 1.1 us a key tile for one
+// query tile, 1.36 for two (d = 128: 1.4 and 1.6); 1024 rows of 32 heads at
+// 2048 keys 32 us, 99 with the decode kernel.
+template <int D, bool WIN, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const FwdParams p, const __grid_constant__ CUtensorMap tmq,
                       const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                       const __grid_constant__ CUtensorMap tmo) {
+  using L = Layout<D>;
+  constexpr int STAGES = L::kStages, kTileBytes = L::kTileBytes, kBoxes = L::kBoxes;
+  constexpr int kOffQ = L::kOffQ, kOffK = L::kOffK, kOffV = L::kOffV, kOffBar = L::kOffBar, kOffMisc = L::kOffMisc;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBar);
@@ -187,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_arrive_expect_tx(q_full, QT * kTileBytes);
     for (int t = 0; t < QT; ++t) {
       tma_load_4d(sm + kOffQ + t * kTileBytes, &tmq, 0, q0 + t * BM, h, b, q_full, pol_q);
-      tma_load_4d(sm + kOffQ + t * kTileBytes + kBox, &tmq, 64, q0 + t * BM, h, b, q_full, pol_q);
+      if (kBoxes == 2) tma_load_4d(sm + kOffQ + t * kTileBytes + kBox, &tmq, 64, q0 + t * BM, h, b, q_full, pol_q);
     }
     if (!PAGED) {
     // K/V tile 0 of the CTA's range right away; with a window the range
@@ -315,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         __syncwarp();
-        if (half < 2)
+        if (half < kBoxes)
           tma_load_4d(sm + (kv ? kOffV : kOffK) + s * kTileBytes + dst_off,
                       kv ? static_cast<const void*>(&tmv) : static_cast<const void*>(&tmk), 64 * half, row, hk, page,
                       full, pol_kv);
@@ -413,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // B = V rows [16ks, 16ks+16) (keys, K) x 128 dims (N, two 64-dim boxes 16 KB apart)
             const uint64_t bdesc = tc::desc_join(vlo + (uint32_t)(ks * 16 * 128 >> 4), kHi);
             const uint32_t acol = tcol + kColS + part * kColPlo + 8 * ks;
-            tc::mma_ts(tcol + kColO, acol, bdesc, kIdescPV, (more || part > 0 || ks > 0) ? 1u : 0u);
+            tc::mma_ts(tcol + kColO, acol, bdesc, kIdescPV<D>, (more || part > 0 || ks > 0) ? 1u : 0u);
           }
         }
       };
@@ -565,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // U rows change reference (U += P_{j-1} V_{j-1} has completed: S_j
           // was issued after it)
 #pragma unroll 1
-          for (int q4 = 0; q4 < 4; ++q4) {
+          for (int q4 = 0; q4 < D / 32; ++q4) {
             uint32_t r[32];
             tc::ld32(tl + kColO + 32 * q4, r);
             tc::wait_ld();
@@ -642,10 +654,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int z0 = WIN && PAGED ? min(max(cta_end - key0, 0), BN) : cta_end - key0;
           const int z1 = WIN && PAGED ? min(max(cta_start - key0, 0), BN) : 0;
           const int nz = BN - z0 + z1;  // rows [z0, BN), then [0, z1)
-          for (int idx = (int)(threadIdx.x & 127); idx < nz * 16; idx += 128) {
-            int r = z0 + (idx >> 4);
+          for (int idx = (int)(threadIdx.x & 127); idx < nz * (D / 8); idx += 128) {
+            int r = z0 + idx / (D / 8);
             if (WIN && PAGED && r >= BN) r -= BN;
-            const int c = idx & 15;  // 16-byte chunk over the 128 dims (two boxes)
+            const int c = idx % (D / 8);  // 16-byte chunk over the dims (64 a box)
             *reinterpret_cast<uint4*>(vt + (c >> 3) * kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
                 make_uint4(0, 0, 0, 0);
           }
@@ -681,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int rows = min(32, p.Tq - r0);
           float* dst0 = static_cast<float*>(p.out) + (int64_t)b * p.o_sb + (int64_t)h * p.o_sh + (int64_t)r0 * p.o_si;
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
+          for (int half = 0; half < kBoxes; ++half) {
 #pragma unroll 1
             for (int q2 = 0; q2 < 2; ++q2) {
               uint32_t r[32];
@@ -713,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // once per CTA).
           unsigned char* stage = sm + (x == 0 ? kOffK : kOffV) + (warp & 3) * 4 * 4096;
 #pragma unroll 1
-          for (int q4 = 0; q4 < 4; ++q4) {
+          for (int q4 = 0; q4 < D / 32; ++q4) {
             uint32_t r[32];
             tc::ld32(tl + kColO + 32 * q4, r);
             tc::wait_ld();
@@ -730,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0 && row_w < p.Tq) {
             // rows past Tq are clipped by the map
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) tma_store_4d(&tmo, stage + q4 * 4096, 32 * q4, row_w, h, b);
+            for (int q4 = 0; q4 < D / 32; ++q4) tma_store_4d(&tmo, stage + q4 * 4096, 32 * q4, row_w, h, b);
             bulk_commit();
           }
         } else if (p.o_vec16) {
@@ -744,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __nv_bfloat16* dst0 =
               static_cast<__nv_bfloat16*>(p.out) + (int64_t)b * p.o_sb + (int64_t)h * p.o_sh + (int64_t)r0 * p.o_si;
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
+          for (int half = 0; half < kBoxes; ++half) {
 #pragma unroll 1
             for (int q2 = 0; q2 < 2; ++q2) {
               uint32_t r[32];
@@ -773,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the tensor-memory loads are warp-collective: every lane takes
           // part, rows past Tq store nothing
 #pragma unroll 1
-          for (int q4 = 0; q4 < 4; ++q4) {
+          for (int q4 = 0; q4 < D / 32; ++q4) {
             uint32_t r[32];
             tc::ld32(tl + kColO + 32 * q4, r);
             tc::wait_ld();
@@ -806,22 +818,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-int prefill_tc_smem_bytes() { return kSmemBytes; }
+int prefill_tc_smem_bytes() { return Layout<128>::kSmemBytes; }
 
 namespace {
 
-template <bool WIN, bool PAGED>
+template <int D, bool WIN, bool PAGED>
 cudaError_t launch_kernel(const FwdParams& p, unsigned blocks, const CUtensorMap& tmq, const CUtensorMap& tmk,
                           const CUtensorMap& tmv, const CUtensorMap& tmo, cudaStream_t stream) {
   static DeviceOnce once;
-  if (cudaError_t e = once.set_smem(reinterpret_cast<const void*>(&prefill_tc_kernel<WIN, PAGED>), kSmemBytes);
+  constexpr int kSmemBytes = Layout<D>::kSmemBytes;
+  if (cudaError_t e = once.set_smem(reinterpret_cast<const void*>(&prefill_tc_kernel<D, WIN, PAGED>), kSmemBytes);
       e != cudaSuccess)
     return e;
-  prefill_tc_kernel<WIN, PAGED><<<blocks, kThreads, kSmemBytes, stream>>>(p, tmq, tmk, tmv, tmo);
+  prefill_tc_kernel<D, WIN, PAGED><<<blocks, kThreads, kSmemBytes, stream>>>(p, tmq, tmk, tmv, tmo);
   return cudaGetLastError();
 }
 
-template <bool PAGED>
+template <int D, bool PAGED>
 cudaError_t launch_form(const FwdParams& p, int n_pairs, const CUtensorMap& tmq, const CUtensorMap& tmk,
                         const CUtensorMap& tmv, const CUtensorMap& tmo, cudaStream_t stream) {
   const int64_t heads = (int64_t)p.Hq * p.B;
@@ -829,20 +842,23 @@ cudaError_t launch_form(const FwdParams& p, int n_pairs, const CUtensorMap& tmq,
   const int64_t groups = (heads + p.head_group - 1) / p.head_group;
   const int64_t blocks = groups * p.head_group * n_pairs;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  if (p.window > 0) return launch_kernel<true, PAGED>(p, (unsigned)blocks, tmq, tmk, tmv, tmo, stream);
-  return launch_kernel<false, PAGED>(p, (unsigned)blocks, tmq, tmk, tmv, tmo, stream);
+  if (p.window > 0) return launch_kernel<D, true, PAGED>(p, (unsigned)blocks, tmq, tmk, tmv, tmo, stream);
+  return launch_kernel<D, false, PAGED>(p, (unsigned)blocks, tmq, tmk, tmv, tmo, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_prefill_tc(const FwdParams& p, int n_pairs, const CUtensorMap& tmq, const CUtensorMap& tmk,
                               const CUtensorMap& tmv, const CUtensorMap& tmo, cudaStream_t stream) {
-  return launch_form<false>(p, n_pairs, tmq, tmk, tmv, tmo, stream);
+  return launch_form<128, false>(p, n_pairs, tmq, tmk, tmv, tmo, stream);
 }
 
-cudaError_t launch_prefill_tc_paged(const FwdParams& p, int n_pairs, const CUtensorMap& tmq, const CUtensorMap& tmk,
-                                    const CUtensorMap& tmv, const CUtensorMap& tmo, cudaStream_t stream) {
-  return launch_form<true>(p, n_pairs, tmq, tmk, tmv, tmo, stream);
+cudaError_t launch_prefill_tc_paged(const FwdParams& p, int d, int n_pairs, const CUtensorMap& tmq,
+                                    const CUtensorMap& tmk, const CUtensorMap& tmv, const CUtensorMap& tmo,
+                                    cudaStream_t stream) {
+  if (d == 128) return launch_form<128, true>(p, n_pairs, tmq, tmk, tmv, tmo, stream);
+  if (d == 64) return launch_form<64, true>(p, n_pairs, tmq, tmk, tmv, tmo, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace blkattn

@@ -79,7 +79,7 @@ def reference(a):
     lse = torch.full((B, Hq, Tq), -math.inf, dtype=F64, device=q.device)
     ob, lb = torch.zeros_like(out), torch.zeros_like(lse)
     table, lens, pos = a["table"].cpu(), a["lens"].cpu(), a["pos"].cpu()
-    prompt = q.dtype == BF16 and d == 128 and Tq >= 64 and a["tree"] is None and a["scale"] > 0
+    prompt = q.dtype == BF16 and Tq >= 64 and a["tree"] is None and a["scale"] > 0
     for b in range(B):
         n = max(0, min(int(lens[b]), table.shape[1] * P))
         ent = table[b, : -(-n // P)].long()
@@ -160,9 +160,10 @@ PROMPT = [(1, 2, 1, 64, 16, [64]), (2, 4, 2, 130, 8, [130, 700]), (1, 4, 1, 300,
 
 @pytest.mark.parametrize("rows_major", [False, True])
 @pytest.mark.parametrize("out_dtype", [F32, BF16])
+@pytest.mark.parametrize("d", [128, 64])
 @pytest.mark.parametrize("B,Hq,Hkv,Tq,P,lens", PROMPT)
-def test_prompt_chunks(B, Hq, Hkv, Tq, P, lens, out_dtype, rows_major):
-    a = make(B, Hq, Hkv, Tq, 128, P, lens, BF16, rows_major, seed=Tq)
+def test_prompt_chunks(B, Hq, Hkv, Tq, P, lens, d, out_dtype, rows_major):
+    a = make(B, Hq, Hkv, Tq, d, P, lens, BF16, rows_major, seed=Tq)
     check(a, *call(a, out_dtype))
 
 
@@ -178,7 +179,8 @@ def test_few_rows_over_long_contexts(Hq, Hkv, Tq, d, K, window):
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("Tq,d,window", [(1, 128, 1), (1, 64, 100), (5, 128, 128), (3, 64, 1000), (65, 128, 1),
-                                         (300, 128, 200), (129, 128, 5000), (100, 64, 37)])
+                                         (300, 128, 200), (129, 128, 5000), (100, 64, 37),
+                                         (300, 64, 200), (260, 64, 1)])
 def test_window(Tq, d, window, dtype):
     # rows before every window were given back: their pages hold NaN and their entries -1
     lens = [1500, max(Tq, 129), max(Tq, 4)]
@@ -217,7 +219,8 @@ def test_tree(Tq, lens, dtype, d):
 
 
 @pytest.mark.parametrize("dtype,Tq,d,P", [(BF16, 1, 128, 16), (BF16, 4, 64, 8), (BF16, 100, 128, 32), (F32, 2, 128, 64),
-                                          (BF16, 3, 128, 128), (BF16, 200, 128, 256), (F32, 1, 64, 16)])
+                                          (BF16, 3, 128, 128), (BF16, 200, 128, 256), (F32, 1, 64, 16),
+                                          (BF16, 150, 64, 16)])
 def test_entries_without_a_page(dtype, Tq, d, P):
     lens = [1300, 700, 3 * P + 1]
     a = make(3, 4, 2, Tq, d, P, lens, dtype, seed=9)
@@ -349,15 +352,18 @@ def test_strides_of_single_dims_do_not_matter(Tq, d, dtype):
 
 
 @pytest.mark.parametrize("out_dtype", [F32, BF16])
-def test_prompt_output_layouts(out_dtype):
-    a = make(1, 4, 2, 150, 128, 32, [400], seed=19)
+@pytest.mark.parametrize("d,window", [(128, 0), (64, 0), (128, 90), (64, 90)])
+def test_prompt_output_layouts(out_dtype, d, window):
+    a = make(1, 4, 2, 150, d, 32, [400], seed=19)
+    a["window"] = window
     want, want_lse = call(a, out_dtype)
     check(a, want, want_lse)
-    for buf, view in ((torch.full((1, 150, 4, 128), 7.0, dtype=out_dtype, device=dev()), lambda t: t.transpose(1, 2)),
-                      (torch.full((1, 4, 150, 131), 7.0, dtype=out_dtype, device=dev()), lambda t: t[..., 1:129]),
-                      (torch.full((1, 4, 150, 136), 7.0, dtype=out_dtype, device=dev()), lambda t: t[..., 8:])):
+    for buf, view in ((torch.full((1, 150, 4, d), 7.0, dtype=out_dtype, device=dev()), lambda t: t.transpose(1, 2)),
+                      (torch.full((1, 4, 150, d + 3), 7.0, dtype=out_dtype, device=dev()), lambda t: t[..., 1:d + 1]),
+                      (torch.full((1, 4, 150, d + 8), 7.0, dtype=out_dtype, device=dev()), lambda t: t[..., 8:])):
         out, lse = view(buf), torch.empty_like(want_lse)
-        blkattn.fwd_paged(a["q"], a["kp"], a["vp"], a["table"], a["lens"], a["pos"], a["scale"], out, lse)
+        blkattn.fwd_paged(a["q"], a["kp"], a["vp"], a["table"], a["lens"], a["pos"], a["scale"], out, lse,
+                          window=window)
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
 
 

@@ -86,6 +86,7 @@ struct Plan {
   int64_t ctas;
   int64_t ws_bytes;
   int64_t units = 0;  // tcgen05 decode kernel: per-unit counters needed
+  int64_t split_from = 0;  // prompt kernel over pages: the first item in parts
 };
 
 int resident_ctas_per_sm(size_t smem_bytes) {
@@ -771,23 +772,65 @@ int fwd_impl(const blkattn_tensor* q, const blkattn_tensor* k, const blkattn_ten
   return launch_fwd(p, c, pl, q, k, v, out, stream);
 }
 
-// Whether T_q >= 64 query rows over pages go to the prompt kernel (a CTA for
-// 256 rows of a head, all its keys in turn) or to the decode kernel (48 rows a
-// unit, the key tiles of all units shared by every SM).  Fitted to both
-// kernels over T_q 64..1024, 512..8192 keys and 1..64 heads: the prompt kernel
-// takes 10 us and 1.4 us (one row tile) or 1.6 us (two) a key tile and wave,
-// the decode kernel 22 us and 1.15 us a unit's tile.  Examples: 64 rows x 32
-// heads at 8192 keys 99 and 43 us, 512 rows 114 and 184 us, 512 rows x 4 heads
-// 109 and 45 us.  The keys are the table's, as everywhere in a plan.
-bool prompt_kernel_pays(const Checked& c, int sms) {
+// The prompt kernel over pages: items of 256 rows of a head, a CTA each.  The
+// items past the last full wave of CTAs would leave SMs idle for all their key
+// tiles; they are split into parts along their keys, whose states a second
+// kernel joins, where that is faster.  The model is fitted to measurements
+// (T_q 64..4096, 512..30000 keys, 1..64 heads, both head dims, parts 1..16):
+// 10 us and 1.63 us a key tile and wave (one row tile 1.38; d = 64 1.37 and
+// 1.12), joining 3 us and 0.055 us a part (d = 64 0.04; its state goes through
+// memory).  Its choice was within 4 % of the best count of parts for each of 56
+// shapes.  Examples at 8192 keys: 256 rows x 32 heads 111 us whole, 44 in 4
+// parts; 512 rows 116 and 74 (2 parts); 128 rows of one head 98 and 19 (16
+// parts); 1024 rows x 40 heads (8 items past a wave) 207 and 140.  The keys
+// are the table's, as everywhere in a plan.
+struct PromptPlan {
+  int64_t items, split_from;  // items from split_from on are split
+  int parts;
+  double us;  // estimated time
+};
+PromptPlan plan_prompt(const Checked& c, int sms) {
+  const int64_t keys = c.window > 0 && c.window + 256 < c.Tmax ? c.window + 256 : c.Tmax;
+  const int64_t tiles = (keys + 127) / 128;  // key tiles of the longest item
+  // and of the mean one, if the rows are the last T_q positions
+  const double mean = c.window > 0 || c.Tq > keys ? (double)tiles : (double)tiles - (double)c.Tq / 256.0 + 0.5;
+  const double tile = c.d == 128 ? (c.Tq > 128 ? 1.63 : 1.38) : (c.Tq > 128 ? 1.37 : 1.12);
+  const int64_t P = sms > 0 ? sms : 148;
+  PromptPlan pp;
+  pp.items = (c.Tq + 255) / 256 * c.Hq * c.B;
+  pp.split_from = pp.items;
+  pp.parts = 1;
+  const int64_t rest = pp.items % P, waves = pp.items / P;
+  pp.us = 10.0 + tile * (waves == 0 ? (double)tiles : (double)(waves + (rest > 0)) * mean);
+  double best = 0.95 * pp.us;
+  // at least 4 tiles a part, at most two waves of parts
+  for (int s = 2; rest > 0 && s <= 16 && 4 * s <= tiles && rest * s <= 2 * P; ++s) {
+    double len = (double)waves * mean + (double)((rest * s + P - 1) / P) * (double)((tiles + s - 1) / s);
+    // (several waves of items of different lengths even out by themselves)
+    const double even = waves == 0 ? 0.0 : mean * ((double)pp.items / (double)P + 1.0 / s);
+    if (even > len) len = even;
+    const double us = 10.0 + tile * len + 3.0 + (c.d == 128 ? 0.055 : 0.04) * (double)(rest * s);
+    if (us < best) {
+      best = pp.us = us;
+      pp.parts = s;
+      pp.split_from = pp.items - rest;
+    }
+  }
+  return pp;
+}
+
+// Whether T_q >= 64 query rows over pages go to the prompt kernel or to the
+// decode kernel (48 rows a unit, the key tiles of all units shared by every
+// SM: 22 us and 1.15 us a unit's tile and SM).  With its parts the prompt
+// kernel mostly wins: 64 rows x 32 heads at 8192 keys 37 and 43 us, at 2048
+// keys 20 and 26.
+bool prompt_kernel_pays(const Checked& c, const PromptPlan& pp, int sms) {
   const int64_t keys = c.window > 0 && c.window + c.Tq < c.Tmax ? c.window + c.Tq : c.Tmax;
   const double tiles = (double)((keys + 127) / 128);
   const int64_t P = sms > 0 ? sms : 148;
-  const int64_t ctas = (c.Tq + 255) / 256 * c.Hq * c.B;
   const int64_t rows = c.Hq / c.Hkv * c.Tq;
-  const double prompt = 10.0 + (c.Tq > 128 ? 1.6 : 1.4) * tiles * (double)((ctas + P - 1) / P);
   const double decode = 22.0 + 1.15 * tiles * (double)(c.B * c.Hkv * ((rows + 47) / 48)) / (double)P;
-  return prompt <= decode;
+  return pp.us <= decode;
 }
 
 // blkattn_fwd_paged: the pools take the places of k and v, their strides those
@@ -836,7 +879,8 @@ int fwd_paged_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages_, con
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState* ds = nullptr;
   if ((st = device_state(&ds)) != BLKATTN_OK) return st;
-  const bool prefill_ok = c.prefill_ok && scale > 0.f && prompt_kernel_pays(c, ds->sms);
+  const PromptPlan pp = plan_prompt(c, ds->sms);
+  const bool prefill_ok = c.prefill_ok && scale > 0.f && prompt_kernel_pays(c, pp, ds->sms);
   auto plan_of = [&](int64_t B) {
     return make_plan(B, c.Hq, c.Hkv, c.Tq, c.Tmax, (int)c.d, c.elt, ds->sms, prefill_ok, c.q_vec_ok, window > 0, true);
   };
@@ -864,6 +908,13 @@ int fwd_paged_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages_, con
     }
   } else if (pl.cfg.kernel == blkattn::Kernel::CudaCore && pl.cfg.row_groups > 65535) {
     return BLKATTN_ERR_UNSUPPORTED;
+  }
+  // (every part leaves 256 rows of m, l and u)
+  const int64_t part_rows = (pp.items - pp.split_from) * pp.parts * 256;
+  if (pl.cfg.kernel == blkattn::Kernel::Prefill) {
+    pl.split_from = pp.split_from;
+    pl.cfg.n_splits = pp.parts;
+    if (pp.parts > 1) pl.ws_bytes = part_rows * (2 + c.d) * 4;
   }
   // (the last slice has a plan of its own; scratch for both, before any launch)
   const int64_t rest = c.B % nb;
@@ -914,6 +965,10 @@ int fwd_paged_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages_, con
     if (prefill) {
       p.o_tma = o_tma ? 1 : 0;
       p.o_vec16 = out_vec16_ok(out) ? 1 : 0;
+      p.split_from = (int)ps.split_from;
+      p.ws_m = static_cast<float*>(ds->ws);
+      p.ws_l = p.ws_m + part_rows;
+      p.ws_u = p.ws_l + part_rows;
       le = blkattn::launch_prefill_tc_paged(p, (int)c.d, ps.cfg.row_groups, mq, mk, mv, mo, stream);
     } else if (ps.cfg.kernel == blkattn::Kernel::DecodeTc) {
       le = blkattn::launch_decode_tc_paged(p, (int)c.d, (int)ps.ctas, mk, mv, stream);

@@ -60,6 +60,10 @@ struct FwdParams {
   float* ws_u;
   int* err;  // device error word
   int head_group;  // prefill: (sequence, head) pairs dispatched together (L2 reuse of K/V)
+  // prefill over pages: the items (256 rows of a head, in dispatch order) from
+  // this one on are split into n_splits parts along their keys; row r of part
+  // s of item i leaves its state at index ((i - split_from) n_splits + s) 256 + r
+  int split_from;
   // tcgen05 decode kernel: query rows per unit (one row group of one KV head);
   // the partial state of unit row r from CTA c sits in slot c + unit, at
   // index slot * rows_cta + r; unit_cnt counts the CTAs of each unit that

@@ -109,6 +109,23 @@ __device__ __forceinline__ int spec_first_tile(int q0, int window) {
   return s0 > 0 ? (int)(s0 / BN) : 0;
 }
 
+// Query-tile pair and (sequence, head) of item r of the dispatch order: groups
+// of head_group (sequence, head) pairs whose K/V fit in L2 together; within a
+// group every head's longest (latest) query-tile pair goes before any shorter
+// one.  The next group's long pairs start while the previous group's short
+// ones finish.  (Over pages the last group is as small as it is; over a
+// contiguous cache it is padded.)
+template <bool PAGED>
+__device__ __forceinline__ void item_of(const FwdParams& p, int r, int n_pairs, int& pair, int& bh) {
+  const int hg = p.head_group;
+  const int per_group = n_pairs * hg;
+  const int group = r / per_group;
+  const int r_in = r % per_group;
+  const int heads = PAGED ? min(hg, p.Hq * p.B - group * hg) : hg;
+  pair = n_pairs - 1 - r_in / heads;
+  bh = group * hg + r_in % heads;
+}
+
 // PAGED: the cache lies in pages (paged.h).  A key tile is one box of a page of
 // at least 128 rows or the boxes of 128 / P pages: the producer warp's lanes
 // look their pages up a tile ahead and issue the copies; a page number outside
@@ -142,18 +159,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (sliding window) [6 + 2x] smallest and [7 + 2x] largest first visible key of x's rows
   int* misc = reinterpret_cast<int*>(sm + kOffMisc);
 
-  // Linear grid in dispatch order: groups of p.head_group (sequence, head)
-  // pairs whose K/V fit in L2 together; within a group every head's longest
-  // (latest) query-tile pair goes before any shorter one.  The next group's
-  // long pairs start while the previous group's short ones finish.
+  // Linear grid in dispatch order; over pages the items from split_from on
+  // have `parts` CTAs each
   const int n_pairs = (p.Tq + 2 * BM - 1) / (2 * BM);
-  const int hg = p.head_group;
-  const int per_group = n_pairs * hg;
-  const int group = blockIdx.x / per_group;
-  const int r_in = blockIdx.x % per_group;
-  const int pair = n_pairs - 1 - r_in / hg;
-  const int bh = group * hg + r_in % hg;
-  if (bh >= p.Hq * p.B) return;  // padding of the last group
+  int item = blockIdx.x, part = 0, parts = 1;
+  if (PAGED && item >= p.split_from) {
+    const int e = item - p.split_from;
+    parts = p.n_splits;
+    item = p.split_from + e / parts;
+    part = e % parts;
+  }
+  // (the joining kernel's blocks may take their places as soon as every CTA
+  // runs; they wait for this kernel's end)
+  if (PAGED && p.n_splits > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int pair, bh;
+  item_of<PAGED>(p, item, n_pairs, pair, bh);
+  if (!PAGED && bh >= p.Hq * p.B) return;  // padding of the last group
   const int h = bh % p.Hq;
   const int b = bh / p.Hq;
   const int hk = h / p.G;
@@ -255,9 +276,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (f_t0 >= e_t0) f_t0 = e_t0 = 0;  // no row of the tile sees a key
     if (f_t1 >= e_t1) f_t1 = e_t1 = 0;
   }
+  if (PAGED && parts > 1) {
+    // this CTA's share of the key tiles
+    const int lo0 = !WIN ? 0 : (e_t0 == f_t0 ? f_t1 : (e_t1 == f_t1 ? f_t0 : min(f_t0, f_t1)));
+    const int n = max(e_t0, e_t1) - lo0;
+    const int lo = lo0 + n * part / parts, hi = lo0 + n * (part + 1) / parts;
+    f_t0 = max(f_t0, lo);
+    f_t1 = max(f_t1, lo);
+    e_t0 = min(e_t0, hi);
+    e_t1 = min(e_t1, hi);
+    if (f_t0 >= e_t0) f_t0 = e_t0 = 0;
+    if (f_t1 >= e_t1) f_t1 = e_t1 = 0;
+  }
   const int n_t0 = e_t0 - f_t0;  // key tiles per query tile
   const int n_t1 = e_t1 - f_t1;
-  const int j_lo = !WIN ? 0 : (n_t0 == 0 ? f_t1 : (n_t1 == 0 ? f_t0 : min(f_t0, f_t1)));
+  const int j_lo = !WIN && !PAGED ? 0 : (n_t0 == 0 ? f_t1 : (n_t1 == 0 ? f_t0 : min(f_t0, f_t1)));
   const int j_hi = max(e_t0, e_t1);
   const int n_max = j_hi - j_lo;  // key tiles the CTA loads
   // ring position of the CTA's key tile j: j + ro (ro = 1 when the copy made
@@ -269,7 +302,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t out_row = (int64_t)b * p.o_sb + (int64_t)h * p.o_sh + (int64_t)row_i * p.o_si;
   const int64_t lse_idx = (int64_t)b * p.l_sb + (int64_t)h * p.l_sh + (int64_t)row_i * p.l_si;
 
+  // partial states of a split item: row of the slot in ws_m, ws_l, ws_u
+  const int64_t ws_row = PAGED ? ((int64_t)(item - p.split_from) * parts + part) * (QT * BM) : 0;
+
   auto write_empty_row = [&]() {  // the defined output of a row with no visible key
+    if (PAGED && parts > 1) {
+      p.ws_m[ws_row + threadIdx.x] = kNegInf;
+      return;
+    }
     for (int d = 0; d < D; ++d) {
       if (p.out_bf16)
         static_cast<__nv_bfloat16*>(p.out)[out_row + (int64_t)d * p.o_sd] = __float2bfloat16_rn(0.f);
@@ -678,8 +718,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         tc::fence_after();
-        const float inv = (m_ref == kNegInf) ? 0.f : 1.f / l;
-        if (p.o_tma && !WIN) {
+        const float inv = PAGED && parts > 1 ? 1.f : ((m_ref == kNegInf) ? 0.f : 1.f / l);
+        if ((p.o_tma && !WIN) || (PAGED && parts > 1)) {
+          // (fp32 rows of the output, or of a split item's partial U)
           // Every MMA has completed (drain), so the K (query tile 0) or V
           // (query tile 1) ring is free.  Each warp stages its 32 rows, 64
           // dims at a time (rows padded to 68 floats: conflict-free both
@@ -691,7 +732,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           float* stg = reinterpret_cast<float*>(sm + (x == 0 ? kOffK : kOffV) + (warp & 3) * 32 * kRow * 4);
           const int r0 = (2 * pair + x) * BM + 32 * (warp & 3);
           const int rows = min(32, p.Tq - r0);
-          float* dst0 = static_cast<float*>(p.out) + (int64_t)b * p.o_sb + (int64_t)h * p.o_sh + (int64_t)r0 * p.o_si;
+          const int64_t dst_si = PAGED && parts > 1 ? D : p.o_si;
+          float* dst0 = PAGED && parts > 1
+                            ? p.ws_u + (ws_row + x * BM + 32 * (warp & 3)) * D
+                            : static_cast<float*>(p.out) + (int64_t)b * p.o_sb + (int64_t)h * p.o_sh + (int64_t)r0 * p.o_si;
 #pragma unroll 1
           for (int half = 0; half < kBoxes; ++half) {
 #pragma unroll 1
@@ -710,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int it = 0; it < 16; ++it) {
               const int rr = 2 * it + (lane >> 4);
               if (rr < rows)
-                *reinterpret_cast<float4*>(dst0 + rr * p.o_si + 64 * half + 4 * (lane & 15)) =
+                *reinterpret_cast<float4*>(dst0 + rr * dst_si + 64 * half + 4 * (lane & 15)) =
                     *reinterpret_cast<const float4*>(stg + rr * kRow + 4 * (lane & 15));
             }
             __syncwarp();
@@ -802,7 +846,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (my_row) p.lse[lse_idx] = (m_ref == kNegInf) ? kNegInf : (m_ref + __log2f(l)) * kLn2;
+        if (PAGED && parts > 1) {
+          if (my_row) {
+            p.ws_m[ws_row + threadIdx.x] = m_ref;
+            p.ws_l[ws_row + threadIdx.x] = l;
+          }
+        } else if (my_row) {
+          p.lse[lse_idx] = (m_ref == kNegInf) ? kNegInf : (m_ref + __log2f(l)) * kLn2;
+        }
         // the staging buffer is released with the CTA: the stores must have
         // read it (no-op for a lane without stores)
         if (WIN && p.o_tma && lane == 0) bulk_wait_read();
@@ -814,6 +865,90 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after();
   if (warp == kMmaWarp) tc::dealloc(tb, kTmemCols);
+}
+
+// Joins the parts of the split items (eqs. 33.4-33.5), a warp a row; the parts
+// in their order, so the result does not depend on which finished first.
+constexpr int kJoinWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) prompt_join_kernel(const FwdParams p) {
+  // launched as a programmatic dependent of the prompt kernel
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int DPL = D / 32;  // dims a lane
+  const int lane = threadIdx.x & 31;
+  const int idx = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);  // of the split items' rows
+  const int n_pairs = (p.Tq + 2 * BM - 1) / (2 * BM);
+  const int e = idx / (QT * BM), r = idx % (QT * BM);
+  int pair, bh;
+  item_of<true>(p, p.split_from + e, n_pairs, pair, bh);
+  const int i = pair * (QT * BM) + r;
+  if (i >= p.Tq) return;
+  const int parts = p.n_splits;  // <= 32
+  const int64_t row0 = (int64_t)e * parts * (QT * BM) + r;
+  const float m = lane < parts ? p.ws_m[row0 + lane * (QT * BM)] : kNegInf;
+  const float lp = lane < parts ? p.ws_l[row0 + lane * (QT * BM)] : 0.f;
+  float M = m;
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  // a part without a visible key of this row wrote no l and no U: whatever
+  // lies there is dropped by select
+  const float w = m == kNegInf ? 0.f : fast_exp2(m - M);
+  float l = m == kNegInf ? 0.f : w * lp;
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+  float u[DPL];
+#pragma unroll
+  for (int c = 0; c < DPL; ++c) u[c] = 0.f;
+  constexpr int kBatch = 4;  // parts whose loads are in flight together
+  for (int s0 = 0; s0 < parts; s0 += kBatch) {
+    float v[kBatch][DPL];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float* us = p.ws_u + (row0 + min(s0 + k, parts - 1) * (QT * BM)) * D + lane * DPL;
+      if constexpr (DPL == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(us);
+        v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(us);
+        v[k][0] = x.x; v[k][1] = x.y;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float ws = __shfl_sync(0xffffffffu, w, min(s0 + k, 31));  // (0 past the last part)
+#pragma unroll
+      for (int c = 0; c < DPL; ++c) u[c] = ws == 0.f ? u[c] : fmaf(ws, v[k][c], u[c]);
+    }
+  }
+  const float inv = M == kNegInf ? 0.f : 1.f / l;
+  const int b = bh / p.Hq, h = bh % p.Hq;
+  const int64_t o = (int64_t)b * p.o_sb + (int64_t)h * p.o_sh + (int64_t)i * p.o_si;
+  const int d0 = lane * DPL;
+  if (p.o_tma) {  // aligned fp32 rows
+    float* dst = static_cast<float*>(p.out) + o + d0;
+    if constexpr (DPL == 4)
+      *reinterpret_cast<float4*>(dst) = make_float4(u[0] * inv, u[1] * inv, u[2] * inv, u[3] * inv);
+    else
+      *reinterpret_cast<float2*>(dst) = make_float2(u[0] * inv, u[1] * inv);
+  } else if (p.o_vec16) {  // aligned bf16 rows
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + o + d0);
+    if constexpr (DPL == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(u[0] * inv, u[1] * inv), pack_bf16(u[2] * inv, u[3] * inv));
+    else
+      *dst = pack_bf16(u[0] * inv, u[1] * inv);
+  } else {
+#pragma unroll
+    for (int c = 0; c < DPL; ++c) {
+      const int64_t oi = o + (int64_t)(d0 + c) * p.o_sd;
+      if (p.out_bf16)
+        static_cast<__nv_bfloat16*>(p.out)[oi] = __float2bfloat16_rn(u[c] * inv);
+      else
+        static_cast<float*>(p.out)[oi] = u[c] * inv;
+    }
+  }
+  if (lane == 0)
+    p.lse[(int64_t)b * p.l_sb + (int64_t)h * p.l_sh + (int64_t)i * p.l_si] =
+        M == kNegInf ? kNegInf : (M + __log2f(l)) * kLn2;
 }
 
 }  // namespace
@@ -840,7 +975,8 @@ cudaError_t launch_form(const FwdParams& p, int n_pairs, const CUtensorMap& tmq,
   const int64_t heads = (int64_t)p.Hq * p.B;
   if (p.head_group < 1) return cudaErrorInvalidValue;
   const int64_t groups = (heads + p.head_group - 1) / p.head_group;
-  const int64_t blocks = groups * p.head_group * n_pairs;
+  int64_t blocks = groups * p.head_group * n_pairs;
+  if (PAGED) blocks = p.split_from + (heads * n_pairs - p.split_from) * p.n_splits;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   if (p.window > 0) return launch_kernel<D, true, PAGED>(p, (unsigned)blocks, tmq, tmk, tmv, tmo, stream);
   return launch_kernel<D, false, PAGED>(p, (unsigned)blocks, tmq, tmk, tmv, tmo, stream);
@@ -856,9 +992,23 @@ cudaError_t launch_prefill_tc(const FwdParams& p, int n_pairs, const CUtensorMap
 cudaError_t launch_prefill_tc_paged(const FwdParams& p, int d, int n_pairs, const CUtensorMap& tmq,
                                     const CUtensorMap& tmk, const CUtensorMap& tmv, const CUtensorMap& tmo,
                                     cudaStream_t stream) {
-  if (d == 128) return launch_form<128, true>(p, n_pairs, tmq, tmk, tmv, tmo, stream);
-  if (d == 64) return launch_form<64, true>(p, n_pairs, tmq, tmk, tmv, tmo, stream);
-  return cudaErrorInvalidValue;
+  if (d != 128 && d != 64) return cudaErrorInvalidValue;
+  if (cudaError_t e = d == 128 ? launch_form<128, true>(p, n_pairs, tmq, tmk, tmv, tmo, stream)
+                               : launch_form<64, true>(p, n_pairs, tmq, tmk, tmv, tmo, stream);
+      e != cudaSuccess || p.n_splits == 1)
+    return e;
+  const int64_t rows = ((int64_t)p.Hq * p.B * n_pairs - p.split_from) * (QT * BM);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows / kJoinWarps));
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return d == 128 ? cudaLaunchKernelEx(&cfg, prompt_join_kernel<128>, p)
+                  : cudaLaunchKernelEx(&cfg, prompt_join_kernel<64>, p);
 }
 
 }  // namespace blkattn

@@ -432,12 +432,13 @@ int blkattn_paged_append(const blkattn_tensor* k, const blkattn_tensor* v, const
  * not followed.  The K and V rows between the earliest and the latest key
  * that query rows of one sequence see must be finite, except tree nodes that
  * no row lists; every other row of the pools may hold anything.
- * Kernels: bf16 prompts (T_q >= 64, no tree, scale > 0; where the
- * decode kernel would not be faster) and bf16 decode and verify rows (d = 64
- * or 128) run on tcgen05 when the query rows are contiguous and 16-byte
- * aligned; the rest (f32, other query layouts, more
- * than 49152 query rows to a KV head) on the CUDA cores.  Results do not
- * depend on P or on the order of the pages.  Workspace, growth and overlap of
+ * Kernels: bf16 prompts (T_q >= 64, no tree, scale > 0; where the decode
+ * kernel would not be faster) and bf16 decode and verify rows (d = 64 or 128)
+ * run on tcgen05 when the query rows are contiguous and 16-byte aligned; the
+ * rest (f32, other query layouts, more than 49152 query rows to a KV head) on
+ * the CUDA cores.  Results do not depend on the order of the pages, nor on P
+ * for the same T_max; T_max and the batch decide where the keys are cut into
+ * parts, which moves the last bits.  Workspace, growth and overlap of
  * calls as for blkattn_fwd.  Returns as blkattn_fwd; BLKATTN_ERR_UNSUPPORTED
  * also for P outside the rule above.
  */

@@ -177,6 +177,89 @@ def test_few_rows_over_long_contexts(Hq, Hkv, Tq, d, K, window):
     check(a, *call(a, BF16))
 
 
+# prompts whose last items are cut into parts along their keys: fewer items than
+# SMs, sequences much shorter than the table (parts without a key), one wave of
+# items and a rest
+PARTS = [(1, 4, 1, 100, 16, [3000]), (3, 4, 2, 300, 32, [2500, 310, 1300]), (1, 3, 3, 700, 256, [4001]),
+         (2, 1, 1, 64, 8, [64, 9000]), (4, 40, 8, 64, 32, [4096, 100, 4000, 2049])]
+
+
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+@pytest.mark.parametrize("B,Hq,Hkv,Tq,P,lens", PARTS)
+def test_prompts_in_parts(B, Hq, Hkv, Tq, P, lens, d, out_dtype):
+    a = make(B, Hq, Hkv, Tq, d, P, lens, seed=Tq + d)
+    check(a, *call(a, out_dtype))
+
+
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("window", [0, 1, 100, 2600, 1 << 20])
+def test_prompts_in_parts_with_windows_and_edges(window, d):
+    lens = [4100, 300, 2900]
+    a = make(3, 2, 1, 270, d, 16, lens, seed=71)
+    a["window"] = window
+    for b, n in enumerate(lens):  # pages behind every window hold nothing
+        gone = max(0, n - 270 - window + 1) // 16 if window else 0
+        a["kp"][a["table"][b, :gone].long()] = math.nan
+        a["vp"][a["table"][b, :gone].long()] = math.nan
+        a["table"][b, :gone] = -1
+    a["pos"][0, :100] = torch.arange(3000, 3100, dtype=torch.int32, device=dev())  # not in order of the keys
+    if window:
+        a["pos"][0, :100] = a["pos"][0, 100:200]
+    a["pos"][1, 200:] = -1                     # padding rows
+    a["pos"][2, :128] = -7                     # a whole row tile without keys
+    a["pos"][2, 128:] += 10                    # and rows past the end
+    check(a, *call(a, BF16))
+
+
+@pytest.mark.parametrize("d", [128, 64])
+def test_prompts_in_parts_without_some_pages(d):
+    a = make(2, 3, 1, 140, d, 32, [3500, 2000], seed=73)
+    a["table"][0, 3] = -1
+    a["table"][0, 40:70] = 1 << 30             # whole parts
+    a["table"][1, 62] = -5                     # the last keys
+    check(a, *call(a, F32))
+
+
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+@pytest.mark.parametrize("d,window", [(128, 0), (64, 0), (128, 3000), (64, 3000)])
+def test_prompts_in_parts_output_layouts(out_dtype, d, window):
+    a = make(1, 4, 2, 150, d, 32, [5000], seed=79)
+    a["window"] = window
+    want, want_lse = call(a, out_dtype)
+    check(a, want, want_lse)
+    for buf, view in ((torch.full((1, 150, 4, d), 7.0, dtype=out_dtype, device=dev()), lambda t: t.transpose(1, 2)),
+                      (torch.full((1, 4, 150, d + 3), 7.0, dtype=out_dtype, device=dev()), lambda t: t[..., 1:d + 1]),
+                      (torch.full((1, 4, d, 150), 7.0, dtype=out_dtype, device=dev()), lambda t: t.transpose(2, 3))):
+        out, lse = view(buf), torch.empty((1, 4, 150, 2), device=dev())[..., 1]
+        blkattn.fwd_paged(a["q"], a["kp"], a["vp"], a["table"], a["lens"], a["pos"], a["scale"], out, lse,
+                          window=window)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+        if buf.shape[-1] == d + 3:
+            assert bool((buf[..., 0] == 7).all()) and bool((buf[..., d + 1:] == 7).all())
+
+
+def test_prompts_in_parts_in_a_graph():
+    a = make(2, 4, 2, 200, 128, 16, [4000, 3000], seed=83)
+    out, lse = torch.empty_like(a["q"]), torch.empty(a["q"].shape[:3], device=dev())
+
+    def run():
+        blkattn.fwd_paged(a["q"], a["kp"], a["vp"], a["table"], a["lens"], a["pos"], a["scale"], out, lse)
+
+    run()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+        run()  # (the second joins after the first: one workspace)
+    for shift in (0, 900, 3900):
+        out.fill_(9.0)
+        lse.fill_(9.0)
+        g.replay()
+        check(a, out, lse)
+        a["lens"] -= 900
+        a["pos"] -= 900
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("Tq,d,window", [(1, 128, 1), (1, 64, 100), (5, 128, 128), (3, 64, 1000), (65, 128, 1),
                                          (300, 128, 200), (129, 128, 5000), (100, 64, 37),
@@ -404,6 +487,7 @@ def test_pool_offsets_past_32_bits(Tq):
     ids = [N - 1, 3, N - 2]
     for i, pg in enumerate(ids):
         kp[pg], vp[pg] = small["kp"][int(small["table"][0, i])], small["vp"][int(small["table"][0, i])]
+    ids += [-1] * (small["table"].shape[1] - len(ids))  # (the same T_max: the keys are cut alike)
     a = dict(small, kp=kp, vp=vp, table=torch.tensor([ids], dtype=torch.int32, device=dev()))
     out, lse = call(a)
     want, want_lse = call(small)

@@ -151,7 +151,7 @@ Plan make_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t Tq, int64_t Tmax, int
       pl.tile = 128;
       pl.ctas = P;
       auto al = [](int64_t x) { return (x + 255) / 256 * 256; };
-      pl.ws_bytes = 2 * al(slots * R * 4) + al(slots * R * d * 4);
+      pl.ws_bytes = 2 * al(slots * R * 4) + al(slots * R * d * 4) + (paged ? al(U * 8) : 0);
       pl.units = U;  // per-unit arrival counters
       return pl;
     }
@@ -971,6 +971,10 @@ int fwd_paged_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages_, con
       p.ws_u = p.ws_l + part_rows;
       le = blkattn::launch_prefill_tc_paged(p, (int)c.d, ps.cfg.row_groups, mq, mk, mv, mo, stream);
     } else if (ps.cfg.kernel == blkattn::Kernel::DecodeTc) {
+      // few units of many parts: at least six each, if the lengths are the table's
+      const int64_t keys = window > 0 && window + c.Tq < c.Tmax ? window + c.Tq : c.Tmax;
+      p.join = 6 * ps.units <= ps.ctas && keys > 5 * 128;
+      p.ws_unit = reinterpret_cast<int2*>(static_cast<char*>(ds->ws) + ps.ws_bytes - (ps.units * 8 + 255) / 256 * 256);
       le = blkattn::launch_decode_tc_paged(p, (int)c.d, (int)ps.ctas, mk, mv, stream);
     } else {
       le = blkattn::launch_decode_split_paged(p, c.elt, (int)c.d, ps.cfg, stream);

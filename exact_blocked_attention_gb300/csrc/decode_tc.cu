@@ -26,7 +26,8 @@
 // one CTA is finished in place; otherwise each CTA writes its partial state
 // of the unit to workspace slot (CTA index + unit index), counts itself in
 // the unit's counter, and the last CTA to arrive folds the unit's partial
-// states (no second kernel, no CTA ever waits for another).
+// states (no second kernel, no CTA ever waits for another); over pages few
+// units of many parts are left to a second kernel, below.
 // The tile counts come from the device-resident lengths and positions, so
 // every CTA streams the same number of tiles whatever the length mix, and no
 // SM idles at the end.
@@ -285,8 +286,8 @@ __device__ __forceinline__ int scatter_base(int lane) {
 // 50 ns to issue, and pages of 16 need 16 of them a tile.  Rows of 128 dims
 // that lie packed (WIDE) come with both 64-dim halves in one box.
 // Measured on batch-32 GQA decode (571 MB), pages of 16: one warp and a box a
-// half 115 us, two warps 107, one box for both halves 100, both 96; pages of 8
-// 99, of 128 96; the contiguous cache 91 (the rest is per unit: the lookups
+// half 115 us, two warps 107, one box for both halves 100, both 95; pages of 8
+// 98, of 128 95; the contiguous cache 91 (the rest is per unit: the lookups
 // and the wider row facts).  One lane issuing every box in a loop: 110.
 // A page number outside the pool goes to the copy as -1, which lies outside
 // the tensor map and reads as zeros; the loader warp scans the unit's entries,
@@ -299,7 +300,7 @@ __device__ __forceinline__ int scatter_base(int lane) {
 // What bounds it: memory at d = 128 (one 131072-key context 89-91 us, 88-90 %
 // of the copy bandwidth).  At d = 64 a tile is half the bytes for the same
 // chain of scores, P and value product, about 0.9 us: 16 x 8 windows of 4096
-// keys 39.7 us, half of the bandwidth, 15 us of it start and finish.  Two
+// keys 38 us, half of the bandwidth, 15 us of it start and finish.  Two
 // issuing threads (scores, value products) did not shorten it.
 // (WIDE is a template argument for the issuing thread's sake: descriptor steps
 // that are constants take 1 us off 96, 1.4 off 39.7 at d = 64.)
@@ -444,14 +445,13 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
       // with fewer tiles than CTAs the last CTAs stay idle, so that every
       // working CTA has a tile and the CTAs holding one unit are consecutive
       long long P = W < (long long)gridDim.x ? W : (long long)gridDim.x;
-      if (PAGED && P > 0) {
-        // Few long units spread over every CTA make many parts, and one CTA
+      if (PAGED && P > 0 && !p.join) {
+        // Short units spread over every CTA make many parts, and one CTA
         // folds a unit's, 512 items (4 dims of a row) at a time, four parts a
         // round trip: t tiles a CTA cost about 1.5 t us, and units of n tiles
         // 0.17 n / t us a fold pass.  At least the t of the minimum (with
-        // twice the fold's cost, which fits best).  One KV head, 16384 keys:
-        // 48 rows 111 us without, 34 us with it, one row 33 and 20 us; 4 x 8
-        // units of 1000 keys 17.6 and 13.2 us.
+        // twice the fold's cost, which fits best).  4 x 8 units of 1000 keys
+        // 17.6 us without, 13.2 with it.
         const float n = (float)W / (float)(B * Hkv * RG);
         const int t_min = (int)ceilf(sqrtf(0.233f * n * (float)((R * D + 2047) / 2048)) - 0.01f);
         if (t_min > 1) P = min(P, max(1ll, W / t_min));
@@ -946,6 +946,8 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
       const int64_t cl = cta_of(pend_su + pend_n - 1, W, P_work);
       const int nparts = (int)(cl - cf + 1);
       const int rr = min(R, p.rows_per_head - pend_rg * R);  // real rows of the unit
+      if (PAGED && p.join && threadIdx.x == 0 && (int64_t)blockIdx.x == cf)
+        p.ws_unit[unit] = make_int2((int)(cf + unit), nparts);
       if (nparts == 1) {
 #pragma unroll
         for (int r = 0; r < NH; ++r) {
@@ -980,17 +982,21 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
           st_global_hint(p.ws_m + slot * R + k, s_mfin[k], keep);
           st_global_hint(p.ws_l + slot * R + k, s_lfin[k], keep);
         }
-        bar_sync(kBarRows, kKeyThreads);
-        if (threadIdx.x == 0) {
-          // one thread's fences order all: the barriers before and after it
-          // carry the other threads' stores and loads (a fence by each of
-          // them costs every warp its round trip)
-          __threadfence();  // the partial state is visible before the count says so
-          misc[3] = (atomicAdd(&p.unit_cnt[unit], 1u) == (unsigned)(nparts - 1)) ? 1 : 0;
-          __threadfence();  // the other parts are read after the count
+        bool fold = false;
+        if (!PAGED || !p.join) {
+          bar_sync(kBarRows, kKeyThreads);
+          if (threadIdx.x == 0) {
+            // one thread's fences order all: the barriers before and after it
+            // carry the other threads' stores and loads (a fence by each of
+            // them costs every warp its round trip)
+            __threadfence();  // the partial state is visible before the count says so
+            misc[3] = (atomicAdd(&p.unit_cnt[unit], 1u) == (unsigned)(nparts - 1)) ? 1 : 0;
+            __threadfence();  // the other parts are read after the count
+          }
+          bar_sync(kBarRows, kKeyThreads);
+          fold = misc[3] != 0;
         }
-        bar_sync(kBarRows, kKeyThreads);
-        if (misc[3] != 0) {
+        if (fold) {
           if (threadIdx.x == 0) p.unit_cnt[unit] = 0u;  // ready for the next launch
           const int64_t fs = cf + unit;  // the unit's first slot; its parts are consecutive
           // items (row, 4 value dims) over the key threads, two items at a
@@ -1324,6 +1330,107 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
   if (warp == kMmaWarp) tc::dealloc(tb, kTmemCols);
 }
 
+// Joins the parts of the units that several CTAs share (eqs. 33.4-33.5, in CTA
+// order), a block a row: its warps take every fourth part.  For few units of
+// many parts: its launch and round trips take some 3 us whatever the count,
+// where the last CTA's fold takes 2 us and 0.3 for every four parts of 512
+// items.  Cache of 8192 keys, 8 KV heads, one sequence: 1 row 18.0 us folded,
+// 17.0 joined; one KV head, 131072 keys x 16 rows 44 and 26, 16384 x 48 rows
+// 34 and 17; 2 heads x 7000 keys 25 and 15.  64 units of 2048 keys 23.1 and
+// 24.3, 144 units of 20 tiles 38 and 42: the fold is kept for these.
+constexpr int kJoinWarps = 4;
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const FwdParams p) {
+  // launched as a programmatic dependent of the decode kernel
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int DPL = D / 32;       // dims a lane
+  constexpr int kMaxParts = 256;    // (at most 255 CTAs)
+  constexpr int kBatch = 8;         // parts of a warp whose loads are in flight together
+  __shared__ float s_c[kMaxParts];
+  __shared__ float s_red[2][kJoinWarps];
+  __shared__ float s_u[kJoinWarps][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int R = p.rows_cta;
+  const int unit = blockIdx.x / R, row = blockIdx.x - unit * R;
+  const int rg = unit % p.row_groups;
+  const int pk = rg * R + row;
+  if (pk >= p.rows_per_head) return;
+  const int2 f = p.ws_unit[unit];  // first slot, parts
+  if (f.y < 2) return;             // finished by its CTA
+  // (a decode kernel that gave up leaves anything here)
+  if (f.y >= kMaxParts || f.x < 0 || f.x > p.n_splits - f.y) return;
+  const int64_t idx0 = (int64_t)f.x * R + row;
+  float m[2], l[2], M = kNegInf;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int s = (int)threadIdx.x + k * 32 * kJoinWarps;
+    m[k] = s < f.y ? p.ws_m[idx0 + (int64_t)s * R] : kNegInf;
+    l[k] = s < f.y ? p.ws_l[idx0 + (int64_t)s * R] : 0.f;
+    M = fmaxf(M, m[k]);
+  }
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  if (lane == 0) s_red[0][warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_red[0][w]);
+  float ls = 0.f;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float c = m[k] == kNegInf ? 0.f : fast_exp2(m[k] - M);  // an empty part contributes nothing
+    s_c[threadIdx.x + k * 32 * kJoinWarps] = c;
+    ls += m[k] == kNegInf ? 0.f : c * l[k];
+  }
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, off);
+  if (lane == 0) s_red[1][warp] = ls;
+  __syncthreads();
+  float u[DPL];
+#pragma unroll
+  for (int c = 0; c < DPL; ++c) u[c] = 0.f;
+  for (int s0 = warp; s0 < f.y; s0 += kJoinWarps * kBatch) {
+    float v[kBatch][DPL];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int s = min(s0 + k * kJoinWarps, f.y - 1);
+      const float* us = p.ws_u + (idx0 + (int64_t)s * R) * D + lane * DPL;
+      if constexpr (DPL == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(us);
+        v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(us);
+        v[k][0] = x.x; v[k][1] = x.y;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int s = s0 + k * kJoinWarps;
+      const float c = s < f.y ? s_c[s] : 0.f;
+#pragma unroll
+      for (int e = 0; e < DPL; ++e) u[e] = c == 0.f ? u[e] : fmaf(c, v[k][e], u[e]);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < DPL; ++c) s_u[warp][lane * DPL + c] = u[c];
+  __syncthreads();
+  const float L = (s_red[1][0] + s_red[1][1]) + (s_red[1][2] + s_red[1][3]);
+  const int d = threadIdx.x;
+  const int g = unit / p.row_groups;  // (sequence, KV head)
+  const int b = g / p.Hkv, hk = g - b * p.Hkv;
+  const int h = hk * p.G + pk / p.Tq, i = pk % p.Tq;
+  if (d < D) {
+    const float o = M == kNegInf ? 0.f : ((s_u[0][d] + s_u[1][d]) + (s_u[2][d] + s_u[3][d])) * (1.f / L);
+    const int64_t oi = (int64_t)b * p.o_sb + (int64_t)h * p.o_sh + (int64_t)i * p.o_si + (int64_t)d * p.o_sd;
+    if (p.out_bf16)
+      static_cast<__nv_bfloat16*>(p.out)[oi] = __float2bfloat16_rn(o);
+    else
+      static_cast<float*>(p.out)[oi] = o;
+  }
+  if (d == 0)
+    p.lse[(int64_t)b * p.l_sb + (int64_t)h * p.l_sh + (int64_t)i * p.l_si] =
+        M == kNegInf ? kNegInf : (M + __log2f(L)) * kLn2;
+}
+
 template <int NR, int D, bool PAGED, bool WIDE>
 cudaError_t launch_nr(const FwdParams& p, int ctas, const CUtensorMap& tmk, const CUtensorMap& tmv,
                       cudaStream_t stream) {
@@ -1362,10 +1469,23 @@ cudaError_t launch_decode_tc(const FwdParams& p, int ctas, const CUtensorMap& tm
 
 cudaError_t launch_decode_tc_paged(const FwdParams& p, int d, int ctas, const CUtensorMap& tmk,
                                    const CUtensorMap& tmv, cudaStream_t stream) {
-  if (d == 128 && p.pages.wide) return launch_rows<128, true, true>(p, ctas, tmk, tmv, stream);
-  if (d == 128) return launch_rows<128, true, false>(p, ctas, tmk, tmv, stream);
-  if (d == 64) return launch_rows<64, true, false>(p, ctas, tmk, tmv, stream);
-  return cudaErrorInvalidValue;
+  if (d != 128 && d != 64) return cudaErrorInvalidValue;
+  if (cudaError_t e = d == 64        ? launch_rows<64, true, false>(p, ctas, tmk, tmv, stream)
+                      : p.pages.wide ? launch_rows<128, true, true>(p, ctas, tmk, tmv, stream)
+                                     : launch_rows<128, true, false>(p, ctas, tmk, tmv, stream);
+      e != cudaSuccess || !p.join)
+    return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.B * p.Hkv * p.row_groups * p.rows_cta));
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return d == 128 ? cudaLaunchKernelEx(&cfg, decode_join_kernel<128>, p)
+                  : cudaLaunchKernelEx(&cfg, decode_join_kernel<64>, p);
 }
 
 }  // namespace blkattn

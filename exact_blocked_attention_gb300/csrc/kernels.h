@@ -70,6 +70,10 @@ struct FwdParams {
   // wrote theirs (zero before the launch, left zero after it)
   int rows_cta;
   unsigned* unit_cnt;
+  // the same kernel over pages: a second kernel joins the units' parts;
+  // ws_unit: each unit's first slot and its parts
+  bool join;
+  int2* ws_unit;
   // prefill: 1 when the output tensor map (fp32, boxes {32, 32}, 128-byte
   // swizzle) is valid and the kernel stores whole output tiles with TMA
   int o_tma;

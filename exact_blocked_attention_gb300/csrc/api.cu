@@ -931,7 +931,7 @@ int fwd_paged_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages_, con
   if (pl.cfg.kernel != blkattn::Kernel::CudaCore) {
     const int box = pt.rows < 128 ? pt.rows : 128;
     int v2 = 0, v3 = 0;
-    if (!prefill && wide_pages(k_pages, &pt.wide_h2, &pt.wide_h3) && wide_pages(v_pages, &v2, &v3) &&
+    if (wide_pages(k_pages, &pt.wide_h2, &pt.wide_h3) && wide_pages(v_pages, &v2, &v3) &&
         v2 == pt.wide_h2 && v3 == pt.wide_h3) {
       pt.wide = 1;
       if ((st = wide_pages_map(dev, k_pages, box, v2, v3, &mk)) != BLKATTN_OK) return st;

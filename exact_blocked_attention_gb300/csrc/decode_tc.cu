@@ -73,6 +73,7 @@
 #include <cuda_bf16.h>
 
 #include "kernels.h"
+#include "paged_tma.cuh"
 #include "ptx.cuh"
 #include "tc.cuh"
 
@@ -202,17 +203,6 @@ struct Cursor {
 __device__ __forceinline__ int64_t cta_of(int64_t t, int64_t W, int64_t P) {
   const uint32_t w = (uint32_t)W;
   return (int64_t)((((uint32_t)t + 1u) * (uint32_t)P + w - 1u) / w) - 1;
-}
-
-// tma_load_4d for a 5-D tensor map.
-__device__ __forceinline__ void tma_load_5d(void* dst, const void* map, int c0, int c1, int c2, int c3, int c4,
-                                            uint64_t* bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar)),
-      "l"(policy)
-      : "memory");
 }
 
 // N consecutive TMEM columns of this thread's lane (N = 8, 16 or 24; the

@@ -14,7 +14,8 @@
 // Roles (320 threads): warps 0-3 and 4-7 = one thread per query row of the
 // first / second query tile (a TMEM lane each): scores, mask by select,
 // online statistics, P; warp 8 = TMA producer (both Q tiles once, K and V
-// tiles into 2-stage rings released separately); warp 9 = TMEM allocation
+// tiles into 2-stage rings released separately; over pages warps 8 and 10, see
+// the kernel); warp 9 = TMEM allocation
 // and the single thread that issues every MMA.  Each query tile has one S
 // buffer in TMEM and P_j is written over it.  On a key tile that some row of
 // the query tile does not see in full (the diagonal, a window's leading
@@ -54,6 +55,7 @@
 #include <cuda_bf16.h>
 
 #include "kernels.h"
+#include "paged_tma.cuh"
 #include "ptx.cuh"
 #include "tc.cuh"
 
@@ -89,9 +91,11 @@ constexpr uint32_t kTileCols = 256;  // per query tile: S / P at [0, 128), U at 
 constexpr uint32_t kColS = 0;
 constexpr uint32_t kColPlo = 64;     // P_hi at [0, 64), P_lo at [64, 128) (bf16 pairs)
 constexpr uint32_t kColO = 128;
-constexpr int kThreads = 320;
 constexpr int kTmaWarp = 8;
 constexpr int kMmaWarp = 9;
+constexpr int kPageVWarp = 10;  // PAGED: V tiles (kTmaWarp: K tiles)
+template <bool PAGED>
+constexpr int kThreads = 32 * (PAGED ? 11 : 10);
 constexpr uint32_t kIdescQK = tc::idesc_bf16(BM, BN, 0, 0);  // Q, K both K-major
 template <int D>
 constexpr uint32_t kIdescPV = tc::idesc_bf16(BM, D, 0, 1);   // P (TMEM), V MN-major
@@ -127,17 +131,20 @@ __device__ __forceinline__ void item_of(const FwdParams& p, int r, int n_pairs, 
 }
 
 // PAGED: the cache lies in pages (paged.h).  A key tile is one box of a page of
-// at least 128 rows or the boxes of 128 / P pages: the producer warp's lanes
-// look their pages up a tile ahead and issue the copies; a page number outside
-// the pool goes to the copy as -1 (zeros) and the rows mask its keys, in
+// at least 128 rows or the boxes of 128 / P pages: the lanes of two producer
+// warps (K, V) look their pages up a tile ahead and issue the copies, with
+// packed rows of 128 dims both halves in one box (WIDE), as in the decode
+// kernel: a copy takes its warp some 50 ns to issue, and one warp with a box a
+// half took 576 us for the case below in pages of 8, 398 in pages of 16, 355
+// in pages of 128; now 359 in any.  A page number outside the pool goes to the copy as -1 (zeros) and the rows mask its keys, in
 // tensor memory (a mask in registers spilled 576 bytes).  The chain of a key
 // tile bounds it as over a contiguous cache: 2 x 2048 rows of 32 heads at 8192
-// keys 376 us (1280 TFLOP/s, 65 % of the bf16 burst rate), contiguous 384.
+// keys 357 us (1350 TFLOP/s, 68 % of the bf16 burst rate), contiguous 384.
 // At d = 64 the chain's products are half as long: 1.1 us a key tile for one
 // query tile, 1.36 for two (d = 128: 1.4 and 1.6); 1024 rows of 32 heads at
 // 2048 keys 32 us, 99 with the decode kernel.
-template <int D, bool WIN, bool PAGED>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, bool WIN, bool PAGED, bool WIDE>
+__global__ void __launch_bounds__(kThreads<PAGED>, 1)
     prefill_tc_kernel(const FwdParams p, const __grid_constant__ CUtensorMap tmq,
                       const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                       const __grid_constant__ CUtensorMap tmo) {
@@ -338,54 +345,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!landed) record_error(p.err, kErrTimeout);
     }
-  } else if (PAGED && warp == kTmaWarp) {
-    // ---------------- TMA producer, pages (whole warp) ----------------
+  } else if (PAGED && (warp == kTmaWarp || warp == kPageVWarp)) {
+    // ---------------- TMA producers, pages (whole warps, one for K, one for V) ----------------
+    const bool kv = warp == kPageVWarp;
+    const void* map = kv ? static_cast<const void*>(&tmv) : static_cast<const void*>(&tmk);
+    uint64_t* full = kv ? v_full : k_full;
+    uint64_t* empty = kv ? v_empty : k_empty;
     const int box_shift = min(p.pages.shift, 7);
     const int n_pieces = BN >> box_shift;
     const int piece = lane & (n_pieces - 1);  // of the tile's keys
     const int half = lane >> (7 - box_shift);  // 64-dim box
-    const uint32_t dst_off = (uint32_t)(half * kBox + (piece << box_shift) * 128);
+    const bool copies = half < (WIDE ? 1 : kBoxes);
+    const uint32_t dst_off = (kv ? kOffV : kOffK) + (WIDE ? (uint32_t)((piece << box_shift) * 256)
+                                                          : (uint32_t)(half * kBox + (piece << box_shift) * 128));
     auto look_up = [&](int j) {  // this lane's page of key tile j: -1 (zeros) past the rows' ends
       const int key = (j_lo + j) * BN + (piece << box_shift);
       return j < n_max && key < cta_end ? page_of(p.pages, b, key) : -1;
     };
-    int issued = 0;  // ring positions whose K and V copies were both issued
-    int k_issued = 0;
+    int issued = 0;  // ring positions
     bool ok = true;
     int page = look_up(0);
     for (int j = 0; j < n_max && ok; ++j) {
       const int s = j % STAGES;
       const int row = ((j_lo + j) * BN + (piece << box_shift)) & (p.pages.rows - 1);
       const int page_next = look_up(j + 1);  // (the load is in flight meanwhile)
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        uint64_t* full = kv ? &v_full[s] : &k_full[s];
-        bool w = true;
-        if (lane == 0) {
-          if (j >= STAGES) w = mbar_wait(kv ? &v_empty[s] : &k_empty[s], ((j / STAGES) - 1) & 1);
-          if (w) mbar_arrive_expect_tx(full, kTileBytes);
-        }
-        if (!__shfl_sync(0xffffffffu, w, 0)) {  // (also orders the expected bytes before the copies)
-          ok = false;
-          break;
-        }
-        __syncwarp();
-        if (half < kBoxes)
-          tma_load_4d(sm + (kv ? kOffV : kOffK) + s * kTileBytes + dst_off,
-                      kv ? static_cast<const void*>(&tmv) : static_cast<const void*>(&tmk), 64 * half, row, hk, page,
-                      full, pol_kv);
-        if (kv == 0) k_issued = j + 1; else issued = j + 1;
+      bool w = true;
+      if (lane == 0) {
+        if (j >= STAGES) w = mbar_wait(&empty[s], ((j / STAGES) - 1) & 1);
+        if (w) mbar_arrive_expect_tx(&full[s], kTileBytes);
       }
+      ok = __shfl_sync(0xffffffffu, w, 0);  // (also orders the expected bytes before the copies)
+      if (!ok) break;
+      __syncwarp();
+      if (copies) {
+        unsigned char* dst = sm + s * kTileBytes + dst_off;
+        if (WIDE)
+          tma_load_5d(dst, map, 0, 0, hk * p.pages.wide_h2, (row >> 3) + hk * p.pages.wide_h3, page, &full[s], pol_kv);
+        else
+          tma_load_4d(dst, map, 64 * half, row, hk, page, &full[s], pol_kv);
+      }
+      issued = j + 1;
       page = page_next;
     }
     __syncwarp();
     if (lane == 0) {
       // every issued copy must land before the CTA can exit
-      if (!mbar_wait(q_full, 0)) ok = false;
-      for (int j = k_issued - STAGES < 0 ? 0 : k_issued - STAGES; j < k_issued; ++j)
-        if (!mbar_wait(&k_full[j % STAGES], (j / STAGES) & 1)) ok = false;
+      if (!kv && !mbar_wait(q_full, 0)) ok = false;
       for (int j = issued - STAGES < 0 ? 0 : issued - STAGES; j < issued; ++j)
-        if (!mbar_wait(&v_full[j % STAGES], (j / STAGES) & 1)) ok = false;
+        if (!mbar_wait(&full[j % STAGES], (j / STAGES) & 1)) ok = false;
       if (!ok) {
         record_error(p.err, kErrTimeout);
         misc[5] = 1;
@@ -435,17 +442,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- MMA issue (one thread) ----------------
     if (lane == 0) {
       bool ok = mbar_wait(q_full, 0);
+      // K and V tiles: 64-dim boxes 16 KB apart, rows 128 bytes apart; a page's
+      // wide box instead has the two halves of 8 rows side by side (8-row
+      // groups 2 KB apart, the second half 1 KB behind the first)
+      constexpr uint32_t kHi = tc::desc_hi(1024);
+      constexpr uint32_t kHiKV = WIDE ? tc::desc_hi(2048) : kHi;
+      constexpr uint32_t kHalf = WIDE ? 1024u : (uint32_t)kBox;
       // S_jj = Q_t K_jj^T into query tile t's S buffer
       auto issue_qk = [&](int t, int jj) {
         // descriptors: only the start address moves (split-word form)
         const uint32_t klo = tc::desc_lo(sK + ((jj + ro) % STAGES) * kTileBytes, 16);
         const uint32_t qlo = tc::desc_lo(sQ + t * kTileBytes, 16);
-        constexpr uint32_t kHi = tc::desc_hi(1024);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (uint32_t)(((ks >> 2) * kBox + (ks & 3) * 32) >> 4);
-          const uint64_t adesc = tc::desc_join(qlo + off, kHi);
-          const uint64_t bdesc = tc::desc_join(klo + off, kHi);
+          const uint64_t adesc = tc::desc_join(qlo + (uint32_t)(((ks >> 2) * kBox + (ks & 3) * 32) >> 4), kHi);
+          const uint64_t bdesc = tc::desc_join(klo + (((uint32_t)(ks >> 2) * kHalf + (ks & 3) * 32) >> 4), kHiKV);
           tc::mma_ss(tb + t * kTileCols + kColS, adesc, bdesc, kIdescQK, ks > 0 ? 1u : 0u);
         }
         tc::commit(&s_full[t]);
@@ -455,8 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int min_end[QT] = {misc[2], misc[4]};
       const int win_max[QT] = {WIN ? misc[7] : 0, WIN ? misc[9] : 0};
       auto issue_pv = [&](int t, int jj, bool more) {
-        const uint32_t vlo = tc::desc_lo(sV + ((jj + ro) % STAGES) * kTileBytes, kBox);
-        constexpr uint32_t kHi = tc::desc_hi(1024);
+        const uint32_t vlo = tc::desc_lo(sV + ((jj + ro) % STAGES) * kTileBytes, kHalf);
         const uint32_t tcol = tb + t * kTileCols;
         const int k0 = (j_lo + jj) * BN;
         const bool split = k0 + BN > min_end[t] || (WIN && k0 < win_max[t]);
@@ -466,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int ks = 0; ks < BN / 16; ++ks) {
             // B = V rows [16ks, 16ks+16) (keys, K) x 128 dims (N, two 64-dim boxes 16 KB apart)
-            const uint64_t bdesc = tc::desc_join(vlo + (uint32_t)(ks * 16 * 128 >> 4), kHi);
+            const uint64_t bdesc = tc::desc_join(vlo + (uint32_t)(ks * (WIDE ? 4096 : 2048) >> 4), kHiKV);
             const uint32_t acol = tcol + kColS + part * kColPlo + 8 * ks;
             tc::mma_ts(tcol + kColO, acol, bdesc, kIdescPV<D>, (more || part > 0 || ks > 0) ? 1u : 0u);
           }
@@ -703,7 +713,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int r = z0 + idx / (D / 8);
             if (WIN && PAGED && r >= BN) r -= BN;
             const int c = idx % (D / 8);  // 16-byte chunk over the dims (64 a box)
-            *reinterpret_cast<uint4*>(vt + (c >> 3) * kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+            const int at = WIDE ? (r >> 3) * 2048 + (c >> 3) * 1024 + (r & 7) * 128 : (c >> 3) * kBox + r * 128;
+            *reinterpret_cast<uint4*>(vt + at + (((c & 7) ^ (r & 7)) << 4)) =
                 make_uint4(0, 0, 0, 0);
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -962,19 +973,19 @@ int prefill_tc_smem_bytes() { return Layout<128>::kSmemBytes; }
 
 namespace {
 
-template <int D, bool WIN, bool PAGED>
+template <int D, bool WIN, bool PAGED, bool WIDE>
 cudaError_t launch_kernel(const FwdParams& p, unsigned blocks, const CUtensorMap& tmq, const CUtensorMap& tmk,
                           const CUtensorMap& tmv, const CUtensorMap& tmo, cudaStream_t stream) {
   static DeviceOnce once;
   constexpr int kSmemBytes = Layout<D>::kSmemBytes;
-  if (cudaError_t e = once.set_smem(reinterpret_cast<const void*>(&prefill_tc_kernel<D, WIN, PAGED>), kSmemBytes);
+  if (cudaError_t e = once.set_smem(reinterpret_cast<const void*>(&prefill_tc_kernel<D, WIN, PAGED, WIDE>), kSmemBytes);
       e != cudaSuccess)
     return e;
-  prefill_tc_kernel<D, WIN, PAGED><<<blocks, kThreads, kSmemBytes, stream>>>(p, tmq, tmk, tmv, tmo);
+  prefill_tc_kernel<D, WIN, PAGED, WIDE><<<blocks, kThreads<PAGED>, kSmemBytes, stream>>>(p, tmq, tmk, tmv, tmo);
   return cudaGetLastError();
 }
 
-template <int D, bool PAGED>
+template <int D, bool PAGED, bool WIDE>
 cudaError_t launch_form(const FwdParams& p, int n_pairs, const CUtensorMap& tmq, const CUtensorMap& tmk,
                         const CUtensorMap& tmv, const CUtensorMap& tmo, cudaStream_t stream) {
   const int64_t heads = (int64_t)p.Hq * p.B;
@@ -983,23 +994,24 @@ cudaError_t launch_form(const FwdParams& p, int n_pairs, const CUtensorMap& tmq,
   int64_t blocks = groups * p.head_group * n_pairs;
   if (PAGED) blocks = p.split_from + (heads * n_pairs - p.split_from) * p.n_splits;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  if (p.window > 0) return launch_kernel<D, true, PAGED>(p, (unsigned)blocks, tmq, tmk, tmv, tmo, stream);
-  return launch_kernel<D, false, PAGED>(p, (unsigned)blocks, tmq, tmk, tmv, tmo, stream);
+  if (p.window > 0) return launch_kernel<D, true, PAGED, WIDE>(p, (unsigned)blocks, tmq, tmk, tmv, tmo, stream);
+  return launch_kernel<D, false, PAGED, WIDE>(p, (unsigned)blocks, tmq, tmk, tmv, tmo, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_prefill_tc(const FwdParams& p, int n_pairs, const CUtensorMap& tmq, const CUtensorMap& tmk,
                               const CUtensorMap& tmv, const CUtensorMap& tmo, cudaStream_t stream) {
-  return launch_form<128, false>(p, n_pairs, tmq, tmk, tmv, tmo, stream);
+  return launch_form<128, false, false>(p, n_pairs, tmq, tmk, tmv, tmo, stream);
 }
 
 cudaError_t launch_prefill_tc_paged(const FwdParams& p, int d, int n_pairs, const CUtensorMap& tmq,
                                     const CUtensorMap& tmk, const CUtensorMap& tmv, const CUtensorMap& tmo,
                                     cudaStream_t stream) {
   if (d != 128 && d != 64) return cudaErrorInvalidValue;
-  if (cudaError_t e = d == 128 ? launch_form<128, true>(p, n_pairs, tmq, tmk, tmv, tmo, stream)
-                               : launch_form<64, true>(p, n_pairs, tmq, tmk, tmv, tmo, stream);
+  if (cudaError_t e = d == 64        ? launch_form<64, true, false>(p, n_pairs, tmq, tmk, tmv, tmo, stream)
+                      : p.pages.wide ? launch_form<128, true, true>(p, n_pairs, tmq, tmk, tmv, tmo, stream)
+                                     : launch_form<128, true, false>(p, n_pairs, tmq, tmk, tmv, tmo, stream);
       e != cudaSuccess || p.n_splits == 1)
     return e;
   const int64_t rows = ((int64_t)p.Hq * p.B * n_pairs - p.split_from) * (QT * BM);

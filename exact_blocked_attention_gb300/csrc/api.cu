@@ -825,6 +825,11 @@ PromptPlan plan_prompt(const Checked& c, int sms) {
 // kernel mostly wins: 64 rows x 32 heads at 8192 keys 37 and 43 us, at 2048
 // keys 20 and 26.
 bool prompt_kernel_pays(const Checked& c, const PromptPlan& pp, int sms) {
+  // what the decode kernel cannot take, as make_plan tells it for one sequence
+  const int64_t groups = (c.Hq / c.Hkv * c.Tq + 47) / 48;
+  if (groups > blkattn::kDecodeTcMaxEntries / 2 || c.Tmax > 65535LL * 128 ||
+      c.Hkv * groups * ((c.Tmax + 127) / 128 + 2) >= (1LL << 24))
+    return true;
   const int64_t keys = c.window > 0 && c.window + c.Tq < c.Tmax ? c.window + c.Tq : c.Tmax;
   const double tiles = (double)((keys + 127) / 128);
   const int64_t P = sms > 0 ? sms : 148;

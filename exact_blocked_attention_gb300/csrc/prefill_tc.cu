@@ -136,10 +136,11 @@ __device__ __forceinline__ void item_of(const FwdParams& p, int r, int n_pairs, 
 // packed rows of 128 dims both halves in one box (WIDE), as in the decode
 // kernel: a copy takes its warp some 50 ns to issue, and one warp with a box a
 // half took 576 us for the case below in pages of 8, 398 in pages of 16, 355
-// in pages of 128; now 359 in any.  A page number outside the pool goes to the copy as -1 (zeros) and the rows mask its keys, in
-// tensor memory (a mask in registers spilled 576 bytes).  The chain of a key
-// tile bounds it as over a contiguous cache: 2 x 2048 rows of 32 heads at 8192
-// keys 357 us (1350 TFLOP/s, 68 % of the bf16 burst rate), contiguous 384.
+// in pages of 128; now 359 in any.  A page number outside the pool goes to the
+// copy as -1 (zeros) and the rows mask its keys, in tensor memory (a mask in
+// registers spilled 576 bytes).  The chain of a key tile bounds it as over a
+// contiguous cache: 2 x 2048 rows of 32 heads at 8192 keys 357 us (1350
+// TFLOP/s, 68 % of the bf16 burst rate), contiguous 384.
 // At d = 64 the chain's products are half as long: 1.1 us a key tile for one
 // query tile, 1.36 for two (d = 128: 1.4 and 1.6); 1024 rows of 32 heads at
 // 2048 keys 32 us, 99 with the decode kernel.

@@ -477,6 +477,27 @@ def test_long_context():
     check(a, *call(a, BF16))
 
 
+@pytest.mark.parametrize("Tq,P,n", [(64, 65536, 129), (64, 32768, 70), (1, 32768, 70)])
+def test_very_long_prompts_and_contexts(Tq, P, n):
+    # one page, n times in the table (129 x 65536 keys are past the decode
+    # kernel's range): the attention of one page's keys, lse + ln n
+    a = make(1, 1, 1, Tq, 64, P, [P], seed=89)
+    a["vp"] += 3  # outputs well away from 0
+    ro, rl, ob, lb = reference(dict(a, pos=torch.full_like(a["pos"], P - 1)))
+    a["table"] = a["table"][:, :1].repeat(1, n)
+    a["lens"] = a["lens"] * n
+    a["pos"] = torch.full_like(a["pos"], n * P - 1)
+    out, lse = call(a)
+    assert blkattn.check_device_error() == 0
+    # One sequence is cut into 16 parts or more.  Within one, l takes a sum a
+    # tile of 128 keys (2^-24 each), U a product of 16 keys (2^-23 each).
+    more_l = n * P / 16 / 128 * 2.0 ** -24
+    more_u = n * P / 16 / 16 * 2.0 ** -23
+    av = float(a["vp"][int(a["table"][0, 0])].double().abs().max())
+    assert bool(((out.double() - ro).abs() <= ob + (more_l + more_u) * av + 2.0 ** -24 * ro.abs()).all())
+    assert bool(((lse.double() - rl - math.log(n)).abs() <= lb + more_l + 2.0 ** -21 * math.log(n)).all())
+
+
 @pytest.mark.parametrize("Tq", [1, 100])
 def test_pool_offsets_past_32_bits(Tq):
     P, H, d = 256, 8, 128

@@ -168,6 +168,17 @@ Plan make_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t Tq, int64_t Tmax, int
     pl.cfg.stages = 3;
     pl.tile = 64;
     smem = blkattn::decode_mma_smem_bytes(d, (int)mt);
+  } else if (paged && elt == Elt::F32 && rows > 8) {
+    // (8 rows are what the split-KV kernel takes at once; 12 rows of one head
+    // at 2000 keys 22.0 us there and 17.5 here, 136 rows of 2 heads at 300 keys
+    // 20.1 and 19.7)
+    const int64_t rg = (rows + 63) / 64;
+    pl.cfg.kernel = blkattn::Kernel::RowsF32;
+    pl.cfg.rows_per_cta = (int)((rows + rg - 1) / rg);
+    pl.cfg.warps = 4;
+    pl.cfg.stages = 2;
+    pl.tile = 32;
+    smem = blkattn::rows_f32_smem_bytes(d, pl.cfg.rows_per_cta);
   } else {
     int R = 1;
     while (R < rows && R < 8) R *= 2;
@@ -194,6 +205,25 @@ Plan make_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t Tq, int64_t Tmax, int
     chunk = (Tmax * units + target - 1) / target;
     const int64_t min_chunk = pl.tile;
     if (chunk < min_chunk) chunk = min_chunk;
+  }
+  if (pl.cfg.kernel == blkattn::Kernel::RowsF32) {
+    // The count of splits n with the least estimated time: waves of CTAs, each
+    // n-th part of the key tiles at 1.1 us a tile for every 8 rows (d = 128,
+    // both resident blocks at work) and 4 us of its own, and the merge of n
+    // states a row.  The rule above left a second wave nearly empty: 7 x 32
+    // heads x 17 rows at 1000 keys 129 us, 102 with this.
+    const int64_t tiles = (Tmax + pl.tile - 1) / pl.tile;
+    const double tile = 1.1 * (double)((pl.cfg.rows_per_cta + 7) / 8) * d / 128.0 * resident / 2.0;
+    double best = 0.0;
+    for (int64_t n = 1; n <= 256 && n <= tiles && (n - 1) * units < 3 * target; ++n) {
+      const int64_t per = (tiles + n - 1) / n;
+      const double us = (double)((units * n + target - 1) / target) * (4.0 + tile * (double)per) +
+                        (n > 1 ? 3.0 + (double)(n * B * Hq * Tq) * d * 8.0 / 3e6 : 0.0);
+      if (n == 1 || us < best) {
+        best = us;
+        chunk = per * pl.tile;
+      }
+    }
   }
   if (const char* env = std::getenv("BLKATTN_CHUNK")) {  // tuning sweeps only
     const long v = std::strtol(env, nullptr, 10);
@@ -838,6 +868,10 @@ bool prompt_kernel_pays(const Checked& c, const PromptPlan& pp, int sms) {
   return pp.us <= decode;
 }
 
+bool on_cuda_cores(const Plan& pl) {
+  return pl.cfg.kernel == blkattn::Kernel::CudaCore || pl.cfg.kernel == blkattn::Kernel::RowsF32;
+}
+
 // blkattn_fwd_paged: the pools take the places of k and v, their strides those
 // of the cache rows.  The tcgen05 decode kernel's unit table holds a limited
 // number of sequences: longer batches run slice by slice, one after another on
@@ -892,7 +926,7 @@ int fwd_paged_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages_, con
   // sequences per launch: all, or as many as keep the fast kernel
   int64_t nb = c.B;
   Plan pl = plan_of(nb);
-  if (pl.cfg.kernel == blkattn::Kernel::CudaCore && nb > 1) {
+  if (on_cuda_cores(pl) && nb > 1) {
     const int64_t rg = (c.Hq / c.Hkv * c.Tq + 47) / 48;
     const int64_t fit = (window > 0 ? blkattn::kDecodeTcMaxEntries / 2 : blkattn::kDecodeTcMaxEntries) / rg;
     const int64_t tiles = c.Hkv * rg * ((c.Tmax + 127) / 128 + 2);
@@ -906,12 +940,12 @@ int fwd_paged_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages_, con
         pl = alt;
       }
     }
-    if (pl.cfg.kernel == blkattn::Kernel::CudaCore && nb * pl.cfg.row_groups > 65535) {  // grid z
+    if (on_cuda_cores(pl) && nb * pl.cfg.row_groups > 65535) {  // grid z
       nb = 65535 / pl.cfg.row_groups;
       if (nb < 1) return BLKATTN_ERR_UNSUPPORTED;
       pl = plan_of(nb);
     }
-  } else if (pl.cfg.kernel == blkattn::Kernel::CudaCore && pl.cfg.row_groups > 65535) {
+  } else if (on_cuda_cores(pl) && pl.cfg.row_groups > 65535) {
     return BLKATTN_ERR_UNSUPPORTED;
   }
   // (every part leaves 256 rows of m, l and u)
@@ -933,7 +967,7 @@ int fwd_paged_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages_, con
   CUtensorMap mk, mv, mq, mo;
   const bool prefill = pl.cfg.kernel == blkattn::Kernel::Prefill;
   bool o_tma = false;
-  if (pl.cfg.kernel != blkattn::Kernel::CudaCore) {
+  if (!on_cuda_cores(pl)) {
     const int box = pt.rows < 128 ? pt.rows : 128;
     int v2 = 0, v3 = 0;
     if (wide_pages(k_pages, &pt.wide_h2, &pt.wide_h3) && wide_pages(v_pages, &v2, &v3) &&
@@ -982,7 +1016,9 @@ int fwd_paged_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages_, con
       p.ws_unit = reinterpret_cast<int2*>(static_cast<char*>(ds->ws) + ps.ws_bytes - (ps.units * 8 + 255) / 256 * 256);
       le = blkattn::launch_decode_tc_paged(p, (int)c.d, (int)ps.ctas, mk, mv, stream);
     } else {
-      le = blkattn::launch_decode_split_paged(p, c.elt, (int)c.d, ps.cfg, stream);
+      le = ps.cfg.kernel == blkattn::Kernel::RowsF32
+               ? blkattn::launch_rows_f32(p, (int)c.d, ps.cfg.n_splits, stream)
+               : blkattn::launch_decode_split_paged(p, c.elt, (int)c.d, ps.cfg, stream);
       if (le == cudaSuccess && ps.cfg.n_splits > 1) le = blkattn::launch_split_merge(p, (int)c.d, stream);
     }
     if (le != cudaSuccess) return cuda_fail(le);

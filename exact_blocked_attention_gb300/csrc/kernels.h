@@ -91,7 +91,7 @@ struct FwdParams {
 };
 
 // Split-KV kernel configuration chosen by the planner.
-enum class Kernel : int { CudaCore = 0, TensorCore = 1, Prefill = 2, DecodeTc = 3 };
+enum class Kernel : int { CudaCore = 0, TensorCore = 1, Prefill = 2, DecodeTc = 3, RowsF32 = 4 };
 struct DecodeConfig {
   Kernel kernel;
   int rows_per_cta;  // CUDA-core: 1, 2, 4 or 8; tensor-core: 16, 32 or 48
@@ -108,6 +108,11 @@ cudaError_t launch_decode_split(const FwdParams& p, Elt elt, int d, const Decode
 cudaError_t launch_decode_split_paged(const FwdParams& p, Elt elt, int d, const DecodeConfig& cfg,
                                       cudaStream_t stream);
 cudaError_t launch_split_merge(const FwdParams& p, int d, cudaStream_t stream);
+
+// Many fp32 rows per KV head over a paged cache, CUDA cores: up to 64 rows a
+// CTA, 32 keys a tile; splits and partial states as for the split-KV kernel.
+cudaError_t launch_rows_f32(const FwdParams& p, int d, int n_splits, cudaStream_t stream);
+size_t rows_f32_smem_bytes(int d, int rows);
 
 struct MergeParams {
   const float* am; const float* al; const float* au; int64_t a_us;

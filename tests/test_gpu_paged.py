@@ -177,6 +177,44 @@ def test_few_rows_over_long_contexts(Hq, Hkv, Tq, d, K, window):
     check(a, *call(a, BF16))
 
 
+# fp32 rows above 8 per KV head: 9 to 140 of them, whole and split, even and odd
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("B,Hq,Hkv,Tq,P,lens", [
+    (1, 9, 1, 1, 16, [700]), (2, 8, 4, 8, 32, [500, 33]), (3, 4, 2, 9, 8, [0, 18, 90]), (1, 20, 2, 3, 64, [1500]),
+    (2, 12, 3, 10, 16, [200, 4000]), (1, 47, 1, 1, 256, [300]), (1, 4, 1, 14, 16, [14]), (1, 8, 1, 8, 128, [9000]),
+    (1, 5, 1, 13, 16, [900]), (2, 7, 1, 20, 32, [100, 1000]), (1, 1, 1, 333, 16, [1200]), (40, 8, 8, 17, 16, [260] * 40)])
+def test_many_f32_rows(B, Hq, Hkv, Tq, P, lens, d):
+    a = make(B, Hq, Hkv, Tq, d, P, lens, F32, rows_major=Tq % 2 == 0, seed=Tq + d)
+    want = call(a)
+    check(a, *want)
+    check(a, *call(a, BF16))
+    # query rows behind one another at an odd stride, and dims apart: the same bits
+    for buf, view in ((torch.zeros(B, Tq, Hq, d + 3, device=dev()), lambda t: t[..., 2:d + 2].transpose(1, 2)),
+                      (torch.zeros(B, Hq, d, Tq, device=dev()), lambda t: t.transpose(2, 3))):
+        q = view(buf)
+        q.copy_(a["q"])
+        out, lse = call(dict(a, q=q))
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("d", [128, 64])
+def test_many_f32_rows_with_windows_trees_and_missing_pages(d):
+    a = make(2, 6, 2, 40, d, 16, [3000, 777], F32, seed=97)
+    for window in (1, 50, 1000):
+        a["window"] = window
+        check(a, *call(a))
+    a["window"] = 0
+    a["pos"][0, 3:9] = -1
+    a["pos"][1, 30:] += 100
+    a["table"][0, 5] = -1
+    a["table"][0, 60:100] = 1 << 30
+    check(a, *call(a))
+    a["q"][0, :, 3:9] = math.nan  # padding rows may hold anything
+    out, lse = call(a)
+    assert bool((out[0, :, 3:9] == 0).all()) and bool((lse[0, :, 3:9] == -math.inf).all())
+    assert bool(torch.isfinite(out).all())
+
+
 # prompts whose last items are cut into parts along their keys: fewer items than
 # SMs, sequences much shorter than the table (parts without a key), one wave of
 # items and a rest

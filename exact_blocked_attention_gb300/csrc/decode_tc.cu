@@ -1287,7 +1287,9 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
         bar_sync(kBarRows, kKeyThreads);
         if (half == 0 && k < NR) {
           const float l = (red[k] + red[NR + k]) + (red[2 * NR + k] + red[3 * NR + k]);
-          const float m = s_m[k];
+          // (over pages a NaN in a row's scores, which no maximum shows, makes
+          // the row NaN instead of empty)
+          const float m = PAGED && l != l ? l : s_m[k];
           s_mfin[k] = m;
           s_lfin[k] = l;
           s_inv[k] = (m == kNegInf) ? 0.f : 1.f / l;
@@ -1409,7 +1411,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const FwdP
   const int b = g / p.Hkv, hk = g - b * p.Hkv;
   const int h = hk * p.G + pk / p.Tq, i = pk % p.Tq;
   if (d < D) {
-    const float o = M == kNegInf ? 0.f : ((s_u[0][d] + s_u[1][d]) + (s_u[2][d] + s_u[3][d])) * (1.f / L);
+    // (L = 0: no part saw a key; a maximum would hide a part's NaN)
+    const float o = L == 0.f ? 0.f : ((s_u[0][d] + s_u[1][d]) + (s_u[2][d] + s_u[3][d])) * (1.f / L);
     const int64_t oi = (int64_t)b * p.o_sb + (int64_t)h * p.o_sh + (int64_t)i * p.o_si + (int64_t)d * p.o_sd;
     if (p.out_bf16)
       static_cast<__nv_bfloat16*>(p.out)[oi] = __float2bfloat16_rn(o);
@@ -1418,7 +1421,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const FwdP
   }
   if (d == 0)
     p.lse[(int64_t)b * p.l_sb + (int64_t)h * p.l_sh + (int64_t)i * p.l_si] =
-        M == kNegInf ? kNegInf : (M + __log2f(L)) * kLn2;
+        L == 0.f ? kNegInf : (M + __log2f(L)) * kLn2;
 }
 
 template <int NR, int D, bool PAGED, bool WIDE>

@@ -937,7 +937,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prompt_join_kernel(const FwdP
       for (int c = 0; c < DPL; ++c) u[c] = ws == 0.f ? u[c] : fmaf(ws, v[k][c], u[c]);
     }
   }
-  const float inv = M == kNegInf ? 0.f : 1.f / l;
+  // (l = 0: no part saw a key; a maximum would hide a part's NaN)
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   const int b = bh / p.Hq, h = bh % p.Hq;
   const int64_t o = (int64_t)b * p.o_sb + (int64_t)h * p.o_sh + (int64_t)i * p.o_si;
   const int d0 = lane * DPL;
@@ -965,7 +966,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prompt_join_kernel(const FwdP
   }
   if (lane == 0)
     p.lse[(int64_t)b * p.l_sb + (int64_t)h * p.l_sh + (int64_t)i * p.l_si] =
-        M == kNegInf ? kNegInf : (M + __log2f(l)) * kLn2;
+        l == 0.f ? kNegInf : (M + __log2f(l)) * kLn2;
 }
 
 }  // namespace

@@ -277,6 +277,20 @@ def test_prompts_in_parts_output_layouts(out_dtype, d, window):
             assert bool((buf[..., 0] == 7).all()) and bool((buf[..., d + 1:] == 7).all())
 
 
+@pytest.mark.parametrize("Hq,Hkv,Tq,d,dtype", [(4, 2, 100, 128, BF16), (4, 2, 100, 64, BF16), (8, 2, 3, 128, BF16),
+                                               (8, 2, 3, 64, BF16), (8, 2, 3, 128, F32), (8, 2, 9, 64, F32)])
+def test_a_row_of_nan_stays_its_own(Hq, Hkv, Tq, d, dtype):
+    a = make(2, Hq, Hkv, Tq, d, 16, [3000, 900], dtype, seed=101)
+    want, want_lse = call(a)
+    a["q"][0, 1, 2] = math.nan
+    out, lse = call(a)
+    if dtype == BF16:  # (the fp32 kernels take a row without a comparable score for an empty one)
+        assert bool(torch.isnan(out[0, 1, 2]).all())
+    rest = torch.ones(out.shape[:3], dtype=torch.bool, device=out.device)
+    rest[0, 1, 2] = False
+    assert torch.equal(out[rest], want[rest]) and torch.equal(lse[rest], want_lse[rest])
+
+
 def test_prompts_in_parts_in_a_graph():
     a = make(2, 4, 2, 200, 128, 16, [4000, 3000], seed=83)
     out, lse = torch.empty_like(a["q"]), torch.empty(a["q"].shape[:3], device=dev())

@@ -54,7 +54,8 @@
 //    P_{j-1}.  Both waits are on the `empty` barrier of the ring slot that
 //    the product read (K_j, V_{j-1}): its next completion needs P_j or a
 //    later one, so a key thread cannot miss it, and the thread issues two
-//    commits a tile instead of four.
+//    commits a tile instead of four.  (48 rows over a contiguous cache keep
+//    two barriers of their own for the waits: see kOwnBars.)
 //
 // Statistics: every key thread keeps its own partial sums l over its keys
 // for its rows; the reference maxima m (base-2 units) live in shared memory.
@@ -145,8 +146,9 @@ struct TcLayout {
   // of the finished unit whose U readout is pending
   static constexpr int kOffStat = kOffRed + 4 * NR * 4;
   static constexpr int kOffBar = kOffStat + 7 * NR * 4;
-  // full[kSlots], empty[kSlots], q_full[2], q_empty[2], p_full[2], u_full[2], drain
-  static constexpr int kNumBars = 2 * kSlots + 2 + 2 + 2 + 2 + 1;
+  // full[kSlots], empty[kSlots], q_full[2], q_empty[2], p_full[2], u_full[2], drain,
+  // s_full[2], pv_done
+  static constexpr int kNumBars = 2 * kSlots + 2 + 2 + 2 + 2 + 1 + 2 + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kBytes = kOffMisc + 128 + 1024;  // + slack to align to 1024
   static_assert(kOffQ % 1024 == 0 && kQBox % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
@@ -304,6 +306,11 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
   // V^T, P^T both MN-major; N spans the P_hi atom (NR used of 64) and the P_lo atom
   constexpr uint32_t kIdescPV = tc::idesc_bf16(D, L::kPVN, 1, 1);
   constexpr int kSlots = L::kSlots;
+  // The scores' and the value product's completion by barriers of their own
+  // instead of the ring slots': 48 rows with a bias (5-row chains of 8 heads)
+  // 104.3 us with the slots', 99.9 with these; 48-row trees the same within
+  // 0.5 us; 16-row windows 55.3 and 57.3, so fewer rows use the slots'.
+  constexpr bool kOwnBars = !PAGED && NR >= 48;
   // weight-only tiles per unit in the partition (its set-up and readout)
   constexpr int kUnitExtra = NR >= 48 ? 2 : 0;  // measured best: 48-row units pay a real set-up cost
   constexpr int kPBytes = L::kPBytes;
@@ -332,6 +339,8 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
   uint64_t* p_full = q_empty + 2;     // [2] by tile parity
   uint64_t* u_full = p_full + 2;      // [2] by unit parity
   uint64_t* drain = u_full + 2;
+  uint64_t* s_full = drain + 1;       // [2] by tile parity (kOwnBars)
+  uint64_t* pv_done = s_full + 2;     // once per U += P V product (kOwnBars)
   // misc: [0] tmem base, [1] error seen by the producer / MMA thread,
   // [2] abort of the key threads, [3] "this CTA folds the unit" (both
   // written before a barrier of the key threads, read after it)
@@ -397,8 +406,10 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
         mbar_init(&u_full[x], 1);
       }
       for (int x = 0; x < 2; ++x) {
+        mbar_init(&s_full[x], 1);
         mbar_init(&p_full[x], kKeyWarps);  // one arrival per key warp
       }
+      mbar_init(pv_done, 1);
       mbar_init(drain, 1);
       fence_barrier_init();
     }
@@ -830,6 +841,7 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
           const uint64_t bdesc = tc::desc_join(qlo + (uint32_t)(((ks >> 2) * L::kQBox + (ks & 3) * 32) >> 4), kHi);
           tc::mma_ss(tb + kColS + 64u * buf, adesc, bdesc, kIdescQK, ks > 0 ? 1u : 0u);
         }
+        if (kOwnBars) tc::commit(&s_full[buf]);
         tc::commit(&empty[ks_slot]);  // K_j is free and S_j is ready
         first_q = false;
         if (--left_q == 0) {
@@ -866,6 +878,7 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
           tc::mma_ss(ucol, adesc, bdesc, kIdescPV, (!first || ks > 0) ? 1u : 0u);
         }
         tc::commit(&empty[vs_slot]);
+        if (kOwnBars) tc::commit(pv_done);
         first = false;
         p_phase ^= buf;
         buf ^= 1u;
@@ -1086,7 +1099,7 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
         for (int r = 0; r < NH; ++r)
           x[r] = kin ? __ldg(p.bias + rf.boff[c0 + r] + (int64_t)key * p.bi_sj) : 0.f;
       }
-      const bool sok = wait_all(&empty[kslot], kphase);
+      const bool sok = kOwnBars ? wait_all(&s_full[g & 1], (uint32_t)((g >> 1) & 1)) : wait_all(&empty[kslot], kphase);
       bool trig = !sok;
       if (sok) {
         tc::fence_after();
@@ -1189,7 +1202,9 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
           // product with P_{j-1} must have completed (U += P_j V_j waits for
           // this tile's P)
           const int64_t pv_seq = 2 * g - 1;  // V_{j-1}
-          const bool pv = bar_and(kBarRows, kKeyThreads, wait_all(&empty[pv_seq % kSlots], (uint32_t)((pv_seq / kSlots) & 1)));
+          const bool done = kOwnBars ? wait_all(pv_done, (uint32_t)((g - 1) & 1))
+                                     : wait_all(&empty[pv_seq % kSlots], (uint32_t)((pv_seq / kSlots) & 1));
+          const bool pv = bar_and(kBarRows, kKeyThreads, done);
           if (!pv) { ok = false; break; }
           tc::fence_after();
           const uint32_t ua = tl + kColU + 128u * (uint32_t)ub + c0;

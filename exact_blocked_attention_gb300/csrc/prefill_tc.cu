@@ -735,6 +735,9 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
         }
       } else {
         tc::fence_after();
+        // (over pages a NaN score, which no maximum shows where the tile's other
+        // keys are masked, makes the row NaN instead of empty)
+        if (PAGED && l != l) m_ref = l;
         const float inv = PAGED && parts > 1 ? 1.f : ((m_ref == kNegInf) ? 0.f : 1.f / l);
         if ((p.o_tma && !WIN) || (PAGED && parts > 1)) {
           // (fp32 rows of the output, or of a split item's partial U)

@@ -1,0 +1,42 @@
+"""A query row of NaN over the paged cache: its output and its lse are NaN
+wherever its keys are cut and masked, and the other rows keep their bits."""
+import math
+
+import pytest
+import torch
+
+from exact_blocked_attention_gb300 import blkattn
+
+from test_gpu_paged import BF16, call, make
+
+pytestmark = pytest.mark.gpu
+
+
+def nan_rows_stay_nan(a, rows):
+    """rows: (sequence, head, row) one after another."""
+    want, want_lse = call(a)
+    for b, h, i in rows:
+        keep = a["q"][b, h, i].clone()
+        a["q"][b, h, i] = math.nan
+        out, lse = call(a)
+        assert blkattn.check_device_error() == 0
+        assert bool(torch.isnan(out[b, h, i]).all()), (b, h, i, out[b, h, i])
+        assert bool(torch.isnan(lse[b, h, i])), (b, h, i, lse[b, h, i])
+        rest = torch.ones(out.shape[:3], dtype=torch.bool, device=out.device)
+        rest[b, h, i] = False
+        assert torch.equal(out[rest], want[rest]) and torch.equal(lse[rest], want_lse[rest])
+        a["q"][b, h, i] = keep
+
+
+# rows whose keys lie in a partly masked key tile only, and rows that also see
+# whole ones; whole items and (with a table much longer than the sequences)
+# items in parts
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("window", [0, 90])
+@pytest.mark.parametrize("Tq,lens,entries", [(100, [100], None), (100, [100], 190), (300, [300, 700], 190),
+                                             (300, [900, 301], None), (70, [3000, 70], 200)])
+def test_prompt_rows(Tq, lens, entries, window, d):
+    a = make(len(lens), 4, 2, Tq, d, 16, lens, BF16, seed=7, entries=entries)
+    a["window"] = window
+    last = len(lens) - 1
+    nan_rows_stay_nan(a, [(0, 1, 0), (0, 1, 5), (last, 2, Tq - 1), (last, 3, Tq // 2)])

@@ -1056,7 +1056,10 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
 #pragma unroll
             for (int x2 = 0; x2 < 2; ++x2) {
               if (!live[x2]) continue;
-              const float inv = (M[x2] == kNegInf) ? 0.f : 1.f / Ls[x2];
+              // (over pages a part of NaN leaves no trace in the maximum, but in
+              // the sum: such a row is not an empty one)
+              const bool none = M[x2] == kNegInf && !(PAGED && Ls[x2] != Ls[x2]);
+              const float inv = none ? 0.f : 1.f / Ls[x2];
               const float o4[4] = {Us[x2].x * inv, Us[x2].y * inv, Us[x2].z * inv, Us[x2].w * inv};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -1067,7 +1070,7 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
                   static_cast<float*>(p.out)[oi] = o4[e];
               }
               if (d4[x2] == 0)
-                p.lse[pf.loff[row[x2]]] = (M[x2] == kNegInf) ? kNegInf : (M[x2] + __log2f(Ls[x2])) * kLn2;
+                p.lse[pf.loff[row[x2]]] = none ? kNegInf : (M[x2] + __log2f(Ls[x2])) * kLn2;
             }
           }
         }

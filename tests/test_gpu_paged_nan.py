@@ -40,3 +40,13 @@ def test_prompt_rows(Tq, lens, entries, window, d):
     a["window"] = window
     last = len(lens) - 1
     nan_rows_stay_nan(a, [(0, 1, 0), (0, 1, 5), (last, 2, Tq - 1), (last, 3, Tq // 2)])
+
+
+# units that one CTA finishes, that their last CTA folds (26 or more of them)
+# and that a second kernel joins
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("B,Hq,Hkv,Tq,lens", [(1, 4, 1, 1, [40]), (4, 32, 8, 1, [3000, 2000, 3000, 100]),
+                                              (1, 8, 2, 3, [3000]), (4, 64, 8, 5, [2500] * 4)])
+def test_decode_rows(B, Hq, Hkv, Tq, lens, d):
+    a = make(B, Hq, Hkv, Tq, d, 16, lens, BF16, seed=11)
+    nan_rows_stay_nan(a, [(0, 0, 0), (B - 1, Hq - 1, Tq - 1), (B - 1, 1, 0)])

@@ -387,6 +387,11 @@ __global__ void __launch_bounds__((NW + (PAGED ? 0 : 1)) * 32, PAGED ? 3 : 1)
           l_lane[r] = fmaf(l_lane[r], alpha, pr[r]);
 #pragma unroll
           for (int e = 0; e < DPL; ++e) u[r][e] *= alpha;
+        } else if (PAGED && s[r] != s[r]) {
+          // a NaN score, which no maximum shows beside masked keys: the row is
+          // not an empty one
+          pr[r] = s[r];
+          l_lane[r] = s[r];
         }
       }
       float* pw = p_s + warp * KPW * R;
@@ -431,6 +436,7 @@ __global__ void __launch_bounds__((NW + (PAGED ? 0 : 1)) * 32, PAGED ? 3 : 1)
 #pragma unroll
       for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
       l_lane[r] = l;
+      if (PAGED && l != l) m_run[r] = l;
     }
   }
 
@@ -483,7 +489,10 @@ __global__ void __launch_bounds__((NW + (PAGED ? 0 : 1)) * 32, PAGED ? 3 : 1)
     if (k0 >= rend && split != 0) continue;
     float M = kNegInf;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) M = fmaxf(M, red_m[w * R + r]);
+    for (int w = 0; w < NW; ++w) {
+      const float mw = red_m[w * R + r];
+      M = PAGED && (mw != mw || M != M) ? mw + M : fmaxf(M, mw);  // (NaN stays)
+    }
     float Ls = 0.f, Us = 0.f;
     if (M != kNegInf) {
 #pragma unroll

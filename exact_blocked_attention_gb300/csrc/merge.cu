@@ -67,22 +67,20 @@ __global__ void __launch_bounds__(kMergeWarps * 32) split_merge_kernel(const Fwd
   float U[DPL];
 #pragma unroll
   for (int e = 0; e < DPL; ++e) U[e] = 0.f;
-  if (M != kNegInf) {
 #pragma unroll 4
-    for (int s = warp; s < n_active; s += kMergeWarps) {
-      const float ms = wm[s];
-      if (ms == kNegInf) continue;  // an empty state contributes nothing
-      const float c = fast_exp2(ms - M);
-      Ls = fmaf(c, wl[s], Ls);
-      const float* us = wu + (int64_t)s * D + lane * DPL;
-      if constexpr (DPL == 4) {
-        const float4 u4 = *reinterpret_cast<const float4*>(us);
-        U[0] = fmaf(c, u4.x, U[0]); U[1] = fmaf(c, u4.y, U[1]);
-        U[2] = fmaf(c, u4.z, U[2]); U[3] = fmaf(c, u4.w, U[3]);
-      } else {
+  for (int s = warp; s < n_active; s += kMergeWarps) {
+    const float ms = wm[s];
+    if (ms == kNegInf) continue;  // an empty state contributes nothing
+    const float c = fast_exp2(ms - M);
+    Ls = fmaf(c, wl[s], Ls);
+    const float* us = wu + (int64_t)s * D + lane * DPL;
+    if constexpr (DPL == 4) {
+      const float4 u4 = *reinterpret_cast<const float4*>(us);
+      U[0] = fmaf(c, u4.x, U[0]); U[1] = fmaf(c, u4.y, U[1]);
+      U[2] = fmaf(c, u4.z, U[2]); U[3] = fmaf(c, u4.w, U[3]);
+    } else {
 #pragma unroll
-        for (int e = 0; e < DPL; ++e) U[e] = fmaf(c, us[e], U[e]);
-      }
+      for (int e = 0; e < DPL; ++e) U[e] = fmaf(c, us[e], U[e]);
     }
   }
   if (lane == 0) red_l[warp] = Ls;
@@ -94,11 +92,13 @@ __global__ void __launch_bounds__(kMergeWarps * 32) split_merge_kernel(const Fwd
   float L = 0.f;
 #pragma unroll
   for (int w = 0; w < kMergeWarps; ++w) L += red_l[w];
+  // (a state of NaN leaves no trace in the maximum, but in the sum)
+  const bool none = M == kNegInf && L == L;
   for (int d = threadIdx.x; d < D; d += kMergeWarps * 32) {
     float u = 0.f;
 #pragma unroll
     for (int w = 0; w < kMergeWarps; ++w) u += red_u[w][d];
-    const float o = (M == kNegInf) ? 0.f : u / L;
+    const float o = none ? 0.f : u / L;
     const int64_t oi = ob + (int64_t)d * p.o_sd;
     if (p.out_bf16)
       static_cast<__nv_bfloat16*>(p.out)[oi] = __float2bfloat16_rn(o);
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) split_merge_kernel(const Fwd
   }
   if (threadIdx.x == 0)
     p.lse[(int64_t)b * p.l_sb + (int64_t)h * p.l_sh + (int64_t)i * p.l_si] =
-        (M == kNegInf) ? kNegInf : (M + __log2f(L)) * kLn2;
+        none ? kNegInf : (M + __log2f(L)) * kLn2;
 }
 
 // Public merge of two states per row (natural-log m).  One warp per row.

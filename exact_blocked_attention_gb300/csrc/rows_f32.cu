@@ -264,7 +264,9 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, RT>::kBlocks) rows_f32
       float mt = fmaxf(x0, x1);
 #pragma unroll
       for (int off = 8; off >= 1; off >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
-      float p0 = 0.f, p1 = 0.f;
+      // (a NaN score, which no maximum shows beside masked keys, is a weight of
+      // NaN: the row is not an empty one)
+      float p0 = x0 != x0 ? x0 : 0.f, p1 = x1 != x1 ? x1 : 0.f;
       if (mt != kNegInf) {  // this block has a valid key for the row
         const float m_new = fmaxf(m[r], mt);
         if (m_new != m[r]) {
@@ -276,8 +278,8 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, RT>::kBlocks) rows_f32
         }
         p0 = fast_exp2(x0 - m_new);  // (masked: 2^-inf = 0)
         p1 = fast_exp2(x1 - m_new);
-        l[r] += p0 + p1;
       }
+      l[r] += p0 + p1;
       p_s[(ty * RT + r) * kPRow + j0] = p0;
       p_s[(ty * RT + r) * kPRow + j0 + 4] = p1;
     }
@@ -316,6 +318,7 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, RT>::kBlocks) rows_f32
   for (int r = 0; r < RT; ++r) {
 #pragma unroll
     for (int off = 8; off >= 1; off >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], off);
+    if (l[r] != l[r]) m[r] = l[r];
     const int row = ty * RT + r;
     if (row >= rows) continue;
     const int pk = pk0 + row, g = pk / p.Tq, i = pk - g * p.Tq, h = hk * p.G + g;

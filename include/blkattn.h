@@ -432,6 +432,8 @@ int blkattn_paged_append(const blkattn_tensor* k, const blkattn_tensor* v, const
  * not followed.  The K and V rows between the earliest and the latest key
  * that query rows of one sequence see must be finite, except tree nodes that
  * no row lists; every other row of the pools may hold anything.
+ * A row with a NaN among the scores of its visible keys gives NaN in out and
+ * lse; the other rows are not touched by it.
  * Kernels: bf16 prompts (T_q >= 64, no tree, scale > 0; where the decode
  * kernel would not be faster) and bf16 decode and verify rows (d = 64 or 128)
  * run on tcgen05 when the query rows are contiguous and 16-byte aligned; the

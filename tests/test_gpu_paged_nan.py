@@ -7,7 +7,7 @@ import torch
 
 from exact_blocked_attention_gb300 import blkattn
 
-from test_gpu_paged import BF16, call, make
+from test_gpu_paged import BF16, F32, call, dev, make
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +50,24 @@ def test_prompt_rows(Tq, lens, entries, window, d):
 def test_decode_rows(B, Hq, Hkv, Tq, lens, d):
     a = make(B, Hq, Hkv, Tq, d, 16, lens, BF16, seed=11)
     nan_rows_stay_nan(a, [(0, 0, 0), (B - 1, Hq - 1, Tq - 1), (B - 1, 1, 0)])
+
+
+# up to 8 rows a KV head and more of them; rows in one split and in several,
+# that end inside a key tile, on its edge and behind it
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("window", [0, 20])
+@pytest.mark.parametrize("Hq,Hkv,Tq", [(2, 2, 1), (4, 2, 3), (8, 2, 3), (2, 1, 20), (4, 1, 60)])
+@pytest.mark.parametrize("n,entries", [(60, None), (64, None), (65, 300), (900, None), (3001, None)])
+def test_f32_rows(Hq, Hkv, Tq, n, entries, window, d):
+    a = make(2, Hq, Hkv, Tq, d, 16, [n, 60], F32, seed=13, entries=entries)
+    a["window"] = window
+    nan_rows_stay_nan(a, [(0, 0, 0), (0, Hq - 1, Tq - 1), (1, 1, Tq // 2)])
+
+
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("n", [9, 64, 1000])
+def test_bf16_rows_without_alignment(n, d):
+    a = make(1, 4, 2, 3, d, 16, [n], BF16, seed=17)
+    q = torch.zeros(1, 4, 3, d + 3, dtype=BF16, device=dev())[..., 1:d + 1]
+    q.copy_(a["q"])
+    nan_rows_stay_nan(dict(a, q=q), [(0, 0, 0), (0, 3, 2)])

@@ -948,12 +948,12 @@ int fwd_paged_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages_, con
   } else if (on_cuda_cores(pl) && pl.cfg.row_groups > 65535) {
     return BLKATTN_ERR_UNSUPPORTED;
   }
-  // (every part leaves 256 rows of m, l and u)
+  // (every part leaves 256 rows of m, both sums and u)
   const int64_t part_rows = (pp.items - pp.split_from) * pp.parts * 256;
   if (pl.cfg.kernel == blkattn::Kernel::Prefill) {
     pl.split_from = pp.split_from;
     pl.cfg.n_splits = pp.parts;
-    if (pp.parts > 1) pl.ws_bytes = part_rows * (2 + c.d) * 4;
+    if (pp.parts > 1) pl.ws_bytes = part_rows * (3 + c.d) * 4;
   }
   // (the last slice has a plan of its own; scratch for both, before any launch)
   const int64_t rest = c.B % nb;
@@ -1007,7 +1007,7 @@ int fwd_paged_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages_, con
       p.split_from = (int)ps.split_from;
       p.ws_m = static_cast<float*>(ds->ws);
       p.ws_l = p.ws_m + part_rows;
-      p.ws_u = p.ws_l + part_rows;
+      p.ws_u = p.ws_l + 2 * part_rows;
       le = blkattn::launch_prefill_tc_paged(p, (int)c.d, ps.cfg.row_groups, mq, mk, mv, mo, stream);
     } else if (ps.cfg.kernel == blkattn::Kernel::DecodeTc) {
       // few units of many parts: at least six each, if the lengths are the table's

@@ -63,6 +63,7 @@ struct FwdParams {
   // prefill over pages: the items (256 rows of a head, in dispatch order) from
   // this one on are split into n_splits parts along their keys; row r of part
   // s of item i leaves its state at index ((i - split_from) n_splits + s) 256 + r
+  // (ws_l: pairs of the sums of the rounded and of the unrounded weights)
   int split_from;
   // tcgen05 decode kernel: query rows per unit (one row group of one KV head);
   // the partial state of unit row r from CTA c sits in slot c + unit, at

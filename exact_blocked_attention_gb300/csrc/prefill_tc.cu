@@ -106,6 +106,16 @@ __device__ __forceinline__ uint64_t policy_evict_last() {
   return pol;
 }
 
+// a += the two bf16 of w (low half first), exactly widened by the addition.
+__device__ __forceinline__ void add_bf16x2(float2& a, uint32_t w) {
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "mov.b32 {lo, hi}, %2;\n\t"
+      "add.f32.bf16 %0, lo, %0;\n\t"
+      "add.f32.bf16 %1, hi, %1;\n\t}"
+      : "+f"(a.x), "+f"(a.y)
+      : "r"(w));
+}
+
 // The first key tile of a CTA whose first row is at position q0 under a
 // sliding window (rows at their own index, the prefill layout).
 __device__ __forceinline__ int spec_first_tile(int q0, int window) {
@@ -548,6 +558,7 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
       const uint32_t tl = tb + x * kTileCols + ((uint32_t)(32 * (warp & 3)) << 16);  // lane quarter
       float m_ref = kNegInf;  // reference maximum (base-2 units), -inf = no valid key yet
       float l = 0.f;
+      float lx = 0.f;  // PAGED: the sum of the weights before any rounding, for lse
       bool ok = true;
       // waits are made warp-uniform: the tensor-memory accesses that follow
       // are warp-collective
@@ -626,6 +637,7 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
             alpha = fast_exp2(m_ref - mt);
             m_ref = mt;
             l *= alpha;
+            if (PAGED) lx *= alpha;
             resc = true;
           }
         }
@@ -649,9 +661,12 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
         const float2 nm2 = make_float2(-m_use, -m_use);
         const float2 neg1 = make_float2(-1.f, -1.f);
+        // sums of the weights; over pages the first two for l, the others for lx
+        // where the two differ
         float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                         make_float2(0.f, 0.f)};
-        if (split_tile(key0)) {
+        const bool split = split_tile(key0);
+        if (split) {
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) {  // 32 keys -> 16 columns of P_hi and of P_lo
             uint32_t hi[16], lo[16];
@@ -675,9 +690,11 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
         } else {
           // every row sees every key of the tile: P rounded to bf16 (to
           // nearest) is the product's operand, and l sums the rounded values,
-          // so u / l stays a convex combination of the values (over pages l
-          // sums the values before rounding: u / l is as near, and lse keeps
-          // fp32 accuracy)
+          // so u / l stays a convex combination of the values: one key that
+          // holds all the weight gives its value back, whatever its rounding.
+          // Over pages lse takes the sum before the rounding, which keeps it
+          // fp32 accurate (one sum, the unrounded, 361 us for the case above;
+          // both 381, 403 with the halves unpacked by shift and mask)
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) {  // 32 keys -> 16 columns of P
             uint32_t pb[16];
@@ -687,8 +704,13 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
               const float2 e = __ffma2_rn(make_float2(xs[k2], xs[k2 + 1]), sc2, nm2);
               const float2 pp = make_float2(fast_exp2(e.x), fast_exp2(e.y));
               pb[c] = pack_bf16(pp.x, pp.y);
-              ls[c & 3] = __fadd2_rn(ls[c & 3], PAGED ? pp : make_float2(__uint_as_float(pb[c] << 16),
-                                                                         __uint_as_float(pb[c] & 0xffff0000u)));
+              if (PAGED) {
+                add_bf16x2(ls[c & 1], pb[c]);
+                ls[2 + (c & 1)] = __fadd2_rn(ls[2 + (c & 1)], pp);
+              } else {
+                ls[c & 3] = __fadd2_rn(ls[c & 3], make_float2(__uint_as_float(pb[c] << 16),
+                                                              __uint_as_float(pb[c] & 0xffff0000u)));
+              }
             }
             tc::st16(tl + kColS + 16 * q4, pb);
           }
@@ -696,8 +718,15 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
         {
           const float2 a = __fadd2_rn(ls[0], ls[1]);
           const float2 c2 = __fadd2_rn(ls[2], ls[3]);
-          const float2 t2 = __fadd2_rn(a, c2);
-          l += t2.x + t2.y;
+          if (PAGED && !split) {
+            l += a.x + a.y;
+            lx += c2.x + c2.y;
+          } else {
+            const float2 t2 = __fadd2_rn(a, c2);
+            const float t = t2.x + t2.y;
+            l += t;
+            if (PAGED) lx += t;
+          }
         }
         if (key0 + BN > cta_end || (WIN && PAGED && key0 < cta_start)) {
           // last tile of the CTA: zero the V rows past every visible key of
@@ -869,10 +898,10 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
         if (PAGED && parts > 1) {
           if (my_row) {
             p.ws_m[ws_row + threadIdx.x] = m_ref;
-            p.ws_l[ws_row + threadIdx.x] = l;
+            reinterpret_cast<float2*>(p.ws_l)[ws_row + threadIdx.x] = make_float2(l, lx);
           }
         } else if (my_row) {
-          p.lse[lse_idx] = (m_ref == kNegInf) ? kNegInf : (m_ref + __log2f(l)) * kLn2;
+          p.lse[lse_idx] = (m_ref == kNegInf) ? kNegInf : (m_ref + __log2f(PAGED ? lx : l)) * kLn2;
         }
         // the staging buffer is released with the CTA: the stores must have
         // read it (no-op for a lane without stores)
@@ -906,16 +935,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prompt_join_kernel(const FwdP
   const int parts = p.n_splits;  // <= 32
   const int64_t row0 = (int64_t)e * parts * (QT * BM) + r;
   const float m = lane < parts ? p.ws_m[row0 + lane * (QT * BM)] : kNegInf;
-  const float lp = lane < parts ? p.ws_l[row0 + lane * (QT * BM)] : 0.f;
+  const float2 lp = lane < parts ? reinterpret_cast<const float2*>(p.ws_l)[row0 + lane * (QT * BM)]
+                                 : make_float2(0.f, 0.f);  // l, lx
   float M = m;
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
   // a part without a visible key of this row wrote no l and no U: whatever
   // lies there is dropped by select
   const float w = m == kNegInf ? 0.f : fast_exp2(m - M);
-  float l = m == kNegInf ? 0.f : w * lp;
+  float l = m == kNegInf ? 0.f : w * lp.x, lx = m == kNegInf ? 0.f : w * lp.y;
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+  for (int off = 16; off >= 1; off >>= 1) {
+    l += __shfl_xor_sync(0xffffffffu, l, off);
+    lx += __shfl_xor_sync(0xffffffffu, lx, off);
+  }
   float u[DPL];
 #pragma unroll
   for (int c = 0; c < DPL; ++c) u[c] = 0.f;
@@ -969,7 +1002,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prompt_join_kernel(const FwdP
   }
   if (lane == 0)
     p.lse[(int64_t)b * p.l_sb + (int64_t)h * p.l_sh + (int64_t)i * p.l_si] =
-        l == 0.f ? kNegInf : (M + __log2f(l)) * kLn2;
+        l == 0.f ? kNegInf : (M + __log2f(lx)) * kLn2;
 }
 
 }  // namespace

@@ -432,6 +432,11 @@ int blkattn_paged_append(const blkattn_tensor* k, const blkattn_tensor* v, const
  * not followed.  The K and V rows between the earliest and the latest key
  * that query rows of one sequence see must be finite, except tree nodes that
  * no row lists; every other row of the pools may hold anything.
+ * Precision: sums and statistics in fp32.  Weights enter the value product
+ * with 16 bits or more, but for bf16 prompts on the key tiles that every row
+ * of a query tile sees: there with bf16's 8, divided by the sum of what was
+ * rounded, which moves out by at most 2^-8 of sum p |v - out| / sum p, for
+ * every out dtype.  lse does not take part in that rounding.
  * A row with a NaN among the scores of its visible keys gives NaN in out and
  * lse; the other rows are not touched by it.
  * Kernels: bf16 prompts (T_q >= 64, no tree, scale > 0; where the decode

@@ -352,12 +352,11 @@ def paged_append(k, v, pos, page_table, k_pages, v_pages, phases=None, layout="h
     """blkattn_paged_append: rows k, v [B,H_kv,T,d] into the pools [N,H_kv,P,d]
     at the cache rows pos int32 [B,T] (negative: padding, not written) through
     page_table int32 [B,entries]; with phases, k and q turn on the way.
-    Returns q_out (allocated as zeros when q is given without it: rows of
-    padding stay unwritten), or None."""
-    if q is not None and q_out is None:
-        q_out = torch.zeros_like(q, memory_format=torch.contiguous_format)
-    _check((_bind or _load_bind()).append(k, v, pos, page_table, k_pages, v_pages, phases, _layout(layout), mscale, q,
-                                          q_out, _handle(stream))[0])
+    Returns q_out (allocated as zeros, on the call's stream, when q is given
+    without it: rows of padding stay unwritten), or None."""
+    st, q_out = (_bind or _load_bind()).append(k, v, pos, page_table, k_pages, v_pages, phases, _layout(layout), mscale,
+                                               q, q_out, _handle(stream))
+    _check(st)
     return q_out
 
 

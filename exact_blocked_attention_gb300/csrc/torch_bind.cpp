@@ -7,10 +7,16 @@
 // Holds no arithmetic and no state but the entry points' addresses.
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <ATen/ops/zeros.h>
+#include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+#include <cmath>
+#include <optional>
 
 #include "blkattn.h"
 
@@ -68,16 +74,46 @@ at::ScalarType dtype_of(PyObject* o, at::ScalarType otherwise) {
   return reinterpret_cast<THPDtype*>(o)->scalar_type;
 }
 
-// The given handle (an int), or the current stream of t's device.
-blkattn_stream_t stream_of(PyObject* o, const at::Tensor& t) {
-  if (o != Py_None) {
-    void* h = PyLong_AsVoidPtr(o);
-    if (h == nullptr && PyErr_Occurred()) throw python_error();
-    return static_cast<blkattn_stream_t>(h);
+// The stream of a call: the given handle (an int), or the current stream of
+// t's device.
+class CallStream {
+ public:
+  CallStream(PyObject* o, const at::Tensor& t) {
+    const bool given = o != Py_None;
+    if (given) {
+      void* h = PyLong_AsVoidPtr(o);
+      if (h == nullptr && PyErr_Occurred()) throw python_error();
+      handle_ = static_cast<cudaStream_t>(h);
+    }
+    if (!t.is_cuda()) return;  // refused by the library
+    const auto current = c10::cuda::getCurrentCUDAStream(t.get_device());
+    if (!given) handle_ = current.stream();
+    const cudaStream_t plain = handle_ == cudaStreamLegacy ? nullptr : handle_;
+    if (plain != current.stream()) current_ = current;
   }
-  if (!t.is_cuda()) return nullptr;  // refused by the library
-  return reinterpret_cast<blkattn_stream_t>(c10::cuda::getCurrentCUDAStream(t.get_device()).stream());
-}
+  blkattn_stream_t get() const { return reinterpret_cast<blkattn_stream_t>(handle_); }
+
+  // An output of the call.  On a given stream that is not the current one it
+  // is allocated, and filled, on the given one: the current stream's memory
+  // may still be in use there, and a fill there is ordered with nothing.  The
+  // current stream is recorded as a user: that is where the caller reads it.
+  at::Tensor fresh(at::IntArrayRef sizes, const at::TensorOptions& options, bool zeros = false) const {
+    if (!current_) return zeros ? at::zeros(sizes, options) : at::empty(sizes, options);
+    TORCH_CHECK_VALUE(handle_ != cudaStreamPerThread,
+                      "blkattn: torch cannot allocate on the per-thread stream: pass the outputs");
+    const auto device = current_->device_index();
+    const c10::cuda::CUDAStreamGuard guard(handle_ == cudaStreamLegacy
+                                               ? c10::cuda::getDefaultCUDAStream(device)
+                                               : c10::cuda::getStreamFromExternal(handle_, device));
+    at::Tensor t = zeros ? at::zeros(sizes, options) : at::empty(sizes, options);
+    c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), *current_);
+    return t;
+  }
+
+ private:
+  cudaStream_t handle_ = nullptr;
+  std::optional<c10::cuda::CUDAStream> current_;  // where it is another one
+};
 
 double number(PyObject* o) {
   const double x = PyFloat_AsDouble(o);
@@ -138,21 +174,28 @@ PyObject* bind_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (a[3] == Py_None) fresh = at::empty(x.sizes(), x.options().dtype(dtype_of(a[6], x.scalar_type())));
   const Desc y = a[3] == Py_None ? Desc(fresh) : Desc(a[3]);
   const int st = (a[8] == Py_True ? g_rope_bwd : g_rope)(dx.get(), pos.get(), ph.get(), (int32_t)integer(a[4]),
-                                                         (float)number(a[5]), y.get(), stream_of(a[7], x));
+                                                         (float)number(a[5]), y.get(), CallStream(a[7], x).get());
   return answer(st, {a[3] == Py_None ? THPVariable_Wrap(fresh) : again(a[3])});
   END_HANDLE_TH_ERRORS
 }
 
 // append(k, v, pos, table, k_pages, v_pages, phases or None, layout, mscale, q or None, q_out or None,
-//        stream or None) -> (status,)
+//        stream or None) -> (status, q_out: given, made of zeros when q is given without it, or None)
 PyObject* bind_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 12);
   const at::Tensor& k = tensor_of(a[0]);
-  const Desc dk(k), v(a[1]), pos(a[2]), table(a[3]), kp(a[4]), vp(a[5]), ph(a[6]), q(a[9]), qo(a[10]);
-  return answer(g_append(dk.get(), v.get(), pos.get(), table.get(), kp.get(), vp.get(), ph.get(),
-                         (int32_t)integer(a[7]), (float)number(a[8]), q.get(), qo.get(), stream_of(a[11], k)),
-                {});
+  const Desc dk(k), v(a[1]), pos(a[2]), table(a[3]), kp(a[4]), vp(a[5]), ph(a[6]), q(a[9]);
+  const CallStream stream(a[11], k);
+  at::Tensor made;
+  if (q.given() && a[10] == Py_None) {  // (zeros: the rows of padding are not written)
+    const at::Tensor& tq = tensor_of(a[9]);
+    made = stream.fresh(tq.sizes(), tq.options(), true);
+  }
+  const Desc qo = made.defined() ? Desc(made) : Desc(a[10]);
+  const int st = g_append(dk.get(), v.get(), pos.get(), table.get(), kp.get(), vp.get(), ph.get(),
+                          (int32_t)integer(a[7]), (float)number(a[8]), q.get(), qo.get(), stream.get());
+  return answer(st, {made.defined() ? THPVariable_Wrap(made) : again(a[10])});
   END_HANDLE_TH_ERRORS
 }
 
@@ -171,7 +214,7 @@ PyObject* bind_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Desc dlse = a[10] == Py_None ? Desc(lse) : Desc(a[10]);
   const float scale = a[8] == Py_None ? (float)(1.0 / std::sqrt((double)q.size(3))) : (float)number(a[8]);
   const int st = g_fwd(dq.get(), kp.get(), vp.get(), table.get(), sl.get(), qp.get(), tree.get(), integer(a[7]),
-                       scale, dout.get(), dlse.get(), stream_of(a[12], q));
+                       scale, dout.get(), dlse.get(), CallStream(a[12], q).get());
   return answer(st, {a[9] == Py_None ? THPVariable_Wrap(out) : again(a[9]),
                      a[10] == Py_None ? THPVariable_Wrap(lse) : again(a[10])});
   END_HANDLE_TH_ERRORS

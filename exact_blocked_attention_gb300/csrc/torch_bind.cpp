@@ -170,12 +170,13 @@ PyObject* bind_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   count(n, 9);
   const at::Tensor& x = tensor_of(a[0]);
   const Desc dx(x), pos(a[1]), ph(a[2]);
-  at::Tensor fresh;
-  if (a[3] == Py_None) fresh = at::empty(x.sizes(), x.options().dtype(dtype_of(a[6], x.scalar_type())));
-  const Desc y = a[3] == Py_None ? Desc(fresh) : Desc(a[3]);
+  const CallStream stream(a[7], x);
+  at::Tensor made;
+  if (a[3] == Py_None) made = stream.fresh(x.sizes(), x.options().dtype(dtype_of(a[6], x.scalar_type())));
+  const Desc y = made.defined() ? Desc(made) : Desc(a[3]);
   const int st = (a[8] == Py_True ? g_rope_bwd : g_rope)(dx.get(), pos.get(), ph.get(), (int32_t)integer(a[4]),
-                                                         (float)number(a[5]), y.get(), CallStream(a[7], x).get());
-  return answer(st, {a[3] == Py_None ? THPVariable_Wrap(fresh) : again(a[3])});
+                                                         (float)number(a[5]), y.get(), stream.get());
+  return answer(st, {made.defined() ? THPVariable_Wrap(made) : again(a[3])});
   END_HANDLE_TH_ERRORS
 }
 
@@ -207,14 +208,15 @@ PyObject* bind_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor& q = tensor_of(a[0]);
   const Desc dq(q), kp(a[1]), vp(a[2]), table(a[3]), sl(a[4]), qp(a[5]), tree(a[6]);
   TORCH_CHECK_VALUE(q.dim() == 4, "blkattn: q is [B, H_q, T_q, d]");
+  const CallStream stream(a[12], q);
   at::Tensor out, lse;
-  if (a[9] == Py_None) out = at::empty(q.sizes(), q.options().dtype(dtype_of(a[11], at::kFloat)));
-  if (a[10] == Py_None) lse = at::empty(q.sizes().slice(0, 3), q.options().dtype(at::kFloat));
+  if (a[9] == Py_None) out = stream.fresh(q.sizes(), q.options().dtype(dtype_of(a[11], at::kFloat)));
+  if (a[10] == Py_None) lse = stream.fresh(q.sizes().slice(0, 3), q.options().dtype(at::kFloat));
   const Desc dout = a[9] == Py_None ? Desc(out) : Desc(a[9]);
   const Desc dlse = a[10] == Py_None ? Desc(lse) : Desc(a[10]);
   const float scale = a[8] == Py_None ? (float)(1.0 / std::sqrt((double)q.size(3))) : (float)number(a[8]);
   const int st = g_fwd(dq.get(), kp.get(), vp.get(), table.get(), sl.get(), qp.get(), tree.get(), integer(a[7]),
-                       scale, dout.get(), dlse.get(), CallStream(a[12], q).get());
+                       scale, dout.get(), dlse.get(), stream.get());
   return answer(st, {a[9] == Py_None ? THPVariable_Wrap(out) : again(a[9]),
                      a[10] == Py_None ? THPVariable_Wrap(lse) : again(a[10])});
   END_HANDLE_TH_ERRORS

@@ -50,3 +50,65 @@ def test_append_without_q_out():
     torch.cuda.synchronize()
     again = torch.empty_like(want)
     assert blkattn.paged_append(*a, q_out=again, stream=s.cuda_stream, **kw) is again
+
+
+def rope_call(seed=3):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(2, 8, 100, 64, generator=g).to(dev())
+    pos = torch.arange(100, dtype=torch.int32, device=dev()).repeat(2, 1)
+    ph = blkattn.rope_phases(blkattn.rope_angles(64)[0])
+    return lambda **kw: (blkattn.rope(x, pos, ph, **kw),)
+
+
+def rope_backward_call(seed=4):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(2, 8, 100, 64, generator=g).to(dev())
+    pos = torch.arange(100, dtype=torch.int32, device=dev()).repeat(2, 1)
+    ph = blkattn.rope_phases(blkattn.rope_angles(64)[0])
+    return lambda **kw: (blkattn.rope_backward(x, pos, ph, **kw),)
+
+
+def paged_call(seed=5):
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn(2, 8, 30, 64, generator=g).to(dev())
+    kp, vp = (torch.randn(20, 2, 16, 64, generator=g).to(dev()) for _ in range(2))
+    table = torch.randperm(20, generator=g).to(torch.int32).reshape(2, 10).to(dev())
+    lens = torch.full((2,), 150, dtype=torch.int32, device=dev())
+    pos = torch.arange(120, 150, dtype=torch.int32, device=dev()).repeat(2, 1)
+    return lambda **kw: blkattn.attention_paged(q, kp, vp, table, lens, pos, **kw)
+
+
+CALLS = [rope_call, rope_backward_call, paged_call]
+
+
+@pytest.mark.parametrize("problem", CALLS)
+def test_outputs_are_not_memory_that_the_current_stream_still_uses(problem):
+    call = problem()
+    want = call()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    busy = [torch.empty_like(t) for t in want]
+    lag()
+    for t in busy:
+        t.fill_(7.0)  # queued behind the lag
+    del busy, t       # free for the current stream, not for another
+    got = call(stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("problem", CALLS)
+def test_outputs_are_kept_for_the_current_stream_s_reads(problem):
+    first, second = problem(), problem(seed=77)
+    want = [t.clone() for t in first()]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = first(stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    lag()
+    read = [t.clone() for t in got]  # queued behind the lag
+    del got
+    later = second(stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(read, want))
+    assert all(torch.equal(a, b) for a, b in zip(later, second()))

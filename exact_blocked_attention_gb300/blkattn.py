@@ -189,6 +189,29 @@ def _stream_handle(stream) -> int | None:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _outputs(stream, *specs):
+    """Outputs of a call, one for each (shape, dtype, device), on the call's
+    stream: where that is not the current one, they are allocated on it (the
+    current stream's memory may still be in use there) and the current stream
+    is recorded as a reader."""
+    device = specs[0][2]
+    other = False
+    if stream is not None and device.type == "cuda":
+        current = torch.cuda.current_stream(device)
+        handle = _stream_handle(stream)
+        handle = 0 if handle == 1 else handle  # (the legacy stream is the default one)
+        other = handle != current.cuda_stream
+    if not other:
+        return [torch.empty(shape, dtype=dtype, device=dev) for shape, dtype, dev in specs]
+    if handle == 2:
+        raise ValueError("blkattn: torch cannot allocate on the per-thread stream: pass the outputs")
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
+        outs = [torch.empty(shape, dtype=dtype, device=dev) for shape, dtype, dev in specs]
+    for t in outs:
+        t.record_stream(current)
+    return outs
+
+
 def _ref(x):
     return None if x is None else ctypes.byref(x)
 
@@ -244,9 +267,7 @@ def attention_backward(q, k, v, seqlens_k, q_logical_pos, out, lse, dout, mask_b
     """Allocate fp32 dq, dk, dv and call bwd (scale defaults to 1/sqrt(d))."""
     if scale is None:
         scale = q.shape[-1] ** -0.5
-    dq = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-    dk = torch.empty(k.shape, dtype=torch.float32, device=k.device)
-    dv = torch.empty(v.shape, dtype=torch.float32, device=v.device)
+    dq, dk, dv = _outputs(stream, *((t.shape, torch.float32, t.device) for t in (q, k, v)))
     return bwd(q, k, v, seqlens_k, q_logical_pos, mask_bias, scale, out, lse, dout, dq, dk, dv, stream, window=window)
 
 
@@ -274,8 +295,7 @@ def attention(q, k, v, seqlens_k, q_logical_pos, mask_bias=None, scale=None,
     B, Hq, Tq, d = q.shape
     if scale is None:
         scale = d ** -0.5
-    out = torch.empty((B, Hq, Tq, v.shape[3]), dtype=out_dtype, device=q.device)
-    lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=q.device)
+    out, lse = _outputs(stream, ((B, Hq, Tq, v.shape[3]), out_dtype, q.device), ((B, Hq, Tq), torch.float32, q.device))
     return fwd(q, k, v, seqlens_k, q_logical_pos, mask_bias, scale, out, lse, stream, tree=tree, window=window)
 
 
@@ -286,9 +306,9 @@ def spec_sample(p, q, draft, u_accept, u_sample, n_accepted=None, token=None, st
     lib = load()
     B = p.shape[0]
     if n_accepted is None:
-        n_accepted = torch.empty(B, dtype=torch.int32, device=p.device)
+        n_accepted, = _outputs(stream, ((B,), torch.int32, p.device))
     if token is None:
-        token = torch.empty(B, dtype=torch.int32, device=p.device)
+        token, = _outputs(stream, ((B,), torch.int32, p.device))
     descs = [describe(t) for t in (p, q, draft, u_accept, u_sample, n_accepted, token)]
     _check(lib.blkattn_spec_sample(*[_ref(d) for d in descs], _stream_handle(stream) if p.is_cuda else None))
     return n_accepted, token

@@ -78,7 +78,34 @@ def paged_call(seed=5):
     return lambda **kw: blkattn.attention_paged(q, kp, vp, table, lens, pos, **kw)
 
 
-CALLS = [rope_call, rope_backward_call, paged_call]
+def contiguous_call(seed=6):
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn(2, 8, 30, 64, generator=g).to(dev())
+    k, v = (torch.randn(2, 2, 150, 64, generator=g).to(dev()) for _ in range(2))
+    lens = torch.full((2,), 150, dtype=torch.int32, device=dev())
+    pos = torch.arange(120, 150, dtype=torch.int32, device=dev()).repeat(2, 1)
+    return lambda **kw: blkattn.attention(q, k, v, lens, pos, **kw)
+
+
+def backward_call(seed=7):
+    g = torch.Generator().manual_seed(seed)
+    q, k, v, do = (torch.randn(1, 2, 130, 128, generator=g).to(BF16).to(dev()) for _ in range(4))
+    lens = torch.full((1,), 130, dtype=torch.int32, device=dev())
+    pos = torch.arange(130, dtype=torch.int32, device=dev()).repeat(1, 1)
+    out, lse = blkattn.attention(q, k, v, lens, pos)
+    return lambda **kw: blkattn.attention_backward(q, k, v, lens, pos, out, lse, do, **kw)
+
+
+def sample_call(seed=8):
+    g = torch.Generator().manual_seed(seed)
+    p, q = (torch.softmax(torch.randn(4, n, 500, generator=g), -1).to(dev()) for n in (4, 3))
+    draft = torch.randint(0, 500, (4, 3), generator=g).to(torch.int32).to(dev())
+    ua = torch.rand(4, 3, generator=g).to(dev())
+    us = torch.randint(-2 ** 31, 2 ** 31, (4,), generator=g).to(torch.int32).to(dev())
+    return lambda **kw: blkattn.spec_sample(p, q, draft, ua, us, **kw)
+
+
+CALLS = [rope_call, rope_backward_call, paged_call, contiguous_call, backward_call, sample_call]
 
 
 @pytest.mark.parametrize("problem", CALLS)

@@ -10,8 +10,9 @@
 // angles come as phases F_i = round(2^64 w_i / 2 pi): the product t F_i mod
 // 2^64 is t w_i in units of 2^-64 turns with whole turns dropped, exactly, so
 // a position near 2^31 loses no more than one near 0 (the table's rounding
-// grows to |t| 2^-63 turns).  Its top 32 bits as a float go to
-// sincospif: the angle is off by at most 2^-24 of itself (|angle| <= pi).
+// grows to |t| 2^-65 turns).  Its top 32 bits as a float go to sincospif: the
+// bits dropped are less than 2^-32 turns, and the float is off by at most
+// 2^-24 of the angle (|angle| <= pi).
 // All arithmetic is fp32; the only rounding to fewer bits is the store.
 //
 // One kernel serves every operator: up to three row sets (append: k, v, q)
@@ -481,15 +482,17 @@ int blkattn_rope_phases(const double* angles, int64_t n, int64_t* phases) {
   if (n < 0 || (n > 0 && (angles == nullptr || phases == nullptr))) return BLKATTN_ERR_INVALID_ARG;
   for (int64_t i = 0; i < n; ++i)
     if (!(std::fabs(angles[i]) <= 8.0)) return BLKATTN_ERR_INVALID_ARG;
-  // 2^66 / (2 pi) rounded down, as 64 + 64 bits below the point
-  constexpr uint64_t kTurnHi = 0xA2F9836E4E441529ull;
+  // 2^66 / (2 pi) = 2^64 * 2 / pi rounded down: 64 bits and 64 below the point
+  constexpr uint64_t kTurnHi = 0xA2F9836E4E441529ull, kTurnLo = 0xFC2757D1F534DDC0ull;
   for (int64_t i = 0; i < n; ++i) {
     int e = 0;
     const double m = std::frexp(std::fabs(angles[i]), &e);  // angle = m 2^e, m in [1/2, 1)
     const uint64_t M = (uint64_t)std::ldexp(m, 53);         // exact: 53 bits
-    // angle 2^64 / (2 pi) = M 2^(e - 53) * 2^64 * (kTurnHi 2^-66)
-    const unsigned __int128 prod = (unsigned __int128)M * kTurnHi;  // below 2^117
-    const int sh = 55 - e;  // phase = prod 2^-sh; at least 51 for the angles allowed
+    // angle 2^64 / (2 pi) = M 2^(e - 53) * 2^64 * (kTurnHi + kTurnLo 2^-64) 2^-66;
+    // the product's whole part decides the rounding
+    const unsigned __int128 prod =
+        (unsigned __int128)M * kTurnHi + (((unsigned __int128)M * kTurnLo) >> 64);  // below 2^117
+    const int sh = 55 - e;  // phase = prod 2^-sh, rounded; at least 51 for the angles allowed
     const uint64_t f = sh > 118 ? 0 : (uint64_t)((prod + ((unsigned __int128)1 << (sh - 1))) >> sh);
     phases[i] = (int64_t)(angles[i] < 0.0 ? 0 - f : f);
   }

@@ -322,8 +322,8 @@ int blkattn_bwd_window(const blkattn_tensor* q, const blkattn_tensor* k,
  * 2i + 1.  The kernels take the angles as phases, int64 on the device:
  * F_i = round(2^64 w_i / 2 pi) mod 2^64, the turn of one position as a 64-bit
  * fraction; t F_i mod 2^64 drops whole turns exactly, so far positions lose
- * no precision: the angle is off by at most 2^-63 |t| turns for the table and
- * 2^-24 of a half turn for the float that the sine is taken of.
+ * no precision: the angle is off by at most 2^-65 |t| turns for the table, and
+ * by 2^-32 turns and 2^-24 of itself for the float that the sine is taken of.
  */
 enum {
   BLKATTN_ROPE_HALF = 0,
@@ -352,7 +352,7 @@ typedef struct {
  * w_i of a spec and, when mscale is not NULL, the factor on the rotated dims
  * that goes with it (0.1 ln factor + 1 for RAMP, else 1; a caller may pass
  * another to the kernels).  blkattn_rope_phases turns any n angles (|w| <= 8)
- * into phases, each within 2 units of the exact value; the caller copies them to the device once.
+ * into phases, each rounded to the nearest; the caller copies them to the device once.
  * Return BLKATTN_OK or BLKATTN_ERR_INVALID_ARG.
  */
 int blkattn_rope_angles(const blkattn_rope_spec* spec, double* angles, float* mscale);

@@ -2,13 +2,17 @@
 
 Also _torch_bind.so, the marshalling extension of the serving-step operators
 (csrc/torch_bind.cpp, host C++ against the installed torch), beside the nvcc
-jobs.  Each translation unit in csrc/ is compiled in parallel to an object file
+jobs.  The library needs no torch: without one, only the extension is left
+out.  Each translation unit in csrc/ is compiled in parallel to an object file
 under _build/, then linked into exact_blocked_attention_gb300/libblkattn.so.
-Rebuilds only what changed (source or any header newer than its object).
+Rebuilds only what changed (source or any header newer than its object; for
+the extension also another torch or Python than it was built against).
 """
 from __future__ import annotations
 
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import subprocess
 import sys
@@ -44,10 +48,29 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_tag() -> str | None:
+    """The installed torch and Python, as the extension depends on them; None without a torch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:  # (a torch that was not installed as a package)
+        version = "?"
+    return f"torch {version} at {spec.origin}, python {sys.version.split()[0]}"
+
+
 def _build_bind() -> None:
     src = os.path.join(CSRC, "torch_bind.cpp")
-    if not _stale(BIND, [src] + _headers()):
+    tag = _torch_tag()
+    if tag is None:
+        print("no torch here: _torch_bind.so is not built (libblkattn.so does not need it)", file=sys.stderr)
         return
+    stamp = os.path.join(BUILD, "torch_bind.built_for")
+    if not _stale(BIND, [src] + _headers()) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == tag:
+                return
     import sysconfig
 
     import torch
@@ -63,6 +86,8 @@ def _build_bind() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BIND)
+    with open(stamp, "w") as f:
+        f.write(tag)
 
 
 def build(verbose: bool = False, jobs: int | None = None, extra_flags=()) -> str:
@@ -93,7 +118,6 @@ def build(verbose: bool = False, jobs: int | None = None, extra_flags=()) -> str
             for (src, _), err in zip(todo, ex.map(compile_one, todo)):
                 if verbose and err.strip():
                     print(f"[{os.path.basename(src)}]\n{err}", file=sys.stderr)
-        bind.result()
     if todo or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc, *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", tmp]
@@ -101,6 +125,7 @@ def build(verbose: bool = False, jobs: int | None = None, extra_flags=()) -> str
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    bind.result()  # (the library stands, whatever became of the extension)
     return LIB
 
 

@@ -16,6 +16,7 @@
 #include "blkattn.h"
 #include "kernels.h"
 #include "paged.h"
+#include "scratch.h"
 
 namespace {
 
@@ -418,18 +419,27 @@ bool out_tma_ok(const blkattn_tensor* out) {
 // stream order (cudaMallocAsync), so no call synchronises the device.  A
 // buffer that was outgrown is kept, not freed: graphs captured while it was
 // the current one hold its address and may be replayed at any time.  Growth
-// at least doubles, so what is kept never exceeds the current buffer.
+// doubles where memory allows (scratch.h), so that what is kept does not exceed
+// the current buffer.
 // Growing while the stream is being captured is refused (a capture may not
 // allocate).
 int grow_stream_ordered(void** buf, size_t* have, size_t bytes, cudaStream_t stream) {
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
   if (cudaError_t e = cudaStreamIsCapturing(stream, &cs); e != cudaSuccess) return cuda_fail(e);
   if (cs != cudaStreamCaptureStatusNone) return BLKATTN_ERR_NO_WORKSPACE;
-  if (bytes < 2 * *have) bytes = 2 * *have;
   void* grown = nullptr;
-  if (cudaError_t e = cudaMallocAsync(&grown, bytes, stream); e != cudaSuccess) return cuda_fail(e);
+  size_t got = 0;
+  const cudaError_t e = blkattn::grow_scratch(
+      *have, bytes, [&](size_t n) { return cudaMallocAsync(&grown, n, stream); },
+      [](cudaError_t failed) {
+        if (failed != cudaErrorMemoryAllocation) return false;
+        cudaGetLastError();  // (not the error of a call that may still succeed)
+        return true;
+      },
+      &got);
+  if (e != cudaSuccess) return cuda_fail(e);
   *buf = grown;
-  *have = bytes;
+  *have = got;
   return BLKATTN_OK;
 }
 

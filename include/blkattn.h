@@ -116,8 +116,8 @@ typedef struct {
  * partial states, and per-unit counters that every call leaves at zero)
  * comes from per-device, grow-only buffers.  They grow stream-ordered on the
  * call's stream (cudaMallocAsync of a new buffer of at least twice the size,
- * counters zeroed by cudaMemsetAsync), so a call never synchronises the
- * device; an outgrown buffer is kept until the process exits, because
+ * or of what the call needs where memory allows no more, counters zeroed by
+ * cudaMemsetAsync), so a call never synchronises the device; an outgrown buffer is kept until the process exits, because
  * captured graphs may hold its address.  Growth during stream capture is
  * refused with BLKATTN_ERR_NO_WORKSPACE.  Calls and graph replays on
  * different streams of one device must not overlap in time (they share the

@@ -115,8 +115,12 @@ struct DecodeLayout {
 // 10.8 and 6.5 us).  Lane i looks up key i's page a tile before its copies.  A key without a
 // page reads zeros and is not visible, and the value product skips every key
 // that no row of the CTA sees (rows never written may hold anything).
+//
+// (Blocks an SM: none stated over a contiguous cache.  A stated 1 let 8 f32 rows
+// of 64 dims grow from 150 to 198 registers, which leaves one block where two
+// fit: 4 x 8 heads x 8 rows at 3000 keys 74 us without, 124 with it.)
 template <typename T, int D, int R, int NW, int STAGES, bool PAGED, int KPW>
-__global__ void __launch_bounds__((NW + (PAGED ? 0 : 1)) * 32, PAGED ? 3 : 1)
+__global__ void __launch_bounds__((NW + (PAGED ? 0 : 1)) * 32, PAGED ? 3 : 0)
     decode_split_kernel(const FwdParams p) {
   using L = DecodeLayout<T, D, R, NW, STAGES, KPW>;
   constexpr int kRowBytes = L::kRowBytes;
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__((NW + (PAGED ? 0 : 1)) * 32, PAGED ? 3 : 1)
       val = load_elt<T>(p.q, (int64_t)b * p.q_sb + (int64_t)(hk * p.G + g) * p.q_sh +
                                  (int64_t)i * p.q_si + (int64_t)d * p.q_sd);
     }
-    q_s[r * L::kQRow + d + 4 * (d / PART)] = val;
+    q_s[r * L::kQRow + (L::kParts == 2 ? (d < PART ? d : d + 4) : d + 4 * (d / PART))] = val;
   }
   __syncthreads();
 

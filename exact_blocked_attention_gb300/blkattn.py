@@ -195,13 +195,12 @@ def _outputs(stream, *specs):
     current stream's memory may still be in use there) and the current stream
     is recorded as a reader."""
     device = specs[0][2]
-    other = False
-    if stream is not None and device.type == "cuda":
-        current = torch.cuda.current_stream(device)
-        handle = _stream_handle(stream)
-        handle = 0 if handle == 1 else handle  # (the legacy stream is the default one)
-        other = handle != current.cuda_stream
-    if not other:
+    if stream is None or device.type != "cuda":
+        return [torch.empty(shape, dtype=dtype, device=dev) for shape, dtype, dev in specs]
+    current = torch.cuda.current_stream(device)
+    handle = _stream_handle(stream)
+    handle = 0 if handle == 1 else handle  # (the legacy stream is the default one)
+    if handle == current.cuda_stream:
         return [torch.empty(shape, dtype=dtype, device=dev) for shape, dtype, dev in specs]
     if handle == 2:
         raise ValueError("blkattn: torch cannot allocate on the per-thread stream: pass the outputs")

@@ -661,8 +661,8 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
         const float2 nm2 = make_float2(-m_use, -m_use);
         const float2 neg1 = make_float2(-1.f, -1.f);
-        // sums of the weights; over pages the first two for l, the others for lx
-        // where the two differ
+        // sums of the weights; over pages, where l and lx differ, the first three
+        // for l and the last for lx
         float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                         make_float2(0.f, 0.f)};
         const bool split = split_tile(key0);
@@ -694,7 +694,8 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
           // holds all the weight gives its value back, whatever its rounding.
           // Over pages lse takes the sum before the rounding, which keeps it
           // fp32 accurate (one sum, the unrounded, 361 us for the case above;
-          // both 381, 403 with the halves unpacked by shift and mask)
+          // both 377, 381 with two accumulators each, 390 with more registers for
+          // them, 403 with the halves unpacked by shift and mask)
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) {  // 32 keys -> 16 columns of P
             uint32_t pb[16];
@@ -705,8 +706,8 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
               const float2 pp = make_float2(fast_exp2(e.x), fast_exp2(e.y));
               pb[c] = pack_bf16(pp.x, pp.y);
               if (PAGED) {
-                add_bf16x2(ls[c & 1], pb[c]);
-                ls[2 + (c & 1)] = __fadd2_rn(ls[2 + (c & 1)], pp);
+                add_bf16x2(ls[c % 3], pb[c]);
+                ls[3] = __fadd2_rn(ls[3], pp);
               } else {
                 ls[c & 3] = __fadd2_rn(ls[c & 3], make_float2(__uint_as_float(pb[c] << 16),
                                                               __uint_as_float(pb[c] & 0xffff0000u)));
@@ -717,12 +718,12 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
         }
         {
           const float2 a = __fadd2_rn(ls[0], ls[1]);
-          const float2 c2 = __fadd2_rn(ls[2], ls[3]);
           if (PAGED && !split) {
-            l += a.x + a.y;
-            lx += c2.x + c2.y;
+            const float2 t2 = __fadd2_rn(a, ls[2]);
+            l += t2.x + t2.y;
+            lx += ls[3].x + ls[3].y;
           } else {
-            const float2 t2 = __fadd2_rn(a, c2);
+            const float2 t2 = __fadd2_rn(a, __fadd2_rn(ls[2], ls[3]));
             const float t = t2.x + t2.y;
             l += t;
             if (PAGED) lx += t;

@@ -820,7 +820,8 @@ int fwd_impl(const blkattn_tensor* q, const blkattn_tensor* k, const blkattn_ten
 // 10 us and 1.63 us a key tile and wave (one row tile 1.38; d = 64 1.37 and
 // 1.12), joining 3 us and 0.055 us a part (d = 64 0.04; its state goes through
 // memory).  Its choice was within 5 % of the best count of parts for each of 32
-// shapes.  Examples at 8192 keys: 256 rows x 32 heads 105 us whole, 43 in 4
+// shapes (with one sum of the weights; both take some 4 % more, whatever the
+// parts).  Examples at 8192 keys: 256 rows x 32 heads 105 us whole, 43 in 4
 // parts; 512 rows 110 and 70 (2 parts); 128 rows of one head 98 and 19 (16
 // parts); 1024 rows x 40 heads (8 items past a wave) 197 and 133.  The keys
 // are the table's, as everywhere in a plan.

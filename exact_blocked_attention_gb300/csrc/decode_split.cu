@@ -110,9 +110,9 @@ struct DecodeLayout {
 // consumer warp copies its own 16 keys of a tile (16-byte asynchronous copies
 // by all its lanes, two or three tiles ahead) and needs nobody's barrier.  A
 // bulk copy a row, as below, costs some 50 ns to issue, 128 of them a tile
-// (16 x 8 KV heads of 1000 f32 keys: 96 us with them, 67 us without, 49 us with
-// 8 keys a warp, which lets three blocks share an SM; one row over 1000 keys
-// 10.8 and 6.5 us).  Lane i looks up key i's page a tile before its copies.  A key without a
+// (on the device, 16 x 8 KV heads of 1000 f32 keys: 96 us with them, 67 us
+// without, 49 us with 8 keys a warp, which lets three blocks share an SM; one row
+// over 1000 keys 10.8 and 6.5 us, some 10 us as a call).  Lane i looks up key i's page a tile before its copies.  A key without a
 // page reads zeros and is not visible, and the value product skips every key
 // that no row of the CTA sees (rows never written may hold anything).
 //

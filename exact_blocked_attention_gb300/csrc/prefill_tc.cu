@@ -146,14 +146,16 @@ __device__ __forceinline__ void item_of(const FwdParams& p, int r, int n_pairs, 
 // packed rows of 128 dims both halves in one box (WIDE), as in the decode
 // kernel: a copy takes its warp some 50 ns to issue, and one warp with a box a
 // half took 576 us for the case below in pages of 8, 398 in pages of 16, 355
-// in pages of 128; now 359 in any.  A page number outside the pool goes to the
+// in pages of 128; two 359 in any (with one sum of the weights; 371 to 377 with
+// both, below).  A page number outside the pool goes to the
 // copy as -1 (zeros) and the rows mask its keys, in tensor memory (a mask in
 // registers spilled 576 bytes).  The chain of a key tile bounds it as over a
-// contiguous cache: 2 x 2048 rows of 32 heads at 8192 keys 357 us (1350
-// TFLOP/s, 68 % of the bf16 burst rate), contiguous 384.
+// contiguous cache: 2 x 2048 rows of 32 heads at 8192 keys 371 us on the device
+// (1300 TFLOP/s, 66 % of the bf16 burst rate; 384 a call among others),
+// contiguous 385.
 // At d = 64 the chain's products are half as long: 1.1 us a key tile for one
 // query tile, 1.36 for two (d = 128: 1.4 and 1.6); 1024 rows of 32 heads at
-// 2048 keys 32 us, 99 with the decode kernel.
+// 2048 keys 35 us, 102 with the decode kernel.
 template <int D, bool WIN, bool PAGED, bool WIDE>
 __global__ void __launch_bounds__(kThreads<PAGED>, 1)
     prefill_tc_kernel(const FwdParams p, const __grid_constant__ CUtensorMap tmq,
@@ -281,7 +283,8 @@ __global__ void __launch_bounds__(kThreads<PAGED>, 1)
     atomicMax(&misc[1 + 2 * x], my_end);
     // (over pages rows without keys are masked by their own warp, below, and
     // do not make every key tile a partly visible one: a chunk of 2 x 1335
-    // rows, three of them padding, x 7 heads at 2908 keys 73 us, 48 with this)
+    // rows, three of them padding, x 7 heads at 2908 keys 73 us, 48 with this; 51 with both sums of the
+    // weights)
     if (!PAGED || my_end > 0) atomicMin(&misc[2 + 2 * x], my_end);
   }
   __syncthreads();

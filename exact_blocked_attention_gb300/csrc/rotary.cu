@@ -74,7 +74,10 @@ __device__ __forceinline__ void turn_of(int t, int64_t F, float& sn, float& cs) 
 
 constexpr int kThreads = 256;
 constexpr int kRegHeads = 4;  // V < 8: heads whose loads a thread has in flight
-constexpr int kFillBlocks = 152 * 4;  // four blocks an SM at the kernels' registers
+// Blocks below which a thread takes fewer heads, so that every SM has its
+// threads: 152 SMs of four blocks (the kernels' registers; the slots of up to
+// six heads; eight heads' 64 KB allow three)
+constexpr int kFillBlocks = 152 * 4;
 
 // V elements of a row in registers, moved as one access.
 template <typename T, int V>

@@ -117,11 +117,12 @@ typedef struct {
  * comes from per-device, grow-only buffers.  They grow stream-ordered on the
  * call's stream (cudaMallocAsync of a new buffer of at least twice the size,
  * or of what the call needs where memory allows no more, counters zeroed by
- * cudaMemsetAsync), so a call never synchronises the device; an outgrown buffer is kept until the process exits, because
- * captured graphs may hold its address.  Growth during stream capture is
- * refused with BLKATTN_ERR_NO_WORKSPACE.  Calls and graph replays on
- * different streams of one device must not overlap in time (they share the
- * buffers): order them with events.
+ * cudaMemsetAsync), so a call never synchronises the device; an outgrown
+ * buffer is kept until the process exits, because captured graphs may hold
+ * its address.  Growth during stream capture is refused with
+ * BLKATTN_ERR_NO_WORKSPACE.  Calls and graph replays on different streams of
+ * one device must not overlap in time (they share the buffers): order them
+ * with events.
  */
 int blkattn_fwd(const blkattn_tensor* q, const blkattn_tensor* k,
                 const blkattn_tensor* v, const blkattn_tensor* seqlens_k,

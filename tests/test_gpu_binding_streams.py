@@ -139,3 +139,18 @@ def test_outputs_are_kept_for_the_current_stream_s_reads(problem):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(read, want))
     assert all(torch.equal(a, b) for a, b in zip(later, second()))
+
+
+@pytest.mark.parametrize("problem", CALLS)
+def test_special_stream_handles(problem):
+    call = problem()
+    want = [t.clone() for t in call()]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for handle in (0, 1, side.cuda_stream):  # the default stream by both its handles, and the current one
+            got = call(stream=handle)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        with pytest.raises(ValueError, match="per-thread"):  # no torch stream stands for it
+            call(stream=2)

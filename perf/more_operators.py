@@ -119,7 +119,9 @@ def draw(rng):
                      rows_major=rows_major)
         return {k: v for k, v in case.items() if k != "name"}
     kind = rng.choice(("causal", "causal", "tree", "window"))
+    out = rng.choice(("bf16", "bf16", "bf16", "f32"))
     if kind != "tree" and rng.random() < 0.3:
+        out = "bf16"  # (what a prompt's next projection takes)
         T, B = _log(rng, 64, 2048), 1 if G * Hkv > 32 else rng.randint(1, 2)  # a prompt's chunk
         hi = _log(rng, T, 8192)
         lo = rng.randint(T, hi)
@@ -129,7 +131,7 @@ def draw(rng):
         lo = rng.randint(max(T, hi // 8), hi)
     case = _attend("", B, G * Hkv, Hkv, T, d, page, S, lo, hi, kind="tree" if kind == "tree" else "causal",
                    window=_log(rng, 1, hi) if kind == "window" else 0, rows_major=rows_major,
-                   absent=rng.randint(0, max(0, min(T - 1, 3))), out=rng.choice(("bf16", "bf16", "bf16", "f32")))
+                   absent=rng.randint(0, max(0, min(T - 1, 3))), out=out)
     return {k: v for k, v in case.items() if k != "name"}
 
 

@@ -2,8 +2,9 @@
 
 Argument marshalling only: torch tensors are turned into strided descriptors
 (data pointer, sizes, strides) and the current torch stream is passed through,
-here with ctypes, for the operators of a serving step (rope, paged_append,
-attention_paged) in the small extension csrc/torch_bind.cpp.
+here with ctypes, for the operators of a serving step (rope, qk_norm_rope,
+paged_append, attention_paged and the 8-bit cache's) in the small extension
+csrc/torch_bind.cpp.
 Every step of the attention runs in the library's CUDA kernels; there is no
 CPU or eager fallback, and a missing library is an error.
 """
@@ -27,15 +28,17 @@ ERR_NO_WORKSPACE = -5
 ERR_SCRATCH_LIMIT = -6
 STATIC_SCRATCH_BYTES = 16 * 1024 * 1024
 
-BF16, F32, I32, I64 = 1, 2, 3, 4
-_DTYPES = {torch.bfloat16: BF16, torch.float32: F32, torch.int32: I32, torch.int64: I64}
+BF16, F32, I32, I64, E4M3, E8M0 = 1, 2, 3, 4, 5, 6
+_DTYPES = {torch.bfloat16: BF16, torch.float32: F32, torch.int32: I32, torch.int64: I64,
+           torch.float8_e4m3fn: E4M3, torch.float8_e8m0fnu: E8M0}
 
 EXPORTED = ("blkattn_fwd", "blkattn_merge", "blkattn_status_string",
             "blkattn_check_device_error", "blkattn_debug_plan", "blkattn_debug_set_split_event",
             "blkattn_fwd_static_scratch", "blkattn_last_cuda_error", "blkattn_fwd_tree",
             "blkattn_spec_sample", "blkattn_fwd_window", "blkattn_bwd", "blkattn_bwd_window",
             "blkattn_debug_stall_next_decode", "blkattn_rope_angles", "blkattn_rope_phases", "blkattn_rope",
-            "blkattn_rope_bwd", "blkattn_paged_append", "blkattn_fwd_paged")
+            "blkattn_rope_bwd", "blkattn_paged_append", "blkattn_fwd_paged", "blkattn_qk_norm_rope",
+            "blkattn_qk_norm_rope_bwd", "blkattn_paged_append_q8", "blkattn_paged_read_q8", "blkattn_fwd_paged_q8")
 
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3}
@@ -111,6 +114,16 @@ def load(path: str = LIB_PATH):
             lib.blkattn_paged_append.argtypes = [P] * 7 + [ctypes.c_int32, ctypes.c_float, P, P, P]
             lib.blkattn_fwd_paged.restype = ctypes.c_int
             lib.blkattn_fwd_paged.argtypes = [P] * 7 + [ctypes.c_int64, ctypes.c_float, P, P, P]
+            lib.blkattn_qk_norm_rope.restype = ctypes.c_int
+            lib.blkattn_qk_norm_rope.argtypes = [P] * 6 + [ctypes.c_int32, ctypes.c_float, ctypes.c_float, P, P, P]
+            lib.blkattn_qk_norm_rope_bwd.restype = ctypes.c_int
+            lib.blkattn_qk_norm_rope_bwd.argtypes = [P] * 8 + [ctypes.c_int32, ctypes.c_float, ctypes.c_float] + [P] * 5
+            lib.blkattn_paged_append_q8.restype = ctypes.c_int
+            lib.blkattn_paged_append_q8.argtypes = [P] * 9 + [ctypes.c_float, P, ctypes.c_int32, ctypes.c_float] + [P] * 4
+            lib.blkattn_paged_read_q8.restype = ctypes.c_int
+            lib.blkattn_paged_read_q8.argtypes = [P] * 9
+            lib.blkattn_fwd_paged_q8.restype = ctypes.c_int
+            lib.blkattn_fwd_paged_q8.argtypes = [P] * 9 + [ctypes.c_int64, ctypes.c_float, P, P, P]
             lib.blkattn_merge.restype = ctypes.c_int
             lib.blkattn_merge.argtypes = [P, P, P, P]
             lib.blkattn_status_string.restype = ctypes.c_char_p
@@ -142,9 +155,10 @@ def _load_bind():
                 from . import _torch_bind as bind
             except ImportError as e:
                 raise RuntimeError(f"_torch_bind is not built or not loadable ({e}); run the package build first") from e
-            bind.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (lib.blkattn_rope, lib.blkattn_rope_bwd,
-                                                                        lib.blkattn_paged_append,
-                                                                        lib.blkattn_fwd_paged)))
+            bind.init(*(ctypes.cast(f, ctypes.c_void_p).value
+                        for f in (lib.blkattn_rope, lib.blkattn_rope_bwd, lib.blkattn_paged_append,
+                                  lib.blkattn_fwd_paged, lib.blkattn_qk_norm_rope, lib.blkattn_qk_norm_rope_bwd,
+                                  lib.blkattn_paged_append_q8, lib.blkattn_paged_read_q8, lib.blkattn_fwd_paged_q8)))
             _bind = bind
     return _bind
 
@@ -395,6 +409,71 @@ def attention_paged(q, k_pages, v_pages, page_table, seqlens_k, q_logical_pos, s
     """Allocate out/lse with torch and run blkattn_fwd_paged (scale defaults to 1/sqrt(d))."""
     st, out, lse = (_bind or _load_bind()).fwd(q, k_pages, v_pages, page_table, seqlens_k, q_logical_pos, tree, window,
                                                scale, None, None, out_dtype, _handle(stream))
+    _check(st)
+    return out, lse
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, pos, phases=None, eps: float = 1e-6, layout="half", mscale: float = 1.0,
+                 out_dtype=None, q_out=None, k_out=None, stream=None):
+    """blkattn_qk_norm_rope: rows q [B,H_q,T,d] and k [B,H_k,T,d] (k and
+    k_weight may be None) RMS-normed over d with the weights [d], then, with
+    phases, turned by their positions pos int32 [B,T].  Returns (q_out, k_out):
+    new contiguous tensors of out_dtype (default: q's) where not given."""
+    st, q_out, k_out = (_bind or _load_bind()).norm(q, k, q_weight, k_weight, pos, phases, _layout(layout), mscale, eps,
+                                                    out_dtype, q_out, k_out, _handle(stream))
+    _check(st)
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, pos, phases=None, eps: float = 1e-6, layout="half",
+                          mscale: float = 1.0, out_dtype=None, dq=None, dk=None, stream=None):
+    """blkattn_qk_norm_rope_bwd: (dq, dk, dq_weight, dk_weight) from the
+    gradients of qk_norm_rope's results; the weights' gradients are fp32 [d]."""
+    st, *grads = (_bind or _load_bind()).norm_bwd(dq_out, dk_out, q, k, q_weight, k_weight, pos, phases,
+                                                  _layout(layout), mscale, eps, out_dtype, dq, dk, _handle(stream))
+    _check(st)
+    return tuple(grads)
+
+
+def paged_append_q8(k, v, pos, page_table, k_pages, v_pages, k_scales, v_scales, phases=None, layout="half",
+                    mscale: float = 1.0, k_weight=None, q_weight=None, eps: float = 1e-6, q=None, q_out=None,
+                    stream=None):
+    """blkattn_paged_append_q8: paged_append into the 8-bit cache, pools
+    float8_e4m3fn [N,H_kv,P,d] with scales float8_e8m0fnu [N,H_kv,P/S]; with
+    k_weight, q_weight the rows are normed (qk_norm_rope) before they turn."""
+    st, q_out = (_bind or _load_bind()).append_q8(k, v, pos, page_table, k_pages, v_pages, k_scales, v_scales, phases,
+                                                  _layout(layout), mscale, k_weight, q_weight, eps, q, q_out,
+                                                  _handle(stream))
+    _check(st)
+    return q_out
+
+
+def paged_read_q8(pos, page_table, k_pages, v_pages, k_scales, v_scales, out_dtype=torch.bfloat16, k_out=None,
+                  v_out=None, stream=None):
+    """blkattn_paged_read_q8: the cache rows pos int32 [B,T] of K and V as
+    numbers [B,H_kv,T,d]; zeros where pos is negative or no page is."""
+    st, k_out, v_out = (_bind or _load_bind()).read_q8(pos, page_table, k_pages, v_pages, k_scales, v_scales,
+                                                       out_dtype, k_out, v_out, _handle(stream))
+    _check(st)
+    return k_out, v_out
+
+
+def fwd_paged_q8(q, k_pages, v_pages, k_scales, v_scales, page_table, seqlens_k, q_logical_pos, scale: float, out, lse,
+                 stream=None, tree=None, window: int = 0):
+    """blkattn_fwd_paged_q8: attention over the 8-bit cache; out and lse are
+    written in place.  tree and window as for fwd."""
+    st, out, lse = (_bind or _load_bind()).fwd_q8(q, k_pages, v_pages, k_scales, v_scales, page_table, seqlens_k,
+                                                  q_logical_pos, tree, window, scale, out, lse, None, _handle(stream))
+    _check(st)
+    return out, lse
+
+
+def attention_paged_q8(q, k_pages, v_pages, k_scales, v_scales, page_table, seqlens_k, q_logical_pos, scale=None,
+                       out_dtype=torch.float32, stream=None, tree=None, window: int = 0):
+    """Allocate out/lse with torch and run blkattn_fwd_paged_q8 (scale defaults to 1/sqrt(d))."""
+    st, out, lse = (_bind or _load_bind()).fwd_q8(q, k_pages, v_pages, k_scales, v_scales, page_table, seqlens_k,
+                                                  q_logical_pos, tree, window, scale, None, None, out_dtype,
+                                                  _handle(stream))
     _check(st)
     return out, lse
 

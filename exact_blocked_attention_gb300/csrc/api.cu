@@ -34,6 +34,9 @@ struct DeviceState {
   int* err = nullptr;
   void* ws = nullptr;
   size_t ws_bytes = 0;
+  // an 8-bit cache's pages as bf16, for the prompt kernel
+  void* pages = nullptr;
+  size_t pages_bytes = 0;
   // per-unit counters of the tcgen05 decode kernel: zeroed when allocated,
   // left zero by every launch
   unsigned* cnt = nullptr;
@@ -890,7 +893,8 @@ bool on_cuda_cores(const Plan& pl) {
 int fwd_paged_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages_, const blkattn_tensor* v_pages_,
                    const blkattn_tensor* page_table, const blkattn_tensor* seqlens_k,
                    const blkattn_tensor* q_logical_pos, const blkattn_tensor* tree, int64_t window, float scale,
-                   const blkattn_tensor* out_, const blkattn_tensor* lse, blkattn_stream_t stream_) {
+                   const blkattn_tensor* out_, const blkattn_tensor* lse, blkattn_stream_t stream_,
+                   bool locked = false) {
   if (!dims_ok(q_, 4) || !dims_ok(k_pages_, 4) || !dims_ok(v_pages_, 4) || !dims_ok(out_, 4))
     return BLKATTN_ERR_INVALID_ARG;
   // The stride of a dim of size 1 is never used, but tensor maps and alignment
@@ -926,7 +930,8 @@ int fwd_paged_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages_, con
   if ((st = check_current_device(c.device)) != BLKATTN_OK) return st;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
 
-  std::lock_guard<std::mutex> lock(g_mu);
+  std::unique_lock<std::mutex> lock(g_mu, std::defer_lock);
+  if (!locked) lock.lock();
   DeviceState* ds = nullptr;
   if ((st = device_state(&ds)) != BLKATTN_OK) return st;
   const PromptPlan pp = plan_prompt(c, ds->sms);
@@ -1037,9 +1042,192 @@ int fwd_paged_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages_, con
   return BLKATTN_OK;
 }
 
+// blkattn_fwd_paged_q8.  Prompts (T_q >= 64, no tree, contiguous query rows,
+// scale > 0): the visible pages are written as bf16 to a buffer of the library
+// and the bf16 prompt kernel reads those (expand_pays tells when); the numbers
+// are the same, a bf16 holds e4m3 times a power of two.  The rest, and longer
+// batches in slices, goes to the kernel that reads the 8-bit pages.
+constexpr int64_t kExpandBytes = 2LL << 30;  // of K and V for one slice of sequences; 8x for a single one
+
+int fwd_paged_q8_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages, const blkattn_tensor* v_pages,
+                      const blkattn_tensor* k_scales, const blkattn_tensor* v_scales, const blkattn_tensor* page_table,
+                      const blkattn_tensor* seqlens_k, const blkattn_tensor* q_logical_pos, const blkattn_tensor* tree,
+                      int64_t window, float scale, const blkattn_tensor* out_, const blkattn_tensor* lse,
+                      blkattn_stream_t stream_) {
+  if (!dims_ok(q_, 4) || !dims_ok(k_pages, 4) || !dims_ok(out_, 4)) return BLKATTN_ERR_INVALID_ARG;
+  if (q_->dtype != BLKATTN_BF16) return is_float_dtype(q_->dtype) ? BLKATTN_ERR_UNSUPPORTED : BLKATTN_ERR_INVALID_ARG;
+  blkattn_tensor qn = *q_, on = *out_;
+  for (blkattn_tensor* t : {&qn, &on})
+    for (int i = 0; i < 3; ++i)
+      if (t->sizes[i] == 1) t->strides[i] = t->sizes[3];
+  const blkattn_tensor *q = &qn, *out = &on;
+  PageTable pt;
+  blkattn_tensor kn, vn;
+  int shift = 0;
+  int st = check_pages_q8(k_pages, v_pages, k_scales, v_scales, page_table, q->sizes[0], k_pages->sizes[1], q->sizes[3],
+                          &kn, &vn, &pt, &shift);
+  if (st != BLKATTN_OK) return st;
+  if (window < 0 || window > 0x7fffffff || (window > 0 && tree != nullptr)) return BLKATTN_ERR_INVALID_ARG;
+  if (!(scale - scale == 0.f)) return BLKATTN_ERR_INVALID_ARG;
+  // a bf16 cache of entries x rows keys a sequence stands in for the checks
+  blkattn_tensor kc = kn;
+  kc.dtype = BLKATTN_BF16;
+  kc.sizes[0] = q->sizes[0];
+  kc.sizes[2] = (int64_t)pt.entries * pt.rows;
+  blkattn_tensor vc = kc;
+  vc.data = vn.data;
+  Checked c;
+  st = validate_fwd(q, &kc, &vc, seqlens_k, q_logical_pos, tree, nullptr, out, lse, &c);
+  if (st != BLKATTN_OK) return st;
+  if (!same_device(q, {page_table, k_pages, v_pages, k_scales, v_scales})) return BLKATTN_ERR_INVALID_ARG;
+  for (const blkattn_tensor* t : {out, lse})
+    for (int i = 0; i < t->ndim; ++i)
+      if (t->sizes[i] > 1 && t->strides[i] == 0 && c.B > 0 && c.Tq > 0) return BLKATTN_ERR_INVALID_ARG;
+  if (c.Hkv > 0x7fff || c.Hq / c.Hkv * c.Tq > 0x7fffffff) return BLKATTN_ERR_UNSUPPORTED;
+  if (c.B == 0 || c.Tq == 0) return BLKATTN_OK;
+  for (const blkattn_tensor* t : {page_table, k_scales, v_scales})
+    if (t->data == nullptr) return BLKATTN_ERR_INVALID_ARG;
+  if ((st = check_current_device(c.device)) != BLKATTN_OK) return st;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState* ds = nullptr;
+  if ((st = device_state(&ds)) != BLKATTN_OK) return st;
+
+  const int64_t seq_bytes = 4 * c.Hkv * c.Tmax * c.d;  // of one sequence's K and V as bf16
+  if (c.prefill_ok && scale > 0.f && c.Tq >= 64 && seq_bytes <= 8 * kExpandBytes) {
+    int64_t nb = kExpandBytes / seq_bytes;
+    nb = nb < 1 ? 1 : (nb > c.B ? c.B : nb);
+    if (nb > 65535) nb = 65535;
+    while (nb > 1 && nb * pt.entries > 0x7fffffff) nb /= 2;
+    const int64_t half = nb * seq_bytes / 2, tab = (nb * pt.entries * 4 + 255) / 256 * 256;
+    const int64_t need = 2 * half + tab;
+    if ((size_t)need > ds->pages_bytes &&
+        (st = grow_stream_ordered(&ds->pages, &ds->pages_bytes, (size_t)need, stream)) != BLKATTN_OK)
+      return st;
+    char* buf = static_cast<char*>(ds->pages);
+    for (int64_t b0 = 0; b0 < c.B; b0 += nb) {
+      const int64_t n = c.B - b0 < nb ? c.B - b0 : nb;
+      ExpandParams e{};
+      const blkattn_tensor* pools[2] = {&kn, &vn};
+      const blkattn_tensor* scales[2] = {k_scales, v_scales};
+      for (int i = 0; i < 2; ++i) {
+        e.pool[i] = static_cast<const unsigned char*>(pools[i]->data);
+        e.s_n[i] = pools[i]->strides[0]; e.s_h[i] = pools[i]->strides[1]; e.s_r[i] = pools[i]->strides[2];
+        e.scales[i] = static_cast<const unsigned char*>(scales[i]->data);
+        e.e_n[i] = scales[i]->strides[0]; e.e_h[i] = scales[i]->strides[1]; e.e_i[i] = scales[i]->strides[2];
+        e.out[i] = buf + i * half;
+      }
+      e.scale_shift = shift;
+      e.table = reinterpret_cast<int32_t*>(buf + 2 * half);
+      e.seqlens = static_cast<const int32_t*>(seqlens_k->data) + b0 * seqlens_k->strides[0];
+      e.sl_s = seqlens_k->strides[0];
+      e.qpos = static_cast<const int32_t*>(q_logical_pos->data) + b0 * q_logical_pos->strides[0];
+      e.qp_sb = q_logical_pos->strides[0]; e.qp_si = q_logical_pos->strides[1];
+      e.window = (int)window;
+      e.Tq = (int)c.Tq; e.B = (int)n; e.Hkv = (int)c.Hkv;
+      e.pages = pt;
+      e.pages.table += b0 * pt.sb;
+      if (cudaError_t err = launch_expand_q8(e, (int)c.d, stream); err != cudaSuccess) return cuda_fail(err);
+      auto slice = [&](const blkattn_tensor* t, int64_t bytes) {
+        blkattn_tensor r = *t;
+        r.data = static_cast<char*>(t->data) + b0 * t->strides[0] * bytes;
+        r.sizes[0] = n;
+        return r;
+      };
+      blkattn_tensor kp = kc;
+      kp.data = e.out[0];
+      kp.sizes[0] = n * pt.entries; kp.sizes[2] = pt.rows;
+      kp.strides[3] = 1; kp.strides[2] = c.d; kp.strides[1] = c.d * pt.rows; kp.strides[0] = c.d * pt.rows * c.Hkv;
+      blkattn_tensor vp = kp;
+      vp.data = e.out[1];
+      blkattn_tensor table = *page_table;
+      table.data = e.table;
+      table.sizes[0] = n;
+      table.strides[0] = pt.entries; table.strides[1] = 1;
+      const blkattn_tensor sq = slice(q, 2), sl = slice(seqlens_k, 4), sp = slice(q_logical_pos, 4);
+      const blkattn_tensor so = slice(out, elt_bytes(out->dtype)), sle = slice(lse, 4);
+      st = fwd_paged_impl(&sq, &kp, &vp, &table, &sl, &sp, nullptr, window, scale, &so, &sle, stream_, true);
+      if (st != BLKATTN_OK) return st;
+    }
+    return BLKATTN_OK;
+  }
+
+  const int64_t rows = c.Hq / c.Hkv * c.Tq;
+  int64_t nb = c.B < kDecodeQ8MaxBatch ? c.B : kDecodeQ8MaxBatch;
+  Q8Plan pl = plan_decode_q8(nb, c.Hkv, rows, c.Tmax, (int)c.d, ds->sms);
+  while (nb > 1 && pl.tiles > kDecodeQ8MaxTiles) {
+    nb = (nb + 1) / 2;
+    pl = plan_decode_q8(nb, c.Hkv, rows, c.Tmax, (int)c.d, ds->sms);
+  }
+  if (pl.tiles > kDecodeQ8MaxTiles) return BLKATTN_ERR_UNSUPPORTED;
+  if ((st = ensure_workspace(ds, pl.ws_bytes, stream)) != BLKATTN_OK) return st;
+  if ((st = ensure_counters(ds, pl.units, stream)) != BLKATTN_OK) return st;
+  Q8Params p{};
+  p.q_sb = q->strides[0]; p.q_sh = q->strides[1]; p.q_si = q->strides[2]; p.q_sd = q->strides[3];
+  p.q_vec = c.q_vec_ok;
+  p.k = static_cast<const char*>(kn.data);
+  p.v = static_cast<const char*>(vn.data);
+  p.k_sn = kn.strides[0]; p.k_sh = kn.strides[1]; p.k_sr = kn.strides[2];
+  p.v_sn = vn.strides[0]; p.v_sh = vn.strides[1]; p.v_sr = vn.strides[2];
+  p.k_sc = static_cast<const unsigned char*>(k_scales->data);
+  p.v_sc = static_cast<const unsigned char*>(v_scales->data);
+  p.ke_sn = k_scales->strides[0]; p.ke_sh = k_scales->strides[1]; p.ke_si = k_scales->strides[2];
+  p.ve_sn = v_scales->strides[0]; p.ve_sh = v_scales->strides[1]; p.ve_si = v_scales->strides[2];
+  p.scale_shift = shift;
+  p.sl_s = seqlens_k->strides[0];
+  p.qp_sb = q_logical_pos->strides[0]; p.qp_si = q_logical_pos->strides[1];
+  if (tree) { p.tr_sb = tree->strides[0]; p.tr_si = tree->strides[1]; }
+  p.window = (int)window;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.out_bf16 = out->dtype == BLKATTN_BF16;
+  p.o_sb = out->strides[0]; p.o_sh = out->strides[1]; p.o_si = out->strides[2]; p.o_sd = out->strides[3];
+  p.l_sb = lse->strides[0]; p.l_sh = lse->strides[1]; p.l_si = lse->strides[2];
+  p.Hq = (int)c.Hq; p.Hkv = (int)c.Hkv; p.G = (int)(c.Hq / c.Hkv); p.Tq = (int)c.Tq; p.Tmax = (int)c.Tmax;
+  p.row_groups = (int)pl.row_groups;
+  p.rows_cta = pl.rows_cta;
+  p.ws = static_cast<float*>(ds->ws);
+  p.cnt = ds->cnt;
+  p.pages = pt;
+  for (int64_t b0 = 0; b0 < c.B; b0 += nb) {  // (slices run one after another in the same workspace)
+    p.B = (int)(c.B - b0 < nb ? c.B - b0 : nb);
+    p.q = static_cast<const char*>(q->data) + b0 * p.q_sb * 2;
+    p.seqlens = static_cast<const int32_t*>(seqlens_k->data) + b0 * p.sl_s;
+    p.qpos = static_cast<const int32_t*>(q_logical_pos->data) + b0 * p.qp_sb;
+    p.tree = tree ? static_cast<const int64_t*>(tree->data) + b0 * p.tr_sb : nullptr;
+    p.out = static_cast<char*>(out->data) + b0 * p.o_sb * elt_bytes(out->dtype);
+    p.lse = static_cast<float*>(lse->data) + b0 * p.l_sb;
+    p.pages.table = pt.table + b0 * pt.sb;
+    if (cudaError_t e = launch_decode_q8(p, (int)c.d, pl.ctas, stream); e != cudaSuccess) return cuda_fail(e);
+  }
+  return BLKATTN_OK;
+}
+
 // CUDA failures of entry points outside this file: recorded for
 // blkattn_last_cuda_error like the ones here.
 int report_cuda_failure(cudaError_t e) { return cuda_fail(e); }
+
+Library::Library() { g_mu.lock(); }
+Library::~Library() { g_mu.unlock(); }
+int Library::sms(int* n) const {
+  DeviceState* ds = nullptr;
+  const int st = device_state(&ds);
+  if (st == BLKATTN_OK) *n = ds->sms;
+  return st;
+}
+int Library::workspace(size_t bytes, cudaStream_t stream, void** ws) const {
+  DeviceState* ds = nullptr;
+  if (const int st = device_state(&ds); st != BLKATTN_OK) return st;
+  if (const int st = ensure_workspace(ds, bytes, stream); st != BLKATTN_OK) return st;
+  *ws = ds->ws;
+  return BLKATTN_OK;
+}
+int Library::counters(int64_t n, cudaStream_t stream, unsigned** cnt) const {
+  DeviceState* ds = nullptr;
+  if (const int st = device_state(&ds); st != BLKATTN_OK) return st;
+  if (const int st = ensure_counters(ds, n, stream); st != BLKATTN_OK) return st;
+  *cnt = ds->cnt;
+  return BLKATTN_OK;
+}
 
 int device_error_word(int** out) {
   std::lock_guard<std::mutex> lock(g_mu);
@@ -1241,6 +1429,15 @@ int blkattn_fwd_paged(const blkattn_tensor* q, const blkattn_tensor* k_pages, co
                       const blkattn_tensor* out, const blkattn_tensor* lse, blkattn_stream_t stream_) {
   return blkattn::fwd_paged_impl(q, k_pages, v_pages, page_table, seqlens_k, q_logical_pos, tree_mask, window, scale,
                                  out, lse, stream_);
+}
+
+int blkattn_fwd_paged_q8(const blkattn_tensor* q, const blkattn_tensor* k_pages, const blkattn_tensor* v_pages,
+                         const blkattn_tensor* k_scales, const blkattn_tensor* v_scales,
+                         const blkattn_tensor* page_table, const blkattn_tensor* seqlens_k,
+                         const blkattn_tensor* q_logical_pos, const blkattn_tensor* tree_mask, int64_t window,
+                         float scale, const blkattn_tensor* out, const blkattn_tensor* lse, blkattn_stream_t stream) {
+  return blkattn::fwd_paged_q8_impl(q, k_pages, v_pages, k_scales, v_scales, page_table, seqlens_k, q_logical_pos,
+                                    tree_mask, window, scale, out, lse, stream);
 }
 
 int blkattn_bwd(const blkattn_tensor* q, const blkattn_tensor* k, const blkattn_tensor* v,

@@ -165,6 +165,68 @@ size_t decode_tc_smem_bytes(int rows_cta);
 cudaError_t launch_decode_tc_paged(const FwdParams& p, int d, int ctas, const CUtensorMap& tmk,
                                    const CUtensorMap& tmv, cudaStream_t stream);
 
+// ---- attention over the 8-bit paged cache (q8.cuh) ----
+struct Q8Params {
+  const void* q;  // bf16 rows; element strides
+  int64_t q_sb, q_sh, q_si, q_sd;
+  bool q_vec;  // unit dim stride, 16-byte aligned rows
+  const char* k;  // e4m3 pools: strides of page, head and row in page
+  const char* v;
+  int64_t k_sn, k_sh, k_sr, v_sn, v_sh, v_sr;
+  const unsigned char* k_sc;  // e8m0 scales: strides of page, head and block
+  const unsigned char* v_sc;
+  int64_t ke_sn, ke_sh, ke_si, ve_sn, ve_sh, ve_si;
+  int scale_shift;  // log2 of the rows of a scale
+  const int32_t* seqlens;
+  int64_t sl_s;
+  const int32_t* qpos;
+  int64_t qp_sb, qp_si;
+  const int64_t* tree;
+  int64_t tr_sb, tr_si;
+  int window;
+  float scale_log2;
+  void* out;
+  int out_bf16;
+  int64_t o_sb, o_sh, o_si, o_sd;
+  float* lse;
+  int64_t l_sb, l_sh, l_si;
+  int B, Hq, Hkv, G, Tq, Tmax;
+  int row_groups, rows_cta;  // of the G Tq rows of a KV head
+  float* ws;      // partial states: [CTAs + units][M, l, R of the rows], then their u
+  unsigned* cnt;  // a unit's CTAs that have written theirs (zero before and after)
+  PageTable pages;
+};
+struct Q8Plan {
+  int64_t row_groups, units, tiles;
+  int rows_cta, ctas;
+  size_t ws_bytes;
+};
+constexpr int kDecodeQ8MaxBatch = 384;  // sequences of one launch (tables in shared memory)
+constexpr int64_t kDecodeQ8MaxTiles = 1 << 30;
+constexpr int kDecodeQ8MaxCtas = 512;  // parts of a unit
+Q8Plan plan_decode_q8(int64_t B, int64_t Hkv, int64_t rows, int64_t Tmax, int d, int sms);
+cudaError_t launch_decode_q8(const Q8Params& p, int d, int ctas, cudaStream_t stream);
+
+// The visible pages of `B` sequences as bf16: row t of sequence b to row t mod P
+// of page b entries + t / P of k_out, v_out [B entries, Hkv, P, d] (contiguous),
+// and that table to `table` [B, entries] (-1 where no page is).
+struct ExpandParams {
+  const unsigned char* pool[2];
+  int64_t s_n[2], s_h[2], s_r[2];
+  const unsigned char* scales[2];
+  int64_t e_n[2], e_h[2], e_i[2];
+  int scale_shift;
+  void* out[2];
+  int32_t* table;
+  const int32_t* seqlens;
+  int64_t sl_s;
+  const int32_t* qpos;
+  int64_t qp_sb, qp_si;
+  int window, Tq, B, Hkv;
+  PageTable pages;
+};
+cudaError_t launch_expand_q8(const ExpandParams& p, int d, cudaStream_t stream);
+
 // ---- backward pass (eqs. 33.6-33.8), tcgen05, bf16, d = 128 ----
 struct BwdParams {
   const void* out;  // forward output o [B, H_q, T_q, d] (bf16 or fp32), read for D = g_o . o
@@ -218,6 +280,22 @@ int fwd_with_scratch(const blkattn_tensor* q, const blkattn_tensor* k, const blk
                      void* scratch, size_t scratch_bytes);
 // Records a CUDA failure for blkattn_last_cuda_error; returns BLKATTN_ERR_CUDA.
 int report_cuda_failure(cudaError_t e);
+// The library's state on the current device, locked while this lives: a call of
+// several launches that passes data through the workspace holds it over all of
+// them (two host threads on one stream must not interleave theirs).
+class Library {
+ public:
+  Library();
+  ~Library();
+  Library(const Library&) = delete;
+  Library& operator=(const Library&) = delete;
+  int sms(int* n) const;
+  // At least so many bytes of the grow-only workspace, and so many per-unit
+  // counters (zero, and left zero by every launch); BLKATTN_ERR_NO_WORKSPACE
+  // where it would have to grow under capture.
+  int workspace(size_t bytes, cudaStream_t stream, void** ws) const;
+  int counters(int64_t n, cudaStream_t stream, unsigned** cnt) const;
+};
 // The current device's error word (kernels record a bounded wait that ran
 // out there; blkattn_check_device_error reads and clears it).
 int device_error_word(int** out);

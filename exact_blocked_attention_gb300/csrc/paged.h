@@ -69,4 +69,13 @@ int require_current_device(int32_t device);
 int check_pages(const blkattn_tensor* k_pages, const blkattn_tensor* v_pages, const blkattn_tensor* table,
                 int32_t dtype, int64_t B, int64_t H, int64_t d, PageTable* out);
 
+// The 8-bit cache: k_pages, v_pages [N, H, rows, d] e4m3 with unit dim stride
+// and rows of 16-byte alignment, and k_scales, v_scales e8m0 [N, H, rows / S]
+// of one shape; *shift = log2 S.  A stride of a dim of size 1 may be any (it is
+// set to the row's length in *kn and *vn, the pools as the kernels take them).
+int check_pages_q8(const blkattn_tensor* k_pages, const blkattn_tensor* v_pages, const blkattn_tensor* k_scales,
+                   const blkattn_tensor* v_scales, const blkattn_tensor* table, int64_t B, int64_t H, int64_t d,
+                   blkattn_tensor* kn, blkattn_tensor* vn, PageTable* out, int* shift);
+constexpr int64_t kMaxScaleRows = 128;  // rows of one scale
+
 }  // namespace blkattn

@@ -1,0 +1,690 @@
+// RMS norm of each query and key head, with the rotary position in the same
+// pass, and its gradient.
+//
+//     h = x r,  r = 1 / sqrt(mean(x^2) + eps),     y = R (w h)
+//
+// over the d dims of one head's row; R turns the pairs of the first `rot` dims
+// by the row's position and scales them by mscale (rotary.cu).  R's transpose
+// turns back with the same factor, so with g = R^T dy and c = w g
+//
+//     dx = r (c - h mean(c h)),     dw = sum over the rows of g h.
+//
+// Everything is fp32 and rounded once, at the store.  A pass moves every row in
+// and out once; both kernels are bound by memory.
+//
+// The lanes of a row: each holds two runs of V dims of 16 bytes, the runs that
+// the rotation pairs (rotary.cuh), so that the mean is log2(d / 2V) shuffles
+// and the rotation needs no exchange.  Rows that do not fit this (d / 2V no
+// power of two up to 32, strides, alignment, rot no multiple of 2V) go to a
+// warp a row through shared memory.
+#include <cuda_bf16.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "kernels.h"
+#include "paged.h"
+#include "rotary.cuh"
+
+namespace blkattn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMostHeads = 8;  // heads of one thread
+constexpr int kFillBlocks = 152 * 4;
+
+// The query heads (set 0) or the key heads (set 1).
+struct NormSet {
+  const void* x;
+  int64_t x_b, x_h, x_t, x_d;
+  const void* w;
+  int64_t w_s;
+  void* y;  // forward: the result; backward: dx
+  int64_t y_b, y_h, y_t, y_d;
+  const void* g;  // backward: dy
+  int64_t g_b, g_h, g_t, g_d;
+  float* dw;  // backward
+  int64_t dw_s;
+  int heads;
+};
+
+struct NormParams {
+  NormSet set[2];
+  int n_sets;
+  const int32_t* pos;
+  int64_t p_b, p_t;
+  const int64_t* phases;
+  int64_t ph_s;
+  bool w_f32;
+  float mscale, eps, inv_d;
+  int rot, d, B, T;
+  int hg;         // heads of a thread (fast kernels)
+  int groups[2];  // ceil(heads / hg) of each set
+  int blocks;     // backward: blocks along the tokens
+  float* ws;      // backward: partial dw [block of the grid][d]
+};
+
+__device__ __forceinline__ float weight_at(const NormSet& s, bool f32, int i) {
+  return f32 ? static_cast<const float*>(s.w)[i * s.w_s]
+             : __bfloat162float(static_cast<const __nv_bfloat16*>(s.w)[i * s.w_s]);
+}
+
+// What a lane of the fast kernels holds of every row: item `it` of d / 2V, the
+// two runs at a0 and a1.
+struct Item {
+  int it, a0, a1;
+  bool turn;
+};
+template <int V>
+__device__ __forceinline__ Item item_of(int it, int rot, int d) {
+  Item m;
+  m.it = it;
+  m.turn = it < rot / (2 * V);
+  const int part0 = m.turn ? 0 : rot, part = m.turn ? rot : d - rot;
+  m.a0 = part0 + V * (it - part0 / (2 * V));
+  m.a1 = m.a0 + part / 2;
+  return m;
+}
+template <int V, bool INTER>
+__device__ __forceinline__ void angles_of(const NormParams& p, const Item& m, int pos, float sign, float (&sn)[V],
+                                          float (&cs)[V]) {
+  if (!m.turn) return;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int pair = !INTER ? V * m.it + j : (j < V / 2 ? m.a0 / 2 + j : m.a1 / 2 + j - V / 2);
+    turn_of(pos, p.phases[pair * p.ph_s], sn[j], cs[j]);
+    sn[j] *= sign * p.mscale;
+    cs[j] *= p.mscale;
+  }
+}
+
+// Sum over the `n` (a power of two) neighbouring lanes of a row, whose mask is
+// `lanes`.
+__device__ __forceinline__ float row_sum(float x, int n, unsigned lanes) {
+  for (int off = n >> 1; off >= 1; off >>= 1) x += __shfl_xor_sync(lanes, x, off);
+  return x;
+}
+__device__ __forceinline__ unsigned lanes_of_row(int n) {
+  const int lane = threadIdx.x & 31;
+  return (n == 32 ? 0xffffffffu : (1u << n) - 1) << (lane & ~(n - 1));
+}
+
+// Forward: a thread takes one item of a token's rows in up to hg heads of one
+// set.  Its heads' runs are copied to slots of its own in shared memory, all at
+// once, and the angles and weights are taken while they land, as in the rotary
+// kernel.
+template <typename TI, typename TO, int V, bool INTER>
+__global__ void __launch_bounds__(kThreads, 3) norm_kernel(const __grid_constant__ NormParams p) {
+  static_assert(sizeof(TI) * V == 16, "runs of 16 bytes");
+  const int si = blockIdx.y >= p.groups[0] ? 1 : 0;
+  const NormSet& s = p.set[si];
+  const int h0 = ((int)blockIdx.y - (si ? p.groups[0] : 0)) * p.hg, nh = min(p.hg, s.heads - h0);
+  const int items = p.d / (2 * V);  // (a power of two)
+  const int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (u >= (int64_t)p.B * p.T * items) return;  // (whole rows leave)
+  const int tok = (int)(u / items);  // B T < 2^31
+  const Item m = item_of<V>((int)(u & (items - 1)), p.rot, p.d);
+  const int b = tok / p.T;
+  const int t = tok - b * p.T;
+  const TI* src = static_cast<const TI*>(s.x) + (b * s.x_b + t * s.x_t + h0 * s.x_h);
+  extern __shared__ __align__(16) unsigned char slots[];
+  uint4* mine = reinterpret_cast<uint4*>(slots) + threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < kMostHeads; ++k) {
+    if (k < nh) {
+      const TI* r = src + k * s.x_h;
+      cp_async_16(smem_u32(mine + 2 * k * kThreads), r + m.a0, 16);
+      cp_async_16(smem_u32(mine + (2 * k + 1) * kThreads), r + m.a1, 16);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  float w[2 * V], sn[V], cs[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    w[j] = weight_at(s, p.w_f32, m.a0 + j);
+    w[V + j] = weight_at(s, p.w_f32, m.a1 + j);
+  }
+  if (p.rot) angles_of<V, INTER>(p, m, p.pos[b * p.p_b + t * p.p_t], 1.f, sn, cs);
+  const unsigned lanes = lanes_of_row(items);
+  TO* dst = static_cast<TO*>(s.y) + (b * s.y_b + t * s.y_t + h0 * s.y_h);
+#pragma unroll
+  for (int k = 0; k < kMostHeads; ++k) {
+    wait_copies(kMostHeads - 1 - k);
+    if (k < nh) {
+      Vec<TI, V> x0, x1;
+      reinterpret_cast<uint4&>(x0) = mine[2 * k * kThreads];
+      reinterpret_cast<uint4&>(x1) = mine[(2 * k + 1) * kThreads];
+      float x[2 * V], y[2 * V];
+      unpack_runs<TI, V>(x0, x1, x);
+      float ss = 0.f;
+#pragma unroll
+      for (int j = 0; j < 2 * V; ++j) ss = fmaf(x[j], x[j], ss);
+      const float r = rsqrtf(fmaf(row_sum(ss, items, lanes), p.inv_d, p.eps));
+#pragma unroll
+      for (int j = 0; j < 2 * V; ++j) x[j] = x[j] * r * w[j];
+      turn_pairs<V, INTER>(x, m.turn, sn, cs, y);
+      Vec<TO, V> y0, y1;
+      pack_runs<TO, V>(y, y0, y1);
+      store(dst + k * s.y_h + m.a0, y0);
+      store(dst + k * s.y_h + m.a1, y1);
+    }
+  }
+}
+
+// V elements as fp32, by accesses of up to 16 bytes.
+template <typename T, int V>
+__device__ __forceinline__ void load_run(const T* p, float* x) {
+  constexpr int N = 16 / sizeof(T) < V ? 16 / (int)sizeof(T) : V;
+#pragma unroll
+  for (int c = 0; c < V; c += N) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p + c));
+    const T* e = reinterpret_cast<const T*>(&w);
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[c + j] = to_f32(e[j]);
+  }
+}
+
+// Backward: a block walks every blocks-th group of kThreads / items tokens; a
+// thread keeps its item, so its 2V sums of dw stay in registers, and joins the
+// block's in shared memory at the end.  Each block leaves its sums in the
+// workspace, and sum_dw_kernel adds those in a fixed order: no atomics, the
+// same bits every time.
+template <typename TX, typename TG, typename TO, int V, bool INTER>
+__global__ void __launch_bounds__(kThreads, 2) norm_bwd_kernel(const __grid_constant__ NormParams p) {
+  static_assert(sizeof(TX) * V == 16, "runs of 16 bytes");
+  const int si = blockIdx.y >= p.groups[0] ? 1 : 0;
+  const NormSet& s = p.set[si];
+  const int h0 = ((int)blockIdx.y - (si ? p.groups[0] : 0)) * p.hg, nh = min(p.hg, s.heads - h0);
+  const int items = p.d / (2 * V);
+  const int per_block = kThreads / items;
+  const Item m = item_of<V>(threadIdx.x & (items - 1), p.rot, p.d);
+  const unsigned lanes = lanes_of_row(items);
+  float w[2 * V], dw[2 * V], sn[V], cs[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    w[j] = weight_at(s, p.w_f32, m.a0 + j);
+    w[V + j] = weight_at(s, p.w_f32, m.a1 + j);
+    dw[j] = dw[V + j] = 0.f;
+  }
+  const int n_tok = p.B * p.T;
+  for (int64_t tok = (int64_t)blockIdx.x * per_block + threadIdx.x / items; tok < n_tok;
+       tok += (int64_t)gridDim.x * per_block) {  // (whole rows leave)
+    const int b = (int)tok / p.T;
+    const int t = (int)tok - b * p.T;
+    const TX* xs = static_cast<const TX*>(s.x) + (b * s.x_b + t * s.x_t + h0 * s.x_h);
+    const TG* gs = static_cast<const TG*>(s.g) + (b * s.g_b + t * s.g_t + h0 * s.g_h);
+    TO* dst = static_cast<TO*>(s.y) + (b * s.y_b + t * s.y_t + h0 * s.y_h);
+    if (p.rot) angles_of<V, INTER>(p, m, p.pos[b * p.p_b + t * p.p_t], -1.f, sn, cs);
+#pragma unroll 1
+    for (int k = 0; k < nh; ++k) {
+      float x[2 * V], dy[2 * V], g[2 * V];
+      load_run<TG, V>(gs + k * s.g_h + m.a0, dy);
+      load_run<TG, V>(gs + k * s.g_h + m.a1, dy + V);
+      load_run<TX, V>(xs + k * s.x_h + m.a0, x);
+      load_run<TX, V>(xs + k * s.x_h + m.a1, x + V);
+      turn_pairs<V, INTER>(dy, m.turn, sn, cs, g);
+      float ss = 0.f, ch = 0.f;
+#pragma unroll
+      for (int j = 0; j < 2 * V; ++j) {
+        ss = fmaf(x[j], x[j], ss);
+        ch = fmaf(g[j] * w[j], x[j], ch);
+      }
+      for (int off = items >> 1; off >= 1; off >>= 1) {
+        ss += __shfl_xor_sync(lanes, ss, off);
+        ch += __shfl_xor_sync(lanes, ch, off);
+      }
+      const float r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
+      const float mean = ch * r * p.inv_d;  // of c h
+#pragma unroll
+      for (int j = 0; j < 2 * V; ++j) {
+        const float h = x[j] * r;
+        dw[j] = fmaf(g[j], h, dw[j]);
+        x[j] = r * (g[j] * w[j] - h * mean);
+      }
+      Vec<TO, V> y0, y1;
+      pack_runs<TO, V>(x, y0, y1);
+      store(dst + k * s.y_h + m.a0, y0);
+      store(dst + k * s.y_h + m.a1, y1);
+    }
+  }
+  // the sums of the threads with the same item: a column each
+  __shared__ float red[kThreads][2 * V + 1];
+#pragma unroll
+  for (int j = 0; j < 2 * V; ++j) red[threadIdx.x][j] = dw[j];
+  __syncthreads();
+  float* out = p.ws + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * p.d;
+  for (int c = threadIdx.x; c < p.d; c += kThreads) {
+    const int it = c / (2 * V), j = c % (2 * V);
+    float sum = 0.f;
+    for (int i = it; i < kThreads; i += items) sum += red[i][j];
+    const Item q = item_of<V>(it, p.rot, p.d);
+    out[j < V ? q.a0 + j : q.a1 + j - V] = sum;
+  }
+}
+
+// Rows of any d, strides and rot: a warp a row, the row in shared memory.
+constexpr int kWarps = kThreads / 32;
+
+// Row u of both sets in order (set, b, head, t); false past the last.
+__device__ __forceinline__ bool row_of(const NormParams& p, int64_t u, int& si, int& b, int& h, int& t) {
+  si = 0;
+  const int64_t n0 = (int64_t)p.B * p.set[0].heads * p.T;
+  if (u >= n0) {
+    u -= n0;
+    si = 1;
+    if (p.n_sets < 2) return false;
+  }
+  const int heads = p.set[si].heads;
+  if (u >= (int64_t)p.B * heads * p.T) return false;
+  t = (int)(u % p.T);
+  const int64_t bh = u / p.T;
+  h = (int)(bh % heads);
+  b = (int)(bh / heads);
+  return true;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+  return x;
+}
+// Dim j of R row (or, back, of R^T row), the row in shared memory.
+template <bool INTER>
+__device__ __forceinline__ float turned_at(const NormParams& p, const float* row, int j, int pos, bool back) {
+  if (j >= p.rot) return row[j];
+  const int half = p.rot / 2;
+  const int pair = INTER ? j >> 1 : (j < half ? j : j - half);
+  const bool second = INTER ? (j & 1) : j >= half;
+  const float u = row[INTER ? 2 * pair : pair], v = row[INTER ? 2 * pair + 1 : pair + half];
+  float sn, cs;
+  turn_of(pos, p.phases[pair * p.ph_s], sn, cs);
+  sn *= back ? -p.mscale : p.mscale;
+  cs *= p.mscale;
+  return second ? u * sn + v * cs : u * cs - v * sn;
+}
+
+template <typename TI, typename TO, bool INTER>
+__global__ void __launch_bounds__(kThreads) norm_rows_kernel(const __grid_constant__ NormParams p) {
+  extern __shared__ float rows[];
+  float* row = rows + (threadIdx.x >> 5) * p.d;
+  const int lane = threadIdx.x & 31;
+  int si, b, h, t;
+  if (!row_of(p, (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), si, b, h, t)) return;
+  const NormSet& s = p.set[si];
+  const TI* x = static_cast<const TI*>(s.x) + (b * s.x_b + h * s.x_h + t * s.x_t);
+  float ss = 0.f;
+  for (int j = lane; j < p.d; j += 32) {
+    const float v = to_f32(x[j * s.x_d]);
+    ss = fmaf(v, v, ss);
+    row[j] = v;
+  }
+  const float r = rsqrtf(fmaf(warp_sum(ss), p.inv_d, p.eps));
+  for (int j = lane; j < p.d; j += 32) row[j] = row[j] * r * weight_at(s, p.w_f32, j);
+  __syncwarp();
+  TO* y = static_cast<TO*>(s.y) + (b * s.y_b + h * s.y_h + t * s.y_t);
+  const int pos = p.rot ? p.pos[b * p.p_b + t * p.p_t] : 0;
+  for (int j = lane; j < p.d; j += 32) y[j * s.y_d] = from_f32<TO>(turned_at<INTER>(p, row, j, pos, false));
+}
+
+// blockIdx.y: the set; a block walks every gridDim.x-th group of kWarps rows of
+// it.  Shared memory: a row of g and one of dw a warp.
+template <typename TX, typename TG, typename TO, bool INTER>
+__global__ void __launch_bounds__(kThreads) norm_bwd_rows_kernel(const __grid_constant__ NormParams p) {
+  extern __shared__ float rows[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* gr = rows + warp * p.d;
+  float* dw = rows + (kWarps + warp) * p.d;
+  const int si = blockIdx.y;
+  const NormSet& s = p.set[si];
+  for (int j = lane; j < p.d; j += 32) dw[j] = 0.f;
+  const int64_t n = (int64_t)p.B * s.heads * p.T;
+  for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < n; u += (int64_t)gridDim.x * kWarps) {
+    const int t = (int)(u % p.T);
+    const int64_t bh = u / p.T;
+    const int h = (int)(bh % s.heads), b = (int)(bh / s.heads);
+    const TX* x = static_cast<const TX*>(s.x) + (b * s.x_b + h * s.x_h + t * s.x_t);
+    const TG* g = static_cast<const TG*>(s.g) + (b * s.g_b + h * s.g_h + t * s.g_t);
+    __syncwarp();
+    for (int j = lane; j < p.d; j += 32) gr[j] = to_f32(g[j * s.g_d]);
+    __syncwarp();
+    const int pos = p.rot ? p.pos[b * p.p_b + t * p.p_t] : 0;
+    float ss = 0.f, ch = 0.f;
+    for (int j = lane; j < p.d; j += 32) {
+      const float v = to_f32(x[j * s.x_d]);
+      ss = fmaf(v, v, ss);
+      ch = fmaf(turned_at<INTER>(p, gr, j, pos, true) * weight_at(s, p.w_f32, j), v, ch);
+    }
+    ss = warp_sum(ss);
+    ch = warp_sum(ch);
+    const float r = rsqrtf(fmaf(ss, p.inv_d, p.eps)), mean = ch * r * p.inv_d;
+    TO* y = static_cast<TO*>(s.y) + (b * s.y_b + h * s.y_h + t * s.y_t);
+    for (int j = lane; j < p.d; j += 32) {
+      const float gj = turned_at<INTER>(p, gr, j, pos, true), hj = to_f32(x[j * s.x_d]) * r;
+      dw[j] = fmaf(gj, hj, dw[j]);
+      y[j * s.y_d] = from_f32<TO>(r * (gj * weight_at(s, p.w_f32, j) - hj * mean));
+    }
+  }
+  __syncthreads();
+  float* out = p.ws + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * p.d;
+  for (int c = threadIdx.x; c < p.d; c += kThreads) {
+    float sum = 0.f;
+    for (int k = 0; k < kWarps; ++k) sum += rows[(kWarps + k) * p.d + c];
+    out[c] = sum;
+  }
+}
+
+// dw: the blocks' sums of each set, 32 dims a block, eight strided sums a dim
+// and then those, in order.
+__global__ void __launch_bounds__(kThreads) sum_dw_kernel(const __grid_constant__ NormParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (the blocks' sums)
+  const NormSet& s = p.set[blockIdx.y];
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  const int n = p.groups[blockIdx.y] * p.blocks;
+  const float* in = p.ws + (int64_t)(blockIdx.y ? p.groups[0] : 0) * p.blocks * p.d;
+  float sum = 0.f;
+  if (c < p.d)
+    for (int i = part; i < n; i += kWarps) sum += in[(int64_t)i * p.d + c];
+  __shared__ float red[kWarps][32];
+  red[part][lane] = sum;
+  __syncthreads();
+  if (part == 0 && c < p.d) {
+#pragma unroll
+    for (int k = 1; k < kWarps; ++k) sum += red[k][lane];
+    s.dw[c * s.dw_s] = sum;
+  }
+}
+
+// ------------------------------------------------------------- launches
+bool run_fits(const void* base, int bytes, int V, bool used_b, int64_t sb, bool used_h, int64_t sh, bool used_t,
+              int64_t st, int64_t sd) {
+  const int access = V * bytes;
+  return sd == 1 && reinterpret_cast<uintptr_t>(base) % 16 == 0 && (!used_b || sb * bytes % access == 0) &&
+         (!used_h || sh * bytes % access == 0) && (!used_t || st * bytes % access == 0);
+}
+// Whether the fast kernels take these rows (a stride of a dim of size 1 is not used).
+bool fast_ok(const NormParams& p, int in_bytes, int out_bytes, int g_bytes) {
+  const int V = 16 / in_bytes, items = p.d / (2 * V);
+  if (p.d % (2 * V) != 0 || p.rot % (2 * V) != 0 || items > 32 || (items & (items - 1)) != 0) return false;
+  for (int i = 0; i < p.n_sets; ++i) {
+    const NormSet& s = p.set[i];
+    const bool ub = p.B > 1, uh = s.heads > 1, ut = p.T > 1;
+    if (!run_fits(s.x, in_bytes, V, ub, s.x_b, uh, s.x_h, ut, s.x_t, s.x_d) ||
+        !run_fits(s.y, out_bytes, V, ub, s.y_b, uh, s.y_h, ut, s.y_t, s.y_d) ||
+        (g_bytes && !run_fits(s.g, g_bytes, V, ub, s.g_b, uh, s.g_h, ut, s.g_t, s.g_d)))
+      return false;
+    // (stores of 8 floats are one access of 32 bytes)
+    if (V * out_bytes == 32 && reinterpret_cast<uintptr_t>(s.y) % 32 != 0) return false;
+  }
+  return true;
+}
+
+int set_groups(NormParams* p, int hg) {
+  p->hg = hg < 1 ? 1 : (hg > kMostHeads ? kMostHeads : hg);
+  int n = 0;
+  for (int i = 0; i < p->n_sets; ++i) n += p->groups[i] = (p->set[i].heads + p->hg - 1) / p->hg;
+  return n;
+}
+int most_heads(const NormParams& p) {
+  return p.n_sets > 1 && p.set[1].heads > p.set[0].heads ? p.set[1].heads : p.set[0].heads;
+}
+
+template <typename TI, typename TO, bool INTER>
+cudaError_t launch_forward(NormParams p, cudaStream_t stream) {
+  constexpr int V = 16 / sizeof(TI);
+  if (fast_ok(p, sizeof(TI), sizeof(TO), 0)) {
+    const int64_t n = (int64_t)p.B * p.T * (p.d / (2 * V));
+    const int64_t blocks = (n + kThreads - 1) / kThreads;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;  // (more elements than the card holds)
+    const int64_t want = (kFillBlocks + blocks - 1) / blocks;  // groups that fill the machine
+    int groups = set_groups(&p, (int)((most_heads(p) + want - 1) / want));
+    if (groups > 65535) groups = set_groups(&p, kMostHeads);
+    const int smem = p.hg * 32 * kThreads;
+    if (smem > 48 * 1024) {
+      static DeviceOnce once;
+      if (cudaError_t e = once.set_smem(reinterpret_cast<const void*>(&norm_kernel<TI, TO, V, INTER>),
+                                        kMostHeads * 32 * kThreads);
+          e != cudaSuccess)
+        return e;
+    }
+    norm_kernel<TI, TO, V, INTER><<<dim3((unsigned)blocks, (unsigned)groups), kThreads, smem, stream>>>(p);
+    return cudaGetLastError();
+  }
+  const int64_t rows = (int64_t)p.B * p.T * (p.set[0].heads + (p.n_sets > 1 ? p.set[1].heads : 0));
+  const int64_t blocks = (rows + kWarps - 1) / kWarps;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  norm_rows_kernel<TI, TO, INTER><<<(unsigned)blocks, kThreads, kWarps * p.d * sizeof(float), stream>>>(p);
+  return cudaGetLastError();
+}
+
+// The grid of the backward kernel, the same for every type: set_groups and
+// `blocks` in *p.  Blocks along the tokens so that the machine is full once
+// (two resident blocks an SM; every block costs a row of partial sums).
+bool plan_backward(NormParams* p, int in_bytes, int out_bytes, int g_bytes, int sms) {
+  const bool fast = fast_ok(*p, in_bytes, out_bytes, g_bytes);
+  int groups = p->n_sets;
+  int64_t most;
+  if (fast) {
+    const int per_block = kThreads / (p->d / (32 / in_bytes));
+    groups = set_groups(p, kMostHeads);
+    most = ((int64_t)p->B * p->T + per_block - 1) / per_block;
+  } else {
+    p->groups[0] = p->groups[1] = 1;
+    most = ((int64_t)p->B * p->T * most_heads(*p) + kWarps - 1) / kWarps;
+  }
+  int64_t blocks = (2 * sms + groups - 1) / groups;
+  if (blocks > most) blocks = most;
+  p->blocks = (int)(blocks < 1 ? 1 : blocks);
+  return fast;
+}
+
+template <typename TX, typename TG, typename TO, bool INTER>
+cudaError_t launch_backward_t(const NormParams& p, bool fast, cudaStream_t stream) {
+  constexpr int V = 16 / sizeof(TX);
+  const int groups = p.groups[0] + (p.n_sets > 1 ? p.groups[1] : 0);
+  const dim3 grid((unsigned)p.blocks, (unsigned)groups);
+  if (groups == 0) {  // no heads at all: dw is zeros
+  } else if (fast) {
+    norm_bwd_kernel<TX, TG, TO, V, INTER><<<grid, kThreads, 0, stream>>>(p);
+  } else {
+    const int smem = 2 * kWarps * p.d * (int)sizeof(float);
+    if (smem > 48 * 1024) {
+      static DeviceOnce once;
+      if (cudaError_t e = once.set_smem(reinterpret_cast<const void*>(&norm_bwd_rows_kernel<TX, TG, TO, INTER>),
+                                        2 * kWarps * (int)kMaxDim * (int)sizeof(float));
+          e != cudaSuccess)
+        return e;
+    }
+    norm_bwd_rows_kernel<TX, TG, TO, INTER><<<grid, kThreads, smem, stream>>>(p);
+  }
+  if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((p.d + 31) / 32), (unsigned)p.n_sets);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;  // scheduled while the backward kernel drains
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sum_dw_kernel, p);
+}
+template <typename TX, typename TG, typename TO>
+cudaError_t launch_backward_l(const NormParams& p, bool fast, bool inter, cudaStream_t stream) {
+  return inter ? launch_backward_t<TX, TG, TO, true>(p, fast, stream)
+               : launch_backward_t<TX, TG, TO, false>(p, fast, stream);
+}
+template <typename TX>
+cudaError_t launch_backward_x(const NormParams& p, bool fast, int32_t g, int32_t out, bool inter, cudaStream_t stream) {
+  if (g == BLKATTN_F32)
+    return out == BLKATTN_F32 ? launch_backward_l<TX, float, float>(p, fast, inter, stream)
+                              : launch_backward_l<TX, float, __nv_bfloat16>(p, fast, inter, stream);
+  return out == BLKATTN_F32 ? launch_backward_l<TX, __nv_bfloat16, float>(p, fast, inter, stream)
+                            : launch_backward_l<TX, __nv_bfloat16, __nv_bfloat16>(p, fast, inter, stream);
+}
+
+template <typename TI, typename TO>
+cudaError_t launch_forward_l(const NormParams& p, bool inter, cudaStream_t stream) {
+  return inter ? launch_forward<TI, TO, true>(p, stream) : launch_forward<TI, TO, false>(p, stream);
+}
+
+// ------------------------------------------------------------- arguments
+int bytes_of(int32_t t) { return t == BLKATTN_BF16 ? 2 : 4; }
+
+// x, y (and g) of one shape; y writable.
+int check_set(const blkattn_tensor* x, const blkattn_tensor* w, const blkattn_tensor* y, const blkattn_tensor* g,
+              const blkattn_tensor* dw) {
+  if (!tensor_dims_ok(x, 4) || !tensor_dims_ok(w, 1) || !tensor_dims_ok(y, 4)) return BLKATTN_ERR_INVALID_ARG;
+  if (!floats(x) || !floats(w) || !floats(y) || w->sizes[0] != x->sizes[3]) return BLKATTN_ERR_INVALID_ARG;
+  for (int i = 0; i < 4; ++i)
+    if (x->sizes[i] != y->sizes[i]) return BLKATTN_ERR_INVALID_ARG;
+  if (!writable(y) || !in_place_ok(g ? g : x, y)) return BLKATTN_ERR_INVALID_ARG;
+  if (!g) return BLKATTN_OK;
+  if (!tensor_dims_ok(g, 4) || !floats(g) || !tensor_dims_ok(dw, 1) || dw->dtype != BLKATTN_F32 ||
+      dw->sizes[0] != x->sizes[3] || !writable(dw))
+    return BLKATTN_ERR_INVALID_ARG;
+  for (int i = 0; i < 4; ++i)
+    if (g->sizes[i] != x->sizes[i]) return BLKATTN_ERR_INVALID_ARG;
+  return BLKATTN_OK;
+}
+
+struct Call {
+  const blkattn_tensor *x[2], *w[2], *y[2], *g[2], *dw[2];
+  const blkattn_tensor *pos, *ph;
+  int32_t layout;
+  float mscale, eps;
+};
+
+void fill_set(NormSet* s, const Call& c, int i) {
+  auto four = [](const blkattn_tensor* t, int64_t& b, int64_t& h, int64_t& n, int64_t& d) {
+    b = t->strides[0]; h = t->strides[1]; n = t->strides[2]; d = t->strides[3];
+  };
+  s->x = c.x[i]->data;
+  four(c.x[i], s->x_b, s->x_h, s->x_t, s->x_d);
+  s->w = c.w[i]->data;
+  s->w_s = c.w[i]->strides[0];
+  s->y = c.y[i]->data;
+  four(c.y[i], s->y_b, s->y_h, s->y_t, s->y_d);
+  s->heads = (int)c.x[i]->sizes[1];
+  if (!c.g[i]) return;
+  s->g = c.g[i]->data;
+  four(c.g[i], s->g_b, s->g_h, s->g_t, s->g_d);
+  s->dw = static_cast<float*>(c.dw[i]->data);
+  s->dw_s = c.dw[i]->strides[0];
+}
+
+int norm(const Call& c, bool back, blkattn_stream_t stream_) {
+  // the second set: all of it or none
+  const bool two = c.x[1] != nullptr;
+  if (two != (c.w[1] != nullptr) || two != (c.y[1] != nullptr) ||
+      (back && (two != (c.g[1] != nullptr) || two != (c.dw[1] != nullptr))))
+    return BLKATTN_ERR_INVALID_ARG;
+  if (back && c.g[0] == nullptr) return BLKATTN_ERR_INVALID_ARG;
+  const int n_sets = two ? 2 : 1;
+  for (int i = 0; i < n_sets; ++i)
+    if (int st = check_set(c.x[i], c.w[i], c.y[i], c.g[i], c.dw[i]); st != BLKATTN_OK) return st;
+  const int64_t B = c.x[0]->sizes[0], T = c.x[0]->sizes[2], d = c.x[0]->sizes[3];
+  if (!tensor_dims_ok(c.pos, 2) || c.pos->dtype != BLKATTN_I32 || c.pos->sizes[0] != B || c.pos->sizes[1] != T || d < 1)
+    return BLKATTN_ERR_INVALID_ARG;
+  if (two) {
+    // one type and one shape but for the heads
+    for (int i : {0, 2, 3})
+      if (c.x[1]->sizes[i] != c.x[0]->sizes[i]) return BLKATTN_ERR_INVALID_ARG;
+    if (c.x[1]->dtype != c.x[0]->dtype || c.w[1]->dtype != c.w[0]->dtype || c.y[1]->dtype != c.y[0]->dtype ||
+        (back && c.g[1]->dtype != c.g[0]->dtype))
+      return BLKATTN_ERR_INVALID_ARG;
+    if (c.y[0]->data == c.y[1]->data && c.y[0]->data != nullptr) return BLKATTN_ERR_INVALID_ARG;
+    if (back && c.dw[0]->data == c.dw[1]->data && c.dw[0]->data != nullptr) return BLKATTN_ERR_INVALID_ARG;
+  }
+  if (c.ph) {
+    if (int st = check_phases(c.ph, c.layout, d); st != BLKATTN_OK) return st;
+    if (!finite(c.mscale)) return BLKATTN_ERR_INVALID_ARG;
+  }
+  if (!finite(c.eps) || c.eps < 0.f) return BLKATTN_ERR_INVALID_ARG;
+  if (!tensors_on_one_device(c.x[0], {c.x[1], c.w[0], c.w[1], c.y[0], c.y[1], c.g[0], c.g[1], c.dw[0], c.dw[1], c.pos, c.ph}))
+    return BLKATTN_ERR_INVALID_ARG;
+  int64_t heads = 0;
+  for (int i = 0; i < n_sets; ++i) {
+    if (c.x[i]->sizes[1] > 0x7fff) return BLKATTN_ERR_UNSUPPORTED;
+    heads += c.x[i]->sizes[1];
+  }
+  if (d > kMaxDim || B > 0x7fffffff || T > 0x7fffffff || (B > 0 && T > 0x7fffffff / B)) return BLKATTN_ERR_UNSUPPORTED;
+  const bool rows = B > 0 && T > 0 && heads > 0;
+  if (!rows && !back) return BLKATTN_OK;
+  for (int i = 0; i < n_sets; ++i) {
+    if (c.w[i]->data == nullptr || (back && c.dw[i]->data == nullptr)) return BLKATTN_ERR_INVALID_ARG;
+    if (B > 0 && T > 0 && c.x[i]->sizes[1] > 0 &&
+        (c.x[i]->data == nullptr || c.y[i]->data == nullptr || (back && c.g[i]->data == nullptr)))
+      return BLKATTN_ERR_INVALID_ARG;
+  }
+  if (rows && ((c.pos->data == nullptr && c.ph) || (c.ph && c.ph->data == nullptr))) return BLKATTN_ERR_INVALID_ARG;
+  if (int st = require_current_device(c.x[0]->device); st != BLKATTN_OK) return st;
+  NormParams p{};
+  p.n_sets = n_sets;
+  for (int i = 0; i < n_sets; ++i) fill_set(&p.set[i], c, i);
+  p.pos = static_cast<const int32_t*>(c.pos->data);
+  p.p_b = c.pos->strides[0]; p.p_t = c.pos->strides[1];
+  if (c.ph) {
+    p.phases = static_cast<const int64_t*>(c.ph->data);
+    p.ph_s = c.ph->strides[0];
+    p.rot = (int)(2 * c.ph->sizes[0]);
+  }
+  p.w_f32 = c.w[0]->dtype == BLKATTN_F32;
+  p.mscale = c.mscale;
+  p.eps = c.eps;
+  p.d = (int)d; p.B = (int)B; p.T = (int)T;
+  p.inv_d = 1.f / (float)d;
+  const bool inter = c.ph && c.layout == BLKATTN_ROPE_INTERLEAVED;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const int32_t ti = c.x[0]->dtype, to = c.y[0]->dtype;
+  if (!back) {
+    // (a set without heads takes no place)
+    if (p.set[0].heads == 0) p.set[0] = p.set[1];
+    if (p.n_sets == 2 && (p.set[1].heads == 0 || c.x[0]->sizes[1] == 0)) p.n_sets = 1;
+    cudaError_t e;
+    if (ti == BLKATTN_BF16)
+      e = to == BLKATTN_BF16 ? launch_forward_l<__nv_bfloat16, __nv_bfloat16>(p, inter, stream)
+                             : launch_forward_l<__nv_bfloat16, float>(p, inter, stream);
+    else
+      e = to == BLKATTN_BF16 ? launch_forward_l<float, __nv_bfloat16>(p, inter, stream)
+                             : launch_forward_l<float, float>(p, inter, stream);
+    return e == cudaSuccess ? BLKATTN_OK : report_cuda_failure(e);
+  }
+  const int32_t tg = c.g[0]->dtype;
+  const Library lib;
+  int sms = 0;
+  if (int st = lib.sms(&sms); st != BLKATTN_OK) return st;
+  const bool fast = plan_backward(&p, bytes_of(ti), bytes_of(to), bytes_of(tg), sms);
+  void* ws = nullptr;
+  const int64_t groups = p.groups[0] + (p.n_sets > 1 ? p.groups[1] : 0);
+  if (int st = lib.workspace((size_t)(groups * p.blocks * d) * sizeof(float), stream, &ws); st != BLKATTN_OK) return st;
+  p.ws = static_cast<float*>(ws);
+  const cudaError_t e = ti == BLKATTN_BF16 ? launch_backward_x<__nv_bfloat16>(p, fast, tg, to, inter, stream)
+                                           : launch_backward_x<float>(p, fast, tg, to, inter, stream);
+  return e == cudaSuccess ? BLKATTN_OK : report_cuda_failure(e);
+}
+
+}  // namespace
+}  // namespace blkattn
+
+extern "C" {
+
+int blkattn_qk_norm_rope(const blkattn_tensor* q, const blkattn_tensor* q_weight, const blkattn_tensor* k,
+                         const blkattn_tensor* k_weight, const blkattn_tensor* pos, const blkattn_tensor* phases,
+                         int32_t layout, float mscale, float eps, const blkattn_tensor* q_out,
+                         const blkattn_tensor* k_out, blkattn_stream_t stream) {
+  const blkattn::Call c{{q, k}, {q_weight, k_weight}, {q_out, k_out}, {}, {}, pos, phases, layout, mscale, eps};
+  return blkattn::norm(c, false, stream);
+}
+
+int blkattn_qk_norm_rope_bwd(const blkattn_tensor* dq_out, const blkattn_tensor* dk_out, const blkattn_tensor* q,
+                             const blkattn_tensor* q_weight, const blkattn_tensor* k, const blkattn_tensor* k_weight,
+                             const blkattn_tensor* pos, const blkattn_tensor* phases, int32_t layout, float mscale,
+                             float eps, const blkattn_tensor* dq, const blkattn_tensor* dk,
+                             const blkattn_tensor* dq_weight, const blkattn_tensor* dk_weight,
+                             blkattn_stream_t stream) {
+  const blkattn::Call c{{q, k},     {q_weight, k_weight},   {dq, dk}, {dq_out, dk_out}, {dq_weight, dk_weight},
+                        pos,        phases,                 layout,   mscale,           eps};
+  return blkattn::norm(c, true, stream);
+}
+
+}  // extern "C"

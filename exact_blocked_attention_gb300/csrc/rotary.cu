@@ -25,6 +25,7 @@
 #include "kernels.h"
 #include "paged.h"
 #include "ptx.cuh"
+#include "rotary.cuh"
 
 namespace blkattn {
 namespace {
@@ -56,22 +57,6 @@ struct RotaryParams {
   PageTable pages;
 };
 
-template <typename T>
-__device__ __forceinline__ float to_f32(T x) { return static_cast<float>(x); }
-template <>
-__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename T>
-__device__ __forceinline__ T from_f32(float x) { return static_cast<T>(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-
-// sin and cos of position t at phase F.
-__device__ __forceinline__ void turn_of(int t, int64_t F, float& sn, float& cs) {
-  const uint64_t a = (uint64_t)(int64_t)t * (uint64_t)F;
-  // the top 32 bits: a signed fraction of half a turn in [-1, 1)
-  sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &sn, &cs);
-}
-
 constexpr int kThreads = 256;
 constexpr int kRegHeads = 4;  // V < 8: heads whose loads a thread has in flight
 // Blocks below which a thread takes fewer heads, so that every SM has its
@@ -79,76 +64,11 @@ constexpr int kRegHeads = 4;  // V < 8: heads whose loads a thread has in flight
 // six heads; eight heads' 64 KB allow three)
 constexpr int kFillBlocks = 152 * 4;
 
-// V elements of a row in registers, moved as one access.
-template <typename T, int V>
-struct alignas(sizeof(T) * V > 16 ? 16 : sizeof(T) * V) Vec {
-  T x[V];
-};
-template <typename T, int V>
-__device__ __forceinline__ void store(T* p, const Vec<T, V>& y) {
-  if constexpr (sizeof(T) * V == 32) {
-    // 8 floats in one 32-byte store (whole sectors)
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(y.x[0]), "f"(y.x[1]),
-                 "f"(y.x[2]), "f"(y.x[3]), "f"(y.x[4]), "f"(y.x[5]), "f"(y.x[6]), "f"(y.x[7])
-                 : "memory");
-  } else {
-    *reinterpret_cast<Vec<T, V>*>(p) = y;
-  }
-}
-
-// Waits until at most n (0..7, a constant after unrolling) of the thread's
-// groups of asynchronous copies are pending.
-__device__ __forceinline__ void wait_copies(int n) {
-  switch (n) {
-    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
-  }
-}
-
 // Runs of 16 bytes go through slots in shared memory, shorter ones through
 // registers.
 template <typename TI, int V>
 constexpr bool kSlots = sizeof(TI) * V == 16;
 constexpr int kMostHeads = 8;  // heads of one thread: 64 KB of slots a block
-
-template <typename TI, typename TO, int V, bool INTER>
-__device__ __forceinline__ void turn_run(const Vec<TI, V>& x0, const Vec<TI, V>& x1, bool turn, const float (&sn)[V],
-                                         const float (&cs)[V], Vec<TO, V>& y0, Vec<TO, V>& y1) {
-  // elements of both runs in order: pair j is (j, V + j) or the neighbours (2j, 2j + 1)
-  float u[2 * V], w[2 * V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    u[j] = to_f32(x0.x[j]);
-    u[V + j] = to_f32(x1.x[j]);
-  }
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int a = INTER ? 2 * j : j, b = INTER ? 2 * j + 1 : V + j;
-    w[a] = turn ? u[a] * cs[j] - u[b] * sn[j] : u[a];
-    w[b] = turn ? u[a] * sn[j] + u[b] * cs[j] : u[b];
-  }
-  if constexpr (sizeof(TO) == 2 && V > 1) {
-    uint32_t* q0 = reinterpret_cast<uint32_t*>(&y0);
-    uint32_t* q1 = reinterpret_cast<uint32_t*>(&y1);
-#pragma unroll
-    for (int j = 0; j < V / 2; ++j) {
-      q0[j] = pack_bf16(w[2 * j], w[2 * j + 1]);
-      q1[j] = pack_bf16(w[V + 2 * j], w[V + 2 * j + 1]);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      y0.x[j] = from_f32<TO>(w[j]);
-      y1.x[j] = from_f32<TO>(w[V + j]);
-    }
-  }
-}
 
 // One thread turns one item of a token's rows, in `hg` heads: two runs of V
 // dims, one from each half of the rotated part (HALF: V pairs across them;
@@ -357,33 +277,6 @@ cudaError_t launch_rotary(const RotaryParams& p, int32_t in, int32_t out, bool i
 }
 
 // ------------------------------------------------------------- validation
-constexpr int64_t kMaxDim = 1024;
-
-bool floats(const blkattn_tensor* t) { return t->dtype == BLKATTN_BF16 || t->dtype == BLKATTN_F32; }
-
-// No two elements of a tensor that is written share an address through a
-// broadcast dim.
-bool writable(const blkattn_tensor* t) {
-  bool ok = true, empty = false;
-  for (int i = 0; i < t->ndim; ++i) {
-    empty = empty || t->sizes[i] == 0;
-    ok = ok && !(t->sizes[i] > 1 && t->strides[i] == 0);
-  }
-  return ok || empty;
-}
-
-// Rows of the same shape at one address: the call may work in place only on
-// the very same view.
-bool in_place_ok(const blkattn_tensor* a, const blkattn_tensor* b) {
-  if (a->data != b->data) return true;
-  if (a->dtype != b->dtype) return false;
-  for (int i = 0; i < a->ndim; ++i)
-    if (a->sizes[i] > 1 && a->strides[i] != b->strides[i]) return false;
-  return true;
-}
-
-bool finite(float x) { return x - x == 0.f; }
-
 void set_src(RowSet* s, const blkattn_tensor* t) {
   s->src = t->data;
   s->s_b = t->strides[0]; s->s_h = t->strides[1]; s->s_t = t->strides[2]; s->s_d = t->strides[3];
@@ -392,14 +285,6 @@ void set_src(RowSet* s, const blkattn_tensor* t) {
 void set_dst(RowSet* s, const blkattn_tensor* t) {
   s->dst = t->data;
   s->d_b = t->strides[0]; s->d_h = t->strides[1]; s->d_t = t->strides[2]; s->d_d = t->strides[3];
-}
-
-// Phases [rot / 2] int64, rot <= d; and the layout.
-int check_phases(const blkattn_tensor* ph, int32_t layout, int64_t d) {
-  if (layout != BLKATTN_ROPE_HALF && layout != BLKATTN_ROPE_INTERLEAVED) return BLKATTN_ERR_INVALID_ARG;
-  if (!tensor_dims_ok(ph, 1) || ph->dtype != BLKATTN_I64 || ph->sizes[0] < 1 || 2 * ph->sizes[0] > d)
-    return BLKATTN_ERR_INVALID_ARG;
-  return BLKATTN_OK;
 }
 
 int rope(const blkattn_tensor* x, const blkattn_tensor* pos, const blkattn_tensor* ph, int32_t layout, float mscale,

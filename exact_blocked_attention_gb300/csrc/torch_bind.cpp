@@ -1,5 +1,5 @@
-// Argument marshalling of the serving-step operators (rope, paged append,
-// attention over pages) for torch tensors: descriptors straight from the
+// Argument marshalling of the serving-step operators (rope, head norms, paged
+// append, attention over pages) for torch tensors: descriptors straight from the
 // tensor objects, outputs allocated, the current stream looked up, then one
 // call into libblkattn's C ABI.  A decode step's kernels take a few
 // microseconds; building nine descriptors in Python took longer than that.
@@ -25,6 +25,11 @@ namespace {
 decltype(&blkattn_rope) g_rope, g_rope_bwd;
 decltype(&blkattn_paged_append) g_append;
 decltype(&blkattn_fwd_paged) g_fwd;
+decltype(&blkattn_qk_norm_rope) g_norm;
+decltype(&blkattn_qk_norm_rope_bwd) g_norm_bwd;
+decltype(&blkattn_paged_append_q8) g_append_q8;
+decltype(&blkattn_paged_read_q8) g_read_q8;
+decltype(&blkattn_fwd_paged_q8) g_fwd_q8;
 
 // A descriptor of a tensor argument; None gives a NULL pointer.
 class Desc {
@@ -47,6 +52,8 @@ class Desc {
       case at::kFloat: d_.dtype = BLKATTN_F32; break;
       case at::kInt: d_.dtype = BLKATTN_I32; break;
       case at::kLong: d_.dtype = BLKATTN_I64; break;
+      case at::kFloat8_e4m3fn: d_.dtype = BLKATTN_E4M3; break;
+      case at::kFloat8_e8m0fnu: d_.dtype = BLKATTN_E8M0; break;
       default: TORCH_CHECK_VALUE(false, "blkattn: unsupported dtype ", t.scalar_type());
     }
     TORCH_CHECK_VALUE(t.dim() <= 4, "blkattn: at most 4 dimensions");
@@ -144,12 +151,14 @@ PyObject* again(PyObject* o) {
   return o;
 }
 
-// init(rope, rope_bwd, paged_append, fwd_paged): addresses in libblkattn
+// init(rope, rope_bwd, paged_append, fwd_paged, qk_norm_rope, qk_norm_rope_bwd, paged_append_q8, paged_read_q8,
+//      fwd_paged_q8): addresses in libblkattn
 PyObject* bind_init(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  count(n, 4);
-  void* f[4];
-  for (int i = 0; i < 4; ++i) {
+  constexpr int kEntries = 9;
+  count(n, kEntries);
+  void* f[kEntries];
+  for (int i = 0; i < kEntries; ++i) {
     f[i] = PyLong_AsVoidPtr(a[i]);
     if (f[i] == nullptr) {
       if (PyErr_Occurred()) throw python_error();
@@ -160,6 +169,11 @@ PyObject* bind_init(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_rope_bwd = reinterpret_cast<decltype(g_rope_bwd)>(f[1]);
   g_append = reinterpret_cast<decltype(g_append)>(f[2]);
   g_fwd = reinterpret_cast<decltype(g_fwd)>(f[3]);
+  g_norm = reinterpret_cast<decltype(g_norm)>(f[4]);
+  g_norm_bwd = reinterpret_cast<decltype(g_norm_bwd)>(f[5]);
+  g_append_q8 = reinterpret_cast<decltype(g_append_q8)>(f[6]);
+  g_read_q8 = reinterpret_cast<decltype(g_read_q8)>(f[7]);
+  g_fwd_q8 = reinterpret_cast<decltype(g_fwd_q8)>(f[8]);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
@@ -222,11 +236,126 @@ PyObject* bind_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// An output argument: the given object, or, for None, a fresh tensor.
+class Out {
+ public:
+  Out(PyObject* given, const CallStream& stream, at::IntArrayRef sizes, const at::TensorOptions& options, bool zeros = false)
+      : given_(given), d_(given == Py_None ? Desc(made_ = stream.fresh(sizes, options, zeros)) : Desc(given)) {}
+  explicit Out(PyObject* none) : given_(none), d_(none) {}  // an output that the call does without
+  const blkattn_tensor* get() const { return d_.get(); }
+  PyObject* object() const { return made_.defined() ? THPVariable_Wrap(made_) : again(given_); }
+
+ private:
+  at::Tensor made_;
+  PyObject* given_;
+  Desc d_;
+};
+
+// norm(q, k or None, wq, wk or None, pos, phases or None, layout, mscale, eps, out_dtype or None, q_out or None,
+//      k_out or None, stream or None) -> (status, q_out, k_out)
+PyObject* bind_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 13);
+  const at::Tensor& q = tensor_of(a[0]);
+  const Desc dq(q), dk(a[1]), wq(a[2]), wk(a[3]), pos(a[4]), ph(a[5]);
+  const CallStream stream(a[12], q);
+  const auto options = q.options().dtype(dtype_of(a[9], q.scalar_type()));
+  const Out qo(a[10], stream, q.sizes(), options);
+  const Out ko = a[1] == Py_None ? Out(a[11]) : Out(a[11], stream, tensor_of(a[1]).sizes(), options);
+  const int st = g_norm(dq.get(), wq.get(), dk.get(), wk.get(), pos.get(), ph.get(), (int32_t)integer(a[6]),
+                        (float)number(a[7]), (float)number(a[8]), qo.get(), ko.get(), stream.get());
+  return answer(st, {qo.object(), ko.object()});
+  END_HANDLE_TH_ERRORS
+}
+
+// norm_bwd(dq_out, dk_out or None, q, k or None, wq, wk or None, pos, phases or None, layout, mscale, eps,
+//          out_dtype or None, dq or None, dk or None, stream or None) -> (status, dq, dk, dq_weight, dk_weight)
+PyObject* bind_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 15);
+  const at::Tensor& q = tensor_of(a[2]);
+  const at::Tensor& w = tensor_of(a[4]);
+  const Desc gq(a[0]), gk(a[1]), dq(q), dk(a[3]), wq(a[4]), wk(a[5]), pos(a[6]), ph(a[7]);
+  const CallStream stream(a[14], q);
+  const auto options = q.options().dtype(dtype_of(a[11], q.scalar_type()));
+  const auto sums = q.options().dtype(at::kFloat);
+  const bool two = a[3] != Py_None;
+  const Out oq(a[12], stream, q.sizes(), options);
+  const Out ok = two ? Out(a[13], stream, tensor_of(a[3]).sizes(), options) : Out(a[13]);
+  const Out owq(Py_None, stream, w.sizes(), sums);
+  const Out owk = two ? Out(Py_None, stream, w.sizes(), sums) : Out(Py_None);
+  const int st = g_norm_bwd(gq.get(), gk.get(), dq.get(), wq.get(), dk.get(), wk.get(), pos.get(), ph.get(),
+                            (int32_t)integer(a[8]), (float)number(a[9]), (float)number(a[10]), oq.get(), ok.get(),
+                            owq.get(), owk.get(), stream.get());
+  return answer(st, {oq.object(), ok.object(), owq.object(), owk.object()});
+  END_HANDLE_TH_ERRORS
+}
+
+// append_q8(k, v, pos, table, k_pages, v_pages, k_scales, v_scales, phases or None, layout, mscale, k_weight or None,
+//           q_weight or None, eps, q or None, q_out or None, stream or None) -> (status, q_out, as append)
+PyObject* bind_append_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 17);
+  const at::Tensor& k = tensor_of(a[0]);
+  const Desc dk(k), v(a[1]), pos(a[2]), table(a[3]), kp(a[4]), vp(a[5]), ks(a[6]), vs(a[7]), ph(a[8]), wk(a[11]),
+      wq(a[12]), q(a[14]);
+  const CallStream stream(a[16], k);
+  // (zeros: the rows of padding are not written)
+  const Out qo = q.given() ? Out(a[15], stream, tensor_of(a[14]).sizes(), tensor_of(a[14]).options(), true) : Out(a[15]);
+  const int st = g_append_q8(dk.get(), v.get(), pos.get(), table.get(), kp.get(), vp.get(), ks.get(), vs.get(),
+                             wk.get(), (float)number(a[13]), ph.get(), (int32_t)integer(a[9]), (float)number(a[10]),
+                             q.get(), wq.get(), qo.get(), stream.get());
+  return answer(st, {qo.object()});
+  END_HANDLE_TH_ERRORS
+}
+
+// read_q8(pos, table, k_pages, v_pages, k_scales, v_scales, out_dtype or None, k_out or None, v_out or None,
+//         stream or None) -> (status, k_out, v_out)
+PyObject* bind_read_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 10);
+  const at::Tensor& kp = tensor_of(a[2]);
+  const at::Tensor& tp = tensor_of(a[0]);
+  const Desc pos(tp), table(a[1]), dk(kp), vp(a[3]), ks(a[4]), vs(a[5]);
+  TORCH_CHECK_VALUE(kp.dim() == 4 && tp.dim() == 2, "blkattn: pos is [B, T], the pools [N, H_kv, P, d]");
+  const CallStream stream(a[9], kp);
+  const int64_t sizes[4] = {tp.size(0), kp.size(1), tp.size(1), kp.size(3)};
+  const auto options = kp.options().dtype(dtype_of(a[6], at::kBFloat16));
+  const Out ko(a[7], stream, sizes, options), vo(a[8], stream, sizes, options);
+  const int st = g_read_q8(pos.get(), table.get(), dk.get(), vp.get(), ks.get(), vs.get(), ko.get(), vo.get(),
+                           stream.get());
+  return answer(st, {ko.object(), vo.object()});
+  END_HANDLE_TH_ERRORS
+}
+
+// fwd_q8(q, k_pages, v_pages, k_scales, v_scales, table, seqlens, qpos, tree or None, window, scale or None,
+//        out or None, lse or None, out_dtype or None, stream or None) -> (status, out, lse)
+PyObject* bind_fwd_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 15);
+  const at::Tensor& q = tensor_of(a[0]);
+  const Desc dq(q), kp(a[1]), vp(a[2]), ks(a[3]), vs(a[4]), table(a[5]), sl(a[6]), qp(a[7]), tree(a[8]);
+  TORCH_CHECK_VALUE(q.dim() == 4, "blkattn: q is [B, H_q, T_q, d]");
+  const CallStream stream(a[14], q);
+  const Out out(a[11], stream, q.sizes(), q.options().dtype(dtype_of(a[13], at::kFloat)));
+  const Out lse(a[12], stream, q.sizes().slice(0, 3), q.options().dtype(at::kFloat));
+  const float scale = a[10] == Py_None ? (float)(1.0 / std::sqrt((double)q.size(3))) : (float)number(a[10]);
+  const int st = g_fwd_q8(dq.get(), kp.get(), vp.get(), ks.get(), vs.get(), table.get(), sl.get(), qp.get(), tree.get(),
+                          integer(a[9]), scale, out.get(), lse.get(), stream.get());
+  return answer(st, {out.object(), lse.object()});
+  END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef kMethods[] = {
     {"init", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind_init)), METH_FASTCALL, nullptr},
     {"rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind_rope)), METH_FASTCALL, nullptr},
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind_append)), METH_FASTCALL, nullptr},
     {"fwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind_fwd)), METH_FASTCALL, nullptr},
+    {"norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind_norm)), METH_FASTCALL, nullptr},
+    {"norm_bwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind_norm_bwd)), METH_FASTCALL, nullptr},
+    {"append_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind_append_q8)), METH_FASTCALL, nullptr},
+    {"read_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind_read_q8)), METH_FASTCALL, nullptr},
+    {"fwd_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind_fwd_q8)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_torch_bind", "libblkattn calls on torch tensors", -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

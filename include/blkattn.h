@@ -64,7 +64,9 @@ enum {
   BLKATTN_BF16 = 1,  /* bfloat16 */
   BLKATTN_F32 = 2,   /* IEEE binary32 */
   BLKATTN_I32 = 3,   /* int32 */
-  BLKATTN_I64 = 4    /* int64 (token-tree node masks) */
+  BLKATTN_I64 = 4,   /* int64 (token-tree node masks, phases) */
+  BLKATTN_E4M3 = 5,  /* 8 bits: sign, 4 exponent and 3 fraction bits; finite to 448, 0x7f and 0xff are NaN */
+  BLKATTN_E8M0 = 6   /* 8 bits: the power of two 2^(byte - 127); 255 is NaN */
 };
 
 /*
@@ -81,7 +83,7 @@ enum {
  */
 typedef struct {
   void* data;
-  int32_t dtype;      /* BLKATTN_BF16 | BLKATTN_F32 | BLKATTN_I32 | BLKATTN_I64 */
+  int32_t dtype;      /* BLKATTN_BF16 | _F32 | _I32 | _I64 | _E4M3 | _E8M0 */
   int32_t ndim;
   int64_t sizes[4];
   int64_t strides[4];
@@ -386,6 +388,52 @@ int blkattn_rope_bwd(const blkattn_tensor* dy, const blkattn_tensor* pos, const 
                      int32_t layout, float mscale, const blkattn_tensor* dx, blkattn_stream_t stream);
 
 /*
+ * blkattn_qk_norm_rope — RMS norm of every query and key head's row, then its
+ * rotary position, in one pass:
+ *     y = R(pos) (w x / sqrt(mean(x^2) + eps)),  the mean over the row's d dims
+ * with R the rotation of blkattn_rope (mscale on its dims).
+ *
+ * q, k    [B, H_q, T, d] and [B, H_k, T, d], bf16 or f32 (the same), any
+ *         strides, d <= 1024.  k, k_weight, k_out may be NULL together.
+ * q_weight, k_weight  [d] bf16 or f32 (the same): the norms' weights.
+ * pos     [B, T] int32, as for blkattn_rope.
+ * phases  NULL (no rotation; pos and layout are then not read) or as for
+ *         blkattn_rope, with layout and mscale.
+ * eps     finite, >= 0.  (A row of zeros with eps = 0 gives NaN.)
+ * q_out, k_out  of q's and k's shape, bf16 or f32 (the same), any strides but
+ *         no broadcast dim: written.  Each may be its input itself (same
+ *         address, dtype and strides); any other overlap is out of contract.
+ * Computed in fp32, rounded once.  One kernel, no workspace, any stream; calls
+ * on different streams are independent.  Sizes of 0 are a no-op.  Returns as
+ * blkattn_rope; BLKATTN_ERR_UNSUPPORTED for d > 1024, more than 32767 heads or
+ * B T > 2^31 - 1.
+ *
+ * blkattn_qk_norm_rope_bwd — its gradients.  With g = R^T dy, h = x r,
+ * r = 1 / sqrt(mean(x^2) + eps) and c = w g:
+ *     dx = r (c - h mean(c h)),    dw = sum of g h over all rows and heads.
+ * q, k, weights, pos, phases, layout, mscale, eps: the forward call's (q and k
+ * as they were before it).
+ * dq_out, dk_out  the gradients of q_out and k_out: bf16 or f32 (the same),
+ *         any strides (blkattn_bwd writes f32).  dk_out NULL as k.
+ * dq, dk  bf16 or f32 (the same), no broadcast dim: written; each may be its
+ *         dq_out or dk_out itself.
+ * dq_weight, dk_weight  f32 [d]: written (zeros where there are no rows).
+ * The sums over rows are fp32 in a fixed order (deterministic).  Two kernels;
+ * the library's workspace holds the blocks' sums, so growth and overlap of
+ * calls are as for blkattn_fwd.  Returns as blkattn_qk_norm_rope.
+ */
+int blkattn_qk_norm_rope(const blkattn_tensor* q, const blkattn_tensor* q_weight, const blkattn_tensor* k,
+                         const blkattn_tensor* k_weight, const blkattn_tensor* pos, const blkattn_tensor* phases,
+                         int32_t layout, float mscale, float eps, const blkattn_tensor* q_out,
+                         const blkattn_tensor* k_out, blkattn_stream_t stream);
+int blkattn_qk_norm_rope_bwd(const blkattn_tensor* dq_out, const blkattn_tensor* dk_out, const blkattn_tensor* q,
+                             const blkattn_tensor* q_weight, const blkattn_tensor* k, const blkattn_tensor* k_weight,
+                             const blkattn_tensor* pos, const blkattn_tensor* phases, int32_t layout, float mscale,
+                             float eps, const blkattn_tensor* dq, const blkattn_tensor* dk,
+                             const blkattn_tensor* dq_weight, const blkattn_tensor* dk_weight,
+                             blkattn_stream_t stream);
+
+/*
  * The paged KV cache.  K and V live in pools of pages [N, H_kv, P, d] (any
  * strides: [N, P, H_kv, d] memory is a view of it); row t of sequence b is
  * row t mod P of page page_table[b, t / P].  An entry outside [0, N) holds no
@@ -454,6 +502,81 @@ int blkattn_fwd_paged(const blkattn_tensor* q, const blkattn_tensor* k_pages, co
                       const blkattn_tensor* page_table, const blkattn_tensor* seqlens_k,
                       const blkattn_tensor* q_logical_pos, const blkattn_tensor* tree_mask, int64_t window,
                       float scale, const blkattn_tensor* out, const blkattn_tensor* lse, blkattn_stream_t stream);
+
+/*
+ * The 8-bit paged cache.  Pools of pages as above, but k_pages and v_pages hold
+ * BLKATTN_E4M3 [N, H_kv, P, d] (d = 64 or 128; last stride 1, the other strides
+ * and the base addresses multiples of 16), and k_scales, v_scales
+ * BLKATTN_E8M0 [N, H_kv, P / S] (any strides but no broadcast dim) hold one
+ * power of two 2^e for each block of S rows of a page and head: a number
+ * stands for e4m3 2^e, exactly a bf16.  S is a power of two, 1 <= S <= 128, and
+ * divides P (greater S give BLKATTN_ERR_UNSUPPORTED).
+ *
+ * blkattn_paged_append_q8 — blkattn_paged_append into that cache, with the head
+ * norms of blkattn_qk_norm_rope on the way.
+ *
+ * k, v, pos, page_table, phases, layout, mscale, q, q_out: as for
+ *             blkattn_paged_append; k and q are of one dtype, bf16 or f32.
+ * k_weight, q_weight, eps  each weight NULL (no norm) or as for
+ *             blkattn_qk_norm_rope (both of one dtype): k and q are normed
+ *             before they turn.
+ * A block's exponent is the least with every number within 448 2^e (at least
+ * -127), taken of the finite new numbers in fp32.  A call that writes a block's
+ * first row begins the block anew: its exponent comes from that call's rows
+ * alone, and the block's other bytes stay and stand for nothing until they are
+ * written.  Any other call keeps the exponent or raises it, and then rounds the
+ * block's other rows again (exact but for the smallest numbers).  Numbers are
+ * rounded once from fp32 to the nearest e4m3; infinities and NaN become NaN.
+ * The rows of a sequence that are not padding have positions that do not
+ * descend with t; of rows that name the same cache row the last is kept.  Rows
+ * in another order leave the blocks concerned with any contents.  Two sequences
+ * of a call must not write the same block.  The new rows must not overlap the
+ * pools.  One kernel, no workspace, any stream.  Returns as blkattn_rope.
+ *
+ * blkattn_paged_read_q8 — rows of the cache as numbers.
+ *
+ * pos         [B, T] int32, any strides, in any order: the cache rows wanted.
+ * k_out, v_out  [B, H_kv, T, d] bf16 or f32 (the same), any strides but no
+ *             broadcast dim: written; zeros for a negative position and for
+ *             one past the table or on an entry that holds no page.
+ * Returns as blkattn_rope; BLKATTN_ERR_UNSUPPORTED for B > 65535 or more than
+ * 32767 heads.
+ */
+int blkattn_paged_append_q8(const blkattn_tensor* k, const blkattn_tensor* v, const blkattn_tensor* pos,
+                            const blkattn_tensor* page_table, const blkattn_tensor* k_pages,
+                            const blkattn_tensor* v_pages, const blkattn_tensor* k_scales,
+                            const blkattn_tensor* v_scales, const blkattn_tensor* k_weight, float eps,
+                            const blkattn_tensor* phases, int32_t layout, float mscale, const blkattn_tensor* q,
+                            const blkattn_tensor* q_weight, const blkattn_tensor* q_out, blkattn_stream_t stream);
+int blkattn_paged_read_q8(const blkattn_tensor* pos, const blkattn_tensor* page_table, const blkattn_tensor* k_pages,
+                          const blkattn_tensor* v_pages, const blkattn_tensor* k_scales,
+                          const blkattn_tensor* v_scales, const blkattn_tensor* k_out, const blkattn_tensor* v_out,
+                          blkattn_stream_t stream);
+
+/*
+ * blkattn_fwd_paged_q8 — blkattn_fwd_paged over the 8-bit cache.
+ *
+ * q           [B, H_q, T_q, d] bf16, any strides.
+ * k_pages, v_pages, k_scales, v_scales  the 8-bit cache, as above.
+ * page_table, seqlens_k, q_logical_pos, tree_mask, window, scale, out, lse,
+ * stream: as for blkattn_fwd_paged, with its visibility.  What a row between
+ * the earliest and the latest key that query rows of one sequence see holds
+ * must not be NaN, except tree nodes that no row lists; every other row of the
+ * pools and its scales may hold anything.
+ * Precision: the cache's numbers are exact, sums and statistics fp32.  Weights
+ * enter the value product with f16's 11 bits for a bf16 out and 22 bits for an
+ * f32 out, relative to the row's largest weight times its scale; bf16 prompts
+ * with the same out go through the kernel of blkattn_fwd_paged and have its
+ * precision.  A row with a NaN among the scores of its visible keys gives NaN
+ * in out and lse; the other rows are not touched by it.
+ * Workspace, growth and overlap of calls as for blkattn_fwd.  Returns as
+ * blkattn_fwd_paged.
+ */
+int blkattn_fwd_paged_q8(const blkattn_tensor* q, const blkattn_tensor* k_pages, const blkattn_tensor* v_pages,
+                         const blkattn_tensor* k_scales, const blkattn_tensor* v_scales,
+                         const blkattn_tensor* page_table, const blkattn_tensor* seqlens_k,
+                         const blkattn_tensor* q_logical_pos, const blkattn_tensor* tree_mask, int64_t window,
+                         float scale, const blkattn_tensor* out, const blkattn_tensor* lse, blkattn_stream_t stream);
 
 /*
  * Attention states of rows, in the sufficient statistics of eq. 33.3:

@@ -1167,8 +1167,14 @@ int fwd_paged_q8_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages, c
   p.q_vec = c.q_vec_ok;
   p.k = static_cast<const char*>(kn.data);
   p.v = static_cast<const char*>(vn.data);
-  p.k_sn = kn.strides[0]; p.k_sh = kn.strides[1]; p.k_sr = kn.strides[2];
-  p.v_sn = vn.strides[0]; p.v_sh = vn.strides[1]; p.v_sr = vn.strides[2];
+  // (the kernel keeps a row's offset within a head as 32 bits of 16 bytes)
+  for (const blkattn_tensor* t : {&kn, &vn})
+    if (t->strides[0] / 16 > 0xffffffffLL || t->strides[2] / 16 > 0xffffffffLL ||
+        (unsigned __int128)(t->sizes[0] - 1) * (t->strides[0] / 16) + (unsigned __int128)(pt.rows - 1) * (t->strides[2] / 16) >
+            0xffffffffu)
+      return BLKATTN_ERR_UNSUPPORTED;
+  p.k_sn16 = (uint32_t)(kn.strides[0] / 16); p.k_sh = kn.strides[1]; p.k_sr16 = (uint32_t)(kn.strides[2] / 16);
+  p.v_sn16 = (uint32_t)(vn.strides[0] / 16); p.v_sh = vn.strides[1]; p.v_sr16 = (uint32_t)(vn.strides[2] / 16);
   p.k_sc = static_cast<const unsigned char*>(k_scales->data);
   p.v_sc = static_cast<const unsigned char*>(v_scales->data);
   p.ke_sn = k_scales->strides[0]; p.ke_sh = k_scales->strides[1]; p.ke_si = k_scales->strides[2];

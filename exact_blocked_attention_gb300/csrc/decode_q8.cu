@@ -29,7 +29,7 @@
 //                                       interleaved), B = P^T (S transposed in
 //                                       registers)
 //
-// Work split: tiles of 128 keys (16 a warp) of all (sequence, KV head, row
+// Work split: tiles of 256 keys (32 a warp) of all (sequence, KV head, row
 // group) units in order, cut into equal ranges, one a CTA; a warp keeps its own
 // statistics, joined when a unit ends.  A unit that lies in several CTAs leaves
 // partial states, and the CTA that arrives last joins them in order.
@@ -50,8 +50,8 @@ constexpr float kLazyM = 8.f, kLazyR = 4.f;
 constexpr float kLift = 11.f;  // weights reach 2^(kLift + kLazyR) = 2^15 in f16
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStep = 16;                // keys of a warp in a tile
-constexpr int kTile = kStep * kWarps;
+constexpr int kOwn = 32;               // keys of a warp in a tile: two products of 16, side by side
+constexpr int kTile = kOwn * kWarps;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -79,11 +79,9 @@ __device__ __forceinline__ void copy8(uint32_t dst, const void* src, int n) {
 
 template <int D, int NT>
 struct Q8Layout {
-  // (tiles in flight: 8 or, with two resident CTAs of 8 rows, 16 warps of 4 KB each)
-  static constexpr int kStages = NT == 1 ? 2 : 3;
   static constexpr int kRows = 8 * NT;
-  static constexpr int kStageBytes = kStep * D * 2;  // a warp's keys, K and V
-  static constexpr int kRing = kWarps * kStages * kStageBytes;
+  static constexpr int kHalf = kOwn * D;             // K, then V, of a warp's keys in a tile
+  static constexpr int kRing = kWarps * 2 * kHalf;
   static constexpr int kPad = D + 4;
   static constexpr int kOffU = kRing;                             // float [kWarps][kRows][kPad]
   static constexpr int kOffStat = kOffU + kWarps * kRows * kPad * 4;  // float [3][kWarps][kRows]
@@ -112,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_q8_kernel(co
   float* s_row = reinterpret_cast<float*>(sm + L::kOffRow);
   uint64_t* s_seen = reinterpret_cast<uint64_t*>(sm + L::kOffTab);  // [B] tree nodes that some row lists
   int* s_end = reinterpret_cast<int*>(s_seen + p.B);  // [B] keys that some row sees are [start, end)
-  int* s_start = s_end + p.B;                            // (a multiple of kStep)
+  int* s_start = s_end + p.B;                            // (a multiple of kOwn)
   int* s_nt = s_start + p.B;
   int* s_tree = s_nt + p.B;  // [B] key of the tree's first node
   int* s_pre = s_tree + p.B;  // [B + 1] tiles before the sequence
@@ -138,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_q8_kernel(co
         start = min(start, f);
       }
     }
-    start = end > 0 ? start & ~(kStep - 1) : 0;
+    start = end > 0 ? start & ~(kOwn - 1) : 0;
     s_seen[b] = seen;
     s_tree[b] = p.tree ? len - p.Tq : 0x7fffffff;
     s_end[b] = end;
@@ -221,68 +219,69 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_q8_kernel(co
     } while (a.nt == 0);
   };
 
-  // ---- the stream: a tile's page numbers, then its rows and scales, ahead of its use
-  unsigned char* ring = sm + warp * (L::kStages * L::kStageBytes);
-  auto key0_of = [&](const Place& a) { return s_start[a.b] + a.j * kTile + warp * kStep; };
-  // page of key (lane mod 16) of the warp's, -1: none, or no row sees the key
-  // (past the end, a tree node that no row lists: its row may hold anything)
-  auto look_up = [&](const Place& a) {
-    const int key = key0_of(a) + (lane & 15), node = key - s_tree[a.b];
-    if (key >= s_end[a.b] || (node >= 0 && !((s_seen[a.b] >> node) & 1))) return -1;
-    return page_of(p.pages, a.b, key);
+  // ---- the stream: a tile's page numbers and scales ahead of its rows, those ahead of their use
+  unsigned char* ring = sm + warp * (2 * L::kHalf);
+  const uint32_t ring_k = smem_u32(ring) + lane * 16, ring_v = smem_u32(ring) + L::kHalf + lane * VB;
+  auto key0_of = [&](const Place& a) { return s_start[a.b] + a.j * kTile + warp * kOwn; };
+  // What lane i knows of the warp's key i in a tile.
+  struct Keys {
+    int key0;        // of the warp
+    uint32_t any;    // lanes whose key some row sees and has a page; the others' rows may hold anything
+    uint32_t ko, vo; // offsets of the key's rows in the pools, in 16 bytes
+    int ek, ev;      // scale bytes, on their way
   };
-  auto issue = [&](const Place& a, int pg, int stage) {  // returns the lane's scale byte
-    const int key0 = key0_of(a), mask = p.pages.rows - 1;
-    const uint32_t dst = smem_u32(ring + stage * L::kStageBytes);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int pr = __shfl_sync(0xffffffffu, pg, g + 8 * r);
-      const char* src = p.k + (int64_t)max(pr, 0) * p.k_sn + a.kvh * p.k_sh + ((key0 + g + 8 * r) & mask) * p.k_sr + 16 * t4;
-#pragma unroll
-      for (int h = 0; h < KL; ++h) copy16(dst + (r * KL + h) * 512 + lane * 16, src + 64 * h, pr < 0 ? 0 : 16);
+  auto look_up = [&](const Place& a, Keys& k) {
+    k.key0 = key0_of(a);
+    const int key = k.key0 + lane, node = key - s_tree[a.b];
+    // (past the end, or a tree node that no row lists: not seen)
+    const bool seen = key < s_end[a.b] && (node < 0 || ((s_seen[a.b] >> node) & 1));
+    const int page = seen ? page_of(p.pages, a.b, key) : -1;
+    const int row = key & (p.pages.rows - 1);
+    k.ek = k.ev = 127;
+    k.ko = k.vo = 0;
+    if (page >= 0) {
+      const int blk = row >> p.scale_shift;
+      k.ek = p.k_sc[(int64_t)page * p.ke_sn + a.kvh * p.ke_sh + blk * p.ke_si];
+      k.ev = p.v_sc[(int64_t)page * p.ve_sn + a.kvh * p.ve_sh + blk * p.ve_si];
+      k.ko = (uint32_t)page * p.k_sn16 + (uint32_t)row * p.k_sr16;
+      k.vo = (uint32_t)page * p.v_sn16 + (uint32_t)row * p.v_sr16;
     }
+    k.any = __ballot_sync(0xffffffffu, page >= 0);
+  };
+  // K rows g + 8 r, 16 t4 bytes in; V rows 8 r + 2 t4 and the next, VB g bytes in
+  auto issue_k = [&](const Place& a, const Keys& k) {
+    const char* base = p.k + a.kvh * p.k_sh + 16 * t4;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int kk = 2 * t4 + (r & 1) + 8 * (r >> 1);
-      const int pr = __shfl_sync(0xffffffffu, pg, kk);
-      const char* src = p.v + (int64_t)max(pr, 0) * p.v_sn + a.kvh * p.v_sh + ((key0 + kk) & mask) * p.v_sr + VB * g;
-      const uint32_t at = dst + 2 * KL * 512 + r * (32 * VB) + lane * VB;
-      if constexpr (VB == 16) copy16(at, src, pr < 0 ? 0 : 16);
-      else copy8(at, src, pr < 0 ? 0 : 8);
+      const char* src = base + (uint64_t)__shfl_sync(0xffffffffu, k.ko, g + 8 * r) * 16;
+      const int n = k.any == 0xffffffffu || ((k.any >> (g + 8 * r)) & 1) ? 16 : 0;
+#pragma unroll
+      for (int c = 0; c < KL; ++c) copy16(ring_k + (r * KL + c) * 512, src + 64 * c, n);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    // lanes 0-15: the scale of K of key `lane`; 16-31: of V
-    int e = 127;
-    if (pg >= 0) {
-      const int blk = ((key0 + (lane & 15)) & mask) >> p.scale_shift;
-      e = lane < 16 ? p.k_sc[(int64_t)pg * p.ke_sn + a.kvh * p.ke_sh + blk * p.ke_si]
-                    : p.v_sc[(int64_t)pg * p.ve_sn + a.kvh * p.ve_sh + blk * p.ve_si];
-    }
-    return e;
+  };
+  auto issue_v = [&](const Place& a, const Keys& k) {
+    const char* base = p.v + a.kvh * p.v_sh + VB * g;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int key = 8 * r + 2 * t4 + c;
+        const char* src = base + (uint64_t)__shfl_sync(0xffffffffu, k.vo, key) * 16;
+        const int n = k.any == 0xffffffffu || ((k.any >> key) & 1) ? VB : 0;
+        const uint32_t dst = ring_v + (2 * r + c) * (32 * VB);
+        if constexpr (VB == 16) copy16(dst, src, n);
+        else copy8(dst, src, n);
+      }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
   Place ahead = place_of(t0), cur = ahead;
   const int n = t1 - t0;
-  int pg_next = look_up(ahead);
-  int pg[L::kStages], sc[L::kStages];  // of the tiles in flight, the oldest first
-  int issued = 0;
-  auto issue_next = [&](int slot) {
-    pg[slot] = -1;
-    sc[slot] = 127;
-    if (issued < n) {
-      pg[slot] = pg_next;
-      sc[slot] = issue(ahead, pg_next, issued % L::kStages);
-      if (issued + 1 < n) {
-        next(ahead);
-        pg_next = look_up(ahead);
-      }
-    } else {
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-    ++issued;
-  };
-#pragma unroll
-  for (int i = 0; i < L::kStages - 1; ++i) issue_next(i);
+  Keys nxt;
+  look_up(ahead, nxt);
+  issue_k(ahead, nxt);
+  issue_v(ahead, nxt);
 
   // ---- one unit's state in this warp
   float U[NT][MT][4];
@@ -507,79 +506,101 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_q8_kernel(co
 
   bool fresh = true;
   for (int s = 0; s < n; ++s) {
-    issue_next(L::kStages - 1);
     if (fresh) begin_unit();
-    asm volatile("cp.async.wait_group %0;" ::"n"(L::kStages - 1) : "memory");
-    const unsigned char* st = ring + (s % L::kStages) * L::kStageBytes;
-    const int key0 = key0_of(cur);
-    if (key0 < s_end[cur.b]) {
-      // ---- scores of 16 keys
-      float S[NT][4];
+    const Keys now = nxt;
+    const bool more = s + 1 < n;
+    if (more) {
+      next(ahead);
+      look_up(ahead, nxt);
+    }
+    if (now.any == 0) {  // (nothing to see for this warp)
+      asm volatile("cp.async.wait_group 0;" ::: "memory");  // (its zeros, before the slots' next rows)
+      if (more) {
+        issue_k(ahead, nxt);
+        issue_v(ahead, nxt);
+      }
+    } else {
+      // ---- scores of two times 16 keys
+      float S[2][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) S[nt][0] = S[nt][1] = S[nt][2] = S[nt][3] = 0.f;
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) S[x][nt][0] = S[x][nt][1] = S[x][nt][2] = S[x][nt][3] = 0.f;
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
 #pragma unroll
       for (int c = 0; c < KL; ++c) {
-        const uint4 x0 = *reinterpret_cast<const uint4*>(st + c * 512 + lane * 16);
-        const uint4 x1 = *reinterpret_cast<const uint4*>(st + (KL + c) * 512 + lane * 16);
-        const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
+        uint4 w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t a0 = e4m3x2_to_h2(w0[k] & 0xffffu), a2 = e4m3x2_to_h2(w0[k] >> 16);
-          const uint32_t a1 = e4m3x2_to_h2(w1[k] & 0xffffu), a3 = e4m3x2_to_h2(w1[k] >> 16);
+        for (int r = 0; r < 4; ++r) w[r] = *reinterpret_cast<const uint4*>(ring + (r * KL + c) * 512 + lane * 16);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16(S[nt], a0, a1, a2, a3, Q[nt][4 * c + k][0], Q[nt][4 * c + k][1]);
-        }
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_h2((&w[2 * x].x)[k], a0, a2);
+            e4m3x4_to_h2((&w[2 * x + 1].x)[k], a1, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(S[x][nt], a0, a1, a2, a3, Q[nt][4 * c + k][0], Q[nt][4 * c + k][1]);
+          }
       }
-      float ks[2], ev[2];
-      int page_r[2];
+      // (K's rows are in the products: the next ones may land)
+      if (more) issue_k(ahead, nxt);
+      else asm volatile("cp.async.commit_group;" ::: "memory");
+      const float my_ks = scale_of(now.ek);
+      const float my_ev = now.ev == 255 ? __uint_as_float(0x7fc00000u) : (float)(now.ev - 127);
+      // (every key seen by every row: no mask)
+      const bool whole = now.any == 0xffffffffu && now.key0 + kOwn <= min_end && now.key0 >= max_first &&
+                         now.key0 + kOwn <= tree_base;
+      float ev[4];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        ks[r] = scale_of(__shfl_sync(0xffffffffu, sc[0], g + 8 * r));
-        const int e = __shfl_sync(0xffffffffu, sc[0], 16 + g + 8 * r);
-        ev[r] = e == 255 ? __uint_as_float(0x7fc00000u) : (float)(e - 127);
-        page_r[r] = __shfl_sync(0xffffffffu, pg[0], g + 8 * r);
+      for (int r = 0; r < 4; ++r) {
+        const float ks = __shfl_sync(0xffffffffu, my_ks, 8 * r + g);
+        ev[r] = __shfl_sync(0xffffffffu, my_ev, 8 * r + g);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) S[r >> 1][nt][2 * (r & 1) + c] *= ks * fac[nt][c];
       }
-      const bool whole = __all_sync(0xffffffffu, pg[0] >= 0) && key0 + kStep <= min_end && key0 >= max_first &&
-                         key0 + kStep <= tree_base;
+      if (!whole) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int key = now.key0 + g + 8 * r;
+              bool see = ((now.any >> (8 * r + g)) & 1) && key < r_end[nt][c] && key >= r_first[nt][c];
+              if (see && key >= tree_base) {
+                int h, i;
+                out_row(cur.b, cur.kvh, row0 + 8 * nt + 2 * t4 + c, h, i);
+                see = (p.tree[cur.b * p.tr_sb + i * p.tr_si] >> (key - tree_base)) & 1;
+              }
+              if (!see) S[r >> 1][nt][2 * (r & 1) + c] = kNegInf;
+            }
+      }
       bool raise = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = k >> 1, c = k & 1;
-          float z = S[nt][k] * (ks[r] * fac[nt][c]);
-          if (!whole) {
-            const int key = key0 + g + 8 * r;
-            bool see = page_r[r] >= 0 && key < r_end[nt][c] && key >= r_first[nt][c];
-            if (see && key >= tree_base) {
-              int h, i;
-              out_row(cur.b, cur.kvh, row0 + 8 * nt + 2 * t4 + c, h, i);
-              see = (p.tree[cur.b * p.tr_sb + i * p.tr_si] >> (key - tree_base)) & 1;
-            }
-            z = see ? z : kNegInf;
-          }
-          S[nt][k] = z;
-        }
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           // (no key seen yet: M is -inf, and any score raises it)
           const float m = M[nt][c] == kNegInf ? 0.f : M[nt][c];
-          const float z0 = S[nt][c] - m, z1 = S[nt][2 + c] - m;
-          raise |= fmaxf(z0, z1) > (M[nt][c] == kNegInf ? kNegInf : kLazyM);
-          raise |= fmaxf(z0 + ev[0], z1 + ev[1]) > R[nt][c] + kLazyR;
+          const float z0 = S[0][nt][c] - m, z1 = S[0][nt][2 + c] - m, z2 = S[1][nt][c] - m, z3 = S[1][nt][2 + c] - m;
+          raise |= fmaxf(fmaxf(z0, z1), fmaxf(z2, z3)) > (M[nt][c] == kNegInf ? kNegInf : kLazyM);
+          raise |= fmaxf(fmaxf(z0 + ev[0], z1 + ev[1]), fmaxf(z2 + ev[2], z3 + ev[3])) > R[nt][c] + kLazyR;
         }
-      }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float zm = fmaxf(S[nt][c], S[nt][2 + c]);
+            float zm = fmaxf(fmaxf(S[0][nt][c], S[0][nt][2 + c]), fmaxf(S[1][nt][c], S[1][nt][2 + c]));
 #pragma unroll
             for (int off = 4; off <= 16; off <<= 1) zm = fmaxf(zm, __shfl_xor_sync(0xffffffffu, zm, off));
             const float m = fmaxf(M[nt][c], zm), m0 = m == kNegInf ? 0.f : m;
             ls[nt][c] *= M[nt][c] == m ? 1.f : fast_exp2(M[nt][c] - m);
-            float ym = fmaxf(S[nt][c] - m0 + ev[0], S[nt][2 + c] - m0 + ev[1]);
+            float ym = fmaxf(fmaxf(S[0][nt][c] - m0 + ev[0], S[0][nt][2 + c] - m0 + ev[1]),
+                             fmaxf(S[1][nt][c] - m0 + ev[2], S[1][nt][2 + c] - m0 + ev[3]));
 #pragma unroll
             for (int off = 4; off <= 16; off <<= 1) ym = fmaxf(ym, __shfl_xor_sync(0xffffffffu, ym, off));
             const float old = moved(R[nt][c], M[nt][c], m), r = fmaxf(old, ym);
@@ -594,60 +615,65 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_q8_kernel(co
           }
       }
       // ---- weights, as the value product's B fragments
-      uint32_t hi[NT][2], lo[NT][2];
+      uint32_t hi[2][NT][2], lo[2][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float w[4];
+        float m[2], lift[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int c = k & 1;
-          const float z = S[nt][k] - (M[nt][c] == kNegInf ? 0.f : M[nt][c]);
-          ls[nt][c] += fast_exp2(z);
-          w[k] = fast_exp2(z + (ev[k >> 1] - (R[nt][c] == kNegInf ? 0.f : R[nt][c]) + kLift));
+        for (int c = 0; c < 2; ++c) {
+          m[c] = M[nt][c] == kNegInf ? 0.f : M[nt][c];
+          lift[c] = kLift - (R[nt][c] == kNegInf ? 0.f : R[nt][c]);
         }
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const uint32_t h2 = pack_h2(w[2 * r], w[2 * r + 1]);
-          hi[nt][r] = transposed(h2);
+        for (int r = 0; r < 4; ++r) {
+          float w[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float z = S[r >> 1][nt][2 * (r & 1) + c] - m[c];
+            ls[nt][c] += fast_exp2(z);
+            w[c] = fast_exp2(z + (ev[r] + lift[c]));
+          }
+          const uint32_t h2 = pack_h2(w[0], w[1]);
+          hi[r >> 1][nt][r & 1] = transposed(h2);
           if constexpr (FINE) {
             const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-            lo[nt][r] = transposed(pack_h2(w[2 * r] - b.x, w[2 * r + 1] - b.y));
+            lo[r >> 1][nt][r & 1] = transposed(pack_h2(w[0] - b.x, w[1] - b.y));
           }
         }
       }
       // ---- values: bytes of two keys side by side, then as f16
-      uint32_t v[4][VB / 4];
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      constexpr int kWords = VB / 4;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const unsigned char* at = st + 2 * KL * 512 + r * (32 * VB) + lane * VB;
-        if constexpr (VB == 16) {
-          const uint4 x = *reinterpret_cast<const uint4*>(at);
-          v[r][0] = x.x; v[r][1] = x.y; v[r][2] = x.z; v[r][3] = x.w;
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(at);
-          v[r][0] = x.x; v[r][1] = x.y;
-        }
-      }
+      for (int x = 0; x < 2; ++x) {
+        uint32_t v[4][kWords];
 #pragma unroll
-      for (int q4 = 0; q4 < VB / 4; ++q4) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t sel = half ? 0x7362 : 0x5140;
-          const uint32_t x = __byte_perm(v[0][q4], v[1][q4], sel), z = __byte_perm(v[2][q4], v[3][q4], sel);
-          const uint32_t a0 = e4m3x2_to_h2(x & 0xffffu), a1 = e4m3x2_to_h2(x >> 16);
-          const uint32_t a2 = e4m3x2_to_h2(z & 0xffffu), a3 = e4m3x2_to_h2(z >> 16);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_f16(U[nt][2 * q4 + half], a0, a1, a2, a3, hi[nt][0], hi[nt][1]);
-            if constexpr (FINE) mma_f16(U[nt][2 * q4 + half], a0, a1, a2, a3, lo[nt][0], lo[nt][1]);
+        for (int r = 0; r < 4; ++r) {
+          const unsigned char* at = ring + L::kHalf + (4 * x + r) * (32 * VB) + lane * VB;
+          if constexpr (VB == 16) {
+            const uint4 y = *reinterpret_cast<const uint4*>(at);
+            v[r][0] = y.x; v[r][1] = y.y; v[r][2] = y.z; v[r][3] = y.w;
+          } else {
+            const uint2 y = *reinterpret_cast<const uint2*>(at);
+            v[r][0] = y.x; v[r][1] = y.y;
           }
         }
-      }
-    }
 #pragma unroll
-    for (int i = 0; i + 1 < L::kStages; ++i) {
-      pg[i] = pg[i + 1];
-      sc[i] = sc[i + 1];
+        for (int q4 = 0; q4 < kWords; ++q4)
+#pragma unroll
+          for (int odd = 0; odd < 2; ++odd) {
+            const uint32_t sel = odd ? 0x7362 : 0x5140;
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_h2(__byte_perm(v[0][q4], v[1][q4], sel), a0, a1);
+            e4m3x4_to_h2(__byte_perm(v[2][q4], v[3][q4], sel), a2, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16(U[nt][2 * q4 + odd], a0, a1, a2, a3, hi[x][nt][0], hi[x][nt][1]);
+              if constexpr (FINE) mma_f16(U[nt][2 * q4 + odd], a0, a1, a2, a3, lo[x][nt][0], lo[x][nt][1]);
+            }
+          }
+      }
+      if (more) issue_v(ahead, nxt);
     }
     fresh = cur.j + 1 == cur.nt || s + 1 == n;
     if (fresh) end_unit(s);

@@ -170,9 +170,10 @@ struct Q8Params {
   const void* q;  // bf16 rows; element strides
   int64_t q_sb, q_sh, q_si, q_sd;
   bool q_vec;  // unit dim stride, 16-byte aligned rows
-  const char* k;  // e4m3 pools: strides of page, head and row in page
+  const char* k;  // e4m3 pools: strides of page and row in page, and of head
   const char* v;
-  int64_t k_sn, k_sh, k_sr, v_sn, v_sh, v_sr;
+  uint32_t k_sn16, k_sr16, v_sn16, v_sr16;  // in 16 bytes: a pool spans less than 64 GiB
+  int64_t k_sh, v_sh;
   const unsigned char* k_sc;  // e8m0 scales: strides of page, head and block
   const unsigned char* v_sc;
   int64_t ke_sn, ke_sh, ke_si, ve_sn, ve_sh, ve_si;

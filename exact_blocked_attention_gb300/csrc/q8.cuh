@@ -40,6 +40,15 @@ __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t w) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)w));
   return r;
 }
+// Four e4m3 of a word as f16: the lower two, the upper two.
+__device__ __forceinline__ void e4m3x4_to_h2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
 __device__ __forceinline__ float2 e4m3x2_to_f2(uint32_t w) {
   const uint32_t h = e4m3x2_to_h2(w);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));

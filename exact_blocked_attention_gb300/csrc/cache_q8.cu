@@ -16,10 +16,13 @@
 // the blocks whose run begins in it, panels of max(S, 16) cache rows at a time:
 // the panel's angles go to shared memory once, then each warp takes a head of K
 // or V: 16 dims a lane, 512 / d rows a pass; the first sweep finds the rows'
-// maxima, the second quantises.  Up to four passes stay in registers between
-// the sweeps, more are computed again from rows that the L1 holds.
+// maxima, the second quantises.  A lane's first new row stays in registers
+// between the sweeps (a decode step has no other), the others are computed again
+// from rows that the L1 holds.
 //
-// Memory bounds a prompt's append, latency a decode step's.
+// Latency bounds a decode step's append: one launch, the query rows in CTAs of
+// their own.  Memory bounds a prompt's, most of it the query rows': from
+// kOwnKernelRows on they go to the norm kernel, which keeps more rows in flight.
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -36,7 +39,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kKvHeads = 4;   // KV heads of a CTA: K and V of each, a warp each
 constexpr int kQHeads = 32;   // query heads of a CTA
-constexpr int kHeld = 4;      // passes of a panel kept in registers
+// query rows from which on they have a kernel of their own
+constexpr int64_t kOwnKernelRows = 16384;
 
 struct Rows {
   const void* p;
@@ -186,7 +190,7 @@ template <int D, bool RUNS>
 constexpr int kStage = RUNS ? 0 : kWarps * Lane<D>::kRows * D;  // floats
 
 template <typename T, int D, bool RUNS, bool INTER, bool VEC>
-__global__ void __launch_bounds__(kThreads) append_q8_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_constant__ AppendParams p) {
   extern __shared__ __align__(16) float smem[];
   float* stage_all = smem;
   float2* cs = reinterpret_cast<float2*>(smem + kStage<D, RUNS>);  // [panel rows][rot / 2]
@@ -331,22 +335,18 @@ __global__ void __launch_bounds__(kThreads) append_q8_kernel(const __grid_consta
         }
         if (l.it == 0 && r < p.panel) amax[warp][r] = a;
       };
-      float held[kHeld][16];
-      bool is_new[kHeld];
-      const bool hold = passes <= kHeld;
-      if (hold) {
+      // the maxima; each lane's first new row stays in registers for the second sweep
+      float held[16];
+      int k_held = -1;
+      for (int k = 0; k < passes; ++k) {
+        const int r = k * Lane<D>::kRows + l.slot;
+        float x[16];
+        const bool nw = values(r, x);
+        row_max(r, nw, x);
+        if (nw && k_held < 0) {
+          k_held = k;
 #pragma unroll
-        for (int k = 0; k < kHeld; ++k) {
-          const int r = k * Lane<D>::kRows + l.slot;
-          is_new[k] = k < passes && values(r, held[k]);
-          if (k < passes) row_max(r, is_new[k], held[k]);
-        }
-      } else {
-        for (int k = 0; k < passes; ++k) {
-          const int r = k * Lane<D>::kRows + l.slot;
-          float x[16];
-          const bool nw = values(r, x);
-          row_max(r, nw, x);
+          for (int j = 0; j < 16; ++j) held[j] = x[j];
         }
       }
       __syncwarp();
@@ -393,13 +393,11 @@ __global__ void __launch_bounds__(kThreads) append_q8_kernel(const __grid_consta
         *reinterpret_cast<uint2*>(o + l.a0) = y0;
         *reinterpret_cast<uint2*>(o + l.a1) = y1;
       };
-      if (hold) {
-#pragma unroll
-        for (int k = 0; k < kHeld; ++k)
-          if (k < passes) put(k * Lane<D>::kRows + l.slot, is_new[k], held[k]);
-      } else {
-        for (int k = 0; k < passes; ++k) {
-          const int r = k * Lane<D>::kRows + l.slot;
+      for (int k = 0; k < passes; ++k) {
+        const int r = k * Lane<D>::kRows + l.slot;
+        if (k == k_held) {
+          put(r, true, held);
+        } else {
           float x[16];
           const bool nw = values(r, x);
           put(r, nw, x);
@@ -691,7 +689,7 @@ int blkattn_paged_append_q8(const blkattn_tensor* k, const blkattn_tensor* v, co
     p.q_out = q_out_opt->data;
     p.o_b = q_out_opt->strides[0]; p.o_h = q_out_opt->strides[1];
     p.o_t = q_out_opt->strides[2]; p.o_d = q_out_opt->strides[3];
-    vec = vec && vec_rows(q_opt) && vec_rows(q_out_opt);
+    if (B * T * Hq < kOwnKernelRows) vec = vec && vec_rows(q_opt) && vec_rows(q_out_opt);
   }
   if (q_weight_opt) { p.wq = q_weight_opt->data; p.wq_s = q_weight_opt->strides[0]; }
   if (k_weight_opt) { p.wk = k_weight_opt->data; p.wk_s = k_weight_opt->strides[0]; }
@@ -713,7 +711,8 @@ int blkattn_paged_append_q8(const blkattn_tensor* k, const blkattn_tensor* v, co
   p.pages = pt;
   const int64_t blocks = B * ((T + p.panel - 1) / p.panel);
   if (blocks > 0x7fffffff) return BLKATTN_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)blocks, (unsigned)(p.kv_groups + (Hq + kQHeads - 1) / kQHeads));
+  const bool own = B * T * Hq >= kOwnKernelRows;
+  const dim3 grid((unsigned)blocks, (unsigned)(p.kv_groups + (own ? 0 : (Hq + kQHeads - 1) / kQHeads)));
   const bool inter = layout == BLKATTN_ROPE_INTERLEAVED;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   cudaError_t e;
@@ -723,6 +722,8 @@ int blkattn_paged_append_q8(const blkattn_tensor* k, const blkattn_tensor* v, co
   else
     e = d == 128 ? launch_append<float, 128>(p, inter, vec, grid, stream)
                  : launch_append<float, 64>(p, inter, vec, grid, stream);
+  if (e == cudaSuccess && own)
+    e = launch_query_rows(q_opt, q_weight_opt, pos, phases_opt, layout, mscale, eps, q_out_opt, stream);
   return e == cudaSuccess ? BLKATTN_OK : report_cuda_failure(e);
 }
 

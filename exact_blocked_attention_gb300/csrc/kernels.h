@@ -165,6 +165,12 @@ size_t decode_tc_smem_bytes(int rows_cta);
 cudaError_t launch_decode_tc_paged(const FwdParams& p, int d, int ctas, const CUtensorMap& tmk,
                                    const CUtensorMap& tmv, cudaStream_t stream);
 
+// Query rows normed (q_weight not NULL) and turned (phases not NULL) by the norm
+// kernel (qk_norm.cu), rows at a negative position left out; arguments checked.
+cudaError_t launch_query_rows(const blkattn_tensor* q, const blkattn_tensor* q_weight, const blkattn_tensor* pos,
+                              const blkattn_tensor* phases, int32_t layout, float mscale, float eps,
+                              const blkattn_tensor* q_out, cudaStream_t stream);
+
 // ---- attention over the 8-bit paged cache (q8.cuh) ----
 struct Q8Params {
   const void* q;  // bf16 rows; element strides

@@ -30,14 +30,14 @@ namespace blkattn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMostHeads = 8;  // heads of one thread
+constexpr int kMostHeads = 8;  // heads of one thread and token
 constexpr int kFillBlocks = 152 * 4;
 
 // The query heads (set 0) or the key heads (set 1).
 struct NormSet {
   const void* x;
   int64_t x_b, x_h, x_t, x_d;
-  const void* w;
+  const void* w;  // nullptr: rows are not normed
   int64_t w_s;
   void* y;  // forward: the result; backward: dx
   int64_t y_b, y_h, y_t, y_d;
@@ -56,6 +56,7 @@ struct NormParams {
   const int64_t* phases;
   int64_t ph_s;
   bool w_f32;
+  bool skip_negative;  // rows at a negative position are left out
   float mscale, eps, inv_d;
   int rot, d, B, T;
   int hg;         // heads of a thread (fast kernels)
@@ -65,6 +66,7 @@ struct NormParams {
 };
 
 __device__ __forceinline__ float weight_at(const NormSet& s, bool f32, int i) {
+  if (s.w == nullptr) return 1.f;
   return f32 ? static_cast<const float*>(s.w)[i * s.w_s]
              : __bfloat162float(static_cast<const __nv_bfloat16*>(s.w)[i * s.w_s]);
 }
@@ -85,16 +87,92 @@ __device__ __forceinline__ Item item_of(int it, int rot, int d) {
   m.a1 = m.a0 + part / 2;
   return m;
 }
+
+// Arithmetic on pairs of neighbouring dims (.f32x2): half the instructions.
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float sum2(uint64_t a) {
+  float lo, hi;
+  f2_split(a, lo, hi);
+  return lo + hi;
+}
+
+// The angles of an item's V pairs, for two runs of V dims as V pairs of
+// neighbours: x[0 .. V/2) the first run, x[V/2 .. V) the second.
 template <int V, bool INTER>
-__device__ __forceinline__ void angles_of(const NormParams& p, const Item& m, int pos, float sign, float (&sn)[V],
-                                          float (&cs)[V]) {
-  if (!m.turn) return;
+struct Angles {
+  float sn[INTER ? V : 1], cs[INTER ? V : 1];
+  uint64_t c[INTER ? 1 : V / 2], s[INTER ? 1 : V / 2], ns[INTER ? 1 : V / 2];
+  __device__ void take(const NormParams& p, const Item& m, int pos, float sign) {
+    if (!m.turn) return;
+    float a[V], b[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int pair = !INTER ? V * m.it + j : (j < V / 2 ? m.a0 / 2 + j : m.a1 / 2 + j - V / 2);
+      turn_of(pos, p.phases[pair * p.ph_s], b[j], a[j]);
+      b[j] *= sign * p.mscale;
+      a[j] *= p.mscale;
+      if constexpr (INTER) {
+        sn[j] = b[j];
+        cs[j] = a[j];
+      }
+    }
+    if constexpr (!INTER) {
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) {
+        c[j] = f2(a[2 * j], a[2 * j + 1]);
+        s[j] = f2(b[2 * j], b[2 * j + 1]);
+        ns[j] = f2(-b[2 * j], -b[2 * j + 1]);
+      }
+    }
+  }
+  __device__ __forceinline__ void turn(const Item& m, uint64_t (&x)[V]) const {
+    if (!m.turn) return;
+#pragma unroll
+    for (int j = 0; j < (INTER ? V : V / 2); ++j) {
+      if constexpr (INTER) {
+        float u, v;
+        f2_split(x[j], u, v);
+        x[j] = f2(u * cs[j] - v * sn[j], u * sn[j] + v * cs[j]);
+      } else {
+        const uint64_t u = x[j], v = x[V / 2 + j];
+        x[j] = ffma2(u, c[j], fmul2(v, ns[j]));
+        x[V / 2 + j] = ffma2(v, c[j], fmul2(u, s[j]));
+      }
+    }
+  }
+};
+// 16 bytes as pairs: 4 of bf16, 2 of f32.
+template <typename T>
+__device__ __forceinline__ void pairs_of(const uint4& w, uint64_t* x) {
+  const uint32_t* v = &w.x;
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = f2(bf16lo(v[j]), bf16hi(v[j]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) x[j] = f2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+  }
+}
+template <typename TO, int V>
+__device__ __forceinline__ void store_pairs(TO* dst, const Item& m, const uint64_t (&x)[V]) {
+  float y[2 * V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) f2_split(x[j], y[2 * j], y[2 * j + 1]);
+  Vec<TO, V> y0, y1;
+  pack_runs<TO, V>(y, y0, y1);
+  store(dst + m.a0, y0);
+  store(dst + m.a1, y1);
+}
+template <int V>
+__device__ __forceinline__ void weights_of(const NormParams& p, const NormSet& s, const Item& m, uint64_t (&w)[V]) {
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int pair = !INTER ? V * m.it + j : (j < V / 2 ? m.a0 / 2 + j : m.a1 / 2 + j - V / 2);
-    turn_of(pos, p.phases[pair * p.ph_s], sn[j], cs[j]);
-    sn[j] *= sign * p.mscale;
-    cs[j] *= p.mscale;
+    const int i = j < V / 2 ? m.a0 + 2 * j : m.a1 + 2 * j - V;
+    w[j] = f2(weight_at(s, p.w_f32, i), weight_at(s, p.w_f32, i + 1));
   }
 }
 
@@ -112,7 +190,9 @@ __device__ __forceinline__ unsigned lanes_of_row(int n) {
 // Forward: a thread takes one item of a token's rows in up to hg heads of one
 // set.  Its heads' runs are copied to slots of its own in shared memory, all at
 // once, and the angles and weights are taken while they land, as in the rotary
-// kernel.
+// kernel.  (Persistent blocks with a ring of rows across tokens were slower:
+// 68 us in place of 63 for 2 x 8192 tokens of 32 and 8 heads, both with scalar
+// arithmetic; the walk's instructions cost more than the ramps.)
 template <typename TI, typename TO, int V, bool INTER>
 __global__ void __launch_bounds__(kThreads, 3) norm_kernel(const __grid_constant__ NormParams p) {
   static_assert(sizeof(TI) * V == 16, "runs of 16 bytes");
@@ -126,6 +206,11 @@ __global__ void __launch_bounds__(kThreads, 3) norm_kernel(const __grid_constant
   const Item m = item_of<V>((int)(u & (items - 1)), p.rot, p.d);
   const int b = tok / p.T;
   const int t = tok - b * p.T;
+  int pos = 0;
+  if (p.pos != nullptr) {
+    pos = p.pos[b * p.p_b + t * p.p_t];
+    if (p.skip_negative && pos < 0) return;  // (before the rows' loads: padding costs no traffic)
+  }
   const TI* src = static_cast<const TI*>(s.x) + (b * s.x_b + t * s.x_t + h0 * s.x_h);
   extern __shared__ __align__(16) unsigned char slots[];
   uint4* mine = reinterpret_cast<uint4*>(slots) + threadIdx.x;
@@ -138,60 +223,76 @@ __global__ void __launch_bounds__(kThreads, 3) norm_kernel(const __grid_constant
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  float w[2 * V], sn[V], cs[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    w[j] = weight_at(s, p.w_f32, m.a0 + j);
-    w[V + j] = weight_at(s, p.w_f32, m.a1 + j);
-  }
-  if (p.rot) angles_of<V, INTER>(p, m, p.pos[b * p.p_b + t * p.p_t], 1.f, sn, cs);
+  uint64_t w[V];
+  weights_of<V>(p, s, m, w);
+  Angles<V, INTER> angles;
+  if (p.rot) angles.take(p, m, pos, 1.f);
   const unsigned lanes = lanes_of_row(items);
   TO* dst = static_cast<TO*>(s.y) + (b * s.y_b + t * s.y_t + h0 * s.y_h);
 #pragma unroll
   for (int k = 0; k < kMostHeads; ++k) {
     wait_copies(kMostHeads - 1 - k);
     if (k < nh) {
-      Vec<TI, V> x0, x1;
-      reinterpret_cast<uint4&>(x0) = mine[2 * k * kThreads];
-      reinterpret_cast<uint4&>(x1) = mine[(2 * k + 1) * kThreads];
-      float x[2 * V], y[2 * V];
-      unpack_runs<TI, V>(x0, x1, x);
-      float ss = 0.f;
+      uint64_t x[V];
+      pairs_of<TI>(mine[2 * k * kThreads], x);
+      pairs_of<TI>(mine[(2 * k + 1) * kThreads], x + V / 2);
+      if (s.w != nullptr) {
+        uint64_t ss = fmul2(x[0], x[0]);
 #pragma unroll
-      for (int j = 0; j < 2 * V; ++j) ss = fmaf(x[j], x[j], ss);
-      const float r = rsqrtf(fmaf(row_sum(ss, items, lanes), p.inv_d, p.eps));
+        for (int j = 1; j < V; ++j) ss = ffma2(x[j], x[j], ss);
+        const float r = rsqrtf(fmaf(row_sum(sum2(ss), items, lanes), p.inv_d, p.eps));
+        const uint64_t rr = f2(r, r);
 #pragma unroll
-      for (int j = 0; j < 2 * V; ++j) x[j] = x[j] * r * w[j];
-      turn_pairs<V, INTER>(x, m.turn, sn, cs, y);
-      Vec<TO, V> y0, y1;
-      pack_runs<TO, V>(y, y0, y1);
-      store(dst + k * s.y_h + m.a0, y0);
-      store(dst + k * s.y_h + m.a1, y1);
+        for (int j = 0; j < V; ++j) x[j] = fmul2(fmul2(x[j], rr), w[j]);
+      }
+      angles.turn(m, x);
+      store_pairs<TO, V>(dst + k * s.y_h, m, x);
     }
   }
 }
 
-// V elements as fp32, by accesses of up to 16 bytes.
+// Rows in flight of a thread in the backward kernel (its own slots in shared
+// memory): an SM needs some 50 KB in flight to stream at the card's rate.
+constexpr int kRing = 4;
+// V elements (16 bytes or more) of a row to the thread's slots, and from there.
 template <typename T, int V>
-__device__ __forceinline__ void load_run(const T* p, float* x) {
-  constexpr int N = 16 / sizeof(T) < V ? 16 / (int)sizeof(T) : V;
+__device__ __forceinline__ void to_slots(uint4* slot, const T* src) {
 #pragma unroll
-  for (int c = 0; c < V; c += N) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p + c));
-    const T* e = reinterpret_cast<const T*>(&w);
+  for (int c = 0; c < V * (int)sizeof(T) / 16; ++c)
+    cp_async_16(smem_u32(slot + c * kThreads), src + c * (16 / sizeof(T)), 16);
+}
+template <typename T, int V>
+__device__ __forceinline__ void from_slots(const uint4* slot, uint64_t* x) {
+  constexpr int N = 8 / sizeof(T);  // pairs of 16 bytes
 #pragma unroll
-    for (int j = 0; j < N; ++j) x[c + j] = to_f32(e[j]);
-  }
+  for (int c = 0; c < V / 2 / N; ++c) pairs_of<T>(slot[c * kThreads], x + c * N);
 }
 
-// Backward: a block walks every blocks-th group of kThreads / items tokens; a
-// thread keeps its item, so its 2V sums of dw stay in registers, and joins the
-// block's in shared memory at the end.  Each block leaves its sums in the
-// workspace, and sum_dw_kernel adds those in a fixed order: no atomics, the
-// same bits every time.
+// The rows that a thread takes: hg heads of one token, then those of the token
+// `step` further, with its item of each.
+struct Walk {
+  int64_t tok;
+  int k, b, t;
+  __device__ void at(const NormParams& p, int64_t token) {
+    tok = token;
+    k = 0;
+    b = (int)tok / p.T;  // B T < 2^31
+    t = (int)tok - b * p.T;
+  }
+};
+
+// Backward: persistent blocks; a thread walks with its item, so its 2V sums of
+// dw stay in registers, and joins the block's in shared memory at the end; the
+// rows ahead of the one at work are on their way to shared memory (straight to
+// registers, one row at a time: 191 us for the call above).  Each block leaves
+// its sums in the workspace, and sum_dw_kernel adds those in a fixed order: no
+// atomics, the same bits every time.
 template <typename TX, typename TG, typename TO, int V, bool INTER>
 __global__ void __launch_bounds__(kThreads, 2) norm_bwd_kernel(const __grid_constant__ NormParams p) {
   static_assert(sizeof(TX) * V == 16, "runs of 16 bytes");
+  constexpr bool kGSlots = V * sizeof(TG) >= 16;  // (V = 4 bf16 are 8 bytes: straight to registers)
+  constexpr int kG = kGSlots ? V * (int)sizeof(TG) / 16 : 0;  // slots of a run of dy
+  constexpr int kSlots = 2 + 2 * kG;
   const int si = blockIdx.y >= p.groups[0] ? 1 : 0;
   const NormSet& s = p.set[si];
   const int h0 = ((int)blockIdx.y - (si ? p.groups[0] : 0)) * p.hg, nh = min(p.hg, s.heads - h0);
@@ -199,64 +300,95 @@ __global__ void __launch_bounds__(kThreads, 2) norm_bwd_kernel(const __grid_cons
   const int per_block = kThreads / items;
   const Item m = item_of<V>(threadIdx.x & (items - 1), p.rot, p.d);
   const unsigned lanes = lanes_of_row(items);
-  float w[2 * V], dw[2 * V], sn[V], cs[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    w[j] = weight_at(s, p.w_f32, m.a0 + j);
-    w[V + j] = weight_at(s, p.w_f32, m.a1 + j);
-    dw[j] = dw[V + j] = 0.f;
-  }
-  const int n_tok = p.B * p.T;
-  for (int64_t tok = (int64_t)blockIdx.x * per_block + threadIdx.x / items; tok < n_tok;
-       tok += (int64_t)gridDim.x * per_block) {  // (whole rows leave)
-    const int b = (int)tok / p.T;
-    const int t = (int)tok - b * p.T;
-    const TX* xs = static_cast<const TX*>(s.x) + (b * s.x_b + t * s.x_t + h0 * s.x_h);
-    const TG* gs = static_cast<const TG*>(s.g) + (b * s.g_b + t * s.g_t + h0 * s.g_h);
-    TO* dst = static_cast<TO*>(s.y) + (b * s.y_b + t * s.y_t + h0 * s.y_h);
-    if (p.rot) angles_of<V, INTER>(p, m, p.pos[b * p.p_b + t * p.p_t], -1.f, sn, cs);
-#pragma unroll 1
-    for (int k = 0; k < nh; ++k) {
-      float x[2 * V], dy[2 * V], g[2 * V];
-      load_run<TG, V>(gs + k * s.g_h + m.a0, dy);
-      load_run<TG, V>(gs + k * s.g_h + m.a1, dy + V);
-      load_run<TX, V>(xs + k * s.x_h + m.a0, x);
-      load_run<TX, V>(xs + k * s.x_h + m.a1, x + V);
-      turn_pairs<V, INTER>(dy, m.turn, sn, cs, g);
-      float ss = 0.f, ch = 0.f;
-#pragma unroll
-      for (int j = 0; j < 2 * V; ++j) {
-        ss = fmaf(x[j], x[j], ss);
-        ch = fmaf(g[j] * w[j], x[j], ch);
+  const int64_t n_tok = (int64_t)p.B * p.T, step = (int64_t)gridDim.x * per_block;
+  Walk cur, next;
+  next.at(p, (int64_t)blockIdx.x * per_block + threadIdx.x / items);
+  cur = next;
+  extern __shared__ __align__(16) unsigned char slots[];
+  uint4* mine = reinterpret_cast<uint4*>(slots) + threadIdx.x;
+  int put = 0, get = 0;
+  auto issue = [&]() {
+    if (next.tok < n_tok) {
+      const TX* x = static_cast<const TX*>(s.x) + (next.b * s.x_b + next.t * s.x_t + (h0 + next.k) * s.x_h);
+      uint4* at = mine + kSlots * put * kThreads;
+      to_slots<TX, V>(at, x + m.a0);
+      to_slots<TX, V>(at + kThreads, x + m.a1);
+      if constexpr (kGSlots) {
+        const TG* g = static_cast<const TG*>(s.g) + (next.b * s.g_b + next.t * s.g_t + (h0 + next.k) * s.g_h);
+        to_slots<TG, V>(at + 2 * kThreads, g + m.a0);
+        to_slots<TG, V>(at + (2 + kG) * kThreads, g + m.a1);
       }
-      for (int off = items >> 1; off >= 1; off >>= 1) {
-        ss += __shfl_xor_sync(lanes, ss, off);
-        ch += __shfl_xor_sync(lanes, ch, off);
-      }
-      const float r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
-      const float mean = ch * r * p.inv_d;  // of c h
-#pragma unroll
-      for (int j = 0; j < 2 * V; ++j) {
-        const float h = x[j] * r;
-        dw[j] = fmaf(g[j], h, dw[j]);
-        x[j] = r * (g[j] * w[j] - h * mean);
-      }
-      Vec<TO, V> y0, y1;
-      pack_runs<TO, V>(x, y0, y1);
-      store(dst + k * s.y_h + m.a0, y0);
-      store(dst + k * s.y_h + m.a1, y1);
+      if (++next.k == nh) next.at(p, next.tok + step);
     }
-  }
-  // the sums of the threads with the same item: a column each
-  __shared__ float red[kThreads][2 * V + 1];
+    put = (put + 1) & (kRing - 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
 #pragma unroll
-  for (int j = 0; j < 2 * V; ++j) red[threadIdx.x][j] = dw[j];
+  for (int i = 0; i < kRing - 1; ++i) issue();
+  uint64_t w[V], dw[V];
+  weights_of<V>(p, s, m, w);
+#pragma unroll
+  for (int j = 0; j < V; ++j) dw[j] = 0;
+  Angles<V, INTER> angles;
+  while (cur.tok < n_tok) {  // (whole rows leave)
+    issue();
+    if (cur.k == 0 && p.rot) angles.take(p, m, p.pos[cur.b * p.p_b + cur.t * p.p_t], -1.f);
+    uint64_t x[V], g[V];
+    if constexpr (!kGSlots) {
+      const TG* gs = static_cast<const TG*>(s.g) + (cur.b * s.g_b + cur.t * s.g_t + (h0 + cur.k) * s.g_h);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint2 y = *reinterpret_cast<const uint2*>(gs + (r ? m.a1 : m.a0));
+        g[2 * r] = f2(bf16lo(y.x), bf16hi(y.x));
+        g[2 * r + 1] = f2(bf16lo(y.y), bf16hi(y.y));
+      }
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+    const uint4* at = mine + kSlots * get * kThreads;
+    get = (get + 1) & (kRing - 1);
+    from_slots<TX, V>(at, x);
+    from_slots<TX, V>(at + kThreads, x + V / 2);
+    if constexpr (kGSlots) {
+      from_slots<TG, V>(at + 2 * kThreads, g);
+      from_slots<TG, V>(at + (2 + kG) * kThreads, g + V / 2);
+    }
+    angles.turn(m, g);
+    uint64_t ss2 = 0, ch2 = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      ss2 = ffma2(x[j], x[j], ss2);
+      ch2 = ffma2(fmul2(g[j], w[j]), x[j], ch2);
+    }
+    float ss = sum2(ss2), ch = sum2(ch2);
+    for (int off = items >> 1; off >= 1; off >>= 1) {
+      ss += __shfl_xor_sync(lanes, ss, off);
+      ch += __shfl_xor_sync(lanes, ch, off);
+    }
+    const float r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
+    const float mean = -ch * r * p.inv_d;  // of c h, negative
+    const uint64_t rr = f2(r, r), mm = f2(mean, mean);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const uint64_t h = fmul2(x[j], rr);
+      dw[j] = ffma2(g[j], h, dw[j]);
+      x[j] = fmul2(rr, ffma2(h, mm, fmul2(g[j], w[j])));
+    }
+    store_pairs<TO, V>(static_cast<TO*>(s.y) + (cur.b * s.y_b + cur.t * s.y_t + (h0 + cur.k) * s.y_h), m, x);
+    if (++cur.k == nh) cur.at(p, cur.tok + step);
+  }
+  // the sums of the threads with the same item: a column each (over the slots: all copies have landed)
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(slots);  // [kThreads][2 V + 1]
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    f2_split(dw[j], red[threadIdx.x * (2 * V + 1) + 2 * j], red[threadIdx.x * (2 * V + 1) + 2 * j + 1]);
   __syncthreads();
   float* out = p.ws + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * p.d;
   for (int c = threadIdx.x; c < p.d; c += kThreads) {
     const int it = c / (2 * V), j = c % (2 * V);
     float sum = 0.f;
-    for (int i = it; i < kThreads; i += items) sum += red[i][j];
+    for (int i = it; i < kThreads; i += items) sum += red[i * (2 * V + 1) + j];
     const Item q = item_of<V>(it, p.rot, p.d);
     out[j < V ? q.a0 + j : q.a1 + j - V] = sum;
   }
@@ -309,6 +441,7 @@ __global__ void __launch_bounds__(kThreads) norm_rows_kernel(const __grid_consta
   const int lane = threadIdx.x & 31;
   int si, b, h, t;
   if (!row_of(p, (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), si, b, h, t)) return;
+  if (p.skip_negative && p.pos[b * p.p_b + t * p.p_t] < 0) return;
   const NormSet& s = p.set[si];
   const TI* x = static_cast<const TI*>(s.x) + (b * s.x_b + h * s.x_h + t * s.x_t);
   float ss = 0.f;
@@ -317,8 +450,10 @@ __global__ void __launch_bounds__(kThreads) norm_rows_kernel(const __grid_consta
     ss = fmaf(v, v, ss);
     row[j] = v;
   }
-  const float r = rsqrtf(fmaf(warp_sum(ss), p.inv_d, p.eps));
-  for (int j = lane; j < p.d; j += 32) row[j] = row[j] * r * weight_at(s, p.w_f32, j);
+  if (s.w != nullptr) {
+    const float r = rsqrtf(fmaf(warp_sum(ss), p.inv_d, p.eps));
+    for (int j = lane; j < p.d; j += 32) row[j] = row[j] * r * weight_at(s, p.w_f32, j);
+  }
   __syncwarp();
   TO* y = static_cast<TO*>(s.y) + (b * s.y_b + h * s.y_h + t * s.y_t);
   const int pos = p.rot ? p.pos[b * p.p_b + t * p.p_t] : 0;
@@ -471,7 +606,8 @@ bool plan_backward(NormParams* p, int in_bytes, int out_bytes, int g_bytes, int 
     p->groups[0] = p->groups[1] = 1;
     most = ((int64_t)p->B * p->T * most_heads(*p) + kWarps - 1) / kWarps;
   }
-  int64_t blocks = (2 * sms + groups - 1) / groups;
+  // (one wave and no block more: one more than fits took 200 us in place of 151)
+  int64_t blocks = 2 * sms / (groups < 1 ? 1 : groups);
   if (blocks > most) blocks = most;
   p->blocks = (int)(blocks < 1 ? 1 : blocks);
   return fast;
@@ -484,7 +620,14 @@ cudaError_t launch_backward_t(const NormParams& p, bool fast, cudaStream_t strea
   const dim3 grid((unsigned)p.blocks, (unsigned)groups);
   if (groups == 0) {  // no heads at all: dw is zeros
   } else if (fast) {
-    norm_bwd_kernel<TX, TG, TO, V, INTER><<<grid, kThreads, 0, stream>>>(p);
+    constexpr int run = V * (int)sizeof(TG) >= 16 ? V * (int)sizeof(TG) : 0;
+    constexpr int ring = kRing * (32 + 2 * run) * kThreads, red = kThreads * (2 * V + 1) * 4;
+    constexpr int smem = ring > red ? ring : red;
+    static DeviceOnce once;
+    if (cudaError_t e = once.set_smem(reinterpret_cast<const void*>(&norm_bwd_kernel<TX, TG, TO, V, INTER>), smem);
+        e != cudaSuccess)
+      return e;
+    norm_bwd_kernel<TX, TG, TO, V, INTER><<<grid, kThreads, smem, stream>>>(p);
   } else {
     const int smem = 2 * kWarps * p.d * (int)sizeof(float);
     if (smem > 48 * 1024) {
@@ -560,8 +703,10 @@ void fill_set(NormSet* s, const Call& c, int i) {
   };
   s->x = c.x[i]->data;
   four(c.x[i], s->x_b, s->x_h, s->x_t, s->x_d);
-  s->w = c.w[i]->data;
-  s->w_s = c.w[i]->strides[0];
+  if (c.w[i]) {
+    s->w = c.w[i]->data;
+    s->w_s = c.w[i]->strides[0];
+  }
   s->y = c.y[i]->data;
   four(c.y[i], s->y_b, s->y_h, s->y_t, s->y_d);
   s->heads = (int)c.x[i]->sizes[1];
@@ -570,6 +715,33 @@ void fill_set(NormSet* s, const Call& c, int i) {
   four(c.g[i], s->g_b, s->g_h, s->g_t, s->g_d);
   s->dw = static_cast<float*>(c.dw[i]->data);
   s->dw_s = c.dw[i]->strides[0];
+}
+
+NormParams fill_params(const Call& c, int n_sets) {
+  NormParams p{};
+  p.n_sets = n_sets;
+  for (int i = 0; i < n_sets; ++i) fill_set(&p.set[i], c, i);
+  p.p_b = c.pos->strides[0]; p.p_t = c.pos->strides[1];
+  if (c.ph) {
+    p.pos = static_cast<const int32_t*>(c.pos->data);
+    p.phases = static_cast<const int64_t*>(c.ph->data);
+    p.ph_s = c.ph->strides[0];
+    p.rot = (int)(2 * c.ph->sizes[0]);
+  }
+  p.w_f32 = c.w[0] && c.w[0]->dtype == BLKATTN_F32;
+  p.mscale = c.mscale;
+  p.eps = c.eps;
+  p.B = (int)c.x[0]->sizes[0]; p.T = (int)c.x[0]->sizes[2]; p.d = (int)c.x[0]->sizes[3];
+  p.inv_d = 1.f / (float)p.d;
+  return p;
+}
+
+cudaError_t launch_forward_types(const NormParams& p, int32_t in, int32_t out, bool inter, cudaStream_t stream) {
+  if (in == BLKATTN_BF16)
+    return out == BLKATTN_BF16 ? launch_forward_l<__nv_bfloat16, __nv_bfloat16>(p, inter, stream)
+                               : launch_forward_l<__nv_bfloat16, float>(p, inter, stream);
+  return out == BLKATTN_BF16 ? launch_forward_l<float, __nv_bfloat16>(p, inter, stream)
+                             : launch_forward_l<float, float>(p, inter, stream);
 }
 
 int norm(const Call& c, bool back, blkattn_stream_t stream_) {
@@ -618,21 +790,7 @@ int norm(const Call& c, bool back, blkattn_stream_t stream_) {
   }
   if (rows && ((c.pos->data == nullptr && c.ph) || (c.ph && c.ph->data == nullptr))) return BLKATTN_ERR_INVALID_ARG;
   if (int st = require_current_device(c.x[0]->device); st != BLKATTN_OK) return st;
-  NormParams p{};
-  p.n_sets = n_sets;
-  for (int i = 0; i < n_sets; ++i) fill_set(&p.set[i], c, i);
-  p.pos = static_cast<const int32_t*>(c.pos->data);
-  p.p_b = c.pos->strides[0]; p.p_t = c.pos->strides[1];
-  if (c.ph) {
-    p.phases = static_cast<const int64_t*>(c.ph->data);
-    p.ph_s = c.ph->strides[0];
-    p.rot = (int)(2 * c.ph->sizes[0]);
-  }
-  p.w_f32 = c.w[0]->dtype == BLKATTN_F32;
-  p.mscale = c.mscale;
-  p.eps = c.eps;
-  p.d = (int)d; p.B = (int)B; p.T = (int)T;
-  p.inv_d = 1.f / (float)d;
+  NormParams p = fill_params(c, n_sets);
   const bool inter = c.ph && c.layout == BLKATTN_ROPE_INTERLEAVED;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   const int32_t ti = c.x[0]->dtype, to = c.y[0]->dtype;
@@ -640,13 +798,7 @@ int norm(const Call& c, bool back, blkattn_stream_t stream_) {
     // (a set without heads takes no place)
     if (p.set[0].heads == 0) p.set[0] = p.set[1];
     if (p.n_sets == 2 && (p.set[1].heads == 0 || c.x[0]->sizes[1] == 0)) p.n_sets = 1;
-    cudaError_t e;
-    if (ti == BLKATTN_BF16)
-      e = to == BLKATTN_BF16 ? launch_forward_l<__nv_bfloat16, __nv_bfloat16>(p, inter, stream)
-                             : launch_forward_l<__nv_bfloat16, float>(p, inter, stream);
-    else
-      e = to == BLKATTN_BF16 ? launch_forward_l<float, __nv_bfloat16>(p, inter, stream)
-                             : launch_forward_l<float, float>(p, inter, stream);
+    const cudaError_t e = launch_forward_types(p, ti, to, inter, stream);
     return e == cudaSuccess ? BLKATTN_OK : report_cuda_failure(e);
   }
   const int32_t tg = c.g[0]->dtype;
@@ -664,6 +816,17 @@ int norm(const Call& c, bool back, blkattn_stream_t stream_) {
 }
 
 }  // namespace
+
+cudaError_t launch_query_rows(const blkattn_tensor* q, const blkattn_tensor* q_weight, const blkattn_tensor* pos,
+                              const blkattn_tensor* phases, int32_t layout, float mscale, float eps,
+                              const blkattn_tensor* q_out, cudaStream_t stream) {
+  const Call c{{q, nullptr}, {q_weight, nullptr}, {q_out, nullptr}, {}, {}, pos, phases, layout, mscale, eps};
+  NormParams p = fill_params(c, 1);
+  p.skip_negative = true;
+  p.pos = static_cast<const int32_t*>(pos->data);
+  return launch_forward_types(p, q->dtype, q_out->dtype, phases && layout == BLKATTN_ROPE_INTERLEAVED, stream);
+}
+
 }  // namespace blkattn
 
 extern "C" {

@@ -284,3 +284,26 @@ def test_captured_and_replayed():
     torch.cuda.synchronize()
     assert torch.equal(q_out, want_q) and all(torch.equal(x, y) for x, y in zip(got, read))
     assert all(torch.equal(x, y) for x, y in zip(snapshot(a).values(), want.values()))
+
+
+@pytest.mark.parametrize("rot,norm", [(128, True), (128, False), (0, True), (0, False), (24, True)])
+def test_many_query_rows(rot, norm):
+    """Query rows enough for a kernel of their own, with padding in front, behind and between."""
+    a = problem(2, 24, 1, 400, 128, 16, 16, [5, 40], news=[300, 250], lead=30)
+    a["pos"][0, 100:117] = -1
+    ang = angles(rot) if rot else []
+    q_out = torch.full_like(a["q"], 7.0)
+    before = snapshot(a)
+    call(a, blkattn.rope_phases(ang) if ang else None, norm, q_out=q_out)
+    u = normed(a["q"], a["wq"]) if norm else a["q"].double().cpu()
+    y, slack = turned(u, a["pos"], ang, "half")
+    if norm:
+        size = u.abs()
+        if ang:
+            i, j = pairs(rot, "half")
+            size[..., i] = size[..., j] = u[..., i].abs() + u[..., j].abs()
+        slack = slack + n_of(128) * size
+    keep = (a["pos"].cpu() >= 0)[:, None, :, None]
+    check(q_out, torch.where(keep, y, 7.0), torch.where(keep, slack, 0.0))
+    if not ang and not norm:
+        expect(a, before, a["k"].double().cpu(), torch.zeros(a["k"].shape, dtype=F64), "kp", "ks")

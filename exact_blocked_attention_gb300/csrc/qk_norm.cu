@@ -251,22 +251,29 @@ __global__ void __launch_bounds__(kThreads, 3) norm_kernel(const __grid_constant
   }
 }
 
-// Rows in flight of a thread in the backward kernel (its own slots in shared
-// memory): an SM needs some 50 KB in flight to stream at the card's rate.
+// Pairs of rows (two heads of a token) of a thread in the backward kernel's
+// slots (its own, in shared memory): one at work, the others on their way.
 constexpr int kRing = 4;
-// V elements (16 bytes or more) of a row to the thread's slots, and from there.
+// V elements (16 or 8 bytes) of a row to the thread's slot, and from there.
 template <typename T, int V>
-__device__ __forceinline__ void to_slots(uint4* slot, const T* src) {
-#pragma unroll
-  for (int c = 0; c < V * (int)sizeof(T) / 16; ++c)
-    cp_async_16(smem_u32(slot + c * kThreads), src + c * (16 / sizeof(T)), 16);
-}
-template <typename T, int V>
-__device__ __forceinline__ void from_slots(const uint4* slot, uint64_t* x) {
-  constexpr int N = 8 / sizeof(T);  // pairs of 16 bytes
-#pragma unroll
-  for (int c = 0; c < V / 2 / N; ++c) pairs_of<T>(slot[c * kThreads], x + c * N);
-}
+struct Slot {
+  static constexpr int kBytes = V * (int)sizeof(T);
+  static_assert(kBytes == 16 || kBytes == 8, "one copy");
+  static __device__ __forceinline__ void copy(unsigned char* block, const T* src) {
+    const uint32_t at = smem_u32(block + threadIdx.x * kBytes);
+    if constexpr (kBytes == 16) cp_async_16(at, src, 16);
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at), "l"(src) : "memory");
+  }
+  static __device__ __forceinline__ void pairs(const unsigned char* block, uint64_t* x) {
+    if constexpr (kBytes == 16) {
+      pairs_of<T>(reinterpret_cast<const uint4*>(block)[threadIdx.x], x);
+    } else {
+      const uint2 w = reinterpret_cast<const uint2*>(block)[threadIdx.x];
+      x[0] = f2(bf16lo(w.x), bf16hi(w.x));
+      x[1] = f2(bf16lo(w.y), bf16hi(w.y));
+    }
+  }
+};
 
 // The rows that a thread takes: hg heads of one token, then those of the token
 // `step` further, with its item of each.
@@ -287,12 +294,19 @@ struct Walk {
 // registers, one row at a time: 191 us for the call above).  Each block leaves
 // its sums in the workspace, and sum_dw_kernel adds those in a fixed order: no
 // atomics, the same bits every time.
-template <typename TX, typename TG, typename TO, int V, bool INTER>
-__global__ void __launch_bounds__(kThreads, 2) norm_bwd_kernel(const __grid_constant__ NormParams p) {
-  static_assert(sizeof(TX) * V == 16, "runs of 16 bytes");
-  constexpr bool kGSlots = V * sizeof(TG) >= 16;  // (V = 4 bf16 are 8 bytes: straight to registers)
-  constexpr int kG = kGSlots ? V * (int)sizeof(TG) / 16 : 0;  // slots of a run of dy
-  constexpr int kSlots = 2 + 2 * kG;
+//
+// Runs of 4 dims: with runs of 8 f32 a warp's 16-byte copies of dy touch every
+// second half of a sector.  Two rows at a time: one alone leaves the chain of
+// its sums and shuffles with nothing beside it.
+constexpr int kBackV = 4;
+constexpr int kBackBlocks = 2;  // an SM (three spill)
+
+template <typename TX, typename TG, typename TO, bool INTER>
+__global__ void __launch_bounds__(kThreads, kBackBlocks) norm_bwd_kernel(const __grid_constant__ NormParams p) {
+  constexpr int V = kBackV;
+  using SX = Slot<TX, V>;
+  using SG = Slot<TG, V>;
+  constexpr int kRow = 2 * (SX::kBytes + SG::kBytes) * kThreads;  // a row's slots of all threads
   const int si = blockIdx.y >= p.groups[0] ? 1 : 0;
   const NormSet& s = p.set[si];
   const int h0 = ((int)blockIdx.y - (si ? p.groups[0] : 0)) * p.hg, nh = min(p.hg, s.heads - h0);
@@ -304,77 +318,108 @@ __global__ void __launch_bounds__(kThreads, 2) norm_bwd_kernel(const __grid_cons
   Walk cur, next;
   next.at(p, (int64_t)blockIdx.x * per_block + threadIdx.x / items);
   cur = next;
+  auto row_x = [&](const Walk& a) { return static_cast<const TX*>(s.x) + (a.b * s.x_b + a.t * s.x_t + h0 * s.x_h); };
+  auto row_g = [&](const Walk& a) { return static_cast<const TG*>(s.g) + (a.b * s.g_b + a.t * s.g_t + h0 * s.g_h); };
+  auto row_y = [&](const Walk& a) { return static_cast<TO*>(s.y) + (a.b * s.y_b + a.t * s.y_t + h0 * s.y_h); };
+  const TX* x_in = row_x(next);
+  const TG* g_in = row_g(next);
+  TO* y_out = row_y(cur);
+  // the position of the token that `next` came to last, fetched ahead of its use
+  int pos_then = p.rot && next.tok < n_tok ? p.pos[next.b * p.p_b + next.t * p.p_t] : 0;
+  int64_t tok_then = next.tok;
   extern __shared__ __align__(16) unsigned char slots[];
-  uint4* mine = reinterpret_cast<uint4*>(slots) + threadIdx.x;
   int put = 0, get = 0;
   auto issue = [&]() {
     if (next.tok < n_tok) {
-      const TX* x = static_cast<const TX*>(s.x) + (next.b * s.x_b + next.t * s.x_t + (h0 + next.k) * s.x_h);
-      uint4* at = mine + kSlots * put * kThreads;
-      to_slots<TX, V>(at, x + m.a0);
-      to_slots<TX, V>(at + kThreads, x + m.a1);
-      if constexpr (kGSlots) {
-        const TG* g = static_cast<const TG*>(s.g) + (next.b * s.g_b + next.t * s.g_t + (h0 + next.k) * s.g_h);
-        to_slots<TG, V>(at + 2 * kThreads, g + m.a0);
-        to_slots<TG, V>(at + (2 + kG) * kThreads, g + m.a1);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (next.k + r < nh) {
+          unsigned char* at = slots + (2 * put + r) * kRow;
+          SX::copy(at, x_in + m.a0);
+          SX::copy(at + SX::kBytes * kThreads, x_in + m.a1);
+          at += 2 * SX::kBytes * kThreads;
+          SG::copy(at, g_in + m.a0);
+          SG::copy(at + SG::kBytes * kThreads, g_in + m.a1);
+          x_in += s.x_h;
+          g_in += s.g_h;
+        }
       }
-      if (++next.k == nh) next.at(p, next.tok + step);
+      if ((next.k += 2) >= nh) {
+        next.at(p, next.tok + step);
+        if (p.rot && next.tok < n_tok) pos_then = p.pos[next.b * p.p_b + next.t * p.p_t];
+        tok_then = next.tok;
+        x_in = row_x(next);
+        g_in = row_g(next);
+      }
     }
     put = (put + 1) & (kRing - 1);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-#pragma unroll
-  for (int i = 0; i < kRing - 1; ++i) issue();
   uint64_t w[V], dw[V];
   weights_of<V>(p, s, m, w);
 #pragma unroll
   for (int j = 0; j < V; ++j) dw[j] = 0;
   Angles<V, INTER> angles;
+  if (p.rot && cur.tok < n_tok) angles.take(p, m, pos_then, -1.f);
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) issue();
   while (cur.tok < n_tok) {  // (whole rows leave)
     issue();
-    if (cur.k == 0 && p.rot) angles.take(p, m, p.pos[cur.b * p.p_b + cur.t * p.p_t], -1.f);
-    uint64_t x[V], g[V];
-    if constexpr (!kGSlots) {
-      const TG* gs = static_cast<const TG*>(s.g) + (cur.b * s.g_b + cur.t * s.g_t + (h0 + cur.k) * s.g_h);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+    const bool two = cur.k + 1 < nh;
+    uint64_t x[2][V], g[2][V];
+    float ss[2], ch[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const unsigned char* at = slots + (2 * get + r) * kRow;
+      SX::pairs(at, x[r]);
+      SX::pairs(at + SX::kBytes * kThreads, x[r] + V / 2);
+      at += 2 * SX::kBytes * kThreads;
+      SG::pairs(at, g[r]);
+      SG::pairs(at + SG::kBytes * kThreads, g[r] + V / 2);
+      if (r == 1 && !two) {  // (what an absent row's slots hold is not used)
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[r][j] = g[r][j] = 0;
+      }
+      angles.turn(m, g[r]);
+      uint64_t ss2 = 0, ch2 = 0;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        ss2 = ffma2(x[r][j], x[r][j], ss2);
+        ch2 = ffma2(fmul2(g[r][j], w[j]), x[r][j], ch2);
+      }
+      ss[r] = sum2(ss2);
+      ch[r] = sum2(ch2);
+    }
+    get = (get + 1) & (kRing - 1);
+    for (int off = items >> 1; off >= 1; off >>= 1) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const uint2 y = *reinterpret_cast<const uint2*>(gs + (r ? m.a1 : m.a0));
-        g[2 * r] = f2(bf16lo(y.x), bf16hi(y.x));
-        g[2 * r + 1] = f2(bf16lo(y.y), bf16hi(y.y));
+        ss[r] += __shfl_xor_sync(lanes, ss[r], off);
+        ch[r] += __shfl_xor_sync(lanes, ch[r], off);
       }
     }
-    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
-    const uint4* at = mine + kSlots * get * kThreads;
-    get = (get + 1) & (kRing - 1);
-    from_slots<TX, V>(at, x);
-    from_slots<TX, V>(at + kThreads, x + V / 2);
-    if constexpr (kGSlots) {
-      from_slots<TG, V>(at + 2 * kThreads, g);
-      from_slots<TG, V>(at + (2 + kG) * kThreads, g + V / 2);
-    }
-    angles.turn(m, g);
-    uint64_t ss2 = 0, ch2 = 0;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      ss2 = ffma2(x[j], x[j], ss2);
-      ch2 = ffma2(fmul2(g[j], w[j]), x[j], ch2);
-    }
-    float ss = sum2(ss2), ch = sum2(ch2);
-    for (int off = items >> 1; off >= 1; off >>= 1) {
-      ss += __shfl_xor_sync(lanes, ss, off);
-      ch += __shfl_xor_sync(lanes, ch, off);
-    }
-    const float r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
-    const float mean = -ch * r * p.inv_d;  // of c h, negative
-    const uint64_t rr = f2(r, r), mm = f2(mean, mean);
+    for (int r = 0; r < 2; ++r) {
+      if (r == 1 && !two) break;
+      const float rs = rsqrtf(fmaf(ss[r], p.inv_d, p.eps));
+      const float mean = -ch[r] * rs * p.inv_d;  // of c h, negative
+      const uint64_t rr = f2(rs, rs), mm = f2(mean, mean);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const uint64_t h = fmul2(x[j], rr);
-      dw[j] = ffma2(g[j], h, dw[j]);
-      x[j] = fmul2(rr, ffma2(h, mm, fmul2(g[j], w[j])));
+      for (int j = 0; j < V; ++j) {
+        const uint64_t h = fmul2(x[r][j], rr);
+        dw[j] = ffma2(g[r][j], h, dw[j]);
+        x[r][j] = fmul2(rr, ffma2(h, mm, fmul2(g[r][j], w[j])));
+      }
+      store_pairs<TO, V>(y_out, m, x[r]);
+      y_out += s.y_h;
     }
-    store_pairs<TO, V>(static_cast<TO*>(s.y) + (cur.b * s.y_b + cur.t * s.y_t + (h0 + cur.k) * s.y_h), m, x);
-    if (++cur.k == nh) cur.at(p, cur.tok + step);
+    if ((cur.k += 2) >= nh) {
+      cur.at(p, cur.tok + step);
+      y_out = row_y(cur);
+      if (p.rot && cur.tok < n_tok)
+        angles.take(p, m, cur.tok == tok_then ? pos_then : p.pos[cur.b * p.p_b + cur.t * p.p_t], -1.f);
+    }
   }
   // the sums of the threads with the same item: a column each (over the slots: all copies have landed)
   asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -538,7 +583,7 @@ bool run_fits(const void* base, int bytes, int V, bool used_b, int64_t sb, bool 
 }
 // Whether the fast kernels take these rows (a stride of a dim of size 1 is not used).
 bool fast_ok(const NormParams& p, int in_bytes, int out_bytes, int g_bytes) {
-  const int V = 16 / in_bytes, items = p.d / (2 * V);
+  const int V = g_bytes ? kBackV : 16 / in_bytes, items = p.d / (2 * V);
   if (p.d % (2 * V) != 0 || p.rot % (2 * V) != 0 || items > 32 || (items & (items - 1)) != 0) return false;
   for (int i = 0; i < p.n_sets; ++i) {
     const NormSet& s = p.set[i];
@@ -599,7 +644,7 @@ bool plan_backward(NormParams* p, int in_bytes, int out_bytes, int g_bytes, int 
   int groups = p->n_sets;
   int64_t most;
   if (fast) {
-    const int per_block = kThreads / (p->d / (32 / in_bytes));
+    const int per_block = kThreads / (p->d / (2 * kBackV));
     groups = set_groups(p, kMostHeads);
     most = ((int64_t)p->B * p->T + per_block - 1) / per_block;
   } else {
@@ -607,7 +652,7 @@ bool plan_backward(NormParams* p, int in_bytes, int out_bytes, int g_bytes, int 
     most = ((int64_t)p->B * p->T * most_heads(*p) + kWarps - 1) / kWarps;
   }
   // (one wave and no block more: one more than fits took 200 us in place of 151)
-  int64_t blocks = 2 * sms / (groups < 1 ? 1 : groups);
+  int64_t blocks = kBackBlocks * sms / (groups < 1 ? 1 : groups);
   if (blocks > most) blocks = most;
   p->blocks = (int)(blocks < 1 ? 1 : blocks);
   return fast;
@@ -615,19 +660,18 @@ bool plan_backward(NormParams* p, int in_bytes, int out_bytes, int g_bytes, int 
 
 template <typename TX, typename TG, typename TO, bool INTER>
 cudaError_t launch_backward_t(const NormParams& p, bool fast, cudaStream_t stream) {
-  constexpr int V = 16 / sizeof(TX);
+  constexpr int V = kBackV;
   const int groups = p.groups[0] + (p.n_sets > 1 ? p.groups[1] : 0);
   const dim3 grid((unsigned)p.blocks, (unsigned)groups);
   if (groups == 0) {  // no heads at all: dw is zeros
   } else if (fast) {
-    constexpr int run = V * (int)sizeof(TG) >= 16 ? V * (int)sizeof(TG) : 0;
-    constexpr int ring = kRing * (32 + 2 * run) * kThreads, red = kThreads * (2 * V + 1) * 4;
+    constexpr int ring = 2 * kRing * 2 * V * (int)(sizeof(TX) + sizeof(TG)) * kThreads, red = kThreads * (2 * V + 1) * 4;
     constexpr int smem = ring > red ? ring : red;
     static DeviceOnce once;
-    if (cudaError_t e = once.set_smem(reinterpret_cast<const void*>(&norm_bwd_kernel<TX, TG, TO, V, INTER>), smem);
+    if (cudaError_t e = once.set_smem(reinterpret_cast<const void*>(&norm_bwd_kernel<TX, TG, TO, INTER>), smem);
         e != cudaSuccess)
       return e;
-    norm_bwd_kernel<TX, TG, TO, V, INTER><<<grid, kThreads, smem, stream>>>(p);
+    norm_bwd_kernel<TX, TG, TO, INTER><<<grid, kThreads, smem, stream>>>(p);
   } else {
     const int smem = 2 * kWarps * p.d * (int)sizeof(float);
     if (smem > 48 * 1024) {

@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMostHeads = 8;  // heads of one thread and token
-constexpr int kFillBlocks = 152 * 4;
+constexpr int kFillBlocks = 152 * 2;  // blocks resident at once
 
 // The query heads (set 0) or the key heads (set 1).
 struct NormSet {
@@ -176,84 +176,17 @@ __device__ __forceinline__ void weights_of(const NormParams& p, const NormSet& s
   }
 }
 
-// Sum over the `n` (a power of two) neighbouring lanes of a row, whose mask is
-// `lanes`.
-__device__ __forceinline__ float row_sum(float x, int n, unsigned lanes) {
-  for (int off = n >> 1; off >= 1; off >>= 1) x += __shfl_xor_sync(lanes, x, off);
-  return x;
-}
+// The lanes of a thread's row, n (a power of two) neighbours.
 __device__ __forceinline__ unsigned lanes_of_row(int n) {
   const int lane = threadIdx.x & 31;
   return (n == 32 ? 0xffffffffu : (1u << n) - 1) << (lane & ~(n - 1));
 }
 
-// Forward: a thread takes one item of a token's rows in up to hg heads of one
-// set.  Its heads' runs are copied to slots of its own in shared memory, all at
-// once, and the angles and weights are taken while they land, as in the rotary
-// kernel.  (Persistent blocks with a ring of rows across tokens were slower:
-// 68 us in place of 63 for 2 x 8192 tokens of 32 and 8 heads, both with scalar
-// arithmetic; the walk's instructions cost more than the ramps.)
-template <typename TI, typename TO, int V, bool INTER>
-__global__ void __launch_bounds__(kThreads, 3) norm_kernel(const __grid_constant__ NormParams p) {
-  static_assert(sizeof(TI) * V == 16, "runs of 16 bytes");
-  const int si = blockIdx.y >= p.groups[0] ? 1 : 0;
-  const NormSet& s = p.set[si];
-  const int h0 = ((int)blockIdx.y - (si ? p.groups[0] : 0)) * p.hg, nh = min(p.hg, s.heads - h0);
-  const int items = p.d / (2 * V);  // (a power of two)
-  const int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (u >= (int64_t)p.B * p.T * items) return;  // (whole rows leave)
-  const int tok = (int)(u / items);  // B T < 2^31
-  const Item m = item_of<V>((int)(u & (items - 1)), p.rot, p.d);
-  const int b = tok / p.T;
-  const int t = tok - b * p.T;
-  int pos = 0;
-  if (p.pos != nullptr) {
-    pos = p.pos[b * p.p_b + t * p.p_t];
-    if (p.skip_negative && pos < 0) return;  // (before the rows' loads: padding costs no traffic)
-  }
-  const TI* src = static_cast<const TI*>(s.x) + (b * s.x_b + t * s.x_t + h0 * s.x_h);
-  extern __shared__ __align__(16) unsigned char slots[];
-  uint4* mine = reinterpret_cast<uint4*>(slots) + threadIdx.x;
-#pragma unroll
-  for (int k = 0; k < kMostHeads; ++k) {
-    if (k < nh) {
-      const TI* r = src + k * s.x_h;
-      cp_async_16(smem_u32(mine + 2 * k * kThreads), r + m.a0, 16);
-      cp_async_16(smem_u32(mine + (2 * k + 1) * kThreads), r + m.a1, 16);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  }
-  uint64_t w[V];
-  weights_of<V>(p, s, m, w);
-  Angles<V, INTER> angles;
-  if (p.rot) angles.take(p, m, pos, 1.f);
-  const unsigned lanes = lanes_of_row(items);
-  TO* dst = static_cast<TO*>(s.y) + (b * s.y_b + t * s.y_t + h0 * s.y_h);
-#pragma unroll
-  for (int k = 0; k < kMostHeads; ++k) {
-    wait_copies(kMostHeads - 1 - k);
-    if (k < nh) {
-      uint64_t x[V];
-      pairs_of<TI>(mine[2 * k * kThreads], x);
-      pairs_of<TI>(mine[(2 * k + 1) * kThreads], x + V / 2);
-      if (s.w != nullptr) {
-        uint64_t ss = fmul2(x[0], x[0]);
-#pragma unroll
-        for (int j = 1; j < V; ++j) ss = ffma2(x[j], x[j], ss);
-        const float r = rsqrtf(fmaf(row_sum(sum2(ss), items, lanes), p.inv_d, p.eps));
-        const uint64_t rr = f2(r, r);
-#pragma unroll
-        for (int j = 0; j < V; ++j) x[j] = fmul2(fmul2(x[j], rr), w[j]);
-      }
-      angles.turn(m, x);
-      store_pairs<TO, V>(dst + k * s.y_h, m, x);
-    }
-  }
-}
-
-// Pairs of rows (two heads of a token) of a thread in the backward kernel's
-// slots (its own, in shared memory): one at work, the others on their way.
+// Pairs of rows (two heads of a token) in a thread's slots (its own, in shared
+// memory): one at work, the others on their way.
 constexpr int kRing = 4;
+constexpr int kResident = 2;  // blocks of either kernel on an SM (three spill)
+
 // V elements (16 or 8 bytes) of a row to the thread's slot, and from there.
 template <typename T, int V>
 struct Slot {
@@ -279,14 +212,119 @@ struct Slot {
 // `step` further, with its item of each.
 struct Walk {
   int64_t tok;
-  int k, b, t;
-  __device__ void at(const NormParams& p, int64_t token) {
-    tok = token;
+  int k, b, t, pos;
+  // the walk's first token from `token` on that is not left out
+  __device__ void at(const NormParams& p, int64_t token, int64_t step) {
     k = 0;
-    b = (int)tok / p.T;  // B T < 2^31
-    t = (int)tok - b * p.T;
+    for (tok = token;; tok += step) {
+      b = (int)tok / p.T;  // B T < 2^31
+      t = (int)tok - b * p.T;
+      if (p.pos == nullptr || tok >= (int64_t)p.B * p.T) return;
+      pos = p.pos[b * p.p_b + t * p.p_t];
+      if (!p.skip_negative || pos >= 0) return;
+    }
   }
 };
+
+// Forward: persistent blocks; a thread walks over its tokens with its item of
+// the rows, two heads at a time (one alone leaves the chain of its sum and
+// shuffles with nothing beside it), the next ones on their way to shared memory
+// (asynchronous copies: no register holds them).  2 x 8192 tokens of 32 and 8
+// heads: 59 us; a block for each 32 tokens, all heads copied and then
+// computed as in the rotary kernel, 62.
+template <typename TI, typename TO, int V, bool INTER>
+__global__ void __launch_bounds__(kThreads, kResident) norm_kernel(const __grid_constant__ NormParams p) {
+  using SX = Slot<TI, V>;
+  constexpr int kRow = 2 * SX::kBytes * kThreads;
+  const int si = blockIdx.y >= p.groups[0] ? 1 : 0;
+  const NormSet& s = p.set[si];
+  const int h0 = ((int)blockIdx.y - (si ? p.groups[0] : 0)) * p.hg, nh = min(p.hg, s.heads - h0);
+  const int items = p.d / (2 * V);  // (a power of two)
+  const int per_block = kThreads / items;
+  const Item m = item_of<V>(threadIdx.x & (items - 1), p.rot, p.d);
+  const unsigned lanes = lanes_of_row(items);
+  const int64_t n_tok = (int64_t)p.B * p.T, step = (int64_t)gridDim.x * per_block;
+  Walk cur, next;
+  next.at(p, (int64_t)blockIdx.x * per_block + threadIdx.x / items, step);
+  cur = next;
+  auto row_x = [&](const Walk& a) { return static_cast<const TI*>(s.x) + (a.b * s.x_b + a.t * s.x_t + h0 * s.x_h); };
+  auto row_y = [&](const Walk& a) { return static_cast<TO*>(s.y) + (a.b * s.y_b + a.t * s.y_t + h0 * s.y_h); };
+  const TI* x_in = row_x(next);
+  TO* y_out = row_y(cur);
+  extern __shared__ __align__(16) unsigned char slots[];
+  int put = 0, get = 0;
+  auto issue = [&]() {
+    if (next.tok < n_tok) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (next.k + r < nh) {
+          unsigned char* at = slots + (2 * put + r) * kRow;
+          SX::copy(at, x_in + m.a0);
+          SX::copy(at + SX::kBytes * kThreads, x_in + m.a1);
+          x_in += s.x_h;
+        }
+      }
+      if ((next.k += 2) >= nh) {
+        next.at(p, next.tok + step, step);
+        x_in = row_x(next);
+      }
+    }
+    put = (put + 1) & (kRing - 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) issue();
+  uint64_t w[V];
+  weights_of<V>(p, s, m, w);
+  Angles<V, INTER> angles;
+  if (p.rot && cur.tok < n_tok) angles.take(p, m, cur.pos, 1.f);
+  while (cur.tok < n_tok) {  // (whole rows leave)
+    issue();
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+    const bool two = cur.k + 1 < nh;
+    uint64_t x[2][V];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {  // (what an absent row's slots hold is not used)
+      const unsigned char* at = slots + (2 * get + r) * kRow;
+      SX::pairs(at, x[r]);
+      SX::pairs(at + SX::kBytes * kThreads, x[r] + V / 2);
+    }
+    get = (get + 1) & (kRing - 1);
+    if (s.w != nullptr) {
+      float ss[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        uint64_t a = fmul2(x[r][0], x[r][0]);
+#pragma unroll
+        for (int j = 1; j < V; ++j) a = ffma2(x[r][j], x[r][j], a);
+        ss[r] = sum2(a);
+      }
+      for (int off = items >> 1; off >= 1; off >>= 1) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) ss[r] += __shfl_xor_sync(lanes, ss[r], off);
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float rs = rsqrtf(fmaf(ss[r], p.inv_d, p.eps));
+        const uint64_t rr = f2(rs, rs);
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[r][j] = fmul2(fmul2(x[r][j], rr), w[j]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if (r == 1 && !two) break;
+      angles.turn(m, x[r]);
+      store_pairs<TO, V>(y_out, m, x[r]);
+      y_out += s.y_h;
+    }
+    if ((cur.k += 2) >= nh) {
+      cur.at(p, cur.tok + step, step);
+      y_out = row_y(cur);
+      if (p.rot && cur.tok < n_tok) angles.take(p, m, cur.pos, 1.f);
+    }
+  }
+}
 
 // Backward: persistent blocks; a thread walks with its item, so its 2V sums of
 // dw stay in registers, and joins the block's in shared memory at the end; the
@@ -299,10 +337,9 @@ struct Walk {
 // second half of a sector.  Two rows at a time: one alone leaves the chain of
 // its sums and shuffles with nothing beside it.
 constexpr int kBackV = 4;
-constexpr int kBackBlocks = 2;  // an SM (three spill)
 
 template <typename TX, typename TG, typename TO, bool INTER>
-__global__ void __launch_bounds__(kThreads, kBackBlocks) norm_bwd_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kThreads, kResident) norm_bwd_kernel(const __grid_constant__ NormParams p) {
   constexpr int V = kBackV;
   using SX = Slot<TX, V>;
   using SG = Slot<TG, V>;
@@ -316,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, kBackBlocks) norm_bwd_kernel(const _
   const unsigned lanes = lanes_of_row(items);
   const int64_t n_tok = (int64_t)p.B * p.T, step = (int64_t)gridDim.x * per_block;
   Walk cur, next;
-  next.at(p, (int64_t)blockIdx.x * per_block + threadIdx.x / items);
+  next.at(p, (int64_t)blockIdx.x * per_block + threadIdx.x / items, step);
   cur = next;
   auto row_x = [&](const Walk& a) { return static_cast<const TX*>(s.x) + (a.b * s.x_b + a.t * s.x_t + h0 * s.x_h); };
   auto row_g = [&](const Walk& a) { return static_cast<const TG*>(s.g) + (a.b * s.g_b + a.t * s.g_t + h0 * s.g_h); };
@@ -324,9 +361,6 @@ __global__ void __launch_bounds__(kThreads, kBackBlocks) norm_bwd_kernel(const _
   const TX* x_in = row_x(next);
   const TG* g_in = row_g(next);
   TO* y_out = row_y(cur);
-  // the position of the token that `next` came to last, fetched ahead of its use
-  int pos_then = p.rot && next.tok < n_tok ? p.pos[next.b * p.p_b + next.t * p.p_t] : 0;
-  int64_t tok_then = next.tok;
   extern __shared__ __align__(16) unsigned char slots[];
   int put = 0, get = 0;
   auto issue = [&]() {
@@ -345,9 +379,7 @@ __global__ void __launch_bounds__(kThreads, kBackBlocks) norm_bwd_kernel(const _
         }
       }
       if ((next.k += 2) >= nh) {
-        next.at(p, next.tok + step);
-        if (p.rot && next.tok < n_tok) pos_then = p.pos[next.b * p.p_b + next.t * p.p_t];
-        tok_then = next.tok;
+        next.at(p, next.tok + step, step);
         x_in = row_x(next);
         g_in = row_g(next);
       }
@@ -360,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, kBackBlocks) norm_bwd_kernel(const _
 #pragma unroll
   for (int j = 0; j < V; ++j) dw[j] = 0;
   Angles<V, INTER> angles;
-  if (p.rot && cur.tok < n_tok) angles.take(p, m, pos_then, -1.f);
+  if (p.rot && cur.tok < n_tok) angles.take(p, m, cur.pos, -1.f);
 #pragma unroll
   for (int i = 0; i < kRing - 1; ++i) issue();
   while (cur.tok < n_tok) {  // (whole rows leave)
@@ -415,10 +447,9 @@ __global__ void __launch_bounds__(kThreads, kBackBlocks) norm_bwd_kernel(const _
       y_out += s.y_h;
     }
     if ((cur.k += 2) >= nh) {
-      cur.at(p, cur.tok + step);
+      cur.at(p, cur.tok + step, step);
       y_out = row_y(cur);
-      if (p.rot && cur.tok < n_tok)
-        angles.take(p, m, cur.tok == tok_then ? pos_then : p.pos[cur.b * p.p_b + cur.t * p.p_t], -1.f);
+      if (p.rot && cur.tok < n_tok) angles.take(p, m, cur.pos, -1.f);
     }
   }
   // the sums of the threads with the same item: a column each (over the slots: all copies have landed)
@@ -612,20 +643,20 @@ template <typename TI, typename TO, bool INTER>
 cudaError_t launch_forward(NormParams p, cudaStream_t stream) {
   constexpr int V = 16 / sizeof(TI);
   if (fast_ok(p, sizeof(TI), sizeof(TO), 0)) {
-    const int64_t n = (int64_t)p.B * p.T * (p.d / (2 * V));
-    const int64_t blocks = (n + kThreads - 1) / kThreads;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;  // (more elements than the card holds)
-    const int64_t want = (kFillBlocks + blocks - 1) / blocks;  // groups that fill the machine
+    const int per_block = kThreads / (p.d / (2 * V));
+    int64_t blocks = ((int64_t)p.B * p.T + per_block - 1) / per_block;
+    // heads of a group: as many as leave enough groups to fill the machine
+    const int64_t want = (kFillBlocks + blocks - 1) / blocks;
     int groups = set_groups(&p, (int)((most_heads(p) + want - 1) / want));
     if (groups > 65535) groups = set_groups(&p, kMostHeads);
-    const int smem = p.hg * 32 * kThreads;
-    if (smem > 48 * 1024) {
-      static DeviceOnce once;
-      if (cudaError_t e = once.set_smem(reinterpret_cast<const void*>(&norm_kernel<TI, TO, V, INTER>),
-                                        kMostHeads * 32 * kThreads);
-          e != cudaSuccess)
-        return e;
-    }
+    // one wave of blocks and no block more
+    const int64_t most = groups < kFillBlocks ? kFillBlocks / groups : 1;
+    if (blocks > most) blocks = most;
+    constexpr int smem = 2 * kRing * 2 * V * (int)sizeof(TI) * kThreads;
+    static DeviceOnce once;
+    if (cudaError_t e = once.set_smem(reinterpret_cast<const void*>(&norm_kernel<TI, TO, V, INTER>), smem);
+        e != cudaSuccess)
+      return e;
     norm_kernel<TI, TO, V, INTER><<<dim3((unsigned)blocks, (unsigned)groups), kThreads, smem, stream>>>(p);
     return cudaGetLastError();
   }
@@ -652,7 +683,7 @@ bool plan_backward(NormParams* p, int in_bytes, int out_bytes, int g_bytes, int 
     most = ((int64_t)p->B * p->T * most_heads(*p) + kWarps - 1) / kWarps;
   }
   // (one wave and no block more: one more than fits took 200 us in place of 151)
-  int64_t blocks = kBackBlocks * sms / (groups < 1 ? 1 : groups);
+  int64_t blocks = kResident * sms / (groups < 1 ? 1 : groups);
   if (blocks > most) blocks = most;
   p->blocks = (int)(blocks < 1 ? 1 : blocks);
   return fast;

@@ -14,11 +14,12 @@
 // A sequence's rows come in ascending positions, so the new rows of a block are
 // one run of t (with padding between, perhaps).  A CTA takes a window of t and
 // the blocks whose run begins in it, panels of max(S, 16) cache rows at a time:
-// the panel's angles go to shared memory once, then each warp takes a head of K
-// or V: 16 dims a lane, 512 / d rows a pass; the first sweep finds the rows'
-// maxima, the second quantises.  A lane's first new row stays in registers
-// between the sweeps (a decode step has no other), the others are computed again
-// from rows that the L1 holds.
+// the panel's angles go to shared memory once, then a warp takes 2048 numbers of
+// a head of K or V (16 dims a lane), in registers from the load to the store;
+// where a panel has more, warps share it and its maxima through shared memory.
+// (A warp for the whole panel, which computes its rows for the maximum and again
+// for the store: 55 us for a prompt of 5120 rows and 8 KV heads in blocks of 32,
+// KVUS so.)
 //
 // Latency bounds a decode step's append: one launch, the query rows in CTAs of
 // their own.  Memory bounds a prompt's, most of it the query rows': from
@@ -37,7 +38,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kKvHeads = 4;   // KV heads of a CTA: K and V of each, a warp each
 constexpr int kQHeads = 32;   // query heads of a CTA
 // query rows from which on they have a kernel of their own
 constexpr int64_t kOwnKernelRows = 16384;
@@ -120,12 +120,9 @@ __device__ __forceinline__ float weight_of(const void* w, int64_t s, bool f32, i
 // One row of k or q: normed (w not NULL), then turned by the angles `cs` (its
 // pairs' (cos, sin) mscale; not read when rot = 0).  stage: RUNS = false, D floats of the
 // row's own.
-template <typename T, int D, bool RUNS, bool INTER, bool VEC>
-__device__ __forceinline__ void row_values(const AppendParams& p, const Lane<D>& l, const T* src, int64_t s_d,
-                                           const float* w, bool norm, bool rotate, const float2* cs, float* stage,
-                                           float (&x)[16]) {
-  load8<T, VEC>(src + l.a0 * s_d, s_d, x);
-  load8<T, VEC>(src + l.a1 * s_d, s_d, x + 8);
+template <typename T, int D, bool RUNS, bool INTER>
+__device__ __forceinline__ void row_values(const AppendParams& p, const Lane<D>& l, const float* w, bool norm,
+                                           bool rotate, const float2* cs, float* stage, float (&x)[16]) {
   if (norm) {
     float ss = 0.f;
 #pragma unroll
@@ -215,8 +212,10 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
       const int i = u / nh, h = h0 + u - i * nh, t = t0 + i;
       if (pos[t * p.p_t] < 0) continue;
       float x[16];
-      row_values<T, D, RUNS, INTER, VEC>(p, l, static_cast<const T*>(p.q.p) + (b * p.q.s_b + h * p.q.s_h + t * p.q.s_t),
-                                         p.q.s_d, w, norm, p.rot > 0, cs + i * (p.rot / 2), stage, x);
+      const T* in = static_cast<const T*>(p.q.p) + (b * p.q.s_b + h * p.q.s_h + t * p.q.s_t);
+      load8<T, VEC>(in + l.a0 * p.q.s_d, p.q.s_d, x);
+      load8<T, VEC>(in + l.a1 * p.q.s_d, p.q.s_d, x + 8);
+      row_values<T, D, RUNS, INTER>(p, l, w, norm, p.rot > 0, cs + i * (p.rot / 2), stage, x);
       T* o = static_cast<T*>(p.q_out) + (b * p.o_b + h * p.o_h + t * p.o_t);
       if constexpr (VEC) {
         Vec<T, 8> y0, y1;
@@ -246,10 +245,21 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
   __shared__ int n_lead;
   __shared__ int src[kMaxScaleRows];        // t of the panel's rows, -1: not new
   __shared__ int page[16], first_row[16];   // of the panel's blocks: page (-1: none), row in page
-  __shared__ float amax[kWarps][kMaxScaleRows];
-  __shared__ int e_old[kWarps][16], e_new[kWarps][16];
+  __shared__ float amax[kWarps][kMaxScaleRows];  // of each pair's rows
   const int S = 1 << p.shift;
   if (threadIdx.x == 0) n_lead = 0;
+  // `parts` warps share a pair's rows, kPasses passes each
+  constexpr int kPasses = 4;
+  const int parts = max(1, p.panel / (kPasses * Lane<D>::kRows)), part = warp % parts;
+  const int pair = blockIdx.y * (kWarps / parts) + warp / parts, h = pair >> 1, which = pair & 1;  // K, V
+  const int row0 = part * kPasses * Lane<D>::kRows;
+  // the first rows, on their way while the runs are found
+  if (part == 0 && h < p.Hkv && lane < 2 * n) {
+    const Rows& rows = p.src[which];
+    const T* r = static_cast<const T*>(rows.p) + (b * rows.s_b + h * rows.s_h + (t0 + (lane >> 1)) * rows.s_t +
+                                                  (lane & 1) * (D / 2) * rows.s_d);
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(r));
+  }
   __syncthreads();
   if (warp == 0) {
     // the last row before the window that is not padding
@@ -273,7 +283,6 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
       __syncwarp();
     }
   }
-  const int h0 = blockIdx.y * kKvHeads;
   float w[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j)
@@ -307,83 +316,88 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
     __syncthreads();
     if (p.rot) fill_angles(p, cs, p.panel, [&](int i) { return src[i] < 0 ? -1 : pos[src[i] * p.p_t]; });
     __syncthreads();
-    const int passes = (min(per_panel, runs - r0) * S + Lane<D>::kRows - 1) / Lane<D>::kRows;
-    for (int u = warp; u < 2 * kKvHeads; u += kWarps) {
-      const int h = h0 + (u >> 1), which = u & 1;  // K, V
-      if (h >= p.Hkv) continue;
-      const Pool& pool = p.pool[which];
-      const Rows& rows = p.src[which];
+    // the warp's pair (head, K or V) and its rows of the panel: kPasses passes of them, in registers
+    const bool works = pair < 2 * p.Hkv;
+    const Pool& pool = p.pool[which];
+    const Rows& rows = p.src[which];
+    float x[kPasses][16];
+    bool is_new[kPasses];
+    if (works) {
       const T* in = static_cast<const T*>(rows.p) + (b * rows.s_b + h * rows.s_h);
-      const bool norm = which == 0 && p.wk != nullptr, rotate = which == 0 && p.rot > 0;
-      auto values = [&](int r, float (&x)[16]) {
+#pragma unroll
+      for (int k = 0; k < kPasses; ++k) {
+        const int r = row0 + k * Lane<D>::kRows + l.slot;
         const int t = r < p.panel ? src[r] : -1;
-        if (t < 0) return false;  // (the lanes of a row together)
-        row_values<T, D, RUNS, INTER, VEC>(p, l, in + t * rows.s_t, rows.s_d, w, norm, rotate, cs + r * (p.rot / 2),
-                                           stage, x);
-        return true;
-      };
-      auto row_max = [&](int r, bool is_new, const float (&x)[16]) {
+        is_new[k] = t >= 0;  // (the lanes of a row together)
+        if (is_new[k]) {
+          load8<T, VEC>(in + t * rows.s_t + l.a0 * rows.s_d, rows.s_d, x[k]);
+          load8<T, VEC>(in + t * rows.s_t + l.a1 * rows.s_d, rows.s_d, x[k] + 8);
+        }
+      }
+    }
+    // the scales as they are, one lane a block (before any warp writes them)
+    unsigned char* scale = nullptr;
+    int old = 0;
+    if (works && lane < per_panel && page[lane] >= 0) {
+      scale = pool.scales + (page[lane] * pool.e_n + h * pool.e_h + (first_row[lane] >> p.shift) * pool.e_i);
+      old = (int)*scale - 127;
+    }
+    if (works) {
+#pragma unroll
+      for (int k = 0; k < kPasses; ++k) {
+        const int r = row0 + k * Lane<D>::kRows + l.slot;
         float a = 0.f;
-        if (is_new) {
+        if (is_new[k]) {
+          row_values<T, D, RUNS, INTER>(p, l, w, which == 0 && p.wk != nullptr, which == 0 && p.rot > 0,
+                                        cs + r * (p.rot / 2), stage, x[k]);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float v = fabsf(x[j]);
+            const float v = fabsf(x[k][j]);
             a = fmaxf(a, v <= 3.4028235e38f ? v : 0.f);
           }
 #pragma unroll
           for (int off = Lane<D>::kLanes / 2; off >= 1; off >>= 1) a = fmaxf(a, __shfl_xor_sync(l.lanes, a, off));
         }
-        if (l.it == 0 && r < p.panel) amax[warp][r] = a;
-      };
-      // the maxima; each lane's first new row stays in registers for the second sweep
-      float held[16];
-      int k_held = -1;
-      for (int k = 0; k < passes; ++k) {
-        const int r = k * Lane<D>::kRows + l.slot;
-        float x[16];
-        const bool nw = values(r, x);
-        row_max(r, nw, x);
-        if (nw && k_held < 0) {
-          k_held = k;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) held[j] = x[j];
-        }
+        if (l.it == 0 && r < p.panel) amax[warp / parts][r] = a;
       }
-      __syncwarp();
-      if (lane < per_panel && page[lane] >= 0) {  // the blocks' exponents
-        float a = 0.f;
-        for (int i = 0; i < S; ++i) a = fmaxf(a, amax[warp][(lane << p.shift) + i]);
-        unsigned char* sc = pool.scales + (page[lane] * pool.e_n + h * pool.e_h + (first_row[lane] >> p.shift) * pool.e_i);
+    }
+    __syncthreads();
+    if (works) {
+      // the blocks' maxima: rows lane, lane + 32, .., then over the lanes of a block
+      float a = 0.f;
+      for (int i = lane; i < p.panel; i += 32) a = fmaxf(a, amax[warp / parts][i]);
+      for (int off = min(S, 32) >> 1; off >= 1; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+      a = __shfl_sync(0xffffffffu, a, (lane << p.shift) & 31);  // lane i: of block i
+      int now = 0;
+      if (scale != nullptr) {
         const bool fresh = src[lane << p.shift] >= 0;
-        const int old = (int)*sc - 127, e = scale_exp(a);
-        const int now = fresh ? e : max(e, old);
-        e_old[warp][lane] = fresh ? now : old;  // (rows that stay are not touched)
-        e_new[warp][lane] = now;
-        if (fresh || now != old) *sc = (unsigned char)(now + 127);
+        const int e = scale_exp(a);
+        now = fresh ? e : max(e, old);
+        if (part == 0 && (fresh || now != old)) *scale = (unsigned char)(now + 127);
+        if (fresh) old = now;  // (rows that stay are not touched)
       }
-      __syncwarp();
-      auto put = [&](int r, bool nw, const float (&x)[16]) {
-        const int k = r >> p.shift;
-        if (r >= p.panel || page[k] < 0) return;
-        const int now = e_new[warp][k], old = e_old[warp][k];
-        if (!nw && now == old) return;
-        unsigned char* o = pool.p + (page[k] * pool.s_n + h * pool.s_h + (first_row[k] + (r & (S - 1))) * pool.s_r);
+#pragma unroll
+      for (int k = 0; k < kPasses; ++k) {
+        const int r = row0 + k * Lane<D>::kRows + l.slot, blk = (r >> p.shift) & 15;
+        const int e_new = __shfl_sync(0xffffffffu, now, blk), e_old = __shfl_sync(0xffffffffu, old, blk);
+        if (r >= p.panel || page[blk] < 0 || (!is_new[k] && e_new == e_old)) continue;
+        unsigned char* o = pool.p + (page[blk] * pool.s_n + h * pool.s_h + (first_row[blk] + (r & (S - 1))) * pool.s_r);
         uint2 y0, y1;
-        if (nw) {
-          const float f = pow2(-now);
+        if (is_new[k]) {
+          const float f = pow2(-e_new);
           float v[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            v[j] = fabsf(x[j]) <= 3.4028235e38f && now < 128 ? x[j] * f : __uint_as_float(0x7fc00000u);
+            v[j] = fabsf(x[k][j]) <= 3.4028235e38f && e_new < 128 ? x[k][j] * f : __uint_as_float(0x7fc00000u);
           y0.x = to_e4m3x2(v[0], v[1]) | to_e4m3x2(v[2], v[3]) << 16;
           y0.y = to_e4m3x2(v[4], v[5]) | to_e4m3x2(v[6], v[7]) << 16;
           y1.x = to_e4m3x2(v[8], v[9]) | to_e4m3x2(v[10], v[11]) << 16;
           y1.y = to_e4m3x2(v[12], v[13]) | to_e4m3x2(v[14], v[15]) << 16;
         } else {  // the scale rose: rounded again
-          const float f = pow2(old - now);
+          const float f = pow2(e_old - e_new);
           auto again = [f](uint32_t z) {
-            const float2 a = e4m3x2_to_f2(z & 0xffffu), c = e4m3x2_to_f2(z >> 16);
-            return to_e4m3x2(a.x * f, a.y * f) | to_e4m3x2(c.x * f, c.y * f) << 16;
+            const float2 u = e4m3x2_to_f2(z & 0xffffu), c = e4m3x2_to_f2(z >> 16);
+            return to_e4m3x2(u.x * f, u.y * f) | to_e4m3x2(c.x * f, c.y * f) << 16;
           };
           y0 = *reinterpret_cast<const uint2*>(o + l.a0);
           y1 = *reinterpret_cast<const uint2*>(o + l.a1);
@@ -392,24 +406,15 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
         }
         *reinterpret_cast<uint2*>(o + l.a0) = y0;
         *reinterpret_cast<uint2*>(o + l.a1) = y1;
-      };
-      for (int k = 0; k < passes; ++k) {
-        const int r = k * Lane<D>::kRows + l.slot;
-        if (k == k_held) {
-          put(r, true, held);
-        } else {
-          float x[16];
-          const bool nw = values(r, x);
-          put(r, nw, x);
-        }
       }
-      __syncwarp();
     }
     __syncthreads();
   }
 }
 
-// ---- reading back: 16 numbers a thread, kRead rows in flight
+// ---- reading back: 16 numbers a thread (8 looked up pages and scales twice as
+// often: 163 us in place of 135 for a cache of 131072 rows and 8 heads), stored
+// by whole sectors, kRead rows in flight
 constexpr int kRead = 4;
 struct ReadParams {
   Pool pool[2];
@@ -418,7 +423,7 @@ struct ReadParams {
   const int32_t* pos;
   int64_t p_b, p_t;
   int T, H, shift;
-  bool vec;  // 16-byte stores
+  bool vec;  // 32-byte stores
   PageTable pages;
 };
 
@@ -426,7 +431,7 @@ struct ReadParams {
 template <typename TO>
 __device__ __forceinline__ void put16(TO* o, int64_t s_d, bool vec, const uint4& w, float f) {
   float x[16];
-  const uint32_t* v = &w.x;
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 a = e4m3x2_to_f2(v[j] & 0xffffu), c = e4m3x2_to_f2(v[j] >> 16);
@@ -439,16 +444,18 @@ __device__ __forceinline__ void put16(TO* o, int64_t s_d, bool vec, const uint4&
 #pragma unroll
     for (int j = 0; j < 16; ++j) o[j * s_d] = from_f32<TO>(x[j]);
   } else if constexpr (sizeof(TO) == 2) {
-    uint4 y[2];
-    uint32_t* z = &y[0].x;
+    Vec<float, 8> y;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) z[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
-    reinterpret_cast<uint4*>(o)[0] = y[0];
-    reinterpret_cast<uint4*>(o)[1] = y[1];
+    for (int j = 0; j < 8; ++j) y.x[j] = __uint_as_float(pack_bf16(x[2 * j], x[2 * j + 1]));
+    store(reinterpret_cast<float*>(o), y);
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      reinterpret_cast<float4*>(o)[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+    for (int j = 0; j < 2; ++j) {
+      Vec<float, 8> y;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y.x[i] = x[8 * j + i];
+      store(o + 8 * j, y);
+    }
   }
 }
 
@@ -573,12 +580,12 @@ Pool pool_of(const blkattn_tensor& t, const blkattn_tensor* e) {
   return {static_cast<unsigned char*>(t.data), t.strides[0], t.strides[1], t.strides[2],
           static_cast<unsigned char*>(e->data), e->strides[0], e->strides[1], e->strides[2]};
 }
-// Rows that the kernels move by 16 bytes (a stride of a dim of size 1 is not used).
-bool vec_rows(const blkattn_tensor* t) {
+// Rows that the kernels move by 16 (or 32) bytes (a stride of a dim of size 1 is not used).
+bool vec_rows(const blkattn_tensor* t, int access = 16) {
   const int64_t bytes = t->dtype == BLKATTN_BF16 ? 2 : 4;
-  if (t->strides[3] != 1 || reinterpret_cast<uintptr_t>(t->data) % 16 != 0) return false;
+  if (t->strides[3] != 1 || reinterpret_cast<uintptr_t>(t->data) % access != 0) return false;
   for (int i = 0; i < 3; ++i)
-    if (t->sizes[i] > 1 && t->strides[i] * bytes % 16 != 0) return false;
+    if (t->sizes[i] > 1 && t->strides[i] * bytes % access != 0) return false;
   return true;
 }
 
@@ -707,7 +714,8 @@ int blkattn_paged_append_q8(const blkattn_tensor* k, const blkattn_tensor* v, co
   p.B = (int)B; p.T = (int)T; p.Hkv = (int)H; p.Hq = (int)Hq;
   p.shift = shift;
   p.panel = (1 << shift) < 16 ? 16 : 1 << shift;
-  p.kv_groups = (int)((H + kKvHeads - 1) / kKvHeads);
+  const int parts = p.panel * (int)d / 2048 < 1 ? 1 : p.panel * (int)d / 2048;  // (as in the kernel)
+  p.kv_groups = (int)((2 * H * parts + kWarps - 1) / kWarps);
   p.pages = pt;
   const int64_t blocks = B * ((T + p.panel - 1) / p.panel);
   if (blocks > 0x7fffffff) return BLKATTN_ERR_UNSUPPORTED;
@@ -765,7 +773,7 @@ int blkattn_paged_read_q8(const blkattn_tensor* pos, const blkattn_tensor* page_
   p.pos = static_cast<const int32_t*>(pos->data);
   p.p_b = pos->strides[0]; p.p_t = pos->strides[1];
   p.T = (int)T; p.H = (int)H; p.shift = shift;
-  p.vec = vec_rows(k_out) && vec_rows(v_out);
+  p.vec = vec_rows(k_out, 32) && vec_rows(v_out, 32);
   p.pages = pt;
   const int rows = kThreads / (int)(d / 16) * kRead;
   const dim3 grid((unsigned)((T + rows - 1) / rows), (unsigned)(2 * H), (unsigned)B);

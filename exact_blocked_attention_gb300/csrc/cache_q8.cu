@@ -39,6 +39,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kQHeads = 32;   // query heads of a CTA
+constexpr int kScan = 8;      // positions of a lane in flight where padding is passed over (one: 17 us past 1500 rows)
 // query rows from which on they have a kernel of their own
 constexpr int64_t kOwnKernelRows = 16384;
 
@@ -247,11 +248,13 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
   __shared__ int page[16], first_row[16];   // of the panel's blocks: page (-1: none), row in page
   __shared__ float amax[kWarps][kMaxScaleRows];  // of each pair's rows
   const int S = 1 << p.shift;
-  if (threadIdx.x == 0) n_lead = 0;
   // `parts` warps share a pair's rows, kPasses passes each
   constexpr int kPasses = 4;
   const int parts = max(1, p.panel / (kPasses * Lane<D>::kRows)), part = warp % parts;
-  const int pair = blockIdx.y * (kWarps / parts) + warp / parts, h = pair >> 1, which = pair & 1;  // K, V
+  // pairs: K's heads, then V's (whose CTAs need no angles)
+  const int pair = blockIdx.y * (kWarps / parts) + warp / parts, which = pair >= p.Hkv ? 1 : 0;
+  const int h = pair - which * p.Hkv;
+  const bool turns = p.rot > 0 && (int)blockIdx.y * (kWarps / parts) < p.Hkv;
   const int row0 = part * kPasses * Lane<D>::kRows;
   // the first rows, on their way while the runs are found
   if (part == 0 && h < p.Hkv && lane < 2 * n) {
@@ -260,14 +263,22 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
                                                   (lane & 1) * (D / 2) * rows.s_d);
     asm volatile("prefetch.global.L1 [%0];" ::"l"(r));
   }
-  __syncthreads();
   if (warp == 0) {
+    int found = 0;
     // the last row before the window that is not padding
     int prev = -1;
-    for (int u = t0 - 32; u > -32 && prev < 0; u -= 32) {
-      const int v = u + lane >= 0 ? pos[(u + lane) * p.p_t] : -1;
-      const unsigned m = __ballot_sync(0xffffffffu, v >= 0);
-      if (m) prev = __shfl_sync(0xffffffffu, v, 31 - __clz(m));
+    for (int u = t0; u > 0 && prev < 0; u -= 32 * kScan) {
+      int v[kScan];
+#pragma unroll
+      for (int i = 0; i < kScan; ++i) {
+        const int t = u - 32 * (i + 1) + lane;
+        v[i] = t >= 0 ? pos[t * p.p_t] : -1;
+      }
+#pragma unroll
+      for (int i = 0; i < kScan; ++i) {
+        const unsigned m = __ballot_sync(0xffffffffu, v[i] >= 0);
+        if (m && prev < 0) prev = __shfl_sync(0xffffffffu, v[i], 31 - __clz(m));
+      }
     }
     for (int i0 = 0; i0 < n; i0 += 32) {
       const int c = i0 + lane < n ? pos[(t0 + i0 + lane) * p.p_t] : -1;
@@ -276,12 +287,11 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
       const int from = below ? near : prev;
       const bool leads = c >= 0 && page_of(p.pages, b, c) >= 0 && (from < 0 || (from >> p.shift) != (c >> p.shift));
       const unsigned m = __ballot_sync(0xffffffffu, leads);
-      if (leads) lead[n_lead + __popc(m & ((1u << lane) - 1))] = t0 + i0 + lane;
+      if (leads) lead[found + __popc(m & ((1u << lane) - 1))] = t0 + i0 + lane;
       if (rows) prev = __shfl_sync(0xffffffffu, c, 31 - __clz(rows));
-      __syncwarp();
-      if (lane == 0) n_lead += __popc(m);
-      __syncwarp();
+      found += __popc(m);
     }
+    if (lane == 0) n_lead = found;
   }
   float w[16];
 #pragma unroll
@@ -291,21 +301,27 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
   __syncthreads();
   const int runs = n_lead;
   for (int r0 = 0; r0 < runs; r0 += per_panel) {
-    for (int i = threadIdx.x; i < p.panel; i += kThreads) src[i] = -1;
-    __syncthreads();
     for (int k = warp; k < per_panel; k += kWarps) {  // the runs' rows, a warp a run
       int pg = -1, row = 0;
+      for (int i = lane; i < S; i += 32) src[k * S + i] = -1;
+      __syncwarp();
       if (r0 + k < runs) {
         const int t = lead[r0 + k], c = pos[t * p.p_t];
         pg = page_of(p.pages, b, c);
         row = (c & (p.pages.rows - 1)) & ~(S - 1);
         bool more = true;
-        for (int u = t; more && u < p.T; u += 32) {
-          const int v = u + lane < p.T ? pos[(u + lane) * p.p_t] : -1;
-          const unsigned other = __ballot_sync(0xffffffffu, v >= 0 && (v >> p.shift) != (c >> p.shift));
-          const int end = other ? __ffs(other) - 1 : 32;
-          if (lane < end && v >= 0) atomicMax(&src[k * S + (v & (S - 1))], u + lane);  // (the later row stays)
-          more = other == 0;
+        for (int u = t; more && u < p.T; u += 32 * kScan) {
+          int v[kScan];
+#pragma unroll
+          for (int i = 0; i < kScan; ++i) v[i] = u + 32 * i + lane < p.T ? pos[(u + 32 * i + lane) * p.p_t] : -1;
+#pragma unroll
+          for (int i = 0; i < kScan; ++i) {
+            const unsigned other = __ballot_sync(0xffffffffu, v[i] >= 0 && (v[i] >> p.shift) != (c >> p.shift));
+            const int end = other ? __ffs(other) - 1 : 32;
+            if (more && lane < end && v[i] >= 0)
+              atomicMax(&src[k * S + (v[i] & (S - 1))], u + 32 * i + lane);  // (the later row stays)
+            more = more && other == 0;
+          }
         }
       }
       if (lane == 0) {
@@ -313,8 +329,6 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
         first_row[k] = row;
       }
     }
-    __syncthreads();
-    if (p.rot) fill_angles(p, cs, p.panel, [&](int i) { return src[i] < 0 ? -1 : pos[src[i] * p.p_t]; });
     __syncthreads();
     // the warp's pair (head, K or V) and its rows of the panel: kPasses passes of them, in registers
     const bool works = pair < 2 * p.Hkv;
@@ -341,6 +355,10 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
     if (works && lane < per_panel && page[lane] >= 0) {
       scale = pool.scales + (page[lane] * pool.e_n + h * pool.e_h + (first_row[lane] >> p.shift) * pool.e_i);
       old = (int)*scale - 127;
+    }
+    if (turns) {  // (while the rows arrive)
+      fill_angles(p, cs, p.panel, [&](int i) { return src[i] < 0 ? -1 : pos[src[i] * p.p_t]; });
+      __syncthreads();
     }
     if (works) {
 #pragma unroll

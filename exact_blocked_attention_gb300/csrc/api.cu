@@ -322,15 +322,18 @@ int tensor_map(int dev, const blkattn_tensor* t, int box_cols, int box_rows, CUt
   if (st != BLKATTN_OK) return st;
   MapEntry& e = g_maps[g_map_next];
   g_map_next = (g_map_next + 1) % kMapCache;
-  const bool f32 = t->dtype == BLKATTN_F32;
-  const cuuint64_t eb = f32 ? 4 : 2;
+  const bool f32 = t->dtype == BLKATTN_F32, bytes = t->dtype == BLKATTN_E4M3;
+  const cuuint64_t eb = f32 ? 4 : (bytes ? 1 : 2);
   const cuuint64_t dims[4] = {(cuuint64_t)t->sizes[3], (cuuint64_t)t->sizes[2], (cuuint64_t)t->sizes[1],
                               (cuuint64_t)t->sizes[0]};
   const cuuint64_t strides[3] = {(cuuint64_t)t->strides[2] * eb, (cuuint64_t)t->strides[1] * eb,
                                  (cuuint64_t)t->strides[0] * eb};
   const cuuint32_t box[4] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  const CUresult r = g_encode(&e.map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+  const CUresult r = g_encode(&e.map, f32     ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                         : bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                              4,
                               t->data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1153,13 +1156,37 @@ int fwd_paged_q8_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages, c
   }
 
   const int64_t rows = c.Hq / c.Hkv * c.Tq;
-  int64_t nb = c.B < kDecodeQ8MaxBatch ? c.B : kDecodeQ8MaxBatch;
-  Q8Plan pl = plan_decode_q8(nb, c.Hkv, rows, c.Tmax, (int)c.d, ds->sms);
-  while (nb > 1 && pl.tiles > kDecodeQ8MaxTiles) {
-    nb = (nb + 1) / 2;
-    pl = plan_decode_q8(nb, c.Hkv, rows, c.Tmax, (int)c.d, ds->sms);
+  int64_t nb = c.B;
+  Q8Plan pl;
+  // tcgen05: heads of 128, bf16 results, contiguous query rows, as many sequences
+  // a launch as the kernel takes
+  bool tc = c.d == 128 && out->dtype == BLKATTN_BF16 && c.q_vec_ok;
+  if (const char* force = std::getenv("BLKATTN_KERNEL")) tc = tc && std::strcmp(force, "mma") != 0;  // comparison runs only
+  if (tc) {
+    pl = plan_decode_tc_q8(nb, c.Hkv, rows, c.Tmax, ds->sms);
+    while (nb > 1 && !decode_tc_q8_takes(pl, nb, c.Tmax)) {
+      nb = (nb + 1) / 2;
+      pl = plan_decode_tc_q8(nb, c.Hkv, rows, c.Tmax, ds->sms);
+    }
+    tc = decode_tc_q8_takes(pl, nb, c.Tmax);
   }
-  if (pl.tiles > kDecodeQ8MaxTiles) return BLKATTN_ERR_UNSUPPORTED;
+  if (!tc) {
+    nb = c.B < kDecodeQ8MaxBatch ? c.B : kDecodeQ8MaxBatch;
+    pl = plan_decode_q8(nb, c.Hkv, rows, c.Tmax, (int)c.d, ds->sms);
+    while (nb > 1 && pl.tiles > kDecodeQ8MaxTiles) {
+      nb = (nb + 1) / 2;
+      pl = plan_decode_q8(nb, c.Hkv, rows, c.Tmax, (int)c.d, ds->sms);
+    }
+    if (pl.tiles > kDecodeQ8MaxTiles) return BLKATTN_ERR_UNSUPPORTED;
+  }
+  CUtensorMap mk, mv;
+  if (tc) {
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return cuda_fail(e);
+    const int box = pt.rows < 128 ? pt.rows : 128;
+    if ((st = tensor_map(dev, &kn, 128, box, &mk)) != BLKATTN_OK) return st;
+    if ((st = tensor_map(dev, &vn, 128, box, &mv)) != BLKATTN_OK) return st;
+  }
   if ((st = ensure_workspace(ds, pl.ws_bytes, stream)) != BLKATTN_OK) return st;
   if ((st = ensure_counters(ds, pl.units, stream)) != BLKATTN_OK) return st;
   Q8Params p{};
@@ -1193,6 +1220,7 @@ int fwd_paged_q8_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages, c
   p.rows_cta = pl.rows_cta;
   p.ws = static_cast<float*>(ds->ws);
   p.cnt = ds->cnt;
+  p.err = ds->err;
   p.pages = pt;
   for (int64_t b0 = 0; b0 < c.B; b0 += nb) {  // (slices run one after another in the same workspace)
     p.B = (int)(c.B - b0 < nb ? c.B - b0 : nb);
@@ -1203,7 +1231,10 @@ int fwd_paged_q8_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages, c
     p.out = static_cast<char*>(out->data) + b0 * p.o_sb * elt_bytes(out->dtype);
     p.lse = static_cast<float*>(lse->data) + b0 * p.l_sb;
     p.pages.table = pt.table + b0 * pt.sb;
-    if (cudaError_t e = launch_decode_q8(p, (int)c.d, pl.ctas, stream); e != cudaSuccess) return cuda_fail(e);
+    if (cudaError_t e = tc ? launch_decode_tc_q8(p, pl.ctas, mk, mv, stream)
+                           : launch_decode_q8(p, (int)c.d, pl.ctas, stream);
+        e != cudaSuccess)
+      return cuda_fail(e);
   }
   return BLKATTN_OK;
 }

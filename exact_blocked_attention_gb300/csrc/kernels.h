@@ -201,6 +201,7 @@ struct Q8Params {
   int row_groups, rows_cta;  // of the G Tq rows of a KV head
   float* ws;      // partial states: [CTAs + units][M, l, R of the rows], then their u
   unsigned* cnt;  // a unit's CTAs that have written theirs (zero before and after)
+  int* err;       // device error word
   PageTable pages;
 };
 struct Q8Plan {
@@ -213,6 +214,12 @@ constexpr int64_t kDecodeQ8MaxTiles = 1 << 30;
 constexpr int kDecodeQ8MaxCtas = 512;  // parts of a unit
 Q8Plan plan_decode_q8(int64_t B, int64_t Hkv, int64_t rows, int64_t Tmax, int d, int sms);
 cudaError_t launch_decode_q8(const Q8Params& p, int d, int ctas, cudaStream_t stream);
+// The same on tcgen05 (d = 128, contiguous 16-byte aligned query rows); maps over
+// the pools' bytes, boxes of 128 x min(rows of a page, 128), 128-byte swizzle.
+Q8Plan plan_decode_tc_q8(int64_t B, int64_t Hkv, int64_t rows, int64_t Tmax, int sms);
+bool decode_tc_q8_takes(const Q8Plan& pl, int64_t B, int64_t Tmax);
+cudaError_t launch_decode_tc_q8(const Q8Params& p, int ctas, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                                cudaStream_t stream);
 
 // The visible pages of `B` sequences as bf16: row t of sequence b to row t mod P
 // of page b entries + t / P of k_out, v_out [B entries, Hkv, P, d] (contiguous),

@@ -11,6 +11,11 @@ for f32; below 2^-36 of the largest weight times scale it loses all of it.  Both
 sums over n keys are fp32 (2^-23 a step).  With e = E + 2^-11 (f32: 2^-21)
 + 2^-21 + n 2^-23, out is off by at most 2 e sum p |v| / sum p, plus
 n 2^-36 448 max (p 2^ev) / sum p; lse by E + 2^-21 + n 2^-23 and 2^-21 |lse|.
+Heads of 128 with a bf16 out go to the tcgen05 kernel.  Its scores add the rest
+of q below 2^-22 of the row's largest dim, scale 2^-22 max |q| sum |k| each, its
+weights are f16 in e4m3 pieces: 2^-11 and a step of 2^-25 (q rows of a unit <= 32:
+2^-29) of the largest weight times scale, which takes the place of 2^-36 (half a
+step, and up to 2^1 of lazy reference: 2^-25 again).
 Prompts that go through the bf16 kernel have its bounds (test_gpu_paged.py):
 2^-8 and 2^-16 in place of 2^-11.  A bf16 store adds 2^-8 of the value.
 """
@@ -84,6 +89,8 @@ def reference(a, out_dtype):
     table, lens, pos = a["table"].cpu(), a["lens"].cpu(), a["pos"].cpu()
     prompt = Tq >= 64 and a["tree"] is None and a["scale"] > 0 and q.stride(3) == 1 and q.stride(2) % 8 == 0
     wt = 2.0 ** -8 + 2.0 ** -16 if prompt else (2.0 ** -11 if out_dtype == BF16 else 2.0 ** -21)
+    pieces = d == 128 and out_dtype == BF16 and not prompt
+    step = 2.0 ** -25 if pieces else 2.0 ** -36
     for b in range(B):
         n = max(0, min(int(lens[b]), table.shape[1] * P))
         ent = table[b, : -(-n // P)].long()
@@ -112,7 +119,11 @@ def reference(a, out_dtype):
             k, _, v, fv = kv
             z = torch.einsum("gtd,nd->gtn", q[b, h * G:(h + 1) * G].double(), k) * a["scale"]
             E = torch.einsum("gtd,nd->gtn", q[b, h * G:(h + 1) * G].double().abs(), k.abs()) * abs(a["scale"])
-            E = (E * 2.0 ** -23 * (d + 6)).masked_fill(~see, 0.0).amax(-1)
+            E = E * 2.0 ** -23 * (d + 6)
+            if pieces:
+                top = q[b, h * G:(h + 1) * G].double().abs().amax(-1, keepdim=True)
+                E = E + 2.0 ** -22 * abs(a["scale"]) * top * k.abs().sum(-1)
+            E = E.masked_fill(~see, 0.0).amax(-1)
             z = z.masked_fill(~see, -math.inf)
             m = z.amax(-1, keepdim=True)
             m = torch.where(m == -math.inf, 0.0, m)
@@ -121,7 +132,7 @@ def reference(a, out_dtype):
             l1 = torch.where(l > 0, l, 1.0)
             out[b, h * G:(h + 1) * G] = torch.where(l > 0, w @ v / l1, 0.0)
             e = E + wt + 2.0 ** -21 + n * 2.0 ** -23
-            lost = n * 2.0 ** -36 * 448 * (w * fv).amax(-1, keepdim=True) / l1
+            lost = n * step * 448 * (w * fv).amax(-1, keepdim=True) / l1
             ob[b, h * G:(h + 1) * G] = 2 * e[..., None] * (w @ v.abs() / l1) + torch.where(l > 0, lost, 0.0)
             s = (m + torch.log(l))[..., 0]
             lse[b, h * G:(h + 1) * G] = s

@@ -39,23 +39,20 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
-constexpr float kLazyM = 8.f, kLazyR = 1.f;
-constexpr float kLift = 7.f;          // weights reach 2^(kLift + kLazyR) = 256 of e4m3's 448
+constexpr float kLazyM = 8.f;
+constexpr float kLift = 7.f;          // a weight at the reference; kMostW before the reference rises, of e4m3's 448
+constexpr float kMostW = 256.f;
 
 constexpr int D = 128;
-constexpr int BK = 128;               // keys per tile (TMEM lanes of S^T)
-constexpr int kSlotBytes = BK * D;    // a tile of K or V: 128 rows of 128 bytes
-constexpr int kKeyWarps = 8;          // two warps per TMEM lane quarter, each with half of the rows
+constexpr int BK = 128;               // keys of a product (TMEM lanes of S^T)
+constexpr int kSlotBytes = BK * D;    // a ring slot, K or V: 128 rows of 128 bytes
+constexpr int kKeyWarps = 8;          // two warps per TMEM lane quarter
 constexpr int kKeyThreads = 32 * kKeyWarps;
 constexpr int kPageKWarp = 8;
 constexpr int kMmaWarp = 9;
 constexpr int kLoadWarp = 10;
 constexpr int kPageVWarp = 11;
 constexpr int kThreads = 32 * 12;
-// Tiles whose scales lie in shared memory.  The K producer writes those of tile g
-// once the slot of K_g is free: U_{g-4} or S_{g-5} has completed, so P_{g-7} was
-// written and the key threads are done with tile g - 7.
-constexpr int kScaleRing = 8;
 constexpr int kBarRows = 1;           // named barrier of the key threads
 constexpr uint32_t kTmemCols = 512;
 
@@ -98,13 +95,25 @@ struct RowFacts {
 
 template <int NR>
 struct TcLayout {
+  // Up to 16 rows a tile is 256 keys, two subtiles, one for each half of the key
+  // threads: what a tile takes is a chain of waits, loads and a vote, some 1.4 us
+  // whatever its size.  More rows: 128 keys, half of the rows for each half.
+  static constexpr int kSub = NR <= 16 ? 2 : 1;
+  static constexpr int kTileKeys = kSub * BK;
   static constexpr int kPieces = NR > 32 ? 3 : 4;
   static constexpr int kPN = kPieces * NR;                   // N of the value product
-  static constexpr int kPBytes = (kPN > 128 ? 2 : 1) * BK * 128;  // one P^T buffer: atoms of 128 columns
+  static constexpr int kPSub = (kPN > 128 ? 2 : 1) * BK * 128;  // P^T of a subtile: atoms of 128 columns
+  static constexpr int kPBytes = kSub * kPSub;               // one P^T buffer
   static constexpr int kQBytes = 2 * NR * 128;               // q_hi rows, then q_lo rows
-  static constexpr int kSlots = NR > 32 ? 7 : 10;
-  static constexpr uint32_t kColS = 0;                       // S^T: tiles of even / odd index
-  static constexpr uint32_t kStepS = 2 * NR;
+  static constexpr int kSlots = NR > 32 ? 7 : (NR > 16 ? 10 : 8);
+  // Subtiles whose scales lie in shared memory.  The K producer writes those of
+  // subtile e once the slot of K_e is free: S of subtile e - 5 (U of e - 4 with 7
+  // slots) has completed, so P of the tile two before that one's was written and
+  // the key threads are done with it and with subtile e - 7 (kSub = 2: e - 10).
+  static constexpr int kScaleRing = kSub == 2 ? 16 : 8;
+  static constexpr uint32_t kColS = 0;                       // S^T: tiles of even / odd index, their subtiles
+  static constexpr uint32_t kSubS = 2 * NR;
+  static constexpr uint32_t kStepS = kSub * kSubS;
   static constexpr uint32_t kColU = 2 * kStepS;              // U^T: units of even / odd index
   static constexpr uint32_t kStepU = kPN;
   static constexpr int kOffQ = kSlots * kSlotBytes;              // two query buffers
@@ -112,10 +121,10 @@ struct TcLayout {
   static constexpr int kOffRows = kOffP + 2 * kPBytes;           // RowFacts[2]
   static constexpr int kRowsBytes = (int)((sizeof(RowFacts<NR>) + 15) / 16 * 16);
   static constexpr int kOffNTab = kOffRows + 2 * kRowsBytes;     // uint16 tiles, first tile per (sequence, row group)
-  static constexpr int kOffRed = kOffNTab + 2 * kDecodeTcMaxEntries * 2;  // float [4][NR]
-  // float [NR] each: m, m_use, thr, r, r_thr, 2^(lift - r), alpha of l, alpha of U of the
+  static constexpr int kOffRed = kOffNTab + 2 * kDecodeTcMaxEntries * 2;  // float [8][NR]
+  // float [NR] each: m, m_use, thr, r, (unused), 2^(lift - r), alpha of l, alpha of U of the
   // current unit; m, l, r, 1 / l of the finished unit whose U readout is pending
-  static constexpr int kOffStat = kOffRed + 4 * NR * 4;
+  static constexpr int kOffStat = kOffRed + 8 * NR * 4;
   static constexpr int kOffScale = kOffStat + 12 * NR * 4;       // float2 [kScaleRing][BK]: 2^ek, ev (-inf: no key)
   static constexpr int kOffBar = kOffScale + kScaleRing * BK * 8;
   // full[kSlots], empty[kSlots], q_full[2], q_empty[2], p_full[2], u_full[2], drain, sc_full[kScaleRing]
@@ -144,7 +153,8 @@ struct Cursor {
   int extra;
   int s0;               // the unit's first tile (sliding window; 0 otherwise)
   const uint16_t* st;   // per-unit first tiles, or nullptr
-  __device__ __forceinline__ int key0() const { return (s0 + j) * BK; }
+  int tk;               // keys of a tile
+  __device__ __forceinline__ int key0() const { return (s0 + j) * tk; }
   // to the first tile of the next unit
   __device__ __forceinline__ void step_unit(const uint16_t* ntab, int RG, int Hkv, int B) {
     su += n + extra;
@@ -247,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = TcLayout<NR>;
   constexpr uint32_t kIdescQK = idesc_e4m3(128, 2 * NR, 0, 0);   // K, Q both K-major
   constexpr uint32_t kIdescPV = idesc_e4m3(128, L::kPN, 1, 1);   // V^T, P^T both MN-major
-  constexpr int kSlots = L::kSlots;
+  constexpr int kSlots = L::kSlots, kSub = L::kSub, TK = L::kTileKeys, kScaleRing = L::kScaleRing;
   constexpr int kPieces = L::kPieces;
   // weight-only tiles per unit in the partition (its set-up and readout)
   constexpr int kUnitExtra = NR >= 48 ? 2 : 0;
@@ -262,7 +272,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* s_muse = s_m + NR;                                  // m, or 0 when none yet
   float* s_thr = s_m + 2 * NR;                               // m + 8, -inf when none yet
   float* s_r = s_m + 3 * NR;                                 // reference of the weights, -inf = none yet
-  float* s_rthr = s_m + 4 * NR;                              // r + 1, -inf when none yet
   float* s_h = s_m + 5 * NR;                                 // 2^(lift - r), 1 when none yet
   float* s_alpha = s_m + 6 * NR;
   float* s_beta = s_m + 7 * NR;
@@ -326,8 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int len = len_raw < 0 ? 0 : (len_raw > p.Tmax ? p.Tmax : len_raw);
       const int uend = maxpos < 0 ? 0 : min(maxpos, len - 1) + 1;  // (a position may be INT_MAX)
       // sliding window: the unit starts at the tile of its earliest visible key
-      const int s0 = (p.window > 0 && minpos != 0x7fffffff) ? max(0, minpos - p.window + 1) / BK : 0;
-      const int n = (uend + BK - 1) / BK - s0;
+      const int s0 = (p.window > 0 && minpos != 0x7fffffff) ? max(0, minpos - p.window + 1) / TK : 0;
+      const int n = (uend + TK - 1) / TK - s0;
       ntab[e] = (uint16_t)(n < 1 ? 1 : n);  // an all-empty unit still takes one (masked) tile
       if (p.window > 0) stab[e] = (uint16_t)s0;
     }
@@ -353,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x < NR) {
       s_m[threadIdx.x] = kNegInf;
       s_muse[threadIdx.x] = 0.f;
-      s_thr[threadIdx.x] = s_r[threadIdx.x] = s_rthr[threadIdx.x] = kNegInf;
+      s_thr[threadIdx.x] = s_r[threadIdx.x] = kNegInf;
       s_h[threadIdx.x] = 1.f;
     }
     if (warp == kMmaWarp) {
@@ -454,6 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   cur.j = start->j;
   cur.n = (t0 < t1) ? (int)ntab[cur.b * RG + cur.rg] : 1;
   cur.extra = kUnitExtra;
+  cur.tk = TK;
   cur.st = p.window > 0 ? stab : nullptr;
   cur.s0 = (t0 < t1 && cur.st != nullptr) ? (int)stab[cur.b * RG + cur.rg] : 0;
   // a range may start among a unit's weight-only tiles: begin at the next unit
@@ -476,8 +486,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // What the lane looks up for a tile, one tile ahead: its piece's table entry
     // and the sequence's length.
     int nx_key = 0, nx_entry = -1, nx_len = 0;
-    auto look_up = [&](const Cursor& c) {
-      nx_key = c.key0() + (piece << box_shift);
+    auto look_up = [&](const Cursor& c, int sub) {
+      nx_key = c.key0() + sub * BK + (piece << box_shift);
       nx_entry = entry_of(p.pages, c.b, nx_key);
       nx_len = p.seqlens[c.b * p.sl_s];
     };
@@ -493,16 +503,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t valid;  // bit i: key 4 l + i
     };
     Cursor at = cur;
+    int at_sub = 0;
     bool more = kv == 0 && at.t < t1;
     auto ask = [&]() {
       Ask a{-1, 0, 0, 0, more};
       if (more) {
-        a.key = at.key0() + 4 * lane;
+        a.key = at.key0() + at_sub * BK + 4 * lane;
         a.entry = entry_of(p.pages, at.b, a.key);
         a.len = p.seqlens[at.b * p.sl_s];
         a.kvh = at.kvh;
-        at.next(ntab, RG, Hkv, B);
-        more = at.t < t1;
+        if (++at_sub == kSub) {
+          at_sub = 0;
+          at.next(ntab, RG, Hkv, B);
+          more = at.t < t1;
+        }
       }
       return a;
     };
@@ -524,7 +538,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int64_t issued = 0;  // entries
     bool ok = true;
-    if (cur.t < t1) look_up(cur);
+    int sub = 0;
+    if (cur.t < t1) look_up(cur, 0);
     Ask a0 = ask(), a1 = ask(), a2 = ask();
     Bytes y0{{}, {}, 0}, y1{{}, {}, 0};
     for (int64_t g = 0; ok && cur.t < t1; ++g) {
@@ -532,9 +547,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kvh = cur.kvh;
       // past the length, or no page: -1 (zeros)
       const int page = nx_key < nx_len && (unsigned)nx_entry < (unsigned)p.pages.n_pages ? nx_entry : -1;
-      cur.next(ntab, RG, Hkv, B);
-      if (cur.t < t1) look_up(cur);
-      const int64_t seq = 2 * g + kv;
+      if (++sub == kSub) {
+        sub = 0;
+        cur.next(ntab, RG, Hkv, B);
+      }
+      if (cur.t < t1) look_up(cur, sub);
+      const int64_t seq = 2 * g + kv;  // (g counts subtiles)
       const int s = (int)(seq % kSlots);
       bool w = true;
       if (lane == 0) {
@@ -756,18 +774,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto issue_qk = [&](uint32_t buf) -> bool {
         const int qb = uq & 1;
         if (first_q && !mbar_wait(&q_full[qb], (uint32_t)((uq >> 1) & 1))) return false;
-        const uint32_t ks_slot = kpos.slot;
-        if (!mbar_wait(&full[ks_slot], kpos.phase)) return false;
-        kpos.adv2();
-        tc::fence_after();
-        // S^T = K_j Q^T into the S buffer of the tile's parity
-        const uint32_t klo = tc::desc_lo(sRing + ks_slot * kSlotBytes, 16);
         const uint32_t qlo = qlo0 + (uint32_t)(qb * L::kQBytes >> 4);
 #pragma unroll
-        for (int ks = 0; ks < D / 32; ++ks)
-          mma_f8(tb + L::kColS + L::kStepS * buf, tc::desc_join(klo + (uint32_t)(ks * 32 >> 4), kHi),
-                 tc::desc_join(qlo + (uint32_t)(ks * 32 >> 4), kHi), kIdescQK, ks > 0 ? 1u : 0u);
-        tc::commit(&empty[ks_slot]);  // K_j is free and S_j is ready
+        for (int x = 0; x < kSub; ++x) {
+          const uint32_t ks_slot = kpos.slot;
+          if (!mbar_wait(&full[ks_slot], kpos.phase)) return false;
+          kpos.adv2();
+          tc::fence_after();
+          // S^T = K_j Q^T into the S buffer of the tile's parity
+          const uint32_t klo = tc::desc_lo(sRing + ks_slot * kSlotBytes, 16);
+#pragma unroll
+          for (int ks = 0; ks < D / 32; ++ks)
+            mma_f8(tb + L::kColS + L::kStepS * buf + L::kSubS * x, tc::desc_join(klo + (uint32_t)(ks * 32 >> 4), kHi),
+                   tc::desc_join(qlo + (uint32_t)(ks * 32 >> 4), kHi), kIdescQK, ks > 0 ? 1u : 0u);
+          tc::commit(&empty[ks_slot]);  // K_j is free and S_j is ready
+        }
         first_q = false;
         if (--left_q == 0) {
           tc::commit(&q_empty[qb]);
@@ -783,20 +804,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (ok && left > 0) {
         if (left_q > 0 && !issue_qk(buf ^ 1u)) { ok = false; break; }
         // U^T += V_j^T [P_hi | P_lo]^T once the key threads wrote P^T
-        const uint32_t vs_slot = vpos.slot;
         if (!mbar_wait(&p_full[buf], p_phase)) { ok = false; break; }
-        if (!mbar_wait(&full[vs_slot], vpos.phase)) { ok = false; break; }
-        vpos.adv2();
-        tc::fence_after();
-        const uint32_t vlo = tc::desc_lo(sRing + vs_slot * kSlotBytes, 16);
-        const uint32_t plo = tc::desc_lo(sP + buf * L::kPBytes, BK * 128);  // (atoms of 128 columns 16 KB apart)
         const uint32_t ucol = tb + L::kColU + L::kStepU * (uint32_t)(up & 1);
 #pragma unroll
-        for (int ks = 0; ks < BK / 32; ++ks)
-          // A = V^T: 128 dims x keys [32 ks, +32); B = P^T: the same keys x the pieces
-          mma_f8(ucol, tc::desc_join(vlo + (uint32_t)(ks * 4096 >> 4), kHi),
-                 tc::desc_join(plo + (uint32_t)(ks * 4096 >> 4), kHi), kIdescPV, (!first || ks > 0) ? 1u : 0u);
-        tc::commit(&empty[vs_slot]);
+        for (int x = 0; x < kSub; ++x) {
+          const uint32_t vs_slot = vpos.slot;
+          if (!mbar_wait(&full[vs_slot], vpos.phase)) { ok = false; break; }
+          vpos.adv2();
+          tc::fence_after();
+          const uint32_t vlo = tc::desc_lo(sRing + vs_slot * kSlotBytes, 16);
+          const uint32_t plo = tc::desc_lo(sP + buf * L::kPBytes + x * L::kPSub, BK * 128);  // (atoms of 128 columns 16 KB apart)
+#pragma unroll
+          for (int ks = 0; ks < BK / 32; ++ks)
+            // A = V^T: 128 dims x keys [32 ks, +32); B = P^T: the same keys x the pieces
+            mma_f8(ucol, tc::desc_join(vlo + (uint32_t)(ks * 4096 >> 4), kHi),
+                   tc::desc_join(plo + (uint32_t)(ks * 4096 >> 4), kHi), kIdescPV,
+                   (!first || x > 0 || ks > 0) ? 1u : 0u);
+          tc::commit(&empty[vs_slot]);
+        }
+        if (!ok) break;
         first = false;
         p_phase ^= buf;
         buf ^= 1u;
@@ -821,13 +847,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---------------- key threads ----------------
-    // warp w: TMEM lane quarter (w mod 4), row half (w / 4): thread = key k of the
-    // tile (value dim k in the epilogue), rows [c0, c0 + NH)
-    constexpr int NH = NR / 2;
+    // warp w: TMEM lane quarter (w mod 4) and half w / 4: thread = key k of the
+    // tile's subtile `half` with all rows, or key k with the rows of its half; value
+    // dim k in the epilogue, with the rows [cu, cu + NU) (subtiles: half 0 alone)
+    constexpr int NH = NR / (3 - kSub), NU = NR / (3 - kSub);
+    constexpr int kRed = kSub == 2 ? 8 : 4;  // warps that share a row's maximum
     const int quarter = warp & 3;
     const int half = warp >> 2;
     const int k = 32 * quarter + lane;
-    const int c0 = half * NH;
+    const int sub = kSub == 2 ? half : 0;
+    const int c0 = kSub == 2 ? 0 : half * NH, cu = c0;
+    const bool has_u = kSub == 1 || half == 0;
+    const int red_row = kSub == 2 ? warp : quarter;
     const uint32_t tl = tb + ((uint32_t)(32 * quarter) << 16);
     auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity));
@@ -862,16 +893,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const RowFacts<NR>& pf = facts0[pb];
       if (!bar_and(kBarRows, kKeyThreads, wait_all(&u_full[pb], (uint32_t)((pend_uidx >> 1) & 1)))) return false;
       tc::fence_after();
-      float u[NH];
-      {
-        const uint32_t ua = tl + L::kColU + L::kStepU * (uint32_t)pb + c0;
-        ld_cols<NH>(ua + (kPieces - 1) * NR, u);
+      float u[NU];
+      if (has_u) {
+        const uint32_t ua = tl + L::kColU + L::kStepU * (uint32_t)pb + cu;
+        ld_cols<NU>(ua + (kPieces - 1) * NR, u);
 #pragma unroll
         for (int c = kPieces - 2; c >= 0; --c) {  // U = U_1 + (U_2 + ..) / 16
-          float hi[NH];
-          ld_cols<NH>(ua + c * NR, hi);
+          float hi[NU];
+          ld_cols<NU>(ua + c * NR, hi);
 #pragma unroll
-          for (int r = 0; r < NH; ++r) u[r] = fmaf(u[r], 0.0625f, hi[r]);
+          for (int r = 0; r < NU; ++r) u[r] = fmaf(u[r], 0.0625f, hi[r]);
         }
       }
       const int64_t unit = ((int64_t)pend_b * Hkv + pend_kvh) * RG + pend_rg;
@@ -881,9 +912,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rr = min(R, rows_per_head - pend_rg * R);  // real rows of the unit
       if (nparts == 1) {
 #pragma unroll
-        for (int r = 0; r < NH; ++r) {
-          const int row = c0 + r;
-          if (row >= rr) break;
+        for (int r = 0; r < NU; ++r) {
+          const int row = cu + r;
+          if (row >= rr || !has_u) break;
           // (two factors: the power of two may pass fp32's range)
           const float f = s_lfin[row] == 0.f ? 0.f : fast_exp2(0.5f * s_rfin[row]);
           put_out(pf.ooff[row] + (int64_t)k * p.o_sd, s_lfin[row] == 0.f ? 0.f : u[r] * f * s_inv[row] * f);
@@ -898,9 +929,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // get here folds all of them, in CTA order
         const int64_t slot = (int64_t)blockIdx.x + unit;
 #pragma unroll
-        for (int r = 0; r < NH; ++r) {
-          const int row = c0 + r;
-          if (row >= rr) break;
+        for (int r = 0; r < NU; ++r) {
+          const int row = cu + r;
+          if (row >= rr || !has_u) break;
           st_global_hint(ws_u + ((slot * R + row) * D) + k, u[r], keep);
         }
         if (half == 0 && k < rr) {
@@ -971,7 +1002,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (threadIdx.x == 0) mbar_arrive(&q_empty[pb]);
       return true;
     };
-    // rows' maxima of v over the tile's 128 keys: red[quarter][row]
+    // rows' maxima of v over the tile's keys: red[..][row]
     auto tile_max = [&](const float (&v)[NH]) {
       float t[NH];
 #pragma unroll
@@ -980,13 +1011,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if ((lane & 3) == 0) {
         const int base = scatter_base<NH>(lane);
 #pragma unroll
-        for (int i = 0; i < NH / 8; ++i) red[quarter * NR + c0 + base + i] = t[i];
+        for (int i = 0; i < NH / 8; ++i) red[red_row * NR + c0 + base + i] = t[i];
       }
     };
     auto red_max = [&](int row) {
-      return fmaxf(fmaxf(red[row], red[NR + row]), fmaxf(red[2 * NR + row], red[3 * NR + row]));
+      float m = red[row];
+#pragma unroll
+      for (int w = 1; w < kRed; ++w) m = fmaxf(m, red[w * NR + row]);
+      return m;
     };
-    uint32_t kslot = 0, kphase = 0;  // ring slot of the current K tile and its phase
+    uint32_t kslot = 2 * sub, kphase = 0;  // ring slot of the current K subtile and its phase
     for (int64_t g = 0; cur.t < t1; cur.next(ntab, RG, Hkv, B), ++g) {
       const bool first = cur.t == t0 || cur.j == 0;
       const bool last = cur.t == t1 - 1 || cur.j == cur.n - 1;
@@ -998,21 +1032,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!w) { ok = false; break; }
       }
       const int key0 = cur.key0();
-      const int key = key0 + k;
+      const int sub0 = key0 + sub * BK, key = sub0 + k;
+      const int64_t gs = kSub * g + sub;  // the subtile, of this CTA's
       float x[NH];
       float ks = 0.f, ev = kNegInf;  // the key's scales: 2^ks', 2^ev
-      bool sok = wait_all(&sc_full[g % kScaleRing], (uint32_t)((g / kScaleRing) & 1));
+      bool sok = wait_all(&sc_full[gs % kScaleRing], (uint32_t)((gs / kScaleRing) & 1));
       if (sok) {
-        const float2 sc = s_sc[(g % kScaleRing) * BK + k];
+        const float2 sc = s_sc[(gs % kScaleRing) * BK + k];
         ks = sc.x;
         ev = sc.y;
         sok = wait_all(&empty[kslot], kphase);
       }
       bool trig = !sok;
+      const float f = ev == kNegInf ? 0.f : fast_exp2(ev);  // (2^-127: 0 beside any other)
+      float pr[NH];         // the weights e^z at m's reference
+      uint32_t w2[NH / 2];  // with the values' scales, at r's, pairs of rows as f16
+      auto weigh = [&]() {
+        const float2 f2v = make_float2(f, f), neg = make_float2(-1.f, -1.f);
+#pragma unroll
+        for (int r4 = 0; r4 < NH / 4; ++r4) {
+          const float4 m4 = reinterpret_cast<const float4*>(s_muse + c0)[r4];
+          const float4 h4 = reinterpret_cast<const float4*>(s_h + c0)[r4];
+          const float2 mu[2] = {make_float2(m4.x, m4.y), make_float2(m4.z, m4.w)};
+          const float2 h[2] = {make_float2(h4.x, h4.y), make_float2(h4.z, h4.w)};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 4 * r4 + 2 * e;
+            const float2 z = __ffma2_rn(mu[e], neg, make_float2(x[r], x[r + 1]));
+            const float2 pp = make_float2(fast_exp2(z.x), fast_exp2(z.y));  // masked: 2^-inf = 0
+            pr[r] = pp.x;
+            pr[r + 1] = pp.y;
+            // (p 2^ev <= 2^(r + 1) first: its product with 2^(lift - r) stays in range)
+            const float2 w = __fmul2_rn(__fmul2_rn(pp, f2v), h[e]);
+            const __half2 h2 = __floats2half2_rn(w.x, w.y);
+            w2[r / 2] = *reinterpret_cast<const uint32_t*>(&h2);
+          }
+        }
+      };
       if (sok) {
         tc::fence_after();
         float lo[NH];
-        const uint32_t sa = tl + L::kColS + L::kStepS * (uint32_t)(g & 1) + c0;
+        const uint32_t sa = tl + L::kColS + L::kStepS * (uint32_t)(g & 1) + L::kSubS * sub + c0;
         ld_cols<NH>(sa, x);
         ld_cols<NH>(sa + NR, lo);
 #pragma unroll
@@ -1025,7 +1085,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             x[r] = fmaf(lo[r], 0.03125f, x[r]) * (ks * f[e]);
           }
         }
-        const bool tail = key0 + BK > rf.min_end;
+        const bool tail = sub0 + BK > rf.min_end;
         if (tail) {
 #pragma unroll
           for (int r = 0; r < NH; ++r)
@@ -1035,13 +1095,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int r = 0; r < NH; ++r) x[r] = kNegInf;
         }
-        if (key0 < rf.win_max) {
+        if (sub0 < rf.win_max) {
           // sliding window: keys before a row's first visible key
 #pragma unroll
           for (int r = 0; r < NH; ++r)
             if (key < (int)rf.tree[c0 + r]) x[r] = kNegInf;
         }
-        if (key0 + BK > rf.tree_base) {
+        if (sub0 + BK > rf.tree_base) {
           // token tree: inside it a row sees only the nodes of its mask
           const int node = key - rf.tree_base;
           if (node >= 0 && node < 64) {
@@ -1050,15 +1110,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!((rf.tree[c0 + r] >> node) & 1ull)) x[r] = kNegInf;
           }
         }
+        weigh();
 #pragma unroll
         for (int r4 = 0; r4 < NH / 4; ++r4) {
           const float4 t4 = reinterpret_cast<const float4*>(s_thr + c0)[r4];
-          const float4 m4 = reinterpret_cast<const float4*>(s_muse + c0)[r4];
-          const float4 y4 = reinterpret_cast<const float4*>(s_rthr + c0)[r4];
           trig |= (x[4 * r4] > t4.x) | (x[4 * r4 + 1] > t4.y) | (x[4 * r4 + 2] > t4.z) | (x[4 * r4 + 3] > t4.w);
-          trig |= (x[4 * r4] - m4.x + ev > y4.x) | (x[4 * r4 + 1] - m4.y + ev > y4.y) |
-                  (x[4 * r4 + 2] - m4.z + ev > y4.z) | (x[4 * r4 + 3] - m4.w + ev > y4.w);
         }
+        __half2 top = *reinterpret_cast<const __half2*>(&w2[0]);
+#pragma unroll
+        for (int i = 1; i < NH / 2; ++i) top = __hmax2(top, *reinterpret_cast<const __half2*>(&w2[i]));
+        trig |= __high2float(top) > kMostW || __low2float(top) > kMostW;
       } else if (lane == 0) {
         misc[2] = 1;
       }
@@ -1093,13 +1154,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float ymax = red_max(k), ro = s_r[k];
           float bt = 1.f, rn = ro;
           // (r fell with m: what it may rise to is measured from there)
-          if (ymax > (ro == kNegInf ? kNegInf : ro + kLazyR)) {
+          if (ymax > ro) {
             bt = ro == kNegInf ? 1.f : fast_exp2(ro - ymax);
             rn = ymax;
           }
           // U's reference in absolute terms moved by bt, and not by m's step
           s_r[k] = rn;
-          s_rthr[k] = rn == kNegInf ? kNegInf : rn + kLazyR;
           // 2^(lift - r) as a factor; |r| < 127 + 127 + 8
           s_h[k] = rn == kNegInf ? 1.f : fast_exp2(fminf(fmaxf(kLift - rn, -126.f), 126.f));
           s_beta[k] = bt;
@@ -1116,47 +1176,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!first) {
           // U^T lane k = value dim k, this half's columns of all pieces; the product
           // with P_{j-1} must have completed (U += P_j V_j waits for this tile's P)
-          const int64_t pv_seq = 2 * g - 1;  // V_{j-1}
+          const int64_t pv_seq = 2 * kSub * g - 1;  // V_{j-1}, its last subtile
           const bool done = wait_all(&empty[pv_seq % kSlots], (uint32_t)((pv_seq / kSlots) & 1));
           const bool pv = bar_and(kBarRows, kKeyThreads, done);
           if (!pv) { ok = false; break; }
           tc::fence_after();
-          const uint32_t ua = tl + L::kColU + L::kStepU * (uint32_t)ub + c0;
+          const uint32_t ua = tl + L::kColU + L::kStepU * (uint32_t)ub + cu;
 #pragma unroll 1
-          for (int part = 0; part < kPieces; ++part) {
-            float u[NH];
-            ld_cols<NH>(ua + NR * part, u);
+          for (int part = 0; has_u && part < kPieces; ++part) {
+            float u[NU];
+            ld_cols<NU>(ua + NR * part, u);
 #pragma unroll
-            for (int r = 0; r < NH; ++r) u[r] *= s_beta[c0 + r];
-            st_cols<NH>(ua + NR * part, u);
+            for (int r = 0; r < NU; ++r) u[r] *= s_beta[cu + r];
+            st_cols<NU>(ua + NR * part, u);
           }
-          resc = true;
+          resc = has_u;
         }
+        weigh();
       }
       // ---- P^T row of key k, this half's rows: the weights' pieces ----
       {
-        unsigned char* ph = sm + L::kOffP + (int)(g & 1) * L::kPBytes + k * 128;
-        const float f = ev == kNegInf ? 0.f : fast_exp2(ev);  // (2^-127: 0 beside any other)
-        uint32_t w2[NH / 2];  // pairs of rows as f16
+        unsigned char* ph = sm + L::kOffP + (int)(g & 1) * L::kPBytes + sub * L::kPSub + k * 128;
 #pragma unroll
-        for (int r4 = 0; r4 < NH / 4; ++r4) {
-          const float4 m4 = reinterpret_cast<const float4*>(s_muse + c0)[r4];
-          const float4 h4 = reinterpret_cast<const float4*>(s_h + c0)[r4];
-          const float mu[4] = {m4.x, m4.y, m4.z, m4.w}, h[4] = {h4.x, h4.y, h4.z, h4.w};
-          float w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = 4 * r4 + e;
-            const float pr = fast_exp2(x[r] - mu[e]);  // masked: 2^-inf = 0
-            lp[r] += pr;
-            w[e] = pr * fminf(f * h[e], 0x1p126f);
-          }
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const __half2 h2 = __floats2half2_rn(w[2 * e], w[2 * e + 1]);
-            w2[2 * r4 + e] = *reinterpret_cast<const uint32_t*>(&h2);
-          }
-        }
+        for (int r = 0; r < NH; ++r) lp[r] += pr[r];
         const __half2 sixteen = __float2half2_rn(16.f);
 #pragma unroll
         for (int c = 0; c < kPieces; ++c) {
@@ -1188,10 +1230,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if ((cur.j == cur.n - 1 && key0 + BK > rf.unit_end) || key0 < rf.unit_start || key0 + BK > rf.tree_base) {
+      if ((cur.j == cur.n - 1 && key0 + TK > rf.unit_end) || key0 < rf.unit_start || key0 + TK > rf.tree_base) {
         // zero the V rows that no row sees: past every visible key, before a
-        // window, tree nodes that no row lists (each half of the warps half a row)
-        const int64_t sv = 2 * g + 1;
+        // window, tree nodes that no row lists (each half of the warps its subtile, or half a row)
+        const int64_t sv = 2 * gs + 1;
         const bool vok = bar_and(kBarRows, kKeyThreads, wait_all(&full[sv % kSlots], (uint32_t)((sv / kSlots) & 1)));
         if (!vok) { ok = false; break; }
         const int node = key - rf.tree_base;
@@ -1200,8 +1242,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (unseen) {
           unsigned char* vr = sm + (int)(sv % kSlots) * kSlotBytes + k * 128;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            *reinterpret_cast<uint4*>(vr + (((4 * half + c) ^ (k & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < 4 * kSub; ++c)
+            *reinterpret_cast<uint4*>(vr + ((((kSub == 1 ? 4 * half : 0) + c) ^ (k & 7)) << 4)) = make_uint4(0, 0, 0, 0);
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // P^T, V rows -> tensor core
@@ -1209,7 +1251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[g & 1]);
-      kslot += 2;
+      kslot += 2 * kSub;
       if (kslot >= (uint32_t)kSlots) {
         kslot -= (uint32_t)kSlots;
         kphase ^= 1u;
@@ -1227,13 +1269,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if ((lane & 3) == 0) {
           const int base = scatter_base<NH>(lane);
 #pragma unroll
-          for (int i = 0; i < NH / 8; ++i) red[quarter * NR + c0 + base + i] = lp[i];
+          for (int i = 0; i < NH / 8; ++i) red[red_row * NR + c0 + base + i] = lp[i];
         }
 #pragma unroll
         for (int r = 0; r < NH; ++r) lp[r] = 0.f;
         bar_sync(kBarRows, kKeyThreads);
         if (half == 0 && k < NR) {
-          const float l = (red[k] + red[NR + k]) + (red[2 * NR + k] + red[3 * NR + k]);
+          float l = red[k];
+#pragma unroll
+          for (int w = 1; w < kRed; ++w) l += red[w * NR + k];
           // (a NaN among a row's scores, which no maximum shows, is in the sum)
           s_mfin[k] = s_m[k];
           s_lfin[k] = l;
@@ -1242,7 +1286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // fresh statistics for the next unit
           s_m[k] = kNegInf;
           s_muse[k] = 0.f;
-          s_thr[k] = s_r[k] = s_rthr[k] = kNegInf;
+          s_thr[k] = s_r[k] = kNegInf;
           s_h[k] = 1.f;
         }
         bar_sync(kBarRows, kKeyThreads);
@@ -1285,7 +1329,7 @@ Q8Plan plan_decode_tc_q8(int64_t B, int64_t Hkv, int64_t rows, int64_t Tmax, int
   pl.rows_cta = (int)((rows + pl.row_groups - 1) / pl.row_groups);
   pl.ctas = sms < 255 ? sms : 255;
   pl.units = B * Hkv * pl.row_groups;
-  pl.tiles = pl.units * ((Tmax + 127) / 128 + 2);  // + the per-unit weight
+  pl.tiles = pl.units * ((Tmax + 127) / 128 + 2);  // + the per-unit weight; at most
   pl.ws_bytes = (size_t)((pl.ctas + pl.units) * pl.rows_cta * (3 + D) + 4) * sizeof(float);
   return pl;
 }
@@ -1297,6 +1341,7 @@ bool decode_tc_q8_takes(const Q8Plan& pl, int64_t B, int64_t Tmax) {
 
 cudaError_t launch_decode_tc_q8(const Q8Params& p, int ctas, const CUtensorMap& tmk, const CUtensorMap& tmv,
                                 cudaStream_t stream) {
+  if (p.rows_cta <= 8) return launch<8>(p, ctas, tmk, tmv, stream);
   if (p.rows_cta <= 16) return launch<16>(p, ctas, tmk, tmv, stream);
   if (p.rows_cta <= 32) return launch<32>(p, ctas, tmk, tmv, stream);
   return launch<48>(p, ctas, tmk, tmv, stream);

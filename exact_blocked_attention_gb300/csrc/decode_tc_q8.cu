@@ -21,7 +21,7 @@
 //
 // Otherwise the kernel is the one of decode_tc.cu over pages: the same cut of
 // all units' tiles into equal ranges, one a CTA, the same roles, order of
-// products, ring and waits; the K producer also brings each key's scales.
+// products, ring and waits; the unit loader also brings each key's scales.
 //
 // Every wait is bounded (%globaltimer); on a timeout the CTA records the error
 // word, stops issuing work, lets its own copies and products drain and frees
@@ -106,11 +106,7 @@ struct TcLayout {
   static constexpr int kPBytes = kSub * kPSub;               // one P^T buffer
   static constexpr int kQBytes = 2 * NR * 128;               // q_hi rows, then q_lo rows
   static constexpr int kSlots = NR > 32 ? 7 : (NR > 16 ? 10 : 8);
-  // Subtiles whose scales lie in shared memory.  The K producer writes those of
-  // subtile e once the slot of K_e is free: S of subtile e - 5 (U of e - 4 with 7
-  // slots) has completed, so P of the tile two before that one's was written and
-  // the key threads are done with it and with subtile e - 7 (kSub = 2: e - 10).
-  static constexpr int kScaleRing = kSub == 2 ? 16 : 8;
+  static constexpr int kScaleRing = 8 * kSub;                // subtiles whose scales lie in shared memory
   static constexpr uint32_t kColS = 0;                       // S^T: tiles of even / odd index, their subtiles
   static constexpr uint32_t kSubS = 2 * NR;
   static constexpr uint32_t kStepS = kSub * kSubS;
@@ -125,14 +121,14 @@ struct TcLayout {
   // float [NR] each: m, m_use, thr, r, (unused), 2^(lift - r), alpha of l, alpha of U of the
   // current unit; m, l, r, 1 / l of the finished unit whose U readout is pending
   static constexpr int kOffStat = kOffRed + 8 * NR * 4;
-  static constexpr int kOffScale = kOffStat + 12 * NR * 4;       // float2 [kScaleRing][BK]: 2^ek, ev (-inf: no key)
-  static constexpr int kOffBar = kOffScale + kScaleRing * BK * 8;
-  // full[kSlots], empty[kSlots], q_full[2], q_empty[2], p_full[2], u_full[2], drain, sc_full[kScaleRing]
-  static constexpr int kNumBars = 2 * kSlots + 2 + 2 + 2 + 2 + 1 + kScaleRing;
+  static constexpr int kOffScale = kOffStat + 12 * NR * 4;       // uint32 [kScaleRing][BK]: each key's scale bytes
+  static constexpr int kOffBar = kOffScale + kScaleRing * BK * 4;
+  // full[kSlots], empty[kSlots], q_full[2], q_empty[2], p_full[2], u_full[2], drain, sc_full[kScaleRing], sc_empty[kScaleRing]
+  static constexpr int kNumBars = 2 * kSlots + 2 + 2 + 2 + 2 + 1 + 2 * kScaleRing;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kBytes = kOffMisc + 128 + 1024;  // + slack to align to 1024
   static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0 && kQBytes % 1024 == 0, "swizzle atoms");
-  static_assert(kOffBar % 8 == 0 && kOffStat % 16 == 0 && kOffScale % 8 == 0, "alignment");
+  static_assert(kOffBar % 8 == 0 && kOffStat % 16 == 0 && kOffScale % 16 == 0, "alignment");
   static_assert(kColU + 2 * kStepU <= kTmemCols, "tensor memory");
   static_assert(kBytes <= 232448, "shared memory per block");
 };
@@ -279,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* s_lfin = s_m + 9 * NR;
   float* s_rfin = s_m + 10 * NR;
   float* s_inv = s_m + 11 * NR;
-  float2* s_sc = reinterpret_cast<float2*>(sm + L::kOffScale);
+  uint32_t* s_sc = reinterpret_cast<uint32_t*>(sm + L::kOffScale);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kOffBar);
   uint64_t* full = bars;
   uint64_t* empty = full + kSlots;
@@ -289,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* u_full = p_full + 2;      // [2] by unit parity
   uint64_t* drain = u_full + 2;
   uint64_t* sc_full = drain + 1;            // [kScaleRing]
+  uint64_t* sc_empty = sc_full + kScaleRing;
   // misc: [0] tmem base, [1] error seen by the producer / MMA thread,
   // [2] abort of the key threads, [3] "this CTA folds the unit" (both
   // written before a barrier of the key threads, read after it)
@@ -355,7 +352,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&u_full[x], 1);
       }
       for (int x = 0; x < 2; ++x) mbar_init(&p_full[x], kKeyWarps);  // one arrival per key warp
-      for (int x = 0; x < kScaleRing; ++x) mbar_init(&sc_full[x], 1);
+      for (int x = 0; x < kScaleRing; ++x) {
+        mbar_init(&sc_full[x], 1);
+        mbar_init(&sc_empty[x], kKeyWarps / kSub);
+      }
       mbar_init(drain, 1);
       fence_barrier_init();
     }
@@ -491,57 +491,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       nx_entry = entry_of(p.pages, c.b, nx_key);
       nx_len = p.seqlens[c.b * p.sl_s];
     };
-    // K's: the scales of lane l's keys 4 l .. 4 l + 3 (of one page).  The table
-    // entries of a tile are on their way three tiles before its scales are handed
-    // over, the scales two.
-    struct Ask {
-      int entry, key, kvh, len;
-      bool live;
-    };
-    struct Bytes {  // (apart, so that nothing waits for them before they are stored)
-      int k[4], v[4];
-      uint32_t valid;  // bit i: key 4 l + i
-    };
-    Cursor at = cur;
-    int at_sub = 0;
-    bool more = kv == 0 && at.t < t1;
-    auto ask = [&]() {
-      Ask a{-1, 0, 0, 0, more};
-      if (more) {
-        a.key = at.key0() + at_sub * BK + 4 * lane;
-        a.entry = entry_of(p.pages, at.b, a.key);
-        a.len = p.seqlens[at.b * p.sl_s];
-        a.kvh = at.kvh;
-        if (++at_sub == kSub) {
-          at_sub = 0;
-          at.next(ntab, RG, Hkv, B);
-          more = at.t < t1;
-        }
-      }
-      return a;
-    };
-    auto fetch = [&](const Ask& a) {
-      Bytes y{{}, {}, 0};
-      if (a.live && (unsigned)a.entry < (unsigned)p.pages.n_pages) {
-        const int row = a.key & (p.pages.rows - 1);
-        const unsigned char* ks = p.k_sc + (int64_t)a.entry * p.ke_sn + a.kvh * p.ke_sh;
-        const unsigned char* vs = p.v_sc + (int64_t)a.entry * p.ve_sn + a.kvh * p.ve_sh;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int blk = (row + i) >> p.scale_shift;
-          y.k[i] = ks[blk * p.ke_si];
-          y.v[i] = vs[blk * p.ve_si];
-          if (a.key + i < a.len) y.valid |= 1u << i;
-        }
-      }
-      return y;
-    };
     int64_t issued = 0;  // entries
     bool ok = true;
     int sub = 0;
     if (cur.t < t1) look_up(cur, 0);
-    Ask a0 = ask(), a1 = ask(), a2 = ask();
-    Bytes y0{{}, {}, 0}, y1{{}, {}, 0};
     for (int64_t g = 0; ok && cur.t < t1; ++g) {
       const int row = nx_key & (p.pages.rows - 1);
       const int kvh = cur.kvh;
@@ -565,28 +518,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (copies)
         tma_load_4d(sm + s * kSlotBytes + ((piece << box_shift) * 128), map, 0, row, kvh, page, &full[s], pol);
       issued = seq + 1;
-      if (kv == 0) {
-        if (g == 0) {
-          y0 = fetch(a0);
-          y1 = fetch(a1);
-        }
-        const Ask a3 = ask();
-        const Bytes y2 = fetch(a2);
-        const int sr = (int)(g % kScaleRing);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int ek = y0.k[i], ev = y0.v[i];
-          float2 f = make_float2(0.f, kNegInf);
-          if ((y0.valid >> i) & 1)
-            f = make_float2(scale_of(ek), ev == 255 ? __uint_as_float(0x7fc00000u) : (float)(ev - 127));
-          s_sc[sr * BK + 4 * lane + i] = f;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sc_full[sr]);
-        a2 = a3;
-        y0 = y1;
-        y1 = y2;
-      }
       // after the first tile, let the first unit's query rows land before the
       // stream fills the memory queues (they gate the first product)
       if (g == 0) {
@@ -608,9 +539,85 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == kLoadWarp) {
-    // ---------------- unit loader: query rows and row facts ----------------
+    // ---------------- loader: query rows and row facts of each unit, scales of each tile ----------------
     int uidx = 0;
     bool ok = true;
+    // The scales of lane l's keys 4 l .. 4 l + 3 (of one page), as bytes: a word a
+    // key, ek | ev << 8 | 1 << 16 (0: no key).  The table entry of a subtile is on
+    // its way three subtiles before the bytes are handed over, the bytes two.
+    struct Ask {
+      int entry, key, kvh, len;
+      bool live;
+    };
+    struct Bytes {  // (apart, so that nothing waits for them before they are stored)
+      int k[4], v[4];
+      int n;  // keys that exist
+    };
+    Cursor at = cur;
+    int at_sub = 0;
+    bool more = at.t < t1;
+    const bool fine = p.scale_shift < 2;  // else one scale for the four
+    auto ask = [&]() {
+      Ask a{-1, 0, 0, 0, more};
+      if (more) {
+        a.key = at.key0() + at_sub * BK + 4 * lane;
+        a.entry = entry_of(p.pages, at.b, a.key);
+        a.len = p.seqlens[at.b * p.sl_s];
+        a.kvh = at.kvh;
+        if (++at_sub == kSub) {
+          at_sub = 0;
+          at.next(ntab, RG, Hkv, B);
+          more = at.t < t1;
+        }
+      }
+      return a;
+    };
+    auto fetch = [&](const Ask& a) {
+      Bytes y{{}, {}, 0};
+      if (a.live && (unsigned)a.entry < (unsigned)p.pages.n_pages) {
+        const int row = a.key & (p.pages.rows - 1);
+        const unsigned char* ks = p.k_sc + (int64_t)a.entry * p.ke_sn + a.kvh * p.ke_sh;
+        const unsigned char* vs = p.v_sc + (int64_t)a.entry * p.ve_sn + a.kvh * p.ve_sh;
+        y.n = a.len - a.key;
+        y.k[0] = ks[(row >> p.scale_shift) * p.ke_si];
+        y.v[0] = vs[(row >> p.scale_shift) * p.ve_si];
+        if (fine) {
+#pragma unroll
+          for (int i = 1; i < 4; ++i) {
+            const int blk = (row + i) >> p.scale_shift;
+            y.k[i] = ks[blk * p.ke_si];
+            y.v[i] = vs[blk * p.ve_si];
+          }
+        }
+      }
+      return y;
+    };
+    Ask a1 = ask(), a2 = ask(), a3 = ask();
+    Bytes y0 = fetch(a1), y1 = fetch(a2);
+    a2 = a3;  // (the one to fetch next)
+    int64_t gs = 0;  // subtiles handed over
+    auto hand_over = [&]() -> bool {
+      const Ask ahead = ask();
+      const Bytes y2 = fetch(a2);
+      const int sr = (int)(gs % kScaleRing);
+      bool w = true;
+      if (lane == 0 && gs >= kScaleRing) w = mbar_wait(&sc_empty[sr], (uint32_t)((gs / kScaleRing - 1) & 1));
+      if (!__shfl_sync(0xffffffffu, w, 0)) return false;
+      uint32_t word[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int ek = fine ? y0.k[i] : y0.k[0], ev = fine ? y0.v[i] : y0.v[0];
+        word[i] = i < y0.n ? (uint32_t)(ek | ev << 8 | 1 << 16) : 0u;
+      }
+      reinterpret_cast<uint4*>(s_sc + sr * BK)[lane] = make_uint4(word[0], word[1], word[2], word[3]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sc_full[sr]);
+      a2 = ahead;
+      y0 = y1;
+      y1 = y2;
+      ++gs;
+      return true;
+    };
     for (; t0 < t1 && cur.su < t1; cur.step_unit(ntab, RG, Hkv, B), ++uidx) {
       const int qb = uidx & 1;
       if (uidx >= 2) {
@@ -736,6 +743,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // Q rows -> tensor core
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[qb]);
+      const int64_t here = min((int64_t)(cur.n - cur.j), t1 - cur.t) * kSub;  // the unit's subtiles of this CTA
+      for (int64_t i = 0; ok && i < here; ++i) ok = hand_over();
+      if (!ok) break;
     }
     if (!ok && lane == 0) {
       record_error(p.err, kErrTimeout);
@@ -875,12 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* ws_l = ws_m + slots * R;
     float* ws_r = ws_l + slots * R;
     float* ws_u = ws_m + (3 * slots * R + 3) / 4 * 4;
-    auto put_out = [&](int64_t at, float o) {
-      if (p.out_bf16)
-        static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(o);
-      else
-        static_cast<float*>(p.out)[at] = o;
-    };
+    auto put_out = [&](int64_t at, float o) { static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(o); };
     // A finished unit's U is read one tile later, after the next tile's P: by then
     // its last product has completed and the readout does not stall the pipeline.
     // Its statistics wait in s_mfin, .., its row facts stay in their buffer until
@@ -1038,9 +1043,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       float ks = 0.f, ev = kNegInf;  // the key's scales: 2^ks', 2^ev
       bool sok = wait_all(&sc_full[gs % kScaleRing], (uint32_t)((gs / kScaleRing) & 1));
       if (sok) {
-        const float2 sc = s_sc[(gs % kScaleRing) * BK + k];
-        ks = sc.x;
-        ev = sc.y;
+        const uint32_t sc = s_sc[(gs % kScaleRing) * BK + k];
+        if (sc != 0) {
+          const int e = (sc >> 8) & 255;
+          ks = scale_of(sc & 255);
+          ev = e == 255 ? __uint_as_float(0x7fc00000u) : (float)(e - 127);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sc_empty[gs % kScaleRing]);
         sok = wait_all(&empty[kslot], kphase);
       }
       bool trig = !sok;
@@ -1085,32 +1095,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             x[r] = fmaf(lo[r], 0.03125f, x[r]) * (ks * f[e]);
           }
         }
-        const bool tail = sub0 + BK > rf.min_end;
-        if (tail) {
-#pragma unroll
-          for (int r = 0; r < NH; ++r)
-            if (key >= rf.end[c0 + r]) x[r] = kNegInf;
-        }
-        if (ev == kNegInf) {  // no page
-#pragma unroll
-          for (int r = 0; r < NH; ++r) x[r] = kNegInf;
-        }
-        if (sub0 < rf.win_max) {
-          // sliding window: keys before a row's first visible key
-#pragma unroll
-          for (int r = 0; r < NH; ++r)
-            if (key < (int)rf.tree[c0 + r]) x[r] = kNegInf;
-        }
-        if (sub0 + BK > rf.tree_base) {
-          // token tree: inside it a row sees only the nodes of its mask
+        // (every row sees every key of the subtile: no mask)
+        if (sub0 + BK > rf.min_end || sub0 < rf.win_max || sub0 + BK > rf.tree_base || ev == kNegInf) {
+          // row ends, windows, trees, keys without a page
           const int node = key - rf.tree_base;
-          if (node >= 0 && node < 64) {
+          const bool in_tree = rf.tree_base != 0x7fffffff && node >= 0 && node < 64;
+          const bool window = p.window > 0;
+          const int last_key = ev == kNegInf ? 0x7fffffff : key;
 #pragma unroll
-            for (int r = 0; r < NH; ++r)
-              if (!((rf.tree[c0 + r] >> node) & 1ull)) x[r] = kNegInf;
+          for (int r = 0; r < NH; ++r) {
+            const uint64_t t = rf.tree[c0 + r];
+            if (last_key >= rf.end[c0 + r] || (window && key < (int)t) || (in_tree && !((t >> node) & 1ull))) x[r] = kNegInf;
           }
         }
+      } else if (lane == 0) {
+        misc[2] = 1;
+      }
+      bool resc = false;
+      for (bool again = false;; again = true) {
         weigh();
+        if (again) break;
 #pragma unroll
         for (int r4 = 0; r4 < NH / 4; ++r4) {
           const float4 t4 = reinterpret_cast<const float4*>(s_thr + c0)[r4];
@@ -1120,12 +1124,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 1; i < NH / 2; ++i) top = __hmax2(top, *reinterpret_cast<const __half2*>(&w2[i]));
         trig |= __high2float(top) > kMostW || __low2float(top) > kMostW;
-      } else if (lane == 0) {
-        misc[2] = 1;
-      }
-      bool resc = false;
-      if (bar_or(kBarRows, kKeyThreads, trig)) {
-        if (misc[2] != 0) { ok = false; break; }  // read after the barrier: same answer everywhere
+        if (!bar_or(kBarRows, kKeyThreads, trig)) break;
+        if (misc[2] != 0) { ok = false; break; }  // read after the barrier: same answer everywhere (both loops end)
         // ---- raise the references: m, then r at the new m ----
         tile_max(x);
         bar_sync(kBarRows, kKeyThreads);
@@ -1179,7 +1179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int64_t pv_seq = 2 * kSub * g - 1;  // V_{j-1}, its last subtile
           const bool done = wait_all(&empty[pv_seq % kSlots], (uint32_t)((pv_seq / kSlots) & 1));
           const bool pv = bar_and(kBarRows, kKeyThreads, done);
-          if (!pv) { ok = false; break; }
+          if (!pv) { ok = false; break; }  // (both loops)
           tc::fence_after();
           const uint32_t ua = tl + L::kColU + L::kStepU * (uint32_t)ub + cu;
 #pragma unroll 1
@@ -1192,8 +1192,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           resc = has_u;
         }
-        weigh();
       }
+      if (!ok) break;
       // ---- P^T row of key k, this half's rows: the weights' pieces ----
       {
         unsigned char* ph = sm + L::kOffP + (int)(g & 1) * L::kPBytes + sub * L::kPSub + k * 128;

@@ -12,12 +12,11 @@
 // q: a row scaled by a power of two to 2^7 <= max |q| < 2^8; q_hi its nearest
 // e4m3 (4 bits) and q_lo = 32 (q - q_hi) the rest of a bf16's 8 bits, exact but
 // for dims below 2^-14 of the row's largest (off by at most 2^-22 of it).
-// p: a weight as f16 (11 bits), taken apart into 3 pieces (more than 32 rows)
-// or 4: all of an f16 down to 2^-9 of the largest weight (with 4: 2^-13),
-// below that to a step of 2^-25 (2^-29) of it.
+// p: a weight as f16 (11 bits), taken apart into 4 pieces: all of an f16 down to
+// 2^-14 of the largest weight, below that to a step of 2^-25 of it (or finer).
 // With k = 2^ek k8 and v = 2^ev v8: x = (S_hi + S_lo / 32) 2^ek fac_row, and the
 // weight is 2^(x - m + ev - r), of two references a row: m >= max x - 8, and r
-// >= max (x - m + ev) - 1 (r relative to m: beside a large x, ev would be lost).
+// >= max (x - m + ev) - 4 (r relative to m: beside a large x, ev would be lost).
 //
 // Otherwise the kernel is the one of decode_tc.cu over pages: the same cut of
 // all units' tiles into equal ranges, one a CTA, the same roles, order of
@@ -40,19 +39,15 @@ namespace {
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLazyM = 8.f;
-constexpr float kLift = 7.f;          // a weight at the reference; kMostW before the reference rises, of e4m3's 448
+// The reference leaves room for a maximum 2^4 above it: raising it takes a tile
+// 1.5 us, and with room for 2^1 some of 40 rows did so in nearly every tile
+// (five-row chains of 64 heads 247 us, SLACKUS with this).
+constexpr float kLift = 4.f;          // a weight at the reference; kMostW before the reference rises, of e4m3's 448
 constexpr float kMostW = 256.f;
 
 constexpr int D = 128;
 constexpr int BK = 128;               // keys of a product (TMEM lanes of S^T)
 constexpr int kSlotBytes = BK * D;    // a ring slot, K or V: 128 rows of 128 bytes
-constexpr int kKeyWarps = 8;          // two warps per TMEM lane quarter
-constexpr int kKeyThreads = 32 * kKeyWarps;
-constexpr int kPageKWarp = 8;
-constexpr int kMmaWarp = 9;
-constexpr int kLoadWarp = 10;
-constexpr int kPageVWarp = 11;
-constexpr int kThreads = 32 * 12;
 constexpr int kBarRows = 1;           // named barrier of the key threads
 constexpr uint32_t kTmemCols = 512;
 
@@ -95,12 +90,17 @@ struct RowFacts {
 
 template <int NR>
 struct TcLayout {
-  // Up to 16 rows a tile is 256 keys, two subtiles, one for each half of the key
-  // threads: what a tile takes is a chain of waits, loads and a vote, some 1.4 us
-  // whatever its size.  More rows: 128 keys, half of the rows for each half.
+  // Up to 16 rows a tile is 256 keys, two subtiles, each with key threads of its
+  // own: what a tile takes is a chain of waits, loads and a vote, some 1.4 us
+  // whatever its size.  More rows: 128 keys.
+  // (12 key warps of 16 rows each for 48, not 8 of 24: MOREUS in place of 240 us
+  // for five-row chains of 64 heads)
   static constexpr int kSub = NR <= 16 ? 2 : 1;
+  static constexpr int kParts = NR == 8 ? 1 : (NR == 16 ? 2 : (NR == 32 ? 4 : 3));
+  static constexpr int kKeyWarps = 4 * kSub * kParts;        // a warp a TMEM lane quarter, subtile and part of the rows
+  static constexpr int kThreads = 32 * (kKeyWarps + 4);
   static constexpr int kTileKeys = kSub * BK;
-  static constexpr int kPieces = NR > 32 ? 3 : 4;
+  static constexpr int kPieces = 4;
   static constexpr int kPN = kPieces * NR;                   // N of the value product
   static constexpr int kPSub = (kPN > 128 ? 2 : 1) * BK * 128;  // P^T of a subtile: atoms of 128 columns
   static constexpr int kPBytes = kSub * kPSub;               // one P^T buffer
@@ -110,8 +110,11 @@ struct TcLayout {
   static constexpr uint32_t kColS = 0;                       // S^T: tiles of even / odd index, their subtiles
   static constexpr uint32_t kSubS = 2 * NR;
   static constexpr uint32_t kStepS = kSub * kSubS;
-  static constexpr uint32_t kColU = 2 * kStepS;              // U^T: units of even / odd index
-  static constexpr uint32_t kStepU = kPN;
+  // U^T of units of even / odd index; more than 32 rows: one, read out before the
+  // next unit's first P is written
+  static constexpr int kBufU = NR > 32 ? 1 : 2;
+  static constexpr uint32_t kColU = 2 * kStepS;
+  static constexpr uint32_t kStepU = kBufU == 2 ? kPN : 0;
   static constexpr int kOffQ = kSlots * kSlotBytes;              // two query buffers
   static constexpr int kOffP = kOffQ + 2 * kQBytes;              // two P^T buffers
   static constexpr int kOffRows = kOffP + 2 * kPBytes;           // RowFacts[2]
@@ -129,7 +132,7 @@ struct TcLayout {
   static constexpr int kBytes = kOffMisc + 128 + 1024;  // + slack to align to 1024
   static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0 && kQBytes % 1024 == 0, "swizzle atoms");
   static_assert(kOffBar % 8 == 0 && kOffStat % 16 == 0 && kOffScale % 16 == 0, "alignment");
-  static_assert(kColU + 2 * kStepU <= kTmemCols, "tensor memory");
+  static_assert(kColU + kBufU * kPN <= kTmemCols, "tensor memory");
   static_assert(kBytes <= 232448, "shared memory per block");
 };
 
@@ -247,7 +250,7 @@ __device__ __forceinline__ int scatter_base(int lane) {
 }
 
 template <int NR>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
     decode_tc_q8_kernel(const __grid_constant__ Q8Params p, const __grid_constant__ CUtensorMap tmk,
                         const __grid_constant__ CUtensorMap tmv) {
   using L = TcLayout<NR>;
@@ -255,6 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kIdescPV = idesc_e4m3(128, L::kPN, 1, 1);   // V^T, P^T both MN-major
   constexpr int kSlots = L::kSlots, kSub = L::kSub, TK = L::kTileKeys, kScaleRing = L::kScaleRing;
   constexpr int kPieces = L::kPieces;
+  constexpr int kKeyWarps = L::kKeyWarps, kKeyThreads = 32 * kKeyWarps, kThreads = L::kThreads;
+  constexpr int kPageKWarp = kKeyWarps, kMmaWarp = kKeyWarps + 1, kLoadWarp = kKeyWarps + 2, kPageVWarp = kKeyWarps + 3;
   // weight-only tiles per unit in the partition (its set-up and readout)
   constexpr int kUnitExtra = NR >= 48 ? 2 : 0;
 
@@ -649,45 +654,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       // query rows: 4 dims a lane, 8 rows in flight; each scaled by a power of two,
       // taken apart into q_hi and q_lo and written in the 128-byte swizzled
       // K-major layout (rows past the unit's end are zeros)
+      // (a loop: unrolled over 48 rows its code alone took 50 us of the first unit)
       float fac[2] = {0.f, 0.f};
-#pragma unroll
+#pragma unroll 1
       for (int r0 = 0; r0 < NR; r0 += 8) {
         uint2 w[8];
+        const bool high = r0 >= 32;
+        const uintptr_t base = reinterpret_cast<uintptr_t>(high ? qrow[1] : qrow[0]);
+        const unsigned live = __ballot_sync(0xffffffffu, high ? real[1] : real[0]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int r = r0 + i, set = r >> 5;
-          const uint2* src = reinterpret_cast<const uint2*>(
-              __shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(qrow[set]), r & 31));
-          const bool rr = __shfl_sync(0xffffffffu, real[set], r & 31);
-          w[i] = rr ? __ldg(src + lane) : make_uint2(0, 0);
+          const uint2* src = reinterpret_cast<const uint2*>(__shfl_sync(0xffffffffu, base, (r0 + i) & 31));
+          w[i] = (live >> ((r0 + i) & 31)) & 1 ? __ldg(src + lane) : make_uint2(0, 0);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int r = r0 + i;
-          const float q[4] = {bf16lo(w[i].x), bf16hi(w[i].x), bf16lo(w[i].y), bf16hi(w[i].y)};
           // (the largest of bit patterns: a NaN is the largest)
-          uint32_t top = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(q[e]) & 0x7fffffffu);
-          top = __reduce_max_sync(0xffffffffu, top);
-          const int e = top == 0 ? 7 : (int)(top >> 23) - 127;
-          // (two factors: 7 - e may pass 127; infinities and NaN become NaN)
-          const float f1 = pow2((7 - e) / 2), f2 = pow2((7 - e) - (7 - e) / 2);
-          uint32_t hi = 0, lo = 0;
+          const uint32_t a0 = w[i].x & 0x7fff7fffu, a1 = w[i].y & 0x7fff7fffu;
+          const uint32_t top = __reduce_max_sync(
+              0xffffffffu, max(max(a0 & 0xffffu, a0 >> 16), max(a1 & 0xffffu, a1 >> 16)));
+          const int e = top == 0 ? 0 : min(7 + 127 - (int)(top >> 7), 127);  // rows times 2^e
+          // (infinities and NaN make the whole row NaN)
+          const float f = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2(e);
+          uint32_t hi[2], lo[2];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const bool bad = top >= 0x7f800000u;
-            const float x0 = bad ? __uint_as_float(0x7fc00000u) : q[2 * c] * f1 * f2;
-            const float x1 = bad ? __uint_as_float(0x7fc00000u) : q[2 * c + 1] * f1 * f2;
-            const uint32_t h = to_e4m3x2(x0, x1);
-            const float2 hf = e4m3x2_to_f2(h);
-            hi |= h << (16 * c);
-            lo |= to_e4m3x2((x0 - hf.x) * 32.f, (x1 - hf.y) * 32.f) << (16 * c);
+            const uint32_t x = c ? w[i].y : w[i].x;
+            const __half2 h = __floats2half2_rn(bf16lo(x) * f, bf16hi(x) * f);
+            hi[c] = h2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&h));
+            const uint32_t back = e4m3x2_to_h2(hi[c]);
+            const __half2 rest = __hmul2(__hsub2(h, *reinterpret_cast<const __half2*>(&back)), __float2half2_rn(32.f));
+            lo[c] = h2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&rest));
           }
           const int at = r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
-          *reinterpret_cast<uint32_t*>(qs + at) = hi;
-          *reinterpret_cast<uint32_t*>(qs + NR * 128 + at) = lo;
-          if (lane == (r & 31)) fac[r >> 5] = p.scale_log2 * pow2(e - 7);
+          *reinterpret_cast<uint32_t*>(qs + at) = hi[0] | hi[1] << 16;
+          *reinterpret_cast<uint32_t*>(qs + NR * 128 + at) = lo[0] | lo[1] << 16;
+          if (lane == (r & 31)) {
+            if (high) fac[1] = p.scale_log2 * pow2(-e);
+            else fac[0] = p.scale_log2 * pow2(-e);
+          }
         }
       }
       // integer facts of the rows
@@ -857,18 +863,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---------------- key threads ----------------
-    // warp w: TMEM lane quarter (w mod 4) and half w / 4: thread = key k of the
-    // tile's subtile `half` with all rows, or key k with the rows of its half; value
-    // dim k in the epilogue, with the rows [cu, cu + NU) (subtiles: half 0 alone)
-    constexpr int NH = NR / (3 - kSub), NU = NR / (3 - kSub);
-    constexpr int kRed = kSub == 2 ? 8 : 4;  // warps that share a row's maximum
+    // warp w: TMEM lane quarter (w mod 4) and group w / 4: thread = key k of the
+    // group's subtile with the group's part of the rows, [c0, c0 + NH); value dim k in
+    // the epilogue, with the same rows (the first subtile's groups)
+    constexpr int NH = NR / L::kParts;
+    constexpr int kRed = 4 * kSub;  // warps that share a row's maximum
     const int quarter = warp & 3;
-    const int half = warp >> 2;
+    const int group = warp >> 2;
     const int k = 32 * quarter + lane;
-    const int sub = kSub == 2 ? half : 0;
-    const int c0 = kSub == 2 ? 0 : half * NH, cu = c0;
-    const bool has_u = kSub == 1 || half == 0;
-    const int red_row = kSub == 2 ? warp : quarter;
+    const int sub = group % kSub, part = group / kSub;
+    const int c0 = part * NH;
+    const bool has_u = sub == 0;
+    const int red_row = quarter + 4 * sub;
     const uint32_t tl = tb + ((uint32_t)(32 * quarter) << 16);
     auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity));
@@ -898,16 +904,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const RowFacts<NR>& pf = facts0[pb];
       if (!bar_and(kBarRows, kKeyThreads, wait_all(&u_full[pb], (uint32_t)((pend_uidx >> 1) & 1)))) return false;
       tc::fence_after();
-      float u[NU];
+      float u[NH];
       if (has_u) {
-        const uint32_t ua = tl + L::kColU + L::kStepU * (uint32_t)pb + cu;
-        ld_cols<NU>(ua + (kPieces - 1) * NR, u);
+        const uint32_t ua = tl + L::kColU + L::kStepU * (uint32_t)pb + c0;
+        ld_cols<NH>(ua + (kPieces - 1) * NR, u);
 #pragma unroll
         for (int c = kPieces - 2; c >= 0; --c) {  // U = U_1 + (U_2 + ..) / 16
-          float hi[NU];
-          ld_cols<NU>(ua + c * NR, hi);
+          float hi[NH];
+          ld_cols<NH>(ua + c * NR, hi);
 #pragma unroll
-          for (int r = 0; r < NU; ++r) u[r] = fmaf(u[r], 0.0625f, hi[r]);
+          for (int r = 0; r < NH; ++r) u[r] = fmaf(u[r], 0.0625f, hi[r]);
         }
       }
       const int64_t unit = ((int64_t)pend_b * Hkv + pend_kvh) * RG + pend_rg;
@@ -917,14 +923,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rr = min(R, rows_per_head - pend_rg * R);  // real rows of the unit
       if (nparts == 1) {
 #pragma unroll
-        for (int r = 0; r < NU; ++r) {
-          const int row = cu + r;
+        for (int r = 0; r < NH; ++r) {
+          const int row = c0 + r;
           if (row >= rr || !has_u) break;
           // (two factors: the power of two may pass fp32's range)
           const float f = s_lfin[row] == 0.f ? 0.f : fast_exp2(0.5f * s_rfin[row]);
           put_out(pf.ooff[row] + (int64_t)k * p.o_sd, s_lfin[row] == 0.f ? 0.f : u[r] * f * s_inv[row] * f);
         }
-        if (half == 0 && k < rr)
+        if (group == 0 && k < rr)
           p.lse[pf.loff[k]] = s_lfin[k] == 0.f ? kNegInf : (s_mfin[k] + __log2f(s_lfin[k])) * kLn2;
       } else {
         // (kept in L2 until the fold reads it: the key stream passing through
@@ -934,12 +940,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // get here folds all of them, in CTA order
         const int64_t slot = (int64_t)blockIdx.x + unit;
 #pragma unroll
-        for (int r = 0; r < NU; ++r) {
-          const int row = cu + r;
+        for (int r = 0; r < NH; ++r) {
+          const int row = c0 + r;
           if (row >= rr || !has_u) break;
           st_global_hint(ws_u + ((slot * R + row) * D) + k, u[r], keep);
         }
-        if (half == 0 && k < rr) {
+        if (group == 0 && k < rr) {
           st_global_hint(ws_m + slot * R + k, s_mfin[k], keep);
           st_global_hint(ws_l + slot * R + k, s_lfin[k], keep);
           st_global_hint(ws_r + slot * R + k, s_rfin[k], keep);
@@ -957,8 +963,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (threadIdx.x == 0) p.cnt[unit] = 0u;  // ready for the next launch
           const int64_t fs = cf + unit;  // the unit's first slot; its parts are consecutive
           // items (row, 4 value dims) over the key threads, the parts in batches of
-          // 8: all loads of a batch in flight
-          constexpr int kBatch = 8;
+          // 4: all loads of a batch in flight
+          constexpr int kBatch = 4;
           for (int item = threadIdx.x; item < rr * (D / 4); item += kKeyThreads) {
             const int row = item / (D / 4), d4 = item % (D / 4);
             float M = kNegInf, Ls = 0.f, Rs = kNegInf;
@@ -1031,6 +1037,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool last = cur.t == t1 - 1 || cur.j == cur.n - 1;
       const int ub = uidx & 1;
       const RowFacts<NR>& rf = facts0[ub];
+      if (L::kBufU == 1 && pend) {
+        if (!flush()) { ok = false; break; }
+        pend = false;
+      }
       if (first) {
         // the row facts come with the query rows
         const bool w = bar_and(kBarRows, kKeyThreads, wait_all(&q_full[ub], (uint32_t)((uidx >> 1) & 1)));
@@ -1129,7 +1139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- raise the references: m, then r at the new m ----
         tile_max(x);
         bar_sync(kBarRows, kKeyThreads);
-        if (half == 0 && k < NR) {
+        if (group == 0 && k < NR) {
           const float tmax = red_max(k);
           const float mo = s_m[k];
           float a = 1.f;
@@ -1150,7 +1160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tile_max(y);
         }
         bar_sync(kBarRows, kKeyThreads);
-        if (half == 0 && k < NR) {
+        if (group == 0 && k < NR) {
           const float ymax = red_max(k), ro = s_r[k];
           float bt = 1.f, rn = ro;
           // (r fell with m: what it may rise to is measured from there)
@@ -1181,14 +1191,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool pv = bar_and(kBarRows, kKeyThreads, done);
           if (!pv) { ok = false; break; }  // (both loops)
           tc::fence_after();
-          const uint32_t ua = tl + L::kColU + L::kStepU * (uint32_t)ub + cu;
+          const uint32_t ua = tl + L::kColU + L::kStepU * (uint32_t)ub + c0;
 #pragma unroll 1
-          for (int part = 0; has_u && part < kPieces; ++part) {
-            float u[NU];
-            ld_cols<NU>(ua + NR * part, u);
+          for (int c = 0; has_u && c < kPieces; ++c) {
+            float u[NH];
+            ld_cols<NH>(ua + NR * c, u);
 #pragma unroll
-            for (int r = 0; r < NU; ++r) u[r] *= s_beta[cu + r];
-            st_cols<NU>(ua + NR * part, u);
+            for (int r = 0; r < NH; ++r) u[r] *= s_beta[c0 + r];
+            st_cols<NH>(ua + NR * c, u);
           }
           resc = has_u;
         }
@@ -1219,7 +1229,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int n0 = c * NR + c0;  // column of the first row
           if constexpr (NH == 16) {
-            *reinterpret_cast<uint4*>(ph + (((n0 >> 4) ^ (k & 7)) << 4)) = make_uint4(by[0], by[1], by[2], by[3]);
+            unsigned char* at = ph + (n0 >= 128 ? BK * 128 : 0) + ((((n0 & 127) >> 4) ^ (k & 7)) << 4);
+            *reinterpret_cast<uint4*>(at) = make_uint4(by[0], by[1], by[2], by[3]);
           } else {
 #pragma unroll
             for (int i = 0; i < NH / 8; ++i) {
@@ -1232,18 +1243,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if ((cur.j == cur.n - 1 && key0 + TK > rf.unit_end) || key0 < rf.unit_start || key0 + TK > rf.tree_base) {
         // zero the V rows that no row sees: past every visible key, before a
-        // window, tree nodes that no row lists (each half of the warps its subtile, or half a row)
+        // window, tree nodes that no row lists (one group of each subtile)
         const int64_t sv = 2 * gs + 1;
         const bool vok = bar_and(kBarRows, kKeyThreads, wait_all(&full[sv % kSlots], (uint32_t)((sv / kSlots) & 1)));
         if (!vok) { ok = false; break; }
         const int node = key - rf.tree_base;
         const bool unseen = key >= rf.unit_end || key < rf.unit_start ||
                             (rf.tree_base != 0x7fffffff && node >= 0 && node < 64 && !((rf.tree_seen >> node) & 1ull));
-        if (unseen) {
+        if (unseen && part == 0) {
           unsigned char* vr = sm + (int)(sv % kSlots) * kSlotBytes + k * 128;
 #pragma unroll
-          for (int c = 0; c < 4 * kSub; ++c)
-            *reinterpret_cast<uint4*>(vr + ((((kSub == 1 ? 4 * half : 0) + c) ^ (k & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vr + (c << 4)) = make_uint4(0, 0, 0, 0);
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // P^T, V rows -> tensor core
@@ -1274,7 +1284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int r = 0; r < NH; ++r) lp[r] = 0.f;
         bar_sync(kBarRows, kKeyThreads);
-        if (half == 0 && k < NR) {
+        if (group == 0 && k < NR) {
           float l = red[k];
 #pragma unroll
           for (int w = 1; w < kRed; ++w) l += red[w * NR + k];
@@ -1317,7 +1327,7 @@ cudaError_t launch(const Q8Params& p, int ctas, const CUtensorMap& tmk, const CU
   if (cudaError_t e = once.set_smem(reinterpret_cast<const void*>(&decode_tc_q8_kernel<NR>), L::kBytes);
       e != cudaSuccess)
     return e;
-  decode_tc_q8_kernel<NR><<<ctas, kThreads, L::kBytes, stream>>>(p, tmk, tmv);
+  decode_tc_q8_kernel<NR><<<ctas, L::kThreads, L::kBytes, stream>>>(p, tmk, tmv);
   return cudaGetLastError();
 }
 

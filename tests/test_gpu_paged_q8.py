@@ -13,9 +13,8 @@ sums over n keys are fp32 (2^-23 a step).  With e = E + 2^-11 (f32: 2^-21)
 n 2^-36 448 max (p 2^ev) / sum p; lse by E + 2^-21 + n 2^-23 and 2^-21 |lse|.
 Heads of 128 with a bf16 out go to the tcgen05 kernel.  Its scores add the rest
 of q below 2^-22 of the row's largest dim, scale 2^-22 max |q| sum |k| each, its
-weights are f16 in e4m3 pieces: 2^-11 and a step of 2^-25 (q rows of a unit <= 32:
-2^-29) of the largest weight times scale, which takes the place of 2^-36 (half a
-step, and up to 2^1 of lazy reference: 2^-25 again).
+weights are f16 in four e4m3 pieces: 2^-11 and half a step of 2^-25 of the largest
+weight times scale, in place of 2^-36 (here 2^-25).
 Prompts that go through the bf16 kernel have its bounds (test_gpu_paged.py):
 2^-8 and 2^-16 in place of 2^-11.  A bf16 store adds 2^-8 of the value.
 """

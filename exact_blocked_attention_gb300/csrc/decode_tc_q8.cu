@@ -13,7 +13,7 @@
 // e4m3 (4 bits) and q_lo = 32 (q - q_hi) the rest of a bf16's 8 bits, exact but
 // for dims below 2^-14 of the row's largest (off by at most 2^-22 of it).
 // p: a weight as f16 (11 bits), taken apart into 4 pieces: all of an f16 down to
-// 2^-14 of the largest weight, below that to a step of 2^-25 of it (or finer).
+// 2^-12 of the largest weight, below that to a step of 2^-23 of it (or finer).
 // With k = 2^ek k8 and v = 2^ev v8: x = (S_hi + S_lo / 32) 2^ek fac_row, and the
 // weight is 2^(x - m + ev - r), of two references a row: m >= max x - 8, and r
 // >= max (x - m + ev) - 4 (r relative to m: beside a large x, ev would be lost).
@@ -39,10 +39,12 @@ namespace {
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLazyM = 8.f;
-// The reference leaves room for a maximum 2^4 above it: raising it takes a tile
-// 1.5 us, and with room for 2^1 some of 40 rows did so in nearly every tile
-// (five-row chains of 64 heads 247 us, SLACKUS with this).
-constexpr float kLift = 4.f;          // a weight at the reference; kMostW before the reference rises, of e4m3's 448
+// A weight at the reference is 2^kLift, and the reference is set 2^kMargin above
+// the largest weight so far: there is room for a maximum 2^6 above it before it
+// has to rise, which takes a tile 1 us and more (with room for 2^4, some of 40
+// rows raised theirs in every second tile where the blocks' scales differ by 2^4:
+// 182 us for five-row chains of 64 heads, MARGINUS so).
+constexpr float kLift = 4.f, kMargin = 2.f;
 constexpr float kMostW = 256.f;
 
 constexpr int D = 128;
@@ -292,8 +294,9 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
   uint64_t* sc_full = drain + 1;            // [kScaleRing]
   uint64_t* sc_empty = sc_full + kScaleRing;
   // misc: [0] tmem base, [1] error seen by the producer / MMA thread,
-  // [2] abort of the key threads, [3] "this CTA folds the unit" (both
-  // written before a barrier of the key threads, read after it)
+  // [2] abort of the key threads, [3] "this CTA folds the unit", [4], [5] "a
+  // row's m rises in this tile", by parity (written before a barrier of the key
+  // threads, read after it)
   int* misc = reinterpret_cast<int*>(sm + L::kOffMisc);
   Start* start = reinterpret_cast<Start*>(sm + L::kOffMisc + 64);
 
@@ -344,7 +347,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
     }
     if (threadIdx.x == 0) {
       misc[1] = 0;
-      misc[2] = 0;
+      misc[2] = misc[4] = misc[5] = 0;
       for (int s = 0; s < kSlots; ++s) {
         mbar_init(&full[s], 1);
         mbar_init(&empty[s], 1);
@@ -1130,6 +1133,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
           const float4 t4 = reinterpret_cast<const float4*>(s_thr + c0)[r4];
           trig |= (x[4 * r4] > t4.x) | (x[4 * r4 + 1] > t4.y) | (x[4 * r4 + 2] > t4.z) | (x[4 * r4 + 3] > t4.w);
         }
+        if (trig) misc[4 + (int)(g & 1)] = 1;  // m has to rise (read after the vote's barrier)
         __half2 top = *reinterpret_cast<const __half2*>(&w2[0]);
 #pragma unroll
         for (int i = 1; i < NH / 2; ++i) top = __hmax2(top, *reinterpret_cast<const __half2*>(&w2[i]));
@@ -1137,22 +1141,26 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
         if (!bar_or(kBarRows, kKeyThreads, trig)) break;
         if (misc[2] != 0) { ok = false; break; }  // read after the barrier: same answer everywhere (both loops end)
         // ---- raise the references: m, then r at the new m ----
-        tile_max(x);
-        bar_sync(kBarRows, kKeyThreads);
-        if (group == 0 && k < NR) {
-          const float tmax = red_max(k);
-          const float mo = s_m[k];
-          float a = 1.f;
-          if (tmax > s_thr[k]) {
-            a = mo == kNegInf ? 1.f : fast_exp2(mo - tmax);  // a row with no key yet has l = u = 0
-            s_r[k] = mo == kNegInf ? kNegInf : s_r[k] + (mo - tmax);
-            s_m[k] = tmax;
-            s_muse[k] = tmax;
-            s_thr[k] = tmax + kLazyM;
+        const bool raise_m = misc[4 + (int)(g & 1)] != 0;
+        if (raise_m) {
+          tile_max(x);
+          bar_sync(kBarRows, kKeyThreads);
+          if (group == 0 && k < NR) {
+            const float tmax = red_max(k);
+            const float mo = s_m[k];
+            float a = 1.f;
+            if (tmax > s_thr[k]) {
+              a = mo == kNegInf ? 1.f : fast_exp2(mo - tmax);  // a row with no key yet has l = u = 0
+              s_r[k] = mo == kNegInf ? kNegInf : s_r[k] + (mo - tmax);
+              s_m[k] = tmax;
+              s_muse[k] = tmax;
+              s_thr[k] = tmax + kLazyM;
+            }
+            s_alpha[k] = a;
           }
-          s_alpha[k] = a;
+          if (threadIdx.x == 0) misc[4 + (int)(g & 1)] = 0;  // (its next use is two tiles on)
+          bar_sync(kBarRows, kKeyThreads);
         }
-        bar_sync(kBarRows, kKeyThreads);
         {
           float y[NH];
 #pragma unroll
@@ -1165,8 +1173,8 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
           float bt = 1.f, rn = ro;
           // (r fell with m: what it may rise to is measured from there)
           if (ymax > ro) {
-            bt = ro == kNegInf ? 1.f : fast_exp2(ro - ymax);
-            rn = ymax;
+            rn = ymax + kMargin;
+            bt = ro == kNegInf ? 1.f : fast_exp2(ro - rn);
           }
           // U's reference in absolute terms moved by bt, and not by m's step
           s_r[k] = rn;
@@ -1175,13 +1183,15 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
           s_beta[k] = bt;
         }
         bar_sync(kBarRows, kKeyThreads);
+        if (raise_m) {
 #pragma unroll
-        for (int r4 = 0; r4 < NH / 4; ++r4) {
-          const float4 a4 = reinterpret_cast<const float4*>(s_alpha + c0)[r4];
-          lp[4 * r4] *= a4.x;
-          lp[4 * r4 + 1] *= a4.y;
-          lp[4 * r4 + 2] *= a4.z;
-          lp[4 * r4 + 3] *= a4.w;
+          for (int r4 = 0; r4 < NH / 4; ++r4) {
+            const float4 a4 = reinterpret_cast<const float4*>(s_alpha + c0)[r4];
+            lp[4 * r4] *= a4.x;
+            lp[4 * r4 + 1] *= a4.y;
+            lp[4 * r4 + 2] *= a4.z;
+            lp[4 * r4 + 3] *= a4.w;
+          }
         }
         if (!first) {
           // U^T lane k = value dim k, this half's columns of all pieces; the product

@@ -13,8 +13,8 @@ sums over n keys are fp32 (2^-23 a step).  With e = E + 2^-11 (f32: 2^-21)
 n 2^-36 448 max (p 2^ev) / sum p; lse by E + 2^-21 + n 2^-23 and 2^-21 |lse|.
 Heads of 128 with a bf16 out go to the tcgen05 kernel.  Its scores add the rest
 of q below 2^-22 of the row's largest dim, scale 2^-22 max |q| sum |k| each, its
-weights are f16 in four e4m3 pieces: 2^-11 and half a step of 2^-25 of the largest
-weight times scale, in place of 2^-36 (here 2^-25).
+weights are f16 in four e4m3 pieces: 2^-11 and half a step of 2^-23 of the largest
+weight times scale, in place of 2^-36 (here 2^-24).
 Prompts that go through the bf16 kernel have its bounds (test_gpu_paged.py):
 2^-8 and 2^-16 in place of 2^-11.  A bf16 store adds 2^-8 of the value.
 """
@@ -89,7 +89,7 @@ def reference(a, out_dtype):
     prompt = Tq >= 64 and a["tree"] is None and a["scale"] > 0 and q.stride(3) == 1 and q.stride(2) % 8 == 0
     wt = 2.0 ** -8 + 2.0 ** -16 if prompt else (2.0 ** -11 if out_dtype == BF16 else 2.0 ** -21)
     pieces = d == 128 and out_dtype == BF16 and not prompt
-    step = 2.0 ** -25 if pieces else 2.0 ** -36
+    step = 2.0 ** -24 if pieces else 2.0 ** -36
     for b in range(B):
         n = max(0, min(int(lens[b]), table.shape[1] * P))
         ent = table[b, : -(-n // P)].long()

@@ -15,8 +15,8 @@
 // p: a weight as f16 (11 bits), taken apart into 4 pieces: all of an f16 down to
 // 2^-12 of the largest weight, below that to a step of 2^-23 of it (or finer).
 // With k = 2^ek k8 and v = 2^ev v8: x = (S_hi + S_lo / 32) 2^ek fac_row, and the
-// weight is 2^(x - m + ev - r), of two references a row: m >= max x - 8, and r
-// >= max (x - m + ev) - 4 (r relative to m: beside a large x, ev would be lost).
+// weight is 2^(x - m + ev - r), of two references a row: m >= max x - 8 for the
+// sum of fp32 weights, and r >= max (x - m + ev) - 4 (r relative to m: beside a large x, ev would be lost).
 //
 // Otherwise the kernel is the one of decode_tc.cu over pages: the same cut of
 // all units' tiles into equal ranges, one a CTA, the same roles, order of
@@ -38,7 +38,9 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
-constexpr float kLazyM = 8.f;
+// m is set 2^16 above the largest score so far (the sum of fp32 weights loses
+// nothing by it) and rises when one passes it by 2^8.
+constexpr float kLazyM = 8.f, kMarginM = 16.f;
 // A weight at the reference is 2^kLift, and the reference is set 2^kMargin above
 // the largest weight so far: there is room for a maximum 2^6 above it before it
 // has to rise, which takes a tile 1 us and more (with room for 2^4, some of 40
@@ -1150,11 +1152,12 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
             const float mo = s_m[k];
             float a = 1.f;
             if (tmax > s_thr[k]) {
-              a = mo == kNegInf ? 1.f : fast_exp2(mo - tmax);  // a row with no key yet has l = u = 0
-              s_r[k] = mo == kNegInf ? kNegInf : s_r[k] + (mo - tmax);
-              s_m[k] = tmax;
-              s_muse[k] = tmax;
-              s_thr[k] = tmax + kLazyM;
+              const float mn = tmax + kMarginM;
+              a = mo == kNegInf ? 1.f : fast_exp2(mo - mn);  // a row with no key yet has l = u = 0
+              s_r[k] = mo == kNegInf ? kNegInf : s_r[k] + (mo - mn);
+              s_m[k] = mn;
+              s_muse[k] = mn;
+              s_thr[k] = mn + kLazyM;
             }
             s_alpha[k] = a;
           }

@@ -100,7 +100,7 @@ struct TcLayout {
   // (12 key warps of 16 rows each for 48, not 8 of 24: MOREUS in place of 240 us
   // for five-row chains of 64 heads)
   static constexpr int kSub = NR <= 16 ? 2 : 1;
-  static constexpr int kParts = NR == 8 ? 1 : (NR == 16 ? 2 : (NR == 32 ? 4 : 3));
+  static constexpr int kParts = NR == 8 ? 1 : (NR == 16 ? 2 : (NR == 32 ? 2 : 3));
   static constexpr int kKeyWarps = 4 * kSub * kParts;        // a warp a TMEM lane quarter, subtile and part of the rows
   static constexpr int kThreads = 32 * (kKeyWarps + 4);
   static constexpr int kTileKeys = kSub * BK;
@@ -1223,14 +1223,16 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
 #pragma unroll
         for (int r = 0; r < NH; ++r) lp[r] += pr[r];
         const __half2 sixteen = __float2half2_rn(16.f);
-#pragma unroll
+        // (a loop, with the last piece's rest for nothing: the code of a tile should stay
+        // in the instruction caches)
+#pragma unroll 1
         for (int c = 0; c < kPieces; ++c) {
           uint32_t by[NH / 4];  // four rows a word
 #pragma unroll
           for (int i = 0; i < NH / 4; ++i) {
             const uint32_t b0 = h2_to_e4m3x2(w2[2 * i]), b1 = h2_to_e4m3x2(w2[2 * i + 1]);
             by[i] = b0 | b1 << 16;
-            if (c + 1 < kPieces) {  // the rest, exact, for the next piece
+            {  // the rest, exact, for the next piece
               const uint32_t v0 = e4m3x2_to_h2(b0), v1 = e4m3x2_to_h2(b1);
               const __half2 r0 = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&w2[2 * i]),
                                                  *reinterpret_cast<const __half2*>(&v0)), sixteen);

@@ -1158,9 +1158,11 @@ int fwd_paged_q8_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages, c
   const int64_t rows = c.Hq / c.Hkv * c.Tq;
   int64_t nb = c.B;
   Q8Plan pl;
-  // tcgen05: heads of 128, bf16 results, contiguous query rows, as many sequences
-  // a launch as the kernel takes
-  bool tc = c.d == 128 && out->dtype == BLKATTN_BF16 && c.q_vec_ok;
+  // tcgen05: heads of 128, bf16 results, contiguous query rows, tables of more than
+  // 256 keys (256: 1 x 32 rows 12 us with mma.sync and 16 with tcgen05, 2 x 5 rows of
+  // 64 heads 18 and 31; 1000: 16 and 18, 43 and 35; 4000 x 32 sequences 90 and 61),
+  // as many sequences a launch as the kernel takes
+  bool tc = c.d == 128 && out->dtype == BLKATTN_BF16 && c.q_vec_ok && c.Tmax > 256;
   if (const char* force = std::getenv("BLKATTN_KERNEL")) tc = tc && std::strcmp(force, "mma") != 0;  // comparison runs only
   if (tc) {
     pl = plan_decode_tc_q8(nb, c.Hkv, rows, c.Tmax, ds->sms);

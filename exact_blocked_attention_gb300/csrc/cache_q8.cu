@@ -170,17 +170,21 @@ __device__ __forceinline__ void row_values(const AppendParams& p, const Lane<D>&
 }
 
 // The angles of `n` rows: (cos, sin) mscale of every pair; pos_of(i) gives row
-// i's position, or a negative one (left out).
+// i's position, or a negative one (left out).  A thread keeps its pair.
 template <typename F>
 __device__ __forceinline__ void fill_angles(const AppendParams& p, float2* cs, int n, F&& pos_of) {
-  const int pairs = p.rot / 2;
-  for (int u = threadIdx.x; u < n * pairs; u += kThreads) {
-    const int i = u / pairs, pair = u - i * pairs;
+  const int pairs = p.rot / 2, step = kThreads / pairs;  // (at most 64 pairs)
+  const int pair = threadIdx.x % pairs;
+  int i = threadIdx.x / pairs;
+  if (i >= step) return;
+  const int64_t phase = p.phases[pair * p.ph_s];
+#pragma unroll 2
+  for (; i < n; i += step) {
     const int t = pos_of(i);
     if (t < 0) continue;
     float sn, c;
-    turn_of(t, p.phases[pair * p.ph_s], sn, c);
-    cs[u] = make_float2(c * p.mscale, sn * p.mscale);
+    turn_of(t, phase, sn, c);
+    cs[i * pairs + pair] = make_float2(c * p.mscale, sn * p.mscale);
   }
 }
 
@@ -245,7 +249,8 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
   __shared__ int lead[kMaxScaleRows];       // the runs' first t
   __shared__ int n_lead;
   __shared__ int src[kMaxScaleRows];        // t of the panel's rows, -1: not new
-  __shared__ int page[16], first_row[16];   // of the panel's blocks: page (-1: none), row in page
+  __shared__ int page[16], first_row[16];   // of the panel's blocks: page (-1: none), row in page,
+  __shared__ int first_pos[16];             // position of their first row
   __shared__ float amax[kWarps][kMaxScaleRows];  // of each pair's rows
   const int S = 1 << p.shift;
   // `parts` warps share a pair's rows, kPasses passes each
@@ -265,9 +270,13 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
   }
   if (warp == 0) {
     int found = 0;
+    // (a window of padding has nothing to look for)
+    bool any = false;
+    for (int i = lane; i < n; i += 32) any |= pos[(t0 + i) * p.p_t] >= 0;
+    any = __any_sync(0xffffffffu, any);
     // the last row before the window that is not padding
     int prev = -1;
-    for (int u = t0; u > 0 && prev < 0; u -= 32 * kScan) {
+    for (int u = t0; any && u > 0 && prev < 0; u -= 32 * kScan) {
       int v[kScan];
 #pragma unroll
       for (int i = 0; i < kScan; ++i) {
@@ -280,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
         if (m && prev < 0) prev = __shfl_sync(0xffffffffu, v[i], 31 - __clz(m));
       }
     }
-    for (int i0 = 0; i0 < n; i0 += 32) {
+    for (int i0 = 0; any && i0 < n; i0 += 32) {
       const int c = i0 + lane < n ? pos[(t0 + i0 + lane) * p.p_t] : -1;
       const unsigned rows = __ballot_sync(0xffffffffu, c >= 0), below = rows & ((1u << lane) - 1);
       const int near = __shfl_sync(0xffffffffu, c, below ? 31 - __clz(below) : 0);
@@ -302,13 +311,14 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
   const int runs = n_lead;
   for (int r0 = 0; r0 < runs; r0 += per_panel) {
     for (int k = warp; k < per_panel; k += kWarps) {  // the runs' rows, a warp a run
-      int pg = -1, row = 0;
+      int pg = -1, row = 0, first = 0;
       for (int i = lane; i < S; i += 32) src[k * S + i] = -1;
       __syncwarp();
       if (r0 + k < runs) {
         const int t = lead[r0 + k], c = pos[t * p.p_t];
         pg = page_of(p.pages, b, c);
         row = (c & (p.pages.rows - 1)) & ~(S - 1);
+        first = c & ~(S - 1);
         bool more = true;
         for (int u = t; more && u < p.T; u += 32 * kScan) {
           int v[kScan];
@@ -327,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
       if (lane == 0) {
         page[k] = pg;
         first_row[k] = row;
+        first_pos[k] = first;
       }
     }
     __syncthreads();
@@ -357,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
       old = (int)*scale - 127;
     }
     if (turns) {  // (while the rows arrive)
-      fill_angles(p, cs, p.panel, [&](int i) { return src[i] < 0 ? -1 : pos[src[i] * p.p_t]; });
+      fill_angles(p, cs, p.panel, [&](int i) { return src[i] < 0 ? -1 : first_pos[i >> p.shift] + (i & (S - 1)); });
       __syncthreads();
     }
     if (works) {

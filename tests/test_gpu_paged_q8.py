@@ -88,7 +88,7 @@ def reference(a, out_dtype):
     table, lens, pos = a["table"].cpu(), a["lens"].cpu(), a["pos"].cpu()
     prompt = Tq >= 64 and a["tree"] is None and a["scale"] > 0 and q.stride(3) == 1 and q.stride(2) % 8 == 0
     wt = 2.0 ** -8 + 2.0 ** -16 if prompt else (2.0 ** -11 if out_dtype == BF16 else 2.0 ** -21)
-    pieces = d == 128 and out_dtype == BF16 and not prompt
+    pieces = d == 128 and out_dtype == BF16 and not prompt and table.shape[1] * P > 256
     step = 2.0 ** -24 if pieces else 2.0 ** -36
     for b in range(B):
         n = max(0, min(int(lens[b]), table.shape[1] * P))

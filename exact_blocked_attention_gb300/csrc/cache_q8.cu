@@ -19,7 +19,7 @@
 // where a panel has more, warps share it and its maxima through shared memory.
 // (A warp for the whole panel, which computes its rows for the maximum and again
 // for the store: 55 us for a prompt of 5120 rows and 8 KV heads in blocks of 32,
-// KVUS so.)
+// 38 so.)
 //
 // Latency bounds a decode step's append: one launch, the query rows in CTAs of
 // their own.  Memory bounds a prompt's, most of it the query rows': from
@@ -125,9 +125,15 @@ template <typename T, int D, bool RUNS, bool INTER>
 __device__ __forceinline__ void row_values(const AppendParams& p, const Lane<D>& l, const float* w, bool norm,
                                            bool rotate, const float2* cs, float* stage, float (&x)[16]) {
   if (norm) {
-    float ss = 0.f;
+    uint64_t s2 = 0;  // (pairs: half the instructions)
 #pragma unroll
-    for (int j = 0; j < 16; ++j) ss = fmaf(x[j], x[j], ss);
+    for (int j = 0; j < 16; j += 2) {
+      const uint64_t v = f2(x[j], x[j + 1]);
+      s2 = ffma2(v, v, s2);
+    }
+    float ss, odd;
+    f2_split(s2, ss, odd);
+    ss += odd;
 #pragma unroll
     for (int off = Lane<D>::kLanes / 2; off >= 1; off >>= 1) ss += __shfl_xor_sync(l.lanes, ss, off);
     const float r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
@@ -170,14 +176,17 @@ __device__ __forceinline__ void row_values(const AppendParams& p, const Lane<D>&
 }
 
 // The angles of `n` rows: (cos, sin) mscale of every pair; pos_of(i) gives row
-// i's position, or a negative one (left out).  A thread keeps its pair.
+// i's position, or a negative one (left out).  A thread keeps its pair, whose
+// phase it loads at the kernel's start (phase_of).
+__device__ __forceinline__ int64_t phase_of(const AppendParams& p) {
+  return p.rot > 0 ? p.phases[threadIdx.x % (p.rot / 2) * p.ph_s] : 0;
+}
 template <typename F>
-__device__ __forceinline__ void fill_angles(const AppendParams& p, float2* cs, int n, F&& pos_of) {
+__device__ __forceinline__ void fill_angles(const AppendParams& p, int64_t phase, float2* cs, int n, F&& pos_of) {
   const int pairs = p.rot / 2, step = kThreads / pairs;  // (at most 64 pairs)
   const int pair = threadIdx.x % pairs;
   int i = threadIdx.x / pairs;
   if (i >= step) return;
-  const int64_t phase = p.phases[pair * p.ph_s];
 #pragma unroll 2
   for (; i < n; i += step) {
     const int t = pos_of(i);
@@ -203,10 +212,11 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
   const int b = blockIdx.x / windows, t0 = (blockIdx.x - b * windows) * p.panel;
   const int n = min(p.panel, p.T - t0);
   const int32_t* pos = p.pos + b * p.p_b;
+  const int64_t phase = phase_of(p);
 
   if ((int)blockIdx.y >= p.kv_groups) {  // ---- query rows of the window
     const int h0 = ((int)blockIdx.y - p.kv_groups) * kQHeads, nh = min(kQHeads, p.Hq - h0);
-    if (p.rot) fill_angles(p, cs, n, [&](int i) { return pos[(t0 + i) * p.p_t]; });
+    if (p.rot) fill_angles(p, phase, cs, n, [&](int i) { return pos[(t0 + i) * p.p_t]; });
     float w[16];
     const bool norm = p.wq != nullptr;
 #pragma unroll
@@ -272,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
     int found = 0;
     // (a window of padding has nothing to look for)
     bool any = false;
+#pragma unroll 4
     for (int i = lane; i < n; i += 32) any |= pos[(t0 + i) * p.p_t] >= 0;
     any = __any_sync(0xffffffffu, any);
     // the last row before the window that is not padding
@@ -368,26 +379,33 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
       old = (int)*scale - 127;
     }
     if (turns) {  // (while the rows arrive)
-      fill_angles(p, cs, p.panel, [&](int i) { return src[i] < 0 ? -1 : first_pos[i >> p.shift] + (i & (S - 1)); });
+      fill_angles(p, phase, cs, p.panel, [&](int i) { return src[i] < 0 ? -1 : first_pos[i >> p.shift] + (i & (S - 1)); });
       __syncthreads();
     }
     if (works) {
 #pragma unroll
       for (int k = 0; k < kPasses; ++k) {
         const int r = row0 + k * Lane<D>::kRows + l.slot;
-        float a = 0.f;
+        uint32_t a = 0;
         if (is_new[k]) {
           row_values<T, D, RUNS, INTER>(p, l, w, which == 0 && p.wk != nullptr, which == 0 && p.rot > 0,
                                         cs + r * (p.rot / 2), stage, x[k]);
+          // sizes as bit patterns: those of infinities and NaN are the largest, and rare
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float v = fabsf(x[k][j]);
-            a = fmaxf(a, v <= 3.4028235e38f ? v : 0.f);
+          for (int j = 0; j < 16; ++j) a = max(a, __float_as_uint(x[k][j]) & 0x7fffffffu);
+          if (a >= 0x7f800000u) {
+            a = 0;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const uint32_t v = __float_as_uint(x[k][j]) & 0x7fffffffu;
+              if (v >= 0x7f800000u) x[k][j] = __uint_as_float(0x7fc00000u);  // they have no 8-bit form
+              else a = max(a, v);
+            }
           }
 #pragma unroll
-          for (int off = Lane<D>::kLanes / 2; off >= 1; off >>= 1) a = fmaxf(a, __shfl_xor_sync(l.lanes, a, off));
+          for (int off = Lane<D>::kLanes / 2; off >= 1; off >>= 1) a = max(a, __shfl_xor_sync(l.lanes, a, off));
         }
-        if (l.it == 0 && r < p.panel) amax[warp / parts][r] = a;
+        if (l.it == 0 && r < p.panel) amax[warp / parts][r] = __uint_as_float(a);
       }
     }
     __syncthreads();
@@ -413,11 +431,10 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
         unsigned char* o = pool.p + (page[blk] * pool.s_n + h * pool.s_h + (first_row[blk] + (r & (S - 1))) * pool.s_r);
         uint2 y0, y1;
         if (is_new[k]) {
-          const float f = pow2(-e_new);
+          const float f = e_new < 128 ? pow2(-e_new) : __uint_as_float(0x7fc00000u);
           float v[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            v[j] = fabsf(x[k][j]) <= 3.4028235e38f && e_new < 128 ? x[k][j] * f : __uint_as_float(0x7fc00000u);
+          for (int j = 0; j < 16; ++j) v[j] = x[k][j] * f;
           y0.x = to_e4m3x2(v[0], v[1]) | to_e4m3x2(v[2], v[3]) << 16;
           y0.y = to_e4m3x2(v[4], v[5]) | to_e4m3x2(v[6], v[7]) << 16;
           y1.x = to_e4m3x2(v[8], v[9]) | to_e4m3x2(v[10], v[11]) << 16;

@@ -45,7 +45,7 @@ constexpr float kLazyM = 8.f, kMarginM = 16.f;
 // the largest weight so far: there is room for a maximum 2^6 above it before it
 // has to rise, which takes a tile 1 us and more (with room for 2^4, some of 40
 // rows raised theirs in every second tile where the blocks' scales differ by 2^4:
-// 182 us for five-row chains of 64 heads, MARGINUS so).
+// 182 us for five-row chains of 64 heads, 170 so).
 constexpr float kLift = 4.f, kMargin = 2.f;
 constexpr float kMostW = 256.f;
 
@@ -97,7 +97,7 @@ struct TcLayout {
   // Up to 16 rows a tile is 256 keys, two subtiles, each with key threads of its
   // own: what a tile takes is a chain of waits, loads and a vote, some 1.4 us
   // whatever its size.  More rows: 128 keys.
-  // (12 key warps of 16 rows each for 48, not 8 of 24: MOREUS in place of 240 us
+  // (12 key warps of 16 rows each for 48, not 8 of 24: 157 us in place of 190
   // for five-row chains of 64 heads)
   static constexpr int kSub = NR <= 16 ? 2 : 1;
   static constexpr int kParts = NR == 8 ? 1 : (NR == 16 ? 2 : (NR == 32 ? 2 : 3));

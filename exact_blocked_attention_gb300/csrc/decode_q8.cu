@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_q8_kernel(co
   float* s_row = reinterpret_cast<float*>(sm + L::kOffRow);
   uint64_t* s_seen = reinterpret_cast<uint64_t*>(sm + L::kOffTab);  // [B] tree nodes that some row lists
   int* s_end = reinterpret_cast<int*>(s_seen + p.B);  // [B] keys that some row sees are [start, end)
-  int* s_start = s_end + p.B;                            // (a multiple of kOwn)
+  int* s_start = s_end + p.B;
   int* s_nt = s_start + p.B;
   int* s_tree = s_nt + p.B;  // [B] key of the tree's first node
   int* s_pre = s_tree + p.B;  // [B + 1] tiles before the sequence
@@ -136,12 +136,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_q8_kernel(co
         start = min(start, f);
       }
     }
-    start = end > 0 ? start & ~(kOwn - 1) : 0;
+    start = end > 0 ? start : 0;
     s_seen[b] = seen;
     s_tree[b] = p.tree ? len - p.Tq : 0x7fffffff;
     s_end[b] = end;
     s_start[b] = start;
-    s_nt[b] = (end - start + kTile - 1) / kTile;
+    s_nt[b] = (end - (start & ~(kOwn - 1)) + kTile - 1) / kTile;
   }
   __syncthreads();
   if (warp == 0) {
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_q8_kernel(co
   // ---- the stream: a tile's page numbers and scales ahead of its rows, those ahead of their use
   unsigned char* ring = sm + warp * (2 * L::kHalf);
   const uint32_t ring_k = smem_u32(ring) + lane * 16, ring_v = smem_u32(ring) + L::kHalf + lane * VB;
-  auto key0_of = [&](const Place& a) { return s_start[a.b] + a.j * kTile + warp * kOwn; };
+  auto key0_of = [&](const Place& a) { return (s_start[a.b] & ~(kOwn - 1)) + a.j * kTile + warp * kOwn; };
   // What lane i knows of the warp's key i in a tile.
   struct Keys {
     int key0;        // of the warp
@@ -233,8 +233,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_q8_kernel(co
   auto look_up = [&](const Place& a, Keys& k) {
     k.key0 = key0_of(a);
     const int key = k.key0 + lane, node = key - s_tree[a.b];
-    // (past the end, or a tree node that no row lists: not seen)
-    const bool seen = key < s_end[a.b] && (node < 0 || ((s_seen[a.b] >> node) & 1));
+    // (past the end, before the windows, or a tree node that no row lists: not seen)
+    const bool seen = key < s_end[a.b] && key >= s_start[a.b] && (node < 0 || ((s_seen[a.b] >> node) & 1));
     const int page = seen ? page_of(p.pages, a.b, key) : -1;
     const int row = key & (p.pages.rows - 1);
     k.ek = k.ev = 127;

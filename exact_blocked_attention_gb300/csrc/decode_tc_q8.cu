@@ -1,8 +1,8 @@
 // Decode and verify rows over the 8-bit paged cache on the 5th-generation tensor
 // cores (tcgen05, kind::f8f6f4), heads of 128.
 //
-// The cache's bytes are the products' operands: a tile of 128 keys goes by TMA
-// into shared memory and is read there by the tensor core, nothing converts it.
+// The cache's bytes are the products' operands: 128 keys at a time go by TMA into
+// shared memory and are read there by the tensor core, nothing converts them.
 // The other operands are split into e4m3 pieces, each 1/16 (q: 1/32) of the one
 // before, side by side along N, so that a tile is read once:
 //
@@ -16,7 +16,8 @@
 // 2^-12 of the largest weight, below that to a step of 2^-23 of it (or finer).
 // With k = 2^ek k8 and v = 2^ev v8: x = (S_hi + S_lo / 32) 2^ek fac_row, and the
 // weight is 2^(x - m + ev - r), of two references a row: m >= max x - 8 for the
-// sum of fp32 weights, and r >= max (x - m + ev) - 4 (r relative to m: beside a large x, ev would be lost).
+// sum of fp32 weights, and r >= max (x - m + ev) - 4 for the product's (r relative
+// to m: beside a large x, ev would be lost).
 //
 // Otherwise the kernel is the one of decode_tc.cu over pages: the same cut of
 // all units' tiles into equal ranges, one a CTA, the same roles, order of
@@ -125,10 +126,10 @@ struct TcLayout {
   static constexpr int kRowsBytes = (int)((sizeof(RowFacts<NR>) + 15) / 16 * 16);
   static constexpr int kOffNTab = kOffRows + 2 * kRowsBytes;     // uint16 tiles, first tile per (sequence, row group)
   static constexpr int kOffRed = kOffNTab + 2 * kDecodeTcMaxEntries * 2;  // float [8][NR]
-  // float [NR] each: m, m_use, thr, r, (unused), 2^(lift - r), alpha of l, alpha of U of the
+  // float [NR] each: m, m_use, thr, r, 2^(lift - r), factor of l, factor of U of the
   // current unit; m, l, r, 1 / l of the finished unit whose U readout is pending
   static constexpr int kOffStat = kOffRed + 8 * NR * 4;
-  static constexpr int kOffScale = kOffStat + 12 * NR * 4;       // uint32 [kScaleRing][BK]: each key's scale bytes
+  static constexpr int kOffScale = kOffStat + 11 * NR * 4;       // uint32 [kScaleRing][BK]: each key's scale bytes
   static constexpr int kOffBar = kOffScale + kScaleRing * BK * 4;
   // full[kSlots], empty[kSlots], q_full[2], q_empty[2], p_full[2], u_full[2], drain, sc_full[kScaleRing], sc_empty[kScaleRing]
   static constexpr int kNumBars = 2 * kSlots + 2 + 2 + 2 + 2 + 1 + 2 * kScaleRing;
@@ -277,13 +278,13 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
   float* s_muse = s_m + NR;                                  // m, or 0 when none yet
   float* s_thr = s_m + 2 * NR;                               // m + 8, -inf when none yet
   float* s_r = s_m + 3 * NR;                                 // reference of the weights, -inf = none yet
-  float* s_h = s_m + 5 * NR;                                 // 2^(lift - r), 1 when none yet
-  float* s_alpha = s_m + 6 * NR;
-  float* s_beta = s_m + 7 * NR;
-  float* s_mfin = s_m + 8 * NR;
-  float* s_lfin = s_m + 9 * NR;
-  float* s_rfin = s_m + 10 * NR;
-  float* s_inv = s_m + 11 * NR;
+  float* s_h = s_m + 4 * NR;                                 // 2^(lift - r), 1 when none yet
+  float* s_alpha = s_m + 5 * NR;
+  float* s_beta = s_m + 6 * NR;
+  float* s_mfin = s_m + 7 * NR;
+  float* s_lfin = s_m + 8 * NR;
+  float* s_rfin = s_m + 9 * NR;
+  float* s_inv = s_m + 10 * NR;
   uint32_t* s_sc = reinterpret_cast<uint32_t*>(sm + L::kOffScale);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kOffBar);
   uint64_t* full = bars;
@@ -824,7 +825,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
       uint32_t buf = 0, p_phase = 0;  // tile parity, phase of its P^T buffer
       while (ok && left > 0) {
         if (left_q > 0 && !issue_qk(buf ^ 1u)) { ok = false; break; }
-        // U^T += V_j^T [P_hi | P_lo]^T once the key threads wrote P^T
+        // U^T += V_j^T [p_1 | p_2 | ..]^T once the key threads wrote P^T
         if (!mbar_wait(&p_full[buf], p_phase)) { ok = false; break; }
         const uint32_t ucol = tb + L::kColU + L::kStepU * (uint32_t)(up & 1);
 #pragma unroll
@@ -1018,6 +1019,13 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
       if (threadIdx.x == 0) mbar_arrive(&q_empty[pb]);
       return true;
     };
+    // A key that no row of the unit sees, past every end, before the windows or a
+    // tree node that no row lists: its rows and scales may hold anything.
+    auto unseen = [](const RowFacts<NR>& rf, int key) {
+      const int node = key - rf.tree_base;
+      return key >= rf.unit_end || key < rf.unit_start ||
+             (rf.tree_base != 0x7fffffff && node >= 0 && node < 64 && !((rf.tree_seen >> node) & 1ull));
+    };
     // rows' maxima of v over the tile's keys: red[..][row]
     auto tile_max = [&](const float (&v)[NH]) {
       float t[NH];
@@ -1062,7 +1070,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
         if (sc != 0) {
           const int e = (sc >> 8) & 255;
           ks = scale_of(sc & 255);
-          ev = e == 255 ? __uint_as_float(0x7fc00000u) : (float)(e - 127);
+          ev = e < 255 ? (float)(e - 127) : (unseen(rf, key) ? 0.f : __uint_as_float(0x7fc00000u));
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sc_empty[gs % kScaleRing]);
@@ -1197,7 +1205,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
           }
         }
         if (!first) {
-          // U^T lane k = value dim k, this half's columns of all pieces; the product
+          // U^T lane k = value dim k, the group's columns of all pieces; the product
           // with P_{j-1} must have completed (U += P_j V_j waits for this tile's P)
           const int64_t pv_seq = 2 * kSub * g - 1;  // V_{j-1}, its last subtile
           const bool done = wait_all(&empty[pv_seq % kSlots], (uint32_t)((pv_seq / kSlots) & 1));
@@ -1217,7 +1225,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
         }
       }
       if (!ok) break;
-      // ---- P^T row of key k, this half's rows: the weights' pieces ----
+      // ---- P^T row of key k, the group's rows: the weights' pieces ----
       {
         unsigned char* ph = sm + L::kOffP + (int)(g & 1) * L::kPBytes + sub * L::kPSub + k * 128;
 #pragma unroll
@@ -1257,15 +1265,11 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
         }
       }
       if ((cur.j == cur.n - 1 && key0 + TK > rf.unit_end) || key0 < rf.unit_start || key0 + TK > rf.tree_base) {
-        // zero the V rows that no row sees: past every visible key, before a
-        // window, tree nodes that no row lists (one group of each subtile)
+        // zero the V rows that no row sees (one group of each subtile)
         const int64_t sv = 2 * gs + 1;
         const bool vok = bar_and(kBarRows, kKeyThreads, wait_all(&full[sv % kSlots], (uint32_t)((sv / kSlots) & 1)));
         if (!vok) { ok = false; break; }
-        const int node = key - rf.tree_base;
-        const bool unseen = key >= rf.unit_end || key < rf.unit_start ||
-                            (rf.tree_base != 0x7fffffff && node >= 0 && node < 64 && !((rf.tree_seen >> node) & 1ull));
-        if (unseen && part == 0) {
+        if (unseen(rf, key) && part == 0) {
           unsigned char* vr = sm + (int)(sv % kSlots) * kSlotBytes + k * 128;
 #pragma unroll
           for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vr + (c << 4)) = make_uint4(0, 0, 0, 0);

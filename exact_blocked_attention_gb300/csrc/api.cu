@@ -1047,9 +1047,9 @@ int fwd_paged_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages_, con
 
 // blkattn_fwd_paged_q8.  Prompts (T_q >= 64, no tree, contiguous query rows,
 // scale > 0): the visible pages are written as bf16 to a buffer of the library
-// and the bf16 prompt kernel reads those (expand_pays tells when); the numbers
-// are the same, a bf16 holds e4m3 times a power of two.  The rest, and longer
-// batches in slices, goes to the kernel that reads the 8-bit pages.
+// and the bf16 prompt kernel reads those, the sequences in slices of kExpandBytes;
+// the numbers are the same, a bf16 holds e4m3 times a power of two.  The rest goes
+// to the kernels that read the 8-bit pages.
 constexpr int64_t kExpandBytes = 2LL << 30;  // of K and V for one slice of sequences; 8x for a single one
 
 int fwd_paged_q8_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages, const blkattn_tensor* v_pages,
@@ -1087,6 +1087,13 @@ int fwd_paged_q8_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages, c
     for (int i = 0; i < t->ndim; ++i)
       if (t->sizes[i] > 1 && t->strides[i] == 0 && c.B > 0 && c.Tq > 0) return BLKATTN_ERR_INVALID_ARG;
   if (c.Hkv > 0x7fff || c.Hq / c.Hkv * c.Tq > 0x7fffffff) return BLKATTN_ERR_UNSUPPORTED;
+  // (the kernels keep a row's offset within a head as 32 bits of 16 bytes)
+  for (const blkattn_tensor* t : {&kn, &vn}) {
+    const int64_t page = t->strides[0] / 16, row = t->strides[2] / 16;
+    if (page > 0xffffffffLL || row > 0xffffffffLL ||
+        (unsigned __int128)(t->sizes[0] - 1) * page + (unsigned __int128)(pt.rows - 1) * row > 0xffffffffu)
+      return BLKATTN_ERR_UNSUPPORTED;
+  }
   if (c.B == 0 || c.Tq == 0) return BLKATTN_OK;
   for (const blkattn_tensor* t : {page_table, k_scales, v_scales})
     if (t->data == nullptr) return BLKATTN_ERR_INVALID_ARG;
@@ -1196,12 +1203,6 @@ int fwd_paged_q8_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages, c
   p.q_vec = c.q_vec_ok;
   p.k = static_cast<const char*>(kn.data);
   p.v = static_cast<const char*>(vn.data);
-  // (the kernel keeps a row's offset within a head as 32 bits of 16 bytes)
-  for (const blkattn_tensor* t : {&kn, &vn})
-    if (t->strides[0] / 16 > 0xffffffffLL || t->strides[2] / 16 > 0xffffffffLL ||
-        (unsigned __int128)(t->sizes[0] - 1) * (t->strides[0] / 16) + (unsigned __int128)(pt.rows - 1) * (t->strides[2] / 16) >
-            0xffffffffu)
-      return BLKATTN_ERR_UNSUPPORTED;
   p.k_sn16 = (uint32_t)(kn.strides[0] / 16); p.k_sh = kn.strides[1]; p.k_sr16 = (uint32_t)(kn.strides[2] / 16);
   p.v_sn16 = (uint32_t)(vn.strides[0] / 16); p.v_sh = vn.strides[1]; p.v_sr16 = (uint32_t)(vn.strides[2] / 16);
   p.k_sc = static_cast<const unsigned char*>(k_scales->data);

@@ -217,3 +217,12 @@ def test_no_rows_is_a_no_op(lib, kw):
         for x in (a, b, c):
             x["table"].addr = None
     assert append(lib, a) == 0 and read(lib, b) == 0 and fwd(lib, c) == 0
+
+
+def test_pools_too_far_apart_for_attention(lib):
+    """Rows of a head more than 64 GiB from the first: the attention kernels keep 32 bits of 16 bytes."""
+    far = Fake((9, 2, 16, 128), F8, strides=(1 << 33, 2048, 128, 1), addr=0x100000)
+    near = Fake((9, 2, 16, 128), F8, strides=((1 << 33) - 1024, 2048, 128, 1), addr=0x100000)
+    for n in ("kp", "vp"):
+        assert fwd(lib, change(fwd_args(), {n: far})) == -2
+    assert fwd(lib, change(fwd_args(), {"kp": near, "sl": Fake((2,), I32, addr=None)})) == -1  # (as far as the next check)

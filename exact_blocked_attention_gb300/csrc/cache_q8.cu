@@ -136,7 +136,7 @@ __device__ __forceinline__ void row_values(const AppendParams& p, const Lane<D>&
     ss += odd;
 #pragma unroll
     for (int off = Lane<D>::kLanes / 2; off >= 1; off >>= 1) ss += __shfl_xor_sync(l.lanes, ss, off);
-    const float r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
+    const float r = rsqrt_fine(fmaf(ss, 1.f / D, p.eps));
 #pragma unroll
     for (int j = 0; j < 16; ++j) x[j] = x[j] * r * w[j];
   }
@@ -192,7 +192,7 @@ __device__ __forceinline__ void fill_angles(const AppendParams& p, int64_t phase
     const int t = pos_of(i);
     if (t < 0) continue;
     float sn, c;
-    turn_of(t, phase, sn, c);
+    turn_of_fine(t, phase, sn, c);
     cs[i * pairs + pair] = make_float2(c * p.mscale, sn * p.mscale);
   }
 }
@@ -722,7 +722,7 @@ int blkattn_paged_append_q8(const blkattn_tensor* k, const blkattn_tensor* v, co
   if (!tensors_on_one_device(k, {v, pos, page_table, k_pages, v_pages, k_scales, v_scales, k_weight_opt, phases_opt,
                                  q_opt, q_weight_opt, q_out_opt}))
     return BLKATTN_ERR_INVALID_ARG;
-  if (H > 0x7fff || Hq > 0x7fff || B > 0x7fffffff || T > 0x7fffffff || (B > 0 && T > 0x7fffffff / B))
+  if (H > 0x7fff || Hq > 0x7fff || B > 0x7fffffff || T > 0x7fffffff - 0xffff || (B > 0 && T > 0x7fffffff / B))
     return BLKATTN_ERR_UNSUPPORTED;
   if (B == 0 || T == 0) return BLKATTN_OK;
   for (const blkattn_tensor* t : {k, v, pos, page_table, k_pages, v_pages, k_scales, v_scales})

@@ -26,6 +26,25 @@ __device__ __forceinline__ void turn_of(int t, int64_t F, float& sn, float& cs) 
   // the top 32 bits: a signed fraction of half a turn in [-1, 1)
   sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &sn, &cs);
 }
+// The same with what the float cannot hold of those 32 bits, to first order: for
+// rows that are rounded to few bits next, where an angle's last bit moves a
+// value over a step now and then.
+__device__ __forceinline__ void turn_of_fine(int t, int64_t F, float& sn, float& cs) {
+  const uint64_t a = (uint64_t)(int64_t)t * (uint64_t)F;
+  const int32_t h = (int32_t)(a >> 32);
+  const int32_t most = h & ~0xff;  // 24 bits
+  float s, c;
+  sincospif((float)most * 0x1p-31f, &s, &c);
+  const float r = (float)(h - most) * (0x1p-31f * 3.14159265f);
+  sn = fmaf(c, r, s);
+  cs = fmaf(-s, r, c);
+}
+// 1 / sqrt(x), with a step of Newton's after the approximation.
+__device__ __forceinline__ float rsqrt_fine(float x) {
+  const float r = rsqrtf(x);
+  const float f = fmaf(0.5f * r, fmaf(-x * r, r, 1.f), r);
+  return f - f == 0.f ? f : r;  // (zeros and infinities)
+}
 
 // V elements of a row in registers, moved as one access.
 template <typename T, int V>

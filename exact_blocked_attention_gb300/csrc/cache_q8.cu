@@ -722,7 +722,8 @@ int blkattn_paged_append_q8(const blkattn_tensor* k, const blkattn_tensor* v, co
   if (!tensors_on_one_device(k, {v, pos, page_table, k_pages, v_pages, k_scales, v_scales, k_weight_opt, phases_opt,
                                  q_opt, q_weight_opt, q_out_opt}))
     return BLKATTN_ERR_INVALID_ARG;
-  if (H > 0x7fff || Hq > 0x7fff || B > 0x7fffffff || T > 0x7fffffff - 0xffff || (B > 0 && T > 0x7fffffff / B))
+  if (H > 0x7fff || Hq > 0x7fff || B > 0x7fffffff || T > 0x7fffffff - 0xffff || (B > 0 && T > 0x7fffffff / B) ||
+      B * T * Hq > kMostRows)
     return BLKATTN_ERR_UNSUPPORTED;
   if (B == 0 || T == 0) return BLKATTN_OK;
   for (const blkattn_tensor* t : {k, v, pos, page_table, k_pages, v_pages, k_scales, v_scales})

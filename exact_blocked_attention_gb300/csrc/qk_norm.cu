@@ -661,8 +661,7 @@ cudaError_t launch_forward(NormParams p, cudaStream_t stream) {
     return cudaGetLastError();
   }
   const int64_t rows = (int64_t)p.B * p.T * (p.set[0].heads + (p.n_sets > 1 ? p.set[1].heads : 0));
-  const int64_t blocks = (rows + kWarps - 1) / kWarps;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  const int64_t blocks = (rows + kWarps - 1) / kWarps;  // (kMostRows: in a grid's range)
   norm_rows_kernel<TI, TO, INTER><<<(unsigned)blocks, kThreads, kWarps * p.d * sizeof(float), stream>>>(p);
   return cudaGetLastError();
 }
@@ -854,7 +853,8 @@ int norm(const Call& c, bool back, blkattn_stream_t stream_) {
     if (c.x[i]->sizes[1] > 0x7fff) return BLKATTN_ERR_UNSUPPORTED;
     heads += c.x[i]->sizes[1];
   }
-  if (d > kMaxDim || B > 0x7fffffff || T > 0x7fffffff || (B > 0 && T > 0x7fffffff / B)) return BLKATTN_ERR_UNSUPPORTED;
+  if (d > kMaxDim || B > 0x7fffffff || T > 0x7fffffff || (B > 0 && T > 0x7fffffff / B) || B * T * heads > kMostRows)
+    return BLKATTN_ERR_UNSUPPORTED;
   const bool rows = B > 0 && T > 0 && heads > 0;
   if (!rows && !back) return BLKATTN_OK;
   for (int i = 0; i < n_sets; ++i) {

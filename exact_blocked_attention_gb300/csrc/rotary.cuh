@@ -127,6 +127,7 @@ __device__ __forceinline__ void turn_run(const Vec<TI, V>& x0, const Vec<TI, V>&
 
 // ------------------------------------------------------------- validation
 constexpr int64_t kMaxDim = 1024;
+constexpr int64_t kMostRows = 1LL << 33;  // of one call of the head norms
 
 inline bool floats(const blkattn_tensor* t) { return t->dtype == BLKATTN_BF16 || t->dtype == BLKATTN_F32; }
 

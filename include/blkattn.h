@@ -405,8 +405,8 @@ int blkattn_rope_bwd(const blkattn_tensor* dy, const blkattn_tensor* pos, const 
  *         address, dtype and strides); any other overlap is out of contract.
  * Computed in fp32, rounded once.  One kernel, no workspace, any stream; calls
  * on different streams are independent.  Sizes of 0 are a no-op.  Returns as
- * blkattn_rope; BLKATTN_ERR_UNSUPPORTED for d > 1024, more than 32767 heads or
- * B T > 2^31 - 1.
+ * blkattn_rope; BLKATTN_ERR_UNSUPPORTED for d > 1024, more than 32767 heads,
+ * B T > 2^31 - 1 or B T (H_q + H_k) > 2^33.
  *
  * blkattn_qk_norm_rope_bwd — its gradients.  With g = R^T dy, h = x r,
  * r = 1 / sqrt(mean(x^2) + eps) and c = w g:
@@ -531,7 +531,9 @@ int blkattn_fwd_paged(const blkattn_tensor* q, const blkattn_tensor* k_pages, co
  * descend with t; of rows that name the same cache row the last is kept.  Rows
  * in another order leave the blocks concerned with any contents.  Two sequences
  * of a call must not write the same block.  The new rows must not overlap the
- * pools.  One kernel, no workspace, any stream.  Returns as blkattn_rope.
+ * pools.  One kernel, or two (the query rows of a prompt have their own); no
+ * workspace, any stream.  Returns as blkattn_rope; BLKATTN_ERR_UNSUPPORTED for
+ * more than 32767 heads, T > 2^31 - 65536, B T > 2^31 - 1 or B T H_q > 2^33.
  *
  * blkattn_paged_read_q8 — rows of the cache as numbers.
  *
@@ -565,12 +567,20 @@ int blkattn_paged_read_q8(const blkattn_tensor* pos, const blkattn_tensor* page_
  * pools and its scales may hold anything.
  * Precision: the cache's numbers are exact, sums and statistics fp32.  Weights
  * enter the value product with f16's 11 bits for a bf16 out and 22 bits for an
- * f32 out, relative to the row's largest weight times its scale; bf16 prompts
- * with the same out go through the kernel of blkattn_fwd_paged and have its
- * precision.  A row with a NaN among the scores of its visible keys gives NaN
- * in out and lse; the other rows are not touched by it.
- * Workspace, growth and overlap of calls as for blkattn_fwd.  Returns as
- * blkattn_fwd_paged.
+ * f32 out, and vanish below 2^-36 of the row's largest weight times scale.  With
+ * a bf16 out and d = 128 (over tables of more than 256 rows, of contiguous query
+ * rows) weights have an absolute step too, 2^-23 of that largest product, and a
+ * query row's dims one of 2^-22 of its largest dim.  Prompts (T_q >= 64, no tree, 16-byte
+ * aligned contiguous rows, scale > 0) go through the kernel of
+ * blkattn_fwd_paged and have its precision.  A row with a NaN or an infinity in q, or a NaN
+ * among the scores of its visible keys, gives NaN in out and lse; the other
+ * rows are not touched by it.
+ * Workspace, growth and overlap of calls as for blkattn_fwd.  For prompts the
+ * library also keeps a bf16 copy of the pages that the call's tables can name:
+ * up to 2 GiB for a slice of the sequences, up to 16 GiB where one sequence
+ * alone has more (beyond that the pages are read as they are).
+ * Returns as blkattn_fwd_paged; BLKATTN_ERR_UNSUPPORTED too for a q of f32 and
+ * for pools whose rows of one head lie 64 GiB or more apart.
  */
 int blkattn_fwd_paged_q8(const blkattn_tensor* q, const blkattn_tensor* k_pages, const blkattn_tensor* v_pages,
                          const blkattn_tensor* k_scales, const blkattn_tensor* v_scales,

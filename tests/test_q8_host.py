@@ -88,7 +88,7 @@ def test_norm_bwd_refuses(lib, what):
 
 
 def test_norm_sizes(lib):
-    for kw in (dict(d=1025, rot=0), dict(Hq=1 << 15), dict(B=1 << 16, T=1 << 16)):
+    for kw in (dict(d=1025, rot=0), dict(Hq=1 << 15), dict(B=1 << 16, T=1 << 16), dict(B=1 << 10, T=1 << 10, Hq=1 << 13)):
         assert norm(lib, norm_args(**kw)) == -2 and norm_bwd(lib, norm_args(**kw)) == -2
     for kw in (dict(B=0), dict(T=0), dict(Hq=0, Hk=0)):
         a = norm_args(**kw)

@@ -348,8 +348,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_q8_kernel(co
           const int pos = p.qpos[cur.b * p.qp_sb + i * p.qp_si];
           end = pos < 0 ? 0 : (pos >= len ? len : pos + 1);
           first = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
-          min_end = min(min_end, end);
-          max_first = max(max_first, first);
+          // (a row that sees nothing takes part in tiles without a mask; what comes of
+          // it is dropped)
+          if (end > 0) {
+            min_end = min(min_end, end);
+            max_first = max(max_first, first);
+          }
         }
         r_end[nt][c] = end;
         r_first[nt][c] = first;
@@ -397,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_q8_kernel(co
           const int r = 8 * nt + 2 * t4 + c;
           sM[r] = M[nt][c];
           sR[r] = R[nt][c];
-          sL[r] = l;
+          sL[r] = r_end[nt][c] > 0 ? l : 0.f;
         }
       }
     __syncthreads();

@@ -3,8 +3,8 @@
 //
 // The cache's bytes are the products' operands: 128 keys at a time go by TMA into
 // shared memory and are read there by the tensor core, nothing converts them.
-// The other operands are split into e4m3 pieces, each 1/16 (q: 1/32) of the one
-// before, side by side along N, so that a tile is read once:
+// The other operands are split into pieces of 8 bits side by side along N, so that
+// a tile is read once:
 //
 //   S^T_j  = K_j [q_hi | q_lo]^T      M = 128 keys, N = 2 NR rows, K = 32 x 4
 //   U^T   += V_j^T [p_1 | p_2 | ..]^T  M = 128 dims, N = pieces x NR, K = 32 x 4
@@ -12,8 +12,12 @@
 // q: a row scaled by a power of two to 2^7 <= max |q| < 2^8; q_hi its nearest
 // e4m3 (4 bits) and q_lo = 32 (q - q_hi) the rest of a bf16's 8 bits, exact but
 // for dims below 2^-14 of the row's largest (off by at most 2^-22 of it).
-// p: a weight as f16 (11 bits), taken apart into 4 pieces: all of an f16 down to
-// 2^-12 of the largest weight, below that to a step of 2^-23 of it (or finer).
+// p: a weight as f16, taken apart exactly into 4 pieces of e5m2: an f16's upper
+// byte is the first (its value cut to 3 bits), the rest times 2^8 has 8 bits, its
+// upper byte is the second, and so on; U = U_1 + (U_2 + U_3 + U_4) / 2^8.  An f16's
+// step is 2^-23 of the row's largest weight or finer.  (Pieces of e4m3, two
+// conversions each and room for weights to 2^8 only: five-row chains of 64 heads
+// 129 us, 118 so.)
 // With k = 2^ek k8 and v = 2^ev v8: x = (S_hi + S_lo / 32) 2^ek fac_row, and the
 // weight is 2^(x - m + ev - r), of two references a row: m >= max x - 8 for the
 // sum of fp32 weights, and r >= max (x - m + ev) - 4 for the product's (r relative
@@ -43,22 +47,23 @@ constexpr float kNegInf = -__builtin_huge_valf();
 // nothing by it) and rises when one passes it by 2^8.
 constexpr float kLazyM = 8.f, kMarginM = 16.f;
 // A weight at the reference is 2^kLift, and the reference is set 2^kMargin above
-// the largest weight so far: there is room for a maximum 2^6 above it before it
-// has to rise, which takes a tile 1 us and more (with room for 2^4, some of 40
-// rows raised theirs in every second tile where the blocks' scales differ by 2^4:
-// 182 us for five-row chains of 64 heads, 170 so).
-constexpr float kLift = 4.f, kMargin = 2.f;
-constexpr float kMostW = 256.f;
+// the largest weight so far: there is room for a maximum 2^12 above that before the
+// reference has to rise, which costs a tile 2.5 us (with room for 2^6 ten tiles of
+// 57 raised one of 40 rows').  kMostW: the largest whose rest times 2^8 is an f16.
+constexpr float kLift = 4.f, kMargin = 5.f;
+constexpr float kMostW = 2047.f;
 
 constexpr int D = 128;
 constexpr int BK = 128;               // keys of a product (TMEM lanes of S^T)
 constexpr int kSlotBytes = BK * D;    // a ring slot, K or V: 128 rows of 128 bytes
 constexpr int kBarRows = 1;           // named barrier of the key threads
+constexpr int kBarFirst = 2;          // of the key threads and the unit loader: the first unit's query rows
 constexpr uint32_t kTmemCols = 512;
 
-// Instruction descriptor for kind::f8f6f4, e4m3 A and B, fp32 accumulator.
-constexpr uint32_t idesc_e4m3(int M, int N, int a_mn, int b_mn) {
-  return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
+// Instruction descriptor for kind::f8f6f4: e4m3 A, e4m3 (0) or e5m2 (1) B, fp32
+// accumulator.
+constexpr uint32_t idesc_f8(int b_type, int M, int N, int a_mn, int b_mn) {
+  return (1u << 4) | ((uint32_t)b_type << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
 __device__ __forceinline__ void mma_f8(uint32_t d_taddr, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -88,7 +93,7 @@ struct RowFacts {
   int unit_end;      // max over the rows
   int unit_start;    // the earliest key that a row sees (INT_MAX: none)
   uint64_t tree_seen;  // bit k = some row sees tree node k
-  int min_end;       // min over the real rows
+  int min_end;       // min over the rows that see keys
   int tree_base;     // first key of the token tree (len - T_q); INT_MAX without a tree
   int win_max;       // sliding window: the largest first visible key of the rows (0 without)
 };
@@ -99,7 +104,7 @@ struct TcLayout {
   // own: what a tile takes is a chain of waits, loads and a vote, some 1.4 us
   // whatever its size.  More rows: 128 keys.
   // (12 key warps of 16 rows each for 48, not 8 of 24: 157 us in place of 190
-  // for five-row chains of 64 heads)
+  // for five-row chains of 64 heads at the time; 113 now)
   static constexpr int kSub = NR <= 16 ? 2 : 1;
   static constexpr int kParts = NR == 8 ? 1 : (NR == 16 ? 2 : (NR == 32 ? 2 : 3));
   static constexpr int kKeyWarps = 4 * kSub * kParts;        // a warp a TMEM lane quarter, subtile and part of the rows
@@ -143,7 +148,7 @@ struct TcLayout {
 
 // The CTA's start in the tile order (written once by warp 0).
 struct Start {
-  long long t0, t1, W, P, su;
+  int t0, t1, W, P, su;  // (the host keeps the tile count below 2^24)
   int b, kvh, rg, j;
 };
 
@@ -152,7 +157,7 @@ struct Start {
 // `extra` weight-only tiles after them (the partition charges a unit for its
 // set-up and readout, so CTAs holding many short units get fewer tiles).
 struct Cursor {
-  int64_t t, su;
+  int t, su;
   int b, kvh, rg, j, n;
   int extra;
   int s0;               // the unit's first tile (sliding window; 0 otherwise)
@@ -186,11 +191,9 @@ struct Cursor {
 
 // CTA whose range [c W / P, (c + 1) W / P) holds global tile t.
 // (32-bit arithmetic: the host keeps the tile count below 2^24 and
-// P <= 255, so (t + 1) P < 2^32; a 64-bit division is a long software
-// sequence on the GPU.)
-__device__ __forceinline__ int64_t cta_of(int64_t t, int64_t W, int64_t P) {
-  const uint32_t w = (uint32_t)W;
-  return (int64_t)((((uint32_t)t + 1u) * (uint32_t)P + w - 1u) / w) - 1;
+// P <= 255, so (t + 1) P < 2^32.)
+__device__ __forceinline__ int cta_of(int t, int W, int P) {
+  return (int)((((uint32_t)t + 1u) * (uint32_t)P + (uint32_t)W - 1u) / (uint32_t)W) - 1;
 }
 
 // N consecutive TMEM columns of this thread's lane (N = 8, 16 or 24; the
@@ -259,8 +262,8 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
     decode_tc_q8_kernel(const __grid_constant__ Q8Params p, const __grid_constant__ CUtensorMap tmk,
                         const __grid_constant__ CUtensorMap tmv) {
   using L = TcLayout<NR>;
-  constexpr uint32_t kIdescQK = idesc_e4m3(128, 2 * NR, 0, 0);   // K, Q both K-major
-  constexpr uint32_t kIdescPV = idesc_e4m3(128, L::kPN, 1, 1);   // V^T, P^T both MN-major
+  constexpr uint32_t kIdescQK = idesc_f8(0, 128, 2 * NR, 0, 0);   // K, Q both K-major
+  constexpr uint32_t kIdescPV = idesc_f8(1, 128, L::kPN, 1, 1);   // V^T, P^T both MN-major
   constexpr int kSlots = L::kSlots, kSub = L::kSub, TK = L::kTileKeys, kScaleRing = L::kScaleRing;
   constexpr int kPieces = L::kPieces;
   constexpr int kKeyWarps = L::kKeyWarps, kKeyThreads = 32 * kKeyWarps, kThreads = L::kThreads;
@@ -424,10 +427,10 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
       const long long excl = incl - s;
       const unsigned own = __ballot_sync(0xffffffffu, t0 < t1 && excl <= t0 && t0 < incl);
       if (lane == 0) {
-        start->t0 = t0;
-        start->t1 = t1;
-        start->W = W;
-        start->P = P;
+        start->t0 = (int)t0;
+        start->t1 = (int)t1;
+        start->W = (int)W;
+        start->P = (int)P;
       }
       if (own != 0 && lane == __ffs(own) - 1) {
         long long pre = excl;
@@ -450,17 +453,17 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
         start->kvh = kvh;
         start->rg = rg;
         start->j = (int)o2;
-        start->su = su;
+        start->su = (int)su;
       }
     }
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
   }
-  const int64_t t0 = start->t0;
-  const int64_t t1 = start->t1;
-  const int64_t W = start->W;
-  const int64_t P_work = start->P;  // CTAs that hold tiles: [0, P_work)
+  const int t0 = start->t0;
+  const int t1 = start->t1;
+  const int W = start->W;
+  const int P_work = start->P;  // CTAs that hold tiles: [0, P_work)
   const uint32_t tb = static_cast<uint32_t>(misc[0]);
   const uint32_t sRing = smem_u32(sm);
   const uint32_t sQ = smem_u32(sm + L::kOffQ);
@@ -479,6 +482,33 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
   cur.s0 = (t0 < t1 && cur.st != nullptr) ? (int)stab[cur.b * RG + cur.rg] : 0;
   // a range may start among a unit's weight-only tiles: begin at the next unit
   if (t0 < t1 && cur.j >= cur.n) cur.step_unit(ntab, RG, Hkv, B);
+
+  // Query row r (4 dims a lane) scaled by a power of two, taken apart into q_hi and
+  // q_lo and written in the 128-byte swizzled K-major layout; returns the row's
+  // factor.
+  auto put_row = [&](unsigned char* qs, int r, const uint2& w) -> float {
+    // (the largest of bit patterns: a NaN is the largest)
+    const uint32_t a0 = w.x & 0x7fff7fffu, a1 = w.y & 0x7fff7fffu;
+    const uint32_t top = __reduce_max_sync(
+        0xffffffffu, max(max(a0 & 0xffffu, a0 >> 16), max(a1 & 0xffffu, a1 >> 16)));
+    const int e = top == 0 ? 0 : min(7 + 127 - (int)(top >> 7), 127);  // rows times 2^e
+    // (infinities and NaN make the whole row NaN)
+    const float f = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2(e);
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const uint32_t x = c ? w.y : w.x;
+      const __half2 h = __floats2half2_rn(bf16lo(x) * f, bf16hi(x) * f);
+      hi[c] = h2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&h));
+      const uint32_t back = e4m3x2_to_h2(hi[c]);
+      const __half2 rest = __hmul2(__hsub2(h, *reinterpret_cast<const __half2*>(&back)), __float2half2_rn(32.f));
+      lo[c] = h2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&rest));
+    }
+    const int at = r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
+    *reinterpret_cast<uint32_t*>(qs + at) = hi[0] | hi[1] << 16;
+    *reinterpret_cast<uint32_t*>(qs + NR * 128 + at) = lo[0] | lo[1] << 16;
+    return p.scale_log2 * pow2(-e);
+  };
 
   if (warp == kPageKWarp || warp == kPageVWarp) {
     // ---------------- producers: K tiles, V tiles from pages (whole warps) ----------------
@@ -502,11 +532,11 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
       nx_entry = entry_of(p.pages, c.b, nx_key);
       nx_len = p.seqlens[c.b * p.sl_s];
     };
-    int64_t issued = 0;  // entries
+    int issued = 0;  // entries
     bool ok = true;
     int sub = 0;
     if (cur.t < t1) look_up(cur, 0);
-    for (int64_t g = 0; ok && cur.t < t1; ++g) {
+    for (int g = 0; ok && cur.t < t1; ++g) {
       const int row = nx_key & (p.pages.rows - 1);
       const int kvh = cur.kvh;
       // past the length, or no page: -1 (zeros)
@@ -516,8 +546,8 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
         cur.next(ntab, RG, Hkv, B);
       }
       if (cur.t < t1) look_up(cur, sub);
-      const int64_t seq = 2 * g + kv;  // (g counts subtiles)
-      const int s = (int)(seq % kSlots);
+      const int seq = 2 * g + kv;  // (g counts subtiles)
+      const int s = seq % kSlots;
       bool w = true;
       if (lane == 0) {
         if (seq >= kSlots) w = mbar_wait(&empty[s], (uint32_t)(((seq / kSlots) - 1) & 1));
@@ -541,8 +571,8 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
       // every issued copy must land before the CTA exits (an entry that has a
       // successor in its slot has: the successor waited for its consumption)
       const bool clean = ok;
-      const int64_t all = (issued + 1) / 2 * 2;  // entries of both producers
-      for (int64_t seq = issued - 1; seq >= 0 && seq >= all - kSlots - (clean ? 0 : kSlots); seq -= 2)
+      const int all = (issued + 1) / 2 * 2;  // entries of both producers
+      for (int seq = issued - 1; seq >= 0 && seq >= all - kSlots - (clean ? 0 : kSlots); seq -= 2)
         if (!mbar_wait(&full[seq % kSlots], (uint32_t)((seq / kSlots) & 1))) ok = false;
       if (!ok) {
         record_error(p.err, kErrTimeout);
@@ -603,14 +633,11 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
       }
       return y;
     };
-    Ask a1 = ask(), a2 = ask(), a3 = ask();
-    Bytes y0 = fetch(a1), y1 = fetch(a2);
-    a2 = a3;  // (the one to fetch next)
-    int64_t gs = 0;  // subtiles handed over
+    Ask a1 = ask(), a2 = ask();
+    Bytes y0, y1;
+    int gs = 0;  // subtiles handed over
     auto hand_over = [&]() -> bool {
-      const Ask ahead = ask();
-      const Bytes y2 = fetch(a2);
-      const int sr = (int)(gs % kScaleRing);
+      const int sr = gs % kScaleRing;
       bool w = true;
       if (lane == 0 && gs >= kScaleRing) w = mbar_wait(&sc_empty[sr], (uint32_t)((gs / kScaleRing - 1) & 1));
       if (!__shfl_sync(0xffffffffu, w, 0)) return false;
@@ -623,9 +650,10 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
       reinterpret_cast<uint4*>(s_sc + sr * BK)[lane] = make_uint4(word[0], word[1], word[2], word[3]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sc_full[sr]);
-      a2 = ahead;
+      // (only now: what is moved on has arrived)
       y0 = y1;
-      y1 = y2;
+      y1 = fetch(a2);
+      a2 = ask();
       ++gs;
       return true;
     };
@@ -657,13 +685,18 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
                    (int64_t)irow[h2] * p.q_si;
         if (real[h2]) pos[h2] = p.qpos[b * p.qp_sb + irow[h2] * p.qp_si];
       }
-      // query rows: 4 dims a lane, 8 rows in flight; each scaled by a power of two,
-      // taken apart into q_hi and q_lo and written in the 128-byte swizzled
-      // K-major layout (rows past the unit's end are zeros)
+      // query rows, 8 in flight (the first unit's are the key threads' work, which
+      // have nothing else to do yet: 13 us of the loader's for 48 rows of a cold
+      // cache), rows past the unit's end as zeros
       // (a loop: unrolled over 48 rows its code alone took 50 us of the first unit)
       float fac[2] = {0.f, 0.f};
+      if (uidx == 0) {
+        y0 = fetch(a1);
+        y1 = fetch(a2);
+        a2 = ask();
+      }
 #pragma unroll 1
-      for (int r0 = 0; r0 < NR; r0 += 8) {
+      for (int r0 = uidx == 0 ? NR : 0; r0 < NR; r0 += 8) {
         uint2 w[8];
         const bool high = r0 >= 32;
         const uintptr_t base = reinterpret_cast<uintptr_t>(high ? qrow[1] : qrow[0]);
@@ -676,32 +709,14 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int r = r0 + i;
-          // (the largest of bit patterns: a NaN is the largest)
-          const uint32_t a0 = w[i].x & 0x7fff7fffu, a1 = w[i].y & 0x7fff7fffu;
-          const uint32_t top = __reduce_max_sync(
-              0xffffffffu, max(max(a0 & 0xffffu, a0 >> 16), max(a1 & 0xffffu, a1 >> 16)));
-          const int e = top == 0 ? 0 : min(7 + 127 - (int)(top >> 7), 127);  // rows times 2^e
-          // (infinities and NaN make the whole row NaN)
-          const float f = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2(e);
-          uint32_t hi[2], lo[2];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint32_t x = c ? w[i].y : w[i].x;
-            const __half2 h = __floats2half2_rn(bf16lo(x) * f, bf16hi(x) * f);
-            hi[c] = h2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&h));
-            const uint32_t back = e4m3x2_to_h2(hi[c]);
-            const __half2 rest = __hmul2(__hsub2(h, *reinterpret_cast<const __half2*>(&back)), __float2half2_rn(32.f));
-            lo[c] = h2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&rest));
-          }
-          const int at = r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
-          *reinterpret_cast<uint32_t*>(qs + at) = hi[0] | hi[1] << 16;
-          *reinterpret_cast<uint32_t*>(qs + NR * 128 + at) = lo[0] | lo[1] << 16;
+          const float f = put_row(qs, r, w[i]);
           if (lane == (r & 31)) {
-            if (high) fac[1] = p.scale_log2 * pow2(-e);
-            else fac[0] = p.scale_log2 * pow2(-e);
+            if (high) fac[1] = f;
+            else fac[0] = f;
           }
         }
       }
+      if (uidx == 0) bar_sync(kBarFirst, kKeyThreads + 32);
       // integer facts of the rows
       const int len = len_raw < 0 ? 0 : (len_raw > p.Tmax ? p.Tmax : len_raw);
       RowFacts<NR>& rf = facts0[qb];
@@ -728,12 +743,15 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
           if (p.tree != nullptr && within > 0) nodes |= within < 64 ? tr & ((1ull << within) - 1) : tr;
           oo = (int64_t)b * p.o_sb + (int64_t)h * p.o_sh + (int64_t)i * p.o_si;
           lo = (int64_t)b * p.l_sb + (int64_t)h * p.l_sh + (int64_t)i * p.l_si;
-          umin = min(umin, e);
+          // (a row that sees nothing takes part in tiles without a mask, with scores of
+          // 0, and what comes of it is dropped: the tiles of its unit stay fast)
+          if (e > 0) umin = min(umin, e);
+          else fac[h2] = 0.f;
         }
         umax = max(umax, e);
         rf.end[r] = e;
         rf.tree[r] = tr;
-        rf.fac[r] = fac[h2];
+        if (uidx > 0 || e == 0) rf.fac[r] = fac[h2];
         rf.ooff[r] = oo;
         rf.loff[r] = lo;
       }
@@ -755,8 +773,8 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // Q rows -> tensor core
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[qb]);
-      const int64_t here = min((int64_t)(cur.n - cur.j), t1 - cur.t) * kSub;  // the unit's subtiles of this CTA
-      for (int64_t i = 0; ok && i < here; ++i) ok = hand_over();
+      const int here = min(cur.n - cur.j, t1 - cur.t) * kSub;  // the unit's subtiles of this CTA
+      for (int i = 0; ok && i < here; ++i) ok = hand_over();
       if (!ok) break;
     }
     if (!ok && lane == 0) {
@@ -771,7 +789,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
       // The S side runs one tile ahead of the U side.  Per tile only `left`
       // (the unit's tiles of this CTA still to come) counts down; the cursors
       // move from unit to unit.
-      auto tiles_here = [&](const Cursor& c) { return c.t < t1 ? (int)min((int64_t)(c.n - c.j), t1 - c.t) : 0; };
+      auto tiles_here = [&](const Cursor& c) { return c.t < t1 ? min(c.n - c.j, t1 - c.t) : 0; };
       Cursor cq = cur;  // unit of the next S product
       int left_q = tiles_here(cq), left = left_q;
       bool first_q = true, first = true;
@@ -885,6 +903,28 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
     auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity));
     };
+    if (cur.t < t1) {  // the first unit's query rows, a warp a row
+      constexpr int kOwn = NR / kKeyWarps;
+      static_assert(NR % kKeyWarps == 0, "rows of a warp");
+      uint2 w[kOwn];
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        const int r = warp + kKeyWarps * i, pk = cur.rg * R + r, g = pk / p.Tq;
+        w[i] = make_uint2(0, 0);
+        if (r < R && pk < rows_per_head)
+          w[i] = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.q) + (int64_t)cur.b * p.q_sb +
+                                                      (int64_t)(cur.kvh * p.G + g) * p.q_sh + (int64_t)(pk - g * p.Tq) * p.q_si) +
+                       lane);
+      }
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        const int r = warp + kKeyWarps * i;
+        const float f = put_row(sm + L::kOffQ, r, w[i]);
+        if (lane == 0) facts0[0].fac[r] = f;
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // Q rows -> tensor core
+      asm volatile("bar.arrive %0, %1;" ::"n"(kBarFirst), "n"(kKeyThreads + 32) : "memory");
+    }
     // R of a state at m as it is at a common m
     auto moved = [](float r, float m, float common) { return m == common ? r : r + (m - common); };
     float lp[NH];  // this thread's partial sums of P over its keys
@@ -892,11 +932,6 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
     for (int r = 0; r < NH; ++r) lp[r] = 0.f;
     int uidx = 0;
     bool ok = true;
-    const int64_t slots = (int64_t)gridDim.x + (int64_t)B * Hkv * RG;
-    float* ws_m = p.ws;
-    float* ws_l = ws_m + slots * R;
-    float* ws_r = ws_l + slots * R;
-    float* ws_u = ws_m + (3 * slots * R + 3) / 4 * 4;
     auto put_out = [&](int64_t at, float o) { static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(o); };
     // A finished unit's U is read one tile later, after the next tile's P: by then
     // its last product has completed and the readout does not stall the pipeline.
@@ -904,7 +939,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
     // the readout releases them.
     bool pend = false;
     int pend_uidx = 0, pend_b = 0, pend_kvh = 0, pend_rg = 0, pend_n = 1;
-    int64_t pend_su = 0;
+    int pend_su = 0;
     auto flush = [&]() -> bool {
       const int pb = pend_uidx & 1;
       const RowFacts<NR>& pf = facts0[pb];
@@ -915,17 +950,21 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
         const uint32_t ua = tl + L::kColU + L::kStepU * (uint32_t)pb + c0;
         ld_cols<NH>(ua + (kPieces - 1) * NR, u);
 #pragma unroll
-        for (int c = kPieces - 2; c >= 0; --c) {  // U = U_1 + (U_2 + ..) / 16
+        for (int c = kPieces - 2; c >= 0; --c) {  // U = U_1 + (U_2 + ..) / 2^8
           float hi[NH];
           ld_cols<NH>(ua + c * NR, hi);
 #pragma unroll
-          for (int r = 0; r < NH; ++r) u[r] = fmaf(u[r], 0.0625f, hi[r]);
+          for (int r = 0; r < NH; ++r) u[r] = fmaf(u[r], c > 0 ? 1.f : 0x1p-8f, hi[r]);
         }
       }
       const int64_t unit = ((int64_t)pend_b * Hkv + pend_kvh) * RG + pend_rg;
-      const int64_t cf = cta_of(pend_su, W, P_work);
-      const int64_t cl = cta_of(pend_su + pend_n - 1, W, P_work);
-      const int nparts = (int)(cl - cf + 1);
+      const int cf = cta_of(pend_su, W, P_work);
+      const int nparts = cta_of(pend_su + pend_n - 1, W, P_work) - cf + 1;
+      const int64_t slots = (int64_t)gridDim.x + (int64_t)B * Hkv * RG;
+      float* ws_m = p.ws;
+      float* ws_l = ws_m + slots * R;
+      float* ws_r = ws_l + slots * R;
+      float* ws_u = ws_m + (3 * slots * R + 3) / 4 * 4;
       const int rr = min(R, rows_per_head - pend_rg * R);  // real rows of the unit
       if (nparts == 1) {
 #pragma unroll
@@ -1045,7 +1084,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
       return m;
     };
     uint32_t kslot = 2 * sub, kphase = 0;  // ring slot of the current K subtile and its phase
-    for (int64_t g = 0; cur.t < t1; cur.next(ntab, RG, Hkv, B), ++g) {
+    for (int g = 0; cur.t < t1; cur.next(ntab, RG, Hkv, B), ++g) {
       const bool first = cur.t == t0 || cur.j == 0;
       const bool last = cur.t == t1 - 1 || cur.j == cur.n - 1;
       const int ub = uidx & 1;
@@ -1061,7 +1100,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
       }
       const int key0 = cur.key0();
       const int sub0 = key0 + sub * BK, key = sub0 + k;
-      const int64_t gs = kSub * g + sub;  // the subtile, of this CTA's
+      const int gs = kSub * g + sub;  // the subtile, of this CTA's
       float x[NH];
       float ks = 0.f, ev = kNegInf;  // the key's scales: 2^ks', 2^ev
       bool sok = wait_all(&sc_full[gs % kScaleRing], (uint32_t)((gs / kScaleRing) & 1));
@@ -1108,14 +1147,18 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
         const uint32_t sa = tl + L::kColS + L::kStepS * (uint32_t)(g & 1) + L::kSubS * sub + c0;
         ld_cols<NH>(sa, x);
         ld_cols<NH>(sa + NR, lo);
+        const float2 low = make_float2(0.03125f, 0.03125f), ks2 = make_float2(ks, ks);
 #pragma unroll
         for (int r4 = 0; r4 < NH / 4; ++r4) {
           const float4 f4 = reinterpret_cast<const float4*>(rf.fac + c0)[r4];
-          const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+          const float2 fc[2] = {make_float2(f4.x, f4.y), make_float2(f4.z, f4.w)};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = 4 * r4 + e;
-            x[r] = fmaf(lo[r], 0.03125f, x[r]) * (ks * f[e]);
+          for (int e = 0; e < 2; ++e) {
+            const int r = 4 * r4 + 2 * e;
+            const float2 v = __ffma2_rn(make_float2(lo[r], lo[r + 1]), low, make_float2(x[r], x[r + 1]));
+            const float2 xx = __fmul2_rn(v, __fmul2_rn(ks2, fc[e]));
+            x[r] = xx.x;
+            x[r + 1] = xx.y;
           }
         }
         // (every row sees every key of the subtile: no mask)
@@ -1207,7 +1250,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
         if (!first) {
           // U^T lane k = value dim k, the group's columns of all pieces; the product
           // with P_{j-1} must have completed (U += P_j V_j waits for this tile's P)
-          const int64_t pv_seq = 2 * kSub * g - 1;  // V_{j-1}, its last subtile
+          const int pv_seq = 2 * kSub * g - 1;  // V_{j-1}, its last subtile
           const bool done = wait_all(&empty[pv_seq % kSlots], (uint32_t)((pv_seq / kSlots) & 1));
           const bool pv = bar_and(kBarRows, kKeyThreads, done);
           if (!pv) { ok = false; break; }  // (both loops)
@@ -1225,29 +1268,23 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
         }
       }
       if (!ok) break;
-      // ---- P^T row of key k, the group's rows: the weights' pieces ----
+      // ---- P^T row of key k, the group's rows: the weights' pieces, exact ----
       {
         unsigned char* ph = sm + L::kOffP + (int)(g & 1) * L::kPBytes + sub * L::kPSub + k * 128;
 #pragma unroll
         for (int r = 0; r < NH; ++r) lp[r] += pr[r];
-        const __half2 sixteen = __float2half2_rn(16.f);
-        // (a loop, with the last piece's rest for nothing: the code of a tile should stay
-        // in the instruction caches)
-#pragma unroll 1
-        for (int c = 0; c < kPieces; ++c) {
-          uint32_t by[NH / 4];  // four rows a word
 #pragma unroll
-          for (int i = 0; i < NH / 4; ++i) {
-            const uint32_t b0 = h2_to_e4m3x2(w2[2 * i]), b1 = h2_to_e4m3x2(w2[2 * i + 1]);
-            by[i] = b0 | b1 << 16;
-            {  // the rest, exact, for the next piece
-              const uint32_t v0 = e4m3x2_to_h2(b0), v1 = e4m3x2_to_h2(b1);
-              const __half2 r0 = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&w2[2 * i]),
-                                                 *reinterpret_cast<const __half2*>(&v0)), sixteen);
-              const __half2 r1 = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&w2[2 * i + 1]),
-                                                 *reinterpret_cast<const __half2*>(&v1)), sixteen);
-              w2[2 * i] = *reinterpret_cast<const uint32_t*>(&r0);
-              w2[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&r1);
+        for (int c = 0; c < kPieces; ++c) {
+          uint32_t by[NH / 4];  // the upper bytes, four rows a word
+#pragma unroll
+          for (int i = 0; i < NH / 4; ++i) by[i] = __byte_perm(w2[2 * i], w2[2 * i + 1], 0x7531);
+          if (c < kPieces - 1) {
+#pragma unroll
+            for (int i = 0; i < NH / 2; ++i) {  // the rest
+              const uint32_t top = w2[i] & 0xff00ff00u;
+              __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&w2[i]), *reinterpret_cast<const __half2*>(&top));
+              if (c == 0) rest = __hmul2(rest, __float2half2_rn(256.f));
+              w2[i] = *reinterpret_cast<const uint32_t*>(&rest);
             }
           }
           const int n0 = c * NR + c0;  // column of the first row
@@ -1266,7 +1303,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
       }
       if ((cur.j == cur.n - 1 && key0 + TK > rf.unit_end) || key0 < rf.unit_start || key0 + TK > rf.tree_base) {
         // zero the V rows that no row sees (one group of each subtile)
-        const int64_t sv = 2 * gs + 1;
+        const int sv = 2 * gs + 1;
         const bool vok = bar_and(kBarRows, kKeyThreads, wait_all(&full[sv % kSlots], (uint32_t)((sv / kSlots) & 1)));
         if (!vok) { ok = false; break; }
         if (unseen(rf, key) && part == 0) {
@@ -1307,6 +1344,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
           float l = red[k];
 #pragma unroll
           for (int w = 1; w < kRed; ++w) l += red[w * NR + k];
+          if (rf.end[k] == 0) l = 0.f;  // (sees nothing)
           // (a NaN among a row's scores, which no maximum shows, is in the sum)
           s_mfin[k] = s_m[k];
           s_lfin[k] = l;

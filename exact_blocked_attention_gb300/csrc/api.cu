@@ -1166,8 +1166,9 @@ int fwd_paged_q8_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages, c
   int64_t nb = c.B;
   Q8Plan pl;
   // tcgen05: heads of 128, bf16 results, contiguous query rows, tables of more than
-  // 256 keys (256: 1 x 32 rows 12 us with mma.sync and 16 with tcgen05, 2 x 5 rows of
-  // 64 heads 18 and 31; 1000: 16 and 18, 43 and 35; 4000 x 32 sequences 90 and 61),
+  // 256 keys (64 keys: 8 x 4 rows 10 us with mma.sync and 14 with tcgen05, 32 sequences
+  // of them 14 and 20; 256: 12 and 14, 18 and 20; 1000: 16 and 16, 41 and 37; 4000: 18
+  // and 20, 92 and 61; five-row chains of 64 heads 43 and 25 at 1000, 80 and 53 at 16000),
   // as many sequences a launch as the kernel takes
   bool tc = c.d == 128 && out->dtype == BLKATTN_BF16 && c.q_vec_ok && c.Tmax > 256;
   if (const char* force = std::getenv("BLKATTN_KERNEL")) tc = tc && std::strcmp(force, "mma") != 0;  // comparison runs only

@@ -16,11 +16,11 @@
 // byte is the first (its value cut to 3 bits), the rest times 2^8 has 8 bits, its
 // upper byte is the second, and so on; U = U_1 + (U_2 + U_3 + U_4) / 2^8.  An f16's
 // step is 2^-23 of the row's largest weight or finer.  (Pieces of e4m3, two
-// conversions each and room for weights to 2^8 only: five-row chains of 64 heads
-// 129 us, 118 so.)
+// conversions each and room for weights to 2^8 only, took five-row chains of 64
+// heads 129 us where these took 118.)
 // With k = 2^ek k8 and v = 2^ev v8: x = (S_hi + S_lo / 32) 2^ek fac_row, and the
-// weight is 2^(x - m + ev - r), of two references a row: m >= max x - 8 for the
-// sum of fp32 weights, and r >= max (x - m + ev) - 4 for the product's (r relative
+// weight is 2^(x - m + ev - r), of two references a row: m >= max x for the
+// sum of fp32 weights, and r >= max (x - m + ev) - 7 for the product's (r relative
 // to m: beside a large x, ev would be lost).
 //
 // Otherwise the kernel is the one of decode_tc.cu over pages: the same cut of
@@ -29,7 +29,7 @@
 //
 // What bounds it: memory for up to 16 rows once the stream runs (5.8 TB/s; 11 us of
 // cold latency before), for more the key threads' arithmetic on the scores (40
-// rows: 113 us where the bytes take 42).
+// rows: 117 us where the bytes take 42).
 //
 // Every wait is bounded (%globaltimer); on a timeout the CTA records the error
 // word, stops issuing work, lets its own copies and products drain and frees
@@ -47,13 +47,15 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
-// m is set 2^16 above the largest score so far (the sum of fp32 weights loses
-// nothing by it) and rises when one passes it by 2^8.
-constexpr float kLazyM = 8.f, kMarginM = 16.f;
+// m is set 2^24 above the largest score so far (the sum of fp32 weights loses
+// nothing by it) and rises when one passes it.
+constexpr float kMarginM = 24.f;
+// r stays above: 2^(kLift - r) is a float.  (Values all below 2^-100 448 lose bits.)
+constexpr float kLeastR = -120.f;
 // A weight at the reference is 2^kLift, and the reference is set 2^kMargin above
 // the largest weight so far: there is room for a maximum 2^12 above that before the
 // reference has to rise, which costs a tile 2.5 us (with room for 2^6 ten tiles of
-// 57 raised one of 40 rows').  kMostW: the largest whose rest times 2^8 is an f16.
+// 57 raised one of 40 rows', with this four).  kMostW: the largest whose rest times 2^8 is an f16.
 constexpr float kLift = 4.f, kMargin = 5.f;
 constexpr float kMostW = 2047.f;
 
@@ -108,7 +110,7 @@ struct TcLayout {
   // own: what a tile takes is a chain of waits, loads and a vote, some 1.5 us
   // whatever its size.  More rows: 128 keys.
   // (12 key warps of 16 rows each for 48, not 8 of 24: 157 us in place of 190
-  // for five-row chains of 64 heads at the time; 113 now)
+  // for five-row chains of 64 heads when it was tried)
   static constexpr int kSub = NR <= 16 ? 2 : 1;
   static constexpr int kParts = NR == 8 ? 1 : (NR == 16 ? 2 : (NR == 32 ? 2 : 3));
   static constexpr int kKeyWarps = 4 * kSub * kParts;        // a warp a TMEM lane quarter, subtile and part of the rows
@@ -135,10 +137,10 @@ struct TcLayout {
   static constexpr int kRowsBytes = (int)((sizeof(RowFacts<NR>) + 15) / 16 * 16);
   static constexpr int kOffNTab = kOffRows + 2 * kRowsBytes;     // uint16 tiles, first tile per (sequence, row group)
   static constexpr int kOffRed = kOffNTab + 2 * kDecodeTcMaxEntries * 2;  // float [8][NR]
-  // float [NR] each: m, m_use, thr, r, 2^(lift - r), factor of l, factor of U of the
+  // float [NR] each: m, m_use, r, 2^(lift - r), factor of l, factor of U of the
   // current unit; m, l, r, 1 / l of the finished unit whose U readout is pending
   static constexpr int kOffStat = kOffRed + 8 * NR * 4;
-  static constexpr int kOffScale = kOffStat + 11 * NR * 4;       // uint32 [kScaleRing][BK]: each key's scale bytes
+  static constexpr int kOffScale = kOffStat + 10 * NR * 4;       // uint32 [kScaleRing][BK]: each key's scale bytes
   static constexpr int kOffBar = kOffScale + kScaleRing * BK * 4;
   // full[kSlots], empty[kSlots], q_full[2], q_empty[2], p_full[2], u_full[2], drain, sc_full[kScaleRing], sc_empty[kScaleRing]
   static constexpr int kNumBars = 2 * kSlots + 2 + 2 + 2 + 2 + 1 + 2 * kScaleRing;
@@ -283,15 +285,14 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
   float* red = reinterpret_cast<float*>(sm + L::kOffRed);
   float* s_m = reinterpret_cast<float*>(sm + L::kOffStat);  // reference maximum, -inf = none yet
   float* s_muse = s_m + NR;                                  // m, or 0 when none yet
-  float* s_thr = s_m + 2 * NR;                               // m + 8, -inf when none yet
-  float* s_r = s_m + 3 * NR;                                 // reference of the weights, -inf = none yet
-  float* s_h = s_m + 4 * NR;                                 // 2^(lift - r), 1 when none yet
-  float* s_alpha = s_m + 5 * NR;
-  float* s_beta = s_m + 6 * NR;
-  float* s_mfin = s_m + 7 * NR;
-  float* s_lfin = s_m + 8 * NR;
-  float* s_rfin = s_m + 9 * NR;
-  float* s_inv = s_m + 10 * NR;
+  float* s_r = s_m + 2 * NR;                                 // reference of the weights, -inf = none yet
+  float* s_h = s_m + 3 * NR;                                 // 2^(lift - r), 1 when none yet
+  float* s_alpha = s_m + 4 * NR;
+  float* s_beta = s_m + 5 * NR;
+  float* s_mfin = s_m + 6 * NR;
+  float* s_lfin = s_m + 7 * NR;
+  float* s_rfin = s_m + 8 * NR;
+  float* s_inv = s_m + 9 * NR;
   uint32_t* s_sc = reinterpret_cast<uint32_t*>(sm + L::kOffScale);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kOffBar);
   uint64_t* full = bars;
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
     if (threadIdx.x < NR) {
       s_m[threadIdx.x] = kNegInf;
       s_muse[threadIdx.x] = 0.f;
-      s_thr[threadIdx.x] = s_r[threadIdx.x] = kNegInf;
+      s_r[threadIdx.x] = kNegInf;
       s_h[threadIdx.x] = 1.f;
     }
     if (warp == kMmaWarp) {
@@ -1120,11 +1121,15 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
         sok = wait_all(&empty[kslot], kphase);
       }
       bool trig = !sok;
-      const float f = ev == kNegInf ? 0.f : fast_exp2(ev);  // (2^-127: 0 beside any other)
+      // 2^ev in two factors, around the row's 2^(lift - r): whatever the exponents are,
+      // the weights between stay in fp32's range (five-row chains of 64 heads 110 us with
+      // one factor, 117 so)
+      const float half = floorf(0.5f * ev);
+      const float f1 = ev == kNegInf ? 0.f : fast_exp2(half), f2 = ev == kNegInf ? 0.f : fast_exp2(ev - half);
       float pr[NH];         // the weights e^z at m's reference
       uint32_t w2[NH / 2];  // with the values' scales, at r's, pairs of rows as f16
       auto weigh = [&]() {
-        const float2 f2v = make_float2(f, f), neg = make_float2(-1.f, -1.f);
+        const float2 fa = make_float2(f1, f1), fb = make_float2(f2, f2), neg = make_float2(-1.f, -1.f);
 #pragma unroll
         for (int r4 = 0; r4 < NH / 4; ++r4) {
           const float4 m4 = reinterpret_cast<const float4*>(s_muse + c0)[r4];
@@ -1138,8 +1143,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
             const float2 pp = make_float2(fast_exp2(z.x), fast_exp2(z.y));  // masked: 2^-inf = 0
             pr[r] = pp.x;
             pr[r + 1] = pp.y;
-            // (p 2^ev <= 2^(r + 1) first: its product with 2^(lift - r) stays in range)
-            const float2 w = __fmul2_rn(__fmul2_rn(pp, f2v), h[e]);
+            const float2 w = __fmul2_rn(__fmul2_rn(__fmul2_rn(pp, fa), h[e]), fb);
             const __half2 h2 = __floats2half2_rn(w.x, w.y);
             w2[r / 2] = *reinterpret_cast<const uint32_t*>(&h2);
           }
@@ -1187,7 +1191,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
         if (again) break;
 #pragma unroll
         for (int r4 = 0; r4 < NH / 4; ++r4) {
-          const float4 t4 = reinterpret_cast<const float4*>(s_thr + c0)[r4];
+          const float4 t4 = reinterpret_cast<const float4*>(s_m + c0)[r4];
           trig |= (x[4 * r4] > t4.x) | (x[4 * r4 + 1] > t4.y) | (x[4 * r4 + 2] > t4.z) | (x[4 * r4 + 3] > t4.w);
         }
         if (trig) misc[4 + (int)(g & 1)] = 1;  // m has to rise (read after the vote's barrier)
@@ -1206,13 +1210,12 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
             const float tmax = red_max(k);
             const float mo = s_m[k];
             float a = 1.f;
-            if (tmax > s_thr[k]) {
+            if (tmax > mo) {
               const float mn = tmax + kMarginM;
               a = mo == kNegInf ? 1.f : fast_exp2(mo - mn);  // a row with no key yet has l = u = 0
               s_r[k] = mo == kNegInf ? kNegInf : s_r[k] + (mo - mn);
               s_m[k] = mn;
               s_muse[k] = mn;
-              s_thr[k] = mn + kLazyM;
             }
             s_alpha[k] = a;
           }
@@ -1230,14 +1233,13 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
           const float ymax = red_max(k), ro = s_r[k];
           float bt = 1.f, rn = ro;
           // (r fell with m: what it may rise to is measured from there)
-          if (ymax > ro) {
-            rn = ymax + kMargin;
-            bt = ro == kNegInf ? 1.f : fast_exp2(ro - rn);
-          }
+          if (ymax > ro) rn = ymax + kMargin;
+          if (rn != kNegInf) rn = fmaxf(rn, kLeastR);
+          if (rn != ro) bt = ro == kNegInf ? 1.f : fast_exp2(ro - rn);
           // U's reference in absolute terms moved by bt, and not by m's step
           s_r[k] = rn;
-          // 2^(lift - r) as a factor; |r| < 127 + 127 + 8
-          s_h[k] = rn == kNegInf ? 1.f : fast_exp2(fminf(fmaxf(kLift - rn, -126.f), 126.f));
+          // (z <= 0 and ev <= 127: r <= 132, and only where numbers pass fp32's range over 125)
+          s_h[k] = rn == kNegInf ? 1.f : fast_exp2(fmaxf(kLift - rn, -126.f));
           s_beta[k] = bt;
         }
         bar_sync(kBarRows, kKeyThreads);
@@ -1357,7 +1359,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
           // fresh statistics for the next unit
           s_m[k] = kNegInf;
           s_muse[k] = 0.f;
-          s_thr[k] = s_r[k] = kNegInf;
+          s_r[k] = kNegInf;
           s_h[k] = 1.f;
         }
         bar_sync(kBarRows, kKeyThreads);

@@ -567,7 +567,8 @@ int blkattn_paged_read_q8(const blkattn_tensor* pos, const blkattn_tensor* page_
  * pools and its scales may hold anything.
  * Precision: the cache's numbers are exact, sums and statistics fp32.  Weights
  * enter the value product with f16's 11 bits for a bf16 out and 22 bits for an
- * f32 out, and vanish below 2^-36 of the row's largest weight times scale.  With
+ * f32 out, and vanish below 2^-36 of the row's largest weight times scale (with
+ * scales of 2^-100 and less throughout, sooner).  With
  * a bf16 out and d = 128 (over tables of more than 256 rows, of contiguous query
  * rows) weights have an absolute step too, 2^-23 of that largest product, and a
  * query row's dims one of 2^-22 of its largest dim.  Prompts (T_q >= 64, no tree, 16-byte

@@ -123,6 +123,18 @@ def test_rows_of_any_size_and_nan():
     assert torch.equal(out[0, :, 0], clean[0][0, :, 0]) and torch.equal(lse[0, :, 0], clean[1][0, :, 0])
 
 
+@pytest.mark.parametrize("Hq", [4, 40])
+@pytest.mark.parametrize("byte", [40, 80, 127, 200, 235])
+def test_all_values_small_or_large(byte, Hq):
+    """Scales of V of 2^-87 to 2^108 throughout: weights go relative to the row's own."""
+    a = make(1, Hq, 1, 1, 128, 16, 16, [1600], spread=0)
+    a["vs"].view(U8)[a["vs"].view(U8) < 255] = byte
+    check(a, call(a, BF16), BF16)
+    check(a, call(a, F32), F32)
+    a["q"] = a["q"] * 20  # (scores that rise by hundreds)
+    check(a, call(a, BF16), BF16)
+
+
 def test_batches_cut_into_launches():
     lens = [(i * 53) % 300 for i in range(1300)]
     a = make(1300, 2, 1, 1, 128, 8, 8, lens, entries=40)

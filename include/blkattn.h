@@ -568,14 +568,14 @@ int blkattn_paged_read_q8(const blkattn_tensor* pos, const blkattn_tensor* page_
  * Precision: the cache's numbers are exact, sums and statistics fp32.  Weights
  * enter the value product with f16's 11 bits for a bf16 out and 22 bits for an
  * f32 out, and vanish below 2^-36 of the row's largest weight times scale (with
- * scales of 2^-100 and less throughout, sooner).  With
- * a bf16 out and d = 128 (over tables of more than 256 rows, of contiguous query
- * rows) weights have an absolute step too, 2^-23 of that largest product, and a
- * query row's dims one of 2^-22 of its largest dim.  Prompts (T_q >= 64, no tree, 16-byte
- * aligned contiguous rows, scale > 0) go through the kernel of
- * blkattn_fwd_paged and have its precision.  A row with a NaN or an infinity in q, or a NaN
- * among the scores of its visible keys, gives NaN in out and lse; the other
- * rows are not touched by it.
+ * scales of 2^-100 and less throughout, sooner).  With a bf16 out and d = 128
+ * (over tables of more than 256 rows, of 16-byte aligned contiguous query rows)
+ * weights have an absolute step too, 2^-23 of that largest product, and a query
+ * row's dims one of 2^-22 of its largest dim.  Prompts (T_q >= 64, no tree,
+ * 16-byte aligned contiguous rows, scale > 0) go through the kernel of
+ * blkattn_fwd_paged and have its precision.  A row with a NaN in q, or among
+ * the scores of its visible keys, gives NaN in out and lse; the other rows are
+ * not touched by it.  (An infinity in q may count as a NaN.)
  * Workspace, growth and overlap of calls as for blkattn_fwd.  For prompts the
  * library also keeps a bf16 copy of the pages that the call's tables can name:
  * up to 2 GiB for a slice of the sequences, up to 16 GiB where one sequence

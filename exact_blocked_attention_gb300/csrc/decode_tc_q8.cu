@@ -52,12 +52,16 @@ constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kMarginM = 24.f;
 // r stays above: 2^(kLift - r) is a float.  (Values all below 2^-100 448 lose bits.)
 constexpr float kLeastR = -120.f;
+// And below kMostR, so that 2^(kLift - r) stays a float, not a subnormal one: a
+// product's largest is 2^127 (x <= m, ev <= 127), 2^(kLift + 127 - kMostR) = 2 then.
+constexpr float kMostR = 130.f;
 // A weight at the reference is 2^kLift, and the reference is set 2^kMargin above
 // the largest weight so far: there is room for a maximum 2^12 above that before the
 // reference has to rise, which costs a tile 2.5 us (with room for 2^6 ten tiles of
 // 57 raised one of 40 rows', with this four).  kMostW: the largest whose rest times 2^8 is an f16.
 constexpr float kLift = 4.f, kMargin = 5.f;
 constexpr float kMostW = 2047.f;
+static_assert(kMostR == kLift + 126.f, "2^(kLift - kMostR) is the least normal float");
 
 constexpr int D = 128;
 constexpr int BK = 128;               // keys of a product (TMEM lanes of S^T)
@@ -1234,12 +1238,11 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
           float bt = 1.f, rn = ro;
           // (r fell with m: what it may rise to is measured from there)
           if (ymax > ro) rn = ymax + kMargin;
-          if (rn != kNegInf) rn = fmaxf(rn, kLeastR);
+          if (rn != kNegInf) rn = fminf(fmaxf(rn, kLeastR), kMostR);
           if (rn != ro) bt = ro == kNegInf ? 1.f : fast_exp2(ro - rn);
           // U's reference in absolute terms moved by bt, and not by m's step
           s_r[k] = rn;
-          // (z <= 0 and ev <= 127: r <= 132, and only where numbers pass fp32's range over 125)
-          s_h[k] = rn == kNegInf ? 1.f : fast_exp2(fmaxf(kLift - rn, -126.f));
+          s_h[k] = rn == kNegInf ? 1.f : fast_exp2(kLift - rn);
           s_beta[k] = bt;
         }
         bar_sync(kBarRows, kKeyThreads);

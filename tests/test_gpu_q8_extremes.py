@@ -1,0 +1,54 @@
+"""The 8-bit cache at the ends of its exponents and over long tails.  Bounds as
+in test_gpu_paged_q8.py where nothing else is said."""
+import math
+
+import pytest
+import torch
+
+from exact_blocked_attention_gb300 import blkattn
+
+from test_gpu_paged_q8 import BF16, E8, F32, F64, F8, I32, U8, call, check, make
+from test_gpu_rotary import dev
+
+pytestmark = pytest.mark.gpu
+
+
+def paged(x, S, byte, P=16):
+    """Rows x [B, Hkv, n, d] of e4m3's numbers as (pool, scales) in table order, n a multiple of P; `byte` the scale
+    of each row (of each block: its first row's)."""
+    B, H, n, d = x.shape
+    pool = x.view(B, H, n // P, P, d).transpose(1, 2).reshape(B * n // P, H, P, d).to(F8).contiguous()
+    scale = byte.view(B, H, n // P, P // S, S)[..., 0].transpose(1, 2).reshape(B * n // P, H, P // S)
+    return pool, scale.to(U8).contiguous().view(E8)
+
+
+def problem(k, v, kb, vb, q, S, scale, P=16):
+    B, H, n, d = k.shape
+    kp, ks = paged(k, S, kb, P)
+    vp, vs = paged(v, S, vb, P)
+    table = torch.arange(B * n // P, dtype=I32, device=k.device).view(B, n // P)
+    T = q.shape[2]
+    pos = (n - T + torch.arange(T, device=k.device, dtype=I32)).expand(B, T).contiguous()
+    return dict(q=q.to(BF16), kp=kp, ks=ks, vp=vp, vs=vs, table=table,
+                lens=torch.full((B,), n, dtype=I32, device=k.device), pos=pos, scale=scale, tree=None, window=0)
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("G", [1, 12, 40])
+@pytest.mark.parametrize("byte", [250, 253, 254])
+def test_largest_scales_of_values(byte, G, out):
+    """V's scales up to 2^127, and scores (base 2: scale is ln 2) that rise by 20 to 24 after a CTA's first tiles: both
+    references of a row at the top of their range."""
+    g = torch.Generator(device=dev()).manual_seed(G)
+    B, H, n, d = 16, 8, 2560, 128
+    k = torch.zeros(B, H, n, d, device=dev())
+    for h in range(H):
+        for tile, t in (((7, 24.0),), ((3, 22.0), (7, 24.0)), ((3, 20.0), (5, 22.0), (7, 24.0)), ((6, 23.5),))[h % 4]:
+            k[:, h, 256 * tile + 100, 0] = min(t, 16)
+            k[:, h, 256 * tile + 100, 1] = max(t - 16, 0)
+    v = (torch.randn(B, H, n, d, generator=g, device=dev()) / 8).clamp(-0.5, 0.5)
+    q = torch.zeros(B, H * G, 1, d, device=dev())
+    q[..., :2] = 1
+    a = problem(k, v, torch.full((B, H, n), 127, device=dev()), torch.full((B, H, n), byte, device=dev()), q, 16,
+                math.log(2.0))
+    check(a, call(a, out), out)

@@ -48,6 +48,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLazyM = 8.f, kLazyR = 4.f;
 constexpr float kLift = 11.f;  // weights reach 2^(kLift + kLazyR) = 2^15 in f16
+constexpr int kMostUp = 110;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kOwn = 32;               // keys of a warp in a tile: two products of 16, side by side
@@ -300,7 +301,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_q8_kernel(co
     max_first = 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      // the fragments of row 8 nt + g, scaled by a power of two into f16's upper range
+      // the fragments of row 8 nt + g, scaled by a power of two into f16's upper range,
+      // but by 2^kMostUp at most: what every bf16 needs to be a number of f16 (2^-133 is
+      // 2^-23 then, f16's step 2^-24), and 2^-kMostUp times a scale is a normal float
       const int r = 8 * nt + g;
       float x[KL][16];
       float amax = 0.f;
@@ -328,16 +331,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_q8_kernel(co
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       const int e = amax > 0.f ? (int)(__float_as_uint(amax) >> 23) - 127 : 14;
-      // (two factors: 14 - e may pass 127; inf and NaN pass through)
-      const float f1 = pow2((14 - e) / 2), f2 = pow2((14 - e) - (14 - e) / 2);
+      const int up = min(14 - e, kMostUp);  // (inf and NaN pass through)
+      const float f = pow2(up);
 #pragma unroll
       for (int c = 0; c < KL; ++c)
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          Q[nt][4 * c + s][0] = pack_h2(x[c][4 * s] * f1 * f2, x[c][4 * s + 1] * f1 * f2);
-          Q[nt][4 * c + s][1] = pack_h2(x[c][4 * s + 2] * f1 * f2, x[c][4 * s + 3] * f1 * f2);
+          Q[nt][4 * c + s][0] = pack_h2(x[c][4 * s] * f, x[c][4 * s + 1] * f);
+          Q[nt][4 * c + s][1] = pack_h2(x[c][4 * s + 2] * f, x[c][4 * s + 3] * f);
         }
-      const float back = p.scale_log2 * pow2(e - 14);
+      const float back = p.scale_log2 * pow2(-up);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int rr = 8 * nt + 2 * t4 + c;

@@ -52,3 +52,15 @@ def test_largest_scales_of_values(byte, G, out):
     a = problem(k, v, torch.full((B, H, n), 127, device=dev()), torch.full((B, H, n), byte, device=dev()), q, 16,
                 math.log(2.0))
     check(a, call(a, out), out)
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("d,G", [(64, 1), (64, 12), (128, 4), (128, 40)])
+def test_small_rows_beside_large_keys(d, G, out):
+    """Query rows of 2^-110 to 2^-133 and keys whose scales make their scores ordinary numbers again."""
+    for e in (-110, -114, -120, -126, -130, -133):
+        a = make(2, G, 1, 1, d, 16, 16, [200, 700], spread=0, seed=-e)
+        a["ks"].view(U8)[a["ks"].view(U8) < 255] = min(254, 127 - e - 7)
+        a["q"] = (a["q"].float().sign() * 2.0 ** (e + 60) * 2.0 ** -60).to(BF16)
+        assert bool((a["q"] != 0).any())
+        check(a, call(a, out), out)

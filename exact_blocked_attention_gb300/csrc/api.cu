@@ -36,7 +36,8 @@ struct DeviceState {
   size_t ws_bytes = 0;
   // an 8-bit cache's pages as bf16, for the prompt kernel
   void* pages = nullptr;
-  size_t pages_bytes = 0;
+  int64_t pages_bytes = 0;
+  int64_t pages_refused = INT64_MAX;  // the least size that found no memory, and none as large has since
   // per-unit counters of the tcgen05 decode kernel: zeroed when allocated,
   // left zero by every launch
   unsigned* cnt = nullptr;
@@ -429,6 +430,11 @@ bool out_tma_ok(const blkattn_tensor* out) {
 // the current buffer.
 // Growing while the stream is being captured is refused (a capture may not
 // allocate).
+bool no_memory(cudaError_t e) {
+  if (e != cudaErrorMemoryAllocation) return false;
+  cudaGetLastError();  // (not the error of a call that may still succeed)
+  return true;
+}
 int grow_stream_ordered(void** buf, size_t* have, size_t bytes, cudaStream_t stream) {
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
   if (cudaError_t e = cudaStreamIsCapturing(stream, &cs); e != cudaSuccess) return cuda_fail(e);
@@ -436,17 +442,40 @@ int grow_stream_ordered(void** buf, size_t* have, size_t bytes, cudaStream_t str
   void* grown = nullptr;
   size_t got = 0;
   const cudaError_t e = blkattn::grow_scratch(
-      *have, bytes, [&](size_t n) { return cudaMallocAsync(&grown, n, stream); },
-      [](cudaError_t failed) {
-        if (failed != cudaErrorMemoryAllocation) return false;
-        cudaGetLastError();  // (not the error of a call that may still succeed)
-        return true;
-      },
-      &got);
+      *have, bytes, [&](size_t n) { return cudaMallocAsync(&grown, n, stream); }, no_memory, &got);
   if (e != cudaSuccess) return cuda_fail(e);
   *buf = grown;
   *have = got;
   return BLKATTN_OK;
+}
+
+// The buffer for slices of an 8-bit cache's pages as bf16 (scratch.h: fit_slices),
+// 2 GiB at most; slice->seqs = 0: none fits.
+constexpr int64_t kCopyBytes = 2LL << 30;
+int ensure_copy(DeviceState* s, int64_t B, int64_t H, int64_t seq, int64_t head, cudaStream_t stream,
+                blkattn::Slice* slice) {
+  constexpr cudaError_t captured = cudaErrorStreamCaptureUnsupported;
+  cudaError_t failed;
+  *slice = blkattn::fit_slices(
+      B, H, seq, head, kCopyBytes, &s->pages_bytes,
+      [&](int64_t n) {
+        cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+        if (cudaError_t e = cudaStreamIsCapturing(stream, &cs); e != cudaSuccess) return e;
+        // (a captured call does what the same call before it did)
+        if (cs != cudaStreamCaptureStatusNone) return n >= s->pages_refused ? cudaErrorMemoryAllocation : captured;
+        void* grown = nullptr;
+        const cudaError_t e = cudaMallocAsync(&grown, (size_t)n, stream);
+        if (e == cudaSuccess) {
+          s->pages = grown;
+          if (n >= s->pages_refused) s->pages_refused = INT64_MAX;
+        } else if (e == cudaErrorMemoryAllocation && n < s->pages_refused) {
+          s->pages_refused = n;
+        }
+        return e;
+      },
+      no_memory, &failed);
+  if (failed == captured) return BLKATTN_ERR_NO_WORKSPACE;
+  return failed == cudaSuccess ? BLKATTN_OK : cuda_fail(failed);
 }
 
 int ensure_workspace(DeviceState* s, size_t bytes, cudaStream_t stream) {
@@ -1047,11 +1076,16 @@ int fwd_paged_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages_, con
 
 // blkattn_fwd_paged_q8.  Prompts (T_q >= 64, no tree, contiguous query rows,
 // scale > 0): the visible pages are written as bf16 to a buffer of the library
-// and the bf16 prompt kernel reads those, the sequences in slices of kExpandBytes;
-// the numbers are the same, a bf16 holds e4m3 times a power of two.  The rest goes
-// to the kernels that read the 8-bit pages.
-constexpr int64_t kExpandBytes = 2LL << 30;  // of K and V for one slice of sequences; 8x for a single one
-
+// and the bf16 prompt kernel reads those, in slices of sequences, or of one's
+// heads, that 2 GiB hold; the numbers are the same, a bf16 holds e4m3 times a
+// power of two.  The rest goes to the kernels that read the 8-bit pages, and so
+// does a prompt whose copy finds no memory.
+// (The copy is written whichever bf16 kernel then takes the rows: where that is the
+// decode kernel, few rows over long tables, it mostly costs less than the 8-bit
+// kernels' 1.55 us a tile of 48 rows.  Bf16 results, us with the copy and without:
+// 72 rows of one head over 32768 keys 38 and 51, 64 rows of 80 heads, 10 KV heads,
+// 292 and 296; over 4096 keys, 20 KV heads, 77 and 70.  Where the copy is large for
+// its rows it does not: 4 x 64 rows of 20 heads, 10 KV heads, 460 and 322.)
 int fwd_paged_q8_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages, const blkattn_tensor* v_pages,
                       const blkattn_tensor* k_scales, const blkattn_tensor* v_scales, const blkattn_tensor* page_table,
                       const blkattn_tensor* seqlens_k, const blkattn_tensor* q_logical_pos, const blkattn_tensor* tree,
@@ -1103,27 +1137,26 @@ int fwd_paged_q8_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages, c
   DeviceState* ds = nullptr;
   if ((st = device_state(&ds)) != BLKATTN_OK) return st;
 
-  const int64_t seq_bytes = 4 * c.Hkv * c.Tmax * c.d;  // of one sequence's K and V as bf16
-  if (c.prefill_ok && scale > 0.f && c.Tq >= 64 && seq_bytes <= 8 * kExpandBytes) {
-    int64_t nb = kExpandBytes / seq_bytes;
-    nb = nb < 1 ? 1 : (nb > c.B ? c.B : nb);
-    if (nb > 65535) nb = 65535;
-    while (nb > 1 && nb * pt.entries > 0x7fffffff) nb /= 2;
-    const int64_t half = nb * seq_bytes / 2, tab = (nb * pt.entries * 4 + 255) / 256 * 256;
-    const int64_t need = 2 * half + tab;
-    if ((size_t)need > ds->pages_bytes &&
-        (st = grow_stream_ordered(&ds->pages, &ds->pages_bytes, (size_t)need, stream)) != BLKATTN_OK)
+  // the copy: K and V of a sequence's head, and a page table
+  const int64_t head_bytes = 4 * c.Tmax * c.d, tab_bytes = ((int64_t)pt.entries * 4 + 255) / 256 * 256;
+  Slice slice{0, 0};
+  if (c.prefill_ok && scale > 0.f && c.Tq >= 64) {
+    int64_t most = 0x7fffffff / pt.entries;  // (page numbers, the grid)
+    if (most > 65535) most = 65535;
+    if ((st = ensure_copy(ds, c.B < most ? c.B : most, c.Hkv, tab_bytes, head_bytes, stream, &slice)) != BLKATTN_OK)
       return st;
+  }
+  if (slice.seqs > 0) {
+    const int64_t nb = slice.seqs, G = c.Hq / c.Hkv, half = nb * slice.heads * (head_bytes / 2);
     char* buf = static_cast<char*>(ds->pages);
-    for (int64_t b0 = 0; b0 < c.B; b0 += nb) {
-      const int64_t n = c.B - b0 < nb ? c.B - b0 : nb;
+    auto run = [&](int64_t b0, int64_t n, int64_t h0, int64_t nh) -> int {  // sequences from b0, KV heads from h0
       ExpandParams e{};
       const blkattn_tensor* pools[2] = {&kn, &vn};
       const blkattn_tensor* scales[2] = {k_scales, v_scales};
       for (int i = 0; i < 2; ++i) {
-        e.pool[i] = static_cast<const unsigned char*>(pools[i]->data);
+        e.pool[i] = static_cast<const unsigned char*>(pools[i]->data) + h0 * pools[i]->strides[1];
         e.s_n[i] = pools[i]->strides[0]; e.s_h[i] = pools[i]->strides[1]; e.s_r[i] = pools[i]->strides[2];
-        e.scales[i] = static_cast<const unsigned char*>(scales[i]->data);
+        e.scales[i] = static_cast<const unsigned char*>(scales[i]->data) + h0 * scales[i]->strides[1];
         e.e_n[i] = scales[i]->strides[0]; e.e_h[i] = scales[i]->strides[1]; e.e_i[i] = scales[i]->strides[2];
         e.out[i] = buf + i * half;
       }
@@ -1134,31 +1167,36 @@ int fwd_paged_q8_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages, c
       e.qpos = static_cast<const int32_t*>(q_logical_pos->data) + b0 * q_logical_pos->strides[0];
       e.qp_sb = q_logical_pos->strides[0]; e.qp_si = q_logical_pos->strides[1];
       e.window = (int)window;
-      e.Tq = (int)c.Tq; e.B = (int)n; e.Hkv = (int)c.Hkv;
+      e.Tq = (int)c.Tq; e.B = (int)n; e.Hkv = (int)nh;
       e.pages = pt;
       e.pages.table += b0 * pt.sb;
       if (cudaError_t err = launch_expand_q8(e, (int)c.d, stream); err != cudaSuccess) return cuda_fail(err);
-      auto slice = [&](const blkattn_tensor* t, int64_t bytes) {
+      auto part = [&](const blkattn_tensor* t, int64_t bytes, bool of_heads) {
         blkattn_tensor r = *t;
-        r.data = static_cast<char*>(t->data) + b0 * t->strides[0] * bytes;
+        r.data = static_cast<char*>(t->data) + (b0 * t->strides[0] + (of_heads ? h0 * G * t->strides[1] : 0)) * bytes;
         r.sizes[0] = n;
+        if (of_heads) r.sizes[1] = nh * G;
         return r;
       };
       blkattn_tensor kp = kc;
       kp.data = e.out[0];
-      kp.sizes[0] = n * pt.entries; kp.sizes[2] = pt.rows;
-      kp.strides[3] = 1; kp.strides[2] = c.d; kp.strides[1] = c.d * pt.rows; kp.strides[0] = c.d * pt.rows * c.Hkv;
+      kp.sizes[0] = n * pt.entries; kp.sizes[1] = nh; kp.sizes[2] = pt.rows;
+      kp.strides[3] = 1; kp.strides[2] = c.d; kp.strides[1] = c.d * pt.rows; kp.strides[0] = c.d * pt.rows * nh;
       blkattn_tensor vp = kp;
       vp.data = e.out[1];
       blkattn_tensor table = *page_table;
       table.data = e.table;
       table.sizes[0] = n;
       table.strides[0] = pt.entries; table.strides[1] = 1;
-      const blkattn_tensor sq = slice(q, 2), sl = slice(seqlens_k, 4), sp = slice(q_logical_pos, 4);
-      const blkattn_tensor so = slice(out, elt_bytes(out->dtype)), sle = slice(lse, 4);
-      st = fwd_paged_impl(&sq, &kp, &vp, &table, &sl, &sp, nullptr, window, scale, &so, &sle, stream_, true);
-      if (st != BLKATTN_OK) return st;
-    }
+      const blkattn_tensor sq = part(q, 2, true), sl = part(seqlens_k, 4, false), sp = part(q_logical_pos, 4, false);
+      const blkattn_tensor so = part(out, elt_bytes(out->dtype), true), sle = part(lse, 4, true);
+      return fwd_paged_impl(&sq, &kp, &vp, &table, &sl, &sp, nullptr, window, scale, &so, &sle, stream_, true);
+    };
+    for (int64_t b0 = 0; b0 < c.B; b0 += nb)
+      for (int64_t h0 = 0; h0 < c.Hkv; h0 += slice.heads) {
+        const int64_t n = c.B - b0 < nb ? c.B - b0 : nb, nh = c.Hkv - h0 < slice.heads ? c.Hkv - h0 : slice.heads;
+        if ((st = run(b0, n, h0, nh)) != BLKATTN_OK) return st;
+      }
     return BLKATTN_OK;
   }
 

@@ -577,9 +577,13 @@ int blkattn_paged_read_q8(const blkattn_tensor* pos, const blkattn_tensor* page_
  * the scores of its visible keys, gives NaN in out and lse; the other rows are
  * not touched by it.  (An infinity in q may count as a NaN.)
  * Workspace, growth and overlap of calls as for blkattn_fwd.  For prompts the
- * library also keeps a bf16 copy of the pages that the call's tables can name:
- * up to 2 GiB for a slice of the sequences, up to 16 GiB where one sequence
- * alone has more (beyond that the pages are read as they are).
+ * library also writes a bf16 copy of the pages that the call's tables can name
+ * (4 d H_kv entries P bytes a sequence, whatever its length), in slices of
+ * sequences, or of one sequence's heads, that 2 GiB hold.  The buffer's size is
+ * 2 GiB / 2^i while memory allows; outgrown ones are kept, together less than
+ * the current one: 4 GiB at most are held.  Where it finds no memory the slices
+ * get smaller, and where the smallest finds none, or one head's copy would pass
+ * 2 GiB, the pages are read as they are (slower, and with the precision above).
  * Returns as blkattn_fwd_paged; BLKATTN_ERR_UNSUPPORTED too for a q of f32 and
  * for pools whose rows of one head lie 64 GiB or more apart.
  */

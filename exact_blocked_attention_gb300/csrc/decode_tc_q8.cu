@@ -13,11 +13,16 @@
 // e4m3 (4 bits) and q_lo = 32 (q - q_hi) the rest of a bf16's 8 bits, exact but
 // for dims below 2^-14 of the row's largest (off by at most 2^-22 of it).
 // p: a weight as f16, taken apart exactly into 4 pieces of e5m2: an f16's upper
-// byte is the first (its value cut to 3 bits), the rest times 2^8 has 8 bits, its
-// upper byte is the second, and so on; U = U_1 + (U_2 + U_3 + U_4) / 2^8.  An f16's
-// step is 2^-23 of the row's largest weight or finer.  (Pieces of e4m3, two
-// conversions each and room for weights to 2^8 only, took five-row chains of 64
-// heads 129 us where these took 118.)
+// byte is the first (its value cut to 3 bits), the rest times 2^4 has 8 bits, its
+// upper byte is the second, the rest of that times 2^2 the third's, and so on: e5m2's
+// least step, 2^-16, reaches f16's, 2^-24, at the last.  U = U_1 + (U_2 + (U_3 + U_4 /
+// 4) / 4) / 16.  An f16's step is 2^-27 of the row's largest weight or finer: a weight
+// below 2^-16 of it is off by as much as 2^-28, which a long tail of equal keys beside
+// one strong key adds up (n keys of a CTA's range: n 2^-28; a million, what rounding
+// to bf16 does).  (One factor 2^8 for the last three pieces leaves room for weights to
+// 2^11 only and steps of 2^-23; the rests of the fp32 weights instead of f16's, 12
+// bits and steps of 2^-29, took five-row chains of 64 heads 124 us where these took
+// 117; pieces of e4m3, two conversions each, 129.)
 // With k = 2^ek k8 and v = 2^ev v8: x = (S_hi + S_lo / 32) 2^ek fac_row, and the
 // weight is 2^(x - m + ev - r), of two references a row: m >= max x for the
 // sum of fp32 weights, and r >= max (x - m + ev) - 7 for the product's (r relative
@@ -50,17 +55,20 @@ constexpr float kNegInf = -__builtin_huge_valf();
 // m is set 2^24 above the largest score so far (the sum of fp32 weights loses
 // nothing by it) and rises when one passes it.
 constexpr float kMarginM = 24.f;
+// In place of m where a row has none yet: any score is above, a masked one's weight 0.
+constexpr float kNoM = -3e38f;
 // r stays above: 2^(kLift - r) is a float.  (Values all below 2^-100 448 lose bits.)
-constexpr float kLeastR = -120.f;
+constexpr float kLeastR = -118.f;
 // And below kMostR, so that 2^(kLift - r) stays a float, not a subnormal one: a
 // product's largest is 2^127 (x <= m, ev <= 127), 2^(kLift + 127 - kMostR) = 2 then.
-constexpr float kMostR = 130.f;
+constexpr float kMostR = 134.f;
 // A weight at the reference is 2^kLift, and the reference is set 2^kMargin above
 // the largest weight so far: there is room for a maximum 2^12 above that before the
 // reference has to rise, which costs a tile 2.5 us (with room for 2^6 ten tiles of
-// 57 raised one of 40 rows', with this four).  kMostW: the largest whose rest times 2^8 is an f16.
-constexpr float kLift = 4.f, kMargin = 5.f;
-constexpr float kMostW = 2047.f;
+// 57 raised one of 40 rows', with this four; for 2^11 and 2^10 five-row chains of 64
+// heads 120 us, for this 117).  kMostW: the largest f16 whose rest times 2^4 is one.
+constexpr float kLift = 8.f, kMargin = 5.f;
+constexpr float kMostW = 32752.f;
 static_assert(kMostR == kLift + 126.f, "2^(kLift - kMostR) is the least normal float");
 
 constexpr int D = 128;
@@ -89,6 +97,12 @@ __device__ __forceinline__ uint32_t h2_to_e4m3x2(uint32_t h) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
   return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // Integer facts of the rows of one unit (written by the unit loader).
@@ -288,7 +302,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
   uint16_t* stab = ntab + kDecodeTcMaxEntries;  // the units' first tiles (sliding window)
   float* red = reinterpret_cast<float*>(sm + L::kOffRed);
   float* s_m = reinterpret_cast<float*>(sm + L::kOffStat);  // reference maximum, -inf = none yet
-  float* s_muse = s_m + NR;                                  // m, or 0 when none yet
+  float* s_muse = s_m + NR;                                  // m, or kNoM when none yet
   float* s_r = s_m + 2 * NR;                                 // reference of the weights, -inf = none yet
   float* s_h = s_m + 3 * NR;                                 // 2^(lift - r), 1 when none yet
   float* s_alpha = s_m + 4 * NR;
@@ -384,7 +398,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
     }
     if (threadIdx.x < NR) {
       s_m[threadIdx.x] = kNegInf;
-      s_muse[threadIdx.x] = 0.f;
+      s_muse[threadIdx.x] = kNoM;
       s_r[threadIdx.x] = kNegInf;
       s_h[threadIdx.x] = 1.f;
     }
@@ -963,7 +977,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
           float hi[NH];
           ld_cols<NH>(ua + c * NR, hi);
 #pragma unroll
-          for (int r = 0; r < NH; ++r) u[r] = fmaf(u[r], c > 0 ? 1.f : 0x1p-8f, hi[r]);
+          for (int r = 0; r < NH; ++r) u[r] = fmaf(u[r], c > 0 ? 0x1p-2f : 0x1p-4f, hi[r]);
         }
       }
       const int64_t unit = ((int64_t)pend_b * Hkv + pend_kvh) * RG + pend_rg;
@@ -1132,6 +1146,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
       const float f1 = ev == kNegInf ? 0.f : fast_exp2(half), f2 = ev == kNegInf ? 0.f : fast_exp2(ev - half);
       float pr[NH];         // the weights e^z at m's reference
       uint32_t w2[NH / 2];  // with the values' scales, at r's, pairs of rows as f16
+      float z_max = kNegInf;  // above 0: some m has to rise
       auto weigh = [&]() {
         const float2 fa = make_float2(f1, f1), fb = make_float2(f2, f2), neg = make_float2(-1.f, -1.f);
 #pragma unroll
@@ -1144,6 +1159,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
           for (int e = 0; e < 2; ++e) {
             const int r = 4 * r4 + 2 * e;
             const float2 z = __ffma2_rn(mu[e], neg, make_float2(x[r], x[r + 1]));
+            z_max = max3(z_max, z.x, z.y);
             const float2 pp = make_float2(fast_exp2(z.x), fast_exp2(z.y));  // masked: 2^-inf = 0
             pr[r] = pp.x;
             pr[r + 1] = pp.y;
@@ -1193,11 +1209,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
       for (bool again = false;; again = true) {
         weigh();
         if (again) break;
-#pragma unroll
-        for (int r4 = 0; r4 < NH / 4; ++r4) {
-          const float4 t4 = reinterpret_cast<const float4*>(s_m + c0)[r4];
-          trig |= (x[4 * r4] > t4.x) | (x[4 * r4 + 1] > t4.y) | (x[4 * r4 + 2] > t4.z) | (x[4 * r4 + 3] > t4.w);
-        }
+        trig |= z_max > 0.f;
         if (trig) misc[4 + (int)(g & 1)] = 1;  // m has to rise (read after the vote's barrier)
         __half2 top = *reinterpret_cast<const __half2*>(&w2[0]);
 #pragma unroll
@@ -1292,7 +1304,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
             for (int i = 0; i < NH / 2; ++i) {  // the rest
               const uint32_t top = w2[i] & 0xff00ff00u;
               __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&w2[i]), *reinterpret_cast<const __half2*>(&top));
-              if (c == 0) rest = __hmul2(rest, __float2half2_rn(256.f));
+              rest = __hmul2(rest, __float2half2_rn(c == 0 ? 16.f : 4.f));
               w2[i] = *reinterpret_cast<const uint32_t*>(&rest);
             }
           }
@@ -1361,7 +1373,7 @@ __global__ void __launch_bounds__(TcLayout<NR>::kThreads, 1)
           s_inv[k] = l == 0.f ? 0.f : 1.f / l;
           // fresh statistics for the next unit
           s_m[k] = kNegInf;
-          s_muse[k] = 0.f;
+          s_muse[k] = kNoM;
           s_r[k] = kNegInf;
           s_h[k] = 1.f;
         }

@@ -570,7 +570,7 @@ int blkattn_paged_read_q8(const blkattn_tensor* pos, const blkattn_tensor* page_
  * f32 out, and vanish below 2^-36 of the row's largest weight times scale (with
  * scales of 2^-100 and less throughout, sooner).  With a bf16 out and d = 128
  * (over tables of more than 256 rows, of 16-byte aligned contiguous query rows)
- * weights have an absolute step too, 2^-23 of that largest product, and a query
+ * weights have an absolute step too, 2^-27 of that largest product, and a query
  * row's dims one of 2^-22 of its largest dim.  Prompts (T_q >= 64, no tree,
  * 16-byte aligned contiguous rows, scale > 0) go through the kernel of
  * blkattn_fwd_paged and have its precision.  A row with a NaN in q, or among

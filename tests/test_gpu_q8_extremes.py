@@ -64,3 +64,35 @@ def test_small_rows_beside_large_keys(d, G, out):
         a["q"] = (a["q"].float().sign() * 2.0 ** (e + 60) * 2.0 ** -60).to(BF16)
         assert bool((a["q"] != 0).any())
         check(a, call(a, out), out)
+
+
+@pytest.mark.parametrize("G", [4, 12, 24, 40])
+@pytest.mark.parametrize("n,far", [(1 << 13, 17), (1 << 17, 17), (1 << 20, 20), (1 << 20, 22)])
+def test_one_strong_key_and_a_long_tail(n, far, G):
+    """A key that outweighs each other one by 2^far and a bit, and a tail of equal ones that has a good part of the mass
+    all the same, in units that lie in one or two CTAs (as many sequences as fill the machine twice, over the same
+    pages).  A weight keeps 11 bits (off by 2^-11 of itself) or a step of 2^-27 of the row's largest (off by 2^-28 of
+    that): out = n p v / (1 + n p) is off by at most 2^-11 + 2^-28 / p of itself, its bf16 by 2^-8, and the fp32 sums
+    and powers by 2^-20 and n / 32 steps of 2^-24."""
+    d, P = 128, 128
+    B = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    worst = 0.0
+    for part in (1.125, 1.375, 1.625, 1.875):
+        k = torch.zeros(1, 1, n, d, device=dev())
+        k[:, :, 1:, 0] = -(far - far % 2)
+        k[:, :, 1:, 1] = part - 2 - far % 2
+        v = torch.zeros(1, 1, n, d, device=dev())
+        v[:, :, 1:] = 1 + torch.arange(d, device=dev()).remainder(8) / 8
+        q = torch.zeros(B, G, 1, d, device=dev())
+        q[..., :2] = 1
+        one = torch.full((1, 1, n), 127, device=dev())
+        a = problem(k, v, one, one, q[:1], 16, math.log(2.0), P=P)
+        a.update(q=q.to(BF16), **{x: a[x].expand(B, -1).contiguous() for x in ("table", "pos")}, lens=a["lens"].expand(B).contiguous())
+        p = math.exp(math.log(2.0) * (part - 2 - far))
+        want = (n - 1) * p / (1 + (n - 1) * p) * v[0, 0, 1].to(F64)
+        got, lse = call(a, BF16)
+        bound = 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -28 / p + 2.0 ** -20 + n / 32 * 2.0 ** -24
+        err = float(((got.to(F64) - want).abs() / want).max())
+        worst = max(worst, err / bound)
+        assert float((lse.to(F64) - math.log1p((n - 1) * p)).abs().max()) < 2.0 ** -20 + n / 32 * 2.0 ** -24
+    assert worst <= 1, worst

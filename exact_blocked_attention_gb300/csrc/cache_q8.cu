@@ -743,7 +743,6 @@ int blkattn_paged_append_q8(const blkattn_tensor* k, const blkattn_tensor* v, co
     p.q_out = q_out_opt->data;
     p.o_b = q_out_opt->strides[0]; p.o_h = q_out_opt->strides[1];
     p.o_t = q_out_opt->strides[2]; p.o_d = q_out_opt->strides[3];
-    if (B * T * Hq < kOwnKernelRows) vec = vec && vec_rows(q_opt) && vec_rows(q_out_opt);
   }
   if (q_weight_opt) { p.wq = q_weight_opt->data; p.wq_s = q_weight_opt->strides[0]; }
   if (k_weight_opt) { p.wk = k_weight_opt->data; p.wk_s = k_weight_opt->strides[0]; }
@@ -764,10 +763,11 @@ int blkattn_paged_append_q8(const blkattn_tensor* k, const blkattn_tensor* v, co
   const int parts = p.panel * (int)d / 2048 < 1 ? 1 : p.panel * (int)d / 2048;  // (as in the kernel)
   p.kv_groups = (int)((2 * H * parts + kWarps - 1) / kWarps);
   p.pages = pt;
-  const int64_t blocks = B * ((T + p.panel - 1) / p.panel);
-  if (blocks > 0x7fffffff) return BLKATTN_ERR_UNSUPPORTED;
-  const bool own = B * T * Hq >= kOwnKernelRows;
-  const dim3 grid((unsigned)blocks, (unsigned)(p.kv_groups + (own ? 0 : (Hq + kQHeads - 1) / kQHeads)));
+  const int64_t q_groups = (Hq + kQHeads - 1) / kQHeads;
+  // (many KV heads in blocks of many rows leave the grid no room for the query rows)
+  const bool own = B * T * Hq >= kOwnKernelRows || (Hq > 0 && p.kv_groups + q_groups > 65535);
+  if (Hq > 0 && !own) vec = vec && vec_rows(q_opt) && vec_rows(q_out_opt);
+  const dim3 grid((unsigned)(B * ((T + p.panel - 1) / p.panel)), (unsigned)(p.kv_groups + (own ? 0 : q_groups)));
   const bool inter = layout == BLKATTN_ROPE_INTERLEAVED;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   cudaError_t e;

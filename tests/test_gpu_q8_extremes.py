@@ -96,3 +96,29 @@ def test_one_strong_key_and_a_long_tail(n, far, G):
         worst = max(worst, err / bound)
         assert float((lse.to(F64) - math.log1p((n - 1) * p)).abs().max()) < 2.0 ** -20 + n / 32 * 2.0 ** -24
     assert worst <= 1, worst
+
+
+def test_append_to_very_many_heads():
+    """As many KV heads as there may be, in blocks of 128 rows, and the query rows of a decode step with them."""
+    H, d, P = 32767, 128, 128
+    g = torch.Generator(device=dev()).manual_seed(1)
+    kp, vp = (torch.zeros(1, H, P, d, dtype=U8, device=dev()).view(F8) for _ in range(2))
+    ks, vs = (torch.full((1, H, 1), 255, dtype=U8, device=dev()).view(E8) for _ in range(2))
+    k, v = (torch.randn(1, H, 2, d, generator=g, device=dev()).to(BF16) for _ in range(2))
+    q = torch.randn(1, 70, 2, d, generator=g, device=dev()).to(BF16)
+    w = (1 + 0.2 * torch.randn(d, generator=g, device=dev())).to(BF16)
+    pos = torch.tensor([[0, 1]], dtype=I32, device=dev())
+    table = torch.zeros(1, 1, dtype=I32, device=dev())
+    ph = blkattn.rope_phases(blkattn.rope_angles(d)[0])
+    got = blkattn.paged_append_q8(k, v, pos, table, kp, vp, ks, vs, phases=ph, q_weight=w, q=q)
+    # the same rows, some heads at a time
+    for h0 in range(0, H, 8000):
+        h1 = min(H, h0 + 8000)
+        kq, vq = (torch.zeros(1, h1 - h0, P, d, dtype=U8, device=dev()).view(F8) for _ in range(2))
+        kc, vc = (torch.full((1, h1 - h0, 1), 255, dtype=U8, device=dev()).view(E8) for _ in range(2))
+        want = blkattn.paged_append_q8(k[:, h0:h1], v[:, h0:h1], pos, table, kq, vq, kc, vc, phases=ph, q_weight=w, q=q)
+        for x, y in ((kp, kq), (vp, vq), (ks, kc), (vs, vc)):
+            assert torch.equal(x.view(U8)[:, h0:h1], y.view(U8))
+    # (a decode step's query rows and a prompt's may differ in an fp32 angle's last bits)
+    err = (got.float() - want.float()).abs()
+    assert bool((err <= 2.0 ** -7 * want.float().abs() + 2.0 ** -16).all())

@@ -31,7 +31,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMostHeads = 8;  // heads of one thread and token
-constexpr int kFillBlocks = 152 * 2;  // blocks resident at once
 
 // The query heads (set 0) or the key heads (set 1).
 struct NormSet {
@@ -645,12 +644,16 @@ cudaError_t launch_forward(NormParams p, cudaStream_t stream) {
   if (fast_ok(p, sizeof(TI), sizeof(TO), 0)) {
     const int per_block = kThreads / (p.d / (2 * V));
     int64_t blocks = ((int64_t)p.B * p.T + per_block - 1) / per_block;
-    // heads of a group: as many as leave enough groups to fill the machine
-    const int64_t want = (kFillBlocks + blocks - 1) / blocks;
-    int groups = set_groups(&p, (int)((most_heads(p) + want - 1) / want));
-    if (groups > 65535) groups = set_groups(&p, kMostHeads);
+    int dev = 0, sms = 0;
+    if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+    if (cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev); e != cudaSuccess) return e;
+    const int fill = kResident * sms;  // blocks resident at once
+    // heads of a group: as many as leave enough groups to fill the machine (at most
+    // 2 x 32767 groups: in a grid's range)
+    const int64_t want = (fill + blocks - 1) / blocks;
+    const int groups = set_groups(&p, (int)((most_heads(p) + want - 1) / want));
     // one wave of blocks and no block more
-    const int64_t most = groups < kFillBlocks ? kFillBlocks / groups : 1;
+    const int64_t most = groups < fill ? fill / groups : 1;
     if (blocks > most) blocks = most;
     constexpr int smem = 2 * kRing * 2 * V * (int)sizeof(TI) * kThreads;
     static DeviceOnce once;

@@ -1300,14 +1300,6 @@ int Library::workspace(size_t bytes, cudaStream_t stream, void** ws) const {
   *ws = ds->ws;
   return BLKATTN_OK;
 }
-int Library::counters(int64_t n, cudaStream_t stream, unsigned** cnt) const {
-  DeviceState* ds = nullptr;
-  if (const int st = device_state(&ds); st != BLKATTN_OK) return st;
-  if (const int st = ensure_counters(ds, n, stream); st != BLKATTN_OK) return st;
-  *cnt = ds->cnt;
-  return BLKATTN_OK;
-}
-
 int device_error_word(int** out) {
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState* ds = nullptr;

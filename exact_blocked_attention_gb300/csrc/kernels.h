@@ -304,11 +304,9 @@ class Library {
   Library(const Library&) = delete;
   Library& operator=(const Library&) = delete;
   int sms(int* n) const;
-  // At least so many bytes of the grow-only workspace, and so many per-unit
-  // counters (zero, and left zero by every launch); BLKATTN_ERR_NO_WORKSPACE
+  // At least so many bytes of the grow-only workspace; BLKATTN_ERR_NO_WORKSPACE
   // where it would have to grow under capture.
   int workspace(size_t bytes, cudaStream_t stream, void** ws) const;
-  int counters(int64_t n, cudaStream_t stream, unsigned** cnt) const;
 };
 // The current device's error word (kernels record a bounded wait that ran
 // out there; blkattn_check_device_error reads and clears it).

@@ -470,7 +470,8 @@ def fwd_paged_q8(q, k_pages, v_pages, k_scales, v_scales, page_table, seqlens_k,
 
 def attention_paged_q8(q, k_pages, v_pages, k_scales, v_scales, page_table, seqlens_k, q_logical_pos, scale=None,
                        out_dtype=torch.float32, stream=None, tree=None, window: int = 0):
-    """Allocate out/lse with torch and run blkattn_fwd_paged_q8 (scale defaults to 1/sqrt(d))."""
+    """Allocate out/lse with torch and run blkattn_fwd_paged_q8 (scale defaults to 1/sqrt(d)).  q is bf16 (round an
+    f32 q_out of paged_append_q8 first); out_dtype=torch.bfloat16 is the faster result."""
     st, out, lse = (_bind or _load_bind()).fwd_q8(q, k_pages, v_pages, k_scales, v_scales, page_table, seqlens_k,
                                                   q_logical_pos, tree, window, scale, None, None, out_dtype,
                                                   _handle(stream))

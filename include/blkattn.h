@@ -509,14 +509,18 @@ int blkattn_fwd_paged(const blkattn_tensor* q, const blkattn_tensor* k_pages, co
  * and the base addresses multiples of 16), and k_scales, v_scales
  * BLKATTN_E8M0 [N, H_kv, P / S] (any strides but no broadcast dim) hold one
  * power of two 2^e for each block of S rows of a page and head: a number
- * stands for e4m3 2^e, exactly a bf16.  S is a power of two, 1 <= S <= 128, and
- * divides P (greater S give BLKATTN_ERR_UNSUPPORTED).
+ * stands for e4m3 2^e, exactly a bf16 where e >= -124.  (Below, bf16's least step
+ * 2^-133 is wider than the smallest numbers': read as bf16, or copied for a
+ * prompt, they are rounded once.)  S is a power of two, 1 <= S <= 128, and divides
+ * P (greater S give BLKATTN_ERR_UNSUPPORTED).
  *
  * blkattn_paged_append_q8 — blkattn_paged_append into that cache, with the head
  * norms of blkattn_qk_norm_rope on the way.
  *
  * k, v, pos, page_table, phases, layout, mscale, q, q_out: as for
  *             blkattn_paged_append; k and q are of one dtype, bf16 or f32.
+ *             (blkattn_fwd_paged_q8 reads bf16 query rows: an f32 q_out has to be
+ *             rounded for it.)
  * k_weight, q_weight, eps  each weight NULL (no norm) or as for
  *             blkattn_qk_norm_rope (both of one dtype): k and q are normed
  *             before they turn.
@@ -558,10 +562,13 @@ int blkattn_paged_read_q8(const blkattn_tensor* pos, const blkattn_tensor* page_
 /*
  * blkattn_fwd_paged_q8 — blkattn_fwd_paged over the 8-bit cache.
  *
- * q           [B, H_q, T_q, d] bf16, any strides.
+ * q           [B, H_q, T_q, d] bf16 (f32 is refused), any strides.
+ * out         bf16 or f32, as for blkattn_fwd_paged.  bf16 is the faster one: decode
+ *             rows of heads of 128 then go to the tensor cores' 8-bit products,
+ *             and the other kernel takes one value product instead of two.
  * k_pages, v_pages, k_scales, v_scales  the 8-bit cache, as above.
- * page_table, seqlens_k, q_logical_pos, tree_mask, window, scale, out, lse,
- * stream: as for blkattn_fwd_paged, with its visibility.  What a row between
+ * page_table, seqlens_k, q_logical_pos, tree_mask, window, scale, lse, stream:
+ * as for blkattn_fwd_paged, with its visibility.  What a row between
  * the earliest and the latest key that query rows of one sequence see holds
  * must not be NaN, except tree nodes that no row lists; every other row of the
  * pools and its scales may hold anything.

@@ -98,6 +98,22 @@ def test_one_strong_key_and_a_long_tail(n, far, G):
     assert worst <= 1, worst
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_small_scales_read_as_bf16(d):
+    """Scales below 2^-124: a number may lie between bf16's, and is rounded once."""
+    a = make(2, 2, 2, 1, d, 16, 1, [300, 77], spread=0)
+    for n in ("ks", "vs"):
+        live = a[n].view(U8) < 255
+        a[n].view(U8)[live] = torch.arange(int(live.sum()), device=dev()).remainder(8).to(U8)
+    pos = torch.arange(300, device=dev(), dtype=I32).expand(2, 300).contiguous()
+    pos[1, 77:] = -1
+    cache = a["kp"], a["vp"], a["ks"], a["vs"]
+    exact = blkattn.paged_read_q8(pos, a["table"], *cache, out_dtype=F32)
+    near = blkattn.paged_read_q8(pos, a["table"], *cache, out_dtype=BF16)
+    for x, y in zip(exact, near):
+        assert torch.equal(x.to(BF16), y) and bool((x != x.to(BF16).float()).any())
+
+
 def test_append_to_very_many_heads():
     """As many KV heads as there may be, in blocks of 128 rows, and the query rows of a decode step with them."""
     H, d, P = 32767, 128, 128

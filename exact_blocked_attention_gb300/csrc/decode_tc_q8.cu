@@ -33,8 +33,11 @@
 // products, ring and waits; the unit loader also brings each key's scales.
 //
 // What bounds it: memory for up to 16 rows once the stream runs (5.8 TB/s; 11 us of
-// cold latency before), for more the key threads' arithmetic on the scores (40
-// rows: 117 us where the bytes take 42).
+// cold latency before).  For more, the chain of a tile, which all key threads pass
+// together: wait for the scores, load them from tensor memory, weights, a vote over
+// all of them, P^T, arrival, some 1.5 us a tile of 128 keys in which no pipe is over
+// a third busy (40 rows: 117 us where the bytes take 42), and raises of a reference,
+// 2.5 us each.
 //
 // Every wait is bounded (%globaltimer); on a timeout the CTA records the error
 // word, stops issuing work, lets its own copies and products drain and frees

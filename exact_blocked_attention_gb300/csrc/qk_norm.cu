@@ -184,7 +184,8 @@ __device__ __forceinline__ unsigned lanes_of_row(int n) {
 // Pairs of rows (two heads of a token) in a thread's slots (its own, in shared
 // memory): one at work, the others on their way.
 constexpr int kRing = 4;
-constexpr int kResident = 2;  // blocks of either kernel on an SM (three spill)
+constexpr int kResident = 2;  // blocks of either kernel on an SM (three spill; the gradient of f32 rows and f32
+                              // gradients has 128 KB of slots, and its blocks run in two waves)
 
 // V elements (16 or 8 bytes) of a row to the thread's slot, and from there.
 template <typename T, int V>

@@ -443,22 +443,26 @@ int grow_stream_ordered(void** buf, size_t* have, size_t bytes, cudaStream_t str
   size_t got = 0;
   const cudaError_t e = blkattn::grow_scratch(
       *have, bytes, [&](size_t n) { return cudaMallocAsync(&grown, n, stream); }, no_memory, &got);
-  if (e != cudaSuccess) return cuda_fail(e);
+  if (e != cudaSuccess) {
+    no_memory(e);  // (nor of the next launch)
+    return cuda_fail(e);
+  }
   *buf = grown;
   *have = got;
   return BLKATTN_OK;
 }
 
 // The buffer for slices of an 8-bit cache's pages as bf16 (scratch.h: fit_slices),
-// 2 GiB at most; slice->seqs = 0: none fits.
+// 2 GiB at most, and it grows to less than `below`; slice->seqs = 0: none fits.
 constexpr int64_t kCopyBytes = 2LL << 30;
-int ensure_copy(DeviceState* s, int64_t B, int64_t H, int64_t seq, int64_t head, cudaStream_t stream,
+int ensure_copy(DeviceState* s, int64_t B, int64_t H, int64_t seq, int64_t head, int64_t below, cudaStream_t stream,
                 blkattn::Slice* slice) {
   constexpr cudaError_t captured = cudaErrorStreamCaptureUnsupported;
   cudaError_t failed;
   *slice = blkattn::fit_slices(
       B, H, seq, head, kCopyBytes, &s->pages_bytes,
       [&](int64_t n) {
+        if (n >= below) return cudaErrorMemoryAllocation;
         cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
         if (cudaError_t e = cudaStreamIsCapturing(stream, &cs); e != cudaSuccess) return e;
         // (a captured call does what the same call before it did)
@@ -1139,14 +1143,17 @@ int fwd_paged_q8_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages, c
 
   // the copy: K and V of a sequence's head, and a page table
   const int64_t head_bytes = 4 * c.Tmax * c.d, tab_bytes = ((int64_t)pt.entries * 4 + 255) / 256 * 256;
-  Slice slice{0, 0};
-  if (c.prefill_ok && scale > 0.f && c.Tq >= 64) {
-    int64_t most = 0x7fffffff / pt.entries;  // (page numbers, the grid)
-    if (most > 65535) most = 65535;
-    if ((st = ensure_copy(ds, c.B < most ? c.B : most, c.Hkv, tab_bytes, head_bytes, stream, &slice)) != BLKATTN_OK)
-      return st;
-  }
-  if (slice.seqs > 0) {
+  const bool prompt = c.prefill_ok && scale > 0.f && c.Tq >= 64;
+  int64_t most = 0x7fffffff / pt.entries;  // (page numbers, the grid)
+  if (most > 65535) most = 65535;
+  if (most > c.B) most = c.B;
+  const cudaError_t said = g_last_cuda_error;
+  for (int64_t below = INT64_MAX; prompt;) {
+    void* const before = ds->pages;
+    const int64_t before_bytes = ds->pages_bytes;
+    Slice slice;
+    if ((st = ensure_copy(ds, most, c.Hkv, tab_bytes, head_bytes, below, stream, &slice)) != BLKATTN_OK) return st;
+    if (slice.seqs == 0) break;
     const int64_t nb = slice.seqs, G = c.Hq / c.Hkv, half = nb * slice.heads * (head_bytes / 2);
     char* buf = static_cast<char*>(ds->pages);
     auto run = [&](int64_t b0, int64_t n, int64_t h0, int64_t nh) -> int {  // sequences from b0, KV heads from h0
@@ -1195,9 +1202,18 @@ int fwd_paged_q8_impl(const blkattn_tensor* q_, const blkattn_tensor* k_pages, c
     for (int64_t b0 = 0; b0 < c.B; b0 += nb)
       for (int64_t h0 = 0; h0 < c.Hkv; h0 += slice.heads) {
         const int64_t n = c.B - b0 < nb ? c.B - b0 : nb, nh = c.Hkv - h0 < slice.heads ? c.Hkv - h0 : slice.heads;
-        if ((st = run(b0, n, h0, nh)) != BLKATTN_OK) return st;
+        if (st == BLKATTN_OK) st = run(b0, n, h0, nh);
       }
-    return BLKATTN_OK;
+    if (st != BLKATTN_ERR_CUDA || g_last_cuda_error != cudaErrorMemoryAllocation) return st;
+    // The workspace found no memory beside the copy.  What the copy took in this call
+    // goes back (no graph holds it), and a smaller one gets a try.
+    g_last_cuda_error = said;
+    if (ds->pages == before) break;
+    below = ds->pages_bytes;
+    if (below < ds->pages_refused) ds->pages_refused = below;
+    if (cudaError_t e = cudaFreeAsync(ds->pages, stream); e != cudaSuccess) return cuda_fail(e);
+    ds->pages = before;
+    ds->pages_bytes = before_bytes;
   }
 
   const int64_t rows = c.Hq / c.Hkv * c.Tq;

@@ -588,9 +588,10 @@ int blkattn_paged_read_q8(const blkattn_tensor* pos, const blkattn_tensor* page_
  * (4 d H_kv entries P bytes a sequence, whatever its length), in slices of
  * sequences, or of one sequence's heads, that 2 GiB hold.  The buffer's size is
  * 2 GiB / 2^i while memory allows; outgrown ones are kept, together less than
- * the current one: 4 GiB at most are held.  Where it finds no memory the slices
- * get smaller, and where the smallest finds none, or one head's copy would pass
- * 2 GiB, the pages are read as they are (slower, and with the precision above).
+ * the current one: 4 GiB at most are held.  Where it finds no memory, or leaves
+ * the workspace none, the slices get smaller, and where the smallest finds none,
+ * or one head's copy would pass 2 GiB, the pages are read as they are (slower,
+ * and with the precision above).
  * Returns as blkattn_fwd_paged; BLKATTN_ERR_UNSUPPORTED too for a q of f32 and
  * for pools whose rows of one head lie 64 GiB or more apart.
  */

@@ -98,3 +98,56 @@ a = make(1, 2, 1, 64, 128, 256, 16, [3000], entries=5 * 4096 + 7, heads_first=Tr
 check(a, call(a, BF16), BF16)
 assert used() < 64 * MIB, used() / MIB
 """)
+
+
+def test_random_prompts_in_slices():
+    """Problems of every kind whose copies go by sequences, by heads or not at all, the workspace beside them in
+    what is left."""
+    run(160 << 20, """
+import random
+r = random.Random(5)
+for seed in range(40):
+    d, P = r.choice([64, 128]), r.choice([16, 64, 256])
+    S = min(P, r.choice([1, 4, 16, 64]))
+    Hkv, T, B = r.choice([1, 2, 3, 5, 8]), r.choice([64, 65, 100, 300]), r.choice([1, 2, 3, 5])
+    Hq = Hkv * r.choice([1, 2, 3])
+    lens = [r.randint(T, T + r.choice([10, 600, 2500])) for _ in range(B)]
+    wide = r.choice([1, 8, 60, 200]) * 1024 * 128 // (d * P)
+    a = make(B, Hq, Hkv, T, d, P, S, lens, seed=seed, heads_first=r.random() < 0.5, rows_major=r.random() < 0.3,
+             entries=max(wide, 2800 // P + 2))
+    mode = r.choice(["causal", "window", "holes"])
+    if mode == "window":
+        a["window"] = r.choice([1, 50, 700])
+    if mode == "holes":
+        a["table"][r.randrange(B), r.randrange(max(1, min(lens) // P))] = -1
+        a["pos"][0, r.randrange(T)] = -1
+    out = r.choice([BF16, F32])
+    check(a, call(a, out), out)
+    assert used() <= 160 * MIB
+""")
+
+
+def test_a_workspace_that_finds_no_memory():
+    """Beside a copy: the copy gives its memory back, and a captured call does as this one did.  Alone: an error of that
+    call only."""
+    for most in (64, 96):
+        run(most << 20, """
+big = make(192, 24, 8, 48, 128, 64, 16, [48] * 192)
+small = make(2, 8, 2, 1, 128, 16, 16, [300, 400])
+a = make(2, 32, 1, 200, 128, 64, 16, [4000, 900], entries=1400, heads_first=True)  # 44 MiB of pages each, 17 of parts
+want = call(a, BF16)
+check(a, want, BF16)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = call(a, BF16)
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(x, y) for x, y in zip(got, want))
+try:
+    call(big, F32)
+except blkattn.BlkattnError as e:
+    assert "memory" in str(e), e
+else:
+    raise AssertionError("a workspace of more than the pool")
+check(small, call(small, BF16), BF16)
+""")
